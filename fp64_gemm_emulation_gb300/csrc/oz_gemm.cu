@@ -713,6 +713,8 @@ static PFN_encodeTiled get_encode_fn() {
   return fn;
 }
 
+void* tensor_map_encoder() { return reinterpret_cast<void*>(get_encode_fn()); }
+
 // 3-D map over planes [s][rows][kp] of bf16, box {64, box_rows, 1}, 128-byte swizzle.
 static bool make_plane_map(CUtensorMap* map, const void* base, int s, int rows, int kp, int box_rows) {
   PFN_encodeTiled enc = get_encode_fn();

@@ -114,6 +114,12 @@ cudaError_t launch_fill_zero(int m, int n, double* C, int ldc, cudaStream_t stre
 // Device status word (set by kernels whose bounded waits expired).
 int* device_status_ptr();
 
+// The driver's cuTensorMapEncodeTiled (null if it cannot be had).
+void* tensor_map_encoder();
+
+// Raises the release threshold of the current device's default pool (once per device).
+void keep_default_pool_cached();
+
 // Time limit of the GEMM epilogue's accumulator wait for the launches that follow
 // (ozaki_set_epilogue_wait_ns).
 unsigned long long epilogue_wait_ns();

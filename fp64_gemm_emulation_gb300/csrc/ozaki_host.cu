@@ -254,11 +254,13 @@ int check_dims(int m, int n, int k, int lda, int ldb, int ldc) {
 
 int cuda_rc(cudaError_t e) { return e == cudaSuccess ? OZ_OK : OZ_ECUDA; }
 
+}  // namespace
+
 // The allocating entry points draw their workspace from the device's default
 // stream-ordered memory pool.  Raise its release threshold once per device so the
 // pool keeps the memory between calls instead of unmapping it at every
 // synchronisation (repeated calls then allocate in microseconds).
-void keep_default_pool_cached() {
+void oz::keep_default_pool_cached() {
   static std::atomic<bool> done[64] = {};  // several host threads may call at once
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || done[dev].load(std::memory_order_acquire))
@@ -271,6 +273,8 @@ void keep_default_pool_cached() {
   cudaGetLastError();
   done[dev].store(true, std::memory_order_release);
 }
+
+namespace {
 
 // A dimension cut into up to kMax blocks whose sizes are multiples of 256 (but the last).
 struct Blocks {

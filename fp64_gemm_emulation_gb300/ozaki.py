@@ -26,6 +26,8 @@ PAD_M, PAD_N, PAD_K = 256, 256, 64
 OZ_NOALLOC_SCRATCH_BYTES = 64 << 20
 OZ_SCALE_UNIFORM, OZ_SCALE_FAST, OZ_SCALE_ACCU = 0, 1, 2
 OZ_OZAKI1_RN, OZ_OZAKI1_EF, OZ_OZAKI1_HYBRID = 0, 1, 2
+OZ_BF16, OZ_F16, OZ_F32 = 1, 2, 3
+OZ_MAX_GROUPS, OZ_MAX_NS_STEPS = 1024, 32
 OZAKI1_VARIANTS = {"rn": OZ_OZAKI1_RN, "ef": OZ_OZAKI1_EF, "hybrid": OZ_OZAKI1_HYBRID}
 SCALINGS = {"uniform": OZ_SCALE_UNIFORM, "fast": OZ_SCALE_FAST, "accu": OZ_SCALE_ACCU}
 
@@ -80,6 +82,18 @@ def _load():
         "ozaki1_accumulate_ex": (I, [I, I, I, I, I, P, P, P, P, I, P]),
         "ozaki1_dgemm_ex_ws": (I, [I, I, I, P, I, P, I, P, I, I, I, P, S, P]),
         "ozaki1_dgemm_ex": (I, [I, I, I, P, I, P, I, P, I, I, I, P]),
+        "ozaki_grouped_gemm_workspace_bytes": (S, [I, I, I, I, I, P, I, L, P, I]),
+        "ozaki_grouped_gemm_dgrad_workspace_bytes": (S, [I, I, I, I, I, P, I, L, P, I]),
+        "ozaki_grouped_gemm_wgrad_workspace_bytes": (S, [I, I, I, I, I, P, I, P, I]),
+        "ozaki_grouped_gemm_ws": (I, [I, I, I, I, I, P, I, L, P, I, P, P, I, P, S, P]),
+        "ozaki_grouped_gemm_dgrad_ws": (I, [I, I, I, I, I, P, I, L, P, I, P, P, I, P, S, P]),
+        "ozaki_grouped_gemm_wgrad_ws": (I, [I, I, I, I, I, P, I, P, I, P, P, I, L, P, S, P]),
+        "ozaki_grouped_gemm": (I, [I, I, I, I, I, P, I, L, P, I, P, P, I, P]),
+        "ozaki_grouped_gemm_dgrad": (I, [I, I, I, I, I, P, I, L, P, I, P, P, I, P]),
+        "ozaki_grouped_gemm_wgrad": (I, [I, I, I, I, I, P, I, P, I, P, P, I, L, P]),
+        "ozaki_newton_schulz_workspace_bytes": (S, [I, I, I, I]),
+        "ozaki_newton_schulz_ws": (I, [I, I, I, I, P, I, L, P, I, L, I, P, ctypes.c_float, I, P, S, P]),
+        "ozaki_newton_schulz": (I, [I, I, I, I, P, I, L, P, I, L, I, P, ctypes.c_float, I, P]),
         "ozaki_get_device_status": (I, [P]),
         "ozaki_status_string": (ctypes.c_char_p, [I]),
         "ozaki_set_epilogue_wait_ns": (I, [L]),
@@ -440,6 +454,227 @@ def ozaki1_dgemm_ws(A, B, num_slices: int, workspace, C=None, stream=None):
                                 _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
            "ozaki1_dgemm_ws")
     return C
+
+
+# ------------------------------------------------------------------ grouped products (experts)
+def _dtype(t) -> int:
+    import torch
+
+    code = {torch.bfloat16: OZ_BF16, torch.float16: OZ_F16, torch.float32: OZ_F32}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"dtype must be bfloat16, float16 or float32: {t.dtype}")
+    return code
+
+
+def _tokens(t, what: str, features: int | None = None):
+    """A row-major (rows, features) matrix whose rows may be strided: (tensor, leading dimension)."""
+    if t.dim() != 2 or (features is not None and t.shape[1] != features):
+        raise ValueError(f"{what} must have shape (rows, {'features' if features is None else features}): {tuple(t.shape)}")
+    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{what} must be row-major (stride(1) == 1, stride(0) >= {t.shape[1]})")
+    return t, max(1, int(t.shape[1]), int(t.stride(0)) if t.shape[0] > 1 else 0)
+
+
+def _experts(t, what: str):
+    """A (groups, n, k) stack whose matrices are row-major: (tensor, leading dimension, stride between matrices)."""
+    if t.dim() != 3:
+        raise ValueError(f"{what} must have shape (groups, n, k): {tuple(t.shape)}")
+    g, n, k = t.shape
+    ld = max(1, int(k), int(t.stride(1)) if n > 1 else 0)
+    if (k > 1 and t.stride(2) != 1) or (n > 1 and t.stride(1) < k) or (g > 1 and t.stride(0) < ld * n):
+        raise ValueError(f"{what} must hold row-major matrices that do not overlap")
+    return t, ld, int(t.stride(0)) if g > 1 else ld * int(n)
+
+
+def _offsets(offsets, groups: int | None, device):
+    import torch
+
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() or offsets.device != device:
+        raise ValueError("offsets must be a contiguous int32 vector on the operands' device")
+    if offsets.numel() < 2 or (groups is not None and offsets.numel() != groups + 1):
+        raise ValueError(f"offsets must hold groups + 1 entries: {offsets.numel()} for {groups} groups")
+
+
+def _same(*tensors):
+    first = tensors[0]
+    for t in tensors:
+        if t.dtype != first.dtype or t.device != first.device:
+            raise ValueError("operands must share one dtype and one device")
+        if not t.is_cuda:
+            raise ValueError("operands must be CUDA tensors")
+
+
+def _run_grouped(name, args, dims, out_args, workspace, stream):
+    """Calls `name`, or its _ws form when a workspace (a uint8 tensor) is given."""
+    st = _stream(stream)
+    if workspace is None:
+        _check(getattr(_lib, name)(*dims, *args, *out_args, st), name)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+        _check(getattr(_lib, name + "_ws")(*dims, *args, *out_args, _ptr(workspace), nbytes, st), name + "_ws")
+
+
+def ozaki_grouped_gemm(X, W, offsets, Y=None, workspace=None, stream=None):
+    """Y[r] = W[e] X[r] for the rows r of group e: X (rows, k), W (groups, n, k), offsets (groups + 1) int32.
+
+    bfloat16 or float16; row-major (rows of X and Y, and the matrices of W, may be strided).
+    Rows outside [offsets[0], offsets[-1]) give zero."""
+    import torch
+
+    X, ldx = _tokens(X, "X", W.shape[-1])
+    W, ldw, sw = _experts(W, "W")
+    groups, n, k = W.shape
+    if Y is None:
+        Y = torch.empty((X.shape[0], n), dtype=X.dtype, device=X.device)
+    _same(X, W, Y)
+    _offsets(offsets, groups, X.device)
+    Y, ldy = _tokens(Y, "Y", n)
+    if Y.shape[0] != X.shape[0]:
+        raise ValueError("Y must have the rows of X")
+    _run_grouped("ozaki_grouped_gemm", (_ptr(W), ldw, sw, _ptr(X), ldx, _ptr(offsets)),
+                 (n, k, X.shape[0], groups, _dtype(X)), (_ptr(Y), ldy), workspace, stream)
+    return Y
+
+
+def ozaki_grouped_gemm_ws(X, W, offsets, workspace, Y=None, stream=None):
+    """ozaki_grouped_gemm with a caller-owned workspace (see ozaki_grouped_gemm_workspace_bytes)."""
+    return ozaki_grouped_gemm(X, W, offsets, Y, workspace, stream)
+
+
+def ozaki_grouped_gemm_dgrad(dY, W, offsets, dX=None, workspace=None, stream=None):
+    """dX[r] = W[e]^T dY[r]: the gradient in X of a loss whose gradient in Y is dY (rows, n)."""
+    import torch
+
+    W, ldw, sw = _experts(W, "W")
+    groups, n, k = W.shape
+    dY, lddy = _tokens(dY, "dY", n)
+    if dX is None:
+        dX = torch.empty((dY.shape[0], k), dtype=dY.dtype, device=dY.device)
+    _same(dY, W, dX)
+    _offsets(offsets, groups, dY.device)
+    dX, lddx = _tokens(dX, "dX", k)
+    if dX.shape[0] != dY.shape[0]:
+        raise ValueError("dX must have the rows of dY")
+    _run_grouped("ozaki_grouped_gemm_dgrad", (_ptr(W), ldw, sw, _ptr(dY), lddy, _ptr(offsets)),
+                 (n, k, dY.shape[0], groups, _dtype(dY)), (_ptr(dX), lddx), workspace, stream)
+    return dX
+
+
+def ozaki_grouped_gemm_dgrad_ws(dY, W, offsets, workspace, dX=None, stream=None):
+    """ozaki_grouped_gemm_dgrad with a caller-owned workspace."""
+    return ozaki_grouped_gemm_dgrad(dY, W, offsets, dX, workspace, stream)
+
+
+def ozaki_grouped_gemm_wgrad(dY, X, offsets, dW=None, workspace=None, stream=None):
+    """dW[e] = sum over the rows r of group e of dY[r] X[r]^T: (groups, n, k)."""
+    import torch
+
+    dY, lddy = _tokens(dY, "dY")
+    X, ldx = _tokens(X, "X")
+    if X.shape[0] != dY.shape[0]:
+        raise ValueError("X and dY must have the same rows")
+    _offsets(offsets, None, dY.device)
+    groups, n, k = offsets.numel() - 1, dY.shape[1], X.shape[1]
+    if dW is None:
+        dW = torch.empty((groups, n, k), dtype=dY.dtype, device=dY.device)
+    _same(dY, X, dW)
+    dW, ldw, sw = _experts(dW, "dW")
+    if tuple(dW.shape) != (groups, n, k):
+        raise ValueError(f"dW must have shape {(groups, n, k)}: {tuple(dW.shape)}")
+    _run_grouped("ozaki_grouped_gemm_wgrad", (_ptr(dY), lddy, _ptr(X), ldx, _ptr(offsets)),
+                 (n, k, X.shape[0], groups, _dtype(X)), (_ptr(dW), ldw, sw), workspace, stream)
+    return dW
+
+
+def ozaki_grouped_gemm_wgrad_ws(dY, X, offsets, workspace, dW=None, stream=None):
+    """ozaki_grouped_gemm_wgrad with a caller-owned workspace."""
+    return ozaki_grouped_gemm_wgrad(dY, X, offsets, dW, workspace, stream)
+
+
+def ozaki_grouped_gemm_workspace_bytes(X, W) -> int:
+    """Device workspace of ozaki_grouped_gemm_ws for these operands (alignment decides part of it)."""
+    X, ldx = _tokens(X, "X", W.shape[-1])
+    W, ldw, sw = _experts(W, "W")
+    groups, n, k = W.shape
+    return int(_lib.ozaki_grouped_gemm_workspace_bytes(n, k, X.shape[0], groups, _dtype(X), _ptr(W), ldw, sw, _ptr(X), ldx))
+
+
+def ozaki_grouped_gemm_dgrad_workspace_bytes(dY, W) -> int:
+    """Device workspace of ozaki_grouped_gemm_dgrad_ws for these operands."""
+    W, ldw, sw = _experts(W, "W")
+    groups, n, k = W.shape
+    dY, lddy = _tokens(dY, "dY", n)
+    return int(_lib.ozaki_grouped_gemm_dgrad_workspace_bytes(n, k, dY.shape[0], groups, _dtype(dY), _ptr(W), ldw, sw,
+                                                             _ptr(dY), lddy))
+
+
+def ozaki_grouped_gemm_wgrad_workspace_bytes(dY, X, groups: int) -> int:
+    """Device workspace of ozaki_grouped_gemm_wgrad_ws for these operands."""
+    dY, lddy = _tokens(dY, "dY")
+    X, ldx = _tokens(X, "X")
+    return int(_lib.ozaki_grouped_gemm_wgrad_workspace_bytes(dY.shape[1], X.shape[1], X.shape[0], groups, _dtype(X),
+                                                             _ptr(dY), lddy, _ptr(X), ldx))
+
+
+# ------------------------------------------------------------------ Newton-Schulz orthogonalisation
+NEWTON_SCHULZ_COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+def ozaki_newton_schulz_workspace_bytes(m: int, n: int, batch: int = 1, num_slices: int = 2) -> int:
+    return int(_lib.ozaki_newton_schulz_workspace_bytes(m, n, batch, num_slices))
+
+
+def ozaki_newton_schulz(G, steps: int = 5, coeffs=NEWTON_SCHULZ_COEFFS, eps: float = 1e-7, num_slices: int | None = None,
+                        out=None, workspace=None, stream=None):
+    """Newton-Schulz orthogonalisation of each matrix of G (..., m, n): X = G / (|G|_F + eps), then
+    `steps` times X <- a X + (b A + c A^2) X with A = X X^T (on the smaller side).
+
+    G is bfloat16, float16 or float32; its matrices are row-major (2-D and 3-D G may have strided
+    rows, a 2-D G may be column-major).  coeffs: one (a, b, c) for every step, or one for each.
+    num_slices: FP16 slices of the intermediate matrices; by default 1 for bfloat16 (11 bits kept) and
+    2 otherwise (22 bits).  `out` has G's shape and dtype; by default it is new and row-major
+    (column-major for a column-major G)."""
+    import torch
+
+    if G.dim() < 2 or not G.is_cuda:
+        raise ValueError("G must be a CUDA tensor of shape (..., m, n)")
+    code = _dtype(G)
+    flat = np.ravel(np.asarray(coeffs, dtype=np.float32))
+    if flat.size == 3:
+        flat = np.tile(flat, max(1, steps))
+    if steps < 1 or flat.size != 3 * steps:
+        raise ValueError("coeffs must be one (a, b, c), or one for each of the steps (at least 1)")
+    flat = np.ascontiguousarray(flat)
+    if out is None:
+        turned = G.dim() == 2 and G.stride(0) == 1 and G.stride(1) != 1
+        out = torch.empty((G.shape[1], G.shape[0]), dtype=G.dtype, device=G.device).t() if turned else \
+            torch.empty(G.shape, dtype=G.dtype, device=G.device)
+    if out.shape != G.shape or out.dtype != G.dtype or out.device != G.device:
+        raise ValueError("out must have G's shape, dtype and device")
+    m, n = G.shape[-2:]
+    lead, result = G.shape[:-2], out
+    if G.dim() == 2 and m > 1 and n > 1 and G.stride(0) == 1 and out.stride(0) == 1:
+        G, out, m, n = G.t(), out.t(), n, m  # the transposed problem is the same one
+    batch = 1
+    for d in lead:
+        batch *= d
+    if G.dim() != 3:  # leading dimensions as one (a view: they have to be contiguous)
+        G, out = (G[None], out[None]) if G.dim() == 2 else (G.view(batch, m, n), out.view(batch, m, n))
+    G, ldg, sg = _experts(G, "G")
+    out, ldo, so = _experts(out, "out")
+    ns = num_slices if num_slices is not None else (1 if code == OZ_BF16 else 2)
+    args = (n, m, batch, code, _ptr(G), ldg, sg, _ptr(out), ldo, so, steps, flat.ctypes.data, float(eps), int(ns))
+    if workspace is None:
+        _check(_lib.ozaki_newton_schulz(*args, _stream(stream)), "ozaki_newton_schulz")
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+        _check(_lib.ozaki_newton_schulz_ws(*args, _ptr(workspace), nbytes, _stream(stream)), "ozaki_newton_schulz_ws")
+    return result
+
+
+def ozaki_newton_schulz_ws(G, workspace, **kwargs):
+    """ozaki_newton_schulz with a caller-owned workspace (see ozaki_newton_schulz_workspace_bytes)."""
+    return ozaki_newton_schulz(G, workspace=workspace, **kwargs)
 
 
 # ------------------------------------------------------------------ Scheme I variants

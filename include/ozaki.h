@@ -325,6 +325,90 @@ int ozaki1_dgemm_ex(int m, int n, int k, const double* A, int lda, const double*
 int ozaki2_dgemm_noalloc(int m, int n, int k, const double* A, int lda, const double* B, int ldb,
                          double* C, int ldc, int num_moduli, cudaStream_t stream);
 
+/* ---------------------------------------------------------------- grouped products (experts) */
+
+/* Element types of the entry points below. */
+#define OZ_BF16 1
+#define OZ_F16 2
+#define OZ_F32 3
+
+/* Products of token rows with the weights of the expert they are routed to.  The tokens are
+ * columns, sorted by expert (group): group e owns the columns offsets[e] .. offsets[e+1]-1.
+ * Everything is column-major as elsewhere, so a token's features are contiguous (a row-major
+ * [tokens, features] array) and so are the k inputs of an output feature:
+ *   W_e  k x n   (ldw >= k, one every strideW >= ldw * n elements; a row-major [groups, n, k])
+ *   X, dX  k x rows (ldx, lddx >= k)        Y, dY  n x rows (ldy, lddy >= n)
+ *   ozaki_grouped_gemm        Y_e  = W_e^T X_e
+ *   ozaki_grouped_gemm_dgrad  dX_e = W_e dY_e      (the gradient of a loss in X, dY that in Y)
+ *   ozaki_grouped_gemm_wgrad  dW_e = X_e dY_e^T    (the gradient in W_e)
+ * Elements are OZ_BF16 or OZ_F16 on both sides (dtype); sums are FP32, rounded once.
+ *  - offsets is DEVICE memory, groups + 1 ints, non-decreasing, within [0, rows]; it is read by
+ *    the kernel (no copy to the host, nothing to fix before a graph capture).  Offsets that break
+ *    this are clamped to [the one before, rows], so that no access leaves the matrices, and
+ *    OZ_EINVAL is recorded in the device status word.
+ *  - A group may own no column: it contributes nothing, and its dW_e is zero.  Columns outside
+ *    [offsets[0], offsets[groups]) belong to no group: their Y and dX are zero.
+ *  - 1 <= groups <= OZ_MAX_GROUPS.  n, k or rows equal to 0: an empty sum gives zeros.
+ *  - Inf and NaN follow IEEE arithmetic within their own group; no other group sees them.
+ *  - Any address and leading dimension (of the element's alignment) is accepted; operands whose
+ *    address or strides are not multiples of 16 bytes are first laid out in the workspace.
+ * Results do not depend on timing (parts of a split sum are added in a fixed order). */
+#define OZ_MAX_GROUPS 1024
+
+/* Device workspace of the _ws entry points for these operands (their addresses and strides
+ * decide what has to be laid out; nothing is read).  0 when none is needed, and on invalid
+ * arguments.  No GPU needed. */
+size_t ozaki_grouped_gemm_workspace_bytes(int n, int k, int rows, int groups, int dtype, const void* W, int ldw,
+                                          long long strideW, const void* X, int ldx);
+size_t ozaki_grouped_gemm_dgrad_workspace_bytes(int n, int k, int rows, int groups, int dtype, const void* W, int ldw,
+                                                long long strideW, const void* dY, int lddy);
+size_t ozaki_grouped_gemm_wgrad_workspace_bytes(int n, int k, int rows, int groups, int dtype, const void* dY, int lddy,
+                                                const void* X, int ldx);
+
+/* With the caller's workspace (256-byte aligned; OZ_ENOMEM if too small). */
+int ozaki_grouped_gemm_ws(int n, int k, int rows, int groups, int dtype, const void* W, int ldw, long long strideW,
+                          const void* X, int ldx, const int32_t* offsets, void* Y, int ldy, void* workspace,
+                          size_t ws_bytes, cudaStream_t stream);
+int ozaki_grouped_gemm_dgrad_ws(int n, int k, int rows, int groups, int dtype, const void* W, int ldw, long long strideW,
+                                const void* dY, int lddy, const int32_t* offsets, void* dX, int lddx, void* workspace,
+                                size_t ws_bytes, cudaStream_t stream);
+int ozaki_grouped_gemm_wgrad_ws(int n, int k, int rows, int groups, int dtype, const void* dY, int lddy, const void* X,
+                                int ldx, const int32_t* offsets, void* dW, int ldw, long long strideW, void* workspace,
+                                size_t ws_bytes, cudaStream_t stream);
+
+/* With the workspace from the stream-ordered allocator (as ozaki2_dgemm). */
+int ozaki_grouped_gemm(int n, int k, int rows, int groups, int dtype, const void* W, int ldw, long long strideW,
+                       const void* X, int ldx, const int32_t* offsets, void* Y, int ldy, cudaStream_t stream);
+int ozaki_grouped_gemm_dgrad(int n, int k, int rows, int groups, int dtype, const void* W, int ldw, long long strideW,
+                             const void* dY, int lddy, const int32_t* offsets, void* dX, int lddx, cudaStream_t stream);
+int ozaki_grouped_gemm_wgrad(int n, int k, int rows, int groups, int dtype, const void* dY, int lddy, const void* X,
+                             int ldx, const int32_t* offsets, void* dW, int ldw, long long strideW, cudaStream_t stream);
+
+/* ---------------------------------------------------------------- Newton-Schulz orthogonalisation */
+
+/* O = X_steps of X_0 = G / (|G|_F + eps), X_{i+1} = (a I + b A + c A^2) X_i with A = X_i X_i^T
+ * on the side of the smaller dimension (the polynomial of the singular values is the same on
+ * either side), for each m x n matrix of the batch (ldg, ldo >= m; strides between matrices
+ * >= ld * n).  dtype (OZ_BF16, OZ_F16 or OZ_F32) is that of G and O.  O must not overlap G.
+ *  - coeffs: HOST memory, 3 * steps floats, (a, b, c) of each step; 1 <= steps <= OZ_MAX_NS_STEPS.
+ *    OZ_ERANGE if the polynomials may carry a singular value in [0, 1] above 16, or if
+ *    b^2 / 4c cancels more than 4 bits of a (neither happens for polynomials that converge).
+ *  - num_slices: FP16 slices of every intermediate matrix: 1 keeps 11 bits (three bits more than
+ *    bf16), at one product for each of the formula's; 2 keeps 22 bits at three times the
+ *    tensor-core work, which FP32 results need.  Sums are FP32 in both.
+ *  - eps >= 0.  A zero matrix gives zero; a matrix that holds Inf or NaN gives NaN everywhere.
+ *  - m, n or batch equal to 0: nothing is done.  batch <= 65535. */
+#define OZ_MAX_NS_STEPS 32
+
+/* Device workspace of ozaki_newton_schulz_ws (0 on invalid or empty arguments).  No GPU needed. */
+size_t ozaki_newton_schulz_workspace_bytes(int m, int n, int batch, int num_slices);
+
+int ozaki_newton_schulz_ws(int m, int n, int batch, int dtype, const void* G, int ldg, long long strideG, void* O, int ldo,
+                           long long strideO, int steps, const float* coeffs, float eps, int num_slices, void* workspace,
+                           size_t ws_bytes, cudaStream_t stream);
+int ozaki_newton_schulz(int m, int n, int batch, int dtype, const void* G, int ldg, long long strideG, void* O, int ldo,
+                        long long strideO, int steps, const float* coeffs, float eps, int num_slices, cudaStream_t stream);
+
 /* ---------------------------------------------------------------- status */
 
 /* Waits for the work queued on `stream` (0 = legacy default stream), then returns the

@@ -150,27 +150,29 @@ int run(Problem p, void* workspace, size_t ws_bytes, cudaStream_t stream) {
   a.stride = p.strideo;
   a.vec = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.ldo % 8 == 0 && p.strideo % 8 == 0;
   a.alpha = 1.0f;
-  CUtensorMap tmA, tmB;
+  CUtensorMap tmA, tmB, tmB128;
   const Operand &w = p.w, &t = p.t;
   const uint64_t wl = 2ull * w.ld, tl = 2ull * t.ld;
   if (p.op == kWgrad) {
     // rows addressed as (offset within the group, the group's first row)
     a.idesc = idesc_base(bf16, true, true);
-    if (!make_map(&tmA, w.p, bf16, w.cols, w.rows, w.rows, wl, wl, 64) ||
-        !make_map(&tmB, t.p, bf16, t.cols, t.rows, t.rows, tl, tl, 64))
+    if (!make_mn_map(&tmA, &a.a_4d, 2, w.p, bf16, w.cols, w.rows, w.rows, wl, wl) ||
+        !make_mn_map(&tmB, &a.b_4d, a.bn / 128, t.p, bf16, t.cols, t.rows, t.rows, tl, tl))
       return OZ_ECUDA;
-    return launch<kRaggedK, true, true, 1>(tmA, tmB, a, pairs, false, stream);
+    return launch<kRaggedK, true, true, 1>(tmA, tmB, tmB, a, pairs, false, stream);
   }
   const uint64_t ws2 = w.mats > 1 ? 2ull * w.stride : wl * w.rows;
-  if (!make_map(&tmB, t.p, bf16, t.cols, t.rows, 1, tl, tl * t.rows, BOX_ROWS)) return OZ_ECUDA;
+  if (!make_map(&tmB, t.p, bf16, t.cols, t.rows, 1, tl, tl * t.rows, BOX_ROWS) ||
+      !make_map(&tmB128, t.p, bf16, t.cols, t.rows, 1, tl, tl * t.rows, HALF_N))
+    return OZ_ECUDA;
   if (p.op == kForward) {
     a.idesc = idesc_base(bf16, false, false);
     if (!make_map(&tmA, w.p, bf16, w.cols, w.rows, w.mats, wl, ws2, HALF_M)) return OZ_ECUDA;
-    return launch<kRaggedN, false, false, 1>(tmA, tmB, a, pairs, false, stream);
+    return launch<kRaggedN, false, false, 1>(tmA, tmB, tmB128, a, pairs, false, stream);
   }
   a.idesc = idesc_base(bf16, true, false);
-  if (!make_map(&tmA, w.p, bf16, w.cols, w.rows, w.mats, wl, ws2, 64)) return OZ_ECUDA;
-  return launch<kRaggedN, true, false, 1>(tmA, tmB, a, pairs, false, stream);
+  if (!make_mn_map(&tmA, &a.a_4d, 2, w.p, bf16, w.cols, w.rows, w.mats, wl, ws2)) return OZ_ECUDA;
+  return launch<kRaggedN, true, false, 1>(tmA, tmB, tmB128, a, pairs, false, stream);
 }
 
 int run_allocating(const Problem& p, cudaStream_t stream) {

@@ -396,10 +396,16 @@ int run(int m, int n, int batch, int dtype, const void* G, int ldg, long long st
     auto x_map = [&](CUtensorMap* t, int box) {
       return make_map(t, X[i], false, sh.cols, sh.rows, mats, xl, 2ull * xplane, box);
     };
+    // rows of ldx: the padding past the last column is the workspace's own (a multiple of 64), and
+    // what is read there only reaches output elements that are never stored
+    auto mn_map = [&](CUtensorMap* t, int blocks) {
+      int is_4d = 0;  // 1: ldx is a multiple of 64
+      return make_mn_map(t, &is_4d, blocks, X[i], false, sh.ldx, sh.rows, mats, xl, 2ull * xplane);
+    };
     if (sh.wide)
-      ok = x_map(&gA[i], HALF_M) && x_map(&gB[i], bn_gram / 2) && x_map(&pA[i], 64);
+      ok = x_map(&gA[i], HALF_M) && x_map(&gB[i], bn_gram / 2) && mn_map(&pA[i], 2);
     else
-      ok = x_map(&gA[i], 64) && x_map(&gB[i], 64) && x_map(&pB[i], bn_app / 2);
+      ok = mn_map(&gA[i], 2) && mn_map(&gB[i], bn_gram / 128) && x_map(&pB[i], bn_app / 2);
   }
   if (!ok) return OZ_ECUDA;
 
@@ -410,6 +416,7 @@ int run(int m, int n, int batch, int dtype, const void* G, int ldg, long long st
   base.counters = counters;
   base.max_split_units = sh.split_units();
   base.vec = 1;
+  base.a_4d = base.b_4d = 1;
   base.planes_out = P;
   auto grid = [&](const Args& a) { return a.tiles * a.nsplit < pairs ? a.tiles * a.nsplit : pairs; };
   const int steps = plan.sc.steps;
@@ -436,12 +443,12 @@ int run(int m, int n, int batch, int dtype, const void* G, int ldg, long long st
     g.diag = plan.square[i] ? plan.diag_s[i] : plan.diag_b[i];
     if (sh.wide) {
       g.idesc = idesc_base(false, false, false);
-      rc = P == 2 ? launch<kDense, false, false, 2>(gA[cur], gB[cur], g, grid(g), i > 0, stream)
-                  : launch<kDense, false, false, 1>(gA[cur], gB[cur], g, grid(g), i > 0, stream);
+      rc = P == 2 ? launch<kDense, false, false, 2>(gA[cur], gB[cur], gB[cur], g, grid(g), i > 0, stream)
+                  : launch<kDense, false, false, 1>(gA[cur], gB[cur], gB[cur], g, grid(g), i > 0, stream);
     } else {
       g.idesc = idesc_base(false, true, true);
-      rc = P == 2 ? launch<kDense, true, true, 2>(gA[cur], gB[cur], g, grid(g), i > 0, stream)
-                  : launch<kDense, true, true, 1>(gA[cur], gB[cur], g, grid(g), i > 0, stream);
+      rc = P == 2 ? launch<kDense, true, true, 2>(gA[cur], gB[cur], gB[cur], g, grid(g), i > 0, stream)
+                  : launch<kDense, true, true, 1>(gA[cur], gB[cur], gB[cur], g, grid(g), i > 0, stream);
     }
     if (rc) return rc;
     if (plan.square[i]) {  // B 2^sb = c 2^(sb - 2 sa) (S 2^sa)^2 + 2^sb (a - b^2 / 4c) I
@@ -456,8 +463,8 @@ int run(int m, int n, int batch, int dtype, const void* G, int ldg, long long st
       q.scale = nullptr;
       q.diag = plan.diag_b[i];
       q.idesc = idesc_base(false, false, false);
-      rc = P == 2 ? launch<kDense, false, false, 2>(sA, sB, q, grid(q), true, stream)
-                  : launch<kDense, false, false, 1>(sA, sB, q, grid(q), true, stream);
+      rc = P == 2 ? launch<kDense, false, false, 2>(sA, sB, sB, q, grid(q), true, stream)
+                  : launch<kDense, false, false, 1>(sA, sB, sB, q, grid(q), true, stream);
       if (rc) return rc;
     }
     Args x = base;  // X_{i+1} 2^t' = 2^(t' - t - sb) (B 2^sb)(X_i 2^t)
@@ -487,12 +494,12 @@ int run(int m, int n, int batch, int dtype, const void* G, int ldg, long long st
     }
     if (sh.wide) {  // D[col, row] = sum_j X[j, col] B[row, j]
       x.idesc = idesc_base(false, true, false);
-      rc = P == 2 ? launch<kDense, true, false, 2>(pA[cur], bOp, x, grid(x), true, stream)
-                  : launch<kDense, true, false, 1>(pA[cur], bOp, x, grid(x), true, stream);
+      rc = P == 2 ? launch<kDense, true, false, 2>(pA[cur], bOp, bOp, x, grid(x), true, stream)
+                  : launch<kDense, true, false, 1>(pA[cur], bOp, bOp, x, grid(x), true, stream);
     } else {  // D[col, row] = sum_j B[col, j] X[row, j]
       x.idesc = idesc_base(false, false, false);
-      rc = P == 2 ? launch<kDense, false, false, 2>(bOp, pB[cur], x, grid(x), true, stream)
-                  : launch<kDense, false, false, 1>(bOp, pB[cur], x, grid(x), true, stream);
+      rc = P == 2 ? launch<kDense, false, false, 2>(bOp, pB[cur], pB[cur], x, grid(x), true, stream)
+                  : launch<kDense, false, false, 1>(bOp, pB[cur], pB[cur], x, grid(x), true, stream);
     }
     if (rc) return rc;
   }

@@ -61,7 +61,7 @@ constexpr uint32_t WARP_STASH = 32 * 32 * 2;  // 32 columns x 32 lanes of 16 bit
 constexpr uint32_t STASH = EPI_WARPS * WARP_STASH;
 constexpr int MAX_GROUPS = OZ_MAX_GROUPS;
 constexpr uint32_t TABLE = 2 * (MAX_GROUPS + 1) * 4;  // row offsets and tile prefix of the groups
-constexpr int BOX_ROWS = 32;                 // rows of one TMA box of a K-major B operand
+constexpr int BOX_ROWS = 32;                 // ragged rows: the small box of B (the large one has HALF_N rows)
 constexpr size_t SMEM_DENSE = 1024 + STAGES * STAGE_BYTES + STASH + 256;
 constexpr size_t SMEM_GROUPED = SMEM_DENSE + TABLE;
 static_assert(SMEM_GROUPED <= 232448, "shared memory budget");
@@ -81,7 +81,9 @@ struct Args {
   int chunk;            // MMA steps (16 k) summed in one accumulator
   int out_type, planes_out;
   int vec;              // 16-byte stores are allowed (base and row stride)
-  int box_rows;         // rows of one TMA box of a K-major B operand
+  int box_rows;         // rows of one TMA box of a K-major B operand (ragged rows: of the small one)
+  int a_4d, b_4d;       // MN-major operands: the map is 4-D and its box holds the CTA's whole tile
+                        // (2 blocks of 64 of A, bn / 128 of B); otherwise 3-D, one block a box
   const int32_t* offsets;
   void* out;
   long long ld, stride;  // output row stride, stride between the groups' outputs (elements)
@@ -209,16 +211,25 @@ __device__ __forceinline__ void unit_at(const Args& a, const Schedule& s, int id
   u.kb1 = static_cast<int>(static_cast<long long>(nkb) * (u.split + 1) / s.nsplit);
 }
 
-// Shared-memory descriptor of an MN-major tile: blocks of 64 contiguous m (128 bytes a k row,
-// 128-byte swizzle); 8 k rows are 1024 bytes apart, the next 64 m MN_BLOCK bytes.
-__device__ __forceinline__ uint64_t umma_desc_mn128(uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(MN_BLOCK >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
+// Shared-memory descriptors, low word: address / 16 and the leading byte offset.  K-major tiles:
+// rows of 64 k (128 bytes, 128-byte swizzle), 8 rows are 1024 bytes, no leading offset.
+// MN-major tiles: blocks of 64 contiguous m (128 bytes a k row, 128-byte swizzle), 8 k rows are
+// 1024 bytes, the next 64 m are MN_BLOCK bytes on.  The high word is the same for both.
+template <bool MN>
+__device__ __forceinline__ uint32_t desc_low(uint32_t smem_addr) {
+  return ((smem_addr >> 4) & 0x3FFFu) | ((MN ? MN_BLOCK >> 4 : 1u) << 16);
+}
+constexpr uint32_t DESC_HIGH = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride, version, 128-byte swizzle
+
+__device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(DESC_HIGH)
+      : "memory");
 }
 
 // Instruction descriptor of kind::f16 with FP32 accumulation, without its N field.
@@ -356,7 +367,7 @@ __device__ __forceinline__ void emit(const Args& a, const Unit& u, float (&v)[32
 template <int MODE, bool A_MN, bool B_MN, int PLANES>
 __global__ void __launch_bounds__(THREADS, 1)
     product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ Args a) {
+                   const __grid_constant__ CUtensorMap tmB128, const __grid_constant__ Args a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
@@ -398,6 +409,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_fence_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
+    if (MODE == kRaggedN) tma_prefetch_desc(&tmB128);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, TMEM_COLS);
@@ -483,8 +495,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int rowA = u.m0 + static_cast<int>(rank) * HALF_M;
         const int half_n = u.nmma >> 1;
         const int rowB = u.n0 + static_cast<int>(rank) * half_n;
-        const int boxes = B_MN ? half_n / 64 : ceil_div(half_n, a.box_rows);
-        const uint32_t bytes = A_STAGE + (B_MN ? boxes * MN_BLOCK : boxes * a.box_rows * BK * 2);
+        // Few TMA instructions a stage: their issue, not the bytes, is what a stage waits for first.
+        const bool wide_b = MODE == kRaggedN && half_n > 64;
+        const int box_b = wide_b ? HALF_N : a.box_rows;
+        const int boxes = B_MN ? (a.b_4d ? 1 : half_n / 64) : ceil_div(half_n, box_b);
+        const CUtensorMap* mapB = wide_b ? &tmB128 : &tmB;
+        const uint32_t box_bytes = B_MN ? (a.b_4d ? a.bn / 128 : 1) * MN_BLOCK : box_b * BK * 2;
+        const uint32_t bytes = A_STAGE + boxes * box_bytes;
         for (int kb = u.kb0; kb < u.kb1 && !*abort_flag; ++kb) {
 #pragma unroll
           for (int p = 0; p < PLANES; ++p) {
@@ -495,22 +512,26 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
             mbar_arrive_expect_tx_cluster(bar, bytes);
             const int k = u.k0 + kb * BK;
-            // third coordinate: matrix (slice) of the batch, or the group's first row
+            // last coordinate: matrix (slice) of the batch, or the group's first row
             const int zA = MODE == kRaggedK ? u.kstart : u.group * PLANES + p;
             const int zB = MODE == kDense ? u.group * PLANES + p : (MODE == kRaggedK ? u.kstart : 0);
             uint8_t* dA = sA + stage * A_STAGE;
             uint8_t* dB = sB + stage * B_STAGE;
-            if (A_MN) {
+            if (!A_MN) {
+              tma_load_3d_pair(dA, &tmA, bar, k, rowA, zA);
+            } else if (a.a_4d) {
+              tma_load_4d_pair(dA, &tmA, bar, 0, k, rowA / 64, zA);
+            } else {
               tma_load_3d_pair(dA, &tmA, bar, rowA, k, zA);
               tma_load_3d_pair(dA + MN_BLOCK, &tmA, bar, rowA + 64, k, zA);
-            } else {
-              tma_load_3d_pair(dA, &tmA, bar, k, rowA, zA);
             }
-            for (int b = 0; b < boxes; ++b) {
-              if (B_MN)
-                tma_load_3d_pair(dB + b * MN_BLOCK, &tmB, bar, rowB + 64 * b, k, zB);
-              else
-                tma_load_3d_pair(dB + b * a.box_rows * BK * 2, &tmB, bar, k, rowB + a.box_rows * b, zB);
+            if (!B_MN) {
+              tma_load_3d_pair(dB, mapB, bar, k, rowB, zB);
+              for (int b = 1; b < boxes; ++b) tma_load_3d_pair(dB + b * box_bytes, mapB, bar, k, rowB + box_b * b, zB);
+            } else if (a.b_4d) {  // a last, narrower tile loads the full box: B_STAGE has room for it
+              tma_load_4d_pair(dB, &tmB, bar, 0, k, rowB / 64, zB);
+            } else {
+              for (int b = 0; b < boxes; ++b) tma_load_3d_pair(dB + b * MN_BLOCK, mapB, bar, rowB + 64 * b, k, zB);
             }
             ++issued;
             if (++stage == STAGES) {
@@ -545,43 +566,58 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t g = 0;
       uint32_t consumed = 0;
       bool ok = true;
+      // Low words of stage 0's descriptors; a stage or a k step only adds to the address field.
+      constexpr uint32_t A_STEP = (A_MN ? UMMA_K * 128 : UMMA_K * 2) >> 4, B_STEP = (B_MN ? UMMA_K * 128 : UMMA_K * 2) >> 4;
+      const uint32_t a_desc = desc_low<A_MN>(smem_u32(sA)), b_desc = desc_low<B_MN>(smem_u32(sB));
       for (int idx = sched.first; idx < sched.total && ok && !*abort_flag; idx += sched.step) {
         Unit u;
         unit_at<MODE, B_MN>(a, sched, idx, u);
         const uint32_t idesc = a.idesc | (static_cast<uint32_t>(u.nmma >> 3) << 17);
-        const int nsteps = (u.kb1 - u.kb0) * KSTEPS;
-        int in_chunk = 0;
-        uint32_t d_tmem = 0;
-        for (int t = 0; t < nsteps && ok; t += KSTEPS) {
+        int left = u.kb1 - u.kb0;
+        if (left == 0) continue;
+        uint32_t in_chunk = 0, d_tmem = 0;
+        if (PLANES == 1) {  // the whole part in one accumulator
+          if (!mbar_wait_or_abort(&accempty[g & 1], ((g >> 1) & 1) ^ 1, kWaitLimitNs, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          d_tmem = tmem_base + (g & 1) * BN;
+        }
+        for (; left > 0; --left) {
 #pragma unroll
           for (int p = 0; p < PLANES; ++p) {
-            if (ok && !mbar_wait_or_abort(&full[stage + p], phase, kWaitLimitNs, abort_flag)) ok = false;
-            if (ok) ++consumed;
+            if (!mbar_wait_or_abort(&full[stage + p], phase, kWaitLimitNs, abort_flag)) {
+              ok = false;
+              break;
+            }
+            ++consumed;
           }
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(sA + stage * A_STAGE), b_addr = smem_u32(sB + stage * B_STAGE);
+          const uint32_t ad = a_desc + stage * (A_STAGE >> 4), bd = b_desc + stage * (B_STAGE >> 4);
 #pragma unroll
           for (int kk = 0; kk < KSTEPS; ++kk) {
-            if (in_chunk == 0) {  // a new sum: the next accumulator
-              if (!mbar_wait_or_abort(&accempty[g & 1], ((g >> 1) & 1) ^ 1, kWaitLimitNs, abort_flag)) {
-                ok = false;
-                break;
+            if (PLANES == 1) {
+              umma_pair(d_tmem, ad + kk * A_STEP, bd + kk * B_STEP, idesc, kk > 0 ? 1u : in_chunk);
+              in_chunk = 1;
+            } else {
+              if (in_chunk == 0) {  // a new sum: the next accumulator
+                if (!mbar_wait_or_abort(&accempty[g & 1], ((g >> 1) & 1) ^ 1, kWaitLimitNs, abort_flag)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+                d_tmem = tmem_base + (g & 1) * BN;
               }
-              tc_fence_after();
-              d_tmem = tmem_base + (g & 1) * BN;
-            }
-#pragma unroll
-            for (int q = 0; q < (PLANES == 2 ? 3 : 1); ++q) {  // h h', h l', l h'
-              const uint32_t aa = a_addr + (q == 2 ? A_STAGE : 0), bb = b_addr + (q == 1 ? B_STAGE : 0);
-              const uint64_t ad = A_MN ? umma_desc_mn128(aa + kk * UMMA_K * 128) : umma_desc_k128(aa + kk * UMMA_K * 2);
-              const uint64_t bd = B_MN ? umma_desc_mn128(bb + kk * UMMA_K * 128) : umma_desc_k128(bb + kk * UMMA_K * 2);
-              umma_bf16_pair(d_tmem + (q ? CROSS : 0), ad, bd, idesc, (in_chunk > 0 || q > 1) ? 1u : 0u);
-            }
-            if (++in_chunk == a.chunk || t + kk + 1 == nsteps) {
-              umma_commit_pair(&accfull[g & 1], 0x3);
-              in_chunk = 0;
-              ++g;
+              umma_pair(d_tmem, ad + kk * A_STEP, bd + kk * B_STEP, idesc, in_chunk);                              // h h'
+              umma_pair(d_tmem + CROSS, ad + kk * A_STEP, bd + (B_STAGE >> 4) + kk * B_STEP, idesc, in_chunk);     // h l'
+              umma_pair(d_tmem + CROSS, ad + (A_STAGE >> 4) + kk * A_STEP, bd + kk * B_STEP, idesc, 1u);           // l h'
+              if (++in_chunk == static_cast<uint32_t>(a.chunk) || (left == 1 && kk + 1 == KSTEPS)) {
+                umma_commit_pair(&accfull[g & 1], 0x3);
+                in_chunk = 0;
+                ++g;
+              }
             }
           }
           if (!ok) break;
@@ -592,6 +628,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             stage = 0;
             phase ^= 1;
           }
+        }
+        if (!ok) break;
+        if (PLANES == 1) {
+          umma_commit_pair(&accfull[g & 1], 0x3);
+          ++g;
         }
       }
       if (!ok && !*abort_flag) stop_pair(abort_flag, a.status);
@@ -780,23 +821,40 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ------------------------------------------------------------------ host side
-// 3-D map of 16-bit elements: box {64, box_rows, 1}, 128-byte swizzle, zeros out of bounds.
-// strides in bytes of the second and third dimension (multiples of 16).
+// An operand's tensor map: 16-bit elements, 128-byte swizzle, zeros out of bounds.
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline bool encode(CUtensorMap* map, const void* base, bool bf16, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                   const cuuint32_t* box) {
+  const EncodeTiled fn = reinterpret_cast<EncodeTiled>(tensor_map_encoder());
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn && fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [d2][d1][d0] with strides s1, s2 in bytes (multiples of 16); box {64, box_rows, 1}.
 inline bool make_map(CUtensorMap* map, const void* base, bool bf16, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
                      uint64_t s2, int box_rows) {
-  void* fn = tensor_map_encoder();
-  if (!fn) return false;
-  typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  cuuint64_t dims[3] = {d0, d1, d2};
-  cuuint64_t strides[2] = {s1, s2};
-  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return reinterpret_cast<Encode>(fn)(
-             map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base),
-             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {s1, s2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  return encode(map, base, bf16, 3, dims, strides, box);
+}
+
+// The same matrix for an MN-major operand: when d0 is a multiple of 64, a 4-D map
+// [d2][d0 / 64][d1][64] whose box is 64 rows by `blocks` blocks of 64 contiguous elements; otherwise
+// (a last partial block in such a map would reach past the end of the last row) make_map's, one
+// block a box.  *is_4d says which: a load's rank has to be its map's.
+inline bool make_mn_map(CUtensorMap* map, int* is_4d, int blocks, const void* base, bool bf16, uint64_t d0, uint64_t d1,
+                        uint64_t d2, uint64_t s1, uint64_t s2) {
+  *is_4d = d0 % 64 == 0;
+  if (!*is_4d) return make_map(map, base, bf16, d0, d1, d2, s1, s2, BK);
+  const cuuint64_t dims[4] = {64, d1, d0 / 64, d2}, strides[3] = {s1, 128, s2};
+  const cuuint32_t box[4] = {64, BK, static_cast<cuuint32_t>(blocks), 1};
+  return encode(map, base, bf16, 4, dims, strides, box);
 }
 
 inline int sm_pairs(int* pairs) {
@@ -810,7 +868,7 @@ inline int sm_pairs(int* pairs) {
 // Launches the product on `pairs` CTA pairs.  dependent: the launch may begin while the one
 // before it on the stream ends (the kernel waits for it before it reads anything).
 template <int MODE, bool A_MN, bool B_MN, int PLANES>
-int launch(const CUtensorMap& tmA, const CUtensorMap& tmB, Args a, int pairs, bool dependent, cudaStream_t stream) {
+int launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmB128, Args a, int pairs, bool dependent, cudaStream_t stream) {
   auto kernel = product_kernel<MODE, A_MN, B_MN, PLANES>;
   const size_t smem = MODE == kDense ? SMEM_DENSE : SMEM_GROUPED;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
@@ -832,7 +890,7 @@ int launch(const CUtensorMap& tmA, const CUtensorMap& tmB, Args a, int pairs, bo
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = dependent ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, a) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmB128, a) != cudaSuccess) {
     cudaGetLastError();
     return OZ_ECUDA;
   }

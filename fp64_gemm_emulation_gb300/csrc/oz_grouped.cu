@@ -119,8 +119,10 @@ int run(Problem p, void* workspace, size_t ws_bytes, cudaStream_t stream) {
   if (!p.w.p || !p.t.p) return OZ_EINVAL;
   const size_t need = p.workspace();
   if (need && (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255))) return OZ_ENOMEM;
-  int pairs, rc;
-  if ((rc = sm_pairs(&pairs))) return rc;
+  Device dev;
+  int rc;
+  if ((rc = current_device(&dev))) return rc;
+  const int pairs = dev.pairs;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   Args a{};
   if (p.may_split()) {
@@ -159,7 +161,7 @@ int run(Problem p, void* workspace, size_t ws_bytes, cudaStream_t stream) {
     if (!make_mn_map(&tmA, &a.a_4d, 2, w.p, bf16, w.cols, w.rows, w.rows, wl, wl) ||
         !make_mn_map(&tmB, &a.b_4d, a.bn / 128, t.p, bf16, t.cols, t.rows, t.rows, tl, tl))
       return OZ_ECUDA;
-    return launch<kRaggedK, true, true, 1>(tmA, tmB, tmB, a, pairs, false, stream);
+    return launch<kRaggedK, true, true, 1>(tmA, tmB, tmB, a, dev, pairs, false, stream);
   }
   const uint64_t ws2 = w.mats > 1 ? 2ull * w.stride : wl * w.rows;
   if (!make_map(&tmB, t.p, bf16, t.cols, t.rows, 1, tl, tl * t.rows, BOX_ROWS) ||
@@ -168,11 +170,11 @@ int run(Problem p, void* workspace, size_t ws_bytes, cudaStream_t stream) {
   if (p.op == kForward) {
     a.idesc = idesc_base(bf16, false, false);
     if (!make_map(&tmA, w.p, bf16, w.cols, w.rows, w.mats, wl, ws2, HALF_M)) return OZ_ECUDA;
-    return launch<kRaggedN, false, false, 1>(tmA, tmB, tmB128, a, pairs, false, stream);
+    return launch<kRaggedN, false, false, 1>(tmA, tmB, tmB128, a, dev, pairs, false, stream);
   }
   a.idesc = idesc_base(bf16, true, false);
   if (!make_mn_map(&tmA, &a.a_4d, 2, w.p, bf16, w.cols, w.rows, w.mats, wl, ws2)) return OZ_ECUDA;
-  return launch<kRaggedN, true, false, 1>(tmA, tmB, tmB128, a, pairs, false, stream);
+  return launch<kRaggedN, true, false, 1>(tmA, tmB, tmB128, a, dev, pairs, false, stream);
 }
 
 int run_allocating(const Problem& p, cudaStream_t stream) {

@@ -355,8 +355,10 @@ int run(int m, int n, int batch, int dtype, const void* G, int ldg, long long st
         cudaStream_t stream) {
   const Shape sh(m, n, batch, slices);
   if (!workspace || ws_bytes < sh.total() || (reinterpret_cast<uintptr_t>(workspace) & 255)) return OZ_ENOMEM;
-  int pairs, rc;
-  if ((rc = sm_pairs(&pairs))) return rc;
+  Device dev;
+  int rc;
+  if ((rc = current_device(&dev))) return rc;
+  const int pairs = dev.pairs;
   uint8_t* at = static_cast<uint8_t*>(workspace);
   auto take = [&](size_t bytes) {
     uint8_t* p = at;
@@ -443,12 +445,12 @@ int run(int m, int n, int batch, int dtype, const void* G, int ldg, long long st
     g.diag = plan.square[i] ? plan.diag_s[i] : plan.diag_b[i];
     if (sh.wide) {
       g.idesc = idesc_base(false, false, false);
-      rc = P == 2 ? launch<kDense, false, false, 2>(gA[cur], gB[cur], gB[cur], g, grid(g), i > 0, stream)
-                  : launch<kDense, false, false, 1>(gA[cur], gB[cur], gB[cur], g, grid(g), i > 0, stream);
+      rc = P == 2 ? launch<kDense, false, false, 2>(gA[cur], gB[cur], gB[cur], g, dev, grid(g), i > 0, stream)
+                  : launch<kDense, false, false, 1>(gA[cur], gB[cur], gB[cur], g, dev, grid(g), i > 0, stream);
     } else {
       g.idesc = idesc_base(false, true, true);
-      rc = P == 2 ? launch<kDense, true, true, 2>(gA[cur], gB[cur], gB[cur], g, grid(g), i > 0, stream)
-                  : launch<kDense, true, true, 1>(gA[cur], gB[cur], gB[cur], g, grid(g), i > 0, stream);
+      rc = P == 2 ? launch<kDense, true, true, 2>(gA[cur], gB[cur], gB[cur], g, dev, grid(g), i > 0, stream)
+                  : launch<kDense, true, true, 1>(gA[cur], gB[cur], gB[cur], g, dev, grid(g), i > 0, stream);
     }
     if (rc) return rc;
     if (plan.square[i]) {  // B 2^sb = c 2^(sb - 2 sa) (S 2^sa)^2 + 2^sb (a - b^2 / 4c) I
@@ -463,8 +465,8 @@ int run(int m, int n, int batch, int dtype, const void* G, int ldg, long long st
       q.scale = nullptr;
       q.diag = plan.diag_b[i];
       q.idesc = idesc_base(false, false, false);
-      rc = P == 2 ? launch<kDense, false, false, 2>(sA, sB, sB, q, grid(q), true, stream)
-                  : launch<kDense, false, false, 1>(sA, sB, sB, q, grid(q), true, stream);
+      rc = P == 2 ? launch<kDense, false, false, 2>(sA, sB, sB, q, dev, grid(q), true, stream)
+                  : launch<kDense, false, false, 1>(sA, sB, sB, q, dev, grid(q), true, stream);
       if (rc) return rc;
     }
     Args x = base;  // X_{i+1} 2^t' = 2^(t' - t - sb) (B 2^sb)(X_i 2^t)
@@ -494,12 +496,12 @@ int run(int m, int n, int batch, int dtype, const void* G, int ldg, long long st
     }
     if (sh.wide) {  // D[col, row] = sum_j X[j, col] B[row, j]
       x.idesc = idesc_base(false, true, false);
-      rc = P == 2 ? launch<kDense, true, false, 2>(pA[cur], bOp, bOp, x, grid(x), true, stream)
-                  : launch<kDense, true, false, 1>(pA[cur], bOp, bOp, x, grid(x), true, stream);
+      rc = P == 2 ? launch<kDense, true, false, 2>(pA[cur], bOp, bOp, x, dev, grid(x), true, stream)
+                  : launch<kDense, true, false, 1>(pA[cur], bOp, bOp, x, dev, grid(x), true, stream);
     } else {  // D[col, row] = sum_j B[col, j] X[row, j]
       x.idesc = idesc_base(false, false, false);
-      rc = P == 2 ? launch<kDense, false, false, 2>(bOp, pB[cur], pB[cur], x, grid(x), true, stream)
-                  : launch<kDense, false, false, 1>(bOp, pB[cur], pB[cur], x, grid(x), true, stream);
+      rc = P == 2 ? launch<kDense, false, false, 2>(bOp, pB[cur], pB[cur], x, dev, grid(x), true, stream)
+                  : launch<kDense, false, false, 1>(bOp, pB[cur], pB[cur], x, dev, grid(x), true, stream);
     }
     if (rc) return rc;
   }

@@ -31,6 +31,8 @@
 // drains what it issued and returns.
 #pragma once
 
+#include <atomic>
+
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -238,8 +240,14 @@ __host__ __device__ constexpr uint32_t idesc_base(bool bf16, bool a_mn, bool b_m
          (static_cast<uint32_t>(BM >> 4) << 24);
 }
 
-__device__ __forceinline__ uint16_t to16(float v, bool bf16) {
-  return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+// Two values as 16-bit elements, the first in the low half.
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool bf16) {
+  if (bf16) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
 }
 
 __device__ __forceinline__ void stop_pair(volatile int* abort_flag, int* status) {
@@ -256,113 +264,171 @@ __device__ __forceinline__ bool warps_meet(uint64_t* bar, uint32_t& phase, const
   return ok;
 }
 
-// Writes 32 lanes x 32 columns of 16-bit values: element (lane l, column i) is out[i * ld + l].
-// Through the warp's stash as [column][lane], then 16-byte stores, four per column.
-__device__ __forceinline__ void store16(const uint16_t (&h)[32], uint16_t* stash, uint16_t* out, long long ld, int cols,
-                                        int lanes, bool vec) {
+// The epilogue works on blocks of 32 m x 32 n.  tcgen05.ld.16x256b gives a thread the elements
+//   m = 16 (i / 16) + lane / 4 + 8 ((i / 2) % 2),   n = 8 ((i / 4) % 4) + 2 (lane % 4) + i % 2
+// in register i: the fragments that stmatrix stores, as they are (rows of m) or transposed (rows
+// of n), so a block goes through the warp's 2 KB stash with 4 + 4 shared-memory instructions and
+// leaves as 16-byte stores in either orientation.  (One lane per m, 32 two-byte stores a block:
+// the epilogue took 7600 cycles of a 256 x 256 tile and bounded the weight gradient.)
+__device__ __forceinline__ int frag_m(int i, int lane) { return ((i >> 4) << 4) + (lane >> 2) + ((i >> 1 & 1) << 3); }
+__device__ __forceinline__ int frag_n(int i, int lane) { return ((i >> 2 & 3) << 3) + ((lane & 3) << 1) + (i & 1); }
+
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr));
+}
+
+// 32 lanes (from the address's) x 32 columns; the values are there after tmem_wait_block.
+__device__ __forceinline__ void tmem_ld_block(uint32_t taddr, float (&v)[32]) {
+  tmem_ld_frag(taddr, v);
+  tmem_ld_frag(taddr + (16u << 16), v + 16);
+}
+
+// Waits for this thread's tensor-memory loads; v passes through, so that no use of it moves above.
+__device__ __forceinline__ void tmem_wait_block(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+  asm volatile(""
+               : "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
+
+// A row of the stash is 64 bytes; its 16-byte parts are permuted so that neither the fragments'
+// stores (8 rows, one part) nor the 16-byte loads (2 rows, 4 parts) conflict.
+__device__ __forceinline__ uint32_t stash_at(int row, int part) {
+  return static_cast<uint32_t>(row * 64 + ((part ^ (row >> 1 & 3)) << 4));
+}
+
+template <bool TRANS>
+__device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  if (TRANS)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1),
+                 "r"(r2), "r"(r3)
+                 : "memory");
+  else
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1), "r"(r2),
+                 "r"(r3)
+                 : "memory");
+}
+
+// Writes a block of 16-bit values, w[i / 2] holding elements i and i + 1.  ROWS_N: rows of n, element
+// (m, n) at out[n * ld + m]; otherwise rows of m, at out[m * ld + n].  rows, width: how much of it exists.
+template <bool ROWS_N>
+__device__ __forceinline__ void store_block(const uint32_t (&w)[16], uint8_t* stash, uint16_t* out, long long ld, int rows,
+                                            int width, bool vec) {
   const int lane = threadIdx.x & 31;
-  if (vec && lanes > 0) {
+  const uint32_t base = smem_u32(stash);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) stash[i * 32 + lane] = h[i];
-    __syncwarp();
+  for (int j = 0; j < 4; ++j) {
+    if (ROWS_N)  // the four 8-element groups of m, rows n = 8 j ..
+      stmatrix4<true>(base + stash_at(8 * j + (lane & 7), lane >> 3), w[2 * j], w[2 * j + 1], w[8 + 2 * j], w[9 + 2 * j]);
+    else  // the four 8-element groups of n, rows m = 8 j ..
+      stmatrix4<false>(base + stash_at(8 * j + (lane & 7), lane >> 3), w[(j >> 1) * 8 + (j & 1)],
+                       w[(j >> 1) * 8 + 2 + (j & 1)], w[(j >> 1) * 8 + 4 + (j & 1)], w[(j >> 1) * 8 + 6 + (j & 1)]);
+  }
+  __syncwarp();
+  if (vec && width == 32) {
+    uint4 x[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int q = j * 32 + lane, col = q >> 2, at = (q & 3) * 8;
-      if (col < cols) {
-        if (at + 8 <= lanes) {
-          *reinterpret_cast<uint4*>(out + col * ld + at) = *reinterpret_cast<const uint4*>(stash + col * 32 + at);
-        } else {
-          for (int e = at; e < lanes; ++e) out[col * ld + e] = stash[col * 32 + e];
-        }
-      }
-    }
-    __syncwarp();
-  } else if (lane < lanes) {
+    for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4*>(stash + stash_at(8 * j + (lane >> 2), lane & 3));
+    uint16_t* dst = out + (lane >> 2) * ld + (lane & 3) * 8;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (8 * j + (lane >> 2) < rows) *reinterpret_cast<uint4*>(dst + 8 * j * ld) = x[j];
+  } else if (lane < width) {
+    for (int r = 0; r < rows; ++r)
+      out[r * ld + lane] = *reinterpret_cast<const uint16_t*>(stash + stash_at(r, lane >> 3) + (lane & 7) * 2);
+  }
+  __syncwarp();
+}
+
+// The finished sums of one block, whose first m is mrow within the tile and first n is c0.  f: their factor (dense).
+template <int MODE>
+__device__ __forceinline__ void emit(const Args& a, const Unit& u, float f, float (&v)[32], int mrow, int c0,
+                                     uint8_t* stash) {
+  const int lane = threadIdx.x & 31;
+  const int m = u.m0 + mrow;
+  const int ncount = min(32, u.nn - c0);
+  const int mcount = min(32, a.M - m);
+  if (ncount <= 0 || mcount <= 0) return;
+  const bool bf16 = a.out_type == kOutBf16;
+  const int n = u.orow + c0;
+  uint32_t w[16];
+  if (MODE != kDense) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) w[i >> 1] = pack16(v[i], v[i + 1], bf16);
+    uint16_t* out = static_cast<uint16_t*>(a.out) + (MODE == kRaggedN ? 0 : u.group * a.stride) + n * a.ld + m;
+    store_block<true>(w, stash, out, a.ld, ncount, mcount, a.vec);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] *= f;
+  if (a.sym && m == n) {  // blocks and tiles start at multiples of 32
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-      if (i < cols) out[i * ld + lane] = h[i];
+      if (frag_m(i, lane) == frag_n(i, lane)) v[i] += a.diag;
+  }
+  if (a.out_type == kOutF32) {
+    float* out = static_cast<float*>(a.out) + u.group * a.stride + n * a.ld + m;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const int mi = frag_m(i, lane), ni = frag_n(i, lane);
+      if (mi < mcount && ni < ncount) out[ni * a.ld + mi] = v[i];
+    }
+    return;
+  }
+  uint16_t* out = static_cast<uint16_t*>(a.out) + u.group * a.stride;
+  const int np = a.out_type == kOutSlices ? a.planes_out : 1;
+  for (int p = 0; p < np; ++p, out += a.plane) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      w[i >> 1] = pack16(v[i], v[i + 1], bf16);
+      if (np > 1) {  // what the slice leaves
+        const __half2 h = *reinterpret_cast<const __half2*>(&w[i >> 1]);
+        v[i] -= __low2float(h);
+        v[i + 1] -= __high2float(h);
+      }
+    }
+    if (!a.sym) {
+      store_block<true>(w, stash, out + n * a.ld + m, a.ld, ncount, mcount, a.vec);
+    } else if (n < m) {  // below the diagonal: both copies
+      store_block<true>(w, stash, out + n * a.ld + m, a.ld, ncount, mcount, a.vec);
+      store_block<false>(w, stash, out + m * a.ld + n, a.ld, mcount, ncount, a.vec);
+    } else if (n == m) {  // on it: the block is its own mirror
+      store_block<true>(w, stash, out + n * a.ld + m, a.ld, ncount, mcount, a.vec);
+    }
   }
 }
 
-// The finished sums of one 32 x 32 block (lane = output element m, register = output row).
-template <int MODE>
-__device__ __forceinline__ void emit(const Args& a, const Unit& u, float (&v)[32], int mrow, int c0, uint16_t* stash) {
-  const int lane = threadIdx.x & 31;
-  const int m = u.m0 + mrow;           // first element of the warp's lanes
-  const int cols = min(32, u.nn - c0);
-  const int lanes = min(32, a.M - m);
-  if (cols <= 0 || lanes <= 0) return;
-  const long long base = static_cast<long long>(u.group) * a.stride;
-  const bool bf16 = a.out_type == kOutBf16;
-  if (MODE != kDense) {
-    uint16_t h[32];
+// One block of a split sum's part: 16 bytes a thread and instruction.
+__device__ __forceinline__ void put_part(float* part, const float (&v)[32]) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) h[i] = to16(v[i], bf16);
-    uint16_t* out = static_cast<uint16_t*>(a.out) + (MODE == kRaggedN ? 0 : base) + (u.orow + c0) * a.ld + m;
-    store16(h, stash, out, a.ld, cols, lanes, a.vec);
-    return;
-  }
-  const float f = a.scale ? a.alpha * a.scale[u.group * a.scale_stride] : a.alpha;
-  const int n = u.orow + c0;
+  for (int i = 0; i < 32; i += 4)
+    __stcg(reinterpret_cast<float4*>(part + i * 32), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+}
+__device__ __forceinline__ void add_part(const float* part, float (&v)[32]) {
+  float4 x[8];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] *= f;
-  if (a.diag != 0.0f && a.sym) {
+  for (int i = 0; i < 8; ++i) x[i] = __ldcg(reinterpret_cast<const float4*>(part + i * 128));
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (m + lane == n + i) v[i] += a.diag;
-  }
-  if (a.out_type == kOutF32) {
-    float* out = static_cast<float*>(a.out) + base + n * a.ld + m + lane;
-    if (lane < lanes) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < cols) out[i * a.ld] = v[i];
-    }
-    return;
-  }
-  uint16_t* out = static_cast<uint16_t*>(a.out) + base;
-  const int np = a.out_type == kOutSlices ? a.planes_out : 1;
-  for (int p = 0; p < np; ++p, out += a.plane) {
-    uint16_t h[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      h[i] = to16(v[i], bf16);
-      if (np > 1) v[i] -= __half2float(__ushort_as_half(h[i]));
-    }
-    if (!a.sym) {
-      store16(h, stash, out + n * a.ld + m, a.ld, cols, lanes, a.vec);
-    } else if (n + 32 <= m) {  // wholly below the diagonal: both copies in full
-      store16(h, stash, out + n * a.ld + m, a.ld, cols, lanes, a.vec);
-      if (lane < lanes) {
-        uint16_t* row = out + (m + lane) * a.ld + n;
-        if (a.vec && cols == 32) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            uint4 w;
-            w.x = h[i] | (static_cast<uint32_t>(h[i + 1]) << 16);
-            w.y = h[i + 2] | (static_cast<uint32_t>(h[i + 3]) << 16);
-            w.z = h[i + 4] | (static_cast<uint32_t>(h[i + 5]) << 16);
-            w.w = h[i + 6] | (static_cast<uint32_t>(h[i + 7]) << 16);
-            *reinterpret_cast<uint4*>(row + i) = w;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i < cols) row[i] = h[i];
-        }
-      }
-    } else if (n <= m + 31) {  // on the diagonal: n <= m only, and its mirror, each once
-      if (lane < lanes) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (i < cols && n + i <= m + lane) {
-            out[(n + i) * a.ld + m + lane] = h[i];
-            if (n + i < m + lane) out[(m + lane) * a.ld + n + i] = h[i];
-          }
-      }
-    }
+  for (int i = 0; i < 8; ++i) {
+    v[4 * i] += x[i].x;
+    v[4 * i + 1] += x[i].y;
+    v[4 * i + 2] += x[i].z;
+    v[4 * i + 3] += x[i].w;
   }
 }
+
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <int MODE, bool A_MN, bool B_MN, int PLANES>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -415,10 +481,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc_pair(tmem_slot, TMEM_COLS);
     tmem_relinquish_pair();
   }
-  // Everything above is this launch's own; what earlier launches wrote is read below.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The next launch may set itself up meanwhile.  Dense launches come in chains: what touches the
+  // matrices waits for the launch before (the producer's first load, the epilogue's first store).
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (MODE != kDense) {
+    wait_for_previous();
     for (int i = threadIdx.x; i <= a.groups; i += THREADS) tab_off[i] = a.offsets[i];
     __syncthreads();
     if (warp == 0) {
@@ -502,6 +569,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const CUtensorMap* mapB = wide_b ? &tmB128 : &tmB;
         const uint32_t box_bytes = B_MN ? (a.b_4d ? a.bn / 128 : 1) * MN_BLOCK : box_b * BK * 2;
         const uint32_t bytes = A_STAGE + boxes * box_bytes;
+        if (MODE == kDense && idx == sched.first) wait_for_previous();
         for (int kb = u.kb0; kb < u.kb1 && !*abort_flag; ++kb) {
 #pragma unroll
           for (int p = 0; p < PLANES; ++p) {
@@ -661,7 +729,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int half = (warp - 2) >> 2;
     const int etid = threadIdx.x - 64;
     const int mrow = static_cast<int>(rank) * HALF_M + quad * 32;
-    uint16_t* my_stash = reinterpret_cast<uint16_t*>(stash + (warp - 2) * WARP_STASH);
+    uint8_t* my_stash = stash + (warp - 2) * WARP_STASH;
     uint32_t g = 0, eph = 0;
     bool ok = true;
     if (MODE == kRaggedN) {  // rows that belong to no group are zero
@@ -676,12 +744,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       Unit u;
       unit_at<MODE, B_MN>(a, sched, idx, u);
       const int nblocks = ceil_div(u.nn, 32);  // this warp: blocks half, half + 2, ...
+      if (MODE == kDense && idx == sched.first) wait_for_previous();
+      const float f = MODE == kDense && a.scale ? a.alpha * a.scale[u.group * a.scale_stride] : a.alpha;
       const bool split = u.nsplit > 1;
       float* part = nullptr;
       const long long part_unit = 2ll * a.part_cols * HALF_M;
       if (split)
         part = a.part + (static_cast<long long>(u.tile) * u.nsplit + u.split) * part_unit +
-               static_cast<long long>(rank) * a.part_cols * HALF_M + quad * 32 + lane;
+               static_cast<long long>(rank) * a.part_cols * HALF_M + quad * 1024 + lane * 4;  // block cb: + cb * 4096
       float run[PLANES == 2 ? 2 : 1][32];
       const int nchunks = ceil_div((u.kb1 - u.kb0) * KSTEPS, a.chunk);
       for (int ch = 0; ch < nchunks; ++ch, ++g) {
@@ -698,37 +768,30 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int j = 0; j < 2; ++j) {
             const int cb = 2 * j + half;
             if (cb < nblocks) {
-              uint32_t v[32], w[32];
-              tmem_ld32(taddr + cb * 32, v);
-              tmem_ld32(taddr + CROSS + cb * 32, w);
-              tmem_ld_wait();
+              float v[32], w[32];
+              tmem_ld_block(taddr + cb * 32, v);
+              tmem_ld_block(taddr + CROSS + cb * 32, w);
+              tmem_wait_block(v);
+              tmem_wait_block(w);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float x = __uint_as_float(v[i]) + __uint_as_float(w[i]);
-                run[j][i] = ch ? run[j][i] + x : x;
-              }
+              for (int i = 0; i < 32; ++i) run[j][i] = ch ? run[j][i] + (v[i] + w[i]) : v[i] + w[i];
             }
           }
         } else {
 #pragma unroll 1
           for (int cb = half; cb < nblocks; cb += 2) {
-            uint32_t v[32];
-            tmem_ld32(taddr + cb * 32, v);
-            tmem_ld_wait();
+            float v[32];
+            tmem_ld_block(taddr + cb * 32, v);
+            tmem_wait_block(v);
             if (cb + 2 >= nblocks) {  // the last block is in registers: hand the accumulator back
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&accempty[acc]), 0));
             }
-            if (split) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) __stcg(part + (cb * 32 + i) * HALF_M, __uint_as_float(v[i]));
-            } else {
-              float f[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-              emit<MODE>(a, u, f, mrow, cb * 32, my_stash);
-            }
+            if (split)
+              put_part(part + cb * 4096, v);
+            else
+              emit<MODE>(a, u, f, v, mrow, cb * 32, my_stash);
           }
         }
         if (PLANES == 2 || half >= nblocks) {
@@ -743,29 +806,25 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int j = 0; j < 2; ++j) {
           const int cb = 2 * j + half;
           if (cb < nblocks) {
-            if (split) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) __stcg(part + (cb * 32 + i) * HALF_M, run[j][i]);
-            } else {
-              emit<MODE>(a, u, run[j], mrow, cb * 32, my_stash);
-            }
+            if (split)
+              put_part(part + cb * 4096, run[j]);
+            else
+              emit<MODE>(a, u, f, run[j], mrow, cb * 32, my_stash);
           }
         }
-      } else if (nchunks == 0 && !split) {  // an empty sum (a group without rows)
+      } else if (nchunks == 0) {  // an empty sum (a group without rows, or with few for this many parts)
 #pragma unroll 1
         for (int cb = half; cb < nblocks; cb += 2) {
-          float f[32];
+          float v[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) f[i] = 0.0f;
-          emit<MODE>(a, u, f, mrow, cb * 32, my_stash);
+          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+          if (split)
+            put_part(part + cb * 4096, v);
+          else
+            emit<MODE>(a, u, f, v, mrow, cb * 32, my_stash);
         }
       }
       if (split) {
-        if (PLANES == 1 && nchunks == 0) {
-#pragma unroll 1
-          for (int cb = half; cb < nblocks; cb += 2)
-            for (int i = 0; i < 32; ++i) __stcg(part + (cb * 32 + i) * HALF_M, 0.0f);
-        }
         // This CTA's part is written; the last of the tile's parts to arrive adds them all.
         __threadfence();
         if (!warps_meet(epibar, eph, abort_flag)) ok = false;
@@ -787,14 +846,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           const float* p0 = part - u.split * part_unit;
 #pragma unroll 1
           for (int cb = half; cb < nblocks; cb += 2) {
-            float f[32];
+            float v[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = __ldcg(p0 + (cb * 32 + i) * HALF_M);
-            for (int q = 1; q < u.nsplit; ++q) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) f[i] += __ldcg(p0 + q * part_unit + (cb * 32 + i) * HALF_M);
-            }
-            emit<MODE>(a, u, f, mrow, cb * 32, my_stash);
+            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+            for (int q = 0; q < u.nsplit; ++q) add_part(p0 + q * part_unit + cb * 4096, v);
+            emit<MODE>(a, u, f, v, mrow, cb * 32, my_stash);
           }
         }
       }
@@ -857,25 +913,30 @@ inline bool make_mn_map(CUtensorMap* map, int* is_4d, int blocks, const void* ba
   return encode(map, base, bf16, 4, dims, strides, box);
 }
 
-inline int sm_pairs(int* pairs) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return OZ_ECUDA;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return OZ_ECUDA;
-  *pairs = sms / 2;
-  return OZ_OK;
+struct Device {
+  int id, pairs;  // CTA pairs that fit at once
+  int* status;
+};
+
+inline int current_device(Device* d) {
+  int sms = 0;
+  if (cudaGetDevice(&d->id) != cudaSuccess) return OZ_ECUDA;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, d->id) != cudaSuccess) return OZ_ECUDA;
+  d->pairs = sms / 2;
+  d->status = device_status_ptr();
+  return d->status ? OZ_OK : OZ_ECUDA;
 }
 
 // Launches the product on `pairs` CTA pairs.  dependent: the launch may begin while the one
 // before it on the stream ends (the kernel waits for it before it reads anything).
 template <int MODE, bool A_MN, bool B_MN, int PLANES>
-int launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmB128, Args a, int pairs, bool dependent, cudaStream_t stream) {
+int launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmB128, Args a, const Device& d, int pairs,
+           bool dependent, cudaStream_t stream) {
+  const int dev = d.id;
+  a.status = d.status;
   auto kernel = product_kernel<MODE, A_MN, B_MN, PLANES>;
   const size_t smem = MODE == kDense ? SMEM_DENSE : SMEM_GROUPED;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-    return OZ_ECUDA;
-  a.status = device_status_ptr();
   a.epi_wait_ns = epilogue_wait_ns();
-  if (!a.status) return OZ_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs, 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
@@ -890,11 +951,21 @@ int launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tm
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = dependent ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmB128, a) != cudaSuccess) {
+  // The shared-memory limit is the function's, in this context: set on the first launch, and again
+  // should a launch be refused (a new context after a device reset).
+  static std::atomic<bool> ready[64] = {};
+  for (int attempt = 0; attempt < 2; ++attempt) {
+    if (dev >= 64 || attempt || !ready[dev].load(std::memory_order_acquire)) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+        return OZ_ECUDA;
+      if (dev < 64) ready[dev].store(true, std::memory_order_release);
+    }
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmB128, a);
+    if (e == cudaSuccess) return OZ_OK;
     cudaGetLastError();
-    return OZ_ECUDA;
+    if (e != cudaErrorInvalidValue) break;
   }
-  return OZ_OK;
+  return OZ_ECUDA;
 }
 
 }  // namespace prod

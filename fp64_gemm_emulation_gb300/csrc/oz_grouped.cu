@@ -13,9 +13,189 @@ namespace {
 
 using namespace prod;
 
-constexpr int kMaxSplitUnits = 160;  // (tile, part) pairs the split workspace holds: about two a CTA pair
+constexpr int kMaxParts = 160;  // parts of split tiles the workspace holds: about two a CTA pair
 
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+enum Op { kForward, kDgrad, kWgrad };
+
+// Deals out the tiles of all groups from the row offsets on the device.
+//   forward, dgrad: a group's rows in equal tiles (a multiple of 32 rows, at most 256) by the
+//     output's m; the group's tiles by row tile, so that a wave shares the rows and the weights.
+//   wgrad: the output's tiles for every group; the sum runs over the group's rows.  Its k-blocks of 64
+//     rows are aligned to the END of the rows, which are addressed as (offset within the group,
+//     first row): the first block starts at a negative offset, where TMA reads zeros.  No row of a
+//     neighbouring group ever enters a sum, so its NaNs cannot leak.
+template <Op OP>
+struct GroupedWalk {
+  static constexpr bool kScaled = false;
+  static constexpr size_t kTableBytes = 2 * (OZ_MAX_GROUPS + 1) * 4;  // offsets, tile prefix
+  static constexpr bool A_MN = OP != kForward, B_MN = OP == kWgrad, RAGGED_SUM = OP == kWgrad;
+  static constexpr int BOX = 32;  // ragged rows: the small box of B (the large one has HALF_N rows)
+
+  struct Params {
+    CUtensorMap tmA, tmB, tmB128;
+    int M, N, K;   // contiguous extent of the output; wgrad: its rows; otherwise the sum's length
+    int groups, rows, bn, max_parts, part_cols, chunk;
+    int a_4d, b_4d, vec, out_type;
+    uint32_t idesc;
+    const int32_t* offsets;
+    void* out;
+    long long ld, stride;
+    float* part;
+    unsigned int* arrivals;
+    int* status;
+    unsigned long long epi_wait_ns;
+  };
+
+  const Params& a;
+  const int *off, *prefix;
+  int tiles, full, nsplit, total, idx, tiles_m, tiles_n;
+
+  // Offsets are clamped to [0, rows] and to their predecessors, so that no access leaves the
+  // matrices whatever they hold; offsets that needed it are reported.
+  __device__ static void setup(const Params& a, int* table) {
+    int* off = table;
+    int* prefix = table + OZ_MAX_GROUPS + 1;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+      tma_prefetch_desc(&a.tmA);
+      tma_prefetch_desc(&a.tmB);
+      if (!B_MN) tma_prefetch_desc(&a.tmB128);
+    }
+    for (int i = threadIdx.x; i <= a.groups; i += THREADS) off[i] = a.offsets[i];
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    const int tiles_m = ceil_div(a.M, BM);
+    int before = 0, sum = 0;
+    bool bad = false;
+    for (int b = 0; b <= a.groups; b += 32) {
+      const int i = b + lane;
+      const int given = i <= a.groups ? off[i] : 0;
+      int v = max(0, min(given, a.rows));
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        if (lane >= d) v = max(v, o);
+      }
+      v = max(v, before);
+      bad |= i <= a.groups && v != given;
+      int prev = __shfl_up_sync(0xFFFFFFFFu, v, 1);
+      if (lane == 0) prev = before;
+      before = __shfl_sync(0xFFFFFFFFu, v, 31);
+      int t = (i >= 1 && i <= a.groups) ? ceil_div(v - prev, a.bn) * tiles_m : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, t, d);
+        if (lane >= d) t += o;
+      }
+      if (i <= a.groups) {
+        off[i] = v;
+        prefix[i] = sum + t;
+      }
+      sum += __shfl_sync(0xFFFFFFFFu, t, 31);
+    }
+    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0 && blockIdx.x == 0) atomicExch(a.status, OZ_EINVAL);
+  }
+
+  __device__ GroupedWalk(const Params& p, const int* table) : a(p), off(table), prefix(table + OZ_MAX_GROUPS + 1) {
+    const int pairs = static_cast<int>(gridDim.x >> 1);
+    tiles_m = ceil_div(a.M, BM);
+    tiles_n = RAGGED_SUM ? ceil_div(a.N, a.bn) : 0;
+    tiles = RAGGED_SUM ? a.groups * tiles_m * tiles_n : prefix[a.groups];
+    const int nkb = RAGGED_SUM ? ceil_div(off[a.groups] - off[0], BK * a.groups) : ceil_div(a.K, BK);
+    const int rest = tiles % pairs;
+    full = tiles - rest;
+    nsplit = a.max_parts ? tail_split(rest, nkb, pairs, a.max_parts, a.part_cols) : 1;
+    total = full + rest * nsplit;
+    idx = static_cast<int>(blockIdx.x >> 1) - pairs;
+  }
+
+  __device__ bool next(Unit& u) {
+    idx += static_cast<int>(gridDim.x >> 1);
+    if (idx >= total) return false;
+    int tile = idx;
+    u.split = 0;
+    u.nsplit = 1;
+    u.part = a.part;
+    u.part_cols = a.part_cols;
+    u.arrivals = a.arrivals;
+    if (idx >= full && nsplit > 1) {
+      const int r = (idx - full) / nsplit;
+      tile = full + r;
+      u.split = idx - full - r * nsplit;
+      u.nsplit = nsplit;
+      u.part = a.part + 2ll * r * nsplit * a.part_cols * HALF_M;
+      u.arrivals = a.arrivals + 2 * r;
+    }
+    int group, nkb;
+    if (RAGGED_SUM) {
+      const int per = tiles_m * tiles_n;
+      group = tile / per;
+      const int r = tile - group * per, tn = r / tiles_m;
+      u.m0 = (r - tn * tiles_m) * BM;
+      u.n0 = u.orow = tn * a.bn;
+      u.nn = min(a.bn, a.N - u.n0);
+      const int len = off[group + 1] - off[group];
+      nkb = ceil_div(len, BK);
+      u.k0 = len - nkb * BK;
+      u.zA = u.zB = off[group];
+    } else {
+      int lo = 0, hi = a.groups;  // prefix[group] <= tile < prefix[group + 1]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= tile) lo = mid; else hi = mid;
+      }
+      group = lo;
+      const int r = tile - prefix[group], tn = r / tiles_m;
+      const int len = off[group + 1] - off[group];
+      // equal tiles: as many as of full ones, with the least padding
+      const int w = ceil_div(ceil_div(len, ceil_div(len, a.bn)), 32) * 32;
+      u.m0 = (r - tn * tiles_m) * BM;
+      u.n0 = u.orow = off[group] + tn * w;
+      u.nn = min(w, len - tn * w);
+      nkb = ceil_div(a.K, BK);
+      u.k0 = 0;
+      u.zA = group;
+      u.zB = 0;
+    }
+    u.nmma = B_MN ? ceil_div(u.nn, 128) * 128 : ceil_div(u.nn, 32) * 32;
+    u.kb0 = static_cast<int>(static_cast<long long>(nkb) * u.split / u.nsplit);
+    u.kb1 = static_cast<int>(static_cast<long long>(nkb) * (u.split + 1) / u.nsplit);
+    u.a_mn = A_MN;
+    u.b_mn = B_MN;
+    u.a_4d = a.a_4d;
+    u.b_4d = a.b_4d;
+    // Few copies a stage: their issue, not their bytes, is what a stage waits for first.
+    const bool wide = u.nmma > 128;
+    u.mapA = &a.tmA;
+    u.mapB = !B_MN && wide ? &a.tmB128 : &a.tmB;
+    u.box_b = wide ? HALF_N : BOX;
+    u.boxes = B_MN ? (a.b_4d ? 1 : u.nmma / 128) : wide ? 1 : ceil_div(u.nmma / 2, BOX);
+    u.box_bytes = B_MN ? (a.b_4d ? a.bn / 128 : 1) * MN_BLOCK : u.box_b * BK * 2;
+    u.idesc = a.idesc;
+    u.m_extent = a.M;
+    u.out = static_cast<uint16_t*>(a.out) + (RAGGED_SUM ? group * a.stride : 0);
+    u.ld = a.ld;
+    u.out_type = a.out_type;
+    u.vec = a.vec;
+    return true;
+  }
+
+  __device__ bool ready(const volatile int*) const { return true; }
+  __device__ void done() const {}
+  __device__ static void gave_up(const Params&) {}
+
+  // Rows that belong to no group are zero.
+  __device__ void outside(int warp) const {
+    if (RAGGED_SUM) return;
+    const int lo = off[0], hi = off[a.groups], loose = lo + a.rows - hi;
+    for (int i = static_cast<int>(blockIdx.x) * EPI_WARPS + warp; i < loose; i += gridDim.x * EPI_WARPS) {
+      uint16_t* row = static_cast<uint16_t*>(a.out) + static_cast<long long>(i < lo ? i : hi + i - lo) * a.ld;
+      for (int c = threadIdx.x & 31; c < a.M; c += 32) row[c] = 0;
+    }
+  }
+};
 
 struct Operand {
   const void* p;
@@ -65,8 +245,6 @@ int repack(Operand& o, uint8_t** ws, cudaStream_t stream) {
   return OZ_OK;
 }
 
-enum Op { kForward, kDgrad, kWgrad };
-
 struct Problem {
   Op op;
   int n, k, rows, groups, dtype;
@@ -78,23 +256,22 @@ struct Problem {
 
   int m_out() const { return op == kForward ? n : k; }
   int bn() const { return op == kWgrad && n <= 128 ? 128 : 256; }
-  int tiles_m() const { return ceil_div(m_out(), BM); }
-  // Fewest tiles there can be (ragged rows: one tile in m), so whether a split is possible.
+  // A part of the sum has to be worth splitting off; whether tiles are left for a split is known on
+  // the device only.
   bool may_split() const {
-    const long long tiles = op == kWgrad ? static_cast<long long>(groups) * tiles_m() * ceil_div(n, bn()) : tiles_m();
-    const long long blocks = op == kWgrad ? ceil_div(rows, BK * groups) : ceil_div(op == kForward ? k : n, BK);
-    return tiles < kMaxSplitUnits && blocks > 1;
+    const int blocks = op == kWgrad ? ceil_div(rows, BK * groups) : ceil_div(op == kForward ? k : n, BK);
+    return blocks > 1;
   }
   int part_cols() const { return op == kWgrad ? bn() : static_cast<int>(roundup(rows < bn() ? rows : bn(), 32)); }
   size_t split_bytes() const {
     if (!may_split()) return 0;
-    return align256(sizeof(unsigned) * 2 * kMaxSplitUnits) + align256(sizeof(float) * 2 * HALF_M * part_cols() * kMaxSplitUnits);
+    return align256(sizeof(unsigned) * 2 * kMaxParts) + align256(sizeof(float) * 2 * HALF_M * part_cols() * kMaxParts);
   }
   size_t workspace() const { return split_bytes() + w.repack_bytes() + t.repack_bytes(); }
 };
 
 int check(int n, int k, int rows, int groups, int dtype, int ldw, long long stride_w, int ldk, int ldn) {
-  if (n < 0 || k < 0 || rows < 0 || groups < 1 || groups > MAX_GROUPS) return OZ_EINVAL;
+  if (n < 0 || k < 0 || rows < 0 || groups < 1 || groups > OZ_MAX_GROUPS) return OZ_EINVAL;
   if (dtype != OZ_BF16 && dtype != OZ_F16) return OZ_EINVAL;
   if (ldw < (k > 1 ? k : 1) || ldk < (k > 1 ? k : 1) || ldn < (n > 1 ? n : 1)) return OZ_EINVAL;
   if (groups > 1 && stride_w < static_cast<long long>(ldw) * n) return OZ_EINVAL;
@@ -111,6 +288,44 @@ int zero_output(const Problem& p, cudaStream_t stream) {
   return OZ_OK;
 }
 
+template <Op OP>
+int launch_op(const Problem& p, float* part, unsigned* arrivals, const Device& dev, cudaStream_t stream) {
+  typedef GroupedWalk<OP> Walk;
+  const bool bf16 = p.dtype == OZ_BF16;
+  typename Walk::Params a{};
+  a.M = p.m_out();
+  a.N = p.n;
+  a.K = OP == kForward ? p.k : p.n;
+  a.groups = p.groups;
+  a.rows = p.rows;
+  a.bn = p.bn();
+  a.max_parts = part ? (kMaxParts < 2 * dev.pairs ? kMaxParts : 2 * dev.pairs) : 0;
+  a.part_cols = p.part_cols();
+  a.idesc = idesc_base(bf16, Walk::A_MN, Walk::B_MN);
+  a.out_type = bf16 ? kOutBf16 : kOutF16;
+  a.offsets = p.offsets;
+  a.out = p.out;
+  a.ld = p.ldo;
+  a.stride = p.strideo;
+  a.vec = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.ldo % 8 == 0 && (p.op != kWgrad || p.strideo % 8 == 0);
+  a.part = part;
+  a.arrivals = arrivals;
+  const Operand &w = p.w, &t = p.t;
+  const uint64_t wl = 2ull * w.ld, tl = 2ull * t.ld;
+  bool ok;
+  if (OP == kWgrad) {  // rows as (offset within the group, the group's first row)
+    ok = make_mn_map(&a.tmA, &a.a_4d, 2, w.p, bf16, w.cols, w.rows, w.rows, wl, wl) &&
+         make_mn_map(&a.tmB, &a.b_4d, a.bn / 128, t.p, bf16, t.cols, t.rows, t.rows, tl, tl);
+  } else {
+    const uint64_t wm = w.mats > 1 ? 2ull * w.stride : wl * w.rows;
+    ok = make_map(&a.tmB, t.p, bf16, t.cols, t.rows, 1, tl, tl * t.rows, Walk::BOX) &&
+         make_map(&a.tmB128, t.p, bf16, t.cols, t.rows, 1, tl, tl * t.rows, HALF_N) &&
+         (Walk::A_MN ? make_mn_map(&a.tmA, &a.a_4d, 2, w.p, bf16, w.cols, w.rows, w.mats, wl, wm)
+                     : make_map(&a.tmA, w.p, bf16, w.cols, w.rows, w.mats, wl, wm, HALF_M));
+  }
+  return ok ? launch<Walk, 1>(a, dev, dev.pairs, false, stream) : OZ_ECUDA;
+}
+
 int run(Problem p, void* workspace, size_t ws_bytes, cudaStream_t stream) {
   const int sum = p.op == kForward ? p.k : p.op == kDgrad ? p.n : p.rows;
   if (p.m_out() == 0 || (p.op == kWgrad ? p.n : p.rows) == 0) return OZ_OK;
@@ -122,59 +337,21 @@ int run(Problem p, void* workspace, size_t ws_bytes, cudaStream_t stream) {
   Device dev;
   int rc;
   if ((rc = current_device(&dev))) return rc;
-  const int pairs = dev.pairs;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  Args a{};
+  float* part = nullptr;
+  unsigned* arrivals = nullptr;
   if (p.may_split()) {
-    a.counters = reinterpret_cast<unsigned*>(ws);
-    a.part = reinterpret_cast<float*>(ws + align256(sizeof(unsigned) * 2 * kMaxSplitUnits));
-    a.part_cols = p.part_cols();
-    a.max_split_units = kMaxSplitUnits < 2 * pairs ? kMaxSplitUnits : 2 * pairs;
-    if (cudaMemsetAsync(a.counters, 0, sizeof(unsigned) * 2 * kMaxSplitUnits, stream) != cudaSuccess) return OZ_ECUDA;
+    arrivals = reinterpret_cast<unsigned*>(ws);
+    part = reinterpret_cast<float*>(ws + align256(sizeof(unsigned) * 2 * kMaxParts));
+    if (cudaMemsetAsync(arrivals, 0, sizeof(unsigned) * 2 * kMaxParts, stream) != cudaSuccess) return OZ_ECUDA;
     ws += p.split_bytes();
   }
   if ((rc = repack(p.w, &ws, stream)) || (rc = repack(p.t, &ws, stream))) return rc;
-  const bool bf16 = p.dtype == OZ_BF16;
-  a.M = p.m_out();
-  a.N = p.n;
-  a.K = sum;
-  a.groups = p.groups;
-  a.rows = p.rows;
-  a.bn = p.bn();
-  a.nsplit = 1;
-  a.chunk = 1 << 28;
-  a.out_type = bf16 ? kOutBf16 : kOutF16;
-  a.planes_out = 1;
-  a.box_rows = BOX_ROWS;
-  a.offsets = p.offsets;
-  a.out = p.out;
-  a.ld = p.ldo;
-  a.stride = p.strideo;
-  a.vec = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.ldo % 8 == 0 && p.strideo % 8 == 0;
-  a.alpha = 1.0f;
-  CUtensorMap tmA, tmB, tmB128;
-  const Operand &w = p.w, &t = p.t;
-  const uint64_t wl = 2ull * w.ld, tl = 2ull * t.ld;
-  if (p.op == kWgrad) {
-    // rows addressed as (offset within the group, the group's first row)
-    a.idesc = idesc_base(bf16, true, true);
-    if (!make_mn_map(&tmA, &a.a_4d, 2, w.p, bf16, w.cols, w.rows, w.rows, wl, wl) ||
-        !make_mn_map(&tmB, &a.b_4d, a.bn / 128, t.p, bf16, t.cols, t.rows, t.rows, tl, tl))
-      return OZ_ECUDA;
-    return launch<kRaggedK, true, true, 1>(tmA, tmB, tmB, a, dev, pairs, false, stream);
+  switch (p.op) {
+    case kForward: return launch_op<kForward>(p, part, arrivals, dev, stream);
+    case kDgrad: return launch_op<kDgrad>(p, part, arrivals, dev, stream);
+    default: return launch_op<kWgrad>(p, part, arrivals, dev, stream);
   }
-  const uint64_t ws2 = w.mats > 1 ? 2ull * w.stride : wl * w.rows;
-  if (!make_map(&tmB, t.p, bf16, t.cols, t.rows, 1, tl, tl * t.rows, BOX_ROWS) ||
-      !make_map(&tmB128, t.p, bf16, t.cols, t.rows, 1, tl, tl * t.rows, HALF_N))
-    return OZ_ECUDA;
-  if (p.op == kForward) {
-    a.idesc = idesc_base(bf16, false, false);
-    if (!make_map(&tmA, w.p, bf16, w.cols, w.rows, w.mats, wl, ws2, HALF_M)) return OZ_ECUDA;
-    return launch<kRaggedN, false, false, 1>(tmA, tmB, tmB128, a, dev, pairs, false, stream);
-  }
-  a.idesc = idesc_base(bf16, true, false);
-  if (!make_mn_map(&tmA, &a.a_4d, 2, w.p, bf16, w.cols, w.rows, w.mats, wl, ws2)) return OZ_ECUDA;
-  return launch<kRaggedN, true, false, 1>(tmA, tmB, tmB128, a, dev, pairs, false, stream);
 }
 
 int run_allocating(const Problem& p, cudaStream_t stream) {

@@ -7,6 +7,12 @@
 // epilogue reads a matrix back.  (c = 0: B = b A + a I comes out of the first product.)
 // S and B are symmetric: only tiles that reach the lower triangle are computed, and mirrored.
 //
+// All products of all steps run in ONE cooperative launch (ChainWalk): the units of the products
+// follow each other in the same order on every CTA pair, and a unit's producer waits until the
+// product before it is finished for its own matrix (a counter per matrix in global memory).  So the
+// matrices of a batch do not wait for one another, and a product boundary costs a flag instead of
+// a launch (one launch per product: 3.7 us a product at 128 x 128 for 1.5 us of work).
+//
 // Numerics.  The products run on the FP16 tensor-core path: FP16 holds 11 bits where bf16
 // holds 8, at the same rate, and every range is known beforehand: |X_0| <= 1, and a host-side
 // bound on the polynomial bounds the singular values of every X_i, S and B, so each is stored
@@ -26,16 +32,199 @@ using namespace prod;
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 constexpr int kNormBlocks = 304;       // partial sums of a matrix's norm, at most
-constexpr int kMaxSplitUnits = 608;    // (tile, part) pairs the split workspace holds
+constexpr int kMaxParts = 160;         // parts of split tiles that a product's workspace holds
 // Two slices: MMA steps (16 k) summed on the tensor core before the sum moves to FP32 registers.
 // The tensor core truncates each addition, which biases long sums; the relative error of the
 // result (five steps, against 64 bits) is proportional to it:
 //   128 x 128:    1.6e-6 (1 step)  2.3e-6 (2)  3.5e-6 (4)  6.1e-6 (8)   plain FP32: 1.3e-6
 //   8192 x 2048:  1.5e-6 (1)       1.9e-6 (2)  2.9e-6 (4)  5.0e-6 (8)   plain FP32: 4.7e-6
 // and so is the epilogue's work: 4.1, 3.0, 2.6 and 2.4 ms at 8192 x 2048.  One k-block (4 steps) keeps
-// the error below plain FP32's where sums are long; sides up to 256 are bound by launches, so
-// they take single steps.
-constexpr int kChunk = 4;
+// the error below plain FP32's where sums are long; sides up to 256 are bound by latency, so
+// they take single steps (run_chain).
+
+// The products of a step.
+enum Kind { kGram = 0, kSquare = 1, kApply = 2 };
+
+struct Product {
+  CUtensorMap mapA[2], mapB[2];  // by the parity of the step (which of the two X)
+  int M, N, K, bn;
+  int tiles_m, tiles_n, tiles;   // of one matrix (symmetric: those that reach the lower triangle)
+  int full, nsplit, units;       // tiles of the batch that are not split, parts of the others, units in all
+  int a_mn, b_mn, sym;
+  uint32_t idesc;
+  float* part;
+  unsigned int* arrivals;
+};
+
+// Deals out the units of every product of every step, in that order.
+template <int PLANES>
+struct ChainWalk {
+  static constexpr bool kScaled = true;
+  static constexpr size_t kTableBytes = 0;
+
+  struct Params {
+    Product prod[3];
+    int batch, steps, chunk;
+    void *X[2], *S, *B, *O;
+    long long xplane, splane, ldx, lds, ldo, stride_o;
+    int out_type, vec_o;
+    const float* scales;          // [matrix][step][2]: factors of the first and the last product
+    float diag_s[OZ_MAX_NS_STEPS], alpha_b[OZ_MAX_NS_STEPS], diag_b[OZ_MAX_NS_STEPS];
+    unsigned int square;          // bit i: step i has the middle product (c != 0)
+    unsigned int* finished;       // [matrix]: epilogue warps that have finished a tile, over all products
+    unsigned int* stopped;        // a pair of this launch gave up
+    int* status;
+    unsigned long long epi_wait_ns;
+  };
+
+  const Params& a;
+  int idx, base, step, kind, group;
+  unsigned int need;  // a matrix's count when the products before this one are finished
+
+  __device__ static void setup(const Params& a, int*) {
+    if (threadIdx.x < 12) {
+      const Product& p = a.prod[threadIdx.x >> 2];
+      tma_prefetch_desc((threadIdx.x & 2) ? &p.mapB[threadIdx.x & 1] : &p.mapA[threadIdx.x & 1]);
+    }
+  }
+
+  __device__ ChainWalk(const Params& p, const int*)
+      : a(p), idx(static_cast<int>(blockIdx.x >> 1) - static_cast<int>(gridDim.x >> 1)), base(0), step(0), kind(kGram),
+        group(0), need(0) {}
+
+  __device__ int units() const { return kind == kSquare && !(a.square >> step & 1) ? 0 : a.prod[kind].units; }
+
+  __device__ bool next(Unit& u) {
+    idx += static_cast<int>(gridDim.x >> 1);
+    for (int n = units(); idx - base >= n; n = units()) {  // on to the unit's product
+      base += n;
+      if (n) need += a.prod[kind].tiles * 2 * EPI_WARPS;
+      if (kind == kApply) {
+        kind = kGram;
+        if (++step == a.steps) return false;
+      } else {
+        ++kind;
+      }
+    }
+    const Product& p = a.prod[kind];
+    int tile = idx - base;
+    u.split = 0;
+    u.nsplit = 1;
+    u.part = p.part;
+    u.part_cols = p.bn;
+    u.arrivals = p.arrivals;
+    if (tile >= p.full && p.nsplit > 1) {
+      const int q = tile - p.full, r = q / p.nsplit;
+      tile = p.full + r;
+      u.split = q - r * p.nsplit;
+      u.nsplit = p.nsplit;
+      u.part = p.part + 2ll * r * p.nsplit * p.bn * HALF_M;
+      u.arrivals = p.arrivals + 2 * r;
+    }
+    group = tile / p.tiles;
+    int r = tile - group * p.tiles, tm, tn;
+    if (p.sym) {  // row tile tm has the column tiles that reach n <= m
+      const int per = BM / p.bn;
+      tm = 0;
+      for (int c = min(per, p.tiles_n); r >= c; c = min(per * (tm + 1), p.tiles_n)) {
+        r -= c;
+        ++tm;
+      }
+      tn = r;
+    } else {  // groups of 8 row tiles swept along the column tiles (L2 reuse of both operands)
+      const int g = r / (8 * p.tiles_n), gm = min(8, p.tiles_m - 8 * g);
+      r -= g * 8 * p.tiles_n;
+      tn = r / gm;
+      tm = 8 * g + r - tn * gm;
+    }
+    u.m0 = tm * BM;
+    u.n0 = u.orow = tn * p.bn;
+    u.nn = min(p.bn, p.N - u.n0);
+    const int nkb = ceil_div(p.K, BK);
+    u.k0 = 0;
+    u.kb0 = nkb * u.split / u.nsplit;
+    u.kb1 = nkb * (u.split + 1) / u.nsplit;
+    u.a_mn = p.a_mn;
+    u.b_mn = p.b_mn;
+    u.a_4d = u.b_4d = true;
+    u.nmma = p.b_mn ? ceil_div(u.nn, 128) * 128 : ceil_div(u.nn, 32) * 32;
+    u.mapA = &p.mapA[step & 1];
+    u.mapB = &p.mapB[step & 1];
+    u.boxes = 1;
+    u.box_b = p.bn / 2;
+    u.box_bytes = p.b_mn ? p.bn / 128 * MN_BLOCK : p.bn / 2 * BK * 2;
+    u.zA = u.zB = group * PLANES;
+    u.idesc = p.idesc;
+    u.m_extent = p.M;
+    u.sym = p.sym;
+    u.planes_out = PLANES;
+    u.out_type = kOutSlices;
+    u.vec = true;
+    u.diag = 0.0f;
+    const long long sc = 2ll * (group * a.steps + step);
+    if (kind == kApply) {  // X_{i+1} 2^t' = 2^(t' - t - sb) (B 2^sb)(X_i 2^t)
+      u.f = a.scales[sc + 1];
+      if (step + 1 == a.steps) {
+        u.out = static_cast<uint8_t*>(a.O) + group * a.stride_o * (a.out_type == kOutF32 ? 4 : 2);
+        u.ld = a.ldo;
+        u.plane = 0;
+        u.planes_out = 1;
+        u.out_type = a.out_type;
+        u.vec = a.vec_o;
+      } else {
+        u.out = static_cast<uint16_t*>(a.X[(step & 1) ^ 1]) + group * PLANES * a.xplane;
+        u.ld = a.ldx;
+        u.plane = a.xplane;
+      }
+    } else {
+      const bool to_s = kind == kGram && (a.square >> step & 1);
+      u.f = kind == kGram ? a.scales[sc] : a.alpha_b[step];
+      u.diag = to_s ? a.diag_s[step] : a.diag_b[step];
+      u.out = static_cast<uint16_t*>(to_s ? a.S : a.B) + group * PLANES * a.splane;
+      u.ld = a.lds;
+      u.plane = a.splane;
+    }
+    return true;
+  }
+
+  // Waits until the products before the unit's are finished for its matrix.  They were dealt out
+  // earlier to pairs that are all running (cooperative launch).  What those pairs stored is then
+  // ordered before this thread's TMA loads (generic to async proxy).
+  __device__ bool ready(const volatile int* abort_flag) const {
+    if (need == 0) return true;
+    const unsigned int* count = a.finished + group;
+    auto reached = [&]() {
+      unsigned int v;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
+      return static_cast<int>(v - need) >= 0;
+    };
+    if (!reached()) {
+      const uint64_t t0 = globaltimer_ns();
+      for (int i = 1; !reached(); ++i) {
+        if (*abort_flag) return false;
+        if ((i & 63) == 0 && (*reinterpret_cast<const volatile unsigned int*>(a.stopped) || globaltimer_ns() - t0 > kWaitLimitNs)) {
+          atomicExch(a.stopped, 1u);
+          return false;
+        }
+      }
+    }
+    asm volatile("fence.proxy.async;" ::: "memory");
+    return true;
+  }
+
+  // An epilogue warp has stored its part of a finished tile.
+  __device__ void done() const {
+    asm volatile("fence.proxy.async;" ::: "memory");
+    __threadfence();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(a.finished + group), "r"(1u) : "memory");
+  }
+
+  __device__ void outside(int) const {}
+
+  // This pair has given up: the others' waits end.
+  __device__ static void gave_up(const Params& a) { atomicExch(a.stopped, 1u); }
+};
 
 // What the small kernels need of the plan.
 struct StepScales {
@@ -288,7 +477,7 @@ struct Shape {
   int cols, rows, batch, planes, side;  // contiguous extent, rows; side: the smaller
   int ldx, lds;
   bool wide;                            // rows <= cols
-  size_t x_bytes, s_bytes, part_bytes;
+  size_t x_bytes, s_bytes;
   int norm_blocks;
   Shape(int m, int n, int b, int slices) : cols(m), rows(n), batch(b), planes(slices) {
     wide = rows <= cols;
@@ -300,37 +489,51 @@ struct Shape {
     const long long per = (static_cast<long long>(rows) * cols + 8191) / 8192;
     norm_blocks = static_cast<int>(per < kNormBlocks ? per : kNormBlocks);
   }
-  // Split workspace: enough for every product's choice (plan_tiles), at full tile width.
-  size_t split_bytes() const { return align256(sizeof(float) * 2 * HALF_M * BN * static_cast<size_t>(split_units())); }
-  int split_units() const {
-    const long long tiles = static_cast<long long>(batch) * ceil_div(side, BM);
-    return tiles >= kMaxSplitUnits ? 0 : kMaxSplitUnits / 4;
-  }
+  size_t part_bytes() const { return align256(sizeof(float) * 2 * HALF_M * BN * kMaxParts); }  // of one product
+  int words() const { return 3 * 2 * kMaxParts + 1 + batch; }  // arrivals, stopped, finished
   size_t total() const {
-    return 2 * x_bytes + 2 * s_bytes + split_bytes() + align256(sizeof(unsigned) * 2 * kMaxSplitUnits) +
+    return 2 * x_bytes + 2 * s_bytes + 3 * part_bytes() + align256(sizeof(unsigned) * words()) +
            align256(sizeof(double) * 3 * norm_blocks * batch) + align256(sizeof(float) * 2 * OZ_MAX_NS_STEPS * batch);
   }
 };
 
-// Tile width and parts of the k range of one product, by a model of its time in SM cycles
-// (units per pair x k-blocks x cycles of a block, plus a unit's start and drain and the
-// joining of parts).
-void plan_tiles(int M, int N, int K, int batch, int sym, int planes, bool b_mn, int pairs, int max_units, int* bn_out,
-                int* split_out) {
-  const int nkb = ceil_div(K, BK);
+int sym_tiles(int side, int bn) {
+  const int tiles_n = ceil_div(side, bn), per = BM / bn;
+  int t = 0;
+  for (int i = 0; i < ceil_div(side, BM); ++i) t += per * (i + 1) < tiles_n ? per * (i + 1) : tiles_n;
+  return t;
+}
+
+// Tile width and parts of the last wave's tiles for one product, by a model of its time in SM
+// cycles: waves x (k-blocks x cycles of a block + a unit's start and drain), and the joining of parts.
+// A block of a 256-wide tile is 512 cycles of MMA with one slice; narrower ones are bound by what
+// they load.  Two slices triple the MMA; single-step chunks are bound by the epilogue.
+void plan_product(Product& p, int batch, int planes, int chunk, int pairs) {
+  const int nkb = ceil_div(p.K, BK);
   double best = 1e30;
-  for (int bn = planes == 2 ? BN2 : BN; bn >= (b_mn ? 128 : 64); bn /= 2) {
-    const long long tiles = static_cast<long long>(batch) * dense_tiles(M, N, bn, sym);
-    const double block = planes == 2 ? (bn == 128 ? 850 : 640) : (bn == 256 ? 560 : bn == 128 ? 380 : 320);
+  for (int bn = BN; bn >= (p.b_mn ? 128 : 64); bn /= 2) {
+    const int tiles_m = ceil_div(p.M, BM), tiles_n = ceil_div(p.N, bn);
+    const int tiles = p.sym ? sym_tiles(p.N, bn) : tiles_m * tiles_n;
+    const long long all = static_cast<long long>(tiles) * batch;
+    double block = planes == 1 ? (bn == 256 ? 540 : bn == 128 ? 380 : 320) : (bn == 256 ? 1580 : bn == 128 ? 820 : 640);
+    if (planes == 2 && chunk == 1) block = KSTEPS * (300.0 + 2 * bn);
+    const double fixed = 2000 + 6.0 * bn * planes;
+    const int rest = static_cast<int>(all % pairs);
+    const double whole = static_cast<double>(all / pairs) * (nkb * block + fixed * 0.3);
     for (int s = 1; s <= 16 && s <= nkb; ++s) {
-      if (s > 1 && (tiles >= pairs || tiles * s > max_units)) break;
-      const double waves = static_cast<double>((tiles * s + pairs - 1) / pairs);
-      double t = waves * (ceil_div(nkb, s) * block + 600) + 3000;
+      if (s > 1 && (rest == 0 || rest * s > kMaxParts)) break;
+      double t = whole;
+      if (rest) t += ceil_div(rest * s, pairs) * (ceil_div(nkb, s) * block + fixed);
       if (s > 1) t += 1500 + 2200.0 * (bn / 256.0) * (1 + s);
       if (t < best) {
         best = t;
-        *bn_out = bn;
-        *split_out = s;
+        p.bn = bn;
+        p.tiles_m = tiles_m;
+        p.tiles_n = tiles_n;
+        p.tiles = tiles;
+        p.nsplit = s;
+        p.full = s > 1 ? static_cast<int>(all - rest) : static_cast<int>(all);
+        p.units = p.full + (s > 1 ? rest * s : 0);
       }
     }
   }
@@ -350,6 +553,88 @@ int check(int m, int n, int batch, int dtype, const void* G, int ldg, long long 
   return OZ_OK;
 }
 
+template <int PLANES>
+int run_chain(const Shape& sh, const Plan& plan, uint16_t* const (&X)[2], uint16_t* S, uint16_t* B, float* part,
+              unsigned* words, const float* scales, void* O, int dtype, int ldo, long long stride_o, const Device& dev,
+              cudaStream_t stream) {
+  typedef ChainWalk<PLANES> Walk;
+  typename Walk::Params a{};
+  const int side = sh.side, long_side = sh.wide ? sh.cols : sh.rows;
+  a.batch = sh.batch;
+  a.steps = plan.sc.steps;
+  a.chunk = side <= 256 ? 1 : KSTEPS;
+  a.X[0] = X[0];
+  a.X[1] = X[1];
+  a.S = S;
+  a.B = B;
+  a.O = O;
+  a.xplane = static_cast<long long>(sh.rows) * sh.ldx;
+  a.splane = static_cast<long long>(side) * sh.lds;
+  a.ldx = sh.ldx;
+  a.lds = sh.lds;
+  a.ldo = ldo;
+  a.stride_o = stride_o;
+  a.out_type = dtype == OZ_F32 ? kOutF32 : dtype == OZ_BF16 ? kOutBf16 : kOutF16;
+  a.vec_o = (reinterpret_cast<uintptr_t>(O) & 15) == 0 && ldo % 8 == 0 && (sh.batch == 1 || stride_o % 8 == 0);
+  a.scales = scales;
+  for (int i = 0; i < a.steps; ++i) {
+    a.diag_s[i] = plan.diag_s[i];
+    a.alpha_b[i] = plan.alpha_b[i];
+    a.diag_b[i] = plan.diag_b[i];
+    if (plan.square[i]) a.square |= 1u << i;
+  }
+  a.stopped = words + 3 * 2 * kMaxParts;
+  a.finished = a.stopped + 1;
+
+  //                 m side, n side, sum
+  Product &g = a.prod[kGram], &q = a.prod[kSquare], &x = a.prod[kApply];
+  g.M = g.N = q.M = q.N = q.K = x.K = side;
+  g.K = long_side;
+  x.M = sh.cols;
+  x.N = sh.rows;
+  g.sym = q.sym = 1;
+  g.a_mn = g.b_mn = !sh.wide;  // wide: X X^T, both along its rows; tall: X^T X, both across them
+  x.a_mn = sh.wide;            // wide: D[col, row] = sum_j X[j, col] B[row, j]; tall: sum_j B[col, j] X[row, j]
+  long long units = 0;
+  for (int i = 0; i < 3; ++i) {
+    Product& p = a.prod[i];
+    plan_product(p, sh.batch, PLANES, a.chunk, dev.pairs);
+    p.idesc = idesc_base(false, p.a_mn, p.b_mn);
+    p.part = part + i * (sh.part_bytes() / sizeof(float));
+    p.arrivals = words + i * 2 * kMaxParts;
+    units += static_cast<long long>(p.units) * a.steps;
+    if (static_cast<long long>(p.tiles) * sh.batch > INT32_MAX / 64 || units > INT32_MAX / 2) return OZ_EINVAL;
+  }
+
+  const uint64_t mats = static_cast<uint64_t>(sh.batch) * PLANES, xl = 2ull * sh.ldx, sl = 2ull * sh.lds;
+  auto s_map = [&](CUtensorMap* t, const void* base, int box) {
+    return make_map(t, base, false, side, side, mats, sl, 2ull * a.splane, box);
+  };
+  auto x_map = [&](CUtensorMap* t, int i, int box) {
+    return make_map(t, X[i], false, sh.cols, sh.rows, mats, xl, 2ull * a.xplane, box);
+  };
+  // Rows of ldx, a multiple of 64 (so the map is 4-D): the padding past the last column is the
+  // workspace's own, and what is read there only reaches output elements that are never stored.
+  auto mn_map = [&](CUtensorMap* t, int i, int blocks) {
+    int is_4d = 0;
+    return make_mn_map(t, &is_4d, blocks, X[i], false, sh.ldx, sh.rows, mats, xl, 2ull * a.xplane) && is_4d;
+  };
+  bool ok = true;
+  for (int i = 0; i < 2 && ok; ++i) {
+    ok = s_map(&q.mapA[i], S, HALF_M) && s_map(&q.mapB[i], S, q.bn / 2);
+    if (sh.wide)
+      ok = ok && x_map(&g.mapA[i], i, HALF_M) && x_map(&g.mapB[i], i, g.bn / 2) && mn_map(&x.mapA[i], i, 2) &&
+           s_map(&x.mapB[i], B, x.bn / 2);
+    else
+      ok = ok && mn_map(&g.mapA[i], i, 2) && mn_map(&g.mapB[i], i, g.bn / 128) && s_map(&x.mapA[i], B, HALF_M) &&
+           x_map(&x.mapB[i], i, x.bn / 2);
+  }
+  if (!ok) return OZ_ECUDA;
+  int most = g.units > x.units ? g.units : x.units;
+  if (a.square && q.units > most) most = q.units;
+  return launch<Walk, PLANES>(a, dev, most < dev.pairs ? most : dev.pairs, true, stream);
+}
+
 int run(int m, int n, int batch, int dtype, const void* G, int ldg, long long stride_g, void* O, int ldo,
         long long stride_o, const Plan& plan, float eps, int slices, void* workspace, size_t ws_bytes,
         cudaStream_t stream) {
@@ -358,7 +643,6 @@ int run(int m, int n, int batch, int dtype, const void* G, int ldg, long long st
   Device dev;
   int rc;
   if ((rc = current_device(&dev))) return rc;
-  const int pairs = dev.pairs;
   uint8_t* at = static_cast<uint8_t*>(workspace);
   auto take = [&](size_t bytes) {
     uint8_t* p = at;
@@ -368,144 +652,19 @@ int run(int m, int n, int batch, int dtype, const void* G, int ldg, long long st
   uint16_t* X[2] = {reinterpret_cast<uint16_t*>(take(sh.x_bytes)), reinterpret_cast<uint16_t*>(take(sh.x_bytes))};
   uint16_t* S = reinterpret_cast<uint16_t*>(take(sh.s_bytes));
   uint16_t* B = reinterpret_cast<uint16_t*>(take(sh.s_bytes));
-  float* part = reinterpret_cast<float*>(take(sh.split_bytes()));
-  unsigned* counters = reinterpret_cast<unsigned*>(take(sizeof(unsigned) * 2 * kMaxSplitUnits));
+  float* part = reinterpret_cast<float*>(take(3 * sh.part_bytes()));
+  unsigned* words = reinterpret_cast<unsigned*>(take(sizeof(unsigned) * sh.words()));
   double* partial = reinterpret_cast<double*>(take(sizeof(double) * 3 * sh.norm_blocks * batch));
   float* scales = reinterpret_cast<float*>(take(sizeof(float) * 2 * OZ_MAX_NS_STEPS * batch));
-  const long long xplane = static_cast<long long>(sh.rows) * sh.ldx, splane = static_cast<long long>(sh.side) * sh.lds;
+  const long long xplane = static_cast<long long>(sh.rows) * sh.ldx;
 
-  norm_kernel<<<dim3(sh.norm_blocks, batch), 256, 0, stream>>>(G, dtype, m, n, ldg, stride_g, partial, counters,
-                                                               2 * kMaxSplitUnits);
+  norm_kernel<<<dim3(sh.norm_blocks, batch), 256, 0, stream>>>(G, dtype, m, n, ldg, stride_g, partial, words, sh.words());
   const long long work = (static_cast<long long>(sh.rows) * (sh.ldx / 8) + 255) / 256;
   convert_kernel<<<dim3(static_cast<unsigned>(work < 1024 ? work : 1024), batch), 256, 0, stream>>>(
       G, dtype, m, n, ldg, stride_g, partial, sh.norm_blocks, eps, plan.sc, X[0], sh.ldx, xplane, slices, scales);
   if (cudaGetLastError() != cudaSuccess) return OZ_ECUDA;
-
-  const int side = sh.side, P = slices;
-  int bn_gram = 0, bn_sq = 0, bn_app = 0, s_gram = 1, s_sq = 1, s_app = 1;
-  const int long_side = sh.wide ? sh.cols : sh.rows;
-  plan_tiles(side, side, long_side, batch, 1, P, !sh.wide, pairs, sh.split_units(), &bn_gram, &s_gram);
-  plan_tiles(side, side, side, batch, 1, P, false, pairs, sh.split_units(), &bn_sq, &s_sq);
-  plan_tiles(sh.cols, sh.rows, side, batch, 0, P, false, pairs, sh.split_units(), &bn_app, &s_app);
-
-  // Maps by role: m side (A) and n side (B) of each product.
-  CUtensorMap gA[2], gB[2], sA, sB, pA[2], pB[2], bOp;
-  const uint64_t mats = static_cast<uint64_t>(batch) * P, xl = 2ull * sh.ldx, sl = 2ull * sh.lds;
-  bool ok = make_map(&sA, S, false, side, side, mats, sl, 2ull * splane, HALF_M) &&
-            make_map(&sB, S, false, side, side, mats, sl, 2ull * splane, bn_sq / 2) &&
-            make_map(&bOp, B, false, side, side, mats, sl, 2ull * splane, sh.wide ? bn_app / 2 : HALF_M);
-  for (int i = 0; i < 2 && ok; ++i) {
-    auto x_map = [&](CUtensorMap* t, int box) {
-      return make_map(t, X[i], false, sh.cols, sh.rows, mats, xl, 2ull * xplane, box);
-    };
-    // rows of ldx: the padding past the last column is the workspace's own (a multiple of 64), and
-    // what is read there only reaches output elements that are never stored
-    auto mn_map = [&](CUtensorMap* t, int blocks) {
-      int is_4d = 0;  // 1: ldx is a multiple of 64
-      return make_mn_map(t, &is_4d, blocks, X[i], false, sh.ldx, sh.rows, mats, xl, 2ull * xplane);
-    };
-    if (sh.wide)
-      ok = x_map(&gA[i], HALF_M) && x_map(&gB[i], bn_gram / 2) && mn_map(&pA[i], 2);
-    else
-      ok = mn_map(&gA[i], 2) && mn_map(&gB[i], bn_gram / 128) && x_map(&pB[i], bn_app / 2);
-  }
-  if (!ok) return OZ_ECUDA;
-
-  Args base{};
-  base.groups = batch;
-  base.chunk = P == 2 ? (side <= 256 ? 1 : kChunk) : 1 << 28;
-  base.part = part;
-  base.counters = counters;
-  base.max_split_units = sh.split_units();
-  base.vec = 1;
-  base.a_4d = base.b_4d = 1;
-  base.planes_out = P;
-  auto grid = [&](const Args& a) { return a.tiles * a.nsplit < pairs ? a.tiles * a.nsplit : pairs; };
-  const int steps = plan.sc.steps;
-  for (int i = 0; i < steps; ++i) {
-    const int cur = i & 1;
-    const bool last = i + 1 == steps;
-    Args g = base;  // S 2^sa = 2^sa A + 2^sa b/(2c) I   (or B itself when c = 0)
-    g.M = g.N = side;
-    g.K = long_side;
-    g.bn = bn_gram;
-    g.part_cols = bn_gram;
-    g.nsplit = s_gram;
-    g.sym = 1;
-    g.tiles = batch * dense_tiles(side, side, bn_gram, 1);
-    g.out_type = kOutSlices;
-    g.box_rows = bn_gram / 2;
-    g.out = plan.square[i] ? S : B;
-    g.ld = sh.lds;
-    g.plane = splane;
-    g.stride = splane * P;
-    g.alpha = 1.0f;
-    g.scale = scales + 2 * i;
-    g.scale_stride = 2 * steps;
-    g.diag = plan.square[i] ? plan.diag_s[i] : plan.diag_b[i];
-    if (sh.wide) {
-      g.idesc = idesc_base(false, false, false);
-      rc = P == 2 ? launch<kDense, false, false, 2>(gA[cur], gB[cur], gB[cur], g, dev, grid(g), i > 0, stream)
-                  : launch<kDense, false, false, 1>(gA[cur], gB[cur], gB[cur], g, dev, grid(g), i > 0, stream);
-    } else {
-      g.idesc = idesc_base(false, true, true);
-      rc = P == 2 ? launch<kDense, true, true, 2>(gA[cur], gB[cur], gB[cur], g, dev, grid(g), i > 0, stream)
-                  : launch<kDense, true, true, 1>(gA[cur], gB[cur], gB[cur], g, dev, grid(g), i > 0, stream);
-    }
-    if (rc) return rc;
-    if (plan.square[i]) {  // B 2^sb = c 2^(sb - 2 sa) (S 2^sa)^2 + 2^sb (a - b^2 / 4c) I
-      Args q = g;
-      q.K = side;
-      q.bn = q.part_cols = bn_sq;
-      q.nsplit = s_sq;
-      q.tiles = batch * dense_tiles(side, side, bn_sq, 1);
-      q.box_rows = bn_sq / 2;
-      q.out = B;
-      q.alpha = plan.alpha_b[i];
-      q.scale = nullptr;
-      q.diag = plan.diag_b[i];
-      q.idesc = idesc_base(false, false, false);
-      rc = P == 2 ? launch<kDense, false, false, 2>(sA, sB, sB, q, dev, grid(q), true, stream)
-                  : launch<kDense, false, false, 1>(sA, sB, sB, q, dev, grid(q), true, stream);
-      if (rc) return rc;
-    }
-    Args x = base;  // X_{i+1} 2^t' = 2^(t' - t - sb) (B 2^sb)(X_i 2^t)
-    x.M = sh.cols;
-    x.N = sh.rows;
-    x.K = side;
-    x.bn = x.part_cols = bn_app;
-    x.nsplit = s_app;
-    x.tiles = batch * dense_tiles(sh.cols, sh.rows, bn_app, 0);
-    x.box_rows = bn_app / 2;
-    x.alpha = 1.0f;
-    x.scale = scales + 2 * i + 1;
-    x.scale_stride = 2 * steps;
-    if (last) {
-      x.out = O;
-      x.ld = ldo;
-      x.stride = stride_o;
-      x.planes_out = 1;
-      x.out_type = dtype == OZ_F32 ? kOutF32 : dtype == OZ_BF16 ? kOutBf16 : kOutF16;
-      x.vec = (reinterpret_cast<uintptr_t>(O) & 15) == 0 && ldo % 8 == 0 && (batch == 1 || stride_o % 8 == 0);
-    } else {
-      x.out = X[cur ^ 1];
-      x.ld = sh.ldx;
-      x.plane = xplane;
-      x.stride = xplane * P;
-      x.out_type = kOutSlices;
-    }
-    if (sh.wide) {  // D[col, row] = sum_j X[j, col] B[row, j]
-      x.idesc = idesc_base(false, true, false);
-      rc = P == 2 ? launch<kDense, true, false, 2>(pA[cur], bOp, bOp, x, dev, grid(x), true, stream)
-                  : launch<kDense, true, false, 1>(pA[cur], bOp, bOp, x, dev, grid(x), true, stream);
-    } else {  // D[col, row] = sum_j B[col, j] X[row, j]
-      x.idesc = idesc_base(false, false, false);
-      rc = P == 2 ? launch<kDense, false, false, 2>(bOp, pB[cur], pB[cur], x, dev, grid(x), true, stream)
-                  : launch<kDense, false, false, 1>(bOp, pB[cur], pB[cur], x, dev, grid(x), true, stream);
-    }
-    if (rc) return rc;
-  }
-  return OZ_OK;
+  return slices == 2 ? run_chain<2>(sh, plan, X, S, B, part, words, scales, O, dtype, ldo, stride_o, dev, stream)
+                     : run_chain<1>(sh, plan, X, S, B, part, words, scales, O, dtype, ldo, stride_o, dev, stream);
 }
 
 }  // namespace

@@ -3,30 +3,27 @@
 //
 // Every product is D[m, n] = sum_k A[m, k] B[n, k] with FP32 sums, where m runs along the
 // output's contiguous dimension and n over its rows.  That orientation is chosen for all
-// operators: an accumulator lane is then one contiguous output element, so a warp's 32 lanes
-// are 64 contiguous bytes of an output row, and a ragged number of output rows (the tokens of
-// an expert) is the MMA's N, which takes any multiple of 32, so a short expert does not pay
-// for a full tile.  Either operand may be K-contiguous ("K-major") or m/n-contiguous
-// ("MN-major"); the tensor core reads both from the 128-byte-swizzled tiles that TMA writes,
-// so nothing is ever transposed in memory.
+// operators: a ragged number of output rows (the tokens of an expert) is then the MMA's N, which
+// takes any multiple of 32, so a short expert does not pay for a full tile.  Either operand may
+// be K-contiguous ("K-major") or m/n-contiguous ("MN-major"); the tensor core reads both from the
+// 128-byte-swizzled tiles that TMA writes, so nothing is ever transposed in memory.
 //
-// Ragged sums (the weight gradient sums over an expert's rows): the k-blocks of 64 rows are
-// aligned to the END of the expert's rows, and its rows are addressed as (offset within the
-// expert, first row): the first block starts at a negative offset, which TMA fills with
-// zeros.  No row of a neighbouring expert is ever read into a sum, so its NaNs cannot leak.
-//
-// Kernel shape: clusters of two CTAs (cta_group::2), persistent over units (tile, split).
+// Kernel shape: clusters of two CTAs (cta_group::2), persistent over the units (tile, part of k)
+// that a walker deals out (GroupedWalk here, the Newton-Schulz chain in oz_newton.cu).
 //   warp 0: TMA producer   warp 1: TMEM owner + MMA issuer (leader)   warps 2-9: epilogue
 //   6 stages of 32 KB (128 x 64 of A and up to 128 x 64 of B in each CTA); two 256-column
 //   FP32 accumulators in tensor memory, so a tile's epilogue runs under the next one's MMAs.
-// Split k: when there are fewer tiles than CTA pairs, a tile's k range is cut into nsplit
-// parts.  Each part's FP32 sums go to the workspace, and the CTA that arrives last (an atomic
-// counter per tile and CTA) adds the parts in their order, so results do not depend on timing
-// and nobody waits.
-// Two slices (PLANES == 2): operands are h + l with h, l in FP16.  h h' has an accumulator of
-// its own and h l' + l h' (2^-11 of it) another, tiles being 128 wide at most; the tensor core
-// truncates as it accumulates, so the sums are taken out every `chunk` MMA steps and
-// continued in FP32 registers (round to nearest).
+// What bounds it: one thread issues every MMA and one every copy, so both loops are kept to a few
+// instructions (at 8192^3, descriptors rebuilt for each MMA: 981 TFLOP/s; two descriptor words and
+// one add: 1524; one TMA copy for each operand and stage instead of up to six: 1780).
+//
+// Split k: the tiles that do not fill a last wave of CTA pairs are cut into parts along k
+// (tail_split).  Each part's FP32 sums go to the workspace, and the CTA that arrives last (an
+// atomic counter for each tile and CTA) adds the parts in their order, so results do not depend
+// on timing and nobody waits.
+// Two slices (PLANES == 2): operands are h + l with h, l in FP16.  A chunk of MMA steps sums
+// h l' + l h' and then h h' into one accumulator; the tensor core truncates as it accumulates,
+// so the sums leave it after every chunk and go on in FP32 registers (round to nearest).
 // Every wait is bounded (as in the residue GEMM): on expiry the pair records OZ_ETIMEOUT,
 // drains what it issued and returns.
 #pragma once
@@ -52,74 +49,52 @@ constexpr int STAGES = 6;
 constexpr uint32_t A_STAGE = HALF_M * BK * 2;
 constexpr uint32_t B_STAGE = HALF_N * BK * 2;
 constexpr uint32_t STAGE_BYTES = A_STAGE + B_STAGE;
-constexpr uint32_t MN_BLOCK = 64 * BK * 2;  // 64 contiguous m (or n) x 64 k
+constexpr uint32_t MN_BLOCK = 64 * BK * 2;    // 64 contiguous m (or n) x 64 k
 constexpr int EPI_WARPS = 8;
-constexpr int EPI_THREADS = EPI_WARPS * 32;
-constexpr int THREADS = 64 + EPI_THREADS;
+constexpr int EPI_FIRST = 2;                  // its first warp
+constexpr int THREADS = (EPI_FIRST + EPI_WARPS) * 32;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int BN2 = 128;                     // tile width with two slices
-constexpr int CROSS = 128;                   // its second accumulator: columns past the first
-constexpr uint32_t WARP_STASH = 32 * 32 * 2;  // 32 columns x 32 lanes of 16 bits, per epilogue warp
+constexpr uint32_t WARP_STASH = 32 * 32 * 2;  // a 32 x 32 block of 16 bits, per epilogue warp
 constexpr uint32_t STASH = EPI_WARPS * WARP_STASH;
-constexpr int MAX_GROUPS = OZ_MAX_GROUPS;
-constexpr uint32_t TABLE = 2 * (MAX_GROUPS + 1) * 4;  // row offsets and tile prefix of the groups
-constexpr int BOX_ROWS = 32;                 // ragged rows: the small box of B (the large one has HALF_N rows)
-constexpr size_t SMEM_DENSE = 1024 + STAGES * STAGE_BYTES + STASH + 256;
-constexpr size_t SMEM_GROUPED = SMEM_DENSE + TABLE;
-static_assert(SMEM_GROUPED <= 232448, "shared memory budget");
+constexpr size_t SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + STASH + 256;  // and the walker's table
+constexpr long long PART_BLOCK = 32 * HALF_M;  // floats of 32 columns of one CTA's part
 
-enum Mode { kDense = 0, kRaggedN = 1, kRaggedK = 2 };
 enum OutType { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2, kOutSlices = 3 };
-
-struct Args {
-  int M, N, K;          // dense: the product's extents; ragged N: N unused; ragged K: K unused
-  int groups;           // dense: matrices of the batch; otherwise the number of groups
-  int tiles;            // dense: tiles of all matrices
-  int rows;             // grouped: rows of the token matrices
-  int bn;               // tile width in n
-  int nsplit;           // dense: parts of the k range; grouped: chosen on the device (see split_for)
-  int max_split_units;  // grouped: units the split workspace holds
-  int sym;              // dense: the product is symmetric; tiles with n <= m only, mirrored
-  int chunk;            // MMA steps (16 k) summed in one accumulator
-  int out_type, planes_out;
-  int vec;              // 16-byte stores are allowed (base and row stride)
-  int box_rows;         // rows of one TMA box of a K-major B operand (ragged rows: of the small one)
-  int a_4d, b_4d;       // MN-major operands: the map is 4-D and its box holds the CTA's whole tile
-                        // (2 blocks of 64 of A, bn / 128 of B); otherwise 3-D, one block a box
-  const int32_t* offsets;
-  void* out;
-  long long ld, stride;  // output row stride, stride between the groups' outputs (elements)
-  long long plane;       // kOutSlices: distance of the low slices
-  float alpha, diag;     // v = alpha v (* scale[group * scale_stride]), + diag on the diagonal
-  const float* scale;    // null: 1
-  int scale_stride;
-  float* part;           // split workspace: [unit][2 CTAs][part_cols][128]
-  unsigned int* counters;
-  int part_cols;
-  uint32_t idesc;        // instruction descriptor without N
-  int* status;
-  unsigned long long epi_wait_ns;
-};
-
-struct Unit {
-  int group;
-  int m0, n0;      // first output element of a row, first output row
-  int orow;        // output row of n0 (grouped by rows: n0; otherwise n0 within the group)
-  int nn, nmma;    // rows of the tile, the MMA's N
-  int k0, kstart;  // coordinate of k-block 0, and the group's first row (ragged K)
-  int kb0, kb1;    // k-blocks of this part
-  int tile, split, nsplit;
-};
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// Parts of the k range for `tiles` tiles of nkb k-blocks on `pairs` CTA pairs: the count that
-// minimises waves * (blocks of a part + fixed cost), the fixed cost in k-blocks.
-__host__ __device__ inline int split_for(int tiles, int nkb, int pairs, int max_units, int fixed) {
-  if (tiles <= 0 || tiles >= pairs) return 1;
+// One unit of work.  A role uses the fields it needs; the rest is never computed for it.
+struct Unit {
+  int m0, n0, nn, nmma;     // the tile: first m, first row of B, its rows, the MMA's N
+  int k0, kb0, kb1;         // k coordinate of k-block 0; the part's k-blocks
+  const CUtensorMap *mapA, *mapB;
+  bool a_mn, b_mn;          // MN-major operands ...
+  bool a_4d, b_4d;          // ... with a 4-D map, whose box holds the CTA's whole tile
+  int box_b, boxes;         // B copies: rows of a box (K-major), boxes of a stage
+  uint32_t box_bytes;
+  int zA, zB;               // last coordinate of A and B (matrix of the batch, or first row)
+  uint32_t idesc;
+  int m_extent;             // the output's m
+  void* out;
+  long long ld, plane;      // output row stride; distance of the low slices
+  int orow;                 // output row of the tile's first n
+  int out_type, planes_out;
+  bool vec, sym;            // 16-byte stores are allowed; a symmetric product, mirrored
+  float f, diag;            // v = f v, + diag on the diagonal (sym)
+  int split, nsplit;
+  float* part;              // the tile's parts: [nsplit][2 CTAs][part_cols][128]
+  int part_cols;
+  unsigned int* arrivals;   // [2 CTAs]
+};
+
+// Parts for the tiles of a last, partial wave: s that minimises, in k-blocks of time, the waves of
+// the parts and the joining (each CTA writes its part and the last one reads all: about 4 k-blocks
+// of time for 256 columns, and 2 for the rendezvous).  fixed: a unit's start and drain.
+__host__ __device__ inline int tail_split(int tiles, int nkb, int pairs, int max_parts, int cols) {
+  constexpr int fixed = 4;
   int best = 1, best_cost = 1 << 30;
-  for (int s = 1; s <= 16 && s <= nkb && (s == 1 || tiles * s <= max_units); ++s) {
-    const int cost = ceil_div(tiles * s, pairs) * (ceil_div(nkb, s) + fixed) + (s > 1 ? fixed : 0);
+  for (int s = 1; s <= 16 && s <= nkb && (s == 1 || tiles * s <= max_parts); ++s) {
+    const int cost = ceil_div(tiles * s, pairs) * (ceil_div(nkb, s) + fixed) + (s > 1 ? 2 + 4 * (1 + s) * cols / 256 : 0);
     if (cost < best_cost) {
       best_cost = cost;
       best = s;
@@ -128,98 +103,12 @@ __host__ __device__ inline int split_for(int tiles, int nkb, int pairs, int max_
   return best;
 }
 
-// Tiles of a symmetric product's row block tm: the column tiles that reach n <= m.
-__host__ __device__ inline int sym_tiles(int tm, int tiles_n, int bn) {
-  const int c = ceil_div((tm + 1) * BM, bn);
-  return c < tiles_n ? c : tiles_n;
-}
-
-__host__ __device__ inline int dense_tiles(int M, int N, int bn, int sym) {
-  const int tm = ceil_div(M, BM), tn = ceil_div(N, bn);
-  if (!sym) return tm * tn;
-  int t = 0;
-  for (int i = 0; i < tm; ++i) t += sym_tiles(i, tn, bn);
-  return t;
-}
-
-struct Schedule {
-  int tiles, total, nsplit, first, step, tiles_m, tiles_n;
-  const int* off;
-  const int* prefix;
-};
-
-template <int MODE, bool B_MN>
-__device__ __forceinline__ void unit_at(const Args& a, const Schedule& s, int idx, Unit& u) {
-  u.nsplit = s.nsplit;
-  u.tile = idx / s.nsplit;
-  u.split = idx - u.tile * s.nsplit;
-  int nkb;
-  if (MODE == kDense) {
-    const int per = s.tiles / a.groups;
-    u.group = u.tile / per;
-    int r = u.tile - u.group * per;
-    int tm, tn;
-    if (a.sym) {
-      tm = 0;
-      for (int c = sym_tiles(0, s.tiles_n, a.bn); r >= c; c = sym_tiles(tm, s.tiles_n, a.bn)) {
-        r -= c;
-        ++tm;
-      }
-      tn = r;
-    } else {  // groups of 8 row blocks swept along the column tiles (L2 reuse of both operands)
-      const int g = r / (8 * s.tiles_n);
-      const int gm = min(8, s.tiles_m - 8 * g);
-      r -= g * 8 * s.tiles_n;
-      tm = 8 * g + r % gm;
-      tn = r / gm;
-    }
-    u.m0 = tm * BM;
-    u.n0 = u.orow = tn * a.bn;
-    u.nn = min(a.bn, a.N - u.n0);
-    u.k0 = u.kstart = 0;
-    nkb = ceil_div(a.K, BK);
-  } else if (MODE == kRaggedN) {
-    int lo = 0, hi = a.groups;  // the group with prefix[g] <= tile < prefix[g + 1]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s.prefix[mid] <= u.tile) lo = mid; else hi = mid;
-    }
-    u.group = lo;
-    const int r = u.tile - s.prefix[lo];
-    const int tn = r / s.tiles_m;
-    const int len = s.off[lo + 1] - s.off[lo];
-    // equal tiles: the same number of them as with full ones, with the least padding
-    const int w = ceil_div(ceil_div(len, ceil_div(len, a.bn)), 32) * 32;
-    u.m0 = (r - tn * s.tiles_m) * BM;
-    u.n0 = u.orow = s.off[lo] + tn * w;
-    u.nn = min(w, len - tn * w);
-    u.k0 = u.kstart = 0;
-    nkb = ceil_div(a.K, BK);
-  } else {
-    const int per = s.tiles_m * s.tiles_n;
-    u.group = u.tile / per;
-    const int r = u.tile - u.group * per;
-    const int tn = r / s.tiles_m;
-    u.m0 = (r - tn * s.tiles_m) * BM;
-    u.n0 = u.orow = tn * a.bn;
-    u.nn = min(a.bn, a.N - u.n0);
-    const int len = s.off[u.group + 1] - s.off[u.group];
-    nkb = ceil_div(len, BK);
-    u.k0 = len - nkb * BK;  // negative in the first block: TMA reads zeros there
-    u.kstart = s.off[u.group];
-  }
-  u.nmma = B_MN ? ceil_div(u.nn, 128) * 128 : ceil_div(u.nn, 32) * 32;
-  u.kb0 = static_cast<int>(static_cast<long long>(nkb) * u.split / s.nsplit);
-  u.kb1 = static_cast<int>(static_cast<long long>(nkb) * (u.split + 1) / s.nsplit);
-}
-
 // Shared-memory descriptors, low word: address / 16 and the leading byte offset.  K-major tiles:
 // rows of 64 k (128 bytes, 128-byte swizzle), 8 rows are 1024 bytes, no leading offset.
 // MN-major tiles: blocks of 64 contiguous m (128 bytes a k row, 128-byte swizzle), 8 k rows are
 // 1024 bytes, the next 64 m are MN_BLOCK bytes on.  The high word is the same for both.
-template <bool MN>
-__device__ __forceinline__ uint32_t desc_low(uint32_t smem_addr) {
-  return ((smem_addr >> 4) & 0x3FFFu) | ((MN ? MN_BLOCK >> 4 : 1u) << 16);
+__device__ __forceinline__ uint32_t desc_low(uint32_t smem_addr, bool mn) {
+  return ((smem_addr >> 4) & 0x3FFFu) | ((mn ? MN_BLOCK >> 4 : 1u) << 16);
 }
 constexpr uint32_t DESC_HIGH = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride, version, 128-byte swizzle
 
@@ -351,60 +240,51 @@ __device__ __forceinline__ void store_block(const uint32_t (&w)[16], uint8_t* st
   __syncwarp();
 }
 
-// The finished sums of one block, whose first m is mrow within the tile and first n is c0.  f: their factor (dense).
-template <int MODE>
-__device__ __forceinline__ void emit(const Args& a, const Unit& u, float f, float (&v)[32], int mrow, int c0,
-                                     uint8_t* stash) {
+// The finished sums of one block, whose first m is mrow within the tile and first n is c0.
+template <bool SCALED>
+__device__ __forceinline__ void emit(const Unit& u, float (&v)[32], int mrow, int c0, uint8_t* stash) {
   const int lane = threadIdx.x & 31;
   const int m = u.m0 + mrow;
   const int ncount = min(32, u.nn - c0);
-  const int mcount = min(32, a.M - m);
+  const int mcount = min(32, u.m_extent - m);
   if (ncount <= 0 || mcount <= 0) return;
-  const bool bf16 = a.out_type == kOutBf16;
+  const bool bf16 = u.out_type == kOutBf16;
   const int n = u.orow + c0;
   uint32_t w[16];
-  if (MODE != kDense) {
+  if (!SCALED) {
 #pragma unroll
     for (int i = 0; i < 32; i += 2) w[i >> 1] = pack16(v[i], v[i + 1], bf16);
-    uint16_t* out = static_cast<uint16_t*>(a.out) + (MODE == kRaggedN ? 0 : u.group * a.stride) + n * a.ld + m;
-    store_block<true>(w, stash, out, a.ld, ncount, mcount, a.vec);
-    return;
-  }
+    store_block<true>(w, stash, static_cast<uint16_t*>(u.out) + n * u.ld + m, u.ld, ncount, mcount, u.vec);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] *= f;
-  if (a.sym && m == n) {  // blocks and tiles start at multiples of 32
+    for (int i = 0; i < 32; ++i) v[i] *= u.f;
+    if (u.sym && m == n) {  // blocks and tiles start at multiples of 32
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (frag_m(i, lane) == frag_n(i, lane)) v[i] += a.diag;
-  }
-  if (a.out_type == kOutF32) {
-    float* out = static_cast<float*>(a.out) + u.group * a.stride + n * a.ld + m;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const int mi = frag_m(i, lane), ni = frag_n(i, lane);
-      if (mi < mcount && ni < ncount) out[ni * a.ld + mi] = v[i];
+      for (int i = 0; i < 32; ++i)
+        if (frag_m(i, lane) == frag_n(i, lane)) v[i] += u.diag;
     }
-    return;
-  }
-  uint16_t* out = static_cast<uint16_t*>(a.out) + u.group * a.stride;
-  const int np = a.out_type == kOutSlices ? a.planes_out : 1;
-  for (int p = 0; p < np; ++p, out += a.plane) {
+    if (u.out_type == kOutF32) {
+      float* out = static_cast<float*>(u.out) + n * u.ld + m;
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      w[i >> 1] = pack16(v[i], v[i + 1], bf16);
-      if (np > 1) {  // what the slice leaves
-        const __half2 h = *reinterpret_cast<const __half2*>(&w[i >> 1]);
+      for (int i = 0; i < 32; ++i) {
+        const int mi = frag_m(i, lane), ni = frag_n(i, lane);
+        if (mi < mcount && ni < ncount) out[ni * u.ld + mi] = v[i];
+      }
+      return;
+    }
+    uint16_t* out = static_cast<uint16_t*>(u.out);
+#pragma unroll 1
+    for (int p = 0; p < u.planes_out; ++p, out += u.plane) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        w[i >> 1] = pack16(v[i], v[i + 1], bf16);
+        const __half2 h = *reinterpret_cast<const __half2*>(&w[i >> 1]);  // FP16 slices: what this one leaves
         v[i] -= __low2float(h);
         v[i + 1] -= __high2float(h);
       }
-    }
-    if (!a.sym) {
-      store_block<true>(w, stash, out + n * a.ld + m, a.ld, ncount, mcount, a.vec);
-    } else if (n < m) {  // below the diagonal: both copies
-      store_block<true>(w, stash, out + n * a.ld + m, a.ld, ncount, mcount, a.vec);
-      store_block<false>(w, stash, out + m * a.ld + n, a.ld, mcount, ncount, a.vec);
-    } else if (n == m) {  // on it: the block is its own mirror
-      store_block<true>(w, stash, out + n * a.ld + m, a.ld, ncount, mcount, a.vec);
+      // Symmetric: a block on the diagonal is its own mirror, those above it are some block's below.
+      if (!u.sym || n <= m) store_block<true>(w, stash, out + n * u.ld + m, u.ld, ncount, mcount, u.vec);
+      if (u.sym && n < m) store_block<false>(w, stash, out + m * u.ld + n, u.ld, mcount, ncount, u.vec);
     }
   }
 }
@@ -428,12 +308,12 @@ __device__ __forceinline__ void add_part(const float* part, float (&v)[32]) {
   }
 }
 
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-template <int MODE, bool A_MN, bool B_MN, int PLANES>
-__global__ void __launch_bounds__(THREADS, 1)
-    product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmB128, const __grid_constant__ Args a) {
+// The kernel.  Walk deals out the units: Walk::Params are the launch's, setup() runs once for the
+// whole CTA, a Walk of its own in every role gives the pair's units in order (next), and
+// ready() / done() are its dependences between units (the producer before a unit's first load,
+// every epilogue warp after its last store); gave_up() tells the other pairs that they wait in vain.
+template <class Walk, int PLANES>
+__global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_constant__ typename Walk::Params a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
@@ -452,8 +332,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile uint32_t* issued_by = reinterpret_cast<volatile uint32_t*>(abort_flag + 1);  // [2] (leader)
   volatile uint32_t* arrived = issued_by + 2;
-  int* tab_off = reinterpret_cast<int*>(stash + STASH + 256);  // grouped modes only
-  int* tab_prefix = tab_off + MAX_GROUPS + 1;
+  int* table = reinterpret_cast<int*>(stash + STASH + 256);  // the walker's
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -473,82 +352,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(proddone, 2);
     *abort_flag = 0;
     mbar_fence_init();
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
-    if (MODE == kRaggedN) tma_prefetch_desc(&tmB128);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, TMEM_COLS);
     tmem_relinquish_pair();
   }
-  // The next launch may set itself up meanwhile.  Dense launches come in chains: what touches the
-  // matrices waits for the launch before (the producer's first load, the epilogue's first store).
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (MODE != kDense) {
-    wait_for_previous();
-    for (int i = threadIdx.x; i <= a.groups; i += THREADS) tab_off[i] = a.offsets[i];
-    __syncthreads();
-    if (warp == 0) {
-      // Offsets are clamped to [0, rows] and to their predecessors, so that no access leaves the
-      // matrices whatever they hold; offsets that needed it are reported.
-      const int tiles_m = ceil_div(a.M, BM);
-      int floor_off = 0, sum = 0;
-      bool bad = false;
-      for (int b = 0; b <= a.groups; b += 32) {
-        const int i = b + lane;
-        int v = i <= a.groups ? tab_off[i] : 0;
-        const int given = v;
-        v = max(0, min(v, a.rows));
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
-          if (lane >= d) v = max(v, o);
-        }
-        v = max(v, floor_off);
-        bad |= i <= a.groups && v != given;
-        int prev = __shfl_up_sync(0xFFFFFFFFu, v, 1);
-        if (lane == 0) prev = floor_off;
-        floor_off = __shfl_sync(0xFFFFFFFFu, v, 31);
-        int t = (i >= 1 && i <= a.groups) ? ceil_div(v - prev, a.bn) * tiles_m : 0;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int o = __shfl_up_sync(0xFFFFFFFFu, t, d);
-          if (lane >= d) t += o;
-        }
-        if (i <= a.groups) {
-          tab_off[i] = v;
-          tab_prefix[i] = sum + t;
-        }
-        sum += __shfl_sync(0xFFFFFFFFu, t, 31);
-      }
-      if (__any_sync(0xFFFFFFFFu, bad) && lane == 0 && blockIdx.x == 0) atomicExch(a.status, OZ_EINVAL);
-    }
-  }
+  Walk::setup(a, table);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-
-  Schedule sched;
-  sched.off = tab_off;
-  sched.prefix = tab_prefix;
-  sched.tiles_m = ceil_div(a.M, BM);
-  sched.tiles_n = MODE == kRaggedN ? 0 : ceil_div(a.N, a.bn);
-  sched.first = static_cast<int>(blockIdx.x >> 1);
-  sched.step = static_cast<int>(gridDim.x >> 1);
-  if (MODE == kDense) {
-    sched.tiles = a.tiles;
-    sched.nsplit = a.nsplit;
-  } else if (MODE == kRaggedN) {
-    sched.tiles = tab_prefix[a.groups];
-    sched.nsplit = split_for(sched.tiles, ceil_div(a.K, BK), sched.step, a.max_split_units, 4);
-  } else {
-    sched.tiles = a.groups * sched.tiles_m * sched.tiles_n;
-    sched.nsplit = split_for(sched.tiles, ceil_div(tab_off[a.groups] - tab_off[0], BK * a.groups), sched.step,
-                             a.max_split_units, 4);
-  }
-  sched.total = sched.tiles * sched.nsplit;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -556,20 +370,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       int stage = 0;
       uint32_t phase = 0;
       long long issued = 0;
-      for (int idx = sched.first; idx < sched.total && !*abort_flag; idx += sched.step) {
-        Unit u;
-        unit_at<MODE, B_MN>(a, sched, idx, u);
+      Walk walk(a, table);
+      Unit u;
+      while (!*abort_flag && walk.next(u)) {
+        if (!walk.ready(abort_flag)) {
+          if (!*abort_flag) stop_pair(abort_flag, a.status);
+          break;
+        }
         const int rowA = u.m0 + static_cast<int>(rank) * HALF_M;
-        const int half_n = u.nmma >> 1;
-        const int rowB = u.n0 + static_cast<int>(rank) * half_n;
-        // Few TMA instructions a stage: their issue, not the bytes, is what a stage waits for first.
-        const bool wide_b = MODE == kRaggedN && half_n > 64;
-        const int box_b = wide_b ? HALF_N : a.box_rows;
-        const int boxes = B_MN ? (a.b_4d ? 1 : half_n / 64) : ceil_div(half_n, box_b);
-        const CUtensorMap* mapB = wide_b ? &tmB128 : &tmB;
-        const uint32_t box_bytes = B_MN ? (a.b_4d ? a.bn / 128 : 1) * MN_BLOCK : box_b * BK * 2;
-        const uint32_t bytes = A_STAGE + boxes * box_bytes;
-        if (MODE == kDense && idx == sched.first) wait_for_previous();
+        const int rowB = u.n0 + static_cast<int>(rank) * (u.nmma >> 1);
+        const uint32_t bytes = A_STAGE + u.boxes * u.box_bytes;
         for (int kb = u.kb0; kb < u.kb1 && !*abort_flag; ++kb) {
 #pragma unroll
           for (int p = 0; p < PLANES; ++p) {
@@ -580,26 +390,25 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
             mbar_arrive_expect_tx_cluster(bar, bytes);
             const int k = u.k0 + kb * BK;
-            // last coordinate: matrix (slice) of the batch, or the group's first row
-            const int zA = MODE == kRaggedK ? u.kstart : u.group * PLANES + p;
-            const int zB = MODE == kDense ? u.group * PLANES + p : (MODE == kRaggedK ? u.kstart : 0);
             uint8_t* dA = sA + stage * A_STAGE;
             uint8_t* dB = sB + stage * B_STAGE;
-            if (!A_MN) {
-              tma_load_3d_pair(dA, &tmA, bar, k, rowA, zA);
-            } else if (a.a_4d) {
-              tma_load_4d_pair(dA, &tmA, bar, 0, k, rowA / 64, zA);
+            if (!u.a_mn) {
+              tma_load_3d_pair(dA, u.mapA, bar, k, rowA, u.zA + p);
+            } else if (u.a_4d) {
+              tma_load_4d_pair(dA, u.mapA, bar, 0, k, rowA / 64, u.zA + p);
             } else {
-              tma_load_3d_pair(dA, &tmA, bar, rowA, k, zA);
-              tma_load_3d_pair(dA + MN_BLOCK, &tmA, bar, rowA + 64, k, zA);
+              tma_load_3d_pair(dA, u.mapA, bar, rowA, k, u.zA + p);
+              tma_load_3d_pair(dA + MN_BLOCK, u.mapA, bar, rowA + 64, k, u.zA + p);
             }
-            if (!B_MN) {
-              tma_load_3d_pair(dB, mapB, bar, k, rowB, zB);
-              for (int b = 1; b < boxes; ++b) tma_load_3d_pair(dB + b * box_bytes, mapB, bar, k, rowB + box_b * b, zB);
-            } else if (a.b_4d) {  // a last, narrower tile loads the full box: B_STAGE has room for it
-              tma_load_4d_pair(dB, &tmB, bar, 0, k, rowB / 64, zB);
+            if (!u.b_mn) {
+              tma_load_3d_pair(dB, u.mapB, bar, k, rowB, u.zB + p);
+              for (int b = 1; b < u.boxes; ++b)
+                tma_load_3d_pair(dB + b * u.box_bytes, u.mapB, bar, k, rowB + u.box_b * b, u.zB + p);
+            } else if (u.b_4d) {  // a last, narrower tile loads the full box: B_STAGE has room for it
+              tma_load_4d_pair(dB, u.mapB, bar, 0, k, rowB / 64, u.zB + p);
             } else {
-              for (int b = 0; b < boxes; ++b) tma_load_3d_pair(dB + b * MN_BLOCK, mapB, bar, rowB + 64 * b, k, zB);
+              for (int b = 0; b < u.boxes; ++b)
+                tma_load_3d_pair(dB + b * MN_BLOCK, u.mapB, bar, rowB + 64 * b, k, u.zB + p);
             }
             ++issued;
             if (++stage == STAGES) {
@@ -634,13 +443,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t g = 0;
       uint32_t consumed = 0;
       bool ok = true;
-      // Low words of stage 0's descriptors; a stage or a k step only adds to the address field.
-      constexpr uint32_t A_STEP = (A_MN ? UMMA_K * 128 : UMMA_K * 2) >> 4, B_STEP = (B_MN ? UMMA_K * 128 : UMMA_K * 2) >> 4;
-      const uint32_t a_desc = desc_low<A_MN>(smem_u32(sA)), b_desc = desc_low<B_MN>(smem_u32(sB));
-      for (int idx = sched.first; idx < sched.total && ok && !*abort_flag; idx += sched.step) {
-        Unit u;
-        unit_at<MODE, B_MN>(a, sched, idx, u);
-        const uint32_t idesc = a.idesc | (static_cast<uint32_t>(u.nmma >> 3) << 17);
+      Walk walk(a, table);
+      Unit u;
+      while (ok && !*abort_flag && walk.next(u)) {
+        // Low words of stage 0's descriptors; a stage or a k step only adds to the address field.
+        const uint32_t a_desc = desc_low(smem_u32(sA), u.a_mn), b_desc = desc_low(smem_u32(sB), u.b_mn);
+        const uint32_t a_step = (u.a_mn ? UMMA_K * 128 : UMMA_K * 2) >> 4, b_step = (u.b_mn ? UMMA_K * 128 : UMMA_K * 2) >> 4;
+        const uint32_t idesc = u.idesc | (static_cast<uint32_t>(u.nmma >> 3) << 17);
         int left = u.kb1 - u.kb0;
         if (left == 0) continue;
         uint32_t in_chunk = 0, d_tmem = 0;
@@ -664,31 +473,32 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t ad = a_desc + stage * (A_STAGE >> 4), bd = b_desc + stage * (B_STAGE >> 4);
+          if (PLANES == 1) {
 #pragma unroll
-          for (int kk = 0; kk < KSTEPS; ++kk) {
-            if (PLANES == 1) {
-              umma_pair(d_tmem, ad + kk * A_STEP, bd + kk * B_STEP, idesc, kk > 0 ? 1u : in_chunk);
+            for (int kk = 0; kk < KSTEPS; ++kk) {
+              umma_pair(d_tmem, ad + kk * a_step, bd + kk * b_step, idesc, kk > 0 ? 1u : in_chunk);
               in_chunk = 1;
-            } else {
-              if (in_chunk == 0) {  // a new sum: the next accumulator
-                if (!mbar_wait_or_abort(&accempty[g & 1], ((g >> 1) & 1) ^ 1, kWaitLimitNs, abort_flag)) {
-                  ok = false;
-                  break;
-                }
-                tc_fence_after();
-                d_tmem = tmem_base + (g & 1) * BN;
-              }
-              umma_pair(d_tmem, ad + kk * A_STEP, bd + kk * B_STEP, idesc, in_chunk);                              // h h'
-              umma_pair(d_tmem + CROSS, ad + kk * A_STEP, bd + (B_STAGE >> 4) + kk * B_STEP, idesc, in_chunk);     // h l'
-              umma_pair(d_tmem + CROSS, ad + (A_STAGE >> 4) + kk * A_STEP, bd + kk * B_STEP, idesc, 1u);           // l h'
-              if (++in_chunk == static_cast<uint32_t>(a.chunk) || (left == 1 && kk + 1 == KSTEPS)) {
-                umma_commit_pair(&accfull[g & 1], 0x3);
-                in_chunk = 0;
-                ++g;
-              }
             }
+          } else {
+            // Chunks of a.chunk steps (a divisor of a k-block's); the small products first, so that
+            // the truncation of their additions is small too.
+            const uint32_t al = ad + (A_STAGE >> 4), bl = bd + (B_STAGE >> 4);
+            for (int k0 = 0; k0 < KSTEPS; k0 += a.chunk, ++g) {
+              if (!mbar_wait_or_abort(&accempty[g & 1], ((g >> 1) & 1) ^ 1, kWaitLimitNs, abort_flag)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              d_tmem = tmem_base + (g & 1) * BN;
+              for (int kk = k0; kk < k0 + a.chunk; ++kk) {
+                umma_pair(d_tmem, ad + kk * a_step, bl + kk * b_step, idesc, kk > k0 ? 1u : 0u);
+                umma_pair(d_tmem, al + kk * a_step, bd + kk * b_step, idesc, 1u);
+              }
+              for (int kk = k0; kk < k0 + a.chunk; ++kk) umma_pair(d_tmem, ad + kk * a_step, bd + kk * b_step, idesc, 1u);
+              umma_commit_pair(&accfull[g & 1], 0x3);
+            }
+            if (!ok) break;
           }
-          if (!ok) break;
 #pragma unroll
           for (int p = 0; p < PLANES; ++p) umma_commit_pair(&empty[stage + p], 0x3);
           stage += PLANES;
@@ -726,34 +536,26 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ------------------------------------------------------------ epilogue (warps 2-9, both CTAs)
     // A warp drains its 32 lanes and every second block of 32 columns.
     const int quad = warp & 3;
-    const int half = (warp - 2) >> 2;
-    const int etid = threadIdx.x - 64;
+    const int half = (warp - EPI_FIRST) >> 2;
     const int mrow = static_cast<int>(rank) * HALF_M + quad * 32;
-    uint8_t* my_stash = stash + (warp - 2) * WARP_STASH;
+    uint8_t* my_stash = stash + (warp - EPI_FIRST) * WARP_STASH;
     uint32_t g = 0, eph = 0;
     bool ok = true;
-    if (MODE == kRaggedN) {  // rows that belong to no group are zero
-      const int lo = tab_off[0], hi = tab_off[a.groups];
-      const int loose = lo + a.rows - hi;
-      for (int i = static_cast<int>(blockIdx.x) * EPI_WARPS + warp - 2; i < loose; i += gridDim.x * EPI_WARPS) {
-        uint16_t* row = static_cast<uint16_t*>(a.out) + static_cast<long long>(i < lo ? i : hi + i - lo) * a.ld;
-        for (int c = lane; c < a.M; c += 32) row[c] = 0;
-      }
-    }
-    for (int idx = sched.first; idx < sched.total && ok; idx += sched.step) {
-      Unit u;
-      unit_at<MODE, B_MN>(a, sched, idx, u);
+    Walk walk(a, table);
+    walk.outside(warp - EPI_FIRST);
+    Unit u;
+    while (ok && walk.next(u)) {
       const int nblocks = ceil_div(u.nn, 32);  // this warp: blocks half, half + 2, ...
-      if (MODE == kDense && idx == sched.first) wait_for_previous();
-      const float f = MODE == kDense && a.scale ? a.alpha * a.scale[u.group * a.scale_stride] : a.alpha;
       const bool split = u.nsplit > 1;
-      float* part = nullptr;
-      const long long part_unit = 2ll * a.part_cols * HALF_M;
-      if (split)
-        part = a.part + (static_cast<long long>(u.tile) * u.nsplit + u.split) * part_unit +
-               static_cast<long long>(rank) * a.part_cols * HALF_M + quad * 1024 + lane * 4;  // block cb: + cb * 4096
-      float run[PLANES == 2 ? 2 : 1][32];
-      const int nchunks = ceil_div((u.kb1 - u.kb0) * KSTEPS, a.chunk);
+      const long long part_unit = 2ll * u.part_cols * HALF_M;
+      float* const parts = u.part + static_cast<long long>(rank) * u.part_cols * HALF_M + quad * 1024 + lane * 4;
+      float* const mine = parts + u.split * part_unit;
+      float run[4][32];  // two slices: the sums of this warp's blocks half, half + 2, ...
+      if (PLANES == 2) {
+#pragma unroll
+        for (int i = 0; i < 128; ++i) run[i >> 5][i & 31] = 0.0f;
+      }
+      const int nchunks = PLANES == 1 ? (u.kb1 > u.kb0 ? 1 : 0) : (u.kb1 - u.kb0) * (KSTEPS / a.chunk);
       for (int ch = 0; ch < nchunks; ++ch, ++g) {
         const uint32_t acc = g & 1;
         if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&accfull[acc], (g >> 1) & 1, a.epi_wait_ns, abort_flag))) {
@@ -765,16 +567,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * BN;
         if (PLANES == 2) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < 4; ++j) {
             const int cb = 2 * j + half;
             if (cb < nblocks) {
-              float v[32], w[32];
+              float v[32];
               tmem_ld_block(taddr + cb * 32, v);
-              tmem_ld_block(taddr + CROSS + cb * 32, w);
               tmem_wait_block(v);
-              tmem_wait_block(w);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) run[j][i] = ch ? run[j][i] + (v[i] + w[i]) : v[i] + w[i];
+              for (int i = 0; i < 32; ++i) run[j][i] += v[i];
             }
           }
         } else {
@@ -789,9 +589,9 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&accempty[acc]), 0));
             }
             if (split)
-              put_part(part + cb * 4096, v);
+              put_part(mine + cb * PART_BLOCK, v);
             else
-              emit<MODE>(a, u, f, v, mrow, cb * 32, my_stash);
+              emit<Walk::kScaled>(u, v, mrow, cb * 32, my_stash);
           }
         }
         if (PLANES == 2 || half >= nblocks) {
@@ -803,13 +603,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) break;
       if (PLANES == 2) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 4; ++j) {
           const int cb = 2 * j + half;
           if (cb < nblocks) {
             if (split)
-              put_part(part + cb * 4096, run[j]);
+              put_part(mine + cb * PART_BLOCK, run[j]);
             else
-              emit<MODE>(a, u, f, run[j], mrow, cb * 32, my_stash);
+              emit<Walk::kScaled>(u, run[j], mrow, cb * 32, my_stash);
           }
         }
       } else if (nchunks == 0) {  // an empty sum (a group without rows, or with few for this many parts)
@@ -819,41 +619,38 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0.0f;
           if (split)
-            put_part(part + cb * 4096, v);
+            put_part(mine + cb * PART_BLOCK, v);
           else
-            emit<MODE>(a, u, f, v, mrow, cb * 32, my_stash);
+            emit<Walk::kScaled>(u, v, mrow, cb * 32, my_stash);
         }
       }
+      bool finished = true;
       if (split) {
         // This CTA's part is written; the last of the tile's parts to arrive adds them all.
         __threadfence();
-        if (!warps_meet(epibar, eph, abort_flag)) ok = false;
-        if (ok && etid == 0) *arrived = atomicAdd(&a.counters[u.tile * 2 + rank], 1u);
-        if (ok && !warps_meet(epibar, eph, abort_flag)) ok = false;
+        ok = warps_meet(epibar, eph, abort_flag);
+        if (ok && threadIdx.x == EPI_FIRST * 32) *arrived = atomicAdd(&u.arrivals[rank], 1u);
+        ok = ok && warps_meet(epibar, eph, abort_flag);
+        finished = ok && *arrived == static_cast<uint32_t>(u.nsplit - 1);
+        ok = ok && warps_meet(epibar, eph, abort_flag);  // everyone has read `arrived`
         if (!ok) {
           if (lane == 0 && !*abort_flag) stop_pair(abort_flag, a.status);
           break;
         }
-        const bool last = *arrived == static_cast<uint32_t>(u.nsplit - 1);
-        if (!warps_meet(epibar, eph, abort_flag)) {  // everyone has read `arrived`
-          ok = false;
-          if (lane == 0 && !*abort_flag) stop_pair(abort_flag, a.status);
-          break;
-        }
-        if (last) {
+        if (finished) {
           __threadfence();
-          if (etid == 0) a.counters[u.tile * 2 + rank] = 0;  // as it was found: a later launch may use it
-          const float* p0 = part - u.split * part_unit;
+          if (threadIdx.x == EPI_FIRST * 32) u.arrivals[rank] = 0;  // as it was found: a later unit may use it
 #pragma unroll 1
           for (int cb = half; cb < nblocks; cb += 2) {
             float v[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-            for (int q = 0; q < u.nsplit; ++q) add_part(p0 + q * part_unit + cb * 4096, v);
-            emit<MODE>(a, u, f, v, mrow, cb * 32, my_stash);
+            for (int q = 0; q < u.nsplit; ++q) add_part(parts + q * part_unit + cb * PART_BLOCK, v);
+            emit<Walk::kScaled>(u, v, mrow, cb * 32, my_stash);
           }
         }
       }
+      if (finished) walk.done();
     }
   }
 
@@ -861,6 +658,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0) {
+    if (*abort_flag) Walk::gave_up(a);
     if (!mbar_wait(drain, 0)) {
       *abort_flag = 1;
       atomicExch(a.status, OZ_ETIMEOUT);
@@ -927,15 +725,14 @@ inline int current_device(Device* d) {
   return d->status ? OZ_OK : OZ_ECUDA;
 }
 
-// Launches the product on `pairs` CTA pairs.  dependent: the launch may begin while the one
-// before it on the stream ends (the kernel waits for it before it reads anything).
-template <int MODE, bool A_MN, bool B_MN, int PLANES>
-int launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmB128, Args a, const Device& d, int pairs,
-           bool dependent, cudaStream_t stream) {
-  const int dev = d.id;
+// Launches on `pairs` CTA pairs.  cooperative: the units depend on one another, so all CTAs have to
+// run at once (the launch is refused if they cannot).
+template <class Walk, int PLANES>
+int launch(typename Walk::Params a, const Device& d, int pairs, bool cooperative, cudaStream_t stream) {
+  auto kernel = product_kernel<Walk, PLANES>;
+  constexpr size_t smem = SMEM_BYTES + Walk::kTableBytes;
+  static_assert(smem <= 232448, "shared memory budget");
   a.status = d.status;
-  auto kernel = product_kernel<MODE, A_MN, B_MN, PLANES>;
-  const size_t smem = MODE == kDense ? SMEM_DENSE : SMEM_GROUPED;
   a.epi_wait_ns = epilogue_wait_ns();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs, 1, 1);
@@ -947,20 +744,20 @@ int launch(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tm
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeCooperative;
+  attr[1].val.cooperative = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 2 : 1;
+  cfg.numAttrs = cooperative ? 2 : 1;
   // The shared-memory limit is the function's, in this context: set on the first launch, and again
   // should a launch be refused (a new context after a device reset).
   static std::atomic<bool> ready[64] = {};
   for (int attempt = 0; attempt < 2; ++attempt) {
-    if (dev >= 64 || attempt || !ready[dev].load(std::memory_order_acquire)) {
+    if (d.id >= 64 || attempt || !ready[d.id].load(std::memory_order_acquire)) {
       if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return OZ_ECUDA;
-      if (dev < 64) ready[dev].store(true, std::memory_order_release);
+      if (d.id < 64) ready[d.id].store(true, std::memory_order_release);
     }
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmB128, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e == cudaSuccess) return OZ_OK;
     cudaGetLastError();
     if (e != cudaErrorInvalidValue) break;

@@ -29,6 +29,7 @@ enum Op { kForward, kDgrad, kWgrad };
 template <Op OP>
 struct GroupedWalk {
   static constexpr bool kScaled = false;
+  static constexpr int kEpiWarps = 8;
   static constexpr size_t kTableBytes = 2 * (OZ_MAX_GROUPS + 1) * 4;  // offsets, tile prefix
   static constexpr bool A_MN = OP != kForward, B_MN = OP == kWgrad, RAGGED_SUM = OP == kWgrad;
   static constexpr int BOX = 32;  // ragged rows: the small box of B (the large one has HALF_N rows)
@@ -63,7 +64,7 @@ struct GroupedWalk {
       tma_prefetch_desc(&a.tmB);
       if (!B_MN) tma_prefetch_desc(&a.tmB128);
     }
-    for (int i = threadIdx.x; i <= a.groups; i += THREADS) off[i] = a.offsets[i];
+    for (int i = threadIdx.x; i <= a.groups; i += blockDim.x) off[i] = a.offsets[i];
     __syncthreads();
     if (threadIdx.x >= 32) return;
     const int tiles_m = ceil_div(a.M, BM);
@@ -190,7 +191,7 @@ struct GroupedWalk {
   __device__ void outside(int warp) const {
     if (RAGGED_SUM) return;
     const int lo = off[0], hi = off[a.groups], loose = lo + a.rows - hi;
-    for (int i = static_cast<int>(blockIdx.x) * EPI_WARPS + warp; i < loose; i += gridDim.x * EPI_WARPS) {
+    for (int i = static_cast<int>(blockIdx.x) * kEpiWarps + warp; i < loose; i += gridDim.x * kEpiWarps) {
       uint16_t* row = static_cast<uint16_t*>(a.out) + static_cast<long long>(i < lo ? i : hi + i - lo) * a.ld;
       for (int c = threadIdx.x & 31; c < a.M; c += 32) row[c] = 0;
     }

@@ -60,6 +60,7 @@ struct Product {
 template <int PLANES>
 struct ChainWalk {
   static constexpr bool kScaled = true;
+  static constexpr int kEpiWarps = PLANES == 2 ? 16 : 8;
   static constexpr size_t kTableBytes = 0;
 
   struct Params {
@@ -98,7 +99,7 @@ struct ChainWalk {
     idx += static_cast<int>(gridDim.x >> 1);
     for (int n = units(); idx - base >= n; n = units()) {  // on to the unit's product
       base += n;
-      if (n) need += a.prod[kind].tiles * 2 * EPI_WARPS;
+      if (n) need += a.prod[kind].tiles * 2 * kEpiWarps;
       if (kind == kApply) {
         kind = kGram;
         if (++step == a.steps) return false;

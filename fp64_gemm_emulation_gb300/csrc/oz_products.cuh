@@ -10,7 +10,7 @@
 //
 // Kernel shape: clusters of two CTAs (cta_group::2), persistent over the units (tile, part of k)
 // that a walker deals out (GroupedWalk here, the Newton-Schulz chain in oz_newton.cu).
-//   warp 0: TMA producer   warp 1: TMEM owner + MMA issuer (leader)   warps 2-9: epilogue
+//   warp 0: TMA producer   warp 1: TMEM owner + MMA issuer (leader)   others: epilogue (Walk::kEpiWarps)
 //   6 stages of 32 KB (128 x 64 of A and up to 128 x 64 of B in each CTA); two 256-column
 //   FP32 accumulators in tensor memory, so a tile's epilogue runs under the next one's MMAs.
 // What bounds it: one thread issues every MMA and one every copy, so both loops are kept to a few
@@ -50,13 +50,10 @@ constexpr uint32_t A_STAGE = HALF_M * BK * 2;
 constexpr uint32_t B_STAGE = HALF_N * BK * 2;
 constexpr uint32_t STAGE_BYTES = A_STAGE + B_STAGE;
 constexpr uint32_t MN_BLOCK = 64 * BK * 2;    // 64 contiguous m (or n) x 64 k
-constexpr int EPI_WARPS = 8;
-constexpr int EPI_FIRST = 2;                  // its first warp
-constexpr int THREADS = (EPI_FIRST + EPI_WARPS) * 32;
+constexpr int EPI_FIRST = 2;                  // the first epilogue warp
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t WARP_STASH = 32 * 32 * 2;  // a 32 x 32 block of 16 bits, per epilogue warp
-constexpr uint32_t STASH = EPI_WARPS * WARP_STASH;
-constexpr size_t SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + STASH + 256;  // and the walker's table
+constexpr size_t SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 256;  // and the stash, and the walker's table
 constexpr long long PART_BLOCK = 32 * HALF_M;  // floats of 32 columns of one CTA's part
 
 enum OutType { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2, kOutSlices = 3 };
@@ -308,12 +305,77 @@ __device__ __forceinline__ void add_part(const float* part, float (&v)[32]) {
   }
 }
 
+// The producer's loop over a unit's stages, compiled for each way its operands are copied, so that
+// a stage is a wait, an arrival and (mostly) two copies and nothing else.  KA: K-major, MN-major 4-D,
+// MN-major in two 3-D boxes.  KB: K-major in one box, in several, MN-major 4-D, 3-D boxes.
+// Returns false when a wait ran out or the pair was stopped.
+template <int KA, int KB, int PLANES>
+__device__ __forceinline__ bool load_unit(const Unit& u, uint8_t* sA, uint8_t* sB, uint64_t* empty, uint32_t full_leader,
+                                          uint32_t rank, int& stage, uint32_t& phase, uint32_t& issued,
+                                          const volatile int* abort_flag) {
+  const int rowA = u.m0 + static_cast<int>(rank) * HALF_M;
+  const int rowB = u.n0 + static_cast<int>(rank) * (u.nmma >> 1);
+  const uint32_t bytes = A_STAGE + (KB == 0 || KB == 2 ? 1 : u.boxes) * u.box_bytes;
+  int k = u.k0 + u.kb0 * BK;
+  for (int kb = u.kb0; kb < u.kb1; ++kb, k += BK) {
+#pragma unroll
+    for (int p = 0; p < PLANES; ++p) {
+      if (!mbar_wait_or_abort(&empty[stage], phase ^ 1, kWaitLimitNs, abort_flag)) return false;
+      const uint32_t bar = full_leader + stage * 8;
+      mbar_arrive_expect_tx_cluster(bar, bytes);
+      uint8_t* dA = sA + stage * A_STAGE;
+      uint8_t* dB = sB + stage * B_STAGE;
+      if (KA == 0) {
+        tma_load_3d_pair(dA, u.mapA, bar, k, rowA, u.zA + p);
+      } else if (KA == 1) {
+        tma_load_4d_pair(dA, u.mapA, bar, 0, k, rowA / 64, u.zA + p);
+      } else {
+        tma_load_3d_pair(dA, u.mapA, bar, rowA, k, u.zA + p);
+        tma_load_3d_pair(dA + MN_BLOCK, u.mapA, bar, rowA + 64, k, u.zA + p);
+      }
+      if (KB == 0) {
+        tma_load_3d_pair(dB, u.mapB, bar, k, rowB, u.zB + p);
+      } else if (KB == 1) {
+        for (int b = 0; b < u.boxes; ++b)
+          tma_load_3d_pair(dB + b * u.box_bytes, u.mapB, bar, k, rowB + u.box_b * b, u.zB + p);
+      } else if (KB == 2) {  // a last, narrower tile loads the full box: B_STAGE has room for it
+        tma_load_4d_pair(dB, u.mapB, bar, 0, k, rowB / 64, u.zB + p);
+      } else {
+        for (int b = 0; b < u.boxes; ++b)
+          tma_load_3d_pair(dB + b * MN_BLOCK, u.mapB, bar, rowB + 64 * b, k, u.zB + p);
+      }
+      ++issued;
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+  }
+  return true;
+}
+
+// One thread of a converged warp, in the form whose uniformity the compiler can see.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t elected;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(elected));
+  return elected != 0;
+}
+
 // The kernel.  Walk deals out the units: Walk::Params are the launch's, setup() runs once for the
 // whole CTA, a Walk of its own in every role gives the pair's units in order (next), and
 // ready() / done() are its dependences between units (the producer before a unit's first load,
-// every epilogue warp after its last store); gave_up() tells the other pairs that they wait in vain.
+// every epilogue warp of the pair after its last store); gave_up() tells the other pairs that they wait in vain.
 template <class Walk, int PLANES>
-__global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_constant__ typename Walk::Params a) {
+__global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
+    product_kernel(const __grid_constant__ typename Walk::Params a) {
+  constexpr int EPI_WARPS = Walk::kEpiWarps;
+  constexpr int COLS = EPI_WARPS / 4;                 // warps that share the blocks of 32 columns of a quadrant
+  constexpr int RUNS = PLANES == 2 ? 8 / COLS : 1;    // two slices: blocks whose sums a warp holds
+  constexpr uint32_t STASH = EPI_WARPS * WARP_STASH;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
@@ -365,11 +427,12 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ------------------------------------------------------------ TMA producer (both CTAs)
       int stage = 0;
       uint32_t phase = 0;
-      long long issued = 0;
+      uint32_t issued = 0;
+      const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
       Walk walk(a, table);
       Unit u;
       while (!*abort_flag && walk.next(u)) {
@@ -377,53 +440,26 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
           if (!*abort_flag) stop_pair(abort_flag, a.status);
           break;
         }
-        const int rowA = u.m0 + static_cast<int>(rank) * HALF_M;
-        const int rowB = u.n0 + static_cast<int>(rank) * (u.nmma >> 1);
-        const uint32_t bytes = A_STAGE + u.boxes * u.box_bytes;
-        for (int kb = u.kb0; kb < u.kb1 && !*abort_flag; ++kb) {
-#pragma unroll
-          for (int p = 0; p < PLANES; ++p) {
-            if (!mbar_wait_or_abort(&empty[stage], phase ^ 1, kWaitLimitNs, abort_flag)) {
-              if (!*abort_flag) stop_pair(abort_flag, a.status);
-              break;
-            }
-            const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
-            mbar_arrive_expect_tx_cluster(bar, bytes);
-            const int k = u.k0 + kb * BK;
-            uint8_t* dA = sA + stage * A_STAGE;
-            uint8_t* dB = sB + stage * B_STAGE;
-            if (!u.a_mn) {
-              tma_load_3d_pair(dA, u.mapA, bar, k, rowA, u.zA + p);
-            } else if (u.a_4d) {
-              tma_load_4d_pair(dA, u.mapA, bar, 0, k, rowA / 64, u.zA + p);
-            } else {
-              tma_load_3d_pair(dA, u.mapA, bar, rowA, k, u.zA + p);
-              tma_load_3d_pair(dA + MN_BLOCK, u.mapA, bar, rowA + 64, k, u.zA + p);
-            }
-            if (!u.b_mn) {
-              tma_load_3d_pair(dB, u.mapB, bar, k, rowB, u.zB + p);
-              for (int b = 1; b < u.boxes; ++b)
-                tma_load_3d_pair(dB + b * u.box_bytes, u.mapB, bar, k, rowB + u.box_b * b, u.zB + p);
-            } else if (u.b_4d) {  // a last, narrower tile loads the full box: B_STAGE has room for it
-              tma_load_4d_pair(dB, u.mapB, bar, 0, k, rowB / 64, u.zB + p);
-            } else {
-              for (int b = 0; b < u.boxes; ++b)
-                tma_load_3d_pair(dB + b * MN_BLOCK, u.mapB, bar, rowB + 64 * b, k, u.zB + p);
-            }
-            ++issued;
-            if (++stage == STAGES) {
-              stage = 0;
-              phase ^= 1;
-            }
-          }
+        const int kind_b = !u.b_mn ? (u.boxes == 1 ? 0 : 1) : (u.b_4d ? 2 : 3);
+        bool ok;
+#define OZ_LOAD(KA, KB) load_unit<KA, KB, PLANES>(u, sA, sB, empty, full_leader, rank, stage, phase, issued, abort_flag)
+        if (!u.a_mn)
+          ok = kind_b == 0 ? OZ_LOAD(0, 0) : OZ_LOAD(0, 1);
+        else if (u.a_4d)
+          ok = kind_b == 0 ? OZ_LOAD(1, 0) : kind_b == 1 ? OZ_LOAD(1, 1) : kind_b == 2 ? OZ_LOAD(1, 2) : OZ_LOAD(1, 3);
+        else
+          ok = kind_b == 0 ? OZ_LOAD(2, 0) : kind_b == 1 ? OZ_LOAD(2, 1) : kind_b == 2 ? OZ_LOAD(2, 2) : OZ_LOAD(2, 3);
+#undef OZ_LOAD
+        if (!ok) {
+          if (!*abort_flag) stop_pair(abort_flag, a.status);
+          break;
         }
       }
       // Every issued copy must have landed before the pair may exit (see the residue GEMM).
-      st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t*>(&issued_by[rank])), 0),
-                            static_cast<uint32_t>(issued));
+      st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t*>(&issued_by[rank])), 0), issued);
       mbar_arrive_release_cluster(mapa_shared(smem_u32(proddone), 0));
       if (!*abort_flag) {
-        for (int i = 0; i < STAGES && i < issued; ++i) {
+        for (uint32_t i = 0; i < STAGES && i < issued; ++i) {
           if (--stage < 0) {
             stage = STAGES - 1;
             phase ^= 1;
@@ -436,7 +472,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       // ------------------------------------------------------------ MMA issuer (leader only)
       int stage = 0;
       uint32_t phase = 0;
@@ -533,10 +569,10 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
       umma_commit_pair(drain, 0x3);
     }
   } else {
-    // ------------------------------------------------------------ epilogue (warps 2-9, both CTAs)
-    // A warp drains its 32 lanes and every second block of 32 columns.
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    // A warp drains its 32 lanes and every COLS-th block of 32 columns.
     const int quad = warp & 3;
-    const int half = (warp - EPI_FIRST) >> 2;
+    const int first = (warp - EPI_FIRST) >> 2;
     const int mrow = static_cast<int>(rank) * HALF_M + quad * 32;
     uint8_t* my_stash = stash + (warp - EPI_FIRST) * WARP_STASH;
     uint32_t g = 0, eph = 0;
@@ -545,15 +581,15 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
     walk.outside(warp - EPI_FIRST);
     Unit u;
     while (ok && walk.next(u)) {
-      const int nblocks = ceil_div(u.nn, 32);  // this warp: blocks half, half + 2, ...
+      const int nblocks = ceil_div(u.nn, 32);  // this warp: blocks first, first + COLS, ...
       const bool split = u.nsplit > 1;
       const long long part_unit = 2ll * u.part_cols * HALF_M;
       float* const parts = u.part + static_cast<long long>(rank) * u.part_cols * HALF_M + quad * 1024 + lane * 4;
       float* const mine = parts + u.split * part_unit;
-      float run[4][32];  // two slices: the sums of this warp's blocks half, half + 2, ...
+      float run[RUNS][32];  // two slices: the sums of this warp's blocks
       if (PLANES == 2) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i) run[i >> 5][i & 31] = 0.0f;
+        for (int i = 0; i < RUNS * 32; ++i) run[i >> 5][i & 31] = 0.0f;
       }
       const int nchunks = PLANES == 1 ? (u.kb1 > u.kb0 ? 1 : 0) : (u.kb1 - u.kb0) * (KSTEPS / a.chunk);
       for (int ch = 0; ch < nchunks; ++ch, ++g) {
@@ -567,8 +603,8 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * BN;
         if (PLANES == 2) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int cb = 2 * j + half;
+          for (int j = 0; j < RUNS; ++j) {
+            const int cb = COLS * j + first;
             if (cb < nblocks) {
               float v[32];
               tmem_ld_block(taddr + cb * 32, v);
@@ -579,11 +615,11 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
           }
         } else {
 #pragma unroll 1
-          for (int cb = half; cb < nblocks; cb += 2) {
+          for (int cb = first; cb < nblocks; cb += COLS) {
             float v[32];
             tmem_ld_block(taddr + cb * 32, v);
             tmem_wait_block(v);
-            if (cb + 2 >= nblocks) {  // the last block is in registers: hand the accumulator back
+            if (cb + COLS >= nblocks) {  // the last block is in registers: hand the accumulator back
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&accempty[acc]), 0));
@@ -594,7 +630,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
               emit<Walk::kScaled>(u, v, mrow, cb * 32, my_stash);
           }
         }
-        if (PLANES == 2 || half >= nblocks) {
+        if (PLANES == 2 || first >= nblocks) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&accempty[acc]), 0));
@@ -603,8 +639,8 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
       if (!ok) break;
       if (PLANES == 2) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int cb = 2 * j + half;
+        for (int j = 0; j < RUNS; ++j) {
+          const int cb = COLS * j + first;
           if (cb < nblocks) {
             if (split)
               put_part(mine + cb * PART_BLOCK, run[j]);
@@ -614,7 +650,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
         }
       } else if (nchunks == 0) {  // an empty sum (a group without rows, or with few for this many parts)
 #pragma unroll 1
-        for (int cb = half; cb < nblocks; cb += 2) {
+        for (int cb = first; cb < nblocks; cb += COLS) {
           float v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0.0f;
@@ -641,7 +677,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const __grid_consta
           __threadfence();
           if (threadIdx.x == EPI_FIRST * 32) u.arrivals[rank] = 0;  // as it was found: a later unit may use it
 #pragma unroll 1
-          for (int cb = half; cb < nblocks; cb += 2) {
+          for (int cb = first; cb < nblocks; cb += COLS) {
             float v[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.0f;
@@ -730,13 +766,13 @@ inline int current_device(Device* d) {
 template <class Walk, int PLANES>
 int launch(typename Walk::Params a, const Device& d, int pairs, bool cooperative, cudaStream_t stream) {
   auto kernel = product_kernel<Walk, PLANES>;
-  constexpr size_t smem = SMEM_BYTES + Walk::kTableBytes;
+  constexpr size_t smem = SMEM_BYTES + Walk::kEpiWarps * WARP_STASH + Walk::kTableBytes;
   static_assert(smem <= 232448, "shared memory budget");
   a.status = d.status;
   a.epi_wait_ns = epilogue_wait_ns();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs, 1, 1);
-  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.blockDim = dim3((EPI_FIRST + Walk::kEpiWarps) * 32, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];

@@ -54,13 +54,19 @@ struct Product {
   uint32_t idesc;
   float* part;
   unsigned int* arrivals;
+
+  // Symmetric: tiles of row tile tm, those that reach n <= m.
+  __host__ __device__ int sym_tiles(int tm) const {
+    const int c = ceil_div((tm + 1) * BM, bn);
+    return c < tiles_n ? c : tiles_n;
+  }
 };
 
 // Deals out the units of every product of every step, in that order.
 template <int PLANES>
 struct ChainWalk {
   static constexpr bool kScaled = true;
-  static constexpr int kEpiWarps = PLANES == 2 ? 16 : 8;
+  static constexpr int kEpiWarps = 8;
   static constexpr size_t kTableBytes = 0;
 
   struct Params {
@@ -125,9 +131,8 @@ struct ChainWalk {
     group = tile / p.tiles;
     int r = tile - group * p.tiles, tm, tn;
     if (p.sym) {  // row tile tm has the column tiles that reach n <= m
-      const int per = BM / p.bn;
       tm = 0;
-      for (int c = min(per, p.tiles_n); r >= c; c = min(per * (tm + 1), p.tiles_n)) {
+      for (int c = p.sym_tiles(0); r >= c; c = p.sym_tiles(tm)) {
         r -= c;
         ++tm;
       }
@@ -147,13 +152,14 @@ struct ChainWalk {
     u.kb1 = nkb * (u.split + 1) / u.nsplit;
     u.a_mn = p.a_mn;
     u.b_mn = p.b_mn;
-    u.a_4d = u.b_4d = true;
-    u.nmma = p.b_mn ? ceil_div(u.nn, 128) * 128 : ceil_div(u.nn, 32) * 32;
+    u.a_4d = true;
+    u.b_4d = p.bn % 128 == 0;  // (MN-major) the CTA's half is whole blocks of 64
+    u.nmma = p.b_mn ? p.bn : ceil_div(u.nn, 32) * 32;
     u.mapA = &p.mapA[step & 1];
     u.mapB = &p.mapB[step & 1];
-    u.boxes = 1;
+    u.boxes = p.b_mn && !u.b_4d ? 2 : 1;
     u.box_b = p.bn / 2;
-    u.box_bytes = p.b_mn ? p.bn / 128 * MN_BLOCK : p.bn / 2 * BK * 2;
+    u.box_bytes = !p.b_mn ? p.bn / 2 * BK * 2 : u.b_4d ? p.bn / 128 * MN_BLOCK : MN_BLOCK;
     u.zA = u.zB = group * PLANES;
     u.idesc = p.idesc;
     u.m_extent = p.M;
@@ -216,7 +222,6 @@ struct ChainWalk {
   // An epilogue warp has stored its part of a finished tile.
   __device__ void done() const {
     asm volatile("fence.proxy.async;" ::: "memory");
-    __threadfence();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(a.finished + group), "r"(1u) : "memory");
   }
@@ -498,25 +503,26 @@ struct Shape {
   }
 };
 
-int sym_tiles(int side, int bn) {
-  const int tiles_n = ceil_div(side, bn), per = BM / bn;
-  int t = 0;
-  for (int i = 0; i < ceil_div(side, BM); ++i) t += per * (i + 1) < tiles_n ? per * (i + 1) : tiles_n;
-  return t;
-}
-
 // Tile width and parts of the last wave's tiles for one product, by a model of its time in SM
-// cycles: waves x (k-blocks x cycles of a block + a unit's start and drain), and the joining of parts.
-// A block of a 256-wide tile is 512 cycles of MMA with one slice; narrower ones are bound by what
-// they load.  Two slices triple the MMA; single-step chunks are bound by the epilogue.
+// cycles: waves x (k-blocks x cycles of a block + a unit's start and drain), and the joining of
+// parts.  Cycles of a block as measured at 8192^2: one slice is bound by what the SM can load
+// (59 bytes a cycle: 558 at 256 columns, 413 at 128, 371 at 64), two slices by the MMAs and their
+// issue; single-step chunks by the epilogue.
 void plan_product(Product& p, int batch, int planes, int chunk, int pairs) {
   const int nkb = ceil_div(p.K, BK);
   double best = 1e30;
-  for (int bn = BN; bn >= (p.b_mn ? 128 : 64); bn /= 2) {
-    const int tiles_m = ceil_div(p.M, BM), tiles_n = ceil_div(p.N, bn);
-    const int tiles = p.sym ? sym_tiles(p.N, bn) : tiles_m * tiles_n;
-    const long long all = static_cast<long long>(tiles) * batch;
-    double block = planes == 1 ? (bn == 256 ? 540 : bn == 128 ? 380 : 320) : (bn == 256 ? 1580 : bn == 128 ? 820 : 640);
+  Product q = p;
+  for (int bn = planes == 2 ? BN2 : BN; bn >= (p.b_mn ? 128 : 64); bn -= 64) {
+    q.bn = bn;
+    q.tiles_m = ceil_div(p.M, BM);
+    q.tiles_n = ceil_div(p.N, bn);
+    q.tiles = q.tiles_m * q.tiles_n;
+    if (p.sym) {
+      q.tiles = 0;
+      for (int i = 0; i < q.tiles_m; ++i) q.tiles += q.sym_tiles(i);
+    }
+    const long long all = static_cast<long long>(q.tiles) * batch;
+    double block = planes == 1 ? 310 + bn : 420 + 4.1 * bn;
     if (planes == 2 && chunk == 1) block = KSTEPS * (300.0 + 2 * bn);
     const double fixed = 2000 + 6.0 * bn * planes;
     const int rest = static_cast<int>(all % pairs);
@@ -525,16 +531,13 @@ void plan_product(Product& p, int batch, int planes, int chunk, int pairs) {
       if (s > 1 && (rest == 0 || rest * s > kMaxParts)) break;
       double t = whole;
       if (rest) t += ceil_div(rest * s, pairs) * (ceil_div(nkb, s) * block + fixed);
-      if (s > 1) t += 1500 + 2200.0 * (bn / 256.0) * (1 + s);
+      if (s > 1) t += 3000 + 2500.0 * (bn / 256.0) * (1 + s);
       if (t < best) {
         best = t;
-        p.bn = bn;
-        p.tiles_m = tiles_m;
-        p.tiles_n = tiles_n;
-        p.tiles = tiles;
-        p.nsplit = s;
-        p.full = s > 1 ? static_cast<int>(all - rest) : static_cast<int>(all);
-        p.units = p.full + (s > 1 ? rest * s : 0);
+        q.nsplit = s;
+        q.full = s > 1 ? static_cast<int>(all - rest) : static_cast<int>(all);
+        q.units = q.full + (s > 1 ? rest * s : 0);
+        p = q;
       }
     }
   }
@@ -627,7 +630,8 @@ int run_chain(const Shape& sh, const Plan& plan, uint16_t* const (&X)[2], uint16
       ok = ok && x_map(&g.mapA[i], i, HALF_M) && x_map(&g.mapB[i], i, g.bn / 2) && mn_map(&x.mapA[i], i, 2) &&
            s_map(&x.mapB[i], B, x.bn / 2);
     else
-      ok = ok && mn_map(&g.mapA[i], i, 2) && mn_map(&g.mapB[i], i, g.bn / 128) && s_map(&x.mapA[i], B, HALF_M) &&
+      ok = ok && mn_map(&g.mapA[i], i, 2) &&
+           (g.bn % 128 ? x_map(&g.mapB[i], i, BK) : mn_map(&g.mapB[i], i, g.bn / 128)) && s_map(&x.mapA[i], B, HALF_M) &&
            x_map(&x.mapB[i], i, x.bn / 2);
   }
   if (!ok) return OZ_ECUDA;

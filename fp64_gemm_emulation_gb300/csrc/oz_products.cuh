@@ -42,6 +42,7 @@ namespace prod {
 
 constexpr int BM = 256, HALF_M = 128;
 constexpr int BN = 256, HALF_N = 128;
+constexpr int BN2 = 192;                      // widest tile with two slices: its running sums fit the registers
 constexpr int BK = 64;
 constexpr int UMMA_K = 16;
 constexpr int KSTEPS = BK / UMMA_K;
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
     product_kernel(const __grid_constant__ typename Walk::Params a) {
   constexpr int EPI_WARPS = Walk::kEpiWarps;
   constexpr int COLS = EPI_WARPS / 4;                 // warps that share the blocks of 32 columns of a quadrant
-  constexpr int RUNS = PLANES == 2 ? 8 / COLS : 1;    // two slices: blocks whose sums a warp holds
+  constexpr int RUNS = PLANES == 2 ? BN2 / 32 / COLS : 1;  // two slices: blocks whose sums a warp holds
   constexpr uint32_t STASH = EPI_WARPS * WARP_STASH;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));

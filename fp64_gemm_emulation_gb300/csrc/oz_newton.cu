@@ -66,7 +66,7 @@ struct Product {
 template <int PLANES>
 struct ChainWalk {
   static constexpr bool kScaled = true;
-  static constexpr int kEpiWarps = 8;
+  static constexpr int kEpiWarps = PLANES == 2 ? 12 : 8;
   static constexpr size_t kTableBytes = 0;
 
   struct Params {
@@ -157,7 +157,7 @@ struct ChainWalk {
     u.nmma = p.b_mn ? p.bn : ceil_div(u.nn, 32) * 32;
     u.mapA = &p.mapA[step & 1];
     u.mapB = &p.mapB[step & 1];
-    u.boxes = p.b_mn && !u.b_4d ? 2 : 1;
+    u.boxes = p.b_mn && !u.b_4d ? ceil_div(p.bn / 2, 64) : 1;
     u.box_b = p.bn / 2;
     u.box_bytes = !p.b_mn ? p.bn / 2 * BK * 2 : u.b_4d ? p.bn / 128 * MN_BLOCK : MN_BLOCK;
     u.zA = u.zB = group * PLANES;
@@ -512,7 +512,7 @@ void plan_product(Product& p, int batch, int planes, int chunk, int pairs) {
   const int nkb = ceil_div(p.K, BK);
   double best = 1e30;
   Product q = p;
-  for (int bn = planes == 2 ? BN2 : BN; bn >= (p.b_mn ? 128 : 64); bn -= 64) {
+  for (int bn = planes == 2 ? BN2 : BN; bn >= 64; bn -= 32) {
     q.bn = bn;
     q.tiles_m = ceil_div(p.M, BM);
     q.tiles_n = ceil_div(p.N, bn);
@@ -522,7 +522,7 @@ void plan_product(Product& p, int batch, int planes, int chunk, int pairs) {
       for (int i = 0; i < q.tiles_m; ++i) q.tiles += q.sym_tiles(i);
     }
     const long long all = static_cast<long long>(q.tiles) * batch;
-    double block = planes == 1 ? 310 + bn : 420 + 4.1 * bn;
+    double block = planes == 1 ? 310 + bn : 200 + 5.2 * bn;
     if (planes == 2 && chunk == 1) block = KSTEPS * (300.0 + 2 * bn);
     const double fixed = 2000 + 6.0 * bn * planes;
     const int rest = static_cast<int>(all % pairs);

@@ -11,8 +11,10 @@
 // Kernel shape: clusters of two CTAs (cta_group::2), persistent over the units (tile, part of k)
 // that a walker deals out (GroupedWalk here, the Newton-Schulz chain in oz_newton.cu).
 //   warp 0: TMA producer   warp 1: TMEM owner + MMA issuer (leader)   others: epilogue (Walk::kEpiWarps)
-//   6 stages of 32 KB (128 x 64 of A and up to 128 x 64 of B in each CTA); two 256-column
-//   FP32 accumulators in tensor memory, so a tile's epilogue runs under the next one's MMAs.
+//   6 stages of 32 KB (128 x 64 of A and up to 128 x 64 of B in each CTA); two 256-column FP32
+//   accumulators in tensor memory, so a tile's epilogue runs under the next one's MMAs (two
+//   slices: three of 160 columns; with two of 192, each chunk's hand-over to the epilogue and back,
+//   about 840 cycles beside its 930 of work, left the tensor cores idle for a fifth of the time).
 // What bounds it: one thread issues every MMA and one every copy, so both loops are kept to a few
 // instructions (at 8192^3, descriptors rebuilt for each MMA: 981 TFLOP/s; two descriptor words and
 // one add: 1524; one TMA copy for each operand and stage instead of up to six: 1780).
@@ -21,8 +23,8 @@
 // (tail_split).  Each part's FP32 sums go to the workspace, and the CTA that arrives last (an
 // atomic counter for each tile and CTA) adds the parts in their order, so results do not depend
 // on timing and nobody waits.
-// Two slices (PLANES == 2): operands are h + l with h, l in FP16.  A chunk of MMA steps sums
-// h l' + l h' and then h h' into one accumulator; the tensor core truncates as it accumulates,
+// Two slices (PLANES == 2): operands are h + l with h, l in FP16.  A chunk (a k-block or one MMA
+// step) sums h l' + l h' and then h h' into one accumulator; the tensor core truncates as it accumulates,
 // so the sums leave it after every chunk and go on in FP32 registers (round to nearest).
 // Every wait is bounded (as in the residue GEMM): on expiry the pair records OZ_ETIMEOUT,
 // drains what it issued and returns.
@@ -42,7 +44,7 @@ namespace prod {
 
 constexpr int BM = 256, HALF_M = 128;
 constexpr int BN = 256, HALF_N = 128;
-constexpr int BN2 = 192;                      // widest tile with two slices: its running sums fit the registers
+constexpr int BN2 = 160;                      // widest tile with two slices: three accumulators fit tensor memory
 constexpr int BK = 64;
 constexpr int UMMA_K = 16;
 constexpr int KSTEPS = BK / UMMA_K;
@@ -375,8 +377,9 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
     product_kernel(const __grid_constant__ typename Walk::Params a) {
   constexpr int EPI_WARPS = Walk::kEpiWarps;
   constexpr int COLS = EPI_WARPS / 4;                 // warps that share the blocks of 32 columns of a quadrant
-  constexpr int RUNS = PLANES == 2 ? BN2 / 32 / COLS : 1;  // two slices: blocks whose sums a warp holds
+  constexpr int RUNS = PLANES == 2 ? (BN2 / 32 + COLS - 1) / COLS : 1;  // two slices: blocks whose sums a warp holds
   constexpr uint32_t STASH = EPI_WARPS * WARP_STASH;
+  constexpr uint32_t NACC = PLANES == 2 ? 3 : 2, ACC_COLS = PLANES == 2 ? BN2 : BN;  // accumulators, their columns
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
@@ -385,9 +388,9 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(stash + STASH);
   uint64_t* full = bars;                   // [STAGES] TMA (both CTAs) -> MMA  (used in the leader)
   uint64_t* empty = bars + STAGES;         // [STAGES] MMA -> TMA              (both CTAs)
-  uint64_t* accfull = bars + 2 * STAGES;   // [2]      MMA -> epilogue         (both CTAs)
-  uint64_t* accempty = accfull + 2;        // [2]      epilogues (both) -> MMA (used in the leader)
-  uint64_t* drain = accempty + 2;          // [1]      all MMAs of the pair done (both CTAs)
+  uint64_t* accfull = bars + 2 * STAGES;   // [NACC]   MMA -> epilogue         (both CTAs)
+  uint64_t* accempty = accfull + NACC;     // [NACC]   epilogues (both) -> MMA (used in the leader)
+  uint64_t* drain = accempty + NACC;         // [1]      all MMAs of the pair done (both CTAs)
   uint64_t* epibar = drain + 1;            // [1]      epilogue warps rendezvous (per CTA)
   uint64_t* exitbar = epibar + 1;          // [1]      the peer has finished (per CTA)
   uint64_t* proddone = exitbar + 1;        // [1]      both producers have stopped (used in the leader)
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
       mbar_init(&full[i], 2);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (uint32_t i = 0; i < NACC; ++i) {
       mbar_init(&accfull[i], 1);
       mbar_init(&accempty[i], 2 * EPI_WARPS);
     }
@@ -477,9 +480,16 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
       // ------------------------------------------------------------ MMA issuer (leader only)
       int stage = 0;
       uint32_t phase = 0;
-      uint32_t g = 0;
+      uint32_t acc = 0, acc_phase = 1;  // the next accumulator, and the parity of its being free
       uint32_t consumed = 0;
       bool ok = true;
+      auto sum_done = [&]() {
+        umma_commit_pair(&accfull[acc], 0x3);
+        if (++acc == NACC) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+      };
       Walk walk(a, table);
       Unit u;
       while (ok && !*abort_flag && walk.next(u)) {
@@ -491,12 +501,12 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
         if (left == 0) continue;
         uint32_t in_chunk = 0, d_tmem = 0;
         if (PLANES == 1) {  // the whole part in one accumulator
-          if (!mbar_wait_or_abort(&accempty[g & 1], ((g >> 1) & 1) ^ 1, kWaitLimitNs, abort_flag)) {
+          if (!mbar_wait_or_abort(&accempty[acc], acc_phase, kWaitLimitNs, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          d_tmem = tmem_base + (g & 1) * BN;
+          d_tmem = tmem_base + acc * ACC_COLS;
         }
         for (; left > 0; --left) {
 #pragma unroll
@@ -517,22 +527,39 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
               in_chunk = 1;
             }
           } else {
-            // Chunks of a.chunk steps (a divisor of a k-block's); the small products first, so that
-            // the truncation of their additions is small too.
+            // A chunk is a whole k-block or a single step; the small products come first, so that the
+            // truncation of their additions is small too.
             const uint32_t al = ad + (A_STAGE >> 4), bl = bd + (B_STAGE >> 4);
-            for (int k0 = 0; k0 < KSTEPS; k0 += a.chunk, ++g) {
-              if (!mbar_wait_or_abort(&accempty[g & 1], ((g >> 1) & 1) ^ 1, kWaitLimitNs, abort_flag)) {
+            auto next_sum = [&]() {
+              if (!mbar_wait_or_abort(&accempty[acc], acc_phase, kWaitLimitNs, abort_flag)) return false;
+              tc_fence_after();
+              d_tmem = tmem_base + acc * ACC_COLS;
+              return true;
+            };
+            if (a.chunk == KSTEPS) {
+              if (!next_sum()) {
                 ok = false;
                 break;
               }
-              tc_fence_after();
-              d_tmem = tmem_base + (g & 1) * BN;
-              for (int kk = k0; kk < k0 + a.chunk; ++kk) {
-                umma_pair(d_tmem, ad + kk * a_step, bl + kk * b_step, idesc, kk > k0 ? 1u : 0u);
+#pragma unroll
+              for (int kk = 0; kk < KSTEPS; ++kk) {
+                umma_pair(d_tmem, ad + kk * a_step, bl + kk * b_step, idesc, kk > 0 ? 1u : 0u);
                 umma_pair(d_tmem, al + kk * a_step, bd + kk * b_step, idesc, 1u);
               }
-              for (int kk = k0; kk < k0 + a.chunk; ++kk) umma_pair(d_tmem, ad + kk * a_step, bd + kk * b_step, idesc, 1u);
-              umma_commit_pair(&accfull[g & 1], 0x3);
+#pragma unroll
+              for (int kk = 0; kk < KSTEPS; ++kk) umma_pair(d_tmem, ad + kk * a_step, bd + kk * b_step, idesc, 1u);
+              sum_done();
+            } else {
+              for (int kk = 0; kk < KSTEPS; ++kk) {
+                if (!next_sum()) {
+                  ok = false;
+                  break;
+                }
+                umma_pair(d_tmem, ad + kk * a_step, bl + kk * b_step, idesc, 0u);
+                umma_pair(d_tmem, al + kk * a_step, bd + kk * b_step, idesc, 1u);
+                umma_pair(d_tmem, ad + kk * a_step, bd + kk * b_step, idesc, 1u);
+                sum_done();
+              }
             }
             if (!ok) break;
           }
@@ -546,8 +573,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
         }
         if (!ok) break;
         if (PLANES == 1) {
-          umma_commit_pair(&accfull[g & 1], 0x3);
-          ++g;
+          sum_done();
         }
       }
       if (!ok && !*abort_flag) stop_pair(abort_flag, a.status);
@@ -576,7 +602,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
     const int first = (warp - EPI_FIRST) >> 2;
     const int mrow = static_cast<int>(rank) * HALF_M + quad * 32;
     uint8_t* my_stash = stash + (warp - EPI_FIRST) * WARP_STASH;
-    uint32_t g = 0, eph = 0;
+    uint32_t acc = 0, acc_phase = 0, eph = 0;
     bool ok = true;
     Walk walk(a, table);
     walk.outside(warp - EPI_FIRST);
@@ -593,15 +619,14 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
         for (int i = 0; i < RUNS * 32; ++i) run[i >> 5][i & 31] = 0.0f;
       }
       const int nchunks = PLANES == 1 ? (u.kb1 > u.kb0 ? 1 : 0) : (u.kb1 - u.kb0) * (KSTEPS / a.chunk);
-      for (int ch = 0; ch < nchunks; ++ch, ++g) {
-        const uint32_t acc = g & 1;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&accfull[acc], (g >> 1) & 1, a.epi_wait_ns, abort_flag))) {
+      for (int ch = 0; ch < nchunks; ++ch) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&accfull[acc], acc_phase, a.epi_wait_ns, abort_flag))) {
           ok = false;
           if (lane == 0 && !*abort_flag) stop_pair(abort_flag, a.status);
           break;
         }
         tc_fence_after();
-        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * BN;
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * ACC_COLS;
         if (PLANES == 2) {
 #pragma unroll
           for (int j = 0; j < RUNS; ++j) {
@@ -635,6 +660,10 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&accempty[acc]), 0));
+        }
+        if (++acc == NACC) {
+          acc = 0;
+          acc_phase ^= 1;
         }
       }
       if (!ok) break;

@@ -159,7 +159,8 @@ struct ChainWalk {
     u.mapB = &p.mapB[step & 1];
     u.boxes = p.b_mn && !u.b_4d ? ceil_div(p.bn / 2, 64) : 1;
     u.box_b = p.bn / 2;
-    u.box_bytes = !p.b_mn ? p.bn / 2 * BK * 2 : u.b_4d ? p.bn / 128 * MN_BLOCK : MN_BLOCK;
+    u.b_plane = !p.b_mn ? p.bn / 2 * BK * 2 : p.bn / 128 * MN_BLOCK;
+    u.box_bytes = !p.b_mn || u.b_4d ? PLANES * u.b_plane : MN_BLOCK;
     u.zA = u.zB = group * PLANES;
     u.idesc = p.idesc;
     u.m_extent = p.M;
@@ -513,6 +514,8 @@ void plan_product(Product& p, int batch, int planes, int chunk, int pairs) {
   double best = 1e30;
   Product q = p;
   for (int bn = planes == 2 ? BN2 : BN; bn >= 64; bn -= 32) {
+    if (planes == 2 && p.b_mn && bn != 128) continue;  // both slices in one box: whole blocks of 64
+    if (p.b_mn && bn < 128) break;
     q.bn = bn;
     q.tiles_m = ceil_div(p.M, BM);
     q.tiles_n = ceil_div(p.N, bn);
@@ -612,16 +615,16 @@ int run_chain(const Shape& sh, const Plan& plan, uint16_t* const (&X)[2], uint16
 
   const uint64_t mats = static_cast<uint64_t>(sh.batch) * PLANES, xl = 2ull * sh.ldx, sl = 2ull * sh.lds;
   auto s_map = [&](CUtensorMap* t, const void* base, int box) {
-    return make_map(t, base, false, side, side, mats, sl, 2ull * a.splane, box);
+    return make_map(t, base, false, side, side, mats, sl, 2ull * a.splane, box, PLANES);
   };
   auto x_map = [&](CUtensorMap* t, int i, int box) {
-    return make_map(t, X[i], false, sh.cols, sh.rows, mats, xl, 2ull * a.xplane, box);
+    return make_map(t, X[i], false, sh.cols, sh.rows, mats, xl, 2ull * a.xplane, box, PLANES);
   };
   // Rows of ldx, a multiple of 64 (so the map is 4-D): the padding past the last column is the
   // workspace's own, and what is read there only reaches output elements that are never stored.
   auto mn_map = [&](CUtensorMap* t, int i, int blocks) {
     int is_4d = 0;
-    return make_mn_map(t, &is_4d, blocks, X[i], false, sh.ldx, sh.rows, mats, xl, 2ull * a.xplane) && is_4d;
+    return make_mn_map(t, &is_4d, blocks, X[i], false, sh.ldx, sh.rows, mats, xl, 2ull * a.xplane, PLANES) && is_4d;
   };
   bool ok = true;
   for (int i = 0; i < 2 && ok; ++i) {

@@ -11,7 +11,8 @@
 // Kernel shape: clusters of two CTAs (cta_group::2), persistent over the units (tile, part of k)
 // that a walker deals out (GroupedWalk here, the Newton-Schulz chain in oz_newton.cu).
 //   warp 0: TMA producer   warp 1: TMEM owner + MMA issuer (leader)   others: epilogue (Walk::kEpiWarps)
-//   6 stages of 32 KB (128 x 64 of A and up to 128 x 64 of B in each CTA); two 256-column FP32
+//   6 stages of 32 KB (128 x 64 of A and up to 128 x 64 of B in each CTA), with two slices 4 of 52 KB;
+//   two 256-column FP32
 //   accumulators in tensor memory, so a tile's epilogue runs under the next one's MMAs (two
 //   slices: three of 160 columns; with two of 192, each chunk's hand-over to the epilogue and back,
 //   about 840 cycles beside its 930 of work, left the tensor cores idle for a fifth of the time).
@@ -48,15 +49,21 @@ constexpr int BN2 = 160;                      // widest tile with two slices: th
 constexpr int BK = 64;
 constexpr int UMMA_K = 16;
 constexpr int KSTEPS = BK / UMMA_K;
-constexpr int STAGES = 6;
-constexpr uint32_t A_STAGE = HALF_M * BK * 2;
-constexpr uint32_t B_STAGE = HALF_N * BK * 2;
-constexpr uint32_t STAGE_BYTES = A_STAGE + B_STAGE;
+constexpr uint32_t A_PLANE = HALF_M * BK * 2;  // one slice of a stage's A
 constexpr uint32_t MN_BLOCK = 64 * BK * 2;    // 64 contiguous m (or n) x 64 k
 constexpr int EPI_FIRST = 2;                  // the first epilogue warp
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t WARP_STASH = 32 * 32 * 2;  // a 32 x 32 block of 16 bits, per epilogue warp
-constexpr size_t SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 256;  // and the stash, and the walker's table
+constexpr uint32_t WARP_STASH = 16 * 32 * 2;  // half of a 32 x 32 block of 16 bits, per epilogue warp
+
+// The ring of stages: 64 k of A and B, both slices of them with two slices.
+template <int PLANES>
+struct Ring {
+  static constexpr int STAGES = PLANES == 2 ? 4 : 6;
+  static constexpr uint32_t A_STAGE = PLANES * A_PLANE;
+  static constexpr uint32_t B_STAGE = PLANES == 2 ? 2 * (BN2 / 2) * BK * 2 : HALF_N * BK * 2;
+  static constexpr uint32_t BYTES = STAGES * (A_STAGE + B_STAGE);
+};
+
 constexpr long long PART_BLOCK = 32 * HALF_M;  // floats of 32 columns of one CTA's part
 
 enum OutType { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2, kOutSlices = 3 };
@@ -71,7 +78,8 @@ struct Unit {
   bool a_mn, b_mn;          // MN-major operands ...
   bool a_4d, b_4d;          // ... with a 4-D map, whose box holds the CTA's whole tile
   int box_b, boxes;         // B copies: rows of a box (K-major), boxes of a stage
-  uint32_t box_bytes;
+  uint32_t box_bytes;       // all slices'
+  uint32_t b_plane;         // distance of B's slices in a stage
   int zA, zB;               // last coordinate of A and B (matrix of the batch, or first row)
   uint32_t idesc;
   int m_extent;             // the output's m
@@ -156,7 +164,7 @@ __device__ __forceinline__ bool warps_meet(uint64_t* bar, uint32_t& phase, const
 // The epilogue works on blocks of 32 m x 32 n.  tcgen05.ld.16x256b gives a thread the elements
 //   m = 16 (i / 16) + lane / 4 + 8 ((i / 2) % 2),   n = 8 ((i / 4) % 4) + 2 (lane % 4) + i % 2
 // in register i: the fragments that stmatrix stores, as they are (rows of m) or transposed (rows
-// of n), so a block goes through the warp's 2 KB stash with 4 + 4 shared-memory instructions and
+// of n), so a block goes through the warp's stash with 4 + 4 shared-memory instructions and
 // leaves as 16-byte stores in either orientation.  (One lane per m, 32 two-byte stores a block:
 // the epilogue took 7600 cycles of a 256 x 256 tile and bounded the weight gradient.)
 __device__ __forceinline__ int frag_m(int i, int lane) { return ((i >> 4) << 4) + (lane >> 2) + ((i >> 1 & 1) << 3); }
@@ -217,27 +225,33 @@ __device__ __forceinline__ void store_block(const uint32_t (&w)[16], uint8_t* st
   const int lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(stash);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (ROWS_N)  // the four 8-element groups of m, rows n = 8 j ..
-      stmatrix4<true>(base + stash_at(8 * j + (lane & 7), lane >> 3), w[2 * j], w[2 * j + 1], w[8 + 2 * j], w[9 + 2 * j]);
-    else  // the four 8-element groups of n, rows m = 8 j ..
-      stmatrix4<false>(base + stash_at(8 * j + (lane & 7), lane >> 3), w[(j >> 1) * 8 + (j & 1)],
-                       w[(j >> 1) * 8 + 2 + (j & 1)], w[(j >> 1) * 8 + 4 + (j & 1)], w[(j >> 1) * 8 + 6 + (j & 1)]);
-  }
-  __syncwarp();
-  if (vec && width == 32) {
-    uint4 x[4];
+  for (int h = 0; h < 2; ++h) {  // 16 rows at a time
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4*>(stash + stash_at(8 * j + (lane >> 2), lane & 3));
-    uint16_t* dst = out + (lane >> 2) * ld + (lane & 3) * 8;
+    for (int i = 0; i < 2; ++i) {
+      const int j = 2 * h + i;
+      const uint32_t at = base + stash_at(8 * i + (lane & 7), lane >> 3);
+      if (ROWS_N)  // the four 8-element groups of m, rows n = 8 j ..
+        stmatrix4<true>(at, w[2 * j], w[2 * j + 1], w[8 + 2 * j], w[9 + 2 * j]);
+      else  // the four 8-element groups of n, rows m = 8 j ..
+        stmatrix4<false>(at, w[h * 8 + i], w[h * 8 + 2 + i], w[h * 8 + 4 + i], w[h * 8 + 6 + i]);
+    }
+    __syncwarp();
+    uint16_t* half = out + 16 * h * ld;
+    if (vec && width == 32) {
+      uint4 x[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (8 * j + (lane >> 2) < rows) *reinterpret_cast<uint4*>(dst + 8 * j * ld) = x[j];
-  } else if (lane < width) {
-    for (int r = 0; r < rows; ++r)
-      out[r * ld + lane] = *reinterpret_cast<const uint16_t*>(stash + stash_at(r, lane >> 3) + (lane & 7) * 2);
+      for (int i = 0; i < 2; ++i) x[i] = *reinterpret_cast<const uint4*>(stash + stash_at(8 * i + (lane >> 2), lane & 3));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        if (16 * h + r < rows) *reinterpret_cast<uint4*>(half + r * ld + (lane & 3) * 8) = x[i];
+      }
+    } else if (lane < width) {
+      for (int r = 0; r < 16 && 16 * h + r < rows; ++r)
+        half[r * ld + lane] = *reinterpret_cast<const uint16_t*>(stash + stash_at(r, lane >> 3) + (lane & 7) * 2);
+    }
+    __syncwarp();
   }
-  __syncwarp();
 }
 
 // The finished sums of one block, whose first m is mrow within the tile and first n is c0.
@@ -309,49 +323,45 @@ __device__ __forceinline__ void add_part(const float* part, float (&v)[32]) {
 }
 
 // The producer's loop over a unit's stages, compiled for each way its operands are copied, so that
-// a stage is a wait, an arrival and (mostly) two copies and nothing else.  KA: K-major, MN-major 4-D,
-// MN-major in two 3-D boxes.  KB: K-major in one box, in several, MN-major 4-D, 3-D boxes.
-// Returns false when a wait ran out or the pair was stopped.
+// a stage is a wait, an arrival and (mostly) two copies and nothing else: boxes hold both slices.
+// KA: K-major, MN-major 4-D, MN-major in two 3-D boxes.  KB: K-major in one box, in several,
+// MN-major 4-D, 3-D boxes.  Returns false when a wait ran out or the pair was stopped.
 template <int KA, int KB, int PLANES>
 __device__ __forceinline__ bool load_unit(const Unit& u, uint8_t* sA, uint8_t* sB, uint64_t* empty, uint32_t full_leader,
                                           uint32_t rank, int& stage, uint32_t& phase, uint32_t& issued,
                                           const volatile int* abort_flag) {
+  typedef Ring<PLANES> R;
   const int rowA = u.m0 + static_cast<int>(rank) * HALF_M;
   const int rowB = u.n0 + static_cast<int>(rank) * (u.nmma >> 1);
-  const uint32_t bytes = A_STAGE + (KB == 0 || KB == 2 ? 1 : u.boxes) * u.box_bytes;
+  const uint32_t bytes = R::A_STAGE + (KB == 0 || KB == 2 ? 1 : u.boxes) * u.box_bytes;
   int k = u.k0 + u.kb0 * BK;
   for (int kb = u.kb0; kb < u.kb1; ++kb, k += BK) {
-#pragma unroll
-    for (int p = 0; p < PLANES; ++p) {
-      if (!mbar_wait_or_abort(&empty[stage], phase ^ 1, kWaitLimitNs, abort_flag)) return false;
-      const uint32_t bar = full_leader + stage * 8;
-      mbar_arrive_expect_tx_cluster(bar, bytes);
-      uint8_t* dA = sA + stage * A_STAGE;
-      uint8_t* dB = sB + stage * B_STAGE;
-      if (KA == 0) {
-        tma_load_3d_pair(dA, u.mapA, bar, k, rowA, u.zA + p);
-      } else if (KA == 1) {
-        tma_load_4d_pair(dA, u.mapA, bar, 0, k, rowA / 64, u.zA + p);
-      } else {
-        tma_load_3d_pair(dA, u.mapA, bar, rowA, k, u.zA + p);
-        tma_load_3d_pair(dA + MN_BLOCK, u.mapA, bar, rowA + 64, k, u.zA + p);
-      }
-      if (KB == 0) {
-        tma_load_3d_pair(dB, u.mapB, bar, k, rowB, u.zB + p);
-      } else if (KB == 1) {
-        for (int b = 0; b < u.boxes; ++b)
-          tma_load_3d_pair(dB + b * u.box_bytes, u.mapB, bar, k, rowB + u.box_b * b, u.zB + p);
-      } else if (KB == 2) {  // a last, narrower tile loads the full box: B_STAGE has room for it
-        tma_load_4d_pair(dB, u.mapB, bar, 0, k, rowB / 64, u.zB + p);
-      } else {
-        for (int b = 0; b < u.boxes; ++b)
-          tma_load_3d_pair(dB + b * MN_BLOCK, u.mapB, bar, rowB + 64 * b, k, u.zB + p);
-      }
-      ++issued;
-      if (++stage == STAGES) {
-        stage = 0;
-        phase ^= 1;
-      }
+    if (!mbar_wait_or_abort(&empty[stage], phase ^ 1, kWaitLimitNs, abort_flag)) return false;
+    const uint32_t bar = full_leader + stage * 8;
+    mbar_arrive_expect_tx_cluster(bar, bytes);
+    uint8_t* dA = sA + stage * R::A_STAGE;
+    uint8_t* dB = sB + stage * R::B_STAGE;
+    if (KA == 0) {
+      tma_load_3d_pair(dA, u.mapA, bar, k, rowA, u.zA);
+    } else if (KA == 1) {
+      tma_load_4d_pair(dA, u.mapA, bar, 0, k, rowA / 64, u.zA);
+    } else {
+      tma_load_3d_pair(dA, u.mapA, bar, rowA, k, u.zA);
+      tma_load_3d_pair(dA + MN_BLOCK, u.mapA, bar, rowA + 64, k, u.zA);
+    }
+    if (KB == 0) {
+      tma_load_3d_pair(dB, u.mapB, bar, k, rowB, u.zB);
+    } else if (KB == 1) {
+      for (int b = 0; b < u.boxes; ++b) tma_load_3d_pair(dB + b * u.box_bytes, u.mapB, bar, k, rowB + u.box_b * b, u.zB);
+    } else if (KB == 2) {  // a last, narrower tile loads the full box: the stage has room for it
+      tma_load_4d_pair(dB, u.mapB, bar, 0, k, rowB / 64, u.zB);
+    } else {
+      for (int b = 0; b < u.boxes; ++b) tma_load_3d_pair(dB + b * MN_BLOCK, u.mapB, bar, rowB + 64 * b, k, u.zB);
+    }
+    ++issued;
+    if (++stage == R::STAGES) {
+      stage = 0;
+      phase ^= 1;
     }
   }
   return true;
@@ -375,6 +385,8 @@ __device__ __forceinline__ bool elect_one() {
 template <class Walk, int PLANES>
 __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
     product_kernel(const __grid_constant__ typename Walk::Params a) {
+  typedef Ring<PLANES> R;
+  constexpr int STAGES = R::STAGES;
   constexpr int EPI_WARPS = Walk::kEpiWarps;
   constexpr int COLS = EPI_WARPS / 4;                 // warps that share the blocks of 32 columns of a quadrant
   constexpr int RUNS = PLANES == 2 ? (BN2 / 32 + COLS - 1) / COLS : 1;  // two slices: blocks whose sums a warp holds
@@ -383,8 +395,8 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
-  uint8_t* sB = smem + STAGES * A_STAGE;
-  uint8_t* stash = smem + STAGES * STAGE_BYTES;
+  uint8_t* sB = smem + STAGES * R::A_STAGE;
+  uint8_t* stash = smem + R::BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(stash + STASH);
   uint64_t* full = bars;                   // [STAGES] TMA (both CTAs) -> MMA  (used in the leader)
   uint64_t* empty = bars + STAGES;         // [STAGES] MMA -> TMA              (both CTAs)
@@ -509,17 +521,13 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
           d_tmem = tmem_base + acc * ACC_COLS;
         }
         for (; left > 0; --left) {
-#pragma unroll
-          for (int p = 0; p < PLANES; ++p) {
-            if (!mbar_wait_or_abort(&full[stage + p], phase, kWaitLimitNs, abort_flag)) {
-              ok = false;
-              break;
-            }
-            ++consumed;
+          if (!mbar_wait_or_abort(&full[stage], phase, kWaitLimitNs, abort_flag)) {
+            ok = false;
+            break;
           }
-          if (!ok) break;
+          ++consumed;
           tc_fence_after();
-          const uint32_t ad = a_desc + stage * (A_STAGE >> 4), bd = b_desc + stage * (B_STAGE >> 4);
+          const uint32_t ad = a_desc + stage * (R::A_STAGE >> 4), bd = b_desc + stage * (R::B_STAGE >> 4);
           if (PLANES == 1) {
 #pragma unroll
             for (int kk = 0; kk < KSTEPS; ++kk) {
@@ -529,7 +537,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
           } else {
             // A chunk is a whole k-block or a single step; the small products come first, so that the
             // truncation of their additions is small too.
-            const uint32_t al = ad + (A_STAGE >> 4), bl = bd + (B_STAGE >> 4);
+            const uint32_t al = ad + (A_PLANE >> 4), bl = bd + (u.b_plane >> 4);
             auto next_sum = [&]() {
               if (!mbar_wait_or_abort(&accempty[acc], acc_phase, kWaitLimitNs, abort_flag)) return false;
               tc_fence_after();
@@ -563,10 +571,8 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
             }
             if (!ok) break;
           }
-#pragma unroll
-          for (int p = 0; p < PLANES; ++p) umma_commit_pair(&empty[stage + p], 0x3);
-          stage += PLANES;
-          if (stage == STAGES) {
+          umma_commit_pair(&empty[stage], 0x3);
+          if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
           }
@@ -756,11 +762,11 @@ inline bool encode(CUtensorMap* map, const void* base, bool bf16, int rank, cons
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [d2][d1][d0] with strides s1, s2 in bytes (multiples of 16); box {64, box_rows, 1}.
+// [d2][d1][d0] with strides s1, s2 in bytes (multiples of 16); box {64, box_rows, mats}.
 inline bool make_map(CUtensorMap* map, const void* base, bool bf16, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
-                     uint64_t s2, int box_rows) {
+                     uint64_t s2, int box_rows, int mats = 1) {
   const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {s1, s2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(mats)};
   return encode(map, base, bf16, 3, dims, strides, box);
 }
 
@@ -769,11 +775,11 @@ inline bool make_map(CUtensorMap* map, const void* base, bool bf16, uint64_t d0,
 // (a last partial block in such a map would reach past the end of the last row) make_map's, one
 // block a box.  *is_4d says which: a load's rank has to be its map's.
 inline bool make_mn_map(CUtensorMap* map, int* is_4d, int blocks, const void* base, bool bf16, uint64_t d0, uint64_t d1,
-                        uint64_t d2, uint64_t s1, uint64_t s2) {
+                        uint64_t d2, uint64_t s1, uint64_t s2, int mats = 1) {
   *is_4d = d0 % 64 == 0;
-  if (!*is_4d) return make_map(map, base, bf16, d0, d1, d2, s1, s2, BK);
+  if (!*is_4d) return make_map(map, base, bf16, d0, d1, d2, s1, s2, BK, mats);
   const cuuint64_t dims[4] = {64, d1, d0 / 64, d2}, strides[3] = {s1, 128, s2};
-  const cuuint32_t box[4] = {64, BK, static_cast<cuuint32_t>(blocks), 1};
+  const cuuint32_t box[4] = {64, BK, static_cast<cuuint32_t>(blocks), static_cast<cuuint32_t>(mats)};
   return encode(map, base, bf16, 4, dims, strides, box);
 }
 
@@ -796,7 +802,7 @@ inline int current_device(Device* d) {
 template <class Walk, int PLANES>
 int launch(typename Walk::Params a, const Device& d, int pairs, bool cooperative, cudaStream_t stream) {
   auto kernel = product_kernel<Walk, PLANES>;
-  constexpr size_t smem = SMEM_BYTES + Walk::kEpiWarps * WARP_STASH + Walk::kTableBytes;
+  constexpr size_t smem = 1024 /*alignment*/ + Ring<PLANES>::BYTES + Walk::kEpiWarps * WARP_STASH + 256 /*barriers*/ + Walk::kTableBytes;
   static_assert(smem <= 232448, "shared memory budget");
   a.status = d.status;
   a.epi_wait_ns = epilogue_wait_ns();

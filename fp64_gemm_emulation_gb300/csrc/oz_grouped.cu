@@ -28,7 +28,7 @@ enum Op { kForward, kDgrad, kWgrad };
 //     neighbouring group ever enters a sum, so its NaNs cannot leak.
 template <Op OP>
 struct GroupedWalk {
-  static constexpr bool kScaled = false;
+  static constexpr bool kScaled = false, kReports = false;
   static constexpr int kEpiWarps = 8;
   static constexpr size_t kTableBytes = 2 * (OZ_MAX_GROUPS + 1) * 4;  // offsets, tile prefix
   static constexpr bool A_MN = OP != kForward, B_MN = OP == kWgrad, RAGGED_SUM = OP == kWgrad;
@@ -184,6 +184,7 @@ struct GroupedWalk {
   }
 
   __device__ bool ready(const volatile int*) const { return true; }
+  __device__ void stored() const {}
   __device__ void done() const {}
   __device__ static void gave_up(const Params&) {}
 
@@ -209,6 +210,11 @@ struct Operand {
     return fits() ? 0 : align256(2 * static_cast<size_t>(roundup(cols, 8)) * rows * mats);
   }
 };
+
+__global__ void zero_kernel(unsigned* words) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  words[threadIdx.x] = 0;
+}
 
 // Copies [mats][rows][cols] of 16-bit elements to rows of ldo (a multiple of 8): one thread per
 // 8 output elements, 2-byte loads (the source has no alignment), one 16-byte store.
@@ -290,7 +296,7 @@ int zero_output(const Problem& p, cudaStream_t stream) {
 }
 
 template <Op OP>
-int launch_op(const Problem& p, float* part, unsigned* arrivals, const Device& dev, cudaStream_t stream) {
+int launch_op(const Problem& p, float* part, unsigned* arrivals, const Device& dev, Start start, cudaStream_t stream) {
   typedef GroupedWalk<OP> Walk;
   const bool bf16 = p.dtype == OZ_BF16;
   typename Walk::Params a{};
@@ -324,7 +330,7 @@ int launch_op(const Problem& p, float* part, unsigned* arrivals, const Device& d
          (Walk::A_MN ? make_mn_map(&a.tmA, &a.a_4d, 2, w.p, bf16, w.cols, w.rows, w.mats, wl, wm)
                      : make_map(&a.tmA, w.p, bf16, w.cols, w.rows, w.mats, wl, wm, HALF_M));
   }
-  return ok ? launch<Walk, 1>(a, dev, dev.pairs, false, stream) : OZ_ECUDA;
+  return ok ? launch<Walk, 1>(a, dev, dev.pairs, start, stream) : OZ_ECUDA;
 }
 
 int run(Problem p, void* workspace, size_t ws_bytes, cudaStream_t stream) {
@@ -344,14 +350,18 @@ int run(Problem p, void* workspace, size_t ws_bytes, cudaStream_t stream) {
   if (p.may_split()) {
     arrivals = reinterpret_cast<unsigned*>(ws);
     part = reinterpret_cast<float*>(ws + align256(sizeof(unsigned) * 2 * kMaxParts));
-    if (cudaMemsetAsync(arrivals, 0, sizeof(unsigned) * 2 * kMaxParts, stream) != cudaSuccess) return OZ_ECUDA;
+    zero_kernel<<<1, 2 * kMaxParts, 0, stream>>>(arrivals);
+    if (cudaGetLastError() != cudaSuccess) return OZ_ECUDA;
     ws += p.split_bytes();
   }
+  // The product overlaps zero_kernel, which everything before it on the stream precedes; a repacked
+  // operand it has to wait for.
+  const Start start = arrivals && p.w.fits() && p.t.fits() ? kOverlap : kAfter;
   if ((rc = repack(p.w, &ws, stream)) || (rc = repack(p.t, &ws, stream))) return rc;
   switch (p.op) {
-    case kForward: return launch_op<kForward>(p, part, arrivals, dev, stream);
-    case kDgrad: return launch_op<kDgrad>(p, part, arrivals, dev, stream);
-    default: return launch_op<kWgrad>(p, part, arrivals, dev, stream);
+    case kForward: return launch_op<kForward>(p, part, arrivals, dev, start, stream);
+    case kDgrad: return launch_op<kDgrad>(p, part, arrivals, dev, start, stream);
+    default: return launch_op<kWgrad>(p, part, arrivals, dev, start, stream);
   }
 }
 

@@ -65,7 +65,7 @@ struct Product {
 // Deals out the units of every product of every step, in that order.
 template <int PLANES>
 struct ChainWalk {
-  static constexpr bool kScaled = true;
+  static constexpr bool kScaled = true, kReports = true;
   static constexpr int kEpiWarps = PLANES == 2 ? 12 : 8;
   static constexpr size_t kTableBytes = 0;
 
@@ -78,7 +78,7 @@ struct ChainWalk {
     const float* scales;          // [matrix][step][2]: factors of the first and the last product
     float diag_s[OZ_MAX_NS_STEPS], alpha_b[OZ_MAX_NS_STEPS], diag_b[OZ_MAX_NS_STEPS];
     unsigned int square;          // bit i: step i has the middle product (c != 0)
-    unsigned int* finished;       // [matrix]: epilogue warps that have finished a tile, over all products
+    unsigned int* finished;       // [matrix]: CTAs that have finished a tile, over all products
     unsigned int* stopped;        // a pair of this launch gave up
     int* status;
     unsigned long long epi_wait_ns;
@@ -105,7 +105,7 @@ struct ChainWalk {
     idx += static_cast<int>(gridDim.x >> 1);
     for (int n = units(); idx - base >= n; n = units()) {  // on to the unit's product
       base += n;
-      if (n) need += a.prod[kind].tiles * 2 * kEpiWarps;
+      if (n) need += a.prod[kind].tiles * 2;  // both CTAs report a tile
       if (kind == kApply) {
         kind = kGram;
         if (++step == a.steps) return false;
@@ -220,11 +220,11 @@ struct ChainWalk {
     return true;
   }
 
-  // An epilogue warp has stored its part of a finished tile.
+  __device__ void stored() const { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+  // A CTA has stored its half of a finished tile.
   __device__ void done() const {
-    asm volatile("fence.proxy.async;" ::: "memory");
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(a.finished + group), "r"(1u) : "memory");
+    asm volatile("red.relaxed.gpu.global.add.u32 [%0], %1;" ::"l"(a.finished + group), "r"(1u) : "memory");
   }
 
   __device__ void outside(int) const {}
@@ -640,7 +640,7 @@ int run_chain(const Shape& sh, const Plan& plan, uint16_t* const (&X)[2], uint16
   if (!ok) return OZ_ECUDA;
   int most = g.units > x.units ? g.units : x.units;
   if (a.square && q.units > most) most = q.units;
-  return launch<Walk, PLANES>(a, dev, most < dev.pairs ? most : dev.pairs, true, stream);
+  return launch<Walk, PLANES>(a, dev, most < dev.pairs ? most : dev.pairs, kCooperative, stream);
 }
 
 int run(int m, int n, int batch, int dtype, const void* G, int ldg, long long stride_g, void* O, int ldo,

@@ -378,10 +378,13 @@ __device__ __forceinline__ bool elect_one() {
   return elected != 0;
 }
 
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The kernel.  Walk deals out the units: Walk::Params are the launch's, setup() runs once for the
 // whole CTA, a Walk of its own in every role gives the pair's units in order (next), and
-// ready() / done() are its dependences between units (the producer before a unit's first load,
-// every epilogue warp of the pair after its last store); gave_up() tells the other pairs that they wait in vain.
+// ready() and, if kReports, stored() / done() are its dependences between units (the producer before a
+// unit's first load, each epilogue thread after its last store, one thread of each CTA when all
+// have stored); gave_up() tells the other pairs that they wait in vain.
 template <class Walk, int PLANES>
 __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
     product_kernel(const __grid_constant__ typename Walk::Params a) {
@@ -410,6 +413,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile uint32_t* issued_by = reinterpret_cast<volatile uint32_t*>(abort_flag + 1);  // [2] (leader)
   volatile uint32_t* arrived = issued_by + 2;
+  uint32_t* warps_done = const_cast<uint32_t*>(issued_by + 3);
   int* table = reinterpret_cast<int*>(stash + STASH + 256);  // the walker's
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -429,6 +433,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
     mbar_init(exitbar, 1);
     mbar_init(proddone, 2);
     *abort_flag = 0;
+    *warps_done = 0;
     mbar_fence_init();
   }
   if (warp == 1) {
@@ -699,6 +704,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
       bool finished = true;
       if (split) {
         // This CTA's part is written; the last of the tile's parts to arrive adds them all.
+        wait_for_previous();  // the arrival counters' zeros may come from a launch that this one overlaps
         __threadfence();
         ok = warps_meet(epibar, eph, abort_flag);
         if (ok && threadIdx.x == EPI_FIRST * 32) *arrived = atomicAdd(&u.arrivals[rank], 1u);
@@ -722,7 +728,19 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
           }
         }
       }
-      if (finished) walk.done();
+      // The CTA's last warp to have stored its blocks reports the tile, so that a tile is one global
+      // atomic a CTA (one a warp: the 1152 of a 2048-wide product held the next one up by 2 us).
+      if (Walk::kReports && finished) {
+        walk.stored();
+        __syncwarp();
+        if (lane == 0) {
+          __threadfence();
+          if (atomicAdd(warps_done, 1u) % EPI_WARPS == EPI_WARPS - 1) {
+            __threadfence();
+            walk.done();
+          }
+        }
+      }
     }
   }
 
@@ -797,10 +815,13 @@ inline int current_device(Device* d) {
   return d->status ? OZ_OK : OZ_ECUDA;
 }
 
-// Launches on `pairs` CTA pairs.  cooperative: the units depend on one another, so all CTAs have to
-// run at once (the launch is refused if they cannot).
+// How a launch follows what is before it: kCooperative: the units depend on one another, so all CTAs
+// have to run at once (the launch is refused if they cannot); kOverlap: it may start while the
+// launch before it ends, of which it needs nothing but the arrival counters' zeros.
+enum Start { kAfter, kCooperative, kOverlap };
+
 template <class Walk, int PLANES>
-int launch(typename Walk::Params a, const Device& d, int pairs, bool cooperative, cudaStream_t stream) {
+int launch(typename Walk::Params a, const Device& d, int pairs, Start start, cudaStream_t stream) {  // on `pairs` CTA pairs
   auto kernel = product_kernel<Walk, PLANES>;
   constexpr size_t smem = 1024 /*alignment*/ + Ring<PLANES>::BYTES + Walk::kEpiWarps * WARP_STASH + 256 /*barriers*/ + Walk::kTableBytes;
   static_assert(smem <= 232448, "shared memory budget");
@@ -816,10 +837,15 @@ int launch(typename Walk::Params a, const Device& d, int pairs, bool cooperative
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeCooperative;
-  attr[1].val.cooperative = 1;
+  if (start == kCooperative) {
+    attr[1].id = cudaLaunchAttributeCooperative;
+    attr[1].val.cooperative = 1;
+  } else {
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = cooperative ? 2 : 1;
+  cfg.numAttrs = start == kAfter ? 1 : 2;
   // The shared-memory limit is the function's, in this context: set on the first launch, and again
   // should a launch be refused (a new context after a device reset).
   static std::atomic<bool> ready[64] = {};

@@ -457,61 +457,89 @@ def ozaki1_dgemm_ws(A, B, num_slices: int, workspace, C=None, stream=None):
 
 
 # ------------------------------------------------------------------ grouped products (experts)
-def _dtype(t) -> int:
-    import torch
+_DTYPE_CODES: dict = {}
 
-    code = {torch.bfloat16: OZ_BF16, torch.float16: OZ_F16, torch.float32: OZ_F32}.get(t.dtype)
+
+def _dtype(t) -> int:
+    if not _DTYPE_CODES:
+        import torch
+
+        _DTYPE_CODES.update({torch.bfloat16: OZ_BF16, torch.float16: OZ_F16, torch.float32: OZ_F32})
+    code = _DTYPE_CODES.get(t.dtype)
     if code is None:
         raise TypeError(f"dtype must be bfloat16, float16 or float32: {t.dtype}")
     return code
 
 
-def _tokens(t, what: str, features: int | None = None):
-    """A row-major (rows, features) matrix whose rows may be strided: (tensor, leading dimension)."""
-    if t.dim() != 2 or (features is not None and t.shape[1] != features):
-        raise ValueError(f"{what} must have shape (rows, {'features' if features is None else features}): {tuple(t.shape)}")
-    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-        raise ValueError(f"{what} must be row-major (stride(1) == 1, stride(0) >= {t.shape[1]})")
-    return t, max(1, int(t.shape[1]), int(t.stride(0)) if t.shape[0] > 1 else 0)
+def _tokens(t, what: str, features: int | None = None) -> int:
+    """Leading dimension of a row-major (rows, features) matrix whose rows may be strided."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (features is not None and shape[1] != features):
+        raise ValueError(f"{what} must have shape (rows, {'features' if features is None else features}): {tuple(shape)}")
+    cols = shape[1]
+    if shape[0] <= 1:
+        if cols > 1 and stride[1] != 1:
+            raise ValueError(f"{what} must be row-major (stride(1) == 1)")
+        return max(1, cols)
+    if (cols > 1 and stride[1] != 1) or stride[0] < cols:
+        raise ValueError(f"{what} must be row-major (stride(1) == 1, stride(0) >= {cols})")
+    return max(1, stride[0])
 
 
-def _experts(t, what: str):
-    """A (groups, n, k) stack whose matrices are row-major: (tensor, leading dimension, stride between matrices)."""
-    if t.dim() != 3:
-        raise ValueError(f"{what} must have shape (groups, n, k): {tuple(t.shape)}")
-    g, n, k = t.shape
-    ld = max(1, int(k), int(t.stride(1)) if n > 1 else 0)
-    if (k > 1 and t.stride(2) != 1) or (n > 1 and t.stride(1) < k) or (g > 1 and t.stride(0) < ld * n):
+def _experts(t, what: str) -> tuple[int, int]:
+    """(leading dimension, stride between matrices) of a (groups, n, k) stack of row-major matrices."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{what} must have shape (groups, n, k): {tuple(shape)}")
+    g, n, k = shape
+    ld = max(1, k, stride[1] if n > 1 else 0)
+    if (k > 1 and stride[2] != 1) or (n > 1 and stride[1] < k) or (g > 1 and stride[0] < ld * n):
         raise ValueError(f"{what} must hold row-major matrices that do not overlap")
-    return t, ld, int(t.stride(0)) if g > 1 else ld * int(n)
+    return ld, (stride[0] if g > 1 else ld * n)
 
 
 def _offsets(offsets, groups: int | None, device):
     import torch
 
+    n = offsets.numel()
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() or offsets.device != device:
         raise ValueError("offsets must be a contiguous int32 vector on the operands' device")
-    if offsets.numel() < 2 or (groups is not None and offsets.numel() != groups + 1):
-        raise ValueError(f"offsets must hold groups + 1 entries: {offsets.numel()} for {groups} groups")
+    if n < 2 or (groups is not None and n != groups + 1):
+        raise ValueError(f"offsets must hold groups + 1 entries: {n} for {groups} groups")
 
 
 def _same(*tensors):
-    first = tensors[0]
-    for t in tensors:
-        if t.dtype != first.dtype or t.device != first.device:
+    dtype, device = tensors[0].dtype, tensors[0].device
+    if device.type != "cuda":
+        raise ValueError("operands must be CUDA tensors")
+    for t in tensors[1:]:
+        if t.dtype != dtype or t.device != device:
             raise ValueError("operands must share one dtype and one device")
-        if not t.is_cuda:
-            raise ValueError("operands must be CUDA tensors")
 
 
-def _run_grouped(name, args, dims, out_args, workspace, stream):
-    """Calls `name`, or its _ws form when a workspace (a uint8 tensor) is given."""
-    st = _stream(stream)
-    if workspace is None:
-        _check(getattr(_lib, name)(*dims, *args, *out_args, st), name)
+def _stream_of(stream, device) -> int:
+    """The raw handle of `stream`, or of the device's current stream."""
+    import torch
+
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return int(getattr(stream, "cuda_stream", stream))
+
+
+def _run_on(name, args, workspace, stream, device):
+    """Calls `name`, or its _ws form when a workspace (a uint8 tensor) is given, on the operands' device."""
+    import torch
+
+    st = _stream_of(stream, device)
+    if workspace is not None:
+        name += "_ws"
+        args += (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    if device.index == torch._C._cuda_getDevice():
+        rc = getattr(_lib, name)(*args, st)
     else:
-        nbytes = workspace.numel() * workspace.element_size()
-        _check(getattr(_lib, name + "_ws")(*dims, *args, *out_args, _ptr(workspace), nbytes, st), name + "_ws")
+        with torch.cuda.device(device):
+            rc = getattr(_lib, name)(*args, st)
+    _check(rc, name)
 
 
 def ozaki_grouped_gemm(X, W, offsets, Y=None, workspace=None, stream=None):
@@ -521,18 +549,18 @@ def ozaki_grouped_gemm(X, W, offsets, Y=None, workspace=None, stream=None):
     Rows outside [offsets[0], offsets[-1]) give zero."""
     import torch
 
-    X, ldx = _tokens(X, "X", W.shape[-1])
-    W, ldw, sw = _experts(W, "W")
+    ldw, sw = _experts(W, "W")
     groups, n, k = W.shape
+    ldx, rows, device = _tokens(X, "X", k), X.shape[0], X.device
     if Y is None:
-        Y = torch.empty((X.shape[0], n), dtype=X.dtype, device=X.device)
+        Y = torch.empty((rows, n), dtype=X.dtype, device=device)
     _same(X, W, Y)
-    _offsets(offsets, groups, X.device)
-    Y, ldy = _tokens(Y, "Y", n)
-    if Y.shape[0] != X.shape[0]:
+    _offsets(offsets, groups, device)
+    ldy = _tokens(Y, "Y", n)
+    if Y.shape[0] != rows:
         raise ValueError("Y must have the rows of X")
-    _run_grouped("ozaki_grouped_gemm", (_ptr(W), ldw, sw, _ptr(X), ldx, _ptr(offsets)),
-                 (n, k, X.shape[0], groups, _dtype(X)), (_ptr(Y), ldy), workspace, stream)
+    _run_on("ozaki_grouped_gemm", (n, k, rows, groups, _dtype(X), W.data_ptr(), ldw, sw, X.data_ptr(), ldx,
+                                        offsets.data_ptr(), Y.data_ptr(), ldy), workspace, stream, device)
     return Y
 
 
@@ -545,18 +573,18 @@ def ozaki_grouped_gemm_dgrad(dY, W, offsets, dX=None, workspace=None, stream=Non
     """dX[r] = W[e]^T dY[r]: the gradient in X of a loss whose gradient in Y is dY (rows, n)."""
     import torch
 
-    W, ldw, sw = _experts(W, "W")
+    ldw, sw = _experts(W, "W")
     groups, n, k = W.shape
-    dY, lddy = _tokens(dY, "dY", n)
+    lddy, rows, device = _tokens(dY, "dY", n), dY.shape[0], dY.device
     if dX is None:
-        dX = torch.empty((dY.shape[0], k), dtype=dY.dtype, device=dY.device)
+        dX = torch.empty((rows, k), dtype=dY.dtype, device=device)
     _same(dY, W, dX)
-    _offsets(offsets, groups, dY.device)
-    dX, lddx = _tokens(dX, "dX", k)
-    if dX.shape[0] != dY.shape[0]:
+    _offsets(offsets, groups, device)
+    lddx = _tokens(dX, "dX", k)
+    if dX.shape[0] != rows:
         raise ValueError("dX must have the rows of dY")
-    _run_grouped("ozaki_grouped_gemm_dgrad", (_ptr(W), ldw, sw, _ptr(dY), lddy, _ptr(offsets)),
-                 (n, k, dY.shape[0], groups, _dtype(dY)), (_ptr(dX), lddx), workspace, stream)
+    _run_on("ozaki_grouped_gemm_dgrad", (n, k, rows, groups, _dtype(dY), W.data_ptr(), ldw, sw, dY.data_ptr(), lddy,
+                                              offsets.data_ptr(), dX.data_ptr(), lddx), workspace, stream, device)
     return dX
 
 
@@ -569,20 +597,19 @@ def ozaki_grouped_gemm_wgrad(dY, X, offsets, dW=None, workspace=None, stream=Non
     """dW[e] = sum over the rows r of group e of dY[r] X[r]^T: (groups, n, k)."""
     import torch
 
-    dY, lddy = _tokens(dY, "dY")
-    X, ldx = _tokens(X, "X")
+    lddy, ldx, device = _tokens(dY, "dY"), _tokens(X, "X"), dY.device
     if X.shape[0] != dY.shape[0]:
         raise ValueError("X and dY must have the same rows")
-    _offsets(offsets, None, dY.device)
-    groups, n, k = offsets.numel() - 1, dY.shape[1], X.shape[1]
+    _offsets(offsets, None, device)
+    groups, n, k, rows = offsets.numel() - 1, dY.shape[1], X.shape[1], X.shape[0]
     if dW is None:
-        dW = torch.empty((groups, n, k), dtype=dY.dtype, device=dY.device)
+        dW = torch.empty((groups, n, k), dtype=dY.dtype, device=device)
     _same(dY, X, dW)
-    dW, ldw, sw = _experts(dW, "dW")
+    ldw, sw = _experts(dW, "dW")
     if tuple(dW.shape) != (groups, n, k):
         raise ValueError(f"dW must have shape {(groups, n, k)}: {tuple(dW.shape)}")
-    _run_grouped("ozaki_grouped_gemm_wgrad", (_ptr(dY), lddy, _ptr(X), ldx, _ptr(offsets)),
-                 (n, k, X.shape[0], groups, _dtype(X)), (_ptr(dW), ldw, sw), workspace, stream)
+    _run_on("ozaki_grouped_gemm_wgrad", (n, k, rows, groups, _dtype(X), dY.data_ptr(), lddy, X.data_ptr(), ldx,
+                                              offsets.data_ptr(), dW.data_ptr(), ldw, sw), workspace, stream, device)
     return dW
 
 
@@ -593,25 +620,24 @@ def ozaki_grouped_gemm_wgrad_ws(dY, X, offsets, workspace, dW=None, stream=None)
 
 def ozaki_grouped_gemm_workspace_bytes(X, W) -> int:
     """Device workspace of ozaki_grouped_gemm_ws for these operands (alignment decides part of it)."""
-    X, ldx = _tokens(X, "X", W.shape[-1])
-    W, ldw, sw = _experts(W, "W")
+    ldw, sw = _experts(W, "W")
     groups, n, k = W.shape
+    ldx = _tokens(X, "X", k)
     return int(_lib.ozaki_grouped_gemm_workspace_bytes(n, k, X.shape[0], groups, _dtype(X), _ptr(W), ldw, sw, _ptr(X), ldx))
 
 
 def ozaki_grouped_gemm_dgrad_workspace_bytes(dY, W) -> int:
     """Device workspace of ozaki_grouped_gemm_dgrad_ws for these operands."""
-    W, ldw, sw = _experts(W, "W")
+    ldw, sw = _experts(W, "W")
     groups, n, k = W.shape
-    dY, lddy = _tokens(dY, "dY", n)
+    lddy = _tokens(dY, "dY", n)
     return int(_lib.ozaki_grouped_gemm_dgrad_workspace_bytes(n, k, dY.shape[0], groups, _dtype(dY), _ptr(W), ldw, sw,
                                                              _ptr(dY), lddy))
 
 
 def ozaki_grouped_gemm_wgrad_workspace_bytes(dY, X, groups: int) -> int:
     """Device workspace of ozaki_grouped_gemm_wgrad_ws for these operands."""
-    dY, lddy = _tokens(dY, "dY")
-    X, ldx = _tokens(X, "X")
+    lddy, ldx = _tokens(dY, "dY"), _tokens(X, "X")
     return int(_lib.ozaki_grouped_gemm_wgrad_workspace_bytes(dY.shape[1], X.shape[1], X.shape[0], groups, _dtype(X),
                                                              _ptr(dY), lddy, _ptr(X), ldx))
 
@@ -660,15 +686,11 @@ def ozaki_newton_schulz(G, steps: int = 5, coeffs=NEWTON_SCHULZ_COEFFS, eps: flo
         batch *= d
     if G.dim() != 3:  # leading dimensions as one (a view: they have to be contiguous)
         G, out = (G[None], out[None]) if G.dim() == 2 else (G.view(batch, m, n), out.view(batch, m, n))
-    G, ldg, sg = _experts(G, "G")
-    out, ldo, so = _experts(out, "out")
+    ldg, sg = _experts(G, "G")
+    ldo, so = _experts(out, "out")
     ns = num_slices if num_slices is not None else (1 if code == OZ_BF16 else 2)
-    args = (n, m, batch, code, _ptr(G), ldg, sg, _ptr(out), ldo, so, steps, flat.ctypes.data, float(eps), int(ns))
-    if workspace is None:
-        _check(_lib.ozaki_newton_schulz(*args, _stream(stream)), "ozaki_newton_schulz")
-    else:
-        nbytes = workspace.numel() * workspace.element_size()
-        _check(_lib.ozaki_newton_schulz_ws(*args, _ptr(workspace), nbytes, _stream(stream)), "ozaki_newton_schulz_ws")
+    args = (n, m, batch, code, G.data_ptr(), ldg, sg, out.data_ptr(), ldo, so, steps, flat.ctypes.data, float(eps), int(ns))
+    _run_on("ozaki_newton_schulz", args, workspace, stream, G.device)
     return result
 
 

@@ -30,7 +30,7 @@ template <Op OP>
 struct GroupedWalk {
   static constexpr bool kScaled = false, kReports = false;
   static constexpr int kEpiWarps = 8;
-  static constexpr size_t kTableBytes = 2 * (OZ_MAX_GROUPS + 1) * 4;  // offsets, tile prefix
+  static constexpr size_t kTableBytes = (2 * (OZ_MAX_GROUPS + 1) + 3) * 4;  // offsets, tile prefix, the split
   static constexpr bool A_MN = OP != kForward, B_MN = OP == kWgrad, RAGGED_SUM = OP == kWgrad;
   static constexpr int BOX = 32;  // ragged rows: the small box of B (the large one has HALF_N rows)
 
@@ -51,7 +51,7 @@ struct GroupedWalk {
 
   const Params& a;
   const int *off, *prefix;
-  int tiles, full, nsplit, total, idx, tiles_m, tiles_n;
+  int full, nsplit, total, idx, tiles_m, tiles_n;
 
   // Offsets are clamped to [0, rows] and to their predecessors, so that no access leaves the
   // matrices whatever they hold; offsets that needed it are reported.
@@ -97,18 +97,31 @@ struct GroupedWalk {
       sum += __shfl_sync(0xFFFFFFFFu, t, 31);
     }
     if (__any_sync(0xFFFFFFFFu, bad) && lane == 0 && blockIdx.x == 0) atomicExch(a.status, OZ_EINVAL);
+    // Parts of the last wave's tiles: a lane weighs each count, the least cost (then count) wins.
+    const int pairs = static_cast<int>(gridDim.x >> 1);
+    const int tiles = RAGGED_SUM ? a.groups * tiles_m * ceil_div(a.N, a.bn) : sum;
+    const int rest = tiles % pairs;
+    const int nkb = ceil_div(RAGGED_SUM ? before : a.K, RAGGED_SUM ? BK * a.groups : BK);
+    int cost = lane < kMaxSplit && (lane == 0 || a.max_parts)
+                   ? split_cost(rest, nkb, pairs, a.max_parts, a.part_cols, lane + 1) : 1 << 30;
+    cost = min(cost, (1 << 25)) * 32 + lane;
+    cost = __reduce_min_sync(0xFFFFFFFFu, cost);
+    if (lane == 0) {
+      int* split = prefix + OZ_MAX_GROUPS + 1;
+      split[0] = tiles;
+      split[1] = tiles - rest;
+      split[2] = (cost & 31) + 1;
+    }
   }
 
   __device__ GroupedWalk(const Params& p, const int* table) : a(p), off(table), prefix(table + OZ_MAX_GROUPS + 1) {
     const int pairs = static_cast<int>(gridDim.x >> 1);
+    const int* split = prefix + OZ_MAX_GROUPS + 1;
     tiles_m = ceil_div(a.M, BM);
     tiles_n = RAGGED_SUM ? ceil_div(a.N, a.bn) : 0;
-    tiles = RAGGED_SUM ? a.groups * tiles_m * tiles_n : prefix[a.groups];
-    const int nkb = RAGGED_SUM ? ceil_div(off[a.groups] - off[0], BK * a.groups) : ceil_div(a.K, BK);
-    const int rest = tiles % pairs;
-    full = tiles - rest;
-    nsplit = a.max_parts ? tail_split(rest, nkb, pairs, a.max_parts, a.part_cols) : 1;
-    total = full + rest * nsplit;
+    full = split[1];
+    nsplit = split[2];
+    total = full + (split[0] - full) * nsplit;
     idx = static_cast<int>(blockIdx.x >> 1) - pairs;
   }
 

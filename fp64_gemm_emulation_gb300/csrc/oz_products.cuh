@@ -53,7 +53,6 @@ constexpr uint32_t A_PLANE = HALF_M * BK * 2;  // one slice of a stage's A
 constexpr uint32_t MN_BLOCK = 64 * BK * 2;    // 64 contiguous m (or n) x 64 k
 constexpr int EPI_FIRST = 2;                  // the first epilogue warp
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t WARP_STASH = 16 * 32 * 2;  // half of a 32 x 32 block of 16 bits, per epilogue warp
 
 // The ring of stages: 64 k of A and B, both slices of them with two slices.
 template <int PLANES>
@@ -62,6 +61,9 @@ struct Ring {
   static constexpr uint32_t A_STAGE = PLANES * A_PLANE;
   static constexpr uint32_t B_STAGE = PLANES == 2 ? 2 * (BN2 / 2) * BK * 2 : HALF_N * BK * 2;
   static constexpr uint32_t BYTES = STAGES * (A_STAGE + B_STAGE);
+  // An epilogue warp's stash: a 32 x 32 block of 16 bits, or (two slices: less room) half of one.
+  static constexpr int STASH_ROWS = PLANES == 2 ? 16 : 32;
+  static constexpr uint32_t WARP_STASH = STASH_ROWS * 64;
 };
 
 constexpr long long PART_BLOCK = 32 * HALF_M;  // floats of 32 columns of one CTA's part
@@ -95,20 +97,13 @@ struct Unit {
   unsigned int* arrivals;   // [2 CTAs]
 };
 
-// Parts for the tiles of a last, partial wave: s that minimises, in k-blocks of time, the waves of
-// the parts and the joining (each CTA writes its part and the last one reads all: about 4 k-blocks
-// of time for 256 columns, and 2 for the rendezvous).  fixed: a unit's start and drain.
-__host__ __device__ inline int tail_split(int tiles, int nkb, int pairs, int max_parts, int cols) {
-  constexpr int fixed = 4;
-  int best = 1, best_cost = 1 << 30;
-  for (int s = 1; s <= 16 && s <= nkb && (s == 1 || tiles * s <= max_parts); ++s) {
-    const int cost = ceil_div(tiles * s, pairs) * (ceil_div(nkb, s) + fixed) + (s > 1 ? 2 + 4 * (1 + s) * cols / 256 : 0);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = s;
-    }
-  }
-  return best;
+// Time, in k-blocks, of a last, partial wave of `tiles` tiles cut into s parts each: the waves of the
+// parts and the joining (each CTA writes its part and the last one reads all: about 4 k-blocks
+// of time for 256 columns, and 2 for the rendezvous).  kSplitFixed: a unit's start and drain.
+constexpr int kSplitFixed = 4, kMaxSplit = 16;
+__host__ __device__ inline int split_cost(int tiles, int nkb, int pairs, int max_parts, int cols, int s) {
+  if (s > 1 && (s > nkb || tiles * s > max_parts)) return 1 << 30;
+  return ceil_div(tiles * s, pairs) * (ceil_div(nkb, s) + kSplitFixed) + (s > 1 ? 2 + 4 * (1 + s) * cols / 256 : 0);
 }
 
 // Shared-memory descriptors, low word: address / 16 and the leading byte offset.  K-major tiles:
@@ -137,14 +132,21 @@ __host__ __device__ constexpr uint32_t idesc_base(bool bf16, bool a_mn, bool b_m
          (static_cast<uint32_t>(BM >> 4) << 24);
 }
 
-// Two values as 16-bit elements, the first in the low half.
-__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool bf16) {
+// Neighbouring values as pairs of 16-bit elements, the first in the low half.
+__device__ __forceinline__ void pack_block(const float (&v)[32], uint32_t (&w)[16], bool bf16) {
   if (bf16) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&p);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const __half2 p = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
   }
-  const __half2 p = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&p);
 }
 
 __device__ __forceinline__ void stop_pair(volatile int* abort_flag, int* status) {
@@ -218,44 +220,52 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t r0, uint32_t r
 }
 
 // Writes a block of 16-bit values, w[i / 2] holding elements i and i + 1.  ROWS_N: rows of n, element
-// (m, n) at out[n * ld + m]; otherwise rows of m, at out[m * ld + n].  rows, width: how much of it exists.
-template <bool ROWS_N>
+// (m, n) at out[n * ld + m]; otherwise rows of m, at out[m * ld + n].  rows, width: how much of it
+// exists.  ROWS of the block go through the stash at a time.
+template <bool ROWS_N, int ROWS>
 __device__ __forceinline__ void store_block(const uint32_t (&w)[16], uint8_t* stash, uint16_t* out, long long ld, int rows,
                                             int width, bool vec) {
   const int lane = threadIdx.x & 31;
-  const uint32_t base = smem_u32(stash);
+  // 8 rows are 512 bytes, which leave the permutation as it is
+  const uint32_t put = smem_u32(stash) + stash_at(lane & 7, lane >> 3);
+  const uint8_t* get = stash + stash_at(lane >> 2, lane & 3);
+  const bool whole = vec && width == 32;
+  uint16_t* dst = out + (lane >> 2) * ld + (lane & 3) * 8;
+  const long long step = 8 * ld;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {  // 16 rows at a time
+  for (int r0 = 0; r0 < 32; r0 += ROWS) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = 2 * h + i;
-      const uint32_t at = base + stash_at(8 * i + (lane & 7), lane >> 3);
+    for (int i = 0; i < ROWS / 8; ++i) {
+      const int j = r0 / 8 + i;
       if (ROWS_N)  // the four 8-element groups of m, rows n = 8 j ..
-        stmatrix4<true>(at, w[2 * j], w[2 * j + 1], w[8 + 2 * j], w[9 + 2 * j]);
+        stmatrix4<true>(put + 512 * i, w[2 * j], w[2 * j + 1], w[8 + 2 * j], w[9 + 2 * j]);
       else  // the four 8-element groups of n, rows m = 8 j ..
-        stmatrix4<false>(at, w[h * 8 + i], w[h * 8 + 2 + i], w[h * 8 + 4 + i], w[h * 8 + 6 + i]);
+        stmatrix4<false>(put + 512 * i, w[(j >> 1) * 8 + (j & 1)], w[(j >> 1) * 8 + 2 + (j & 1)],
+                         w[(j >> 1) * 8 + 4 + (j & 1)], w[(j >> 1) * 8 + 6 + (j & 1)]);
     }
     __syncwarp();
-    uint16_t* half = out + 16 * h * ld;
-    if (vec && width == 32) {
-      uint4 x[2];
+    if (whole) {
+      uint4 x[ROWS / 8];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) x[i] = *reinterpret_cast<const uint4*>(stash + stash_at(8 * i + (lane >> 2), lane & 3));
+      for (int i = 0; i < ROWS / 8; ++i) x[i] = *reinterpret_cast<const uint4*>(get + 512 * i);
+      if (rows == 32) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 8 * i + (lane >> 2);
-        if (16 * h + r < rows) *reinterpret_cast<uint4*>(half + r * ld + (lane & 3) * 8) = x[i];
+        for (int i = 0; i < ROWS / 8; ++i, dst += step) *reinterpret_cast<uint4*>(dst) = x[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < ROWS / 8; ++i, dst += step)
+          if (r0 + 8 * i + (lane >> 2) < rows) *reinterpret_cast<uint4*>(dst) = x[i];
       }
     } else if (lane < width) {
-      for (int r = 0; r < 16 && 16 * h + r < rows; ++r)
-        half[r * ld + lane] = *reinterpret_cast<const uint16_t*>(stash + stash_at(r, lane >> 3) + (lane & 7) * 2);
+      for (int r = 0; r < ROWS && r0 + r < rows; ++r)
+        out[(r0 + r) * ld + lane] = *reinterpret_cast<const uint16_t*>(stash + stash_at(r, lane >> 3) + (lane & 7) * 2);
     }
     __syncwarp();
   }
 }
 
 // The finished sums of one block, whose first m is mrow within the tile and first n is c0.
-template <bool SCALED>
+template <bool SCALED, int ROWS>
 __device__ __forceinline__ void emit(const Unit& u, float (&v)[32], int mrow, int c0, uint8_t* stash) {
   const int lane = threadIdx.x & 31;
   const int m = u.m0 + mrow;
@@ -266,9 +276,8 @@ __device__ __forceinline__ void emit(const Unit& u, float (&v)[32], int mrow, in
   const int n = u.orow + c0;
   uint32_t w[16];
   if (!SCALED) {
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) w[i >> 1] = pack16(v[i], v[i + 1], bf16);
-    store_block<true>(w, stash, static_cast<uint16_t*>(u.out) + n * u.ld + m, u.ld, ncount, mcount, u.vec);
+    pack_block(v, w, bf16);
+    store_block<true, ROWS>(w, stash, static_cast<uint16_t*>(u.out) + n * u.ld + m, u.ld, ncount, mcount, u.vec);
   } else {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= u.f;
@@ -289,16 +298,18 @@ __device__ __forceinline__ void emit(const Unit& u, float (&v)[32], int mrow, in
     uint16_t* out = static_cast<uint16_t*>(u.out);
 #pragma unroll 1
     for (int p = 0; p < u.planes_out; ++p, out += u.plane) {
+      pack_block(v, w, bf16);
+      if (p + 1 < u.planes_out) {  // FP16 slices: what this one leaves
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        w[i >> 1] = pack16(v[i], v[i + 1], bf16);
-        const __half2 h = *reinterpret_cast<const __half2*>(&w[i >> 1]);  // FP16 slices: what this one leaves
-        v[i] -= __low2float(h);
-        v[i + 1] -= __high2float(h);
+        for (int i = 0; i < 32; i += 2) {
+          const __half2 h = *reinterpret_cast<const __half2*>(&w[i >> 1]);
+          v[i] -= __low2float(h);
+          v[i + 1] -= __high2float(h);
+        }
       }
       // Symmetric: a block on the diagonal is its own mirror, those above it are some block's below.
-      if (!u.sym || n <= m) store_block<true>(w, stash, out + n * u.ld + m, u.ld, ncount, mcount, u.vec);
-      if (u.sym && n < m) store_block<false>(w, stash, out + m * u.ld + n, u.ld, mcount, ncount, u.vec);
+      if (!u.sym || n <= m) store_block<true, ROWS>(w, stash, out + n * u.ld + m, u.ld, ncount, mcount, u.vec);
+      if (u.sym && n < m) store_block<false, ROWS>(w, stash, out + m * u.ld + n, u.ld, mcount, ncount, u.vec);
     }
   }
 }
@@ -393,7 +404,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
   constexpr int EPI_WARPS = Walk::kEpiWarps;
   constexpr int COLS = EPI_WARPS / 4;                 // warps that share the blocks of 32 columns of a quadrant
   constexpr int RUNS = PLANES == 2 ? (BN2 / 32 + COLS - 1) / COLS : 1;  // two slices: blocks whose sums a warp holds
-  constexpr uint32_t STASH = EPI_WARPS * WARP_STASH;
+  constexpr uint32_t STASH = EPI_WARPS * R::WARP_STASH;
   constexpr uint32_t NACC = PLANES == 2 ? 3 : 2, ACC_COLS = PLANES == 2 ? BN2 : BN;  // accumulators, their columns
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -413,7 +424,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile uint32_t* issued_by = reinterpret_cast<volatile uint32_t*>(abort_flag + 1);  // [2] (leader)
   volatile uint32_t* arrived = issued_by + 2;
-  uint32_t* warps_done = const_cast<uint32_t*>(issued_by + 3);
+  uint32_t* warps_done = const_cast<uint32_t*>(issued_by + 3);  // [4]
   int* table = reinterpret_cast<int*>(stash + STASH + 256);  // the walker's
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -433,7 +444,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
     mbar_init(exitbar, 1);
     mbar_init(proddone, 2);
     *abort_flag = 0;
-    *warps_done = 0;
+    for (int i = 0; i < 4; ++i) warps_done[i] = 0;
     mbar_fence_init();
   }
   if (warp == 1) {
@@ -612,13 +623,13 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
     const int quad = warp & 3;
     const int first = (warp - EPI_FIRST) >> 2;
     const int mrow = static_cast<int>(rank) * HALF_M + quad * 32;
-    uint8_t* my_stash = stash + (warp - EPI_FIRST) * WARP_STASH;
-    uint32_t acc = 0, acc_phase = 0, eph = 0;
+    uint8_t* my_stash = stash + (warp - EPI_FIRST) * R::WARP_STASH;
+    uint32_t acc = 0, acc_phase = 0, eph = 0, seq = 0;
     bool ok = true;
     Walk walk(a, table);
     walk.outside(warp - EPI_FIRST);
     Unit u;
-    while (ok && walk.next(u)) {
+    for (; ok && walk.next(u); ++seq) {
       const int nblocks = ceil_div(u.nn, 32);  // this warp: blocks first, first + COLS, ...
       const bool split = u.nsplit > 1;
       const long long part_unit = 2ll * u.part_cols * HALF_M;
@@ -664,7 +675,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
             if (split)
               put_part(mine + cb * PART_BLOCK, v);
             else
-              emit<Walk::kScaled>(u, v, mrow, cb * 32, my_stash);
+              emit<Walk::kScaled, R::STASH_ROWS>(u, v, mrow, cb * 32, my_stash);
           }
         }
         if (PLANES == 2 || first >= nblocks) {
@@ -686,7 +697,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
             if (split)
               put_part(mine + cb * PART_BLOCK, run[j]);
             else
-              emit<Walk::kScaled>(u, run[j], mrow, cb * 32, my_stash);
+              emit<Walk::kScaled, R::STASH_ROWS>(u, run[j], mrow, cb * 32, my_stash);
           }
         }
       } else if (nchunks == 0) {  // an empty sum (a group without rows, or with few for this many parts)
@@ -698,7 +709,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
           if (split)
             put_part(mine + cb * PART_BLOCK, v);
           else
-            emit<Walk::kScaled>(u, v, mrow, cb * 32, my_stash);
+            emit<Walk::kScaled, R::STASH_ROWS>(u, v, mrow, cb * 32, my_stash);
         }
       }
       bool finished = true;
@@ -724,7 +735,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.0f;
             for (int q = 0; q < u.nsplit; ++q) add_part(parts + q * part_unit + cb * PART_BLOCK, v);
-            emit<Walk::kScaled>(u, v, mrow, cb * 32, my_stash);
+            emit<Walk::kScaled, R::STASH_ROWS>(u, v, mrow, cb * 32, my_stash);
           }
         }
       }
@@ -735,7 +746,11 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
         __syncwarp();
         if (lane == 0) {
           __threadfence();
-          if (atomicAdd(warps_done, 1u) % EPI_WARPS == EPI_WARPS - 1) {
+          // A warp can be NACC units ahead of another (the next one needs an accumulator that the other
+          // has yet to hand back), so units in a row count apart.
+          static_assert(NACC + 1 <= 4, "counters of warps_done");
+          if (atomicAdd(&warps_done[seq & 3], 1u) == EPI_WARPS - 1) {
+            warps_done[seq & 3] = 0;
             __threadfence();
             walk.done();
           }
@@ -823,7 +838,7 @@ enum Start { kAfter, kCooperative, kOverlap };
 template <class Walk, int PLANES>
 int launch(typename Walk::Params a, const Device& d, int pairs, Start start, cudaStream_t stream) {  // on `pairs` CTA pairs
   auto kernel = product_kernel<Walk, PLANES>;
-  constexpr size_t smem = 1024 /*alignment*/ + Ring<PLANES>::BYTES + Walk::kEpiWarps * WARP_STASH + 256 /*barriers*/ + Walk::kTableBytes;
+  constexpr size_t smem = 1024 /*alignment*/ + Ring<PLANES>::BYTES + Walk::kEpiWarps * Ring<PLANES>::WARP_STASH + 256 /*barriers*/ + Walk::kTableBytes;
   static_assert(smem <= 232448, "shared memory budget");
   a.status = d.status;
   a.epi_wait_ns = epilogue_wait_ns();

@@ -219,44 +219,77 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t r0, uint32_t r
                  : "memory");
 }
 
-// Writes a block of 16-bit values, w[i / 2] holding elements i and i + 1.  ROWS_N: rows of n, element
-// (m, n) at out[n * ld + m]; otherwise rows of m, at out[m * ld + n].  rows, width: how much of it
-// exists.  ROWS of the block go through the stash at a time.
-template <bool ROWS_N, int ROWS>
-__device__ __forceinline__ void store_block(const uint32_t (&w)[16], uint8_t* stash, uint16_t* out, long long ld, int rows,
-                                            int width, bool vec) {
+// Where a thread's stores of a tile go, set up once for a unit: a block is then little more than its
+// conversions and its 12 shared and global accesses.  (With the addresses and the cases of each
+// block worked out in place it was 130 instructions at 8 cycles each, and two warps to a
+// scheduler cannot hide that: 4260 cycles a tile in the weight gradient.)
+struct Target {
+  uint32_t put;         // stmatrix's row, and the 16 bytes read back, in the warp's stash
+  const uint8_t* get;
+  uint16_t* by_n;       // this lane's 16 bytes of row n = lane / 4 of the tile's first block
+  long long step;       // 8 rows
+  int m, mcount;        // first m of the warp's lanes, how many exist
+  bool fast;            // 16-bit output, whole lanes, 16-byte stores
+};
+
+__device__ __forceinline__ Target target_of(const Unit& u, int mrow, uint8_t* stash) {
   const int lane = threadIdx.x & 31;
-  // 8 rows are 512 bytes, which leave the permutation as it is
-  const uint32_t put = smem_u32(stash) + stash_at(lane & 7, lane >> 3);
-  const uint8_t* get = stash + stash_at(lane >> 2, lane & 3);
-  const bool whole = vec && width == 32;
-  uint16_t* dst = out + (lane >> 2) * ld + (lane & 3) * 8;
-  const long long step = 8 * ld;
+  Target t;
+  t.put = smem_u32(stash) + stash_at(lane & 7, lane >> 3);
+  t.get = stash + stash_at(lane >> 2, lane & 3);
+  t.m = u.m0 + mrow;
+  t.mcount = min(32, u.m_extent - t.m);
+  t.step = 8 * u.ld;
+  t.by_n = static_cast<uint16_t*>(u.out) + (u.orow + (lane >> 2)) * u.ld + t.m + (lane & 3) * 8;
+  t.fast = u.vec && t.mcount == 32 && u.out_type != kOutF32;
+  return t;
+}
+
+// A whole block of 16-bit values, w[i / 2] holding elements i and i + 1, through the warp's stash
+// (ROWS of it at a time; 8 rows are 512 bytes, which leave the permutation as it is).  ROWS_N: rows of
+// n, otherwise rows of m; dst: this lane's 16 bytes of row lane / 4.
+template <bool ROWS_N, int ROWS>
+__device__ __forceinline__ void store_whole(const uint32_t (&w)[16], const Target& t, uint16_t* dst) {
 #pragma unroll
   for (int r0 = 0; r0 < 32; r0 += ROWS) {
 #pragma unroll
     for (int i = 0; i < ROWS / 8; ++i) {
       const int j = r0 / 8 + i;
       if (ROWS_N)  // the four 8-element groups of m, rows n = 8 j ..
-        stmatrix4<true>(put + 512 * i, w[2 * j], w[2 * j + 1], w[8 + 2 * j], w[9 + 2 * j]);
+        stmatrix4<true>(t.put + 512 * i, w[2 * j], w[2 * j + 1], w[8 + 2 * j], w[9 + 2 * j]);
       else  // the four 8-element groups of n, rows m = 8 j ..
-        stmatrix4<false>(put + 512 * i, w[(j >> 1) * 8 + (j & 1)], w[(j >> 1) * 8 + 2 + (j & 1)],
+        stmatrix4<false>(t.put + 512 * i, w[(j >> 1) * 8 + (j & 1)], w[(j >> 1) * 8 + 2 + (j & 1)],
                          w[(j >> 1) * 8 + 4 + (j & 1)], w[(j >> 1) * 8 + 6 + (j & 1)]);
     }
     __syncwarp();
-    if (whole) {
-      uint4 x[ROWS / 8];
+    uint4 x[ROWS / 8];
 #pragma unroll
-      for (int i = 0; i < ROWS / 8; ++i) x[i] = *reinterpret_cast<const uint4*>(get + 512 * i);
-      if (rows == 32) {
+    for (int i = 0; i < ROWS / 8; ++i) x[i] = *reinterpret_cast<const uint4*>(t.get + 512 * i);
 #pragma unroll
-        for (int i = 0; i < ROWS / 8; ++i, dst += step) *reinterpret_cast<uint4*>(dst) = x[i];
-      } else {
+    for (int i = 0; i < ROWS / 8; ++i, dst += t.step) *reinterpret_cast<uint4*>(dst) = x[i];
+    __syncwarp();
+  }
+}
+
+// A block of which only `rows` rows of `width` elements exist, or whose stores cannot be wide: a row at a
+// time, one element a lane.  out: the block's first element.
+template <bool ROWS_N, int ROWS>
+__device__ __forceinline__ void store_part(const uint32_t (&w)[16], const Target& t, uint8_t* stash, uint16_t* out,
+                                           long long ld, int rows, int width) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int i = 0; i < ROWS / 8; ++i, dst += step)
-          if (r0 + 8 * i + (lane >> 2) < rows) *reinterpret_cast<uint4*>(dst) = x[i];
-      }
-    } else if (lane < width) {
+  for (int r0 = 0; r0 < 32; r0 += ROWS) {
+#pragma unroll
+    for (int i = 0; i < ROWS / 8; ++i) {
+      const int j = r0 / 8 + i;
+      if (ROWS_N)
+        stmatrix4<true>(t.put + 512 * i, w[2 * j], w[2 * j + 1], w[8 + 2 * j], w[9 + 2 * j]);
+      else
+        stmatrix4<false>(t.put + 512 * i, w[(j >> 1) * 8 + (j & 1)], w[(j >> 1) * 8 + 2 + (j & 1)],
+                         w[(j >> 1) * 8 + 4 + (j & 1)], w[(j >> 1) * 8 + 6 + (j & 1)]);
+    }
+    __syncwarp();
+    if (lane < width) {
       for (int r = 0; r < ROWS && r0 + r < rows; ++r)
         out[(r0 + r) * ld + lane] = *reinterpret_cast<const uint16_t*>(stash + stash_at(r, lane >> 3) + (lane & 7) * 2);
     }
@@ -264,41 +297,44 @@ __device__ __forceinline__ void store_block(const uint32_t (&w)[16], uint8_t* st
   }
 }
 
-// The finished sums of one block, whose first m is mrow within the tile and first n is c0.
+// The finished sums of block cb (32 columns) of a tile.
 template <bool SCALED, int ROWS>
-__device__ __forceinline__ void emit(const Unit& u, float (&v)[32], int mrow, int c0, uint8_t* stash) {
+__device__ __forceinline__ void emit(const Unit& u, const Target& t, float (&v)[32], int cb, uint8_t* stash) {
   const int lane = threadIdx.x & 31;
-  const int m = u.m0 + mrow;
-  const int ncount = min(32, u.nn - c0);
-  const int mcount = min(32, u.m_extent - m);
-  if (ncount <= 0 || mcount <= 0) return;
-  const bool bf16 = u.out_type == kOutBf16;
-  const int n = u.orow + c0;
+  const int ncount = min(32, u.nn - 32 * cb);
   uint32_t w[16];
   if (!SCALED) {
-    pack_block(v, w, bf16);
-    store_block<true, ROWS>(w, stash, static_cast<uint16_t*>(u.out) + n * u.ld + m, u.ld, ncount, mcount, u.vec);
+    pack_block(v, w, u.out_type == kOutBf16);
+    if (t.fast && ncount == 32)
+      store_whole<true, ROWS>(w, t, t.by_n + 4 * cb * t.step);
+    else if (t.mcount > 0)
+      store_part<true, ROWS>(w, t, stash, static_cast<uint16_t*>(u.out) + (u.orow + 32 * cb) * u.ld + t.m, u.ld, ncount,
+                             t.mcount);
   } else {
+    const int n = u.orow + 32 * cb;
+    if (t.mcount <= 0 || (u.sym && n > t.m)) return;  // above the diagonal: some block's mirror
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= u.f;
-    if (u.sym && m == n) {  // blocks and tiles start at multiples of 32
+    if (u.sym && t.m == n) {  // blocks and tiles start at multiples of 32
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         if (frag_m(i, lane) == frag_n(i, lane)) v[i] += u.diag;
     }
     if (u.out_type == kOutF32) {
-      float* out = static_cast<float*>(u.out) + n * u.ld + m;
+      float* out = static_cast<float*>(u.out) + n * u.ld + t.m;
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         const int mi = frag_m(i, lane), ni = frag_n(i, lane);
-        if (mi < mcount && ni < ncount) out[ni * u.ld + mi] = v[i];
+        if (mi < t.mcount && ni < ncount) out[ni * u.ld + mi] = v[i];
       }
       return;
     }
-    uint16_t* out = static_cast<uint16_t*>(u.out);
+    const bool whole = t.fast && ncount == 32;
+    const bool mirror = u.sym && n < t.m;  // a block on the diagonal is its own mirror
+    long long plane = 0;
 #pragma unroll 1
-    for (int p = 0; p < u.planes_out; ++p, out += u.plane) {
-      pack_block(v, w, bf16);
+    for (int p = 0; p < u.planes_out; ++p, plane += u.plane) {
+      pack_block(v, w, u.out_type == kOutBf16);
       if (p + 1 < u.planes_out) {  // FP16 slices: what this one leaves
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
@@ -307,9 +343,14 @@ __device__ __forceinline__ void emit(const Unit& u, float (&v)[32], int mrow, in
           v[i + 1] -= __high2float(h);
         }
       }
-      // Symmetric: a block on the diagonal is its own mirror, those above it are some block's below.
-      if (!u.sym || n <= m) store_block<true, ROWS>(w, stash, out + n * u.ld + m, u.ld, ncount, mcount, u.vec);
-      if (u.sym && n < m) store_block<false, ROWS>(w, stash, out + m * u.ld + n, u.ld, mcount, ncount, u.vec);
+      uint16_t* out = static_cast<uint16_t*>(u.out) + plane;
+      if (whole) {
+        store_whole<true, ROWS>(w, t, t.by_n + plane + 4 * cb * t.step);
+        if (mirror) store_whole<false, ROWS>(w, t, out + (t.m + (lane >> 2)) * u.ld + n + (lane & 3) * 8);
+      } else {
+        store_part<true, ROWS>(w, t, stash, out + n * u.ld + t.m, u.ld, ncount, t.mcount);
+        if (mirror) store_part<false, ROWS>(w, t, stash, out + t.m * u.ld + n, u.ld, t.mcount, ncount);
+      }
     }
   }
 }
@@ -631,6 +672,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
     Unit u;
     for (; ok && walk.next(u); ++seq) {
       const int nblocks = ceil_div(u.nn, 32);  // this warp: blocks first, first + COLS, ...
+      const Target target = target_of(u, mrow, my_stash);
       const bool split = u.nsplit > 1;
       const long long part_unit = 2ll * u.part_cols * HALF_M;
       float* const parts = u.part + static_cast<long long>(rank) * u.part_cols * HALF_M + quad * 1024 + lane * 4;
@@ -675,7 +717,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
             if (split)
               put_part(mine + cb * PART_BLOCK, v);
             else
-              emit<Walk::kScaled, R::STASH_ROWS>(u, v, mrow, cb * 32, my_stash);
+              emit<Walk::kScaled, R::STASH_ROWS>(u, target, v, cb, my_stash);
           }
         }
         if (PLANES == 2 || first >= nblocks) {
@@ -697,7 +739,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
             if (split)
               put_part(mine + cb * PART_BLOCK, run[j]);
             else
-              emit<Walk::kScaled, R::STASH_ROWS>(u, run[j], mrow, cb * 32, my_stash);
+              emit<Walk::kScaled, R::STASH_ROWS>(u, target, run[j], cb, my_stash);
           }
         }
       } else if (nchunks == 0) {  // an empty sum (a group without rows, or with few for this many parts)
@@ -709,7 +751,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
           if (split)
             put_part(mine + cb * PART_BLOCK, v);
           else
-            emit<Walk::kScaled, R::STASH_ROWS>(u, v, mrow, cb * 32, my_stash);
+            emit<Walk::kScaled, R::STASH_ROWS>(u, target, v, cb, my_stash);
         }
       }
       bool finished = true;
@@ -735,7 +777,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.0f;
             for (int q = 0; q < u.nsplit; ++q) add_part(parts + q * part_unit + cb * PART_BLOCK, v);
-            emit<Walk::kScaled, R::STASH_ROWS>(u, v, mrow, cb * 32, my_stash);
+            emit<Walk::kScaled, R::STASH_ROWS>(u, target, v, cb, my_stash);
           }
         }
       }

@@ -193,9 +193,15 @@ struct GroupedWalk {
     u.ld = a.ld;
     u.out_type = a.out_type;
     u.vec = a.vec;
+    u.sym = false;
+    u.planes_out = 1;
+    u.plane = 0;
+    u.f = 1.0f;
+    u.diag = 0.0f;
     return true;
   }
 
+  __device__ void again(Unit&) const {}
   __device__ bool ready(const volatile int*) const { return true; }
   __device__ void stored() const {}
   __device__ void done() const {}

@@ -113,6 +113,17 @@ struct ChainWalk {
         ++kind;
       }
     }
+    describe(u);
+    return true;
+  }
+
+  // The same unit again, worked out anew, so that nothing of it has to be kept meanwhile.
+  __device__ void again(Unit& u) {
+    asm volatile("" : "+r"(idx));
+    describe(u);
+  }
+
+  __device__ void describe(Unit& u) {
     const Product& p = a.prod[kind];
     int tile = idx - base;
     u.split = 0;
@@ -192,7 +203,6 @@ struct ChainWalk {
       u.ld = a.lds;
       u.plane = a.splane;
     }
-    return true;
   }
 
   // Waits until the products before the unit's are finished for its matrix.  They were dealt out

@@ -61,8 +61,8 @@ struct Ring {
   static constexpr uint32_t A_STAGE = PLANES * A_PLANE;
   static constexpr uint32_t B_STAGE = PLANES == 2 ? 2 * (BN2 / 2) * BK * 2 : HALF_N * BK * 2;
   static constexpr uint32_t BYTES = STAGES * (A_STAGE + B_STAGE);
-  // An epilogue warp's stash: a 32 x 32 block of 16 bits, or (two slices: less room) half of one.
-  static constexpr int STASH_ROWS = PLANES == 2 ? 16 : 32;
+  // An epilogue warp's stash: a 32 x 32 block of 16 bits (two slices: no room, store_regs).
+  static constexpr int STASH_ROWS = PLANES == 2 ? 0 : 32;
   static constexpr uint32_t WARP_STASH = STASH_ROWS * 64;
 };
 
@@ -251,7 +251,7 @@ __device__ __forceinline__ Target target_of(const Unit& u, int mrow, uint8_t* st
 template <bool ROWS_N, int ROWS>
 __device__ __forceinline__ void store_whole(const uint32_t (&w)[16], const Target& t, uint16_t* dst) {
 #pragma unroll
-  for (int r0 = 0; r0 < 32; r0 += ROWS) {
+  for (int r0 = 0; r0 < 32; r0 += ROWS ? ROWS : 32) {
 #pragma unroll
     for (int i = 0; i < ROWS / 8; ++i) {
       const int j = r0 / 8 + i;
@@ -262,12 +262,56 @@ __device__ __forceinline__ void store_whole(const uint32_t (&w)[16], const Targe
                          w[(j >> 1) * 8 + 4 + (j & 1)], w[(j >> 1) * 8 + 6 + (j & 1)]);
     }
     __syncwarp();
-    uint4 x[ROWS / 8];
+    uint4 x[ROWS ? ROWS / 8 : 1];
 #pragma unroll
     for (int i = 0; i < ROWS / 8; ++i) x[i] = *reinterpret_cast<const uint4*>(t.get + 512 * i);
 #pragma unroll
     for (int i = 0; i < ROWS / 8; ++i, dst += t.step) *reinterpret_cast<uint4*>(dst) = x[i];
     __syncwarp();
+  }
+}
+
+// The 4 x 4 words of four neighbouring lanes, transposed: lane q gets word q of each.
+__device__ __forceinline__ void transpose4(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+  uint32_t x = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1), y = __shfl_xor_sync(0xFFFFFFFFu, odd ? c : d, 1);
+  if (odd) a = x, c = y; else b = x, d = y;
+  x = __shfl_xor_sync(0xFFFFFFFFu, high ? a : c, 2);
+  y = __shfl_xor_sync(0xFFFFFFFFu, high ? b : d, 2);
+  if (high) a = x, b = y; else c = x, d = y;
+}
+
+// A block without a stash (two slices have no shared memory left): each 8 x 8 of the fragments
+// transposed in registers where rows of n are wanted, and 16 bytes gathered in each lane.
+// out: the block's first element; rows of `width` elements.  w is used up.
+template <bool ROWS_N>
+__device__ __forceinline__ void store_regs(uint32_t (&w)[16], uint16_t* out, long long ld, int rows, int width, bool vec) {
+  const int lane = threadIdx.x & 31, q = 8 * (lane & 3);
+  uint16_t* dst = out + (lane >> 2) * ld + q;
+#pragma unroll
+  for (int j = 0; j < 4; ++j, dst += 8 * ld) {  // rows 8 j + lane / 4
+    uint32_t a, b, c, d;
+    if (ROWS_N) {
+      const uint32_t f[4] = {w[2 * j], w[2 * j + 1], w[8 + 2 * j], w[9 + 2 * j]};  // the groups of 8 m
+      uint32_t g[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(g[i]) : "r"(f[i]));
+      a = g[0], b = g[1], c = g[2], d = g[3];
+    } else {  // the groups of 8 n
+      a = w[(j >> 1) * 8 + (j & 1)], b = w[(j >> 1) * 8 + 2 + (j & 1)];
+      c = w[(j >> 1) * 8 + 4 + (j & 1)], d = w[(j >> 1) * 8 + 6 + (j & 1)];
+    }
+    transpose4(a, b, c, d);
+    if (8 * j + (lane >> 2) < rows) {
+      if (vec && q + 8 <= width) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(a, b, c, d);
+      } else {
+        const uint32_t x[4] = {a, b, c, d};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (q + e < width) dst[e] = static_cast<uint16_t>(x[e >> 1] >> (16 * (e & 1)));
+      }
+    }
   }
 }
 
@@ -278,7 +322,7 @@ __device__ __forceinline__ void store_part(const uint32_t (&w)[16], const Target
                                            long long ld, int rows, int width) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int r0 = 0; r0 < 32; r0 += ROWS) {
+  for (int r0 = 0; r0 < 32; r0 += ROWS ? ROWS : 32) {
 #pragma unroll
     for (int i = 0; i < ROWS / 8; ++i) {
       const int j = r0 / 8 + i;
@@ -331,26 +375,38 @@ __device__ __forceinline__ void emit(const Unit& u, const Target& t, float (&v)[
     }
     const bool whole = t.fast && ncount == 32;
     const bool mirror = u.sym && n < t.m;  // a block on the diagonal is its own mirror
-    long long plane = 0;
-#pragma unroll 1
-    for (int p = 0; p < u.planes_out; ++p, plane += u.plane) {
-      pack_block(v, w, u.out_type == kOutBf16);
-      if (p + 1 < u.planes_out) {  // FP16 slices: what this one leaves
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const __half2 h = *reinterpret_cast<const __half2*>(&w[i >> 1]);
-          v[i] -= __low2float(h);
-          v[i + 1] -= __high2float(h);
-        }
-      }
+    auto store = [&](uint32_t (&x)[16], long long plane) {
       uint16_t* out = static_cast<uint16_t*>(u.out) + plane;
-      if (whole) {
-        store_whole<true, ROWS>(w, t, t.by_n + plane + 4 * cb * t.step);
-        if (mirror) store_whole<false, ROWS>(w, t, out + (t.m + (lane >> 2)) * u.ld + n + (lane & 3) * 8);
+      if (ROWS == 0) {
+        if (mirror) {
+          uint32_t y[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] = x[i];
+          store_regs<false>(y, out + t.m * u.ld + n, u.ld, t.mcount, ncount, u.vec);
+        }
+        store_regs<true>(x, out + n * u.ld + t.m, u.ld, ncount, t.mcount, u.vec);
+      } else if (whole) {
+        store_whole<true, ROWS>(x, t, t.by_n + plane + 4 * cb * t.step);
+        if (mirror) store_whole<false, ROWS>(x, t, out + (t.m + (lane >> 2)) * u.ld + n + (lane & 3) * 8);
       } else {
-        store_part<true, ROWS>(w, t, stash, out + n * u.ld + t.m, u.ld, ncount, t.mcount);
-        if (mirror) store_part<false, ROWS>(w, t, stash, out + t.m * u.ld + n, u.ld, t.mcount, ncount);
+        store_part<true, ROWS>(x, t, stash, out + n * u.ld + t.m, u.ld, ncount, t.mcount);
+        if (mirror) store_part<false, ROWS>(x, t, stash, out + t.m * u.ld + n, u.ld, t.mcount, ncount);
       }
+    };
+    if (ROWS == 0 && u.planes_out == 2) {  // FP16 slices: the second is what the first leaves; both take the sums' registers
+      uint32_t l[16];
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const __half2 h = __floats2half2_rn(v[i], v[i + 1]);
+        const __half2 r = __floats2half2_rn(v[i] - __low2float(h), v[i + 1] - __high2float(h));
+        w[i >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+        l[i >> 1] = *reinterpret_cast<const uint32_t*>(&r);
+      }
+      store(w, 0);
+      store(l, u.plane);
+    } else {
+      pack_block(v, w, u.out_type == kOutBf16);
+      store(w, 0);
     }
   }
 }
@@ -433,7 +489,8 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The kernel.  Walk deals out the units: Walk::Params are the launch's, setup() runs once for the
-// whole CTA, a Walk of its own in every role gives the pair's units in order (next), and
+// whole CTA, a Walk of its own in every role gives the pair's units in order (next; again() works
+// the present one out anew), and
 // ready() and, if kReports, stored() / done() are its dependences between units (the producer before a
 // unit's first load, each epilogue thread after its last store, one thread of each CTA when all
 // have stored); gave_up() tells the other pairs that they wait in vain.
@@ -507,7 +564,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
       uint32_t issued = 0;
       const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
       Walk walk(a, table);
-      Unit u;
+      Unit u{};
       while (!*abort_flag && walk.next(u)) {
         if (!walk.ready(abort_flag)) {
           if (!*abort_flag) stop_pair(abort_flag, a.status);
@@ -560,7 +617,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
         }
       };
       Walk walk(a, table);
-      Unit u;
+      Unit u{};
       while (ok && !*abort_flag && walk.next(u)) {
         // Low words of stage 0's descriptors; a stage or a k step only adds to the address field.
         const uint32_t a_desc = desc_low(smem_u32(sA), u.a_mn), b_desc = desc_low(smem_u32(sB), u.b_mn);
@@ -669,14 +726,20 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
     bool ok = true;
     Walk walk(a, table);
     walk.outside(warp - EPI_FIRST);
-    Unit u;
+    Unit u{};
     for (; ok && walk.next(u); ++seq) {
       const int nblocks = ceil_div(u.nn, 32);  // this warp: blocks first, first + COLS, ...
-      const Target target = target_of(u, mrow, my_stash);
-      const bool split = u.nsplit > 1;
-      const long long part_unit = 2ll * u.part_cols * HALF_M;
-      float* const parts = u.part + static_cast<long long>(rank) * u.part_cols * HALF_M + quad * 1024 + lane * 4;
-      float* const mine = parts + u.split * part_unit;
+      Target target;
+      bool split;
+      auto place = [&]() {  // where the tile's blocks go
+        if (PLANES == 2) walk.again(u);
+        target = target_of(u, mrow, my_stash);
+        split = u.nsplit > 1;
+      };
+      auto parts = [&](int q) {  // this thread's values of part q of a split tile
+        return u.part + (2ll * q + rank) * u.part_cols * HALF_M + quad * 1024 + lane * 4;
+      };
+      if (PLANES == 1) place();  // two slices: after the sums, whose registers it would take
       float run[RUNS][32];  // two slices: the sums of this warp's blocks
       if (PLANES == 2) {
 #pragma unroll
@@ -715,7 +778,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
               if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&accempty[acc]), 0));
             }
             if (split)
-              put_part(mine + cb * PART_BLOCK, v);
+              put_part(parts(u.split) + cb * PART_BLOCK, v);
             else
               emit<Walk::kScaled, R::STASH_ROWS>(u, target, v, cb, my_stash);
           }
@@ -732,12 +795,13 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
       }
       if (!ok) break;
       if (PLANES == 2) {
+        place();
 #pragma unroll
         for (int j = 0; j < RUNS; ++j) {
           const int cb = COLS * j + first;
           if (cb < nblocks) {
             if (split)
-              put_part(mine + cb * PART_BLOCK, run[j]);
+              put_part(parts(u.split) + cb * PART_BLOCK, run[j]);
             else
               emit<Walk::kScaled, R::STASH_ROWS>(u, target, run[j], cb, my_stash);
           }
@@ -749,7 +813,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0.0f;
           if (split)
-            put_part(mine + cb * PART_BLOCK, v);
+            put_part(parts(u.split) + cb * PART_BLOCK, v);
           else
             emit<Walk::kScaled, R::STASH_ROWS>(u, target, v, cb, my_stash);
         }
@@ -776,7 +840,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
             float v[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-            for (int q = 0; q < u.nsplit; ++q) add_part(parts + q * part_unit + cb * PART_BLOCK, v);
+            for (int q = 0; q < u.nsplit; ++q) add_part(parts(q) + cb * PART_BLOCK, v);
             emit<Walk::kScaled, R::STASH_ROWS>(u, target, v, cb, my_stash);
           }
         }

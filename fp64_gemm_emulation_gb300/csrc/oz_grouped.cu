@@ -293,6 +293,9 @@ struct Problem {
     if (!may_split()) return 0;
     return align256(sizeof(unsigned) * 2 * kMaxParts) + align256(sizeof(float) * 2 * HALF_M * part_cols() * kMaxParts);
   }
+  int sum() const { return op == kForward ? k : op == kDgrad ? n : rows; }
+  bool empty() const { return m_out() == 0 || (op == kWgrad ? n : rows) == 0; }
+  bool has_operands() const { return out && offsets && (sum() == 0 || (w.p && t.p)); }
   size_t workspace() const { return split_bytes() + w.repack_bytes() + t.repack_bytes(); }
 };
 
@@ -353,11 +356,9 @@ int launch_op(const Problem& p, float* part, unsigned* arrivals, const Device& d
 }
 
 int run(Problem p, void* workspace, size_t ws_bytes, cudaStream_t stream) {
-  const int sum = p.op == kForward ? p.k : p.op == kDgrad ? p.n : p.rows;
-  if (p.m_out() == 0 || (p.op == kWgrad ? p.n : p.rows) == 0) return OZ_OK;
-  if (!p.out || !p.offsets) return OZ_EINVAL;
-  if (sum == 0) return zero_output(p, stream);
-  if (!p.w.p || !p.t.p) return OZ_EINVAL;
+  if (p.empty()) return OZ_OK;
+  if (!p.has_operands()) return OZ_EINVAL;
+  if (p.sum() == 0) return zero_output(p, stream);
   const size_t need = p.workspace();
   if (need && (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255))) return OZ_ENOMEM;
   Device dev;
@@ -385,7 +386,8 @@ int run(Problem p, void* workspace, size_t ws_bytes, cudaStream_t stream) {
 }
 
 int run_allocating(const Problem& p, cudaStream_t stream) {
-  const size_t bytes = p.workspace();
+  const bool none = p.empty() || !p.has_operands() || p.sum() == 0;  // argument errors before any allocation
+  const size_t bytes = none ? 0 : p.workspace();
   void* ws = nullptr;
   if (bytes) {
     keep_default_pool_cached();

@@ -22,6 +22,7 @@
 // are FP32; the norm's partial sums are joined in FP64.
 #include <cmath>
 
+#include "oz_newton.h"
 #include "oz_products.cuh"
 
 namespace oz {
@@ -243,42 +244,21 @@ struct ChainWalk {
   __device__ static void gave_up(const Params& a) { atomicExch(a.stopped, 1u); }
 };
 
-// What the small kernels need of the plan.
-struct StepScales {
-  int steps;
-  int sx;                           // |X_i| 2^sx fits FP16
-  int drop;                         // 2^drop >= max |p|: bits a tiny X may gain in a step
-  float gram[OZ_MAX_NS_STEPS];      // the first product's factor
-  int sb[OZ_MAX_NS_STEPS];          // B is stored times 2^sb
-};
-
 __device__ __forceinline__ float load_value(const void* p, long long i, int dtype) {
   if (dtype == OZ_F32) return static_cast<const float*>(p)[i];
   const uint16_t h = static_cast<const uint16_t*>(p)[i];
   return dtype == OZ_BF16 ? __bfloat162float(__ushort_as_bfloat16(h)) : __half2float(__ushort_as_half(h));
 }
 
-// Sums of squares in three ranges (Blue's method), so that no square over- or underflows:
-// partial[matrix][block] = {sum (x 2^-70)^2 of the large, sum x^2, sum (x 2^90)^2 of the small}.
+// partial[matrix][block]: the three sums of SumSquares.
 __global__ void __launch_bounds__(256) norm_kernel(const void* __restrict__ G, int dtype, int cols, long long rows,
                                                    long long ld, long long stride, double* __restrict__ partial,
                                                    unsigned* __restrict__ counters, int ncounters) {
   if (blockIdx.y == 0)
     for (int i = blockIdx.x * 256 + threadIdx.x; i < ncounters; i += gridDim.x * 256) counters[i] = 0;
   const long long base = blockIdx.y * stride;
-  float big = 0.0f, mid = 0.0f, small = 0.0f;
-  auto add = [&](float x) {
-    const float m = fabsf(x);
-    if (m > 0x1p50f) {
-      const float y = x * 0x1p-70f;
-      big = fmaf(y, y, big);
-    } else if (m < 0x1p-50f) {
-      const float y = x * 0x1p90f;
-      small = fmaf(y, y, small);
-    } else {
-      mid = fmaf(x, x, mid);  // and NaN
-    }
-  };
+  SumSquares sq;
+  auto add = [&](float x) { sq.add(x); };
   const bool dense = ld == cols && (reinterpret_cast<uintptr_t>(G) & 15) == 0 && stride % 8 == 0;
   if (dense) {  // 16-byte loads over the whole matrix
     const long long n = rows * cols;
@@ -288,8 +268,8 @@ __global__ void __launch_bounds__(256) norm_kernel(const void* __restrict__ G, i
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < nv; i += gridDim.x * 256ll) {
       const uint4 w = __ldg(v + i);
       const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-      const float before = mid;  // the vector's squares are summed by themselves first
-      mid = 0.0f;
+      const float before = sq.mid;  // the vector's squares are summed by themselves first
+      sq.mid = 0.0f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (dtype == OZ_F32) {
@@ -302,7 +282,7 @@ __global__ void __launch_bounds__(256) norm_kernel(const void* __restrict__ G, i
           add(__half2float(__ushort_as_half(static_cast<uint16_t>(q[e] >> 16))));
         }
       }
-      mid += before;
+      sq.mid += before;
     }
     for (long long i = nv * per + blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll)
       add(load_value(G, base + i, dtype));
@@ -311,7 +291,7 @@ __global__ void __launch_bounds__(256) norm_kernel(const void* __restrict__ G, i
       for (int c = threadIdx.x; c < cols; c += 256) add(load_value(G, base + r * ld + c, dtype));
   }
   __shared__ double sums[3][8];
-  double s[3] = {big, mid, small};
+  double s[3] = {sq.big, sq.mid, sq.small};
 #pragma unroll
   for (int j = 0; j < 3; ++j) {
 #pragma unroll
@@ -326,13 +306,10 @@ __global__ void __launch_bounds__(256) norm_kernel(const void* __restrict__ G, i
   }
 }
 
-// X_0 = G / (|G|_F + eps) as FP16 slices times 2^t, t = sx + t0: G 2^-e 2^sx with
-// 2^e >= |G|_F > 2^(e-1), and what remains, 2^e / (|G|_F + eps) = r 2^-t0 with r in [1, 2),
-// goes into the factors of the products (t0 > 0 only when eps dominates the norm; it shrinks
-// by `drop` a step, the most a tiny X can grow).
+// X_0 as FP16 slices, and the factors of the products (newton_scales).
 __global__ void __launch_bounds__(256) convert_kernel(const void* __restrict__ G, int dtype, int cols, long long rows,
                                                       long long ld, long long stride, const double* __restrict__ partial,
-                                                      int nblocks, float eps, const __grid_constant__ StepScales sc,
+                                                      int nblocks, float eps, const __grid_constant__ NewtonPlan plan,
                                                       uint16_t* __restrict__ X, int ldx, long long plane, int planes,
                                                       float* __restrict__ scales) {
   __shared__ float s_mul[2];
@@ -346,35 +323,7 @@ __global__ void __launch_bounds__(256) convert_kernel(const void* __restrict__ G
 #pragma unroll
       for (int d = 16; d; d >>= 1) s[j] += __shfl_xor_sync(0xFFFFFFFFu, s[j], d);
     if (threadIdx.x == 0) {
-      const double norm = sqrt(scalbn(s[0], 140) + s[1] + scalbn(s[2], -180));
-      const double whole = norm + static_cast<double>(eps);
-      int e = 0, t0 = 0;
-      double r = 0.0;
-      if (isfinite(norm) && norm > 0.0) {
-        e = ilogb(norm);
-        if (scalbn(1.0, e) < norm) ++e;
-        const double q = scalbn(1.0, e) / whole;
-        t0 = -ilogb(q);
-        r = scalbn(q, t0);
-      } else if (norm != 0.0) {
-        r = NAN;  // a matrix that holds Inf or NaN gives NaN everywhere
-      }
-      const int h = (sc.sx - e) / 2;
-      s_mul[0] = static_cast<float>(scalbn(1.0, h));
-      s_mul[1] = static_cast<float>(scalbn(1.0, sc.sx - e - h));
-      if (blockIdx.x == 0) {
-        // factors of the steps: gram_i = gram 2^(-2 t_i), apply_i = 2^(t_{i+1} - t_i - sb), the last to t = 0
-        float* f = scales + static_cast<long long>(blockIdx.y) * 2 * sc.steps;
-        int t = sc.sx + t0;
-        for (int i = 0; i < sc.steps; ++i) {
-          int next = t - sc.drop < sc.sx ? sc.sx : t - sc.drop;
-          if (i + 1 == sc.steps) next = 0;
-          const double q = i == 0 ? r : 1.0;
-          f[2 * i] = static_cast<float>(scalbn(sc.gram[i] * q * q, -2 * t));
-          f[2 * i + 1] = static_cast<float>(scalbn(q, next - t - sc.sb[i]));
-          t = next;
-        }
-      }
+      newton_scales(s, eps, plan, s_mul, blockIdx.x == 0 ? scales + static_cast<long long>(blockIdx.y) * 2 * plan.steps : nullptr);
     }
   }
   __syncthreads();
@@ -424,26 +373,20 @@ __global__ void __launch_bounds__(256) convert_kernel(const void* __restrict__ G
   }
 }
 
-// The iteration's plan: power-of-two scales from bounds on the singular values.
-struct Plan {
-  StepScales sc;
-  float diag_s[OZ_MAX_NS_STEPS], alpha_b[OZ_MAX_NS_STEPS], diag_b[OZ_MAX_NS_STEPS];
-  bool square[OZ_MAX_NS_STEPS];
-};
-
 int room(double bound) { return static_cast<int>(std::floor(std::log2(60000.0 / bound))); }
 
 // OZ_ERANGE if the singular values may leave the range in which the scales keep 11 (22) bits
 // useful: a bound above 16 on X, or a square whose completion cancels more than 4 bits.
-int make_plan(int steps, const float* coeffs, Plan* out) {
-  Plan p{};
-  p.sc.steps = steps;
+int make_plan(int steps, const float* coeffs, NewtonPlan* out) {
+  NewtonPlan p{};
+  p.steps = steps;
   double bound = 1.0, worst = 1.0, gain = 1.0;
   for (int i = 0; i < steps; ++i) {
     const double a = coeffs[3 * i], b = coeffs[3 * i + 1], c = coeffs[3 * i + 2];
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return OZ_EINVAL;
-    p.square[i] = c != 0.0;
-    const double beta = p.square[i] ? b / (2 * c) : 0.0;
+    const bool square = c != 0.0;
+    if (square) p.square |= 1u << i;
+    const double beta = square ? b / (2 * c) : 0.0;
     const double top = bound * 1.02, l_top = top * top;  // 2 %: rounding of the stored matrices
     // Maxima over [0, top] at the ends and where the derivative vanishes: of p(l) at l = -b/2c,
     // of s p(s^2) where a + 3 b l + 5 c l^2 = 0.
@@ -454,7 +397,7 @@ int make_plan(int steps, const float* coeffs, Plan* out) {
     auto stationary = [&](double l) {
       if (l > 0.0 && l < l_top) x_max = std::fmax(x_max, std::sqrt(l) * p_at(l));
     };
-    if (p.square[i]) {
+    if (square) {
       if (-beta > 0.0 && -beta < l_top) p_max = std::fmax(p_max, p_at(-beta));
       const double d = 9 * b * b - 20 * a * c;
       if (d >= 0.0) {
@@ -468,24 +411,24 @@ int make_plan(int steps, const float* coeffs, Plan* out) {
     x_max *= 1.01;
     s_max *= 1.01;
     if (!(x_max <= 16.0) || !(p_max <= 1024.0) || p_max == 0.0) return OZ_ERANGE;
-    p.sc.sb[i] = room(p_max);
-    if (p.square[i]) {
+    p.sb[i] = room(p_max);
+    if (square) {
       if (std::fabs(c) * s_max * s_max > 16.0 * p_max) return OZ_ERANGE;
       const int sa = room(s_max);
-      p.sc.gram[i] = static_cast<float>(std::ldexp(1.0, sa));
+      p.gram[i] = static_cast<float>(std::ldexp(1.0, sa));
       p.diag_s[i] = static_cast<float>(std::ldexp(beta, sa));
-      p.alpha_b[i] = static_cast<float>(std::ldexp(c, p.sc.sb[i] - 2 * sa));
-      p.diag_b[i] = static_cast<float>(std::ldexp(a - b * beta / 2, p.sc.sb[i]));
+      p.alpha_b[i] = static_cast<float>(std::ldexp(c, p.sb[i] - 2 * sa));
+      p.diag_b[i] = static_cast<float>(std::ldexp(a - b * beta / 2, p.sb[i]));
     } else {
-      p.sc.gram[i] = static_cast<float>(std::ldexp(b, p.sc.sb[i]));
-      p.diag_b[i] = static_cast<float>(std::ldexp(a, p.sc.sb[i]));
+      p.gram[i] = static_cast<float>(std::ldexp(b, p.sb[i]));
+      p.diag_b[i] = static_cast<float>(std::ldexp(a, p.sb[i]));
     }
     bound = std::fmax(x_max, 1e-3);
     worst = std::fmax(worst, x_max);
     gain = std::fmax(gain, p_max);
   }
-  p.sc.sx = room(worst) < 14 ? room(worst) : 14;
-  p.sc.drop = static_cast<int>(std::ceil(std::log2(gain)));
+  p.sx = room(worst) < 14 ? room(worst) : 14;
+  p.drop = static_cast<int>(std::ceil(std::log2(gain)));
   *out = p;
   return OZ_OK;
 }
@@ -509,6 +452,7 @@ struct Shape {
   size_t part_bytes() const { return align256(sizeof(float) * 2 * HALF_M * BN * kMaxParts); }  // of one product
   int words() const { return 3 * 2 * kMaxParts + 1 + batch; }  // arrivals, stopped, finished
   size_t total() const {
+    if (newton_is_small(rows, cols, planes)) return 0;
     return 2 * x_bytes + 2 * s_bytes + 3 * part_bytes() + align256(sizeof(unsigned) * words()) +
            align256(sizeof(double) * 3 * norm_blocks * batch) + align256(sizeof(float) * 2 * OZ_MAX_NS_STEPS * batch);
   }
@@ -571,14 +515,14 @@ int check(int m, int n, int batch, int dtype, const void* G, int ldg, long long 
 }
 
 template <int PLANES>
-int run_chain(const Shape& sh, const Plan& plan, uint16_t* const (&X)[2], uint16_t* S, uint16_t* B, float* part,
+int run_chain(const Shape& sh, const NewtonPlan& plan, uint16_t* const (&X)[2], uint16_t* S, uint16_t* B, float* part,
               unsigned* words, const float* scales, void* O, int dtype, int ldo, long long stride_o, const Device& dev,
               cudaStream_t stream) {
   typedef ChainWalk<PLANES> Walk;
   typename Walk::Params a{};
   const int side = sh.side, long_side = sh.wide ? sh.cols : sh.rows;
   a.batch = sh.batch;
-  a.steps = plan.sc.steps;
+  a.steps = plan.steps;
   a.chunk = side <= 256 ? 1 : KSTEPS;
   a.X[0] = X[0];
   a.X[1] = X[1];
@@ -594,11 +538,11 @@ int run_chain(const Shape& sh, const Plan& plan, uint16_t* const (&X)[2], uint16
   a.out_type = dtype == OZ_F32 ? kOutF32 : dtype == OZ_BF16 ? kOutBf16 : kOutF16;
   a.vec_o = (reinterpret_cast<uintptr_t>(O) & 15) == 0 && ldo % 8 == 0 && (sh.batch == 1 || stride_o % 8 == 0);
   a.scales = scales;
+  a.square = plan.square;
   for (int i = 0; i < a.steps; ++i) {
     a.diag_s[i] = plan.diag_s[i];
     a.alpha_b[i] = plan.alpha_b[i];
     a.diag_b[i] = plan.diag_b[i];
-    if (plan.square[i]) a.square |= 1u << i;
   }
   a.stopped = words + 3 * 2 * kMaxParts;
   a.finished = a.stopped + 1;
@@ -654,8 +598,10 @@ int run_chain(const Shape& sh, const Plan& plan, uint16_t* const (&X)[2], uint16
 }
 
 int run(int m, int n, int batch, int dtype, const void* G, int ldg, long long stride_g, void* O, int ldo,
-        long long stride_o, const Plan& plan, float eps, int slices, void* workspace, size_t ws_bytes,
+        long long stride_o, const NewtonPlan& plan, float eps, int slices, void* workspace, size_t ws_bytes,
         cudaStream_t stream) {
+  if (newton_is_small(n, m, slices))
+    return launch_newton_small(n, m, batch, dtype, G, ldg, stride_g, O, ldo, stride_o, plan, eps, slices, stream);
   const Shape sh(m, n, batch, slices);
   if (!workspace || ws_bytes < sh.total() || (reinterpret_cast<uintptr_t>(workspace) & 255)) return OZ_ENOMEM;
   Device dev;
@@ -679,7 +625,7 @@ int run(int m, int n, int batch, int dtype, const void* G, int ldg, long long st
   norm_kernel<<<dim3(sh.norm_blocks, batch), 256, 0, stream>>>(G, dtype, m, n, ldg, stride_g, partial, words, sh.words());
   const long long work = (static_cast<long long>(sh.rows) * (sh.ldx / 8) + 255) / 256;
   convert_kernel<<<dim3(static_cast<unsigned>(work < 1024 ? work : 1024), batch), 256, 0, stream>>>(
-      G, dtype, m, n, ldg, stride_g, partial, sh.norm_blocks, eps, plan.sc, X[0], sh.ldx, xplane, slices, scales);
+      G, dtype, m, n, ldg, stride_g, partial, sh.norm_blocks, eps, plan, X[0], sh.ldx, xplane, slices, scales);
   if (cudaGetLastError() != cudaSuccess) return OZ_ECUDA;
   return slices == 2 ? run_chain<2>(sh, plan, X, S, B, part, words, scales, O, dtype, ldo, stride_o, dev, stream)
                      : run_chain<1>(sh, plan, X, S, B, part, words, scales, O, dtype, ldo, stride_o, dev, stream);
@@ -702,7 +648,7 @@ int ozaki_newton_schulz_ws(int m, int n, int batch, int dtype, const void* G, in
                            size_t ws_bytes, cudaStream_t stream) {
   int rc = check(m, n, batch, dtype, G, ldg, strideG, ldo, strideO, steps, coeffs, eps, num_slices);
   if (rc) return rc;
-  Plan plan;
+  NewtonPlan plan;
   if ((rc = make_plan(steps, coeffs, &plan))) return rc;
   if (m == 0 || n == 0 || batch == 0) return OZ_OK;
   if (!G || !O) return OZ_EINVAL;
@@ -714,19 +660,21 @@ int ozaki_newton_schulz(int m, int n, int batch, int dtype, const void* G, int l
                         cudaStream_t stream) {
   int rc = check(m, n, batch, dtype, G, ldg, strideG, ldo, strideO, steps, coeffs, eps, num_slices);
   if (rc) return rc;
-  Plan plan;
+  NewtonPlan plan;
   if ((rc = make_plan(steps, coeffs, &plan))) return rc;
   if (m == 0 || n == 0 || batch == 0) return OZ_OK;
   if (!G || !O) return OZ_EINVAL;
   const size_t bytes = ozaki_newton_schulz_workspace_bytes(m, n, batch, num_slices);
-  keep_default_pool_cached();
   void* ws = nullptr;
-  if (cudaMallocAsync(&ws, bytes, stream) != cudaSuccess) {
-    cudaGetLastError();
-    return OZ_ENOMEM;
+  if (bytes) {
+    keep_default_pool_cached();
+    if (cudaMallocAsync(&ws, bytes, stream) != cudaSuccess) {
+      cudaGetLastError();
+      return OZ_ENOMEM;
+    }
   }
   rc = run(m, n, batch, dtype, G, ldg, strideG, O, ldo, strideO, plan, eps, num_slices, ws, bytes, stream);
-  if (cudaFreeAsync(ws, stream) != cudaSuccess && rc == OZ_OK) rc = OZ_ECUDA;
+  if (ws && cudaFreeAsync(ws, stream) != cudaSuccess && rc == OZ_OK) rc = OZ_ECUDA;
   return rc;
 }
 

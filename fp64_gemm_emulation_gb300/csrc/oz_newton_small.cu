@@ -1,0 +1,413 @@
+// oz_newton_small.cu -- the Newton-Schulz iteration of a small matrix inside one CTA.
+//
+// The same iteration, scales and slices as oz_newton.cu (S = A + b/2c I, B = c S^2 + .., X <- B X), for
+// matrices whose X and S fit shared memory: the smaller side at most 128, the larger at most 256 (two
+// slices) or 512.  Between products of a chain that spans CTAs, half of the time is a fence, a flag
+// and a reload (4.5 of 9 us a product at 128 x 128 with two slices); here a product is handed on
+// by an mbarrier, and the whole operator, norm included, is one launch.  One CTA a matrix.
+//
+// X is kept with its smaller side as rows, in 128-byte-swizzled blocks of 64 columns.  That one
+// layout is the K-major operand of the Gram product (K = columns) and the MN-major operand of
+// B X (N = columns, K = rows), so nothing is rearranged.  S and B share one buffer, and X_{i+1}
+// replaces X_i: a product's sums are all in tensor memory before its operands are overwritten.
+// An accumulator lane is a matrix row, so a thread writes 32 consecutive columns as 16-byte stores.
+//   warps 0-7: epilogue (lanes 32 (warp % 4) .., every second block of 32 columns)   warp 8: MMA
+// Two slices: each MMA step (16 k) is a sum of its own, h l' + l h' first and then h h', added up in
+// FP32 registers (the tensor core's truncation; see oz_newton.cu), through a ring of accumulators.
+// Bound by the latency of a product (MMA, tensor-memory read, stores, two hand-overs).
+#include <atomic>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "oz_device.cuh"
+#include "oz_newton.h"
+
+namespace oz {
+namespace {
+
+constexpr int kRows = 128;
+constexpr uint32_t kBlock = kRows * 128;  // 64 columns of 128 rows
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = (kEpiWarps + 1) * 32;
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride, version, 128-byte swizzle
+
+struct SmallArgs {
+  const void* G;
+  void* O;
+  long long ldg, stride_g, ldo, stride_o;
+  int side, lng, wide, dtype;
+  float eps;
+  NewtonPlan plan;
+  int* status;
+  unsigned long long epi_wait_ns;
+};
+
+__device__ __forceinline__ float load_value(const void* p, long long i, int dtype) {
+  if (dtype == OZ_F32) return static_cast<const float*>(p)[i];
+  const uint16_t h = static_cast<const uint16_t*>(p)[i];
+  return dtype == OZ_BF16 ? __bfloat162float(__ushort_as_bfloat16(h)) : __half2float(__ushort_as_half(h));
+}
+
+// 16 bytes of row r: columns 8 chunk .. of block blk.
+__device__ __forceinline__ uint32_t tile_at(int r, int blk, int chunk) {
+  return blk * kBlock + r * 128 + ((chunk ^ (r & 7)) << 4);
+}
+
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
+      : "memory");
+}
+
+template <int SLICES>
+__global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_constant__ SmallArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t accfull[4], accempty[4], ready, drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  __shared__ double sums[3][kEpiWarps];
+  __shared__ float f01[2], factors[2 * OZ_MAX_NS_STEPS];
+  volatile int* abort_flag = &abort_word;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int side = a.side, lng = a.lng, steps = a.plan.steps;
+  const int xblocks = (lng + 63) / 64, sblocks = (side + 63) / 64;
+  const uint32_t xplane = xblocks * kBlock, splane = sblocks * kBlock;
+  uint8_t* X = smem;
+  uint8_t* S = smem + SLICES * xplane;
+  const int dtype = a.dtype;
+  const void* G = static_cast<const uint8_t*>(a.G) + blockIdx.x * a.stride_g * (dtype == OZ_F32 ? 4 : 2);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&accfull[i], 1);
+      mbar_init(&accempty[i], kEpiWarps);
+    }
+    mbar_init(&ready, kEpiWarps);
+    mbar_init(&drain, 1);
+    abort_word = 0;
+    mbar_fence_init();
+  }
+  if (warp == kEpiWarps) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+
+  // The norm, and X_0.
+  if (warp < kEpiWarps) {
+    SumSquares s;
+    const int cols = a.wide ? lng : side, rows = a.wide ? side : lng;
+    for (int r = warp; r < rows; r += kEpiWarps)
+      for (int c = lane; c < cols; c += 32) s.add(load_value(G, r * a.ldg + c, dtype));
+    double d[3] = {s.big, s.mid, s.small};
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) d[j] += __shfl_xor_sync(0xFFFFFFFFu, d[j], o);
+      if (lane == 0) sums[j][warp] = d[j];
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (threadIdx.x == 0) {
+    double d[3] = {0.0, 0.0, 0.0};
+    for (int j = 0; j < 3; ++j)
+      for (int w = 0; w < kEpiWarps; ++w) d[j] += sums[j][w];
+    newton_scales(d, a.eps, a.plan, f01, factors);
+  }
+  __syncthreads();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp < kEpiWarps) {
+    const float f0 = f01[0], f1 = f01[1];
+    const int chunks = xblocks * 8;
+    for (int q = threadIdx.x; q < kRows * chunks; q += kEpiWarps * 32) {
+      const int i = a.wide ? q / chunks : q % kRows, c = a.wide ? q % chunks : q / kRows;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int l = 8 * c + e;
+        v[e] = i < side && l < lng ? load_value(G, a.wide ? i * a.ldg + l : l * a.ldg + i, dtype) * f0 * f1 : 0.0f;
+      }
+#pragma unroll
+      for (int p = 0; p < SLICES; ++p) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half2 h = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
+          v[2 * e] -= __low2float(h);
+          v[2 * e + 1] -= __high2float(h);
+          w[e] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(X + p * xplane + tile_at(i, c >> 3, c & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+
+  // One product after another: the Gram product, the square (unless c = 0) and B X of each step.
+  // Columns of the sums, steps of 16 k, accumulators: alike for both roles.
+  const int side_n = (side + 31) / 32 * 32, lng_n = (lng + 31) / 32 * 32;
+  struct Shape {
+    int n, k, accs, width;
+  };
+  auto shape_of = [&](int kind) {
+    Shape s;
+    s.n = kind == 2 ? lng_n : side_n;
+    s.k = ((kind == 0 ? lng : side) + 15) / 16;
+    s.accs = SLICES == 1 ? 1 : s.n > 128 ? 2 : 4;
+    s.width = 512 / s.accs;
+    return s;
+  };
+
+  if (warp == kEpiWarps) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      const uint32_t x_lo = smem_u32(X) >> 4, s_lo = smem_u32(S) >> 4;
+      uint32_t ready_phase = 0, empty_bits = 0xFu;  // parities to wait for
+      bool ok = true;
+      for (int i = 0; i < steps && ok; ++i) {
+        for (int kind = 0; kind < 3 && ok; ++kind) {
+          if (kind == 1 && !(a.plan.square >> i & 1)) continue;
+          const Shape s = shape_of(kind);
+          if (!mbar_wait_or_abort(&ready, ready_phase, kWaitLimitNs, abort_flag)) {
+            ok = false;
+            break;
+          }
+          ready_phase ^= 1;
+          tc_fence_after();
+          // D[i, j] = sum A[i, k] B[j, k]: Gram X X^T, S S, and B X with X as its MN-major operand
+          const bool b_mn = kind == 2;
+          const uint32_t a_base = (kind == 0 ? x_lo : s_lo) | (1u << 16);
+          const uint32_t b_base = (kind == 1 ? s_lo : x_lo) | (b_mn ? (kBlock >> 4) << 16 : 1u << 16);
+          const uint32_t a_plane = (kind == 0 ? xplane : splane) >> 4, b_plane = (kind == 1 ? splane : xplane) >> 4;
+          const uint32_t idesc = (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(kRows >> 4) << 24);
+          int acc = 0;
+          for (int k = 0; k < s.k; ++k) {
+            const uint32_t along = (k >> 2) * (kBlock >> 4) + (k & 3) * 2;  // 16 k along a row
+            const uint32_t ak = a_base + along, bk = b_base + (b_mn ? k * (16 * 128 >> 4) : along);
+            if (SLICES == 2 || k == 0) {
+              if (!mbar_wait_or_abort(&accempty[acc], empty_bits >> acc & 1, kWaitLimitNs, abort_flag)) {
+                ok = false;
+                break;
+              }
+              empty_bits ^= 1u << acc;
+              tc_fence_after();
+            }
+            const uint32_t d = tmem + acc * s.width;
+            for (int n0 = 0; n0 < s.n; n0 += 256) {  // an MMA's N is 256 at most
+              const uint32_t id = idesc | static_cast<uint32_t>(min(256, s.n - n0) >> 3) << 17;
+              const uint32_t bn = bk + (b_mn ? (n0 >> 6) * (kBlock >> 4) : n0 * 128 >> 4);
+              if (SLICES == 2) {
+                mma(d + n0, ak, bn + b_plane, id, 0u);
+                mma(d + n0, ak + a_plane, bn, id, 1u);
+                mma(d + n0, ak, bn, id, 1u);
+              } else {
+                mma(d + n0, ak, bn, id, k > 0 ? 1u : 0u);
+              }
+            }
+            if (SLICES == 2 || k + 1 == s.k) {
+              umma_commit(&accfull[acc]);
+              if (++acc == s.accs) acc = 0;
+            }
+          }
+        }
+      }
+      if (!ok && !*abort_flag) {
+        *abort_flag = 1;
+        atomicExch(a.status, OZ_ETIMEOUT);
+      }
+      umma_commit(&drain);  // arrives when every MMA above is done
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quad = warp & 3, half = warp >> 2;
+    const int row = quad * 32 + lane;
+    uint32_t full_bits = 0;
+    bool ok = true;
+    auto hand_on = [&]() {  // what this warp stored is an operand of the next product
+      asm volatile("fence.proxy.async;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ready);
+    };
+    hand_on();
+    for (int i = 0; i < steps && ok; ++i) {
+      for (int kind = 0; kind < 3 && ok; ++kind) {
+        if (kind == 1 && !(a.plan.square >> i & 1)) continue;
+        const Shape s = shape_of(kind);
+        const int nblocks = s.n / 32;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        const bool to_s = kind == 0 && (a.plan.square >> i & 1);
+        const float f = kind == 1 ? a.plan.alpha_b[i] : factors[2 * i + (kind == 2 ? 1 : 0)];
+        const float diag = kind == 2 ? 0.0f : to_s ? a.plan.diag_s[i] : a.plan.diag_b[i];
+        const bool last = kind == 2 && i + 1 == steps;
+        uint8_t* dst = kind == 2 ? X : S;
+        const uint32_t plane = kind == 2 ? xplane : splane;
+
+        auto wait_full = [&](int acc) {
+          const bool got = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&accfull[acc], full_bits >> acc & 1, a.epi_wait_ns, abort_flag));
+          full_bits ^= 1u << acc;
+          if (!got && lane == 0 && !*abort_flag) {
+            *abort_flag = 1;
+            atomicExch(a.status, OZ_ETIMEOUT);
+          }
+          tc_fence_after();
+          return got;
+        };
+        auto release = [&](int acc) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&accempty[acc]);
+        };
+        // 32 finished columns of this thread's row
+        auto finish = [&](float (&v)[32], int cb) {
+          const int n = 32 * cb;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] *= f;
+          if (diag != 0.0f && row >= n && row < n + 32 && row < side) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (row == n + e) v[e] += diag;
+          }
+          if (!last) {
+#pragma unroll
+            for (int p = 0; p < SLICES; ++p) {
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const __half2 h = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
+                if (p + 1 < SLICES) {
+                  v[2 * e] -= __low2float(h);
+                  v[2 * e + 1] -= __high2float(h);
+                }
+                w[e] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4*>(dst + p * plane + tile_at(row, cb >> 1, (cb & 1) * 4 + q)) =
+                    make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+            }
+            return;
+          }
+          if (row >= side) return;
+          const long long base = blockIdx.x * a.stride_o + (a.wide ? row * a.ldo + n : n * a.ldo + row);
+          const long long step = a.wide ? 1 : a.ldo;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            if (n + e < lng) {
+              const long long at = base + e * step;
+              if (dtype == OZ_F32)
+                static_cast<float*>(a.O)[at] = v[e];
+              else if (dtype == OZ_BF16)
+                static_cast<__nv_bfloat16*>(a.O)[at] = __float2bfloat16_rn(v[e]);
+              else
+                static_cast<__half*>(a.O)[at] = __float2half_rn(v[e]);
+            }
+          }
+        };
+
+        if (SLICES == 1) {
+          if (!wait_full(0)) {
+            ok = false;
+            break;
+          }
+          for (int cb = half; cb < nblocks; cb += 2) {
+            uint32_t r[32];
+            tmem_ld32(lanes + 32 * cb, r);
+            tmem_ld_wait();
+            float v[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
+            finish(v, cb);
+          }
+          release(0);
+        } else {
+          float run[4][32];
+#pragma unroll
+          for (int e = 0; e < 128; ++e) run[e >> 5][e & 31] = 0.0f;
+          int acc = 0;
+          for (int k = 0; k < s.k; ++k) {
+            if (!wait_full(acc)) {
+              ok = false;
+              break;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int cb = 2 * j + half;
+              if (cb < nblocks) {
+                uint32_t r[32];
+                tmem_ld32(lanes + acc * s.width + 32 * cb, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) run[j][e] += __uint_as_float(r[e]);
+              }
+            }
+            release(acc);
+            if (++acc == s.accs) acc = 0;
+          }
+          if (!ok) break;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (2 * j + half < nblocks) finish(run[j], 2 * j + half);
+        }
+        hand_on();
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kEpiWarps && lane == 0 && !mbar_wait(&drain, 0)) atomicExch(a.status, OZ_ETIMEOUT);
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kEpiWarps) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+int launch_newton_small(int rows, int cols, int batch, int dtype, const void* G, long long ldg, long long stride_g, void* O,
+                        long long ldo, long long stride_o, const NewtonPlan& plan, float eps, int slices,
+                        cudaStream_t stream) {
+  SmallArgs a{};
+  a.G = G;
+  a.O = O;
+  a.ldg = ldg;
+  a.stride_g = stride_g;
+  a.ldo = ldo;
+  a.stride_o = stride_o;
+  a.wide = rows <= cols;
+  a.side = a.wide ? rows : cols;
+  a.lng = a.wide ? cols : rows;
+  a.dtype = dtype;
+  a.eps = eps;
+  a.plan = plan;
+  a.status = device_status_ptr();
+  a.epi_wait_ns = epilogue_wait_ns();
+  int dev = 0;
+  if (!a.status || cudaGetDevice(&dev) != cudaSuccess) return OZ_ECUDA;
+  const int blocks = (a.lng + 63) / 64 + (a.side + 63) / 64;
+  const size_t smem = 1024 + static_cast<size_t>(slices) * blocks * kBlock;
+  auto kernel = slices == 2 ? newton_small_kernel<2> : newton_small_kernel<1>;
+  constexpr int most = 1024 + 12 * static_cast<int>(kBlock);  // two slices of 256 + 128 columns, or one of 512 + 128
+  static_assert(most + 2048 <= 232448, "shared memory budget");
+  static std::atomic<bool> set[64][2] = {};
+  for (int attempt = 0; attempt < 2; ++attempt) {  // the limit is set again in a new context (see launch)
+    if (dev >= 64 || attempt || !set[dev][slices - 1].load(std::memory_order_acquire)) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return OZ_ECUDA;
+      if (dev < 64) set[dev][slices - 1].store(true, std::memory_order_release);
+    }
+    kernel<<<batch, kThreads, smem, stream>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) return OZ_OK;
+    if (e != cudaErrorInvalidValue) break;
+  }
+  return OZ_ECUDA;
+}
+
+}  // namespace oz

@@ -400,7 +400,8 @@ int ozaki_grouped_gemm_wgrad(int n, int k, int rows, int groups, int dtype, cons
  *  - m, n or batch equal to 0: nothing is done.  batch <= 65535. */
 #define OZ_MAX_NS_STEPS 32
 
-/* Device workspace of ozaki_newton_schulz_ws (0 on invalid or empty arguments).  No GPU needed. */
+/* Device workspace of ozaki_newton_schulz_ws: 0 on invalid or empty arguments, and for matrices that the
+ * kernel holds on the chip (smaller side <= 128, larger <= 512, or 256 with two slices).  No GPU needed. */
 size_t ozaki_newton_schulz_workspace_bytes(int m, int n, int batch, int num_slices);
 
 int ozaki_newton_schulz_ws(int m, int n, int batch, int dtype, const void* G, int ldg, long long strideG, void* O, int ldo,

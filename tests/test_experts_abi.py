@@ -75,14 +75,14 @@ def test_grouped_workspace():
     assert lib.ozaki_grouped_gemm_ws(*args, None, long, None) == oz.OZ_ENOMEM
 
 
-def newton(m=8, n=8, batch=1, dtype=oz.OZ_F32, G=P, ldg=8, sg=64, O=P, ldo=8, so=64, steps=5, coeffs=MUON, eps=1e-7, slices=2):
+def newton(m=300, n=300, batch=1, dtype=oz.OZ_F32, G=P, ldg=300, sg=90000, O=P, ldo=300, so=90000, steps=5, coeffs=MUON, eps=1e-7, slices=2):
     c = None if coeffs is None else np.ascontiguousarray(coeffs, dtype=np.float32)
     return lib.ozaki_newton_schulz_ws(m, n, batch, dtype, G, ldg, sg, O, ldo, so, steps, None if c is None else c.ctypes.data,
                                       ctypes.c_float(eps), slices, P, 16, None)
 
 
 @pytest.mark.parametrize("bad", [dict(m=-1), dict(n=-1), dict(batch=-1), dict(batch=65536), dict(dtype=0), dict(dtype=4),
-                                 dict(ldg=7), dict(ldo=7), dict(batch=2, sg=63), dict(batch=2, so=63), dict(steps=0),
+                                 dict(ldg=299), dict(ldo=299), dict(batch=2, sg=89999), dict(batch=2, so=89999), dict(steps=0),
                                  dict(steps=oz.OZ_MAX_NS_STEPS + 1), dict(coeffs=None), dict(eps=-1.0),
                                  dict(eps=float("nan")), dict(eps=float("inf")), dict(slices=0), dict(slices=3),
                                  dict(G=None), dict(O=None), dict(coeffs=[float("nan")] * 15)])
@@ -101,12 +101,14 @@ def test_newton_schulz_refuses_polynomials_out_of_range():
 
 
 def test_newton_schulz_empty_and_workspace():
-    assert newton(m=0, ldg=1, ldo=1) == oz.OZ_OK
+    assert newton(m=0) == oz.OZ_OK
     assert newton(n=0) == oz.OZ_OK
     assert newton(batch=0) == oz.OZ_OK
     one, two = (oz.ozaki_newton_schulz_workspace_bytes(300, 500, 3, s) for s in (1, 2))
     assert one >= 2 * 2 * 3 * 300 * 512 and two >= 2 * 2 * 2 * 3 * 300 * 512
     assert oz.ozaki_newton_schulz_workspace_bytes(0, 5) == 0
+    assert oz.ozaki_newton_schulz_workspace_bytes(128, 256, 7, 2) == 0  # small matrices need none
+    assert oz.ozaki_newton_schulz_workspace_bytes(129, 129, 1, 1) > 0
     assert oz.ozaki_newton_schulz_workspace_bytes(5, 5, 1, 3) == 0
 
 

@@ -322,9 +322,7 @@ __global__ void __launch_bounds__(256) convert_kernel(const void* __restrict__ G
     for (int j = 0; j < 3; ++j)
 #pragma unroll
       for (int d = 16; d; d >>= 1) s[j] += __shfl_xor_sync(0xFFFFFFFFu, s[j], d);
-    if (threadIdx.x == 0) {
-      newton_scales(s, eps, plan, s_mul, blockIdx.x == 0 ? scales + static_cast<long long>(blockIdx.y) * 2 * plan.steps : nullptr);
-    }
+    newton_scales(s, eps, plan, s_mul, blockIdx.x == 0 ? scales + static_cast<long long>(blockIdx.y) * 2 * plan.steps : nullptr);
   }
   __syncthreads();
   const float f0 = s_mul[0], f1 = s_mul[1];

@@ -34,38 +34,38 @@ struct SumSquares {
   }
 };
 
-// From the three sums: X_0 = G / (|G|_F + eps) is stored as G f0 f1 = G 2^(sx - e) with
+// From the three sums, by a warp: X_0 = G / (|G|_F + eps) is stored as G f0 f1 = G 2^(sx - e) with
 // 2^e >= |G|_F > 2^(e-1); what remains, 2^e / (|G|_F + eps) = r 2^-t0 with r in [1, 2), goes into
-// the factors of the products (t0 > 0 only when eps dominates the norm; it shrinks by `drop` a step,
-// the most a tiny X can grow): factors[2 i] = gram_i 2^(-2 t_i) and factors[2 i + 1] = 2^(t_{i+1} - t_i - sb),
-// the last to t = 0.  factors may be null.
+// the factors of the products, a step a lane.  X_i is stored times 2^t_i, t_i = sx + max(0, t0 - drop i)
+// (t0 > 0 only when eps dominates the norm; a tiny X gains at most `drop` bits a step) and t = 0 at the end:
+// factors[2 i] = gram_i 2^(-2 t_i) and factors[2 i + 1] = 2^(t_{i+1} - t_i - sb_i), the first step's times
+// r^2 and r.  factors may be null.
 __device__ inline void newton_scales(const double (&s)[3], float eps, const NewtonPlan& plan, float* f01, float* factors) {
+  const int lane = threadIdx.x & 31;
   const double norm = sqrt(scalbn(s[0], 140) + s[1] + scalbn(s[2], -180));
-  const double whole = norm + static_cast<double>(eps);
   int e = 0, t0 = 0;
-  double r = 0.0;
+  float r = 0.0f;
   if (isfinite(norm) && norm > 0.0) {
     e = ilogb(norm);
     if (scalbn(1.0, e) < norm) ++e;
-    const double q = scalbn(1.0, e) / whole;
+    const double q = scalbn(1.0, e) / (norm + static_cast<double>(eps));
     t0 = -ilogb(q);
-    r = scalbn(q, t0);
+    r = static_cast<float>(scalbn(q, t0));
   } else if (norm != 0.0) {
     r = NAN;  // a matrix that holds Inf or NaN gives NaN everywhere
   }
   const int h = (plan.sx - e) / 2;
-  f01[0] = static_cast<float>(scalbn(1.0, h));
-  f01[1] = static_cast<float>(scalbn(1.0, plan.sx - e - h));
-  if (!factors) return;
-  int t = plan.sx + t0;
-  for (int i = 0; i < plan.steps; ++i) {
-    int next = t - plan.drop < plan.sx ? plan.sx : t - plan.drop;
-    if (i + 1 == plan.steps) next = 0;
-    const double q = i == 0 ? r : 1.0;
-    factors[2 * i] = static_cast<float>(scalbn(plan.gram[i] * q * q, -2 * t));
-    factors[2 * i + 1] = static_cast<float>(scalbn(q, next - t - plan.sb[i]));
-    t = next;
+  if (lane == 0) {
+    f01[0] = ldexpf(1.0f, h);
+    f01[1] = ldexpf(1.0f, plan.sx - e - h);
   }
+  if (!factors || lane >= plan.steps) return;
+  static_assert(OZ_MAX_NS_STEPS <= 32, "a lane for each step");
+  auto stored = [&](int i) { return plan.sx + max(0, t0 - plan.drop * i); };
+  const int t = stored(lane), next = lane + 1 == plan.steps ? 0 : stored(lane + 1);
+  const float q = lane == 0 ? r : 1.0f;
+  factors[2 * lane] = ldexpf(plan.gram[lane] * q * q, -2 * t);
+  factors[2 * lane + 1] = ldexpf(q, next - t - plan.sb[lane]);
 }
 
 // Matrices that one CTA's shared memory holds (oz_newton_small.cu).

@@ -49,6 +49,28 @@ __device__ __forceinline__ float load_value(const void* p, long long i, int dtyp
   return dtype == OZ_BF16 ? __bfloat162float(__ushort_as_bfloat16(h)) : __half2float(__ushort_as_half(h));
 }
 
+// Eight values from element `at` on, `count` of which exist (zeros for the others).
+__device__ __forceinline__ void load8(float (&v)[8], const void* p, long long at, int count, int dtype, bool vec) {
+  if (vec && count == 8) {
+    if (dtype == OZ_F32) {
+      const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+      const float4 y = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + 4);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    } else {
+      const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+      const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint16_t h = static_cast<uint16_t>(q[e >> 1] >> (16 * (e & 1)));
+        v[e] = dtype == OZ_BF16 ? __bfloat162float(__ushort_as_bfloat16(h)) : __half2float(__ushort_as_half(h));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < count ? load_value(p, at + e, dtype) : 0.0f;
+  }
+}
+
 // 16 bytes of row r: columns 8 chunk .. of block blk.
 __device__ __forceinline__ uint32_t tile_at(int r, int blk, int chunk) {
   return blk * kBlock + r * 128 + ((chunk ^ (r & 7)) << 4);
@@ -64,7 +86,13 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a_low, uint32_t b_low, 
       : "memory");
 }
 
-template <int SLICES>
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
+// BROAD: the larger side is over 128 (two slices: a thread then holds 128 running sums instead of 64).
+template <int SLICES, bool BROAD>
 __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_constant__ SmallArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -82,7 +110,11 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
   uint8_t* X = smem;
   uint8_t* S = smem + SLICES * xplane;
   const int dtype = a.dtype;
-  const void* G = static_cast<const uint8_t*>(a.G) + blockIdx.x * a.stride_g * (dtype == OZ_F32 ? 4 : 2);
+  const int size = dtype == OZ_F32 ? 4 : 2;
+  const uint8_t* G = static_cast<const uint8_t*>(a.G) + blockIdx.x * a.stride_g * size;
+  uint8_t* O = static_cast<uint8_t*>(a.O) + blockIdx.x * a.stride_o * size;
+  const bool vec_in = ((reinterpret_cast<uintptr_t>(G) | (a.ldg * size)) & 15) == 0;
+  const bool vec_out = a.wide && ((reinterpret_cast<uintptr_t>(O) | (a.ldo * size)) & 15) == 0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
@@ -103,8 +135,18 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
   if (warp < kEpiWarps) {
     SumSquares s;
     const int cols = a.wide ? lng : side, rows = a.wide ? side : lng;
-    for (int r = warp; r < rows; r += kEpiWarps)
-      for (int c = lane; c < cols; c += 32) s.add(load_value(G, r * a.ldg + c, dtype));
+    const int chunks = (cols + 7) / 8;
+#pragma unroll 4
+    for (int q = threadIdx.x; q < rows * chunks; q += kEpiWarps * 32) {
+      const int r = q / chunks, c = 8 * (q - r * chunks);
+      float v[8];
+      load8(v, G, r * a.ldg + c, min(8, cols - c), dtype, vec_in);
+      float own = s.mid;  // eight squares are summed by themselves first
+      s.mid = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s.add(v[e]);
+      s.mid += own;
+    }
     double d[3] = {s.big, s.mid, s.small};
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
@@ -116,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (threadIdx.x == 0) {
+  if (warp == 0) {
     double d[3] = {0.0, 0.0, 0.0};
     for (int j = 0; j < 3; ++j)
       for (int w = 0; w < kEpiWarps; ++w) d[j] += sums[j][w];
@@ -128,14 +170,18 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
   if (warp < kEpiWarps) {
     const float f0 = f01[0], f1 = f01[1];
     const int chunks = xblocks * 8;
+#pragma unroll 2
     for (int q = threadIdx.x; q < kRows * chunks; q += kEpiWarps * 32) {
       const int i = a.wide ? q / chunks : q % kRows, c = a.wide ? q % chunks : q / kRows;
       float v[8];
+      if (a.wide) {
+        load8(v, G, i * a.ldg + 8 * c, i < side ? min(8, lng - 8 * c) : 0, dtype, vec_in);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int l = 8 * c + e;
-        v[e] = i < side && l < lng ? load_value(G, a.wide ? i * a.ldg + l : l * a.ldg + i, dtype) * f0 * f1 : 0.0f;
+        for (int e = 0; e < 8; ++e) v[e] = i < side && 8 * c + e < lng ? load_value(G, (8 * c + e) * a.ldg + i, dtype) : 0.0f;
       }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * f0 * f1;
 #pragma unroll
       for (int p = 0; p < SLICES; ++p) {
         uint32_t w[4];
@@ -152,26 +198,34 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
   }
 
   // One product after another: the Gram product, the square (unless c = 0) and B X of each step.
-  // Columns of the sums, steps of 16 k, accumulators: alike for both roles.
+  // Columns of the sums, steps of 16 k, accumulators (those of a group are handed over together):
+  // alike for both roles.
   const int side_n = (side + 31) / 32 * 32, lng_n = (lng + 31) / 32 * 32;
   struct Shape {
-    int n, k, accs, width;
+    int n, k, accs, group, width;
   };
   auto shape_of = [&](int kind) {
     Shape s;
     s.n = kind == 2 ? lng_n : side_n;
     s.k = ((kind == 0 ? lng : side) + 15) / 16;
     s.accs = SLICES == 1 ? 1 : s.n > 128 ? 2 : 4;
+    s.group = s.accs == 4 ? 2 : 1;
     s.width = 512 / s.accs;
     return s;
   };
 
   if (warp == kEpiWarps) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ------------------------------------------------------------ MMA issuer
       const uint32_t x_lo = smem_u32(X) >> 4, s_lo = smem_u32(S) >> 4;
       uint32_t ready_phase = 0, empty_bits = 0xFu;  // parities to wait for
       bool ok = true;
+      auto next_acc = [&](int b) {  // waits until the epilogue has emptied buffer b
+        if (!mbar_wait_or_abort(&accempty[b], empty_bits >> b & 1, kWaitLimitNs, abort_flag)) return false;
+        empty_bits ^= 1u << b;
+        tc_fence_after();
+        return true;
+      };
       for (int i = 0; i < steps && ok; ++i) {
         for (int kind = 0; kind < 3 && ok; ++kind) {
           if (kind == 1 && !(a.plan.square >> i & 1)) continue;
@@ -188,33 +242,49 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
           const uint32_t b_base = (kind == 1 ? s_lo : x_lo) | (b_mn ? (kBlock >> 4) << 16 : 1u << 16);
           const uint32_t a_plane = (kind == 0 ? xplane : splane) >> 4, b_plane = (kind == 1 ? splane : xplane) >> 4;
           const uint32_t idesc = (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(kRows >> 4) << 24);
-          int acc = 0;
-          for (int k = 0; k < s.k; ++k) {
-            const uint32_t along = (k >> 2) * (kBlock >> 4) + (k & 3) * 2;  // 16 k along a row
-            const uint32_t ak = a_base + along, bk = b_base + (b_mn ? k * (16 * 128 >> 4) : along);
-            if (SLICES == 2 || k == 0) {
-              if (!mbar_wait_or_abort(&accempty[acc], empty_bits >> acc & 1, kWaitLimitNs, abort_flag)) {
-                ok = false;
-                break;
+          const uint32_t b_step = b_mn ? 16 * 128 >> 4 : 2, b_skip = b_mn ? 0 : (kBlock >> 4) - 8;
+          const uint32_t id = idesc | static_cast<uint32_t>(min(256, s.n) >> 3) << 17;
+          uint32_t ak = a_base, bk = b_base;
+          if (SLICES == 1) {
+            ok = next_acc(0);
+            if (!ok) break;
+            // an MMA's N is 256 at most: the columns past it (B X only) are a second product
+            const uint32_t id2 = idesc | static_cast<uint32_t>((s.n - 256) >> 3) << 17, b2 = 4 * (kBlock >> 4);
+            for (int k = 0; k < s.k; k += 4) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (k + q < s.k) {
+                  mma(tmem, ak, bk, id, (k | q) > 0);
+                  if (s.n > 256) mma(tmem + 256, ak, bk + b2, id2, (k | q) > 0);
+                }
+                ak += 2;
+                bk += b_step;
               }
-              empty_bits ^= 1u << acc;
-              tc_fence_after();
+              ak += (kBlock >> 4) - 8;
+              bk += b_skip;
             }
-            const uint32_t d = tmem + acc * s.width;
-            for (int n0 = 0; n0 < s.n; n0 += 256) {  // an MMA's N is 256 at most
-              const uint32_t id = idesc | static_cast<uint32_t>(min(256, s.n - n0) >> 3) << 17;
-              const uint32_t bn = bk + (b_mn ? (n0 >> 6) * (kBlock >> 4) : n0 * 128 >> 4);
-              if (SLICES == 2) {
-                mma(d + n0, ak, bn + b_plane, id, 0u);
-                mma(d + n0, ak + a_plane, bn, id, 1u);
-                mma(d + n0, ak, bn, id, 1u);
-              } else {
-                mma(d + n0, ak, bn, id, k > 0 ? 1u : 0u);
+            umma_commit(&accfull[0]);
+          } else {
+            // a sum of every k step; two of them go through the hand-over together
+            int acc = 0;
+            for (int k = 0; k < s.k && ok; k += 4) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (k + q < s.k) {
+                  const int buffer = acc / s.group, within = acc - buffer * s.group;
+                  if (within == 0 && !(ok = next_acc(buffer))) break;
+                  const uint32_t d = tmem + acc * s.width;
+                  mma(d, ak, bk + b_plane, id, 0u);
+                  mma(d, ak + a_plane, bk, id, 1u);
+                  mma(d, ak, bk, id, 1u);
+                  if (within + 1 == s.group || k + q + 1 == s.k) umma_commit(&accfull[buffer]);
+                  if (++acc == s.accs) acc = 0;
+                }
+                ak += 2;
+                bk += b_step;
               }
-            }
-            if (SLICES == 2 || k + 1 == s.k) {
-              umma_commit(&accfull[acc]);
-              if (++acc == s.accs) acc = 0;
+              ak += (kBlock >> 4) - 8;
+              bk += b_skip;
             }
           }
         }
@@ -296,18 +366,37 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
             return;
           }
           if (row >= side) return;
-          const long long base = blockIdx.x * a.stride_o + (a.wide ? row * a.ldo + n : n * a.ldo + row);
-          const long long step = a.wide ? 1 : a.ldo;
+          if (vec_out && n + 32 <= lng) {
+            uint4* to = reinterpret_cast<uint4*>(O + (row * a.ldo + n) * size);
+            if (dtype == OZ_F32) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                to[q] = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                                   __float_as_uint(v[4 * q + 3]));
+            } else {
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const __half2 h = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+                w[e] = dtype == OZ_BF16 ? *reinterpret_cast<const uint32_t*>(&b) : *reinterpret_cast<const uint32_t*>(&h);
+              }
+#pragma unroll
+              for (int q = 0; q < 4; ++q) to[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+            }
+            return;
+          }
+          const long long base = a.wide ? row * a.ldo + n : n * a.ldo + row, step = a.wide ? 1 : a.ldo;
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             if (n + e < lng) {
               const long long at = base + e * step;
               if (dtype == OZ_F32)
-                static_cast<float*>(a.O)[at] = v[e];
+                reinterpret_cast<float*>(O)[at] = v[e];
               else if (dtype == OZ_BF16)
-                static_cast<__nv_bfloat16*>(a.O)[at] = __float2bfloat16_rn(v[e]);
+                reinterpret_cast<__nv_bfloat16*>(O)[at] = __float2bfloat16_rn(v[e]);
               else
-                static_cast<__half*>(a.O)[at] = __float2half_rn(v[e]);
+                reinterpret_cast<__half*>(O)[at] = __float2half_rn(v[e]);
             }
           }
         };
@@ -328,33 +417,45 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
           }
           release(0);
         } else {
-          float run[4][32];
+          // narrow: up to 128 columns, two accumulators a hand-over; otherwise up to 256, one
+          auto sum_up = [&](auto blocks, auto group) {
+            constexpr int B = decltype(blocks)::value, GROUP = decltype(group)::value;
+            float run[B][32];
 #pragma unroll
-          for (int e = 0; e < 128; ++e) run[e >> 5][e & 31] = 0.0f;
-          int acc = 0;
-          for (int k = 0; k < s.k; ++k) {
-            if (!wait_full(acc)) {
-              ok = false;
-              break;
-            }
+            for (int e = 0; e < B * 32; ++e) run[e >> 5][e & 31] = 0.0f;
+            int buffer = 0;
+            for (int k = 0; k < s.k; k += GROUP) {
+              if (!wait_full(buffer)) return false;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int cb = 2 * j + half;
-              if (cb < nblocks) {
-                uint32_t r[32];
-                tmem_ld32(lanes + acc * s.width + 32 * cb, r);
-                tmem_ld_wait();
+              for (int j = 0; j < B; ++j) {
+                const int cb = 2 * j + half;
+                if (cb < nblocks) {
+                  uint32_t r[GROUP][32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) run[j][e] += __uint_as_float(r[e]);
+                  for (int g = 0; g < GROUP; ++g)
+                    if (k + g < s.k) tmem_ld32(lanes + (buffer * GROUP + g) * s.width + 32 * cb, r[g]);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int g = 0; g < GROUP; ++g)
+                    if (k + g < s.k) {
+#pragma unroll
+                      for (int e = 0; e < 32; ++e) run[j][e] += __uint_as_float(r[g][e]);
+                    }
+                }
               }
+              release(buffer);
+              buffer ^= 1;
             }
-            release(acc);
-            if (++acc == s.accs) acc = 0;
-          }
-          if (!ok) break;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (2 * j + half < nblocks) finish(run[j], 2 * j + half);
+            for (int j = 0; j < B; ++j)
+              if (2 * j + half < nblocks) finish(run[j], 2 * j + half);
+            return true;
+          };
+          if (!BROAD || s.group == 2)
+            ok = sum_up(Int<2>(), Int<2>());
+          else
+            ok = sum_up(Int<BROAD ? 4 : 2>(), Int<1>());
+          if (!ok) break;
         }
         hand_on();
       }
@@ -363,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kEpiWarps && lane == 0 && !mbar_wait(&drain, 0)) atomicExch(a.status, OZ_ETIMEOUT);
+  if (threadIdx.x == 0 && !mbar_wait(&drain, 0)) atomicExch(a.status, OZ_ETIMEOUT);
   __syncthreads();
   tc_fence_after();
   if (warp == kEpiWarps) tmem_dealloc(tmem, 512);
@@ -393,14 +494,15 @@ int launch_newton_small(int rows, int cols, int batch, int dtype, const void* G,
   if (!a.status || cudaGetDevice(&dev) != cudaSuccess) return OZ_ECUDA;
   const int blocks = (a.lng + 63) / 64 + (a.side + 63) / 64;
   const size_t smem = 1024 + static_cast<size_t>(slices) * blocks * kBlock;
-  auto kernel = slices == 2 ? newton_small_kernel<2> : newton_small_kernel<1>;
+  const int variant = slices == 1 ? 0 : a.lng > 128 ? 2 : 1;
+  auto kernel = variant == 0 ? newton_small_kernel<1, true> : variant == 1 ? newton_small_kernel<2, false> : newton_small_kernel<2, true>;
   constexpr int most = 1024 + 12 * static_cast<int>(kBlock);  // two slices of 256 + 128 columns, or one of 512 + 128
   static_assert(most + 2048 <= 232448, "shared memory budget");
-  static std::atomic<bool> set[64][2] = {};
+  static std::atomic<bool> set[64][3] = {};
   for (int attempt = 0; attempt < 2; ++attempt) {  // the limit is set again in a new context (see launch)
-    if (dev >= 64 || attempt || !set[dev][slices - 1].load(std::memory_order_acquire)) {
+    if (dev >= 64 || attempt || !set[dev][variant].load(std::memory_order_acquire)) {
       if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return OZ_ECUDA;
-      if (dev < 64) set[dev][slices - 1].store(true, std::memory_order_release);
+      if (dev < 64) set[dev][variant].store(true, std::memory_order_release);
     }
     kernel<<<batch, kThreads, smem, stream>>>(a);
     const cudaError_t e = cudaGetLastError();

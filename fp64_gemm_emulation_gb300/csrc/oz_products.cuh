@@ -475,17 +475,6 @@ __device__ __forceinline__ bool load_unit(const Unit& u, uint8_t* sA, uint8_t* s
   return true;
 }
 
-// One thread of a converged warp, in the form whose uniformity the compiler can see.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t elected;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xFFFFFFFF;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(elected));
-  return elected != 0;
-}
-
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The kernel.  Walk deals out the units: Walk::Params are the launch's, setup() runs once for the

@@ -322,7 +322,8 @@ __global__ void __launch_bounds__(256) convert_kernel(const void* __restrict__ G
     for (int j = 0; j < 3; ++j)
 #pragma unroll
       for (int d = 16; d; d >>= 1) s[j] += __shfl_xor_sync(0xFFFFFFFFu, s[j], d);
-    newton_scales(s, eps, plan, s_mul, blockIdx.x == 0 ? scales + static_cast<long long>(blockIdx.y) * 2 * plan.steps : nullptr);
+    newton_scales(static_cast<float>(s[0]), static_cast<float>(s[1]), static_cast<float>(s[2]), eps, plan, s_mul,
+                  blockIdx.x == 0 ? scales + static_cast<long long>(blockIdx.y) * 2 * plan.steps : nullptr);
   }
   __syncthreads();
   const float f0 = s_mul[0], f1 = s_mul[1];

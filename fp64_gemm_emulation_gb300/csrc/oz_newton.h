@@ -19,11 +19,11 @@ struct NewtonPlan {
 
 // A sum of squares in three ranges (Blue's method), so that no square over- or underflows.
 struct SumSquares {
-  float big = 0.0f, mid = 0.0f, small = 0.0f;  // (x 2^-70)^2, x^2, (x 2^90)^2
+  float big = 0.0f, mid = 0.0f, small = 0.0f;  // (x 2^-80)^2, x^2, (x 2^90)^2
   __device__ __forceinline__ void add(float x) {
     const float m = fabsf(x);
     if (m > 0x1p50f) {
-      const float y = x * 0x1p-70f;
+      const float y = x * 0x1p-80f;
       big = fmaf(y, y, big);
     } else if (m < 0x1p-50f) {
       const float y = x * 0x1p90f;
@@ -40,18 +40,24 @@ struct SumSquares {
 // (t0 > 0 only when eps dominates the norm; a tiny X gains at most `drop` bits a step) and t = 0 at the end:
 // factors[2 i] = gram_i 2^(-2 t_i) and factors[2 i + 1] = 2^(t_{i+1} - t_i - sb_i), the first step's times
 // r^2 and r.  factors may be null.
-__device__ inline void newton_scales(const double (&s)[3], float eps, const NewtonPlan& plan, float* f01, float* factors) {
+__device__ inline void newton_scales(float big, float mid, float small, float eps, const NewtonPlan& plan, float* f01,
+                                     float* factors) {
   const int lane = threadIdx.x & 31;
-  const double norm = sqrt(scalbn(s[0], 140) + s[1] + scalbn(s[2], -180));
+  // |G|_F = root 2^k, by the largest range that holds anything (with the next one, which may reach into it)
+  const int k = big != 0.0f ? 80 : mid != 0.0f ? 0 : -90;
+  const float root = sqrtf(k > 0 ? big + ldexpf(mid, -160) : k == 0 ? mid + ldexpf(small, -180) : small);
   int e = 0, t0 = 0;
   float r = 0.0f;
-  if (isfinite(norm) && norm > 0.0) {
-    e = ilogb(norm);
-    if (scalbn(1.0, e) < norm) ++e;
-    const double q = scalbn(1.0, e) / (norm + static_cast<double>(eps));
-    t0 = -ilogb(q);
-    r = static_cast<float>(scalbn(q, t0));
-  } else if (norm != 0.0) {
+  if (isfinite(root) && root > 0.0f) {
+    e = ilogbf(root);
+    if (ldexpf(1.0f, e) < root) ++e;
+    const float q = ldexpf(1.0f, e) / (root + ldexpf(eps, -k));
+    if (q > 0.0f) {
+      t0 = -ilogbf(q);
+      r = ldexpf(q, t0);
+    }
+    e += k;
+  } else if (root != 0.0f) {
     r = NAN;  // a matrix that holds Inf or NaN gives NaN everywhere
   }
   const int h = (plan.sx - e) / 2;

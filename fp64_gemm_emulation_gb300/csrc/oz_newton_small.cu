@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
   __shared__ uint64_t accfull[4], accempty[4], ready, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
-  __shared__ double sums[3][kEpiWarps];
+  __shared__ float sums[3][kEpiWarps];
   __shared__ float f01[2], factors[2 * OZ_MAX_NS_STEPS];
   volatile int* abort_flag = &abort_word;
 
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
       for (int e = 0; e < 8; ++e) s.add(v[e]);
       s.mid += own;
     }
-    double d[3] = {s.big, s.mid, s.small};
+    float d[3] = {s.big, s.mid, s.small};
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
 #pragma unroll
@@ -159,10 +159,15 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   if (warp == 0) {
-    double d[3] = {0.0, 0.0, 0.0};
-    for (int j = 0; j < 3; ++j)
-      for (int w = 0; w < kEpiWarps; ++w) d[j] += sums[j][w];
-    newton_scales(d, a.eps, a.plan, f01, factors);
+    float d[3];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      d[j] = lane < kEpiWarps ? sums[j][lane] : 0.0f;
+#pragma unroll
+      for (int o = kEpiWarps / 2; o; o >>= 1) d[j] += __shfl_xor_sync(0xFFFFFFFFu, d[j], o);
+      d[j] = __shfl_sync(0xFFFFFFFFu, d[j], 0);
+    }
+    newton_scales(d[0], d[1], d[2], a.eps, a.plan, f01, factors);
   }
   __syncthreads();
   const uint32_t tmem = tmem_slot;
@@ -170,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
   if (warp < kEpiWarps) {
     const float f0 = f01[0], f1 = f01[1];
     const int chunks = xblocks * 8;
-#pragma unroll 2
+#pragma unroll 4
     for (int q = threadIdx.x; q < kRows * chunks; q += kEpiWarps * 32) {
       const int i = a.wide ? q / chunks : q % kRows, c = a.wide ? q % chunks : q / kRows;
       float v[8];

@@ -86,13 +86,7 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a_low, uint32_t b_low, 
       : "memory");
 }
 
-template <int N>
-struct Int {
-  static constexpr int value = N;
-};
-
-// BROAD: the larger side is over 128 (two slices: a thread then holds 128 running sums instead of 64).
-template <int SLICES, bool BROAD>
+template <int SLICES>
 __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_constant__ SmallArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -203,21 +197,13 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
   }
 
   // One product after another: the Gram product, the square (unless c = 0) and B X of each step.
-  // Columns of the sums, steps of 16 k, accumulators (those of a group are handed over together):
-  // alike for both roles.
+  // With two slices a product is summed 128 columns at a time, so that a thread's running sums stay in
+  // registers: the columns of B X do not depend on one another, and those that are done replace X's
+  // while the next are still being summed.  Each k step has an accumulator of its own; two are
+  // handed over together (four of 128 columns).
   const int side_n = (side + 31) / 32 * 32, lng_n = (lng + 31) / 32 * 32;
-  struct Shape {
-    int n, k, accs, group, width;
-  };
-  auto shape_of = [&](int kind) {
-    Shape s;
-    s.n = kind == 2 ? lng_n : side_n;
-    s.k = ((kind == 0 ? lng : side) + 15) / 16;
-    s.accs = SLICES == 1 ? 1 : s.n > 128 ? 2 : 4;
-    s.group = s.accs == 4 ? 2 : 1;
-    s.width = 512 / s.accs;
-    return s;
-  };
+  auto columns = [&](int kind) { return kind == 2 ? lng_n : side_n; };
+  auto k_steps = [&](int kind) { return ((kind == 0 ? lng : side) + 15) / 16; };
 
   if (warp == kEpiWarps) {
     if (elect_one()) {
@@ -234,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
       for (int i = 0; i < steps && ok; ++i) {
         for (int kind = 0; kind < 3 && ok; ++kind) {
           if (kind == 1 && !(a.plan.square >> i & 1)) continue;
-          const Shape s = shape_of(kind);
+          const int n = columns(kind), ks = k_steps(kind);
           if (!mbar_wait_or_abort(&ready, ready_phase, kWaitLimitNs, abort_flag)) {
             ok = false;
             break;
@@ -248,19 +234,19 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
           const uint32_t a_plane = (kind == 0 ? xplane : splane) >> 4, b_plane = (kind == 1 ? splane : xplane) >> 4;
           const uint32_t idesc = (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(kRows >> 4) << 24);
           const uint32_t b_step = b_mn ? 16 * 128 >> 4 : 2, b_skip = b_mn ? 0 : (kBlock >> 4) - 8;
-          const uint32_t id = idesc | static_cast<uint32_t>(min(256, s.n) >> 3) << 17;
-          uint32_t ak = a_base, bk = b_base;
           if (SLICES == 1) {
             ok = next_acc(0);
             if (!ok) break;
             // an MMA's N is 256 at most: the columns past it (B X only) are a second product
-            const uint32_t id2 = idesc | static_cast<uint32_t>((s.n - 256) >> 3) << 17, b2 = 4 * (kBlock >> 4);
-            for (int k = 0; k < s.k; k += 4) {
+            const uint32_t id = idesc | static_cast<uint32_t>(min(256, n) >> 3) << 17;
+            const uint32_t id2 = idesc | static_cast<uint32_t>((n - 256) >> 3) << 17, b2 = 4 * (kBlock >> 4);
+            uint32_t ak = a_base, bk = b_base;
+            for (int k = 0; k < ks; k += 4) {
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                if (k + q < s.k) {
+                if (k + q < ks) {
                   mma(tmem, ak, bk, id, (k | q) > 0);
-                  if (s.n > 256) mma(tmem + 256, ak, bk + b2, id2, (k | q) > 0);
+                  if (n > 256) mma(tmem + 256, ak, bk + b2, id2, (k | q) > 0);
                 }
                 ak += 2;
                 bk += b_step;
@@ -270,26 +256,30 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
             }
             umma_commit(&accfull[0]);
           } else {
-            // a sum of every k step; two of them go through the hand-over together
-            int acc = 0;
-            for (int k = 0; k < s.k && ok; k += 4) {
+            for (int n0 = 0; n0 < n && ok; n0 += 128) {
+              const uint32_t id = idesc | static_cast<uint32_t>(min(128, n - n0) >> 3) << 17;
+              uint32_t ak = a_base, bk = b_base + (n0 >> 6) * (kBlock >> 4);
+              int buffer = 0;
+              for (int k = 0; k < ks && ok; k += 4) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                if (k + q < s.k) {
-                  const int buffer = acc / s.group, within = acc - buffer * s.group;
-                  if (within == 0 && !(ok = next_acc(buffer))) break;
-                  const uint32_t d = tmem + acc * s.width;
-                  mma(d, ak, bk + b_plane, id, 0u);
-                  mma(d, ak + a_plane, bk, id, 1u);
-                  mma(d, ak, bk, id, 1u);
-                  if (within + 1 == s.group || k + q + 1 == s.k) umma_commit(&accfull[buffer]);
-                  if (++acc == s.accs) acc = 0;
+                for (int q = 0; q < 4; ++q) {
+                  if (k + q < ks) {
+                    if ((q & 1) == 0 && !(ok = next_acc(buffer))) break;
+                    const uint32_t d = tmem + 256 * buffer + 128 * (q & 1);
+                    mma(d, ak, bk + b_plane, id, 0u);
+                    mma(d, ak + a_plane, bk, id, 1u);
+                    mma(d, ak, bk, id, 1u);
+                    if ((q & 1) == 1 || k + q + 1 == ks) {
+                      umma_commit(&accfull[buffer]);
+                      buffer ^= 1;
+                    }
+                  }
+                  ak += 2;
+                  bk += b_step;
                 }
-                ak += 2;
-                bk += b_step;
+                ak += (kBlock >> 4) - 8;
+                bk += b_skip;
               }
-              ak += (kBlock >> 4) - 8;
-              bk += b_skip;
             }
           }
         }
@@ -315,8 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
     for (int i = 0; i < steps && ok; ++i) {
       for (int kind = 0; kind < 3 && ok; ++kind) {
         if (kind == 1 && !(a.plan.square >> i & 1)) continue;
-        const Shape s = shape_of(kind);
-        const int nblocks = s.n / 32;
+        const int nblocks = columns(kind) / 32, ks = k_steps(kind);
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const bool to_s = kind == 0 && (a.plan.square >> i & 1);
         const float f = kind == 1 ? a.plan.alpha_b[i] : factors[2 * i + (kind == 2 ? 1 : 0)];
@@ -422,44 +411,40 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
           }
           release(0);
         } else {
-          // narrow: up to 128 columns, two accumulators a hand-over; otherwise up to 256, one
-          auto sum_up = [&](auto blocks, auto group) {
-            constexpr int B = decltype(blocks)::value, GROUP = decltype(group)::value;
-            float run[B][32];
+          for (int b0 = 0; b0 < nblocks && ok; b0 += 4) {  // 128 columns
+            float run[2][32];
 #pragma unroll
-            for (int e = 0; e < B * 32; ++e) run[e >> 5][e & 31] = 0.0f;
+            for (int e = 0; e < 64; ++e) run[e >> 5][e & 31] = 0.0f;
             int buffer = 0;
-            for (int k = 0; k < s.k; k += GROUP) {
-              if (!wait_full(buffer)) return false;
+            for (int k = 0; k < ks; k += 2, buffer ^= 1) {
+              if (!wait_full(buffer)) {
+                ok = false;
+                break;
+              }
 #pragma unroll
-              for (int j = 0; j < B; ++j) {
+              for (int j = 0; j < 2; ++j) {
                 const int cb = 2 * j + half;
-                if (cb < nblocks) {
-                  uint32_t r[GROUP][32];
-#pragma unroll
-                  for (int g = 0; g < GROUP; ++g)
-                    if (k + g < s.k) tmem_ld32(lanes + (buffer * GROUP + g) * s.width + 32 * cb, r[g]);
+                if (b0 + cb < nblocks) {
+                  uint32_t r0[32], r1[32];
+                  const uint32_t at = lanes + 256 * buffer + 32 * cb;
+                  tmem_ld32(at, r0);
+                  if (k + 1 < ks) tmem_ld32(at + 128, r1);
                   tmem_ld_wait();
 #pragma unroll
-                  for (int g = 0; g < GROUP; ++g)
-                    if (k + g < s.k) {
+                  for (int e = 0; e < 32; ++e) run[j][e] += __uint_as_float(r0[e]);
+                  if (k + 1 < ks) {
 #pragma unroll
-                      for (int e = 0; e < 32; ++e) run[j][e] += __uint_as_float(r[g][e]);
-                    }
+                    for (int e = 0; e < 32; ++e) run[j][e] += __uint_as_float(r1[e]);
+                  }
                 }
               }
               release(buffer);
-              buffer ^= 1;
             }
+            if (!ok) break;
 #pragma unroll
-            for (int j = 0; j < B; ++j)
-              if (2 * j + half < nblocks) finish(run[j], 2 * j + half);
-            return true;
-          };
-          if (!BROAD || s.group == 2)
-            ok = sum_up(Int<2>(), Int<2>());
-          else
-            ok = sum_up(Int<BROAD ? 4 : 2>(), Int<1>());
+            for (int j = 0; j < 2; ++j)
+              if (b0 + 2 * j + half < nblocks) finish(run[j], b0 + 2 * j + half);
+          }
           if (!ok) break;
         }
         hand_on();
@@ -499,15 +484,14 @@ int launch_newton_small(int rows, int cols, int batch, int dtype, const void* G,
   if (!a.status || cudaGetDevice(&dev) != cudaSuccess) return OZ_ECUDA;
   const int blocks = (a.lng + 63) / 64 + (a.side + 63) / 64;
   const size_t smem = 1024 + static_cast<size_t>(slices) * blocks * kBlock;
-  const int variant = slices == 1 ? 0 : a.lng > 128 ? 2 : 1;
-  auto kernel = variant == 0 ? newton_small_kernel<1, true> : variant == 1 ? newton_small_kernel<2, false> : newton_small_kernel<2, true>;
+  auto kernel = slices == 2 ? newton_small_kernel<2> : newton_small_kernel<1>;
   constexpr int most = 1024 + 12 * static_cast<int>(kBlock);  // two slices of 256 + 128 columns, or one of 512 + 128
   static_assert(most + 2048 <= 232448, "shared memory budget");
-  static std::atomic<bool> set[64][3] = {};
+  static std::atomic<bool> set[64][2] = {};
   for (int attempt = 0; attempt < 2; ++attempt) {  // the limit is set again in a new context (see launch)
-    if (dev >= 64 || attempt || !set[dev][variant].load(std::memory_order_acquire)) {
+    if (dev >= 64 || attempt || !set[dev][slices - 1].load(std::memory_order_acquire)) {
       if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return OZ_ECUDA;
-      if (dev < 64) set[dev][variant].store(true, std::memory_order_release);
+      if (dev < 64) set[dev][slices - 1].store(true, std::memory_order_release);
     }
     kernel<<<batch, kThreads, smem, stream>>>(a);
     const cudaError_t e = cudaGetLastError();

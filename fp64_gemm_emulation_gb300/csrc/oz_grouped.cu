@@ -300,7 +300,7 @@ struct Problem {
 };
 
 int check(int n, int k, int rows, int groups, int dtype, int ldw, long long stride_w, int ldk, int ldn) {
-  if (n < 0 || k < 0 || rows < 0 || groups < 1 || groups > OZ_MAX_GROUPS) return OZ_EINVAL;
+  if (n < 0 || k < 0 || rows < 0 || n > kMaxExtent || k > kMaxExtent || rows > kMaxExtent || groups < 1 || groups > OZ_MAX_GROUPS) return OZ_EINVAL;
   if (dtype != OZ_BF16 && dtype != OZ_F16) return OZ_EINVAL;
   if (ldw < (k > 1 ? k : 1) || ldk < (k > 1 ? k : 1) || ldn < (n > 1 ? n : 1)) return OZ_EINVAL;
   if (groups > 1 && stride_w < static_cast<long long>(ldw) * n) return OZ_EINVAL;

@@ -480,14 +480,17 @@ void plan_product(Product& p, int batch, int planes, int chunk, int pairs) {
     const long long all = static_cast<long long>(q.tiles) * batch;
     double block = planes == 1 ? 310 + bn : 200 + 5.2 * bn;
     if (planes == 2 && chunk == 1) block = KSTEPS * (300.0 + 2 * bn);
-    const double fixed = 2000 + 6.0 * bn * planes;
+    // The epilogue of a tile runs under the next tile's MMAs; that of the last one shows.
+    const double drain = bn / 64.0 * (planes == 2 ? 800 : p.sym ? 1900 : 1150);
     const int rest = static_cast<int>(all % pairs);
-    const double whole = static_cast<double>(all / pairs) * (nkb * block + fixed * 0.3);
+    const double whole = static_cast<double>(all / pairs) * std::fmax(nkb * block, drain);
     for (int s = 1; s <= 16 && s <= nkb; ++s) {
       if (s > 1 && (rest == 0 || rest * s > kMaxParts)) break;
-      double t = whole;
-      if (rest) t += ceil_div(rest * s, pairs) * (ceil_div(nkb, s) * block + fixed);
-      if (s > 1) t += 3000 + 2500.0 * (bn / 256.0) * (1 + s);
+      double t = whole + drain + 2500;
+      if (rest) t += ceil_div(rest * s, pairs) * ceil_div(nkb, s) * block;
+      // parts: each wave's are written out, and the last reads them all (1024 x 4096 FP32: one wave of
+      // three parts 379 us, two waves of five 430)
+      if (s > 1) t += 3000 + 2500.0 * (bn / 256.0) * (1 + s) + ceil_div(rest * s, pairs) * (2500 + 16.0 * bn);
       if (t < best) {
         best = t;
         q.nsplit = s;
@@ -501,7 +504,7 @@ void plan_product(Product& p, int batch, int planes, int chunk, int pairs) {
 
 int check(int m, int n, int batch, int dtype, const void* G, int ldg, long long stride_g, int ldo, long long stride_o,
           int steps, const float* coeffs, float eps, int slices) {
-  if (m < 0 || n < 0 || batch < 0) return OZ_EINVAL;
+  if (m < 0 || n < 0 || batch < 0 || m > kMaxExtent || n > kMaxExtent) return OZ_EINVAL;
   if (dtype != OZ_BF16 && dtype != OZ_F16 && dtype != OZ_F32) return OZ_EINVAL;
   if (ldg < (m > 1 ? m : 1) || ldo < (m > 1 ? m : 1)) return OZ_EINVAL;
   if (batch > 1 && (stride_g < static_cast<long long>(ldg) * n || stride_o < static_cast<long long>(ldo) * n))
@@ -522,7 +525,7 @@ int run_chain(const Shape& sh, const NewtonPlan& plan, uint16_t* const (&X)[2], 
   const int side = sh.side, long_side = sh.wide ? sh.cols : sh.rows;
   a.batch = sh.batch;
   a.steps = plan.steps;
-  a.chunk = side <= 256 ? 1 : KSTEPS;
+  a.chunk = side <= 128 ? 1 : KSTEPS;
   a.X[0] = X[0];
   a.X[1] = X[1];
   a.S = S;
@@ -638,7 +641,7 @@ using namespace oz;
 extern "C" {
 
 size_t ozaki_newton_schulz_workspace_bytes(int m, int n, int batch, int num_slices) {
-  if (m <= 0 || n <= 0 || batch <= 0 || batch > 65535 || num_slices < 1 || num_slices > 2) return 0;
+  if (m <= 0 || n <= 0 || m > kMaxExtent || n > kMaxExtent || batch <= 0 || batch > 65535 || num_slices < 1 || num_slices > 2) return 0;
   return Shape(m, n, batch, num_slices).total();
 }
 

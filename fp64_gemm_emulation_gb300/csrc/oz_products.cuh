@@ -70,6 +70,8 @@ constexpr long long PART_BLOCK = 32 * HALF_M;  // floats of 32 columns of one CT
 
 enum OutType { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2, kOutSlices = 3 };
 
+constexpr int kMaxExtent = INT32_MAX - 1024;  // dimensions round up within an int
+
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // One unit of work.  A role uses the fields it needs; the rest is never computed for it.

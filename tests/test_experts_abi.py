@@ -25,7 +25,7 @@ def wgrad(n=8, k=8, rows=8, groups=2, dtype=oz.OZ_BF16, dY=P, lddy=8, X=P, ldx=8
 
 
 @pytest.mark.parametrize("call", [forward, dgrad, wgrad])
-@pytest.mark.parametrize("bad", [dict(n=-1), dict(k=-1), dict(rows=-1), dict(groups=0), dict(groups=oz.OZ_MAX_GROUPS + 1),
+@pytest.mark.parametrize("bad", [dict(n=-1), dict(k=-1), dict(rows=-1), dict(rows=2**31 - 1), dict(groups=0), dict(groups=oz.OZ_MAX_GROUPS + 1),
                                  dict(dtype=oz.OZ_F32), dict(dtype=0), dict(ldw=7), dict(sw=63)])
 def test_grouped_refuses_bad_arguments(call, bad):
     assert call(**bad) == oz.OZ_EINVAL

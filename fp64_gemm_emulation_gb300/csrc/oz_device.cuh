@@ -22,6 +22,11 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
   return t;
 }
 
+// Programmatic dependent launch: the next launch may begin (and wait in turn); what the launch before
+// wrote is there.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // One thread of a converged warp, in the form whose uniformity the compiler can see.
 __device__ __forceinline__ bool elect_one() {
   uint32_t elected;

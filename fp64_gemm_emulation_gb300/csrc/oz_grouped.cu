@@ -231,7 +231,7 @@ struct Operand {
 };
 
 __global__ void zero_kernel(unsigned* words) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_start();
   words[threadIdx.x] = 0;
 }
 

@@ -477,8 +477,6 @@ __device__ __forceinline__ bool load_unit(const Unit& u, uint8_t* sA, uint8_t* s
   return true;
 }
 
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // The kernel.  Walk deals out the units: Walk::Params are the launch's, setup() runs once for the
 // whole CTA, a Walk of its own in every role gives the pair's units in order (next; again() works
 // the present one out anew), and
@@ -927,10 +925,10 @@ inline int current_device(Device* d) {
   return d->status ? OZ_OK : OZ_ECUDA;
 }
 
-// How a launch follows what is before it: kCooperative: the units depend on one another, so all CTAs
-// have to run at once (the launch is refused if they cannot); kOverlap: it may start while the
-// launch before it ends, of which it needs nothing but the arrival counters' zeros.
-enum Start { kAfter, kCooperative, kOverlap };
+// How a launch follows what is before it.  kOverlap: it may start while the launch before it ends
+// (wait_for_previous in the kernel).  kCooperative: so too, and all CTAs have to run at once, since units
+// depend on one another (the launch is refused if they cannot).
+enum Start { kAfter, kOverlap, kCooperative };
 
 template <class Walk, int PLANES>
 int launch(typename Walk::Params a, const Device& d, int pairs, Start start, cudaStream_t stream) {  // on `pairs` CTA pairs
@@ -944,20 +942,17 @@ int launch(typename Walk::Params a, const Device& d, int pairs, Start start, cud
   cfg.blockDim = dim3((EPI_FIRST + Walk::kEpiWarps) * 32, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[3];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  if (start == kCooperative) {
-    attr[1].id = cudaLaunchAttributeCooperative;
-    attr[1].val.cooperative = 1;
-  } else {
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-  }
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[2].id = cudaLaunchAttributeCooperative;
+  attr[2].val.cooperative = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = start == kAfter ? 1 : 2;
+  cfg.numAttrs = start == kAfter ? 1 : start == kOverlap ? 2 : 3;
   // The shared-memory limit is the function's, in this context: set on the first launch, and again
   // should a launch be refused (a new context after a device reset).
   static std::atomic<bool> ready[64] = {};

@@ -28,7 +28,7 @@ enum Op { kForward, kDgrad, kWgrad };
 //     neighbouring group ever enters a sum, so its NaNs cannot leak.
 template <Op OP>
 struct GroupedWalk {
-  static constexpr bool kScaled = false, kReports = false;
+  static constexpr bool kScaled = false, kChained = false;
   static constexpr int kEpiWarps = 8;
   static constexpr size_t kTableBytes = (2 * (OZ_MAX_GROUPS + 1) + 3) * 4;  // offsets, tile prefix, the split
   static constexpr bool A_MN = OP != kForward, B_MN = OP == kWgrad, RAGGED_SUM = OP == kWgrad;
@@ -37,7 +37,7 @@ struct GroupedWalk {
   struct Params {
     CUtensorMap tmA, tmB, tmB128;
     int M, N, K;   // contiguous extent of the output; wgrad: its rows; otherwise the sum's length
-    int groups, rows, bn, max_parts, part_cols, chunk;
+    int groups, rows, bn, max_parts, part_cols;
     int a_4d, b_4d, vec, out_type;
     uint32_t idesc;
     const int32_t* offsets;
@@ -200,12 +200,6 @@ struct GroupedWalk {
     u.diag = 0.0f;
     return true;
   }
-
-  __device__ void again(Unit&) const {}
-  __device__ bool ready(const volatile int*) const { return true; }
-  __device__ void stored() const {}
-  __device__ void done() const {}
-  __device__ static void gave_up(const Params&) {}
 
   // Rows that belong to no group are zero.
   __device__ void outside(int warp) const {

@@ -11,7 +11,7 @@
 // follow each other in the same order on every CTA pair, and a unit's producer waits until the
 // product before it is finished for its own matrix (a counter per matrix in global memory).  So the
 // matrices of a batch do not wait for one another, and a product boundary costs a flag instead of
-// a launch (one launch per product: 3.7 us a product at 128 x 128 for 1.5 us of work).
+// a launch (a launch a product took 3.7 us each at 128 x 128, for 1.5 us of work).
 //
 // Numerics.  The products run on the FP16 tensor-core path: FP16 holds 11 bits where bf16
 // holds 8, at the same rate, and every range is known beforehand: |X_0| <= 1, and a host-side
@@ -40,8 +40,8 @@ constexpr int kMaxParts = 160;         // parts of split tiles that a product's 
 //   128 x 128:    1.6e-6 (1 step)  2.3e-6 (2)  3.5e-6 (4)  6.1e-6 (8)   plain FP32: 1.3e-6
 //   8192 x 2048:  1.5e-6 (1)       1.9e-6 (2)  2.9e-6 (4)  5.0e-6 (8)   plain FP32: 4.7e-6
 // and so is the epilogue's work: 4.1, 3.0, 2.6 and 2.4 ms at 8192 x 2048.  One k-block (4 steps) keeps
-// the error below plain FP32's where sums are long; sides up to 256 are bound by latency, so
-// they take single steps (run_chain).
+// the error below plain FP32's where sums are long; sides up to 128 (here and in
+// oz_newton_small.cu) are bound by latency, so they take single steps (run_chain).
 
 // The products of a step.
 enum Kind { kGram = 0, kSquare = 1, kApply = 2 };
@@ -66,7 +66,7 @@ struct Product {
 // Deals out the units of every product of every step, in that order.
 template <int PLANES>
 struct ChainWalk {
-  static constexpr bool kScaled = true, kReports = true;
+  static constexpr bool kScaled = true, kChained = true;
   static constexpr int kEpiWarps = PLANES == 2 ? 12 : 8;
   static constexpr size_t kTableBytes = 0;
 
@@ -238,8 +238,6 @@ struct ChainWalk {
   __device__ void done() const {
     asm volatile("red.relaxed.gpu.global.add.u32 [%0], %1;" ::"l"(a.finished + group), "r"(1u) : "memory");
   }
-
-  __device__ void outside(int) const {}
 
   // This pair has given up: the others' waits end.
   __device__ static void gave_up(const Params& a) { atomicExch(a.stopped, 1u); }
@@ -506,7 +504,7 @@ void plan_product(Product& p, int batch, int planes, int chunk, int pairs) {
   }
 }
 
-int check(int m, int n, int batch, int dtype, const void* G, int ldg, long long stride_g, int ldo, long long stride_o,
+int check(int m, int n, int batch, int dtype, int ldg, long long stride_g, int ldo, long long stride_o,
           int steps, const float* coeffs, float eps, int slices) {
   if (m < 0 || n < 0 || batch < 0 || m > kMaxExtent || n > kMaxExtent) return OZ_EINVAL;
   if (dtype != OZ_BF16 && dtype != OZ_F16 && dtype != OZ_F32) return OZ_EINVAL;
@@ -516,7 +514,6 @@ int check(int m, int n, int batch, int dtype, const void* G, int ldg, long long 
   if (steps < 1 || steps > OZ_MAX_NS_STEPS || !coeffs || slices < 1 || slices > 2) return OZ_EINVAL;
   if (!(eps >= 0.0f) || !std::isfinite(eps)) return OZ_EINVAL;
   if (batch > 65535) return OZ_EINVAL;
-  (void)G;
   return OZ_OK;
 }
 
@@ -665,7 +662,7 @@ size_t ozaki_newton_schulz_workspace_bytes(int m, int n, int batch, int num_slic
 int ozaki_newton_schulz_ws(int m, int n, int batch, int dtype, const void* G, int ldg, long long strideG, void* O, int ldo,
                            long long strideO, int steps, const float* coeffs, float eps, int num_slices, void* workspace,
                            size_t ws_bytes, cudaStream_t stream) {
-  int rc = check(m, n, batch, dtype, G, ldg, strideG, ldo, strideO, steps, coeffs, eps, num_slices);
+  int rc = check(m, n, batch, dtype, ldg, strideG, ldo, strideO, steps, coeffs, eps, num_slices);
   if (rc) return rc;
   NewtonPlan plan;
   if ((rc = make_plan(steps, coeffs, &plan))) return rc;
@@ -677,7 +674,7 @@ int ozaki_newton_schulz_ws(int m, int n, int batch, int dtype, const void* G, in
 int ozaki_newton_schulz(int m, int n, int batch, int dtype, const void* G, int ldg, long long strideG, void* O, int ldo,
                         long long strideO, int steps, const float* coeffs, float eps, int num_slices,
                         cudaStream_t stream) {
-  int rc = check(m, n, batch, dtype, G, ldg, strideG, ldo, strideO, steps, coeffs, eps, num_slices);
+  int rc = check(m, n, batch, dtype, ldg, strideG, ldo, strideO, steps, coeffs, eps, num_slices);
   if (rc) return rc;
   NewtonPlan plan;
   if ((rc = make_plan(steps, coeffs, &plan))) return rc;

@@ -9,7 +9,7 @@
 // 128-byte-swizzled tiles that TMA writes, so nothing is ever transposed in memory.
 //
 // Kernel shape: clusters of two CTAs (cta_group::2), persistent over the units (tile, part of k)
-// that a walker deals out (GroupedWalk here, the Newton-Schulz chain in oz_newton.cu).
+// that a walker deals out (GroupedWalk in oz_grouped.cu, ChainWalk in oz_newton.cu).
 //   warp 0: TMA producer   warp 1: TMEM owner + MMA issuer (leader)   others: epilogue (Walk::kEpiWarps)
 //   6 stages of 32 KB (128 x 64 of A and up to 128 x 64 of B in each CTA), with two slices 4 of 52 KB;
 //   two 256-column FP32
@@ -62,17 +62,16 @@ struct Ring {
   static constexpr uint32_t B_STAGE = PLANES == 2 ? 2 * (BN2 / 2) * BK * 2 : HALF_N * BK * 2;
   static constexpr uint32_t BYTES = STAGES * (A_STAGE + B_STAGE);
   // An epilogue warp's stash: a 32 x 32 block of 16 bits (two slices: no room, store_regs).
-  static constexpr int STASH_ROWS = PLANES == 2 ? 0 : 32;
-  static constexpr uint32_t WARP_STASH = STASH_ROWS * 64;
+  static constexpr uint32_t WARP_STASH = PLANES == 2 ? 0 : 32 * 64;
 };
 
 constexpr long long PART_BLOCK = 32 * HALF_M;  // floats of 32 columns of one CTA's part
 
 enum OutType { kOutBf16 = 0, kOutF16 = 1, kOutF32 = 2, kOutSlices = 3 };
 
-constexpr int kMaxExtent = INT32_MAX - 1024;  // dimensions round up within an int
+constexpr int kMaxExtent = INT32_MAX - 1024;  // a dimension rounded up to a tile stays an int
 
-__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__host__ __device__ inline int ceil_div(int a, int b) { return a / b + (a % b > 0); }
 
 // One unit of work.  A role uses the fields it needs; the rest is never computed for it.
 struct Unit {
@@ -247,30 +246,31 @@ __device__ __forceinline__ Target target_of(const Unit& u, int mrow, uint8_t* st
   return t;
 }
 
-// A whole block of 16-bit values, w[i / 2] holding elements i and i + 1, through the warp's stash
-// (ROWS of it at a time; 8 rows are 512 bytes, which leave the permutation as it is).  ROWS_N: rows of
-// n, otherwise rows of m; dst: this lane's 16 bytes of row lane / 4.
-template <bool ROWS_N, int ROWS>
-__device__ __forceinline__ void store_whole(const uint32_t (&w)[16], const Target& t, uint16_t* dst) {
+// A block of 16-bit values, w[i / 2] holding elements i and i + 1, into the warp's stash (8 rows are
+// 512 bytes, which leave the permutation as it is).  ROWS_N: rows of n, otherwise rows of m.
+template <bool ROWS_N>
+__device__ __forceinline__ void stash_block(const uint32_t (&w)[16], const Target& t) {
 #pragma unroll
-  for (int r0 = 0; r0 < 32; r0 += ROWS ? ROWS : 32) {
-#pragma unroll
-    for (int i = 0; i < ROWS / 8; ++i) {
-      const int j = r0 / 8 + i;
-      if (ROWS_N)  // the four 8-element groups of m, rows n = 8 j ..
-        stmatrix4<true>(t.put + 512 * i, w[2 * j], w[2 * j + 1], w[8 + 2 * j], w[9 + 2 * j]);
-      else  // the four 8-element groups of n, rows m = 8 j ..
-        stmatrix4<false>(t.put + 512 * i, w[(j >> 1) * 8 + (j & 1)], w[(j >> 1) * 8 + 2 + (j & 1)],
-                         w[(j >> 1) * 8 + 4 + (j & 1)], w[(j >> 1) * 8 + 6 + (j & 1)]);
-    }
-    __syncwarp();
-    uint4 x[ROWS ? ROWS / 8 : 1];
-#pragma unroll
-    for (int i = 0; i < ROWS / 8; ++i) x[i] = *reinterpret_cast<const uint4*>(t.get + 512 * i);
-#pragma unroll
-    for (int i = 0; i < ROWS / 8; ++i, dst += t.step) *reinterpret_cast<uint4*>(dst) = x[i];
-    __syncwarp();
+  for (int j = 0; j < 4; ++j) {
+    if (ROWS_N)  // the four 8-element groups of m, rows n = 8 j ..
+      stmatrix4<true>(t.put + 512 * j, w[2 * j], w[2 * j + 1], w[8 + 2 * j], w[9 + 2 * j]);
+    else  // the four 8-element groups of n, rows m = 8 j ..
+      stmatrix4<false>(t.put + 512 * j, w[(j >> 1) * 8 + (j & 1)], w[(j >> 1) * 8 + 2 + (j & 1)],
+                       w[(j >> 1) * 8 + 4 + (j & 1)], w[(j >> 1) * 8 + 6 + (j & 1)]);
   }
+  __syncwarp();
+}
+
+// A whole block; dst: this lane's 16 bytes of row lane / 4.
+template <bool ROWS_N>
+__device__ __forceinline__ void store_whole(const uint32_t (&w)[16], const Target& t, uint16_t* dst) {
+  stash_block<ROWS_N>(w, t);
+  uint4 x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4*>(t.get + 512 * i);
+#pragma unroll
+  for (int i = 0; i < 4; ++i, dst += t.step) *reinterpret_cast<uint4*>(dst) = x[i];
+  __syncwarp();
 }
 
 // The 4 x 4 words of four neighbouring lanes, transposed: lane q gets word q of each.
@@ -319,32 +319,20 @@ __device__ __forceinline__ void store_regs(uint32_t (&w)[16], uint16_t* out, lon
 
 // A block of which only `rows` rows of `width` elements exist, or whose stores cannot be wide: a row at a
 // time, one element a lane.  out: the block's first element.
-template <bool ROWS_N, int ROWS>
-__device__ __forceinline__ void store_part(const uint32_t (&w)[16], const Target& t, uint8_t* stash, uint16_t* out,
+template <bool ROWS_N>
+__device__ __forceinline__ void store_part(const uint32_t (&w)[16], const Target& t, const uint8_t* stash, uint16_t* out,
                                            long long ld, int rows, int width) {
   const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int r0 = 0; r0 < 32; r0 += ROWS ? ROWS : 32) {
-#pragma unroll
-    for (int i = 0; i < ROWS / 8; ++i) {
-      const int j = r0 / 8 + i;
-      if (ROWS_N)
-        stmatrix4<true>(t.put + 512 * i, w[2 * j], w[2 * j + 1], w[8 + 2 * j], w[9 + 2 * j]);
-      else
-        stmatrix4<false>(t.put + 512 * i, w[(j >> 1) * 8 + (j & 1)], w[(j >> 1) * 8 + 2 + (j & 1)],
-                         w[(j >> 1) * 8 + 4 + (j & 1)], w[(j >> 1) * 8 + 6 + (j & 1)]);
-    }
-    __syncwarp();
-    if (lane < width) {
-      for (int r = 0; r < ROWS && r0 + r < rows; ++r)
-        out[(r0 + r) * ld + lane] = *reinterpret_cast<const uint16_t*>(stash + stash_at(r, lane >> 3) + (lane & 7) * 2);
-    }
-    __syncwarp();
+  stash_block<ROWS_N>(w, t);
+  if (lane < width) {
+    for (int r = 0; r < rows; ++r)
+      out[r * ld + lane] = *reinterpret_cast<const uint16_t*>(stash + stash_at(r, lane >> 3) + (lane & 7) * 2);
   }
+  __syncwarp();
 }
 
-// The finished sums of block cb (32 columns) of a tile.
-template <bool SCALED, int ROWS>
+// The finished sums of block cb (32 columns) of a tile.  SCALED: the Newton-Schulz products; STASH: one slice.
+template <bool SCALED, bool STASH>
 __device__ __forceinline__ void emit(const Unit& u, const Target& t, float (&v)[32], int cb, uint8_t* stash) {
   const int lane = threadIdx.x & 31;
   const int ncount = min(32, u.nn - 32 * cb);
@@ -352,9 +340,9 @@ __device__ __forceinline__ void emit(const Unit& u, const Target& t, float (&v)[
   if (!SCALED) {
     pack_block(v, w, u.out_type == kOutBf16);
     if (t.fast && ncount == 32)
-      store_whole<true, ROWS>(w, t, t.by_n + 4 * cb * t.step);
+      store_whole<true>(w, t, t.by_n + 4 * cb * t.step);
     else if (t.mcount > 0)
-      store_part<true, ROWS>(w, t, stash, static_cast<uint16_t*>(u.out) + (u.orow + 32 * cb) * u.ld + t.m, u.ld, ncount,
+      store_part<true>(w, t, stash, static_cast<uint16_t*>(u.out) + (u.orow + 32 * cb) * u.ld + t.m, u.ld, ncount,
                              t.mcount);
   } else {
     const int n = u.orow + 32 * cb;
@@ -379,7 +367,7 @@ __device__ __forceinline__ void emit(const Unit& u, const Target& t, float (&v)[
     const bool mirror = u.sym && n < t.m;  // a block on the diagonal is its own mirror
     auto store = [&](uint32_t (&x)[16], long long plane) {
       uint16_t* out = static_cast<uint16_t*>(u.out) + plane;
-      if (ROWS == 0) {
+      if (!STASH) {
         if (mirror) {
           uint32_t y[16];
 #pragma unroll
@@ -388,14 +376,14 @@ __device__ __forceinline__ void emit(const Unit& u, const Target& t, float (&v)[
         }
         store_regs<true>(x, out + n * u.ld + t.m, u.ld, ncount, t.mcount, u.vec);
       } else if (whole) {
-        store_whole<true, ROWS>(x, t, t.by_n + plane + 4 * cb * t.step);
-        if (mirror) store_whole<false, ROWS>(x, t, out + (t.m + (lane >> 2)) * u.ld + n + (lane & 3) * 8);
+        store_whole<true>(x, t, t.by_n + plane + 4 * cb * t.step);
+        if (mirror) store_whole<false>(x, t, out + (t.m + (lane >> 2)) * u.ld + n + (lane & 3) * 8);
       } else {
-        store_part<true, ROWS>(x, t, stash, out + n * u.ld + t.m, u.ld, ncount, t.mcount);
-        if (mirror) store_part<false, ROWS>(x, t, stash, out + t.m * u.ld + n, u.ld, t.mcount, ncount);
+        store_part<true>(x, t, stash, out + n * u.ld + t.m, u.ld, ncount, t.mcount);
+        if (mirror) store_part<false>(x, t, stash, out + t.m * u.ld + n, u.ld, t.mcount, ncount);
       }
     };
-    if (ROWS == 0 && u.planes_out == 2) {  // FP16 slices: the second is what the first leaves; both take the sums' registers
+    if (!STASH && u.planes_out == 2) {  // FP16 slices: the second is what the first leaves; both take the sums' registers
       uint32_t l[16];
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
@@ -478,11 +466,12 @@ __device__ __forceinline__ bool load_unit(const Unit& u, uint8_t* sA, uint8_t* s
 }
 
 // The kernel.  Walk deals out the units: Walk::Params are the launch's, setup() runs once for the
-// whole CTA, a Walk of its own in every role gives the pair's units in order (next; again() works
-// the present one out anew), and
-// ready() and, if kReports, stored() / done() are its dependences between units (the producer before a
-// unit's first load, each epilogue thread after its last store, one thread of each CTA when all
-// have stored); gave_up() tells the other pairs that they wait in vain.
+// whole CTA, and a Walk of its own in every role gives the pair's units in order (next; with two
+// slices again() works the present one out anew).  kChained: units depend on one another.  ready()
+// waits for what a unit depends on (the producer, before its first load), stored() and done() report
+// a tile (each epilogue thread after its last store, one thread of each CTA when all have stored),
+// and gave_up() tells the other pairs that they wait in vain.  Otherwise outside() stores what
+// belongs to no unit.
 template <class Walk, int PLANES>
 __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
     product_kernel(const __grid_constant__ typename Walk::Params a) {
@@ -555,9 +544,11 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
       Walk walk(a, table);
       Unit u{};
       while (!*abort_flag && walk.next(u)) {
-        if (!walk.ready(abort_flag)) {
-          if (!*abort_flag) stop_pair(abort_flag, a.status);
-          break;
+        if constexpr (Walk::kChained) {
+          if (!walk.ready(abort_flag)) {
+            if (!*abort_flag) stop_pair(abort_flag, a.status);
+            break;
+          }
         }
         const int kind_b = !u.b_mn ? (u.boxes == 1 ? 0 : 1) : (u.b_4d ? 2 : 3);
         bool ok;
@@ -631,7 +622,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
           ++consumed;
           tc_fence_after();
           const uint32_t ad = a_desc + stage * (R::A_STAGE >> 4), bd = b_desc + stage * (R::B_STAGE >> 4);
-          if (PLANES == 1) {
+          if constexpr (PLANES == 1) {
 #pragma unroll
             for (int kk = 0; kk < KSTEPS; ++kk) {
               umma_pair(d_tmem, ad + kk * a_step, bd + kk * b_step, idesc, kk > 0 ? 1u : in_chunk);
@@ -714,14 +705,14 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
     uint32_t acc = 0, acc_phase = 0, eph = 0, seq = 0;
     bool ok = true;
     Walk walk(a, table);
-    walk.outside(warp - EPI_FIRST);
+    if constexpr (!Walk::kChained) walk.outside(warp - EPI_FIRST);
     Unit u{};
     for (; ok && walk.next(u); ++seq) {
       const int nblocks = ceil_div(u.nn, 32);  // this warp: blocks first, first + COLS, ...
       Target target;
       bool split;
       auto place = [&]() {  // where the tile's blocks go
-        if (PLANES == 2) walk.again(u);
+        if constexpr (PLANES == 2) walk.again(u);
         target = target_of(u, mrow, my_stash);
         split = u.nsplit > 1;
       };
@@ -734,7 +725,8 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
 #pragma unroll
         for (int i = 0; i < RUNS * 32; ++i) run[i >> 5][i & 31] = 0.0f;
       }
-      const int nchunks = PLANES == 1 ? (u.kb1 > u.kb0 ? 1 : 0) : (u.kb1 - u.kb0) * (KSTEPS / a.chunk);
+      int nchunks = u.kb1 > u.kb0;
+      if constexpr (PLANES == 2) nchunks = (u.kb1 - u.kb0) * (KSTEPS / a.chunk);
       for (int ch = 0; ch < nchunks; ++ch) {
         if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&accfull[acc], acc_phase, a.epi_wait_ns, abort_flag))) {
           ok = false;
@@ -769,7 +761,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
             if (split)
               put_part(parts(u.split) + cb * PART_BLOCK, v);
             else
-              emit<Walk::kScaled, R::STASH_ROWS>(u, target, v, cb, my_stash);
+              emit<Walk::kScaled, PLANES == 1>(u, target, v, cb, my_stash);
           }
         }
         if (PLANES == 2 || first >= nblocks) {
@@ -792,7 +784,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
             if (split)
               put_part(parts(u.split) + cb * PART_BLOCK, run[j]);
             else
-              emit<Walk::kScaled, R::STASH_ROWS>(u, target, run[j], cb, my_stash);
+              emit<Walk::kScaled, PLANES == 1>(u, target, run[j], cb, my_stash);
           }
         }
       } else if (nchunks == 0) {  // an empty sum (a group without rows, or with few for this many parts)
@@ -804,7 +796,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
           if (split)
             put_part(parts(u.split) + cb * PART_BLOCK, v);
           else
-            emit<Walk::kScaled, R::STASH_ROWS>(u, target, v, cb, my_stash);
+            emit<Walk::kScaled, PLANES == 1>(u, target, v, cb, my_stash);
         }
       }
       bool finished = true;
@@ -830,24 +822,26 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.0f;
             for (int q = 0; q < u.nsplit; ++q) add_part(parts(q) + cb * PART_BLOCK, v);
-            emit<Walk::kScaled, R::STASH_ROWS>(u, target, v, cb, my_stash);
+            emit<Walk::kScaled, PLANES == 1>(u, target, v, cb, my_stash);
           }
         }
       }
       // The CTA's last warp to have stored its blocks reports the tile, so that a tile is one global
       // atomic a CTA (one a warp: the 1152 of a 2048-wide product held the next one up by 2 us).
-      if (Walk::kReports && finished) {
-        walk.stored();
-        __syncwarp();
-        if (lane == 0) {
-          __threadfence();
-          // A warp can be NACC units ahead of another (the next one needs an accumulator that the other
-          // has yet to hand back), so units in a row count apart.
-          static_assert(NACC + 1 <= 4, "counters of warps_done");
-          if (atomicAdd(&warps_done[seq & 3], 1u) == EPI_WARPS - 1) {
-            warps_done[seq & 3] = 0;
+      if constexpr (Walk::kChained) {
+        if (finished) {
+          walk.stored();
+          __syncwarp();
+          if (lane == 0) {
             __threadfence();
-            walk.done();
+            // A warp can be NACC units ahead of another (the next one needs an accumulator that the other
+            // has yet to hand back), so units in a row count apart.
+            static_assert(NACC + 1 <= 4, "counters of warps_done");
+            if (atomicAdd(&warps_done[seq & 3], 1u) == EPI_WARPS - 1) {
+              warps_done[seq & 3] = 0;
+              __threadfence();
+              walk.done();
+            }
           }
         }
       }
@@ -858,7 +852,10 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0) {
-    if (*abort_flag) Walk::gave_up(a);
+    wait_for_previous();  // no launch ends before the one that it overlapped
+    if constexpr (Walk::kChained) {
+      if (*abort_flag) Walk::gave_up(a);
+    }
     if (!mbar_wait(drain, 0)) {
       *abort_flag = 1;
       atomicExch(a.status, OZ_ETIMEOUT);

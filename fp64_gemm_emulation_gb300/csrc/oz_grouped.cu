@@ -14,6 +14,7 @@ namespace {
 using namespace prod;
 
 constexpr int kMaxParts = 160;  // parts of split tiles the workspace holds: about two a CTA pair
+constexpr int kMaxUnsplit = 64;  // k-blocks of the longest sum that is never split (may_split)
 
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -38,7 +39,7 @@ struct GroupedWalk {
     CUtensorMap tmA, tmB, tmB128;
     int M, N, K;   // contiguous extent of the output; wgrad: its rows; otherwise the sum's length
     int groups, rows, bn, max_parts, part_cols;
-    int a_4d, b_4d, vec, out_type;
+    int a_4d, b_4d, vec, out_type, after;
     uint32_t idesc;
     const int32_t* offsets;
     void* out;
@@ -64,6 +65,9 @@ struct GroupedWalk {
       tma_prefetch_desc(&a.tmB);
       if (!B_MN) tma_prefetch_desc(&a.tmB128);
     }
+    // A product after this one may set itself up on SMs that this one leaves idle; it waits here too.
+    let_next_start();
+    if (a.after) wait_for_previous();
     for (int i = threadIdx.x; i <= a.groups; i += blockDim.x) off[i] = a.offsets[i];
     __syncthreads();
     if (threadIdx.x >= 32) return;
@@ -276,11 +280,14 @@ struct Problem {
 
   int m_out() const { return op == kForward ? n : k; }
   int bn() const { return op == kWgrad && n <= 128 ? 128 : 256; }
-  // A part of the sum has to be worth splitting off; whether tiles are left for a split is known on
-  // the device only.
+  // Whether tiles are left for a split is known on the device only, but parts need arrival counters
+  // that a launch before the product's has to zero, and a rendezvous: 3.5 to 4 us on this side, and no
+  // workspace on the other.  Parts win that back only when a sum is long (one token of 8 experts,
+  // n = 1024, and 512 rows of one, n = 4096; unsplit / split us):
+  //   k 2048: 12.5 / 14.9    k 4096: 20.1 / 22.3, 24.5 / 27.9    k 8192: 20.9 / 16.5, 41.6 / 37.1
   bool may_split() const {
     const int blocks = op == kWgrad ? ceil_div(rows, BK * groups) : ceil_div(op == kForward ? k : n, BK);
-    return blocks > 1;
+    return blocks > kMaxUnsplit;
   }
   int part_cols() const { return op == kWgrad ? bn() : static_cast<int>(roundup(rows < bn() ? rows : bn(), 32)); }
   size_t split_bytes() const {
@@ -331,6 +338,7 @@ int launch_op(const Problem& p, float* part, unsigned* arrivals, const Device& d
   a.ld = p.ldo;
   a.stride = p.strideo;
   a.vec = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.ldo % 8 == 0 && (p.op != kWgrad || p.strideo % 8 == 0);
+  a.after = start == kAfter;
   a.part = part;
   a.arrivals = arrivals;
   const Operand &w = p.w, &t = p.t;
@@ -368,8 +376,8 @@ int run(Problem p, void* workspace, size_t ws_bytes, cudaStream_t stream) {
     if (cudaGetLastError() != cudaSuccess) return OZ_ECUDA;
     ws += p.split_bytes();
   }
-  // The product overlaps zero_kernel, which everything before it on the stream precedes; a repacked
-  // operand it has to wait for.
+  // The product overlaps zero_kernel, which everything before it on the stream precedes; for anything
+  // else before it, a repacked operand or a caller's launch, it waits.
   const Start start = arrivals && p.w.fits() && p.t.fits() ? kOverlap : kAfter;
   if ((rc = repack(p.w, &ws, stream)) || (rc = repack(p.t, &ws, stream))) return rc;
   switch (p.op) {

@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(256) norm_kernel(const void* __restrict__ G, i
                                                    long long ld, long long stride, double* __restrict__ partial,
                                                    unsigned* __restrict__ counters, int ncounters) {
   let_next_start();
+  wait_for_previous();
   if (blockIdx.y == 0)
     for (int i = blockIdx.x * 256 + threadIdx.x; i < ncounters; i += gridDim.x * 256) counters[i] = 0;
   const long long base = blockIdx.y * stride;
@@ -625,24 +626,12 @@ int run(int m, int n, int batch, int dtype, const void* G, int ldg, long long st
   float* scales = reinterpret_cast<float*>(take(sizeof(float) * 2 * OZ_MAX_NS_STEPS * batch));
   const long long xplane = static_cast<long long>(sh.rows) * sh.ldx;
 
-  norm_kernel<<<dim3(sh.norm_blocks, batch), 256, 0, stream>>>(G, dtype, m, n, ldg, stride_g, partial, words, sh.words());
   const long long work = (static_cast<long long>(sh.rows) * (sh.ldx / 8) + 255) / 256;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(work < 1024 ? work : 1024), batch);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, convert_kernel, G, dtype, m, static_cast<long long>(n), static_cast<long long>(ldg), stride_g,
-                         static_cast<const double*>(partial), sh.norm_blocks, eps, plan, X[0], sh.ldx, xplane, slices,
-                         scales) != cudaSuccess) {
-    cudaGetLastError();
+  if (launch_overlapping(norm_kernel, dim3(sh.norm_blocks, batch), 256, 0, stream, G, dtype, m, n, ldg, stride_g, partial, words,
+                         sh.words()) != cudaSuccess ||
+      launch_overlapping(convert_kernel, dim3(static_cast<unsigned>(work < 1024 ? work : 1024), batch), 256, 0, stream, G, dtype, m,
+                         n, ldg, stride_g, partial, sh.norm_blocks, eps, plan, X[0], sh.ldx, xplane, slices, scales) != cudaSuccess)
     return OZ_ECUDA;
-  }
-  if (cudaGetLastError() != cudaSuccess) return OZ_ECUDA;
   return slices == 2 ? run_chain<2>(sh, plan, X, S, B, part, words, scales, O, dtype, ldo, stride_o, dev, stream)
                      : run_chain<1>(sh, plan, X, S, B, part, words, scales, O, dtype, ldo, stride_o, dev, stream);
 }

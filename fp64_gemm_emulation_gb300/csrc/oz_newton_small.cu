@@ -125,6 +125,9 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
     tmem_relinquish();
   }
 
+  let_next_start();
+  wait_for_previous();
+
   // The norm, and X_0.
   if (warp < kEpiWarps) {
     SumSquares s;
@@ -493,8 +496,7 @@ int launch_newton_small(int rows, int cols, int batch, int dtype, const void* G,
       if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return OZ_ECUDA;
       if (dev < 64) set[dev][slices - 1].store(true, std::memory_order_release);
     }
-    kernel<<<batch, kThreads, smem, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_overlapping(kernel, dim3(batch), kThreads, smem, stream, a);
     if (e == cudaSuccess) return OZ_OK;
     if (e != cudaErrorInvalidValue) break;
   }

@@ -460,6 +460,9 @@ def ozaki1_dgemm_ws(A, B, num_slices: int, workspace, C=None, stream=None):
 _DTYPE_CODES: dict = {}
 
 
+_INT_MAX = 2**31 - 1
+
+
 def _dtype(t) -> int:
     if not _DTYPE_CODES:
         import torch
@@ -477,6 +480,8 @@ def _tokens(t, what: str, features: int | None = None) -> int:
     if len(shape) != 2 or (features is not None and shape[1] != features):
         raise ValueError(f"{what} must have shape (rows, {'features' if features is None else features}): {tuple(shape)}")
     cols = shape[1]
+    if max(shape[0], cols, stride[0] if shape[0] > 1 else 0) > _INT_MAX:
+        raise ValueError(f"{what} must have dimensions and a row stride below 2^31")
     if shape[0] <= 1:
         if cols > 1 and stride[1] != 1:
             raise ValueError(f"{what} must be row-major (stride(1) == 1)")
@@ -493,6 +498,8 @@ def _experts(t, what: str) -> tuple[int, int]:
         raise ValueError(f"{what} must have shape (groups, n, k): {tuple(shape)}")
     g, n, k = shape
     ld = max(1, k, stride[1] if n > 1 else 0)
+    if max(ld, n) > _INT_MAX:
+        raise ValueError(f"{what} must have dimensions and a row stride below 2^31")
     if (k > 1 and stride[2] != 1) or (n > 1 and stride[1] < k) or (g > 1 and stride[0] < ld * n):
         raise ValueError(f"{what} must hold row-major matrices that do not overlap")
     return ld, (stride[0] if g > 1 else ld * n)
@@ -665,12 +672,14 @@ def ozaki_newton_schulz(G, steps: int = 5, coeffs=NEWTON_SCHULZ_COEFFS, eps: flo
     if G.dim() < 2 or not G.is_cuda:
         raise ValueError("G must be a CUDA tensor of shape (..., m, n)")
     code = _dtype(G)
-    flat = np.ravel(np.asarray(coeffs, dtype=np.float32))
-    if flat.size == 3:
-        flat = np.tile(flat, max(1, steps))
-    if steps < 1 or flat.size != 3 * steps:
+    try:
+        flat = [float(c) for c in coeffs]
+    except (TypeError, ValueError):  # a sequence of (a, b, c)
+        flat = [float(c) for triple in coeffs for c in triple]
+    if len(flat) == 3:
+        flat *= max(1, steps)
+    if steps < 1 or len(flat) != 3 * steps:
         raise ValueError("coeffs must be one (a, b, c), or one for each of the steps (at least 1)")
-    flat = np.ascontiguousarray(flat)
     if out is None:
         turned = G.dim() == 2 and G.stride(0) == 1 and G.stride(1) != 1
         out = torch.empty((G.shape[1], G.shape[0]), dtype=G.dtype, device=G.device).t() if turned else \
@@ -689,7 +698,7 @@ def ozaki_newton_schulz(G, steps: int = 5, coeffs=NEWTON_SCHULZ_COEFFS, eps: flo
     ldg, sg = _experts(G, "G")
     ldo, so = _experts(out, "out")
     ns = num_slices if num_slices is not None else (1 if code == OZ_BF16 else 2)
-    args = (n, m, batch, code, G.data_ptr(), ldg, sg, out.data_ptr(), ldo, so, steps, flat.ctypes.data, float(eps), int(ns))
+    args = (n, m, batch, code, G.data_ptr(), ldg, sg, out.data_ptr(), ldo, so, steps, (ctypes.c_float * len(flat))(*flat), float(eps), int(ns))
     _run_on("ozaki_newton_schulz", args, workspace, stream, G.device)
     return result
 

@@ -42,8 +42,8 @@ def test_grouped_refuses_bad_arguments(call, bad):
 def test_grouped_refuses_bad_strides_and_null_pointers(call, bad):
     assert call(**bad) == oz.OZ_EINVAL
     # null operands are found before anything is allocated, at sizes that need a workspace too
-    big = dict(n=512, k=512, rows=512, ldw=512, sw=512 * 512)
-    big.update({name: 512 for name in call.__code__.co_varnames[:call.__code__.co_argcount] if name in ("ldx", "ldy", "lddx", "lddy")})
+    big = dict(n=8192, k=8192, rows=16384, ldw=8192, sw=8192 * 8192)
+    big.update({name: 8192 for name in call.__code__.co_varnames[:call.__code__.co_argcount] if name in ("ldx", "ldy", "lddx", "lddy")})
     assert call(**{**big, **bad}) == oz.OZ_EINVAL
 
 
@@ -57,19 +57,20 @@ def test_grouped_empty_problems_do_nothing():
 
 
 def test_grouped_workspace():
-    # one k-block of the sum and 16-byte aligned operands: nothing to split, nothing to lay out
+    # a sum of few k-blocks and 16-byte aligned operands: nothing to split, nothing to lay out
     assert lib.ozaki_grouped_gemm_workspace_bytes(64, 64, 32, 2, oz.OZ_BF16, P, 64, 4096, P, 64) == 0
-    long = lib.ozaki_grouped_gemm_workspace_bytes(64, 1024, 32, 2, oz.OZ_BF16, P, 1024, 65536, P, 1024)
+    assert lib.ozaki_grouped_gemm_workspace_bytes(64, 1024, 32, 2, oz.OZ_BF16, P, 1024, 65536, P, 1024) == 0
+    long = lib.ozaki_grouped_gemm_workspace_bytes(64, 8192, 32, 2, oz.OZ_BF16, P, 8192, 524288, P, 8192)
     assert long > 0
     # an odd row stride of W or X, or an odd address, adds the room to lay it out
-    odd = lib.ozaki_grouped_gemm_workspace_bytes(64, 1024, 32, 2, oz.OZ_BF16, P, 1025, 65600, P, 1024)
-    assert odd >= long + 2 * 2 * 64 * 1024
-    assert lib.ozaki_grouped_gemm_workspace_bytes(64, 1024, 32, 2, oz.OZ_BF16, P, 1024, 65536, P + 2, 1024) >= long + 2 * 32 * 1024
+    odd = lib.ozaki_grouped_gemm_workspace_bytes(64, 8192, 32, 2, oz.OZ_BF16, P, 8193, 524400, P, 8192)
+    assert odd >= long + 2 * 2 * 64 * 8192
+    assert lib.ozaki_grouped_gemm_workspace_bytes(64, 8192, 32, 2, oz.OZ_BF16, P, 8192, 524288, P + 2, 8192) >= long + 2 * 32 * 8192
     assert lib.ozaki_grouped_gemm_workspace_bytes(64, -1, 32, 2, oz.OZ_BF16, P, 1024, 65536, P, 1024) == 0
-    assert lib.ozaki_grouped_gemm_dgrad_workspace_bytes(1024, 64, 32, 2, oz.OZ_F16, P, 64, 65536, P, 1024) > 0
-    assert lib.ozaki_grouped_gemm_wgrad_workspace_bytes(64, 64, 4096, 2, oz.OZ_F16, P, 64, P, 64) > 0
+    assert lib.ozaki_grouped_gemm_dgrad_workspace_bytes(8192, 64, 32, 2, oz.OZ_F16, P, 64, 524288, P, 8192) > 0
+    assert lib.ozaki_grouped_gemm_wgrad_workspace_bytes(64, 64, 16384, 2, oz.OZ_F16, P, 64, P, 64) > 0
     # too small, or not aligned to 256 bytes
-    args = (64, 1024, 32, 2, oz.OZ_BF16, P, 1024, 65536, P, 1024, P, P, 64)
+    args = (64, 8192, 32, 2, oz.OZ_BF16, P, 8192, 524288, P, 8192, P, P, 64)
     assert lib.ozaki_grouped_gemm_ws(*args, P, long - 1, None) == oz.OZ_ENOMEM
     assert lib.ozaki_grouped_gemm_ws(*args, P + 16, long, None) == oz.OZ_ENOMEM
     assert lib.ozaki_grouped_gemm_ws(*args, None, long, None) == oz.OZ_ENOMEM
@@ -135,3 +136,16 @@ def test_the_completed_square_is_the_polynomial():
         A = x @ x.T
         S = A + b / (2 * c) * np.eye(6)
         assert np.allclose(c * S @ S + (a - b * b / (4 * c)) * np.eye(6), a * np.eye(6) + b * A + c * A @ A, atol=1e-12)
+
+
+def test_strides_beyond_an_int_are_refused():
+    torch = pytest.importorskip("torch")
+    far = 2**31
+    assert oz._tokens(torch.empty_strided((1, 8), (far, 1), device="meta"), "X") == 8  # one row: its stride says nothing
+    with pytest.raises(ValueError):
+        oz._tokens(torch.empty_strided((2, 8), (far, 1), device="meta"), "X")
+    with pytest.raises(ValueError):
+        oz._tokens(torch.empty_strided((far, 8), (8, 1), device="meta"), "X")
+    assert oz._experts(torch.empty_strided((2, 4, 8), (far, 8, 1), device="meta"), "W") == (8, far)  # between matrices: 64 bits
+    with pytest.raises(ValueError):
+        oz._experts(torch.empty_strided((2, 4, 8), (4 * far, far, 1), device="meta"), "W")

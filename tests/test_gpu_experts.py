@@ -95,7 +95,7 @@ def test_grouped_rows_outside_every_group_are_zero():
     check_all([40, 0, 300], 192, 320, torch.bfloat16, before=37, after=270)
 
 
-@pytest.mark.parametrize("counts,n,k", [([1], 4096, 8192), ([2, 0, 3], 8192, 2048), ([4000], 128, 64), ([1] * 8, 1024, 2048)])
+@pytest.mark.parametrize("counts,n,k", [([1], 4096, 8192), ([2, 0, 3], 8192, 2048), ([4000], 128, 64), ([1] * 8, 1024, 2048), ([9000], 128, 64), ([40, 0, 300], 700, 8192)])
 def test_grouped_long_sums_are_split(counts, n, k):
     check_all(counts, n, k, torch.bfloat16)
 
@@ -178,8 +178,9 @@ def test_grouped_bad_offsets_are_clamped_and_reported(offsets):
         assert torch.equal(got, call(torch.tensor(fixed, dtype=torch.int32, device="cuda")))
 
 
-def test_grouped_results_repeat_on_any_stream_workspace_and_in_a_graph():
-    counts, n, k = [3, 0, 40, 300], 384, 2048
+# the last two split their sums: the forward product's and the weight gradient's, the input gradient's
+@pytest.mark.parametrize("counts,n,k", [([3, 0, 40, 300], 384, 2048), ([5000, 40, 9000], 320, 8192), ([3, 0, 70], 8192, 320)])
+def test_grouped_results_repeat_on_any_stream_workspace_and_in_a_graph(counts, n, k):
     x, w, dy, o, _ = make(counts, n, k, torch.bfloat16)
     calls = {"f": lambda **kw: oz.ozaki_grouped_gemm(x, w, o, **kw), "d": lambda **kw: oz.ozaki_grouped_gemm_dgrad(dy, w, o, **kw),
              "w": lambda **kw: oz.ozaki_grouped_gemm_wgrad(dy, x, o, **kw)}

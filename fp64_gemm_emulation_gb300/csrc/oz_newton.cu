@@ -215,7 +215,7 @@ struct ChainWalk {
     const unsigned int* count = a.finished + group;
     auto reached = [&]() {
       unsigned int v;
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
+      asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
       return static_cast<int>(v - need) >= 0;
     };
     if (!reached()) {
@@ -228,11 +228,9 @@ struct ChainWalk {
         }
       }
     }
-    asm volatile("fence.proxy.async;" ::: "memory");
+    asm volatile("fence.acq_rel.gpu;\n\tfence.proxy.async;" ::: "memory");
     return true;
   }
-
-  __device__ void stored() const { asm volatile("fence.proxy.async;" ::: "memory"); }
 
   // A CTA has stored its half of a finished tile.
   __device__ void done() const {

@@ -159,6 +159,12 @@ __device__ __forceinline__ void stop_pair(volatile int* abort_flag, int* status)
   atomicExch(status, OZ_ETIMEOUT);
 }
 
+__device__ __forceinline__ uint32_t add_shared_acq_rel(uint32_t* p, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(smem_u32(p)), "r"(v) : "memory");
+  return old;
+}
+
 __device__ __forceinline__ bool warps_meet(uint64_t* bar, uint32_t& phase, const volatile int* abort) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
@@ -471,10 +477,9 @@ __device__ __forceinline__ bool load_unit(const Unit& u, uint8_t* sA, uint8_t* s
 // The kernel.  Walk deals out the units: Walk::Params are the launch's, setup() runs once for the
 // whole CTA, and a Walk of its own in every role gives the pair's units in order (next; with two
 // slices again() works the present one out anew).  kChained: units depend on one another.  ready()
-// waits for what a unit depends on (the producer, before its first load), stored() and done() report
-// a tile (each epilogue thread after its last store, one thread of each CTA when all have stored),
-// and gave_up() tells the other pairs that they wait in vain.  Otherwise outside() stores what
-// belongs to no unit.
+// waits for what a unit depends on (the producer, before its first load), done() reports a tile (one
+// thread of each CTA, when all its warps have stored their blocks), and gave_up() tells the other
+// pairs that they wait in vain.  Otherwise outside() stores what belongs to no unit.
 template <class Walk, int PLANES>
 __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
     product_kernel(const __grid_constant__ typename Walk::Params a) {
@@ -804,20 +809,22 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
       }
       bool finished = true;
       if (split) {
-        // This CTA's part is written; the last of the tile's parts to arrive adds them all.
-        wait_for_previous();  // the arrival counters' zeros may come from a launch that this one overlaps
-        __threadfence();
+        // This CTA's part is written; the last of the tile's parts to arrive adds them all.  One thread's
+        // fences order what all warps wrote before they met, and what they read after they meet again.
         ok = warps_meet(epibar, eph, abort_flag);
-        if (ok && threadIdx.x == EPI_FIRST * 32) *arrived = atomicAdd(&u.arrivals[rank], 1u);
+        if (ok && threadIdx.x == EPI_FIRST * 32) {
+          wait_for_previous();  // the arrival counters' zeros may come from a launch that this one overlaps
+          __threadfence();
+          *arrived = atomicAdd(&u.arrivals[rank], 1u);  // all have read the last one: they met since
+          __threadfence();
+        }
         ok = ok && warps_meet(epibar, eph, abort_flag);
         finished = ok && *arrived == static_cast<uint32_t>(u.nsplit - 1);
-        ok = ok && warps_meet(epibar, eph, abort_flag);  // everyone has read `arrived`
         if (!ok) {
           if (lane == 0 && !*abort_flag) stop_pair(abort_flag, a.status);
           break;
         }
         if (finished) {
-          __threadfence();
           if (threadIdx.x == EPI_FIRST * 32) u.arrivals[rank] = 0;  // as it was found: a later unit may use it
 #pragma unroll 1
           for (int cb = first; cb < nblocks; cb += COLS) {
@@ -829,20 +836,18 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
           }
         }
       }
-      // The CTA's last warp to have stored its blocks reports the tile, so that a tile is one global
-      // atomic a CTA (one a warp: the 1152 of a 2048-wide product held the next one up by 2 us).
+      // The CTA's last warp to have stored its blocks reports the tile, so that a tile is one fence and
+      // one global atomic a CTA (one a warp: the 1152 of a 2048-wide product held the next one up by 2 us).
       if constexpr (Walk::kChained) {
         if (finished) {
-          walk.stored();
           __syncwarp();
           if (lane == 0) {
-            __threadfence();
             // A warp can be NACC units ahead of another (the next one needs an accumulator that the other
             // has yet to hand back), so units in a row count apart.
             static_assert(NACC + 1 <= 4, "counters of warps_done");
-            if (atomicAdd(&warps_done[seq & 3], 1u) == EPI_WARPS - 1) {
+            if (add_shared_acq_rel(&warps_done[seq & 3], 1u) == EPI_WARPS - 1) {
               warps_done[seq & 3] = 0;
-              __threadfence();
+              __threadfence();  // of all warps' stores: they were counted before this
               walk.done();
             }
           }

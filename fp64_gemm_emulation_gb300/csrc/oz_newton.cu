@@ -458,11 +458,15 @@ struct Shape {
   }
 };
 
-// Tile width and parts of the last wave's tiles for one product, by a model of its time in SM
-// cycles: waves x (k-blocks x cycles of a block + a unit's start and drain), and the joining of
-// parts.  Cycles of a block as measured at 8192^2: one slice is bound by what the SM can load
-// (59 bytes a cycle: 558 at 256 columns, 413 at 128, 371 at 64), two slices by the MMAs and their
-// issue; single-step chunks by the epilogue.
+// Tile width and parts of split tiles for one product, by a model of its time in SM cycles.  Cycles
+// of a k-block as measured at 8192^2: one slice is bound by what the SM can load (59 bytes a cycle:
+// 558 at 256 columns, 413 at 128, 371 at 64), two slices by the MMAs and their issue; single-step
+// chunks by the epilogue.
+//   One or two matrices, or a single wave: the waves, the last one's drain, and the joining of parts.
+//   More: the matrices do not wait for one another, so a wave that one product leaves open is filled by
+//     the next one.  A product then costs the larger of its work and its latency (what one matrix
+//     waits), and some of the other; splitting gains nothing.  (Counted in waves as for one matrix / so:
+//     64 x 256 x 1024 bf16 246 / 187 us, 16 x 2048 x 1024 635 / 575, FP32 1940 / 1841.)
 void plan_product(Product& p, int batch, int planes, int chunk, int pairs) {
   const int nkb = ceil_div(p.K, BK);
   double best = 1e30;
@@ -484,14 +488,23 @@ void plan_product(Product& p, int batch, int planes, int chunk, int pairs) {
     // The epilogue of a tile runs under the next tile's MMAs; that of the last one shows.
     const double drain = bn / 64.0 * (planes == 2 ? 800 : p.sym ? 1900 : 1150);
     const int rest = static_cast<int>(all % pairs);
-    const double whole = static_cast<double>(all / pairs) * std::fmax(nkb * block, drain);
+    const bool shared = batch > 2 && all > pairs;  // products share their waves
     for (int s = 1; s <= 16 && s <= nkb; ++s) {
-      if (s > 1 && (rest == 0 || rest * s > kMaxParts)) break;
-      double t = whole + drain + 2500;
-      if (rest) t += ceil_div(rest * s, pairs) * ceil_div(nkb, s) * block;
-      // parts: each wave's are written out, and the last reads them all (1024 x 4096 FP32: one wave of
-      // three parts 379 us, two waves of five 430)
-      if (s > 1) t += 3000 + 2500.0 * (bn / 256.0) * (1 + s) + ceil_div(rest * s, pairs) * (2500 + 16.0 * bn);
+      if (s > 1 && (rest == 0 || rest * s > kMaxParts || shared)) break;
+      const double unit = ceil_div(nkb, s) * block, join = 2500.0 * (bn / 256.0) * (1 + s);
+      double t;
+      if (!shared) {
+        t = static_cast<double>(all / pairs) * std::fmax(nkb * block, drain) + drain + 2500;
+        if (rest) t += ceil_div(rest * s, pairs) * unit;
+        // parts: each wave's are written out, and the last reads them all (1024 x 4096 FP32: one wave of
+        // three parts 379 us, two waves of five 430)
+        if (s > 1) t += 3000 + join + ceil_div(rest * s, pairs) * (2500 + 16.0 * bn);
+      } else {
+        const double step = planes == 2 ? unit + drain + 3000 : std::fmax(unit, drain + 3000);
+        const double work = static_cast<double>(all) / pairs * step;
+        const double latency = ceil_div(q.tiles, pairs) * unit + drain + 3000;
+        t = std::fmax(work, latency) + 0.3 * std::fmin(work, latency);
+      }
       if (t < best) {
         best = t;
         q.nsplit = s;

@@ -74,25 +74,6 @@ __device__ inline void newton_scales(float big, float mid, float small, float ep
   factors[2 * lane + 1] = ldexpf(q, next - t - plan.sb[lane]);
 }
 
-// Launches a kernel that may start while the launch before it ends (it calls wait_for_previous).
-template <class... Params, class... Args>
-cudaError_t launch_overlapping(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
-                               const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
-  if (e != cudaSuccess) cudaGetLastError();
-  return e;
-}
-
 // Matrices that one CTA's shared memory holds (oz_newton_small.cu).
 inline bool newton_is_small(int rows, int cols, int slices) {
   const int side = rows < cols ? rows : cols, lng = rows < cols ? cols : rows;

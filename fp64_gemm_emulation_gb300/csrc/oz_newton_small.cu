@@ -11,7 +11,7 @@
 // B X (N = columns, K = rows), so nothing is rearranged.  S and B share one buffer, and X_{i+1}
 // replaces X_i: a product's sums are all in tensor memory before its operands are overwritten.
 // An accumulator lane is a matrix row, so a thread writes 32 consecutive columns as 16-byte stores.
-//   warps 0-7: epilogue (lanes 32 (warp % 4) .., every second block of 32 columns)   warp 8: MMA
+//   epilogue warps (lanes 32 (warp % 4) .., every second or fourth block of 32 columns), then one for the MMAs
 // Two slices: each MMA step (16 k) is a sum of its own, h l' + l h' first and then h h', added up in
 // FP32 registers (the tensor core's truncation; see oz_newton.cu), through a ring of accumulators.
 // Bound by the latency of a product (MMA, tensor-memory read, stores, two hand-overs).
@@ -28,8 +28,12 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr uint32_t kBlock = kRows * 128;  // 64 columns of 128 rows
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = (kEpiWarps + 1) * 32;
+// One slice: 16 epilogue warps (128 x 512 bf16 57 us; with 8: 71).  Two: 8, whose running sums and
+// hand-overs cost more with 16 (128 x 128 FP32 58 us; with 16: 69).
+template <int SLICES>
+constexpr int kEpiWarpsOf = SLICES == 2 ? 8 : 16;
+template <int SLICES>
+constexpr int kThreadsOf = (kEpiWarpsOf<SLICES> + 1) * 32;
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride, version, 128-byte swizzle
 
 struct SmallArgs {
@@ -86,8 +90,18 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a_low, uint32_t b_low, 
       : "memory");
 }
 
+// The values pass through, so that no use of them moves above the wait before this.
+__device__ __forceinline__ void tie(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 8)
+    asm volatile("" : "+r"(r[e]), "+r"(r[e + 1]), "+r"(r[e + 2]), "+r"(r[e + 3]), "+r"(r[e + 4]), "+r"(r[e + 5]), "+r"(r[e + 6]),
+                      "+r"(r[e + 7]));
+}
+
 template <int SLICES>
-__global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_constant__ SmallArgs a) {
+__global__ void __launch_bounds__(kThreadsOf<SLICES>, 1) newton_small_kernel(const __grid_constant__ SmallArgs a) {
+  constexpr int kEpiWarps = kEpiWarpsOf<SLICES>;
+  constexpr int kCols = kEpiWarps / 4;  // warps that share the blocks of 32 columns of a quadrant
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t accfull[4], accempty[4], ready, drain;
@@ -295,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int quad = warp & 3, half = warp >> 2;
+    const int quad = warp & 3, part = warp >> 2;
     const int row = quad * 32 + lane;
     uint32_t full_bits = 0;
     bool ok = true;
@@ -403,10 +417,11 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
             ok = false;
             break;
           }
-          for (int cb = half; cb < nblocks; cb += 2) {
+          for (int cb = part; cb < nblocks; cb += kCols) {
             uint32_t r[32];
             tmem_ld32(lanes + 32 * cb, r);
             tmem_ld_wait();
+            tie(r);
             float v[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
@@ -426,16 +441,18 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
               }
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const int cb = 2 * j + half;
+                const int cb = kCols * j + part;
                 if (b0 + cb < nblocks) {
                   uint32_t r0[32], r1[32];
                   const uint32_t at = lanes + 256 * buffer + 32 * cb;
                   tmem_ld32(at, r0);
                   if (k + 1 < ks) tmem_ld32(at + 128, r1);
                   tmem_ld_wait();
+                  tie(r0);
 #pragma unroll
                   for (int e = 0; e < 32; ++e) run[j][e] += __uint_as_float(r0[e]);
                   if (k + 1 < ks) {
+                    tie(r1);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) run[j][e] += __uint_as_float(r1[e]);
                   }
@@ -446,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) newton_small_kernel(const __grid_
             if (!ok) break;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              if (b0 + 2 * j + half < nblocks) finish(run[j], b0 + 2 * j + half);
+              if (b0 + kCols * j + part < nblocks) finish(run[j], b0 + kCols * j + part);
           }
           if (!ok) break;
         }
@@ -496,7 +513,7 @@ int launch_newton_small(int rows, int cols, int batch, int dtype, const void* G,
       if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return OZ_ECUDA;
       if (dev < 64) set[dev][slices - 1].store(true, std::memory_order_release);
     }
-    const cudaError_t e = launch_overlapping(kernel, dim3(batch), kThreads, smem, stream, a);
+    const cudaError_t e = launch_overlapping(kernel, dim3(batch), slices == 2 ? kThreadsOf<2> : kThreadsOf<1>, smem, stream, a);
     if (e == cudaSuccess) return OZ_OK;
     if (e != cudaErrorInvalidValue) break;
   }

@@ -752,7 +752,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
               tmem_ld_block(taddr + cb * 32, v);
               tmem_wait_block(v);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) run[j][i] += v[i];
+              for (int i = 0; i < 32; i += 2) add_two(run[j][i], run[j][i + 1], v[i], v[i + 1]);
             }
           }
         } else {

@@ -9,7 +9,7 @@ from fp64_gemm_emulation_gb300 import ozaki as oz
 
 lib = oz._lib
 P = 4096  # an address that is never read: every call below returns before any CUDA call
-MUON = np.tile(np.array(oz.NEWTON_SCHULZ_COEFFS, dtype=np.float32), 5)
+FIVE_STEPS = np.tile(np.array(oz.NEWTON_SCHULZ_COEFFS, dtype=np.float32), 5)
 
 
 def forward(n=8, k=8, rows=8, groups=2, dtype=oz.OZ_BF16, W=P, ldw=8, sw=64, X=P, ldx=8, off=P, Y=P, ldy=8):
@@ -76,7 +76,7 @@ def test_grouped_workspace():
     assert lib.ozaki_grouped_gemm_ws(*args, None, long, None) == oz.OZ_ENOMEM
 
 
-def newton(m=300, n=300, batch=1, dtype=oz.OZ_F32, G=P, ldg=300, sg=90000, O=P, ldo=300, so=90000, steps=5, coeffs=MUON, eps=1e-7, slices=2):
+def newton(m=300, n=300, batch=1, dtype=oz.OZ_F32, G=P, ldg=300, sg=90000, O=P, ldo=300, so=90000, steps=5, coeffs=FIVE_STEPS, eps=1e-7, slices=2):
     c = None if coeffs is None else np.ascontiguousarray(coeffs, dtype=np.float32)
     return lib.ozaki_newton_schulz_ws(m, n, batch, dtype, G, ldg, sg, O, ldo, so, steps, None if c is None else c.ctypes.data,
                                       ctypes.c_float(eps), slices, P, 16, None)

@@ -391,10 +391,11 @@ int launch_op(const Problem& p, float* part, unsigned* arrivals, const Device& d
   } else {
     const uint64_t wm = w.mats > 1 ? 2ull * w.stride : wl * w.rows;
     ok = make_map(&a.tmB, t.p, bf16, t.cols, t.rows, 1, tl, tl * t.rows, Walk::BOX) &&
-         make_map(&a.tmB128, t.p, bf16, t.cols, t.rows, 1, tl, tl * t.rows, HALF_N) &&
+         (p.rows <= HALF_N || make_map(&a.tmB128, t.p, bf16, t.cols, t.rows, 1, tl, tl * t.rows, HALF_N)) &&
          (Walk::A_MN ? make_mn_map(&a.tmA, &a.a_4d, 2, w.p, bf16, w.cols, w.rows, w.mats, wl, wm)
                      : make_map(&a.tmA, w.p, bf16, w.cols, w.rows, w.mats, wl, wm, HALF_M));
   }
+  if (p.rows <= HALF_N) a.tmB128 = a.tmB;  // no tile is that wide
   return ok ? launch<Walk, 1>(a, dev, dev.pairs, start, stream) : OZ_ECUDA;
 }
 

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 import numpy as np
 
@@ -463,6 +464,11 @@ _DTYPE_CODES: dict = {}
 _INT_MAX = 2**31 - 1
 
 
+def _torch():
+    """torch, which whoever passes tensors has imported (an import statement costs more than this lookup)."""
+    return sys.modules["torch"]
+
+
 def _dtype(t) -> int:
     if not _DTYPE_CODES:
         import torch
@@ -506,10 +512,8 @@ def _experts(t, what: str) -> tuple[int, int]:
 
 
 def _offsets(offsets, groups: int | None, device):
-    import torch
-
     n = offsets.numel()
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() or offsets.device != device:
+    if offsets.dtype != _torch().int32 or offsets.dim() != 1 or not offsets.is_contiguous() or offsets.device != device:
         raise ValueError("offsets must be a contiguous int32 vector on the operands' device")
     if n < 2 or (groups is not None and n != groups + 1):
         raise ValueError(f"offsets must hold groups + 1 entries: {n} for {groups} groups")
@@ -520,23 +524,30 @@ def _same(*tensors):
     if device.type != "cuda":
         raise ValueError("operands must be CUDA tensors")
     for t in tensors[1:]:
-        if t.dtype != dtype or t.device != device:
+        if t is not None and (t.dtype != dtype or t.device != device):
             raise ValueError("operands must share one dtype and one device")
+
+
+def _result(out, what: str, rows: int, features: int, like):
+    """(out, its leading dimension): checked, or new."""
+    if out is None:
+        return _torch().empty((rows, features), dtype=like.dtype, device=like.device), max(1, features)
+    ld = _tokens(out, what, features)
+    if out.shape[0] != rows:
+        raise ValueError(f"{what} must have {rows} rows")
+    return out, ld
 
 
 def _stream_of(stream, device) -> int:
     """The raw handle of `stream`, or of the device's current stream."""
-    import torch
-
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return _torch()._C._cuda_getCurrentRawStream(device.index)
     return int(getattr(stream, "cuda_stream", stream))
 
 
 def _run_on(name, args, workspace, stream, device):
     """Calls `name`, or its _ws form when a workspace (a uint8 tensor) is given, on the operands' device."""
-    import torch
-
+    torch = _torch()
     st = _stream_of(stream, device)
     if workspace is not None:
         name += "_ws"
@@ -554,18 +565,12 @@ def ozaki_grouped_gemm(X, W, offsets, Y=None, workspace=None, stream=None):
 
     bfloat16 or float16; row-major (rows of X and Y, and the matrices of W, may be strided).
     Rows outside [offsets[0], offsets[-1]) give zero."""
-    import torch
-
     ldw, sw = _experts(W, "W")
     groups, n, k = W.shape
     ldx, rows, device = _tokens(X, "X", k), X.shape[0], X.device
-    if Y is None:
-        Y = torch.empty((rows, n), dtype=X.dtype, device=device)
     _same(X, W, Y)
     _offsets(offsets, groups, device)
-    ldy = _tokens(Y, "Y", n)
-    if Y.shape[0] != rows:
-        raise ValueError("Y must have the rows of X")
+    Y, ldy = _result(Y, "Y", rows, n, X)
     _run_on("ozaki_grouped_gemm", (n, k, rows, groups, _dtype(X), W.data_ptr(), ldw, sw, X.data_ptr(), ldx,
                                         offsets.data_ptr(), Y.data_ptr(), ldy), workspace, stream, device)
     return Y
@@ -578,18 +583,12 @@ def ozaki_grouped_gemm_ws(X, W, offsets, workspace, Y=None, stream=None):
 
 def ozaki_grouped_gemm_dgrad(dY, W, offsets, dX=None, workspace=None, stream=None):
     """dX[r] = W[e]^T dY[r]: the gradient in X of a loss whose gradient in Y is dY (rows, n)."""
-    import torch
-
     ldw, sw = _experts(W, "W")
     groups, n, k = W.shape
     lddy, rows, device = _tokens(dY, "dY", n), dY.shape[0], dY.device
-    if dX is None:
-        dX = torch.empty((rows, k), dtype=dY.dtype, device=device)
     _same(dY, W, dX)
     _offsets(offsets, groups, device)
-    lddx = _tokens(dX, "dX", k)
-    if dX.shape[0] != rows:
-        raise ValueError("dX must have the rows of dY")
+    dX, lddx = _result(dX, "dX", rows, k, dY)
     _run_on("ozaki_grouped_gemm_dgrad", (n, k, rows, groups, _dtype(dY), W.data_ptr(), ldw, sw, dY.data_ptr(), lddy,
                                               offsets.data_ptr(), dX.data_ptr(), lddx), workspace, stream, device)
     return dX
@@ -602,15 +601,13 @@ def ozaki_grouped_gemm_dgrad_ws(dY, W, offsets, workspace, dX=None, stream=None)
 
 def ozaki_grouped_gemm_wgrad(dY, X, offsets, dW=None, workspace=None, stream=None):
     """dW[e] = sum over the rows r of group e of dY[r] X[r]^T: (groups, n, k)."""
-    import torch
-
     lddy, ldx, device = _tokens(dY, "dY"), _tokens(X, "X"), dY.device
     if X.shape[0] != dY.shape[0]:
         raise ValueError("X and dY must have the same rows")
     _offsets(offsets, None, device)
     groups, n, k, rows = offsets.numel() - 1, dY.shape[1], X.shape[1], X.shape[0]
     if dW is None:
-        dW = torch.empty((groups, n, k), dtype=dY.dtype, device=device)
+        dW = _torch().empty((groups, n, k), dtype=dY.dtype, device=device)
     _same(dY, X, dW)
     ldw, sw = _experts(dW, "dW")
     if tuple(dW.shape) != (groups, n, k):

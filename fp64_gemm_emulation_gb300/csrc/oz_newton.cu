@@ -119,12 +119,6 @@ struct ChainWalk {
     return true;
   }
 
-  // The same unit again, worked out anew, so that nothing of it has to be kept meanwhile.
-  __device__ void again(Unit& u) {
-    asm volatile("" : "+r"(idx));
-    describe(u);
-  }
-
   __device__ void describe(Unit& u) {
     const Product& p = a.prod[kind];
     int tile = idx - base;

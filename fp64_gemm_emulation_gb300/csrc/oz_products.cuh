@@ -61,8 +61,8 @@ struct Ring {
   static constexpr uint32_t A_STAGE = PLANES * A_PLANE;
   static constexpr uint32_t B_STAGE = PLANES == 2 ? 2 * (BN2 / 2) * BK * 2 : HALF_N * BK * 2;
   static constexpr uint32_t BYTES = STAGES * (A_STAGE + B_STAGE);
-  // An epilogue warp's stash: a 32 x 32 block of 16 bits (two slices: no room, store_regs).
-  static constexpr uint32_t WARP_STASH = PLANES == 2 ? 0 : 32 * 64;
+  // An epilogue warp's stash: a 32 x 32 block of 16 bits (two slices: no room, store_regs; the warp's unit).
+  static constexpr uint32_t WARP_STASH = PLANES == 2 ? 256 : 32 * 64;
 };
 
 constexpr long long PART_BLOCK = 32 * HALF_M;  // floats of 32 columns of one CTA's part
@@ -100,6 +100,7 @@ struct Unit {
   int part_cols;
   unsigned int* arrivals;   // [2 CTAs]
 };
+static_assert(sizeof(Unit) <= Ring<2>::WARP_STASH, "the stash holds a unit");
 
 // Time, in k-blocks, of a last, partial wave of `tiles` tiles cut into s parts each: the waves of the
 // parts and the joining (each CTA writes its part and the last one reads all: about 4 k-blocks
@@ -293,37 +294,40 @@ __device__ __forceinline__ void transpose4(uint32_t& a, uint32_t& b, uint32_t& c
 }
 
 // A block without a stash (two slices have no shared memory left): each 8 x 8 of the fragments
-// transposed in registers where rows of n are wanted, and 16 bytes gathered in each lane.
+// transposed in registers where rows of n are wanted, and 16 bytes gathered in each lane.  All
+// of it comes before the first store, so that the latencies of the 32 exchanges overlap.
 // out: the block's first element; rows of `width` elements.  w is used up.
 template <bool ROWS_N>
 __device__ __forceinline__ void store_regs(uint32_t (&w)[16], uint16_t* out, long long ld, int rows, int width, bool vec) {
   const int lane = threadIdx.x & 31, q = 8 * (lane & 3);
+  if (ROWS_N) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(w[i]));
+  }
+  // Rows 8 j + lane / 4: the groups of 8 m, or of 8 n.
+#define OZ_GROUP(j, e) w[ROWS_N ? 8 * ((e) >> 1) + 2 * (j) + ((e) & 1) : 8 * ((j) >> 1) + ((j) & 1) + 2 * (e)]
+#pragma unroll
+  for (int j = 0; j < 4; ++j) transpose4(OZ_GROUP(j, 0), OZ_GROUP(j, 1), OZ_GROUP(j, 2), OZ_GROUP(j, 3));
   uint16_t* dst = out + (lane >> 2) * ld + q;
+  if (vec && rows >= 32 && width >= 32) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j, dst += 8 * ld) {  // rows 8 j + lane / 4
-    uint32_t a, b, c, d;
-    if (ROWS_N) {
-      const uint32_t f[4] = {w[2 * j], w[2 * j + 1], w[8 + 2 * j], w[9 + 2 * j]};  // the groups of 8 m
-      uint32_t g[4];
+    for (int j = 0; j < 4; ++j, dst += 8 * ld)
+      *reinterpret_cast<uint4*>(dst) = make_uint4(OZ_GROUP(j, 0), OZ_GROUP(j, 1), OZ_GROUP(j, 2), OZ_GROUP(j, 3));
+    return;
+  }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(g[i]) : "r"(f[i]));
-      a = g[0], b = g[1], c = g[2], d = g[3];
-    } else {  // the groups of 8 n
-      a = w[(j >> 1) * 8 + (j & 1)], b = w[(j >> 1) * 8 + 2 + (j & 1)];
-      c = w[(j >> 1) * 8 + 4 + (j & 1)], d = w[(j >> 1) * 8 + 6 + (j & 1)];
-    }
-    transpose4(a, b, c, d);
+  for (int j = 0; j < 4; ++j, dst += 8 * ld) {
     if (8 * j + (lane >> 2) < rows) {
       if (vec && q + 8 <= width) {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(a, b, c, d);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(OZ_GROUP(j, 0), OZ_GROUP(j, 1), OZ_GROUP(j, 2), OZ_GROUP(j, 3));
       } else {
-        const uint32_t x[4] = {a, b, c, d};
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (q + e < width) dst[e] = static_cast<uint16_t>(x[e >> 1] >> (16 * (e & 1)));
+          if (q + e < width) dst[e] = static_cast<uint16_t>(OZ_GROUP(j, e >> 1) >> (16 * (e & 1)));
       }
     }
   }
+#undef OZ_GROUP
 }
 
 // A block of which only `rows` rows of `width` elements exist, or whose stores cannot be wide: a row at a
@@ -475,8 +479,8 @@ __device__ __forceinline__ bool load_unit(const Unit& u, uint8_t* sA, uint8_t* s
 }
 
 // The kernel.  Walk deals out the units: Walk::Params are the launch's, setup() runs once for the
-// whole CTA, and a Walk of its own in every role gives the pair's units in order (next; with two
-// slices again() works the present one out anew).  kChained: units depend on one another.  ready()
+// whole CTA, and a Walk of its own in every role gives the pair's units in order (next).  kChained: units
+// depend on one another.  ready()
 // waits for what a unit depends on (the producer, before its first load), done() reports a tile (one
 // thread of each CTA, when all its warps have stored their blocks), and gave_up() tells the other
 // pairs that they wait in vain.  Otherwise outside() stores what belongs to no unit.
@@ -717,17 +721,25 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
     Unit u{};
     for (; ok && walk.next(u); ++seq) {
       const int nblocks = ceil_div(u.nn, 32);  // this warp: blocks first, first + COLS, ...
+      // Two slices: the sums take all registers meanwhile, so the unit waits in shared memory (working it
+      // out anew took 0.8 us a tile).
+      Unit* kept = reinterpret_cast<Unit*>(my_stash);
+      if (PLANES == 2) {
+        __syncwarp();
+        if (lane == 0) *kept = u;
+        __syncwarp();
+      }
       Target target;
       bool split;
       auto place = [&]() {  // where the tile's blocks go
-        if constexpr (PLANES == 2) walk.again(u);
+        if (PLANES == 2) u = *kept;
         target = target_of(u, mrow, my_stash);
         split = u.nsplit > 1;
       };
       auto parts = [&](int q) {  // this thread's values of part q of a split tile
         return u.part + (2ll * q + rank) * u.part_cols * HALF_M + quad * 1024 + lane * 4;
       };
-      if (PLANES == 1) place();  // two slices: after the sums, whose registers it would take
+      if (PLANES == 1) place();
       float run[RUNS][32];  // two slices: the sums of this warp's blocks
       if (PLANES == 2) {
 #pragma unroll

@@ -40,8 +40,9 @@ constexpr int kMaxParts = 160;         // parts of split tiles that a product's 
 //   128 x 128:    1.6e-6 (1 step)  2.3e-6 (2)  3.5e-6 (4)  6.1e-6 (8)   plain FP32: 1.3e-6
 //   8192 x 2048:  1.5e-6 (1)       1.9e-6 (2)  2.9e-6 (4)  5.0e-6 (8)   plain FP32: 4.7e-6
 // and so is the epilogue's work: 4.1, 3.0, 2.6 and 2.4 ms at 8192 x 2048.  One k-block (4 steps) keeps
-// the error below plain FP32's where sums are long; sides up to 128 (here and in
-// oz_newton_small.cu) are bound by latency, so they take single steps (run_chain).
+// the error below plain FP32's where sums are long.  Where the smaller side is at most 128 it does
+// not, but single steps of S^2 alone do: 128 x 300 1.2e-6 and 132 us with single steps everywhere, 1.3e-6 and
+// 108 us so, 2.4e-6 and 101 us with k-blocks (plain FP32: 1.6e-6).
 
 // The products of a step.
 enum Kind { kGram = 0, kSquare = 1, kApply = 2 };
@@ -49,6 +50,7 @@ enum Kind { kGram = 0, kSquare = 1, kApply = 2 };
 struct Product {
   CUtensorMap mapA[2], mapB[2];  // by the parity of the step (which of the two X)
   int M, N, K, bn;
+  int chunk;                     // MMA steps of a sum (two slices)
   int tiles_m, tiles_n, tiles;   // of one matrix (symmetric: those that reach the lower triangle)
   int full, nsplit, units;       // tiles of the batch that are not split, parts of the others, units in all
   int a_mn, b_mn, sym;
@@ -72,7 +74,7 @@ struct ChainWalk {
 
   struct Params {
     Product prod[3];
-    int batch, steps, chunk;
+    int batch, steps;
     void *X[2], *S, *B, *O;
     long long xplane, splane, ldx, lds, ldo, stride_o;
     int out_type, vec_o;
@@ -155,6 +157,7 @@ struct ChainWalk {
     u.nn = min(p.bn, p.N - u.n0);
     const int nkb = ceil_div(p.K, BK);
     u.k0 = 0;
+    u.chunk = p.chunk;
     u.kb0 = nkb * u.split / u.nsplit;
     u.kb1 = nkb * (u.split + 1) / u.nsplit;
     u.a_mn = p.a_mn;
@@ -461,7 +464,7 @@ struct Shape {
 //     the next one.  A product then costs the larger of its work and its latency (what one matrix
 //     waits), and some of the other; splitting gains nothing.  (Counted in waves as for one matrix / so:
 //     64 x 256 x 1024 bf16 246 / 187 us, 16 x 2048 x 1024 635 / 575, FP32 1940 / 1841.)
-void plan_product(Product& p, int batch, int planes, int chunk, int pairs) {
+void plan_product(Product& p, int batch, int planes, int pairs) {
   const int nkb = ceil_div(p.K, BK);
   double best = 1e30;
   Product q = p;
@@ -478,7 +481,7 @@ void plan_product(Product& p, int batch, int planes, int chunk, int pairs) {
     }
     const long long all = static_cast<long long>(q.tiles) * batch;
     double block = planes == 1 ? 310 + bn : 200 + 5.2 * bn;
-    if (planes == 2 && chunk == 1) block = KSTEPS * (300.0 + 2 * bn);
+    if (planes == 2 && p.chunk == 1) block = KSTEPS * (300.0 + 2 * bn);
     // The epilogue of a tile runs under the next tile's MMAs; that of the last one shows.
     const double drain = bn / 64.0 * (planes == 2 ? 800 : p.sym ? 1900 : 1150);
     const int rest = static_cast<int>(all % pairs);
@@ -532,7 +535,6 @@ int run_chain(const Shape& sh, const NewtonPlan& plan, uint16_t* const (&X)[2], 
   const int side = sh.side, long_side = sh.wide ? sh.cols : sh.rows;
   a.batch = sh.batch;
   a.steps = plan.steps;
-  a.chunk = side <= 128 ? 1 : KSTEPS;
   a.X[0] = X[0];
   a.X[1] = X[1];
   a.S = S;
@@ -568,7 +570,8 @@ int run_chain(const Shape& sh, const NewtonPlan& plan, uint16_t* const (&X)[2], 
   long long units = 0;
   for (int i = 0; i < 3; ++i) {
     Product& p = a.prod[i];
-    plan_product(p, sh.batch, PLANES, a.chunk, dev.pairs);
+    p.chunk = i == kSquare && side <= 128 ? 1 : KSTEPS;
+    plan_product(p, sh.batch, PLANES, dev.pairs);
     p.idesc = idesc_base(false, p.a_mn, p.b_mn);
     p.part = part + i * (sh.part_bytes() / sizeof(float));
     p.arrivals = words + i * 2 * kMaxParts;

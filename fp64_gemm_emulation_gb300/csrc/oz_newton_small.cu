@@ -12,10 +12,14 @@
 // replaces X_i: a product's sums are all in tensor memory before its operands are overwritten.
 // An accumulator lane is a matrix row, so a thread writes 32 consecutive columns as 16-byte stores.
 //   epilogue warps (lanes 32 (warp % 4) .., every second or fourth block of 32 columns), then one for the MMAs
-// Two slices: each MMA step (16 k) is a sum of its own, h l' + l h' first and then h h', added up in
-// FP32 registers (the tensor core's truncation; see oz_newton.cu), through a ring of accumulators.
+// Two slices: sums leave the tensor core, which truncates, and are added up in FP32 registers, h l' + l h'
+// before h h'.  S^2 decides the error, so there each MMA step (16 k) is a sum of its own and l l' is kept
+// too; the other products take four steps at a time (100 x 100, five steps, against 64 bits; plain FP32 1.3e-6):
+//   all by single steps, no l l'    1.8e-6  55 us (128 x 256: 87)
+//   four steps but S^2              2.0e-6  49    (72)
+//   and with l l' in S^2            1.6e-6  49    (72)   in all products: 1.6e-6  52 (77)
 // Bound by the latency of a product (MMA, tensor-memory read, stores, two hand-overs): with five steps
-// 128 x 128 bf16 27.5 us, FP32 56 us (58 with single additions of the running sums), 300 of them 55 and 113.
+// 128 x 128 bf16 27.5 us, FP32 50, 300 of them 55 and 103.
 #include <atomic>
 
 #include <cuda_bf16.h>
@@ -217,8 +221,8 @@ __global__ void __launch_bounds__(kThreadsOf<SLICES>, 1) newton_small_kernel(con
   // One product after another: the Gram product, the square (unless c = 0) and B X of each step.
   // With two slices a product is summed 128 columns at a time, so that a thread's running sums stay in
   // registers: the columns of B X do not depend on one another, and those that are done replace X's
-  // while the next are still being summed.  Each k step has an accumulator of its own; two are
-  // handed over together (four of 128 columns).
+  // while the next are still being summed.  Each sum (one k step or four) has an accumulator of its own;
+  // two are handed over together (four of 128 columns).
   const int side_n = (side + 31) / 32 * 32, lng_n = (lng + 31) / 32 * 32;
   auto columns = [&](int kind) { return kind == 2 ? lng_n : side_n; };
   auto k_steps = [&](int kind) { return ((kind == 0 ? lng : side) + 15) / 16; };
@@ -278,13 +282,35 @@ __global__ void __launch_bounds__(kThreadsOf<SLICES>, 1) newton_small_kernel(con
               const uint32_t id = idesc | static_cast<uint32_t>(min(128, n - n0) >> 3) << 17;
               uint32_t ak = a_base, bk = b_base + (n0 >> 6) * (kBlock >> 4);
               int buffer = 0;
-              for (int k = 0; k < ks && ok; k += 4) {
+              // the Gram product and B X: a sum for four steps, the small products first
+              for (int k = 0; k < ks && kind != 1; k += 4) {
+                if ((k & 4) == 0 && !(ok = next_acc(buffer))) break;
+                const uint32_t d = tmem + 256 * buffer + 32 * (k & 4);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  if (k + q < ks) {
+                    mma(d, ak + 2 * q, bk + b_plane + b_step * q, id, q > 0);
+                    mma(d, ak + a_plane + 2 * q, bk + b_step * q, id, 1u);
+                  }
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  if (k + q < ks) mma(d, ak + 2 * q, bk + b_step * q, id, 1u);
+                if ((k & 4) != 0 || k + 4 >= ks) {
+                  umma_commit(&accfull[buffer]);
+                  buffer ^= 1;
+                }
+                ak += kBlock >> 4;
+                bk += 4 * b_step + b_skip;
+              }
+              for (int k = 0; k < ks && kind == 1 && ok; k += 4) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                   if (k + q < ks) {
                     if ((q & 1) == 0 && !(ok = next_acc(buffer))) break;
                     const uint32_t d = tmem + 256 * buffer + 128 * (q & 1);
-                    mma(d, ak, bk + b_plane, id, 0u);
+                    mma(d, ak + a_plane, bk + b_plane, id, 0u);
+                    mma(d, ak, bk + b_plane, id, 1u);
                     mma(d, ak + a_plane, bk, id, 1u);
                     mma(d, ak, bk, id, 1u);
                     if ((q & 1) == 1 || k + q + 1 == ks) {
@@ -323,7 +349,8 @@ __global__ void __launch_bounds__(kThreadsOf<SLICES>, 1) newton_small_kernel(con
     for (int i = 0; i < steps && ok; ++i) {
       for (int kind = 0; kind < 3 && ok; ++kind) {
         if (kind == 1 && !(a.plan.square >> i & 1)) continue;
-        const int nblocks = columns(kind) / 32, ks = k_steps(kind);
+        const int nblocks = columns(kind) / 32;
+        const int sums = kind == 1 ? k_steps(kind) : (k_steps(kind) + 3) / 4;  // two slices
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const bool to_s = kind == 0 && (a.plan.square >> i & 1);
         const float f = kind == 1 ? a.plan.alpha_b[i] : factors[2 * i + (kind == 2 ? 1 : 0)];
@@ -434,7 +461,7 @@ __global__ void __launch_bounds__(kThreadsOf<SLICES>, 1) newton_small_kernel(con
 #pragma unroll
             for (int e = 0; e < 64; ++e) run[e >> 5][e & 31] = 0.0f;
             int buffer = 0;
-            for (int k = 0; k < ks; k += 2, buffer ^= 1) {
+            for (int k = 0; k < sums; k += 2, buffer ^= 1) {
               if (!wait_full(buffer)) {
                 ok = false;
                 break;
@@ -446,12 +473,12 @@ __global__ void __launch_bounds__(kThreadsOf<SLICES>, 1) newton_small_kernel(con
                   uint32_t r0[32], r1[32];
                   const uint32_t at = lanes + 256 * buffer + 32 * cb;
                   tmem_ld32(at, r0);
-                  if (k + 1 < ks) tmem_ld32(at + 128, r1);
+                  if (k + 1 < sums) tmem_ld32(at + 128, r1);
                   tmem_ld_wait();
                   tie(r0);
 #pragma unroll
                   for (int e = 0; e < 32; e += 2) add_two(run[j][e], run[j][e + 1], __uint_as_float(r0[e]), __uint_as_float(r0[e + 1]));
-                  if (k + 1 < ks) {
+                  if (k + 1 < sums) {
                     tie(r1);
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) add_two(run[j][e], run[j][e + 1], __uint_as_float(r1[e]), __uint_as_float(r1[e + 1]));

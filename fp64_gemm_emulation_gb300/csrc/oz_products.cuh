@@ -80,6 +80,7 @@ __host__ __device__ inline int ceil_div(int a, int b) {
 struct Unit {
   int m0, n0, nn, nmma;     // the tile: first m, first row of B, its rows, the MMA's N
   int k0, kb0, kb1;         // k coordinate of k-block 0; the part's k-blocks
+  int chunk;                // two slices: MMA steps summed on the tensor core (1, or KSTEPS: a k-block)
   const CUtensorMap *mapA, *mapB;
   bool a_mn, b_mn;          // MN-major operands ...
   bool a_4d, b_4d;          // ... with a 4-D map, whose box holds the CTA's whole tile
@@ -650,7 +651,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
               d_tmem = tmem_base + acc * ACC_COLS;
               return true;
             };
-            if (a.chunk == KSTEPS) {
+            if (u.chunk == KSTEPS) {
               if (!next_sum()) {
                 ok = false;
                 break;
@@ -746,7 +747,7 @@ __global__ void __launch_bounds__((EPI_FIRST + Walk::kEpiWarps) * 32, 1)
         for (int i = 0; i < RUNS * 32; ++i) run[i >> 5][i & 31] = 0.0f;
       }
       int nchunks = u.kb1 > u.kb0;
-      if constexpr (PLANES == 2) nchunks = (u.kb1 - u.kb0) * (KSTEPS / a.chunk);
+      if (PLANES == 2) nchunks = (u.kb1 - u.kb0) * (u.chunk == 1 ? KSTEPS : 1);
       for (int ch = 0; ch < nchunks; ++ch) {
         if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&accfull[acc], acc_phase, a.epi_wait_ns, abort_flag))) {
           ok = false;

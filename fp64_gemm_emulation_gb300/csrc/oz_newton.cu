@@ -75,6 +75,7 @@ struct ChainWalk {
   struct Params {
     Product prod[3];
     int batch, steps;
+    int scout;                    // a warp runs ahead of the producer (product_kernel)
     void *X[2], *S, *B, *O;
     long long xplane, splane, ldx, lds, ldo, stride_o;
     int out_type, vec_o;
@@ -606,6 +607,7 @@ int run_chain(const Shape& sh, const NewtonPlan& plan, uint16_t* const (&X)[2], 
   if (!ok) return OZ_ECUDA;
   int most = g.units > x.units ? g.units : x.units;
   if (a.square && q.units > most) most = q.units;
+  a.scout = most > dev.pairs;
   return launch<Walk, PLANES>(a, dev, most < dev.pairs ? most : dev.pairs, kCooperative, stream);
 }
 

@@ -12,17 +12,16 @@
 // that a walker deals out (GroupedWalk in oz_grouped.cu, ChainWalk in oz_newton.cu).
 //   warp 0: TMA producer   warp 1: TMEM owner + MMA issuer (leader)   then Walk::kEpiWarps: epilogue
 //   a last one, where units depend on one another: the scout, which looks whether the next ones may start
-//   6 stages of 32 KB (128 x 64 of A and up to 128 x 64 of B in each CTA), with two slices 4 of 52 KB;
-//   two 256-column FP32
-//   accumulators in tensor memory, so a tile's epilogue runs under the next one's MMAs (two
-//   slices: three of 160 columns; with two of 192, each chunk's hand-over to the epilogue and back,
-//   about 840 cycles beside its 930 of work, left the tensor cores idle for a fifth of the time).
+//   6 stages of 32 KB (128 x 64 of A and up to 128 x 64 of B in each CTA), with two slices 4 of 52 KB
+//   two 256-column FP32 accumulators in tensor memory, so that a tile's epilogue runs under the next one's
+//   MMAs (two slices: three of 160 columns; with two of 192, each chunk's hand-over to the epilogue and
+//   back, about 840 cycles beside its 930 of work, left the tensor cores idle for a fifth of the time)
 // What bounds it: one thread issues every MMA and one every copy, so both loops are kept to a few
 // instructions (at 8192^3, descriptors rebuilt for each MMA: 981 TFLOP/s; two descriptor words and
 // one add: 1524; one TMA copy for each operand and stage instead of up to six: 1780).
 //
 // Split k: the tiles that do not fill a last wave of CTA pairs are cut into parts along k
-// (tail_split).  Each part's FP32 sums go to the workspace, and the CTA that arrives last (an
+// (split_cost, or plan_product in oz_newton.cu).  Each part's FP32 sums go to the workspace, and the CTA that arrives last (an
 // atomic counter for each tile and CTA) adds the parts in their order, so results do not depend
 // on timing and nobody waits.
 // Two slices (PLANES == 2): operands are h + l with h, l in FP16.  A chunk (a k-block or one MMA

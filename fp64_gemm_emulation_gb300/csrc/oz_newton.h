@@ -17,13 +17,15 @@ struct NewtonPlan {
   float diag_s[OZ_MAX_NS_STEPS], alpha_b[OZ_MAX_NS_STEPS], diag_b[OZ_MAX_NS_STEPS];
 };
 
-// A sum of squares in three ranges (Blue's method), so that no square over- or underflows.
+// A sum of squares in three ranges (Blue's method), so that no square over- or underflows, and no sum of
+// fewer than 2^37 of them: the squares stay below 2^76, 2^90 and 2^80 (with values up to 2^50 in the middle
+// range, 2^28 of them added up to more than FP32 holds).
 struct SumSquares {
-  float big = 0.0f, mid = 0.0f, small = 0.0f;  // (x 2^-80)^2, x^2, (x 2^90)^2
+  float big = 0.0f, mid = 0.0f, small = 0.0f;  // (x 2^-90)^2, x^2, (x 2^90)^2
   __device__ __forceinline__ void add(float x) {
     const float m = fabsf(x);
-    if (m > 0x1p50f) {
-      const float y = x * 0x1p-80f;
+    if (m > 0x1p45f) {
+      const float y = x * 0x1p-90f;
       big = fmaf(y, y, big);
     } else if (m < 0x1p-50f) {
       const float y = x * 0x1p90f;
@@ -44,8 +46,8 @@ __device__ inline void newton_scales(float big, float mid, float small, float ep
                                      float* factors) {
   const int lane = threadIdx.x & 31;
   // |G|_F = root 2^k, by the largest range that holds anything (with the next one, which may reach into it)
-  const int k = big != 0.0f ? 80 : mid != 0.0f ? 0 : -90;
-  const float root = sqrtf(k > 0 ? big + ldexpf(mid, -160) : k == 0 ? mid + ldexpf(small, -180) : small);
+  const int k = big != 0.0f ? 90 : mid != 0.0f ? 0 : -90;
+  const float root = sqrtf(k > 0 ? big + ldexpf(mid, -180) : k == 0 ? mid + ldexpf(small, -180) : small);
   int e = 0, t0 = 0;
   float r = 0.0f;
   if (isfinite(root) && root > 0.0f) {

@@ -1,0 +1,39 @@
+"""Expert products and Newton-Schulz as programs call them: large values (GPU)."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from fp64_gemm_emulation_gb300 import ozaki as oz
+
+
+@pytest.fixture(autouse=True)
+def clean_status():
+    oz.ozaki_get_device_status()
+    yield
+    assert oz.ozaki_get_device_status() == oz.OZ_OK
+
+
+def randn(*shape, dtype=torch.float32, seed=0):
+    return torch.randn(*shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda").to(dtype)
+
+
+# ------------------------------------------------------------------ the norm's range
+def test_newton_schulz_norm_of_many_large_values():
+    # 2^28 values of 2^50: their squares add up to 2^128.  One step of the polynomial x leaves X_0, here exact.
+    g = torch.randint(0, 2, (64, 1 << 22), device="cuda", dtype=torch.int8,
+                      generator=torch.Generator(device="cuda").manual_seed(0)).to(torch.bfloat16)
+    g.mul_(2.0 ** 51).sub_(2.0 ** 50)
+    got = oz.ozaki_newton_schulz(g, steps=1, coeffs=(1.0, 0.0, 0.0), eps=0.0)
+    assert torch.equal(got, g * 2.0 ** -64)
+
+
+@pytest.mark.parametrize("m,n", [(90, 130), (300, 301)])
+@pytest.mark.parametrize("power", [-120, -90, -50, 44, 45, 46, 50, 80, 120])
+def test_newton_schulz_ranges_of_the_norm(m, n, power):
+    # a power of two only moves values between the norm's ranges: the sums' rounding (2^-22) passes on at most 2^5 fold
+    g = randn(m, n)
+    want = oz.ozaki_newton_schulz(g, eps=0.0)
+    got = oz.ozaki_newton_schulz(g * 2.0 ** power, eps=0.0)
+    assert (got - want).norm() <= 2.0 ** -17 * want.norm()

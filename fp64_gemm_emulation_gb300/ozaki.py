@@ -651,7 +651,11 @@ NEWTON_SCHULZ_COEFFS = (3.4445, -4.7750, 2.0315)
 
 
 def ozaki_newton_schulz_workspace_bytes(m: int, n: int, batch: int = 1, num_slices: int = 2) -> int:
-    return int(_lib.ozaki_newton_schulz_workspace_bytes(m, n, batch, num_slices))
+    """Device workspace of ozaki_newton_schulz_ws for a G of shape (batch, m, n), or (m, n) in either layout.
+
+    (The C query wants the contiguous extent first, whose rows are padded: the larger of both orders serves
+    row-major and column-major matrices.)"""
+    return max(int(_lib.ozaki_newton_schulz_workspace_bytes(a, b, batch, num_slices)) for a, b in ((m, n), (n, m)))
 
 
 def ozaki_newton_schulz(G, steps: int = 5, coeffs=NEWTON_SCHULZ_COEFFS, eps: float = 1e-7, num_slices: int | None = None,

@@ -1,4 +1,4 @@
-"""Expert products and Newton-Schulz as programs call them: large values (GPU)."""
+"""Expert products and Newton-Schulz as programs call them: workspaces, large values (GPU)."""
 import pytest
 import torch
 
@@ -37,3 +37,18 @@ def test_newton_schulz_ranges_of_the_norm(m, n, power):
     want = oz.ozaki_newton_schulz(g, eps=0.0)
     got = oz.ozaki_newton_schulz(g * 2.0 ** power, eps=0.0)
     assert (got - want).norm() <= 2.0 ** -17 * want.norm()
+
+
+# ------------------------------------------------------------------ workspaces
+@pytest.mark.parametrize("slices", [1, 2])
+@pytest.mark.parametrize("m,n", [(4096, 200), (200, 4096), (301, 129), (129, 301), (1001, 999)])
+def test_newton_schulz_runs_in_the_workspace_that_its_shape_asks_for(m, n, slices):
+    g = randn(m, n)
+    ws = torch.empty(oz.ozaki_newton_schulz_workspace_bytes(m, n, 1, slices), dtype=torch.uint8, device="cuda")
+    want = oz.ozaki_newton_schulz(g, num_slices=slices)
+    assert torch.equal(oz.ozaki_newton_schulz_ws(g, ws, num_slices=slices), want)
+    turned = g.t().contiguous().t()
+    assert torch.equal(oz.ozaki_newton_schulz_ws(turned, ws, num_slices=slices), oz.ozaki_newton_schulz(turned, num_slices=slices))
+    three = torch.stack([g, 2 * g, g])
+    ws = torch.empty(oz.ozaki_newton_schulz_workspace_bytes(m, n, 3, slices), dtype=torch.uint8, device="cuda")
+    assert torch.equal(oz.ozaki_newton_schulz_ws(three, ws, num_slices=slices), oz.ozaki_newton_schulz(three, num_slices=slices))

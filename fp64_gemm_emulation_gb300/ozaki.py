@@ -664,7 +664,7 @@ def ozaki_newton_schulz(G, steps: int = 5, coeffs=NEWTON_SCHULZ_COEFFS, eps: flo
     `steps` times X <- a X + (b A + c A^2) X with A = X X^T (on the smaller side).
 
     G is bfloat16, float16 or float32; its matrices are row-major (2-D and 3-D G may have strided
-    rows, a 2-D G may be column-major).  coeffs: one (a, b, c) for every step, or one for each.
+    rows, a 2-D G may be column-major if out is too).  coeffs: one (a, b, c) for every step, or one for each.
     num_slices: FP16 slices of the intermediate matrices; by default 1 for bfloat16 (11 bits kept) and
     2 otherwise (22 bits).  `out` has G's shape and dtype; by default it is new and row-major
     (column-major for a column-major G)."""
@@ -689,8 +689,10 @@ def ozaki_newton_schulz(G, steps: int = 5, coeffs=NEWTON_SCHULZ_COEFFS, eps: flo
         raise ValueError("out must have G's shape, dtype and device")
     m, n = G.shape[-2:]
     lead, result = G.shape[:-2], out
-    if G.dim() == 2 and m > 1 and n > 1 and G.stride(0) == 1 and out.stride(0) == 1:
-        G, out, m, n = G.t(), out.t(), n, m  # the transposed problem is the same one
+    # The transposed problem is the same one.  (One row has no row stride to go by, only its elements'.)
+    turn = (G.stride(0) == 1 and out.stride(0) == 1) if m > 1 else (G.stride(1) != 1 or out.stride(1) != 1)
+    if G.dim() == 2 and n > 1 and turn:
+        G, out, m, n = G.t(), out.t(), n, m
     batch = 1
     for d in lead:
         batch *= d

@@ -1,4 +1,4 @@
-"""Expert products and Newton-Schulz as programs call them: workspaces, large values (GPU)."""
+"""Expert products and Newton-Schulz as programs call them: workspaces, layouts, large values (GPU)."""
 import pytest
 import torch
 
@@ -52,3 +52,19 @@ def test_newton_schulz_runs_in_the_workspace_that_its_shape_asks_for(m, n, slice
     three = torch.stack([g, 2 * g, g])
     ws = torch.empty(oz.ozaki_newton_schulz_workspace_bytes(m, n, 3, slices), dtype=torch.uint8, device="cuda")
     assert torch.equal(oz.ozaki_newton_schulz_ws(three, ws, num_slices=slices), oz.ozaki_newton_schulz(three, num_slices=slices))
+
+
+# ------------------------------------------------------------------ layouts
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [1, 7, 300])
+def test_newton_schulz_one_row_of_a_column_major_matrix(n, dtype):
+    # the norm's sum has another order: an ulp of bfloat16, and of FP32 after five steps a few
+    ulp = {torch.bfloat16: 2.0 ** -7, torch.float32: 2.0 ** -19}[dtype]
+    row = randn(n, 12, dtype=dtype)[:, 3:4].t()  # (1, n), its elements 12 apart
+    want = oz.ozaki_newton_schulz(row.contiguous())
+    assert ((oz.ozaki_newton_schulz(row) - want).abs() <= ulp * want.abs()).all()
+    out = torch.zeros(n, 5, dtype=dtype, device="cuda")
+    for g in (row, row.contiguous()):  # and into one
+        out.zero_()
+        oz.ozaki_newton_schulz(g, out=out[:, 2:3].t())
+        assert ((out[:, 2:3].t() - want).abs() <= ulp * want.abs()).all() and (out[:, [0, 1, 3, 4]] == 0).all()

@@ -3,7 +3,10 @@
 The functions carry the C ABI's names (``include/ozaki.h``).  Device operands are
 torch CUDA tensors; matrices are column-major float64 (a tensor ``X`` of shape
 (rows, cols) with ``X.stride(0) == 1``; :func:`colmajor` makes one).  Calls are
-ordered on the current torch CUDA stream unless ``stream`` is given.
+ordered on the current torch CUDA stream unless ``stream`` (a torch stream or a raw handle) is
+given.  Such a call is what it would be inside ``with torch.cuda.stream(stream)``: the caller
+sees to it that the operands are ready there, and new results are memory of that stream.  The
+operands' memory is kept until the stream has done the call's work, so the stream has to outlive them.
 
 There is no fallback: if ``libozaki.so`` is missing or fails to load, importing
 this module raises, and every call reports the library's status code as an
@@ -12,6 +15,7 @@ exception.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import sys
 
@@ -122,6 +126,55 @@ def _stream(stream):
     return int(getattr(stream, "cuda_stream", stream))
 
 
+def _other_stream(stream, device):
+    """`stream` as a torch stream, or None where it is (or stands for) the device's current one."""
+    if stream is None or device.type != "cuda":
+        return None
+    torch = _torch()
+    handle = int(getattr(stream, "cuda_stream", stream))
+    if handle == torch._C._cuda_getCurrentRawStream(device.index):
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+
+
+def _call_on(stream, fn, *operands, **named):
+    """fn on another stream than the current one: what it allocates comes from that stream's memory (a block of the
+    current stream's may still be in use there), and the operands' blocks are not handed out again before
+    that stream has done with them."""
+    torch = _torch()
+    with torch.cuda.stream(stream):
+        result = fn(*operands, **named)
+    for t in (*operands, *named.values()):
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    return result
+
+
+def _on_given_stream(fn):
+    """A function whose last parameter is the stream, able to run on one that is not the current one."""
+    last = fn.__code__.co_argcount - 1
+
+    @functools.wraps(fn)
+    def call(*args, **named):
+        stream = args[last] if len(args) > last else named.get("stream")
+        if stream is not None:
+            device = next((t.device for t in (*args, *named.values()) if isinstance(t, _torch().Tensor)), None)
+            other = device and _other_stream(stream, device)
+            if other:
+                named.pop("stream", None)
+                return _call_on(other, fn, *args[:last], **named)
+        return fn(*args, **named)
+
+    return call
+
+
+def _torch():
+    """torch, which whoever passes tensors has imported (an import statement costs more than this lookup)."""
+    return sys.modules["torch"]
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -160,6 +213,7 @@ def ozaki2_workspace_bytes(m: int, n: int, k: int, num_moduli: int) -> int:
 
 
 # ------------------------------------------------------------------ steps
+@_on_given_stream
 def ozaki2_exponents(A, B, stream=None):
     """Step a1: (rowexp[m], colexp[n]) int32 tensors on A's device."""
     import torch
@@ -173,6 +227,7 @@ def ozaki2_exponents(A, B, stream=None):
     return rowexp, colexp
 
 
+@_on_given_stream
 def ozaki2_split(A, B, num_moduli: int, rowexp, colexp, stream=None):
     """Step a2: bf16-bit residue planes (uint16 views as int16 tensors) [s, Mp, Kp] and [s, Np, Kp]."""
     import torch
@@ -187,6 +242,7 @@ def ozaki2_split(A, B, num_moduli: int, rowexp, colexp, stream=None):
     return Ap, Bp
 
 
+@_on_given_stream
 def ozaki2_scale_split(A, B, num_moduli: int, stream=None):
     """Steps a1 + a2 in one call: (rowexp, colexp, A_planes, B_planes); either operand may be None."""
     import torch
@@ -206,6 +262,7 @@ def ozaki2_scale_split(A, B, num_moduli: int, stream=None):
     return rowexp, colexp, Ap, Bp
 
 
+@_on_given_stream
 def ozaki2_residue_gemm(m: int, n: int, k: int, num_moduli: int, A_planes, B_planes, stream=None):
     """Steps a3+a4: C_res uint8 tensor [s, Np, Mp] with C''_t = (A'_t B'_t) mod m_t."""
     import torch
@@ -217,6 +274,7 @@ def ozaki2_residue_gemm(m: int, n: int, k: int, num_moduli: int, A_planes, B_pla
     return Cr
 
 
+@_on_given_stream
 def ozaki2_crt(m: int, n: int, k: int, num_moduli: int, C_res, rowexp, colexp, C=None, stream=None):
     """Steps a5+a6: C (m x n column-major float64)."""
     import torch
@@ -229,6 +287,7 @@ def ozaki2_crt(m: int, n: int, k: int, num_moduli: int, C_res, rowexp, colexp, C
 
 
 # ------------------------------------------------------------------ composed
+@_on_given_stream
 def ozaki2_dgemm(A, B, num_moduli: int = 14, C=None, stream=None):
     """C = A B by Ozaki Scheme II (stream-ordered workspace allocation inside the library)."""
     import torch
@@ -242,6 +301,7 @@ def ozaki2_dgemm(A, B, num_moduli: int = 14, C=None, stream=None):
     return C
 
 
+@_on_given_stream
 def ozaki2_dgemm_ws(A, B, num_moduli: int, workspace, C=None, stream=None):
     """C = A B using a caller-owned device workspace (a uint8 tensor of at least
     ozaki2_workspace_bytes(m, n, k, num_moduli) bytes)."""
@@ -257,6 +317,7 @@ def ozaki2_dgemm_ws(A, B, num_moduli: int, workspace, C=None, stream=None):
     return C
 
 
+@_on_given_stream
 def ozaki2_dgemm_noalloc(A, B, num_moduli: int = 14, C=None, stream=None):
     """C = A B without any device allocation: the library's fixed 64 MiB scratch buffer
     holds the workspace (for callers that cannot allocate; see include/ozaki.h)."""
@@ -309,6 +370,7 @@ def ozaki2_workspace_bytes_ex(m: int, n: int, k: int, num_moduli: int, scaling="
     return int(_lib.ozaki2_workspace_bytes_ex(m, n, k, num_moduli, _scaling(scaling)))
 
 
+@_on_given_stream
 def ozaki2_exponents_ex(A, B, num_moduli: int, scaling="uniform", stream=None):
     """Step a1 in a scaling mode: (rowexp[m], colexp[n]) int32 tensors."""
     import torch
@@ -325,6 +387,7 @@ def ozaki2_exponents_ex(A, B, num_moduli: int, scaling="uniform", stream=None):
     return rowexp, colexp
 
 
+@_on_given_stream
 def ozaki2_split_ex(A, B, num_moduli: int, rowexp, colexp, scaling="uniform", stream=None):
     """Step a2 for exponents of a scaling mode (planes as in ozaki2_split)."""
     import torch
@@ -339,6 +402,7 @@ def ozaki2_split_ex(A, B, num_moduli: int, rowexp, colexp, scaling="uniform", st
     return Ap, Bp
 
 
+@_on_given_stream
 def ozaki2_crt_ex(m: int, n: int, k: int, num_moduli: int, C_res, rowexp, colexp, scaling="uniform", C=None,
                   stream=None):
     """Steps a5+a6 for exponents of a scaling mode."""
@@ -351,6 +415,7 @@ def ozaki2_crt_ex(m: int, n: int, k: int, num_moduli: int, C_res, rowexp, colexp
     return C
 
 
+@_on_given_stream
 def ozaki2_dgemm_ex(A, B, num_moduli: int = 14, scaling="uniform", C=None, workspace=None, stream=None):
     """C = A B by Ozaki Scheme II in a scaling mode ("uniform", "fast", "accu");
     with ``workspace`` (uint8 tensor of ozaki2_workspace_bytes_ex bytes) the _ws form."""
@@ -371,6 +436,7 @@ def ozaki2_dgemm_ex(A, B, num_moduli: int = 14, scaling="uniform", C=None, works
     return C
 
 
+@_on_given_stream
 def ozaki2_dgemm_ex_ws(A, B, num_moduli: int, scaling, workspace, C=None, stream=None):
     """C = A B in a scaling mode with a caller-owned workspace (ozaki2_workspace_bytes_ex bytes)."""
     return ozaki2_dgemm_ex(A, B, num_moduli, scaling, C=C, workspace=workspace, stream=stream)
@@ -391,6 +457,7 @@ def ozaki1_workspace_bytes(m: int, n: int, k: int, num_slices: int) -> int:
     return int(_lib.ozaki1_workspace_bytes(m, n, k, num_slices))
 
 
+@_on_given_stream
 def ozaki1_split(A, B, num_slices: int, stream=None):
     """RN split: (A_planes [s,Mp,Kp], B_planes [s,Np,Kp] as int16 bf16 bits, A_exps [s,m], B_exps [s,n])."""
     import torch
@@ -410,6 +477,7 @@ def ozaki1_split(A, B, num_slices: int, stream=None):
     return Ap, Bp, Ae, Be
 
 
+@_on_given_stream
 def ozaki1_slice_gemm(m: int, n: int, k: int, num_slices: int, A_planes, B_planes, stream=None):
     """Exact INT32 products [s(s+1)/2, Np, Mp] of the slice pairs (i outer, j inner)."""
     import torch
@@ -421,6 +489,7 @@ def ozaki1_slice_gemm(m: int, n: int, k: int, num_slices: int, A_planes, B_plane
     return P
 
 
+@_on_given_stream
 def ozaki1_accumulate(m: int, n: int, k: int, num_slices: int, products, A_exps, B_exps, C=None, stream=None):
     import torch
 
@@ -431,6 +500,7 @@ def ozaki1_accumulate(m: int, n: int, k: int, num_slices: int, products, A_exps,
     return C
 
 
+@_on_given_stream
 def ozaki1_dgemm(A, B, num_slices: int = 7, C=None, stream=None):
     """C = A B by Ozaki Scheme I (stream-ordered workspace inside the library)."""
     import torch
@@ -444,6 +514,7 @@ def ozaki1_dgemm(A, B, num_slices: int = 7, C=None, stream=None):
     return C
 
 
+@_on_given_stream
 def ozaki1_dgemm_ws(A, B, num_slices: int, workspace, C=None, stream=None):
     import torch
 
@@ -462,11 +533,6 @@ _DTYPE_CODES: dict = {}
 
 
 _INT_MAX = 2**31 - 1
-
-
-def _torch():
-    """torch, which whoever passes tensors has imported (an import statement costs more than this lookup)."""
-    return sys.modules["torch"]
 
 
 def _dtype(t) -> int:
@@ -565,6 +631,8 @@ def ozaki_grouped_gemm(X, W, offsets, Y=None, workspace=None, stream=None):
 
     bfloat16 or float16; row-major (rows of X and Y, and the matrices of W, may be strided).
     Rows outside [offsets[0], offsets[-1]) give zero."""
+    if stream is not None and (other := _other_stream(stream, X.device)):
+        return _call_on(other, ozaki_grouped_gemm, X, W, offsets, Y, workspace)
     ldw, sw = _experts(W, "W")
     groups, n, k = W.shape
     ldx, rows, device = _tokens(X, "X", k), X.shape[0], X.device
@@ -583,6 +651,8 @@ def ozaki_grouped_gemm_ws(X, W, offsets, workspace, Y=None, stream=None):
 
 def ozaki_grouped_gemm_dgrad(dY, W, offsets, dX=None, workspace=None, stream=None):
     """dX[r] = W[e]^T dY[r]: the gradient in X of a loss whose gradient in Y is dY (rows, n)."""
+    if stream is not None and (other := _other_stream(stream, dY.device)):
+        return _call_on(other, ozaki_grouped_gemm_dgrad, dY, W, offsets, dX, workspace)
     ldw, sw = _experts(W, "W")
     groups, n, k = W.shape
     lddy, rows, device = _tokens(dY, "dY", n), dY.shape[0], dY.device
@@ -601,6 +671,8 @@ def ozaki_grouped_gemm_dgrad_ws(dY, W, offsets, workspace, dX=None, stream=None)
 
 def ozaki_grouped_gemm_wgrad(dY, X, offsets, dW=None, workspace=None, stream=None):
     """dW[e] = sum over the rows r of group e of dY[r] X[r]^T: (groups, n, k)."""
+    if stream is not None and (other := _other_stream(stream, dY.device)):
+        return _call_on(other, ozaki_grouped_gemm_wgrad, dY, X, offsets, dW, workspace)
     lddy, ldx, device = _tokens(dY, "dY"), _tokens(X, "X"), dY.device
     if X.shape[0] != dY.shape[0]:
         raise ValueError("X and dY must have the same rows")
@@ -672,6 +744,8 @@ def ozaki_newton_schulz(G, steps: int = 5, coeffs=NEWTON_SCHULZ_COEFFS, eps: flo
 
     if G.dim() < 2 or not G.is_cuda:
         raise ValueError("G must be a CUDA tensor of shape (..., m, n)")
+    if stream is not None and (other := _other_stream(stream, G.device)):
+        return _call_on(other, ozaki_newton_schulz, G, steps, coeffs, eps, num_slices, out, workspace)
     code = _dtype(G)
     try:
         flat = [float(c) for c in coeffs]
@@ -736,6 +810,7 @@ def ozaki1_workspace_bytes_ex(m: int, n: int, k: int, num_slices: int, variant="
     return int(_lib.ozaki1_workspace_bytes_ex(m, n, k, num_slices, _variant(variant)))
 
 
+@_on_given_stream
 def ozaki1_split_ex(A, B, num_slices: int, variant="rn", stream=None):
     """Split of a variant: (A_planes, B_planes, A_exps, B_exps) as ozaki1_split."""
     import torch
@@ -756,6 +831,7 @@ def ozaki1_split_ex(A, B, num_slices: int, variant="rn", stream=None):
     return Ap, Bp, Ae, Be
 
 
+@_on_given_stream
 def ozaki1_slice_gemm_ex(m: int, n: int, k: int, num_slices: int, variant, A_planes, B_planes, stream=None):
     """Exact INT32 pair products of a variant, in its order: [s(s+1)/2, Np, Mp]."""
     import torch
@@ -768,6 +844,7 @@ def ozaki1_slice_gemm_ex(m: int, n: int, k: int, num_slices: int, variant, A_pla
     return P
 
 
+@_on_given_stream
 def ozaki1_accumulate_ex(m: int, n: int, k: int, num_slices: int, variant, products, A_exps, B_exps, C=None,
                          stream=None):
     import torch
@@ -779,6 +856,7 @@ def ozaki1_accumulate_ex(m: int, n: int, k: int, num_slices: int, variant, produ
     return C
 
 
+@_on_given_stream
 def ozaki1_dgemm_ex(A, B, num_slices: int = 7, variant="rn", C=None, workspace=None, stream=None):
     """C = A B by Scheme I in a variant ("rn", "ef", "hybrid"); with ``workspace`` the _ws form."""
     import torch
@@ -798,6 +876,7 @@ def ozaki1_dgemm_ex(A, B, num_slices: int = 7, variant="rn", C=None, workspace=N
     return C
 
 
+@_on_given_stream
 def ozaki1_dgemm_ex_ws(A, B, num_slices: int, variant, workspace, C=None, stream=None):
     return ozaki1_dgemm_ex(A, B, num_slices, variant, C=C, workspace=workspace, stream=stream)
 

@@ -1,4 +1,4 @@
-"""Expert products and Newton-Schulz as programs call them: workspaces, layouts, large values (GPU)."""
+"""Expert products and Newton-Schulz as programs call them: streams, workspaces, layouts, large values (GPU)."""
 import pytest
 import torch
 
@@ -68,3 +68,78 @@ def test_newton_schulz_one_row_of_a_column_major_matrix(n, dtype):
         out.zero_()
         oz.ozaki_newton_schulz(g, out=out[:, 2:3].t())
         assert ((out[:, 2:3].t() - want).abs() <= ulp * want.abs()).all() and (out[:, [0, 1, 3, 4]] == 0).all()
+
+
+# ------------------------------------------------------------------ streams other than the current one
+def operators():
+    """name -> (operands, call); results of a few MB, so that the allocator's blocks are theirs alone."""
+    rows, n, k = 1900, 1500, 1100
+    x, w, dy = (randn(*s, dtype=torch.bfloat16, seed=i) for i, s in enumerate(((rows, k), (3, n, k), (rows, n))))
+    o = torch.tensor([0, 700, 700, 1900], dtype=torch.int32, device="cuda")
+    a, b = (oz.colmajor(randn(700, 900, dtype=torch.float64, seed=5)), oz.colmajor(randn(900, 800, dtype=torch.float64, seed=6)))
+    return {
+        "forward": ([x, w, o], oz.ozaki_grouped_gemm),
+        "dgrad": ([dy, w, o], oz.ozaki_grouped_gemm_dgrad),
+        "wgrad": ([dy, x, o], oz.ozaki_grouped_gemm_wgrad),
+        "newton": ([x], oz.ozaki_newton_schulz),
+        "newton small": ([randn(300, 100, 100)], oz.ozaki_newton_schulz),
+        "scheme 2": ([a, b], lambda a, b, **kw: oz.ozaki2_dgemm(a, b, 14, **kw)),
+        "scheme 2 scaled": ([a, b], lambda a, b, **kw: oz.ozaki2_dgemm_ex(a, b, 14, "accu", **kw)),
+        "scheme 1": ([a, b], lambda a, b, **kw: oz.ozaki1_dgemm(a, b, 7, **kw)),
+    }
+
+
+NAMES = ["forward", "dgrad", "wgrad", "newton", "newton small", "scheme 2", "scheme 2 scaled", "scheme 1"]
+
+
+def handles(side):
+    return {"stream": side, "handle": side.cuda_stream}
+
+
+@pytest.mark.parametrize("form", ["stream", "handle"])
+@pytest.mark.parametrize("name", NAMES)
+def test_results_for_another_stream_are_not_the_current_streams_memory(name, form):
+    # the block that a result of this size would get on the current stream, where work may still use it
+    operands, call = operators()[name]
+    first = call(*operands)
+    want, block = first.clone(), first.data_ptr()
+    torch.cuda.synchronize()
+    del first
+    side = torch.cuda.Stream()
+    got = call(*operands, stream=handles(side)[form])
+    side.synchronize()
+    assert torch.equal(got, want)
+    assert got.data_ptr() != block
+
+
+@pytest.mark.parametrize("form", ["stream", "handle"])
+@pytest.mark.parametrize("name", NAMES)
+def test_operands_are_kept_until_another_stream_is_done(name, form):
+    operands, call = operators()[name]
+    want = call(*operands)
+    copies = [t.clone() if t.stride(-1) == 1 or t.dim() != 2 else oz.colmajor(t.t().clone().t()) for t in operands]
+    blocks = {t.data_ptr() for t in copies if t.numel() > 1 << 16}
+    sizes = [t.numel() * t.element_size() for t in copies if t.numel() > 1 << 16]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(1_000_000_000)  # about half a second
+    got = call(*copies, stream=handles(side)[form])
+    del copies
+    again = [torch.empty(s, dtype=torch.uint8, device="cuda") for s in sizes]  # never written
+    reused = blocks & {t.data_ptr() for t in again}
+    side.synchronize()
+    assert not reused
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_the_default_stream_named_from_another_one(name):
+    operands, call = operators()[name]
+    want = call(*operands)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = call(*operands, stream=0)
+        named = call(*operands, stream=torch.cuda.default_stream())
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(named, want)

@@ -144,6 +144,9 @@ __global__ void __launch_bounds__(kThreadsOf<SLICES>, 1) newton_small_kernel(con
     tmem_relinquish();
   }
 
+  // The next launch may start once every CTA of this one holds its tensor memory: one of that launch's that
+  // got an SM's columns first would wait for this launch, and this one for the columns.
+  __syncthreads();
   let_next_start();
   wait_for_previous();
 

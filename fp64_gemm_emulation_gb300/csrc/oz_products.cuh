@@ -995,6 +995,9 @@ int launch(typename Walk::Params a, const Device& d, int pairs, Start start, cud
   auto kernel = product_kernel<Walk, PLANES>;
   constexpr size_t smem = 1024 /*alignment*/ + Ring<PLANES>::BYTES + Walk::kEpiWarps * Ring<PLANES>::WARP_STASH + 256 /*barriers*/ + Walk::kTableBytes;
   static_assert(smem <= 232448, "shared memory budget");
+  // No other kernel that holds tensor memory fits beside this one on an SM (the smallest takes two blocks of
+  // 16 KB, newton_small_kernel), so a launch that starts early cannot take the columns this one is waiting for.
+  static_assert(smem + 2 * 16384 > 232448, "alone on its SM");
   a.status = d.status;
   a.epi_wait_ns = epilogue_wait_ns();
   cudaLaunchConfig_t cfg = {};

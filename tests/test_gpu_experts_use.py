@@ -143,3 +143,16 @@ def test_the_default_stream_named_from_another_one(name):
         named = call(*operands, stream=torch.cuda.default_stream())
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(named, want)
+
+
+# ------------------------------------------------------------------ launches that overlap
+def test_overlapping_launches_of_small_matrices():
+    # more matrices than SMs, one launch after another, of kernels that each hold all tensor memory of their SM
+    sets = [(randn(400, 64, 64, seed=1), s) for s in (1, 2)] + [(randn(500, 16, 40, seed=2), s) for s in (1, 2)]
+    want = []
+    for g, s in sets:
+        want.append(oz.ozaki_newton_schulz(g, num_slices=s))
+        torch.cuda.synchronize()
+    got = [[oz.ozaki_newton_schulz(g, num_slices=s) for g, s in sets] for _ in range(10)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for row in got for a, b in zip(row, want))

@@ -616,6 +616,8 @@ def _run_on(name, args, workspace, stream, device):
     torch = _torch()
     st = _stream_of(stream, device)
     if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the operands' device")
         name += "_ws"
         args += (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     if device.index == torch._C._cuda_getDevice():

@@ -54,6 +54,18 @@ def test_newton_schulz_runs_in_the_workspace_that_its_shape_asks_for(m, n, slice
     assert torch.equal(oz.ozaki_newton_schulz_ws(three, ws, num_slices=slices), oz.ozaki_newton_schulz(three, num_slices=slices))
 
 
+def test_workspaces_that_the_device_cannot_use_are_refused():
+    x, w, o = randn(8, 8192, dtype=torch.bfloat16), randn(1, 64, 8192, dtype=torch.bfloat16), torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    need = max(oz.ozaki_grouped_gemm_workspace_bytes(x, w), oz.ozaki_newton_schulz_workspace_bytes(300, 300))
+    assert need > 0
+    for ws in (torch.empty(need, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8, device="cuda").expand(need),
+               torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            oz.ozaki_grouped_gemm_ws(x, w, o, ws)
+        with pytest.raises(ValueError, match="workspace"):
+            oz.ozaki_newton_schulz_ws(randn(300, 300), ws)
+
+
 # ------------------------------------------------------------------ layouts
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("n", [1, 7, 300])

@@ -322,10 +322,11 @@ struct Problem {
   int m_out() const { return op == kForward ? n : k; }
   int bn() const { return op == kWgrad && n <= 128 ? 128 : 256; }
   // Whether tiles are left for a split is known on the device only, but parts need arrival counters
-  // that a launch before the product's has to zero, and a rendezvous: 3.5 to 4 us on this side, and no
-  // workspace on the other.  Parts win that back only when a sum is long (one token of 8 experts,
-  // n = 1024, and 512 rows of one, n = 4096; unsplit / split us):
-  //   k 2048: 12.5 / 14.9    k 4096: 20.1 / 22.3, 24.5 / 27.9    k 8192: 20.9 / 16.5, 41.6 / 37.1
+  // that a launch before the product's has to zero, and a rendezvous: 1.4 to 4.6 us (from the host, with the
+  // allocation of a workspace, 3 to 8).  Parts win that back only when a sum is long.  In a graph, us unsplit / split,
+  // one token of 8 experts with n = 1024, and 512 rows of one with n = 4096:
+  //   k 1024:  8.4 / 11.3, 10.6 / 12.0    k 2048: 11.8 / 14.4, 15.0 / 19.6    k 4096: 18.4 / 19.9, 23.5 / 24.0
+  //   k 6144: 25.4 / 25.3, 31.9 / 28.4    k 8192: 32.5 / 30.6, 40.5 / 33.9    k 16384: 60.5 / 53.0, 74.2 / 52.2
   bool may_split() const {
     const int blocks = op == kWgrad ? ceil_div(rows, BK * groups) : ceil_div(op == kForward ? k : n, BK);
     return blocks > kMaxUnsplit;

@@ -35,14 +35,15 @@ inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255);
 constexpr int kNormBlocks = 304;       // partial sums of a matrix's norm, at most
 constexpr int kMaxParts = 160;         // parts of split tiles that a product's workspace holds
 // Two slices: MMA steps (16 k) summed on the tensor core before the sum moves to FP32 registers.
-// The tensor core truncates each addition, which biases long sums; the relative error of the
-// result (five steps, against 64 bits) is proportional to it:
-//   128 x 128:    1.6e-6 (1 step)  2.3e-6 (2)  3.5e-6 (4)  6.1e-6 (8)   plain FP32: 1.3e-6
-//   8192 x 2048:  1.5e-6 (1)       1.9e-6 (2)  2.9e-6 (4)  5.0e-6 (8)   plain FP32: 4.7e-6
-// and so is the epilogue's work: 4.1, 3.0, 2.6 and 2.4 ms at 8192 x 2048.  One k-block (4 steps) keeps
-// the error below plain FP32's where sums are long.  Where the smaller side is at most 128 it does
-// not, but single steps of S^2 alone do: 128 x 300 1.2e-6 and 132 us with single steps everywhere, 1.3e-6 and
-// 108 us so, 2.4e-6 and 101 us with k-blocks (plain FP32: 1.6e-6).
+// The tensor core truncates each addition, which biases long sums, so the result's relative error (five
+// steps, against 64 bits) grows with the steps of a sum, while the epilogue's work shrinks:
+//                  single steps        k-blocks (4 steps)    plain FP32
+//   128 x 300      0.95e-6   124 us    2.0e-6     96 us      1.6e-6
+//   512 x 512      1.3e-6    170 us    2.8e-6    123 us      2.1e-6
+//   1023 x 2777    1.2e-6    509 us    2.3e-6    281 us      3.7e-6
+//   8192 x 2048    1.4e-6   2.58 ms    2.1e-6   1.35 ms      4.5e-6
+// K-blocks keep it below plain FP32's from a side of about 1000 on, and within 1.4 times that below.  Where the
+// smaller side is at most 128, S^2 is taken in single steps, which alone is enough: 128 x 300 1.1e-6 and 104 us.
 
 // The products of a step.
 enum Kind { kGram = 0, kSquare = 1, kApply = 2 };

@@ -3,7 +3,7 @@
 // The same iteration, scales and slices as oz_newton.cu (S = A + b/2c I, B = c S^2 + .., X <- B X), for
 // matrices whose X and S fit shared memory: the smaller side at most 128, the larger at most 256 (two
 // slices) or 512.  Between products of a chain that spans CTAs there is a fence, a flag and a reload
-// (128 x 128 FP32: 9 us a product); here a product is handed on by an mbarrier (3.7 us), and the whole
+// (128 x 128 FP32: 9 us a product); here a product is handed on by an mbarrier (3.3 us), and the whole
 // operator, norm included, is one launch.  One CTA a matrix.
 //
 // X is kept with its smaller side as rows, in 128-byte-swizzled blocks of 64 columns.  That one
@@ -15,11 +15,11 @@
 // Two slices: sums leave the tensor core, which truncates, and are added up in FP32 registers, h l' + l h'
 // before h h'.  S^2 decides the error, so there each MMA step (16 k) is a sum of its own and l l' is kept
 // too; the other products take four steps at a time (100 x 100, five steps, against 64 bits; plain FP32 1.3e-6):
-//   all by single steps, no l l'    1.8e-6  55 us (128 x 256: 87)
+//   all by single steps, no l l'    1.8e-6  55 us (128 x 256: 87)   (times when this was chosen)
 //   four steps but S^2              2.0e-6  49    (72)
 //   and with l l' in S^2            1.6e-6  49    (72)   in all products: 1.6e-6  52 (77)
 // Bound by the latency of a product (MMA, tensor-memory read, stores, two hand-overs): with five steps
-// 128 x 128 bf16 27.5 us, FP32 50, 300 of them 55 and 103.
+// 128 x 128 bf16 27.7 us, FP32 50, 300 of them 56 and 102.
 #include <atomic>
 
 #include <cuda_bf16.h>
@@ -33,8 +33,8 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr uint32_t kBlock = kRows * 128;  // 64 columns of 128 rows
-// One slice: 16 epilogue warps (128 x 512 bf16 57 us; with 8: 71).  Two: 8, whose running sums and
-// hand-overs cost more with 16 (128 x 128 FP32 58 us; with 16: 69).
+// One slice: 16 epilogue warps (128 x 512 bf16 56 us, 128 x 128 27.7; with 8: 69 and 29.8).  Two: 8, whose running
+// sums and hand-overs cost more with 16 (128 x 128 FP32, when this was chosen: 58 us; with 16: 69).
 template <int SLICES>
 constexpr int kEpiWarpsOf = SLICES == 2 ? 8 : 16;
 template <int SLICES>
@@ -107,6 +107,7 @@ template <int SLICES>
 __global__ void __launch_bounds__(kThreadsOf<SLICES>, 1) newton_small_kernel(const __grid_constant__ SmallArgs a) {
   constexpr int kEpiWarps = kEpiWarpsOf<SLICES>;
   constexpr int kCols = kEpiWarps / 4;  // warps that share the blocks of 32 columns of a quadrant
+  static_assert(SLICES == 1 || kCols == 2, "two slices: two blocks a warp are the 128 columns of a sum");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t accfull[4], accempty[4], ready, drain;

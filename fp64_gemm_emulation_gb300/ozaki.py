@@ -632,7 +632,8 @@ def ozaki_grouped_gemm(X, W, offsets, Y=None, workspace=None, stream=None):
     """Y[r] = W[e] X[r] for the rows r of group e: X (rows, k), W (groups, n, k), offsets (groups + 1) int32.
 
     bfloat16 or float16; row-major (rows of X and Y, and the matrices of W, may be strided).
-    Rows outside [offsets[0], offsets[-1]) give zero."""
+    Rows outside [offsets[0], offsets[-1]) give zero.  Like all functions here it records nothing for
+    autograd: the gradients are ozaki_grouped_gemm_dgrad and ozaki_grouped_gemm_wgrad."""
     if stream is not None and (other := _other_stream(stream, X.device)):
         return _call_on(other, ozaki_grouped_gemm, X, W, offsets, Y, workspace)
     ldw, sw = _experts(W, "W")
@@ -739,8 +740,9 @@ def ozaki_newton_schulz(G, steps: int = 5, coeffs=NEWTON_SCHULZ_COEFFS, eps: flo
 
     G is bfloat16, float16 or float32; its matrices are row-major (2-D and 3-D G may have strided
     rows, a 2-D G may be column-major if out is too).  coeffs: one (a, b, c) for every step, or one for each.
-    num_slices: FP16 slices of the intermediate matrices; by default 1 for bfloat16 (11 bits kept) and
-    2 otherwise (22 bits).  `out` has G's shape and dtype; by default it is new and row-major
+    num_slices: FP16 slices of the intermediate matrices; by default 1 for bfloat16 (11 bits kept: the
+    result is off by 2.0e-3 to 2.3e-3, where rounding it alone costs 1.7e-3; 2 slices reach that in
+    1.8 to 3.2 times the time) and 2 otherwise (22 bits).  `out` has G's shape and dtype; by default it is new and row-major
     (column-major for a column-major G)."""
     import torch
 

@@ -352,6 +352,7 @@ int ozaki2_dgemm_noalloc(int m, int n, int k, const double* A, int lda, const do
  *  - Inf and NaN follow IEEE arithmetic within their own group; no other group sees them.
  *  - Any address and leading dimension (of the element's alignment) is accepted; operands whose
  *    address or strides are not multiples of 16 bytes are first laid out in the workspace.
+ *  - Outputs must overlap neither operands nor the workspace.
  * Results do not depend on timing (parts of a split sum are added in a fixed order). */
 #define OZ_MAX_GROUPS 1024
 
@@ -396,7 +397,12 @@ int ozaki_grouped_gemm_wgrad(int n, int k, int rows, int groups, int dtype, cons
  *  - num_slices: FP16 slices of every intermediate matrix: 1 keeps 11 bits (three bits more than
  *    bf16), at one product for each of the formula's; 2 keeps 22 bits at three times the
  *    tensor-core work, which FP32 results need.  Sums are FP32 in both.
+ *    Against 64 bits (five steps of the usual polynomial, 2-norm): a bf16 result is off by 2.0e-3 to
+ *    2.3e-3 with one slice, and by 1.7e-3 where only the result is rounded; an FP32 result with two slices
+ *    by 1e-6 to 2.8e-6, an iteration in plain FP32 by 1.2e-6 to 4.5e-6.
  *  - eps >= 0.  A zero matrix gives zero; a matrix that holds Inf or NaN gives NaN everywhere.
+ *  - Results do not depend on timing.  The order of a sum depends on the sizes, the batch among them, so the
+ *    last bits of a matrix's result may differ between batches that hold it.
  *  - m, n or batch equal to 0: nothing is done.  batch <= 65535. */
 #define OZ_MAX_NS_STEPS 32
 

@@ -362,8 +362,7 @@ def run(state):
         return {"dx": r["dx"].to(s["h"].dtype), "dw": r["dw"].to(s["w"].dtype)}
     g = s["flat"].float()  # the tensors lie in one buffer, zeros between them
     norm = g.square().sum().sqrt()
-    torch.mul(g, (s["limit"] / (norm + 1e-6)).clamp(max=1.0), out=g)
-    s["out"].copy_(g)
+    s["out"].copy_(g * (s["limit"] / (norm + 1e-6)).clamp(max=1.0))  # (g is flat itself where that is in 32 bits)
     return {"norm": norm, "grads": s["out"]}
 
 

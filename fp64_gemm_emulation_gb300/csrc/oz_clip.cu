@@ -1,0 +1,277 @@
+// oz_clip.cu -- the 2-norm over many tensors, and each of them times min(1, limit / (norm + eps)).
+//
+// Bound by memory: the tensors are read for the norm, and read again and written where that is below 1 or
+// the results go elsewhere.  The tensors of a launch are in its parameters (no copy to the device), cut into
+// chunks of equal length that CTAs take in turn.  Each CTA's sum of squares is a double at a place of its
+// own, and every CTA of the second launch adds them all in the same order (at most 32 KB from the L2): the norm
+// does not depend on timing, and there is no counter to be zeroed first.  The second launch goes through
+// the chunks backwards: the first it meets are the last that were read, still in the L2.
+//
+// Squares: 32 elements at a time in FP32 where the largest of them is between 2^-50 and 2^55 (what the others
+// then lose below 2^-126 is under 2^-26 of the sum), otherwise in FP64; the running sum is FP64 throughout.
+#include "oz_elements.cuh"
+#include "oz_device.cuh"
+
+namespace oz {
+namespace {
+
+constexpr int kThreads = 256, kChunk = 16384;  // elements of a chunk
+constexpr int kMaxSums = 4096;                 // CTAs whose sums the workspace holds
+
+struct Tensor {
+  const void* in;
+  void* out;
+  long long count;
+  long long first;  // chunks before it in this launch
+  int dtype, aligned;
+};
+
+template <int N>
+struct ClipParams {
+  Tensor t[N];
+  int tensors;
+  int first_sum, all_sums;  // where this launch's sums start; how many there are
+  long long chunks;
+  double* sums;
+  float limit, eps;
+  float* norm;
+};
+
+template <class P>
+__device__ __forceinline__ int tensor_of(const P& a, long long chunk) {
+  int lo = 0, hi = a.tensors;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.t[mid].first <= chunk) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// The squares of the eights v[0 .. N - 1].
+template <class T, int N>
+__device__ __forceinline__ double squares(const Eight<T> (&v)[N]) {
+  float most = 0.0f, sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = to_float(v[i].e[e]);
+      most = fmaxf(most, fabsf(x));
+      sum = fmaf(x, x, sum);
+    }
+  }
+  // (a NaN is not in most, but in sum)
+  if (most == 0.0f || (most >= 8.8817842e-16f && most <= 3.6028797e16f)) return static_cast<double>(sum);
+  double d = 0.0;
+#pragma unroll 1
+  for (int i = 0; i < N; ++i) {
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+      const double x = to_float(v[i].e[e]);
+      d = fma(x, x, d);
+    }
+  }
+  return d;
+}
+
+template <class T>
+__device__ __forceinline__ double chunk_squares(const Tensor& t, long long from) {
+  const T* p = static_cast<const T*>(t.in) + from;
+  const int count = static_cast<int>(min(static_cast<long long>(kChunk), t.count - from));
+  double d = 0.0;
+  constexpr int N = 4, STEP = kThreads * 8;
+  for (int c = 8 * threadIdx.x; c < count; c += N * STEP) {
+    Eight<T> v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = c + i * STEP;
+      if (t.aligned && at + 8 <= count) {
+        v[i] = load_eight(p + at);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (at + e < count) v[i].e[e] = p[at + e];
+          else from_float(0.0f, v[i].e[e]);
+        }
+      }
+    }
+    d += squares(v);
+  }
+  return d;
+}
+
+__device__ __forceinline__ double block_sum(double d, double* meet) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, s);
+  if ((threadIdx.x & 31) == 0) meet[threadIdx.x >> 5] = d;
+  __syncthreads();
+  d = 0.0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) d += meet[w];
+  __syncthreads();
+  return d;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ ClipParams<N> a) {
+  __shared__ double meet[kThreads / 32];
+  let_next_start();
+  wait_for_previous();
+  double d = 0.0;
+  for (long long chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
+    const Tensor& t = a.t[tensor_of(a, chunk)];
+    const long long from = (chunk - t.first) * kChunk;
+    d += t.dtype == OZ_F32 ? chunk_squares<float>(t, from)
+         : t.dtype == OZ_BF16 ? chunk_squares<__nv_bfloat16>(t, from)
+                              : chunk_squares<__half>(t, from);
+  }
+  d = block_sum(d, meet);
+  if (threadIdx.x == 0) a.sums[a.first_sum + blockIdx.x] = d;
+}
+
+template <class T>
+__device__ __forceinline__ void scale_chunk(const Tensor& t, long long from, float f) {
+  const T* p = static_cast<const T*>(t.in) + from;
+  T* q = static_cast<T*>(t.out) + from;
+  const int count = static_cast<int>(min(static_cast<long long>(kChunk), t.count - from));
+  constexpr int STEP = kThreads * 8;
+#pragma unroll 4
+  for (int c = 8 * threadIdx.x; c < count; c += STEP) {
+    if (t.aligned && c + 8 <= count) {
+      const Eight<T> v = load_eight(p + c);
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = to_float(v.e[e]) * f;
+      store_eight(q + c, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < count) from_float(to_float(p[c + e]) * f, q[c + e]);
+    }
+  }
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ ClipParams<N> a) {
+  __shared__ double meet[kThreads / 32];
+  let_next_start();
+  wait_for_previous();
+  double all = 0.0;
+  for (int i = threadIdx.x; i < a.all_sums; i += kThreads) all += __ldcg(a.sums + i);
+  const float norm = static_cast<float>(sqrt(block_sum(all, meet)));
+  float f = a.limit / (norm + a.eps);
+  if (f > 1.0f) f = 1.0f;  // NaN stays
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
+  for (long long i = blockIdx.x; i < a.chunks; i += gridDim.x) {
+    const long long chunk = a.chunks - 1 - i;
+    const Tensor& t = a.t[tensor_of(a, chunk)];
+    if (f == 1.0f && t.in == t.out) continue;
+    const long long from = (chunk - t.first) * kChunk;
+    if (t.dtype == OZ_F32) scale_chunk<float>(t, from, f);
+    else if (t.dtype == OZ_BF16) scale_chunk<__nv_bfloat16>(t, from, f);
+    else scale_chunk<__half>(t, from, f);
+  }
+}
+
+// Tensors of a launch: its parameters hold them all (at most 32764 bytes).
+constexpr int kFew = 64, kMany = 640;
+
+struct Work {
+  int count;
+  const int* dtypes;
+  const void* const* in;
+  void* const* out;
+  const long long* counts;
+};
+
+template <int N>
+int clip_launches(const Work& w, float limit, float eps, float* norm, uint8_t* ws, int sms, cudaStream_t stream) {
+  ClipParams<N> a;
+  a.sums = reinterpret_cast<double*>(ws);
+  a.norm = norm;
+  a.limit = limit;
+  a.eps = eps;
+  const int launches = w.count ? (w.count + N - 1) / N : 1;
+  const int most = kMaxSums / launches < 8 * sms ? kMaxSums / launches : 8 * sms;
+  int sums = 0;
+  auto fill = [&](int l) {
+    a.tensors = 0;
+    a.chunks = 0;
+    for (int i = l * N; i < w.count && i < (l + 1) * N; ++i) {
+      if (w.counts[i] == 0) continue;
+      Tensor& t = a.t[a.tensors++];
+      t.in = w.in[i];
+      t.out = w.out[i];
+      t.count = w.counts[i];
+      t.first = a.chunks;
+      t.dtype = w.dtypes[i];
+      t.aligned = ((reinterpret_cast<uintptr_t>(t.in) | reinterpret_cast<uintptr_t>(t.out)) & 15) == 0;
+      a.chunks += (t.count + kChunk - 1) / kChunk;
+    }
+    const long long grid = a.chunks < most ? a.chunks : most;
+    return static_cast<unsigned>(grid < 1 ? 1 : grid);
+  };
+  for (int l = 0; l < launches; ++l) {
+    const unsigned grid = fill(l);
+    a.first_sum = sums;
+    sums += static_cast<int>(grid);
+    if (launch_overlapping(sum_kernel<N>, dim3(grid), kThreads, 0, stream, a) != cudaSuccess) return OZ_ECUDA;
+  }
+  a.all_sums = sums;
+  for (int l = launches - 1; l >= 0; --l) {  // each of them writes the norm, the same one
+    const unsigned grid = fill(l);
+    if (launch_overlapping(scale_kernel<N>, dim3(grid), kThreads, 0, stream, a) != cudaSuccess) return OZ_ECUDA;
+  }
+  return OZ_OK;
+}
+
+constexpr size_t kClipBytes = sizeof(double) * kMaxSums;
+constexpr int kMaxTensors = kMany * 64;
+
+}  // namespace
+}  // namespace oz
+
+using namespace oz;
+
+extern "C" {
+
+size_t ozaki_clip_grad_norm_workspace_bytes(void) { return kClipBytes; }
+
+static int clip_check(const Work& w, float limit, float eps, const float* norm) {
+  if (w.count < 0 || w.count > kMaxTensors || !(limit >= 0.0f) || !(eps >= 0.0f) || !norm || (reinterpret_cast<uintptr_t>(norm) & 3)) return OZ_EINVAL;
+  if (w.count && (!w.dtypes || !w.in || !w.out || !w.counts)) return OZ_EINVAL;
+  for (int i = 0; i < w.count; ++i) {
+    if (!element_bytes(w.dtypes[i]) || w.counts[i] < 0) return OZ_EINVAL;
+    if (w.counts[i] && (!w.in[i] || !w.out[i] || !element_aligned(w.in[i], w.dtypes[i]) || !element_aligned(w.out[i], w.dtypes[i]))) return OZ_EINVAL;
+  }
+  return OZ_OK;
+}
+
+int ozaki_clip_grad_norm_ws(int count, const int* dtypes, const void* const* grads, void* const* outs, const long long* counts,
+                            float max_norm, float eps, float* norm, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  const Work w{count, dtypes, grads, outs, counts};
+  const int rc = clip_check(w, max_norm, eps, norm);
+  if (rc) return rc;
+  if (!workspace || ws_bytes < kClipBytes || (reinterpret_cast<uintptr_t>(workspace) & 255)) return OZ_ENOMEM;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return OZ_ECUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  return count <= kFew ? clip_launches<kFew>(w, max_norm, eps, norm, ws, sms, stream) : clip_launches<kMany>(w, max_norm, eps, norm, ws, sms, stream);
+}
+
+int ozaki_clip_grad_norm(int count, const int* dtypes, const void* const* grads, void* const* outs, const long long* counts,
+                         float max_norm, float eps, float* norm, cudaStream_t stream) {
+  int rc = clip_check(Work{count, dtypes, grads, outs, counts}, max_norm, eps, norm);
+  if (rc) return rc;
+  void* ws = nullptr;
+  keep_default_pool_cached();
+  if (cudaMallocAsync(&ws, kClipBytes, stream) != cudaSuccess) {
+    cudaGetLastError();
+    return OZ_ENOMEM;
+  }
+  rc = ozaki_clip_grad_norm_ws(count, dtypes, grads, outs, counts, max_norm, eps, norm, ws, kClipBytes, stream);
+  if (cudaFreeAsync(ws, stream) != cudaSuccess && rc == OZ_OK) rc = OZ_ECUDA;
+  return rc;
+}
+
+}  // extern "C"

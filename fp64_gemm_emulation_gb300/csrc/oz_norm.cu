@@ -1,0 +1,409 @@
+// oz_norm.cu -- root-mean-square norm of rows with the residual's addition, its result in 8 bits with a scale
+// for each block of 128, and its gradients.
+//
+//   forward   h = x + residual,  r = 1 / sqrt(mean(h^2) + eps),  y = h r w   -> q, scales (of y), h, r; y if wanted
+//   backward  g = dy w,  dx = dh + r (g - h r^2 mean(g h)),  dw = sum over rows of dy h r
+// All in FP32: y is quantised (and rounded, where wanted) from the FP32 sum h, not from the stored one, so each
+// output is rounded once.
+//
+// Bound by memory: every row is read once, held in registers between its sum and its results, and written
+// once.  Several threads share a row, eight elements each: neighbours where rows start at multiples of 16
+// bytes (16-byte accesses; a block of 128 is 16 threads), otherwise 32 apart (a warp's accesses of two
+// bytes are then neighbours; a block is half of a warp's 256 elements).
+#include "oz_elements.cuh"
+#include "oz_device.cuh"
+#include "oz_ragged.cuh"
+
+namespace oz {
+namespace {
+
+constexpr int kRowsBack = 2;  // CTAs of the backward pass on an SM
+
+struct NormParams {
+  int k, rows;
+  const void *x, *residual, *w;
+  void *h, *y;
+  uint8_t* q;
+  float *s, *rstd;
+  long long ldx, ldr, ldh, ldy, ldq, lds;
+  float eps;
+};
+
+struct NormBackParams {
+  int k, rows;
+  const void *dy, *h, *w, *dh;
+  const float* rstd;
+  void *dx, *dw;
+  long long lddy, ldh, lddh, lddx;
+  float* part;  // [CTAs][k]
+  int parts;
+};
+
+// The sum over a row's threads (blockDim.x of them, whole warps); meet: room for 32 floats of each row.
+__device__ __forceinline__ float row_sum(float v, float* meet) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) meet[warp] = v;
+  __syncthreads();
+  v = lane < warps ? meet[lane] : 0.0f;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  return v;
+}
+
+// Where a thread's eight elements of run j lie: column(j) + e * STEP.
+template <bool VEC>
+__device__ __forceinline__ int first_column(int j) {
+  const int t = threadIdx.x + j * blockDim.x;
+  return VEC ? 8 * t : (t >> 5) * 256 + (t & 31);
+}
+
+template <class T, bool VEC>
+__device__ __forceinline__ Eight<T> fetch(const T* row, int c, int k) {
+  Eight<T> r;
+  if (VEC && c + 8 <= k) return load_eight(row + c);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int at = c + e * (VEC ? 1 : 32);
+    if (at < k) r.e[e] = row[at];
+    else from_float(0.0f, r.e[e]);
+  }
+  return r;
+}
+template <class T, bool VEC>
+__device__ __forceinline__ void put(T* row, int c, int k, const float (&v)[8]) {
+  if (VEC && c + 8 <= k) {
+    store_eight(row + c, v);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int at = c + e * (VEC ? 1 : 32);
+    if (at < k) from_float(v[e], row[at]);
+  }
+}
+
+// RUNS: runs of eight elements a thread holds.  blockDim (threads of a row, rows).
+template <class T, bool VEC, int RUNS>
+__global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormParams a) {
+  __shared__ float meet[32];
+  let_next_start();
+  wait_for_previous();
+  const int row = blockIdx.x * blockDim.y + threadIdx.y;
+  const bool have = row < a.rows;  // (a whole warp's; rows of several warps are alone in their CTA)
+  const int lane = threadIdx.x & 31;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  const T* res = static_cast<const T*>(a.residual) + row * a.ldr;
+  float h[RUNS][8];
+  float sum = 0.0f;
+#pragma unroll
+  for (int j = 0; j < RUNS; ++j) {
+    const int c = first_column<VEC>(j);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[j][e] = 0.0f;
+    if (have && c < a.k) {
+      const Eight<T> vx = fetch<T, VEC>(x, c, a.k);
+      if (a.residual) {
+        const Eight<T> vr = fetch<T, VEC>(res, c, a.k);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[j][e] = to_float(vx.e[e]) + to_float(vr.e[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[j][e] = to_float(vx.e[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fmaf(h[j][e], h[j][e], sum);
+  }
+  sum = row_sum(sum, meet);
+  const float r = 1.0f / sqrtf(sum / static_cast<float>(a.k) + a.eps);
+  if (!have) return;
+  if (threadIdx.x == 0) a.rstd[row] = r;
+#pragma unroll
+  for (int j = 0; j < RUNS; ++j) {
+    const int c = first_column<VEC>(j);
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = 0.0f;
+    if (c < a.k) {
+      if (a.h) put<T, VEC>(static_cast<T*>(a.h) + row * a.ldh, c, a.k, h[j]);
+      const Eight<T> w = fetch<T, VEC>(static_cast<const T*>(a.w), c, a.k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = h[j][e] * r * to_float(w.e[e]);
+      if (a.y) put<T, VEC>(static_cast<T*>(a.y) + row * a.ldy, c, a.k, y);
+    }
+    uint8_t* q = a.q + row * a.ldq;
+    if (VEC) {  // 16 lanes hold a block
+      uint32_t most = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) most = max(most, magnitude(y[e]));
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+      const float scale = scale_of<false>(most);
+      const uint2 v = eight_bits<false>(y, 1.0f / scale);
+      if (c + 8 <= a.k) {
+        *reinterpret_cast<uint2*>(q + c) = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < a.k) q[c + e] = static_cast<uint8_t>(e < 4 ? v.x >> (8 * e) : v.y >> (8 * (e - 4)));
+      }
+      if ((lane & 15) == 0 && c < a.k) a.s[c / kScaleBlock * a.lds + row] = scale;
+    } else {  // the warp holds two blocks, elements 0 - 3 and 4 - 7
+      uint32_t first = 0, second = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        first = max(first, magnitude(y[e]));
+        second = max(second, magnitude(y[e + 4]));
+      }
+      const float scale[2] = {scale_of<false>(__reduce_max_sync(0xFFFFFFFFu, first)), scale_of<false>(__reduce_max_sync(0xFFFFFFFFu, second))};
+      const float inverse[2] = {1.0f / scale[0], 1.0f / scale[1]};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] *= inverse[e >> 2];
+      const uint2 v = eight_bits<false>(y, 1.0f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + 32 * e < a.k) q[c + 32 * e] = static_cast<uint8_t>(e < 4 ? v.x >> (8 * e) : v.y >> (8 * (e - 4)));
+      if (lane == 0 && c < a.k) a.s[c / kScaleBlock * a.lds + row] = scale[0];
+      if (lane == 0 && c + 128 < a.k) a.s[(c / kScaleBlock + 1) * a.lds + row] = scale[1];
+    }
+  }
+}
+
+// Gradients: a CTA takes every gridDim.x-th row and keeps dw's sums of its columns in registers; the CTAs' sums
+// go to the workspace and are added in their order by a second launch, so results do not depend on timing.
+template <class T, bool VEC, int RUNS>
+__global__ void __launch_bounds__(1024) norm_back_kernel(const __grid_constant__ NormBackParams a) {
+  __shared__ float meet[2][32];
+  let_next_start();
+  wait_for_previous();
+  float dw[RUNS][8];
+#pragma unroll
+  for (int i = 0; i < RUNS * 8; ++i) dw[i >> 3][i & 7] = 0.0f;
+  Eight<T> dy[RUNS], h[RUNS], w[RUNS];
+#pragma unroll
+  for (int j = 0; j < RUNS; ++j) w[j] = fetch<T, VEC>(static_cast<const T*>(a.w), first_column<VEC>(j), a.k);
+  int turn = 0;
+  for (int row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+    const float r = a.rstd[row];
+    float dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < RUNS; ++j) {
+      const int c = first_column<VEC>(j);
+      dy[j] = fetch<T, VEC>(static_cast<const T*>(a.dy) + row * a.lddy, c, a.k);
+      h[j] = fetch<T, VEC>(static_cast<const T*>(a.h) + row * a.ldh, c, a.k);
+    }
+#pragma unroll
+    for (int j = 0; j < RUNS; ++j) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = to_float(dy[j].e[e]), x = to_float(h[j].e[e]);
+        dot = fmaf(d * to_float(w[j].e[e]), x, dot);
+        dw[j][e] = fmaf(d * r, x, dw[j][e]);
+      }
+    }
+    // Two rooms in turn: a warp writes one again only after the other's barrier.
+    dot = row_sum(dot, meet[turn]) / static_cast<float>(a.k);
+    const float f = r * r * dot;
+#pragma unroll
+    for (int j = 0; j < RUNS; ++j) {
+      const int c = first_column<VEC>(j);
+      if (c >= a.k) continue;
+      float dx[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dx[e] = r * (to_float(dy[j].e[e]) * to_float(w[j].e[e]) - to_float(h[j].e[e]) * f);
+      if (a.dh) {
+        const Eight<T> dh = fetch<T, VEC>(static_cast<const T*>(a.dh) + row * a.lddh, c, a.k);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dx[e] += to_float(dh.e[e]);
+      }
+      put<T, VEC>(static_cast<T*>(a.dx) + row * a.lddx, c, a.k, dx);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < RUNS; ++j) {
+    const int c = first_column<VEC>(j);
+    float* part = a.part + static_cast<long long>(blockIdx.x) * a.k;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int at = c + e * (VEC ? 1 : 32);
+      if (at < a.k) part[at] = dw[j][e];
+    }
+  }
+}
+
+// dw: 32 columns a CTA, 8 warps each a run of parts, added in order.
+template <class T>
+__global__ void __launch_bounds__(256) norm_weight_kernel(const float* part, int parts, int k, T* dw) {
+  __shared__ float sums[8][32];
+  let_next_start();
+  wait_for_previous();
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
+  float v = 0.0f;
+  if (c < k) {
+#pragma unroll 4
+    for (int i = warp; i < parts; i += 8) v += part[static_cast<long long>(i) * k + c];
+  }
+  sums[warp][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (warp == 0 && c < k) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) v += sums[i][threadIdx.x];
+    from_float(v, dw[c]);
+  }
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  return sms;
+}
+
+struct Shape {
+  int threads, rows, runs;  // threads of a row, rows of a CTA, runs a thread
+};
+
+// Threads of a row: one run each where that is few rows' latency or few threads, otherwise about 256 threads.
+Shape shape_of(int k, bool spread) {
+  const int runs_all = (k + 255) / 256 * 32;  // whole warps of runs
+  int runs = 1;
+  while (runs < 4 && (runs_all / runs > 1024 || (!spread && runs_all / runs > 256))) runs *= 2;
+  const int threads = ((runs_all + runs - 1) / runs + 31) / 32 * 32;
+  return {threads, threads > 32 ? 1 : 4, runs};
+}
+
+template <class T, bool VEC>
+cudaError_t launch_norm(const NormParams& a, int sms, cudaStream_t stream) {
+  const Shape s = shape_of(a.k, a.rows < 4 * sms);
+  cudaError_t e = cudaErrorInvalidValue;
+  auto go = [&](void (*kernel)(NormParams)) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.rows + s.rows - 1) / s.rows);
+    cfg.blockDim = dim3(s.threads, s.rows);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, a);
+    if (e != cudaSuccess) cudaGetLastError();
+  };
+  switch (s.runs) {
+    case 1: go(norm_kernel<T, VEC, 1>); break;
+    case 2: go(norm_kernel<T, VEC, 2>); break;
+    default: go(norm_kernel<T, VEC, 4>); break;
+  }
+  return e;
+}
+
+template <class T>
+cudaError_t norm_of_type(const NormParams& a, int sms, cudaStream_t stream) {
+  const bool vec = rows_aligned<T>(a.x, a.ldx, a.rows) && rows_aligned<T>(a.w, 0, 1) &&
+                   (!a.residual || rows_aligned<T>(a.residual, a.ldr, a.rows)) && (!a.h || rows_aligned<T>(a.h, a.ldh, a.rows)) &&
+                   (!a.y || rows_aligned<T>(a.y, a.ldy, a.rows));
+  return vec ? launch_norm<T, true>(a, sms, stream) : launch_norm<T, false>(a, sms, stream);
+}
+
+template <class T, bool VEC>
+cudaError_t launch_norm_back(const NormBackParams& a, cudaStream_t stream) {
+  const Shape s = shape_of(a.k, true);
+  auto kernel = s.runs == 1 ? norm_back_kernel<T, VEC, 1> : s.runs == 2 ? norm_back_kernel<T, VEC, 2> : norm_back_kernel<T, VEC, 4>;
+  return launch_overlapping(kernel, dim3(a.parts), s.threads, 0, stream, a);
+}
+
+template <class T>
+cudaError_t norm_back_of_type(const NormBackParams& a, cudaStream_t stream) {
+  const bool vec = rows_aligned<T>(a.dy, a.lddy, a.rows) && rows_aligned<T>(a.h, a.ldh, a.rows) && rows_aligned<T>(a.w, 0, 1) &&
+                   rows_aligned<T>(a.dx, a.lddx, a.rows) && (!a.dh || rows_aligned<T>(a.dh, a.lddh, a.rows));
+  const cudaError_t e = vec ? launch_norm_back<T, true>(a, stream) : launch_norm_back<T, false>(a, stream);
+  if (e != cudaSuccess) return e;
+  return launch_overlapping(norm_weight_kernel<T>, dim3((a.k + 31) / 32), 256, 0, stream, a.part, a.parts, a.k, static_cast<T*>(a.dw));
+}
+
+int parts_of(int rows, int k) {
+  const int most = 152 * kRowsBack * (k <= 2048 ? 4 : k <= 4096 ? 2 : 1);
+  return rows < most ? rows : most;
+}
+
+int check_back(int k, int rows, int dtype, long long lddy, long long ldh, long long lddh, long long lddx) {
+  if (k < 0 || rows < 0 || k > OZ_MAX_NORM_WIDTH || !element_bytes(dtype)) return OZ_EINVAL;
+  const long long least = k > 1 ? k : 1;
+  return lddy < least || ldh < least || lddh < least || lddx < least ? OZ_EINVAL : OZ_OK;
+}
+
+int norm_back(int k, int rows, int dtype, const void* dY, int lddy, const void* H, int ldh, const void* W, const float* rstd,
+              const void* dH, int lddh, void* dX, int lddx, void* dW, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  if (k == 0) return OZ_OK;
+  if (!dW || !element_aligned(dW, dtype)) return OZ_EINVAL;
+  if (rows == 0) return cudaMemsetAsync(dW, 0, element_bytes(dtype) * k, stream) == cudaSuccess ? OZ_OK : OZ_ECUDA;
+  for (const void* p : {dY, H, W, static_cast<const void*>(dX)})
+    if (!p || !element_aligned(p, dtype)) return OZ_EINVAL;
+  if (!rstd || (reinterpret_cast<uintptr_t>(rstd) & 3) || !element_aligned(dH, dtype)) return OZ_EINVAL;
+  const NormBackParams a{k, rows, dY, H, W, dH, rstd, dX, dW, lddy, ldh, lddh, lddx, static_cast<float*>(workspace), parts_of(rows, k)};
+  if (!workspace || ws_bytes < sizeof(float) * static_cast<size_t>(k) * a.parts || (reinterpret_cast<uintptr_t>(workspace) & 255)) return OZ_ENOMEM;
+  const cudaError_t e = dtype == OZ_BF16 ? norm_back_of_type<__nv_bfloat16>(a, stream)
+                        : dtype == OZ_F16 ? norm_back_of_type<__half>(a, stream)
+                                          : norm_back_of_type<float>(a, stream);
+  return e == cudaSuccess ? OZ_OK : OZ_ECUDA;
+}
+
+}  // namespace
+}  // namespace oz
+
+using namespace oz;
+
+extern "C" {
+
+int ozaki_rms_norm_f8(int k, int rows, int dtype, const void* X, int ldx, const void* residual, int ldr, const void* W, float eps,
+                      void* Q, int ldq, float* S, int lds, void* H, int ldh, float* rstd, void* Y, int ldy, cudaStream_t stream) {
+  if (k < 0 || rows < 0 || k > OZ_MAX_NORM_WIDTH || !element_bytes(dtype) || !(eps >= 0.0f)) return OZ_EINVAL;
+  const int least = k > 1 ? k : 1;
+  if (ldx < least || ldr < least || ldh < least || ldy < least || ldq < least || lds < (rows > 1 ? rows : 1)) return OZ_EINVAL;
+  if (k == 0 || rows == 0) return OZ_OK;
+  if (!X || !W || !Q || !S || !rstd || (reinterpret_cast<uintptr_t>(Q) & 15) || (rows > 1 && ldq % 16)) return OZ_EINVAL;
+  if ((reinterpret_cast<uintptr_t>(S) & 3) || (reinterpret_cast<uintptr_t>(rstd) & 3)) return OZ_EINVAL;
+  for (const void* p : {X, residual, W, static_cast<const void*>(H), static_cast<const void*>(Y)})
+    if (!element_aligned(p, dtype)) return OZ_EINVAL;
+  const int sms = sm_count();
+  if (!sms) return OZ_ECUDA;
+  const NormParams a{k, rows, X, residual, W, H, Y, static_cast<uint8_t*>(Q), S, rstd, ldx, ldr, ldh, ldy, ldq, lds, eps};
+  const cudaError_t e = dtype == OZ_BF16 ? norm_of_type<__nv_bfloat16>(a, sms, stream)
+                        : dtype == OZ_F16 ? norm_of_type<__half>(a, sms, stream)
+                                          : norm_of_type<float>(a, sms, stream);
+  return e == cudaSuccess ? OZ_OK : OZ_ECUDA;
+}
+
+size_t ozaki_rms_norm_backward_workspace_bytes(int k, int rows) {
+  if (check_back(k, rows, OZ_F32, k > 1 ? k : 1, k > 1 ? k : 1, k > 1 ? k : 1, k > 1 ? k : 1)) return 0;
+  return sizeof(float) * static_cast<size_t>(k) * parts_of(rows, k);
+}
+int ozaki_rms_norm_backward_ws(int k, int rows, int dtype, const void* dY, int lddy, const void* H, int ldh, const void* W,
+                               const float* rstd, const void* dH, int lddh, void* dX, int lddx, void* dW, void* workspace,
+                               size_t ws_bytes, cudaStream_t stream) {
+  const int rc = check_back(k, rows, dtype, lddy, ldh, lddh, lddx);
+  return rc ? rc : norm_back(k, rows, dtype, dY, lddy, H, ldh, W, rstd, dH, lddh, dX, lddx, dW, workspace, ws_bytes, stream);
+}
+int ozaki_rms_norm_backward(int k, int rows, int dtype, const void* dY, int lddy, const void* H, int ldh, const void* W,
+                            const float* rstd, const void* dH, int lddh, void* dX, int lddx, void* dW, cudaStream_t stream) {
+  int rc = check_back(k, rows, dtype, lddy, ldh, lddh, lddx);
+  if (rc) return rc;
+  const bool operands = dY && H && W && rstd && dX && dW;  // argument errors before any allocation
+  const size_t bytes = operands ? ozaki_rms_norm_backward_workspace_bytes(k, rows) : 0;
+  void* ws = nullptr;
+  if (bytes) {
+    keep_default_pool_cached();
+    if (cudaMallocAsync(&ws, bytes, stream) != cudaSuccess) {
+      cudaGetLastError();
+      return OZ_ENOMEM;
+    }
+  }
+  rc = norm_back(k, rows, dtype, dY, lddy, H, ldh, W, rstd, dH, lddh, dX, lddx, dW, ws, bytes, stream);
+  if (ws && cudaFreeAsync(ws, stream) != cudaSuccess && rc == OZ_OK) rc = OZ_ECUDA;
+  return rc;
+}
+
+}  // extern "C"

@@ -1,0 +1,288 @@
+// oz_quantize.cu -- matrices of bfloat16, float16 or FP32 to 8-bit floating point, a scale for each block of 128.
+//
+// A block is 128 neighbours of a row (the operand of a forward or dgrad product), 128 rows of a column (of a
+// wgrad product; anew with each group of rows) or 128 x 128 (weights): scale = max |x| / (the type's
+// largest value), q = x / scale to nearest.  A gradient needs both of the first two, which one pass gives.
+//
+// Bound by memory: an element is read once and its one or two bytes are written once.  A CTA holds a 128 x 128
+// tile in registers (a thread eight neighbours of eight rows, 16 rows apart), so that all three kinds of
+// block are inside a tile: rows by shuffles among 16 lanes, columns by one exchange in shared memory.
+#include "oz_elements.cuh"
+#include "oz_device.cuh"
+#include "oz_ragged.cuh"
+
+namespace oz {
+namespace {
+
+constexpr int TILE = kScaleBlock, kThreads = 256;
+
+struct QuantParams {
+  int k, rows, groups, mats;
+  const void* x;
+  long long ldx, stride_x;
+  const int32_t* offsets;
+  uint8_t *q, *qc;
+  long long ldq, stride_q, ldqc;
+  float *s, *sc;
+  long long lds, ldsc;
+  int col_tiles, row_tiles;
+  long long tiles;
+  int aligned;
+  int* status;
+};
+
+// Eight bytes of a row from column c on, of which those below k exist.
+__device__ __forceinline__ void put_bytes(uint8_t* row, int c, int k, uint2 w) {
+  if (c + 8 <= k) {
+    *reinterpret_cast<uint2*>(row + c) = w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < k) row[c + e] = static_cast<uint8_t>((e < 4 ? w.x >> (8 * e) : w.y >> (8 * (e - 4))));
+  }
+}
+
+// BLOCK: an OZ_BLOCK_*.
+template <class T, int BLOCK, bool E5M2>
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constant__ QuantParams a) {
+  constexpr bool ROW = BLOCK == OZ_BLOCK_ROW || BLOCK == OZ_BLOCK_BOTH, COLUMN = BLOCK == OZ_BLOCK_COLUMN || BLOCK == OZ_BLOCK_BOTH;
+  constexpr bool MATRIX = BLOCK == OZ_BLOCK_MATRIX;
+  __shared__ int off[COLUMN ? OZ_MAX_GROUPS + 1 : 1];
+  __shared__ uint32_t most[kThreads / 32][TILE];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c8 = 8 * (threadIdx.x & 15), r0 = threadIdx.x >> 4;
+  let_next_start();
+  wait_for_previous();
+  const bool ragged = COLUMN && a.offsets;
+  if (ragged) {
+    if (warp == 0 && clamp_offsets(a.offsets, a.groups, a.rows, off) && lane == 0 && blockIdx.x == 0) atomicExch(a.status, OZ_EINVAL);
+    __syncthreads();
+  }
+  for (long long tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+    const long long rt = tile / a.col_tiles;
+    const int c = static_cast<int>(tile - rt * a.col_tiles) * TILE + c8;
+    const int mat = MATRIX ? static_cast<int>(rt / a.row_tiles) : 0;
+    const int block = static_cast<int>(rt - static_cast<long long>(mat) * a.row_tiles);
+    int row = block * TILE, count = min(TILE, a.rows - row);  // the tile's first row, how many it has
+    if (ragged) {
+      int lo = 0, hi = a.groups;  // the last group whose first block is not past this one
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first_column_block(off[mid], mid) <= block) lo = mid; else hi = mid;
+      }
+      const int b = block - first_column_block(off[lo], lo);
+      row = off[lo] + b * TILE;
+      count = b < 0 ? 0 : max(0, min(TILE, off[lo + 1] - row));
+    }
+    const T* x = static_cast<const T*>(a.x) + mat * a.stride_x;
+    Eight<T> v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = r0 + 16 * i;
+      const T* from = x + static_cast<long long>(row + r) * a.ldx + c;
+      if (r < count && a.aligned && c + 8 <= a.k) {
+        v[i] = load_eight(from);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (r < count && c + e < a.k) v[i].e[e] = from[e];
+          else from_float(0.0f, v[i].e[e]);
+        }
+      }
+    }
+    uint32_t by_row[8], by_col[8] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      by_row[i] = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t m = magnitude(to_float(v[i].e[e]));
+        by_row[i] = max(by_row[i], m);
+        if (COLUMN) by_col[e] = max(by_col[e], m);
+      }
+    }
+    if (ROW) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) by_row[i] = max(by_row[i], __shfl_xor_sync(0xFFFFFFFFu, by_row[i], d));
+        const int r = r0 + 16 * i;
+        if (r < count) {
+          const float scale = scale_of<E5M2>(by_row[i]);
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = to_float(v[i].e[e]);
+          put_bytes(a.q + static_cast<long long>(row + r) * a.ldq, c, a.k, eight_bits<E5M2>(f, 1.0f / scale));
+          if (c8 == 0) a.s[c / TILE * a.lds + row + r] = scale;
+        }
+      }
+    }
+    if (COLUMN) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) by_col[e] = max(by_col[e], __shfl_xor_sync(0xFFFFFFFFu, by_col[e], 16));
+      if (lane < 16) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most[warp][c8 + e] = by_col[e];
+      }
+      __syncthreads();
+      float inverse[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) m = max(m, most[w][c8 + e]);
+        const float scale = scale_of<E5M2>(m);
+        inverse[e] = 1.0f / scale;
+        if (r0 == 0 && c + e < a.k) a.sc[block * a.ldsc + c + e] = scale;
+      }
+      // The rows as they are, or the block's own 128 with zeros behind the group's last.
+      const long long to = ragged ? static_cast<long long>(block) * TILE : row;
+      const int written = ragged ? TILE : count;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + 16 * i;
+        if (r < written) {
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = to_float(v[i].e[e]) * inverse[e];
+          put_bytes(a.qc + (to + r) * a.ldqc, c, a.k, r < count ? eight_bits<E5M2>(f, 1.0f) : make_uint2(0, 0));
+        }
+      }
+      __syncthreads();  // most is free again
+    }
+    if (MATRIX) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, by_row[i]);
+      m = __reduce_max_sync(0xFFFFFFFFu, m);
+      if (lane == 0) most[0][warp] = m;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) m = max(m, most[0][w]);
+      __syncthreads();
+      const float scale = scale_of<E5M2>(m), inverse = 1.0f / scale;
+      if (threadIdx.x == 0) a.s[(static_cast<long long>(mat) * a.row_tiles + block) * a.col_tiles + c / TILE] = scale;
+      uint8_t* q = a.q + mat * a.stride_q;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + 16 * i;
+        if (r < count) {
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = to_float(v[i].e[e]);
+          put_bytes(q + static_cast<long long>(row + r) * a.ldq, c, a.k, eight_bits<E5M2>(f, inverse));
+        }
+      }
+    }
+  }
+  // Rows that belong to no group are in no tile: a warp a block of 128.
+  if (ROW && ragged) {
+    const int lo = off[0], hi = off[a.groups];
+    const long long loose = static_cast<long long>(lo + a.rows - hi) * a.col_tiles;
+    for (long long i = blockIdx.x * (kThreads / 32) + warp; i < loose; i += gridDim.x * (kThreads / 32)) {
+      const int at = static_cast<int>(i / a.col_tiles), b = static_cast<int>(i - static_cast<long long>(at) * a.col_tiles);
+      const long long r = at < lo ? at : hi + at - lo;
+      const T* x = static_cast<const T*>(a.x) + r * a.ldx;
+      float f[8] = {};
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = b * TILE + lane + 32 * e;
+        if (c < a.k) f[e] = to_float(x[c]);
+        m = max(m, magnitude(f[e]));
+      }
+      const float scale = scale_of<E5M2>(__reduce_max_sync(0xFFFFFFFFu, m));
+      const uint2 v = eight_bits<E5M2>(f, 1.0f / scale);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = b * TILE + lane + 32 * e;
+        if (c < a.k) a.q[r * a.ldq + c] = static_cast<uint8_t>(v.x >> (8 * e));
+      }
+      if (lane == 0) a.s[b * a.lds + r] = scale;
+    }
+  }
+}
+
+template <class T, int BLOCK>
+cudaError_t launch_quantize(QuantParams a, bool e5m2, cudaStream_t stream) {
+  a.aligned = rows_aligned<T>(a.x, a.ldx, a.rows) && (a.mats == 1 || a.stride_x * sizeof(T) % 16 == 0);
+  const unsigned grid = static_cast<unsigned>(a.tiles < 1 << 20 ? a.tiles : 1 << 20);
+  return launch_overlapping(e5m2 ? quantize_kernel<T, BLOCK, true> : quantize_kernel<T, BLOCK, false>, dim3(grid), kThreads, 0, stream, a);
+}
+
+template <class T>
+cudaError_t launch_of_type(int block, const QuantParams& a, bool e5m2, cudaStream_t stream) {
+  switch (block) {
+    case OZ_BLOCK_ROW: return launch_quantize<T, OZ_BLOCK_ROW>(a, e5m2, stream);
+    case OZ_BLOCK_COLUMN: return launch_quantize<T, OZ_BLOCK_COLUMN>(a, e5m2, stream);
+    case OZ_BLOCK_BOTH: return launch_quantize<T, OZ_BLOCK_BOTH>(a, e5m2, stream);
+    default: return launch_quantize<T, OZ_BLOCK_MATRIX>(a, e5m2, stream);
+  }
+}
+
+// An 8-bit output: rows at multiples of 16 bytes.
+bool output_ok(const void* q, long long ldq, const float* s, long long k, long long rows) {
+  return rows == 0 || (q && s && (reinterpret_cast<uintptr_t>(q) & 15) == 0 && (reinterpret_cast<uintptr_t>(s) & 3) == 0 && ldq >= k &&
+         (rows <= 1 || ldq % 16 == 0));
+}
+
+}  // namespace
+}  // namespace oz
+
+using namespace oz;
+
+extern "C" {
+
+int ozaki_f8_column_blocks(int rows, int groups, int ragged) {
+  if (rows < 0 || groups < 1 || groups > OZ_MAX_GROUPS) return OZ_EINVAL;
+  return column_blocks(rows, groups, ragged != 0);
+}
+
+int ozaki_quantize_f8(int block, int k, int rows, int groups, int dtype, const void* X, int ldx, long long strideX,
+                      const int32_t* offsets, int type, void* Q, int ldq, long long strideQ, float* S, int lds, void* QC, int ldqc,
+                      float* SC, int ldsc, cudaStream_t stream) {
+  const bool matrix = block == OZ_BLOCK_MATRIX, row = block == OZ_BLOCK_ROW || block == OZ_BLOCK_BOTH;
+  const bool column = block == OZ_BLOCK_COLUMN || block == OZ_BLOCK_BOTH;
+  if (!matrix && !row && !column) return OZ_EINVAL;
+  if (k < 0 || rows < 0 || k > INT32_MAX - 1024 || rows > INT32_MAX - 1024 - 128 * (OZ_MAX_GROUPS + 1) || groups < 1) return OZ_EINVAL;
+  if (!matrix && (groups > OZ_MAX_GROUPS || (!offsets && groups != 1))) return OZ_EINVAL;
+  if (!column && offsets) return OZ_EINVAL;
+  if (!element_bytes(dtype) || (type != OZ_E4M3 && type != OZ_E5M2)) return OZ_EINVAL;
+  if (ldx < (k > 1 ? k : 1)) return OZ_EINVAL;
+  if (matrix && groups > 1 && (strideX < static_cast<long long>(ldx) * rows || strideQ < static_cast<long long>(ldq) * rows || strideQ % 16)) return OZ_EINVAL;
+  if (k == 0 || (rows == 0 && !(column && offsets))) return OZ_OK;
+  if ((!X && rows) || !element_aligned(X, dtype)) return OZ_EINVAL;
+  if ((row || matrix) && !output_ok(Q, ldq, S, k, matrix ? static_cast<long long>(rows) * groups : rows)) return OZ_EINVAL;
+  if (row && lds < rows) return OZ_EINVAL;
+  QuantParams a{};
+  a.row_tiles = matrix || !offsets ? column_blocks(rows, 1, false) : column_blocks(rows, groups, true);
+  if (column && (!output_ok(QC, ldqc, SC, k, offsets ? static_cast<long long>(a.row_tiles) * TILE : rows) || ldsc < k)) return OZ_EINVAL;
+  a.k = k;
+  a.rows = rows;
+  a.groups = groups;
+  a.mats = matrix ? groups : 1;
+  a.x = X;
+  a.ldx = ldx;
+  a.stride_x = strideX;
+  a.offsets = offsets;
+  a.q = static_cast<uint8_t*>(Q);
+  a.qc = static_cast<uint8_t*>(QC);
+  a.ldq = ldq;
+  a.stride_q = strideQ;
+  a.ldqc = ldqc;
+  a.s = S;
+  a.sc = SC;
+  a.lds = lds;
+  a.ldsc = ldsc;
+  a.col_tiles = column_blocks(k, 1, false);
+  a.tiles = static_cast<long long>(a.col_tiles) * a.row_tiles * a.mats;
+  a.status = device_status_ptr();
+  if (!a.status) return OZ_ECUDA;
+  const bool e5m2 = type == OZ_E5M2;
+  const cudaError_t e = dtype == OZ_BF16 ? launch_of_type<__nv_bfloat16>(block, a, e5m2, stream)
+                        : dtype == OZ_F16 ? launch_of_type<__half>(block, a, e5m2, stream)
+                                          : launch_of_type<float>(block, a, e5m2, stream);
+  return e == cudaSuccess ? OZ_OK : OZ_ECUDA;
+}
+
+}  // extern "C"

@@ -32,7 +32,11 @@ OZ_NOALLOC_SCRATCH_BYTES = 64 << 20
 OZ_SCALE_UNIFORM, OZ_SCALE_FAST, OZ_SCALE_ACCU = 0, 1, 2
 OZ_OZAKI1_RN, OZ_OZAKI1_EF, OZ_OZAKI1_HYBRID = 0, 1, 2
 OZ_BF16, OZ_F16, OZ_F32 = 1, 2, 3
-OZ_MAX_GROUPS, OZ_MAX_NS_STEPS = 1024, 32
+OZ_E4M3, OZ_E5M2 = 4, 5
+OZ_BLOCK_ROW, OZ_BLOCK_COLUMN, OZ_BLOCK_BOTH, OZ_BLOCK_MATRIX = 1, 2, 3, 4
+OZ_MAX_GROUPS, OZ_MAX_NS_STEPS, OZ_MAX_NORM_WIDTH = 1024, 32, 32768
+F8_BLOCK = 128
+F8_BLOCKS = {"row": OZ_BLOCK_ROW, "column": OZ_BLOCK_COLUMN, "both": OZ_BLOCK_BOTH, "matrix": OZ_BLOCK_MATRIX}
 OZAKI1_VARIANTS = {"rn": OZ_OZAKI1_RN, "ef": OZ_OZAKI1_EF, "hybrid": OZ_OZAKI1_HYBRID}
 SCALINGS = {"uniform": OZ_SCALE_UNIFORM, "fast": OZ_SCALE_FAST, "accu": OZ_SCALE_ACCU}
 
@@ -47,7 +51,7 @@ def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m fp64_gemm_emulation_gb300.build_lib`")
     lib = ctypes.CDLL(LIB_PATH)
-    I, L, P, S = ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p, ctypes.c_size_t
+    I, L, P, S, F = ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
     sig = {
         "ozaki2_moduli": (I, [I, P]),
         "ozaki2_choose_k": (I, [I, L, P]),
@@ -99,6 +103,18 @@ def _load():
         "ozaki_newton_schulz_workspace_bytes": (S, [I, I, I, I]),
         "ozaki_newton_schulz_ws": (I, [I, I, I, I, P, I, L, P, I, L, I, P, ctypes.c_float, I, P, S, P]),
         "ozaki_newton_schulz": (I, [I, I, I, I, P, I, L, P, I, L, I, P, ctypes.c_float, I, P]),
+        "ozaki_f8_column_blocks": (I, [I, I, I]),
+        "ozaki_quantize_f8": (I, [I, I, I, I, I, P, I, L, P, I, P, I, L, P, I, P, I, P, I, P]),
+        "ozaki_grouped_gemm_f8": (I, [I, I, I, I, I, P, I, L, P, I, P, I, P, I, P, I, P, I, P]),
+        "ozaki_grouped_gemm_f8_dgrad": (I, [I, I, I, I, I, P, I, L, P, I, P, I, P, I, P, I, P, I, P]),
+        "ozaki_grouped_gemm_f8_wgrad": (I, [I, I, I, I, I, P, I, P, I, I, P, I, P, I, P, I, P, I, L, P]),
+        "ozaki_rms_norm_f8": (I, [I, I, I, P, I, P, I, P, F, P, I, P, I, P, I, P, P, I, P]),
+        "ozaki_rms_norm_backward_workspace_bytes": (S, [I, I]),
+        "ozaki_rms_norm_backward_ws": (I, [I, I, I, P, I, P, I, P, P, P, I, P, I, P, P, S, P]),
+        "ozaki_rms_norm_backward": (I, [I, I, I, P, I, P, I, P, P, P, I, P, I, P, P]),
+        "ozaki_clip_grad_norm_workspace_bytes": (S, []),
+        "ozaki_clip_grad_norm_ws": (I, [I, P, P, P, P, F, F, P, P, S, P]),
+        "ozaki_clip_grad_norm": (I, [I, P, P, P, P, F, F, P, P]),
         "ozaki_get_device_status": (I, [P]),
         "ozaki_status_string": (ctypes.c_char_p, [I]),
         "ozaki_set_epilogue_wait_ns": (I, [L]),
@@ -787,6 +803,389 @@ def ozaki_newton_schulz(G, steps: int = 5, coeffs=NEWTON_SCHULZ_COEFFS, eps: flo
 def ozaki_newton_schulz_ws(G, workspace, **kwargs):
     """ozaki_newton_schulz with a caller-owned workspace (see ozaki_newton_schulz_workspace_bytes)."""
     return ozaki_newton_schulz(G, workspace=workspace, **kwargs)
+
+
+# ------------------------------------------------------------------ 8-bit operands with scales
+_F8_CODES: dict = {}
+
+
+def _f8(dtype) -> int:
+    if not _F8_CODES:
+        torch = _torch()
+        _F8_CODES.update({torch.float8_e4m3fn: OZ_E4M3, torch.float8_e5m2: OZ_E5M2})
+    code = _F8_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"8-bit type must be float8_e4m3fn or float8_e5m2: {dtype}")
+    return code
+
+
+def _new_f8(shape, dtype, device):
+    """A new 8-bit tensor whose rows start at multiples of 16 bytes."""
+    k = shape[-1]
+    if k % 16 == 0:
+        return _torch().empty(shape, dtype=dtype, device=device)
+    return _torch().empty((*shape[:-1], (k + 15) // 16 * 16), dtype=dtype, device=device)[..., :k]
+
+
+def _row_scales(S, what: str, rows: int, k: int, device) -> int:
+    """Leading dimension of the scales of row blocks: (rows, blocks) with the rows of a block next to each other."""
+    shape, blocks = S.shape, (k + 127) // 128
+    if S.dtype != _torch().float32 or S.device != device:
+        raise ValueError(f"{what} must be float32 on the operands' device")
+    if len(shape) != 2 or shape[0] != rows or shape[1] != blocks:
+        raise ValueError(f"{what} must have shape ({rows}, {blocks}): {tuple(shape)}")
+    stride = S.stride()
+    if (rows > 1 and stride[0] != 1) or (blocks > 1 and stride[1] < rows):
+        raise ValueError(f"{what} must be column-major (stride(0) == 1): colmajor makes it so")
+    return max(1, rows, stride[1] if blocks > 1 else 0)
+
+
+def _column_scales(S, what: str, blocks: int, k: int, device) -> int:
+    if S.dtype != _torch().float32 or S.device != device:
+        raise ValueError(f"{what} must be float32 on the operands' device")
+    if tuple(S.shape) != (blocks, k):
+        raise ValueError(f"{what} must have shape ({blocks}, {k}): {tuple(S.shape)}")
+    return _tokens(S, what, k)
+
+
+def _matrix_scales(S, what: str, shape, device):
+    want = (*shape[:-2], (shape[-2] + 127) // 128, (shape[-1] + 127) // 128)
+    if S.dtype != _torch().float32 or S.device != device or not S.is_contiguous():
+        raise ValueError(f"{what} must be contiguous float32 on the operands' device")
+    if S.shape != want:
+        raise ValueError(f"{what} must have shape {want}: {tuple(S.shape)}")
+
+
+def _f8_rows(Q, what: str, features: int | None = None) -> int:
+    """Leading dimension of an 8-bit operand, whose rows start at multiples of 16 bytes."""
+    ld = _tokens(Q, what, features)
+    if Q.numel() and (Q.data_ptr() % 16 or (Q.shape[0] > 1 and ld % 16)):
+        raise ValueError(f"{what} must have rows that start at multiples of 16 bytes")
+    return ld
+
+
+def _f8_experts(W, SW, device):
+    """(groups, n, k, row stride, matrix stride) of 8-bit weights (groups, n, k), or (n, k) for one group."""
+    if W.dim() == 2:
+        W, SW = W[None], (SW[None] if SW.dim() == 2 else SW)
+    ld, stride = _experts(W, "W")
+    groups, n, k = W.shape
+    if n and k and (W.data_ptr() % 16 or (n > 1 and ld % 16) or (groups > 1 and stride % 16)):
+        raise ValueError("W must have rows and matrices that start at multiples of 16 bytes")
+    if W.device != device:
+        raise ValueError("operands must share one device")
+    _matrix_scales(SW, "the scales of W", W.shape, device)
+    return groups, n, k, ld, stride
+
+
+def _cuda(t, what: str):
+    if t.device.type != "cuda":
+        raise ValueError(f"{what} must be a CUDA tensor")
+    return t.device
+
+
+def _product_offsets(offsets, groups: int | None, device):
+    if offsets is None:
+        if groups not in (None, 1):
+            raise ValueError(f"{groups} groups need offsets")
+        return None
+    _offsets(offsets, groups, device)
+    return offsets.data_ptr()
+
+
+def _output(out, what: str, shape, dtype, device):
+    """A new 16-bit output, or the given one, checked."""
+    if out is None:
+        if dtype is None:
+            dtype = _torch().bfloat16
+        out = _torch().empty(shape, dtype=dtype, device=device)
+    elif out.device != device or (dtype is not None and out.dtype != dtype):
+        raise ValueError(f"{what} must be on the operands' device, with the dtype asked for")
+    if out.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}: {tuple(out.shape)}")
+    code = _dtype(out)
+    if code == OZ_F32:
+        raise TypeError(f"{what} must be bfloat16 or float16")
+    return out, code
+
+
+def ozaki_f8_column_blocks(rows: int, groups: int | None = None) -> int:
+    """Blocks of 128 rows of one column: ceil(rows / 128), or with groups (offsets) rows // 128 + groups."""
+    n = int(_lib.ozaki_f8_column_blocks(rows, 1 if groups is None else groups, groups is not None))
+    if n < 0:
+        _check(n, "ozaki_f8_column_blocks")
+    return n
+
+
+def ozaki_quantize_f8(X, block: str = "row", offsets=None, dtype=None, stream=None):
+    """X (bfloat16, float16 or float32) in 8 bits (dtype: float8_e4m3fn, the default, or float8_e5m2), with a float32 scale for
+    each block of 128: X = Q * scale.  Returns new tensors; Q's rows start at multiples of 16 bytes.
+
+    block="row":    (Q, S)  128 neighbours of a row of X (rows, k): Q (rows, k), S (rows, ceil(k / 128)), column-major.
+    block="column": (Q, S)  128 rows of a column: S (blocks, k).  With offsets (groups + 1, int32) blocks start anew with each
+                    group: group e's rows lie from 128 * (offsets[e] // 128 + e) on, zeros behind its last one,
+                    in 128 * (rows // 128 + groups) rows of Q.
+    block="both":   (Q, S, Qc, Sc)  both of them in one pass (a gradient on its way into dgrad and wgrad).
+    block="matrix": (Q, S)  128 x 128 of each matrix of X (..., n, k): S (..., ceil(n / 128), ceil(k / 128)).
+
+    Row blocks do not depend on offsets.  A scale is the block's largest magnitude over the type's largest value, 1 for a
+    block of zeros; a block with Inf or NaN gets an Inf or NaN scale."""
+    if stream is not None and (other := _other_stream(stream, X.device)):
+        return _call_on(other, ozaki_quantize_f8, X, block, offsets, dtype)
+    torch = _torch()
+    kind = F8_BLOCKS.get(block)
+    if kind is None:
+        raise ValueError(f"block must be one of {sorted(F8_BLOCKS)}: {block!r}")
+    device, code = _cuda(X, "X"), _dtype(X)
+    if dtype is None:
+        dtype = torch.float8_e4m3fn
+    eight = _f8(dtype)
+    if kind == OZ_BLOCK_MATRIX:
+        if offsets is not None:
+            raise ValueError("matrix blocks have no offsets")
+        if X.dim() < 2:
+            raise ValueError("X must have shape (..., n, k)")
+        n, k = X.shape[-2:]
+        X3 = X if X.dim() == 3 else X[None] if X.dim() == 2 else X.view(-1, n, k)
+        ldx, sx = _experts(X3, "X")
+        mats = X3.shape[0]
+        Q = _new_f8(X.shape, dtype, device)
+        S = torch.empty((*X.shape[:-2], (n + 127) // 128, (k + 127) // 128), dtype=torch.float32, device=device)
+        ldq = (k + 15) // 16 * 16 or 16
+        if mats:
+            _run_on("ozaki_quantize_f8", (kind, k, n, mats, code, X.data_ptr(), ldx, sx, None, eight, Q.data_ptr(), ldq, ldq * n,
+                                          S.data_ptr(), 0, None, 0, None, 0), None, None, device)
+        return Q, S
+    ldx = _tokens(X, "X")
+    rows, k = X.shape
+    ldq = (k + 15) // 16 * 16 or 16
+    groups, off, results, args = 1, None, [], []
+    if offsets is not None:
+        _offsets(offsets, None, device)
+        if kind != OZ_BLOCK_ROW:
+            groups, off = offsets.numel() - 1, offsets.data_ptr()
+            if groups > OZ_MAX_GROUPS:
+                raise ValueError(f"at most {OZ_MAX_GROUPS} groups: {groups}")
+    if kind != OZ_BLOCK_COLUMN:
+        Q = _new_f8((rows, k), dtype, device)
+        S = torch.empty(((k + 127) // 128, rows), dtype=torch.float32, device=device)
+        results += [Q, S.t()]
+        args += [Q.data_ptr(), ldq, 0, S.data_ptr(), max(1, rows)]
+    else:
+        args += [None, 0, 0, None, 0]
+    if kind != OZ_BLOCK_ROW:
+        blocks = rows // 128 + groups if off else (rows + 127) // 128
+        Q = _new_f8((128 * blocks if off else rows, k), dtype, device)
+        S = torch.empty((blocks, k), dtype=torch.float32, device=device)
+        results += [Q, S]
+        args += [Q.data_ptr(), ldq, S.data_ptr(), max(1, k)]
+    else:
+        args += [None, 0, None, 0]
+    _run_on("ozaki_quantize_f8", (kind, k, rows, groups, code, X.data_ptr(), ldx, 0, off, eight, *args), None, None, device)
+    return tuple(results)
+
+
+def ozaki_grouped_gemm_f8(X, SX, W, SW, offsets=None, Y=None, dtype=None, stream=None):
+    """Y[r] = W[e] X[r] for the rows r of group e, from 8-bit operands and their scales (ozaki_quantize_f8).
+
+    X (rows, k) with SX in row blocks, W (groups, n, k) with SW in matrix blocks; Y (rows, n) is bfloat16 (or float16: dtype, or
+    a Y of that type).  offsets (groups + 1, int32) as in ozaki_grouped_gemm; None: one group of all rows, W (n, k) or (1, n, k).
+    X and W may each be float8_e4m3fn or float8_e5m2; their rows start at multiples of 16 bytes."""
+    if stream is not None and (other := _other_stream(stream, X.device)):
+        return _call_on(other, ozaki_grouped_gemm_f8, X, SX, W, SW, offsets, Y, dtype)
+    device = _cuda(X, "X")
+    groups, n, k, ldw, sw = _f8_experts(W, SW, device)
+    ldx, rows = _f8_rows(X, "X", k), X.shape[0]
+    lds = _row_scales(SX, "the scales of X", rows, k, device)
+    off = _product_offsets(offsets, groups, device)
+    Y, code = _output(Y, "Y", (rows, n), dtype, device)
+    ldy = _tokens(Y, "Y", n)
+    _run_on("ozaki_grouped_gemm_f8", (n, k, rows, groups, _f8(W.dtype), W.data_ptr(), ldw, sw, SW.data_ptr(), _f8(X.dtype), X.data_ptr(),
+                                      ldx, SX.data_ptr(), lds, off, code, Y.data_ptr(), ldy), None, None, device)
+    return Y
+
+
+def ozaki_grouped_gemm_f8_dgrad(dY, SdY, W, SW, offsets=None, dX=None, dtype=None, stream=None):
+    """dX[r] = W[e]^T dY[r]: the gradient in X; dY (rows, n) with SdY in row blocks, W and SW as in the forward product."""
+    if stream is not None and (other := _other_stream(stream, dY.device)):
+        return _call_on(other, ozaki_grouped_gemm_f8_dgrad, dY, SdY, W, SW, offsets, dX, dtype)
+    device = _cuda(dY, "dY")
+    groups, n, k, ldw, sw = _f8_experts(W, SW, device)
+    lddy, rows = _f8_rows(dY, "dY", n), dY.shape[0]
+    lds = _row_scales(SdY, "the scales of dY", rows, n, device)
+    off = _product_offsets(offsets, groups, device)
+    dX, code = _output(dX, "dX", (rows, k), dtype, device)
+    lddx = _tokens(dX, "dX", k)
+    _run_on("ozaki_grouped_gemm_f8_dgrad", (n, k, rows, groups, _f8(W.dtype), W.data_ptr(), ldw, sw, SW.data_ptr(), _f8(dY.dtype), dY.data_ptr(),
+                                            lddy, SdY.data_ptr(), lds, off, code, dX.data_ptr(), lddx), None, None, device)
+    return dX
+
+
+def ozaki_grouped_gemm_f8_wgrad(dY, SdY, X, SX, offsets=None, dW=None, dtype=None, rows: int | None = None, stream=None):
+    """dW[e] = sum over the rows r of group e of dY[r] X[r]^T: (groups, n, k), or (1, n, k) without offsets.
+
+    dY (laid, n) and X (laid, k) in column blocks with their scales (blocks, n) and (blocks, k).  With offsets they are laid
+    out by group as ozaki_quantize_f8 does, in 128 * (rows // 128 + groups) rows; rows, the number of tokens, is only
+    needed where offsets speak of other tokens than those (any number with the same rows // 128 serves)."""
+    if stream is not None and (other := _other_stream(stream, dY.device)):
+        return _call_on(other, ozaki_grouped_gemm_f8_wgrad, dY, SdY, X, SX, offsets, dW, dtype, rows)
+    device = _cuda(dY, "dY")
+    lddy, ldx = _f8_rows(dY, "dY"), _f8_rows(X, "X")
+    laid, n, k = dY.shape[0], dY.shape[1], X.shape[1]
+    if X.shape[0] != laid or X.device != device:
+        raise ValueError("X and dY must have the same rows, on one device")
+    off = _product_offsets(offsets, None, device)
+    if off is None:
+        groups, blocks = 1, (laid + 127) // 128
+        if rows not in (None, laid):
+            raise ValueError(f"without offsets the rows are those of dY and X: {laid}")
+        rows = laid
+    else:
+        groups, blocks = offsets.numel() - 1, laid // 128
+        if rows is None:  # the most tokens that are laid out in so many blocks
+            rows = max(0, 128 * (blocks - groups) + 127)
+        if laid != 128 * (rows // 128 + groups):
+            raise ValueError(f"with offsets X and dY must have 128 * (rows // 128 + groups) rows: {laid}")
+    ldsy, ldsx = _column_scales(SdY, "the scales of dY", blocks, n, device), _column_scales(SX, "the scales of X", blocks, k, device)
+    dW, code = _output(dW, "dW", (groups, n, k), dtype, device)
+    ldw, sw = _experts(dW, "dW")
+    _run_on("ozaki_grouped_gemm_f8_wgrad", (n, k, rows, groups, _f8(dY.dtype), dY.data_ptr(), lddy, SdY.data_ptr(), ldsy, _f8(X.dtype),
+                                            X.data_ptr(), ldx, SX.data_ptr(), ldsx, off, code, dW.data_ptr(), ldw, sw), None, None, device)
+    return dW
+
+
+# ------------------------------------------------------------------ root-mean-square norm
+def _norm_rows(t, what: str, rows: int, k: int, like) -> int:
+    if t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{what} must have X's dtype and device")
+    if t.shape[0] != rows:
+        raise ValueError(f"{what} must have {rows} rows")
+    return _tokens(t, what, k)
+
+
+def _norm_weight(W, k: int, like):
+    if W.dtype != like.dtype or W.device != like.device or W.shape != (k,) or not W.is_contiguous():
+        raise ValueError(f"W must be a contiguous vector of {k} values with the operands' dtype and device")
+
+
+def ozaki_rms_norm_f8(X, W, residual=None, eps: float = 1e-6, H=None, Y=None, stream=None):
+    """h = X + residual, y = h / sqrt(mean(h^2) + eps) * W for each row of X (rows, k): (Q, S, H, rstd).
+
+    Q (float8_e4m3fn) and S are y in row blocks, ready for ozaki_grouped_gemm_f8; H is h in X's dtype (X itself without a
+    residual) and rstd (rows, float32) the rows' 1 / sqrt(...), which ozaki_rms_norm_backward needs.  H: where to write it (may
+    be X or residual); Y: where to write y in X's dtype too.  X is bfloat16, float16 or float32, k <= OZ_MAX_NORM_WIDTH."""
+    if stream is not None and (other := _other_stream(stream, X.device)):
+        return _call_on(other, ozaki_rms_norm_f8, X, W, residual, eps, H, Y)
+    torch = _torch()
+    device, code = _cuda(X, "X"), _dtype(X)
+    ldx = _tokens(X, "X")
+    rows, k = X.shape
+    if k > OZ_MAX_NORM_WIDTH:
+        raise ValueError(f"at most {OZ_MAX_NORM_WIDTH} features: {k}")
+    _norm_weight(W, k, X)
+    least = max(1, k)
+    ldr = ldh = ldy = least
+    if residual is not None:
+        ldr = _norm_rows(residual, "residual", rows, k, X)
+        if H is None:
+            H = torch.empty((rows, k), dtype=X.dtype, device=device)
+    if H is not None:
+        ldh = _norm_rows(H, "H", rows, k, X)
+    if Y is not None:
+        ldy = _norm_rows(Y, "Y", rows, k, X)
+    Q = _new_f8((rows, k), torch.float8_e4m3fn, device)
+    S = torch.empty(((k + 127) // 128, rows), dtype=torch.float32, device=device)
+    rstd = torch.empty(rows, dtype=torch.float32, device=device)
+    _run_on("ozaki_rms_norm_f8", (k, rows, code, X.data_ptr(), ldx, _ptr(residual), ldr, W.data_ptr(), float(eps), Q.data_ptr(),
+                                  (k + 15) // 16 * 16 or 16, S.data_ptr(), max(1, rows), _ptr(H), ldh, rstd.data_ptr(), _ptr(Y), ldy),
+            None, None, device)
+    return Q, S.t(), X if H is None else H, rstd
+
+
+def ozaki_rms_norm_backward(dY, H, W, rstd, dH=None, dX=None, workspace=None, stream=None):
+    """The gradients of a loss in X (and the residual, the same) and in W: (dX, dW).
+
+    dY (rows, k): its gradient in y; H and rstd: the forward's; dH: its gradient in h by other paths (the residual stream).  dX
+    may be dY, H or dH.  Sums are float32; dX and dW have dY's dtype."""
+    if stream is not None and (other := _other_stream(stream, dY.device)):
+        return _call_on(other, ozaki_rms_norm_backward, dY, H, W, rstd, dH, dX, workspace)
+    torch = _torch()
+    device, code = _cuda(dY, "dY"), _dtype(dY)
+    lddy = _tokens(dY, "dY")
+    rows, k = dY.shape
+    if k > OZ_MAX_NORM_WIDTH:
+        raise ValueError(f"at most {OZ_MAX_NORM_WIDTH} features: {k}")
+    ldh = _norm_rows(H, "H", rows, k, dY)
+    _norm_weight(W, k, dY)
+    if rstd.dtype != torch.float32 or rstd.device != device or rstd.shape != (rows,) or not rstd.is_contiguous():
+        raise ValueError(f"rstd must be a contiguous float32 vector of {rows} values on the operands' device")
+    lddh = _norm_rows(dH, "dH", rows, k, dY) if dH is not None else max(1, k)
+    if dX is None:
+        dX = torch.empty((rows, k), dtype=dY.dtype, device=device)
+    lddx = _norm_rows(dX, "dX", rows, k, dY)
+    dW = torch.empty(k, dtype=dY.dtype, device=device)
+    _run_on("ozaki_rms_norm_backward", (k, rows, code, dY.data_ptr(), lddy, H.data_ptr(), ldh, W.data_ptr(), rstd.data_ptr(), _ptr(dH), lddh,
+                                        dX.data_ptr(), lddx, dW.data_ptr()), workspace, None, device)
+    return dX, dW
+
+
+def ozaki_rms_norm_backward_ws(dY, H, W, rstd, workspace, dH=None, dX=None, stream=None):
+    """ozaki_rms_norm_backward with a caller-owned workspace (see ozaki_rms_norm_backward_workspace_bytes)."""
+    return ozaki_rms_norm_backward(dY, H, W, rstd, dH, dX, workspace, stream)
+
+
+def ozaki_rms_norm_backward_workspace_bytes(k: int, rows: int) -> int:
+    """Device workspace of ozaki_rms_norm_backward_ws."""
+    return int(_lib.ozaki_rms_norm_backward_workspace_bytes(k, rows))
+
+
+# ------------------------------------------------------------------ clipping by the global norm
+def ozaki_clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None, workspace=None, stream=None):
+    """The 2-norm over all tensors of grads (a float32 scalar on the device), each of which is multiplied by
+    min(1, max_norm / (norm + eps)): in place, or into the tensors of out.
+
+    Tensors are contiguous, bfloat16, float16 or float32 (each its own), on one device; out has their shapes and dtypes, and each of
+    its tensors is its gradient itself or does not overlap any.  A norm of Inf makes the factor 0, one of NaN makes it NaN."""
+    torch = _torch()
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if not grads:
+        raise ValueError("no gradients")
+    device = _cuda(grads[0], "gradients")
+    if stream is not None and (other := _other_stream(stream, device)):
+        result = _call_on(other, ozaki_clip_grad_norm, grads, max_norm, eps, out, workspace)
+        for t in (*grads, *outs):
+            t.record_stream(other)
+        return result
+    if len(outs) != len(grads):
+        raise ValueError(f"out must hold {len(grads)} tensors: {len(outs)}")
+    _dtype(grads[0])
+    try:
+        codes = [_DTYPE_CODES[t.dtype] for t in grads]
+    except KeyError as e:
+        raise TypeError(f"dtype must be bfloat16, float16 or float32: {e}") from None
+    n = len(grads)
+    tensors = grads if outs is grads else grads + outs
+    if any([t.device != device for t in tensors]) or not all([t.is_contiguous() for t in tensors]):
+        raise ValueError("gradients and outputs must be contiguous CUDA tensors on one device")
+    if outs is not grads and any([a.dtype != b.dtype or a.shape != b.shape for a, b in zip(grads, outs)]):
+        raise ValueError("outputs must have their gradients' shapes and dtypes")
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    pointers = (ctypes.c_void_p * n)(*[t.data_ptr() for t in grads])
+    to = pointers if outs is grads else (ctypes.c_void_p * n)(*[t.data_ptr() for t in outs])
+    _run_on("ozaki_clip_grad_norm", (n, (ctypes.c_int * n)(*codes), pointers, to, (ctypes.c_longlong * n)(*[t.numel() for t in grads]),
+                                     float(max_norm), float(eps), norm.data_ptr()), workspace, None, device)
+    return norm
+
+
+def ozaki_clip_grad_norm_ws(grads, max_norm: float, workspace, eps: float = 1e-6, out=None, stream=None):
+    """ozaki_clip_grad_norm with a caller-owned workspace (see ozaki_clip_grad_norm_workspace_bytes)."""
+    return ozaki_clip_grad_norm(grads, max_norm, eps, out, workspace, stream)
+
+
+def ozaki_clip_grad_norm_workspace_bytes() -> int:
+    """Device workspace of ozaki_clip_grad_norm_ws."""
+    return int(_lib.ozaki_clip_grad_norm_workspace_bytes())
 
 
 # ------------------------------------------------------------------ Scheme I variants

@@ -416,6 +416,114 @@ int ozaki_newton_schulz_ws(int m, int n, int batch, int dtype, const void* G, in
 int ozaki_newton_schulz(int m, int n, int batch, int dtype, const void* G, int ldg, long long strideG, void* O, int ldo,
                         long long strideO, int steps, const float* coeffs, float eps, int num_slices, cudaStream_t stream);
 
+/* ---------------------------------------------------------------- 8-bit operands with scales */
+
+/* 8-bit floating-point values with an FP32 scale for each block of 128: value = q * scale. */
+#define OZ_E4M3 4
+#define OZ_E5M2 5
+
+/* The blocks.  A token's (or an output feature's) k inputs are contiguous, as above: a k x rows matrix.
+ *   OZ_BLOCK_ROW     128 neighbours of one token's features, the last block shorter: what a sum over the
+ *                    features needs.  Scale (token r, block b) is S[b * lds + r], lds >= rows.
+ *   OZ_BLOCK_COLUMN  128 tokens of one feature: what a sum over tokens (wgrad) needs.  Scale (block b, feature c) is
+ *                    SC[b * ldsc + c], ldsc >= k.  Without offsets the tokens lie as they are in X, the last
+ *                    block is shorter.  With offsets the blocks start anew with each group: group e's first
+ *                    block is number offsets[e] / 128 + e, its tokens lie from 128 times that on, and what is
+ *                    left of its last block is zero; ozaki_f8_column_blocks(rows, groups, 1) = rows / 128 + groups
+ *                    blocks in all (a block that no group uses: zeros, scale 1).
+ *   OZ_BLOCK_BOTH    both of them from one pass over X.
+ *   OZ_BLOCK_MATRIX  128 x 128 of each k x rows matrix of a batch (weights): scale (block i of the rows, block j of
+ *                    the k) of matrix e is S[(e * ceil(rows / 128) + i) * ceil(k / 128) + j]. */
+#define OZ_BLOCK_ROW 1
+#define OZ_BLOCK_COLUMN 2
+#define OZ_BLOCK_BOTH 3
+#define OZ_BLOCK_MATRIX 4
+
+/* Blocks of 128 tokens of `rows` tokens: ceil(rows / 128), or with offsets (ragged) rows / 128 + groups.  A negative
+ * oz_status on invalid arguments.  No GPU needed. */
+int ozaki_f8_column_blocks(int rows, int groups, int ragged);
+
+/* X (OZ_BF16, OZ_F16 or OZ_F32; ldx >= k) in 8 bits (type: OZ_E4M3 or OZ_E5M2): a block's scale is its largest magnitude
+ * over the type's largest value (448, 57344), not below 2^-126, and 1 for a block of zeros; q is x / scale to
+ * the nearest (through the scale's reciprocal: a quotient within 2^-22 of the middle between two values may go
+ * to either).  A block that holds Inf or NaN gets an Inf or NaN scale, and everything computed from it is NaN or Inf.
+ *  - Q and S: OZ_BLOCK_ROW, _BOTH, _MATRIX.  QC and SC: OZ_BLOCK_COLUMN, _BOTH.  The others are not used.
+ *  - groups: the matrices of OZ_BLOCK_MATRIX (strideX, strideQ between them), or the groups of `offsets` (device
+ *    memory, groups + 1 ints, as in the grouped products, clamped and reported likewise), 1 without them.
+ *    offsets: OZ_BLOCK_COLUMN and _BOTH only.
+ *  - Q and QC start at multiples of 16 bytes, and so do their columns (ldq, ldqc, strideQ).  X may have any address and
+ *    leading dimension of its element's alignment; multiples of 16 bytes are read faster.
+ *  - Bytes of Q and QC between a column's k values and the next column are left as they were.
+ *  - Outputs must overlap neither X nor each other. */
+int ozaki_quantize_f8(int block, int k, int rows, int groups, int dtype, const void* X, int ldx, long long strideX,
+                      const int32_t* offsets, int type, void* Q, int ldq, long long strideQ, float* S, int lds, void* QC, int ldqc,
+                      float* SC, int ldsc, cudaStream_t stream);
+
+/* The grouped products of 8-bit operands with scales, and their gradients:
+ *   ozaki_grouped_gemm_f8        Y_e  = W_e^T X_e     W in OZ_BLOCK_MATRIX blocks, X in OZ_BLOCK_ROW ones
+ *   ozaki_grouped_gemm_f8_dgrad  dX_e = W_e dY_e      W in OZ_BLOCK_MATRIX blocks, dY in OZ_BLOCK_ROW ones (along n)
+ *   ozaki_grouped_gemm_f8_wgrad  dW_e = X_e dY_e^T    both in OZ_BLOCK_COLUMN blocks
+ * Shapes, groups and offsets as in ozaki_grouped_gemm; offsets == NULL (with groups == 1): one group of all rows, a
+ * dense layer.  Each operand is OZ_E4M3 or OZ_E5M2 (type_*), the output OZ_BF16 or OZ_F16 (dtype).
+ *  - A block's 128 products are summed by the tensor cores, scaled in FP32 and added to FP32 sums; the result is rounded once.
+ *  - Scales: any FP32 numbers (SW, SX, SdY, laid out as above).
+ *  - Operands start at multiples of 16 bytes, and so do their columns and matrices; OZ_EINVAL otherwise (quantised
+ *    operands are made that way).
+ *  - wgrad with offsets: rows is the number of tokens that the offsets speak of; X and dY hold the
+ *    128 * (rows / 128 + groups) laid-out rows, with zeros behind each group's last one.
+ *  - Empty groups, rows outside every group, sums of length 0, Inf and NaN as in ozaki_grouped_gemm, except
+ *    that a scale of Inf or NaN reaches every result that its block enters.
+ *  - No workspace.  Outputs must not overlap operands. */
+int ozaki_grouped_gemm_f8(int n, int k, int rows, int groups, int type_w, const void* W, int ldw, long long strideW, const float* SW,
+                          int type_x, const void* X, int ldx, const float* SX, int ldsx, const int32_t* offsets, int dtype, void* Y,
+                          int ldy, cudaStream_t stream);
+int ozaki_grouped_gemm_f8_dgrad(int n, int k, int rows, int groups, int type_w, const void* W, int ldw, long long strideW, const float* SW,
+                                int type_dy, const void* dY, int lddy, const float* SdY, int ldsdy, const int32_t* offsets, int dtype,
+                                void* dX, int lddx, cudaStream_t stream);
+int ozaki_grouped_gemm_f8_wgrad(int n, int k, int rows, int groups, int type_dy, const void* dY, int lddy, const float* SdY, int ldsdy,
+                                int type_x, const void* X, int ldx, const float* SX, int ldsx, const int32_t* offsets, int dtype,
+                                void* dW, int ldw, long long strideW, cudaStream_t stream);
+
+/* ---------------------------------------------------------------- root-mean-square norm into 8 bits */
+
+/* For each token (column of X, k features): h = x + residual, rstd = 1 / sqrt(mean(h^2) + eps), y = h rstd W (feature by
+ * feature), and y in OZ_E4M3 with OZ_BLOCK_ROW scales.  Elements of X, residual, W, H and Y are of dtype (OZ_BF16, OZ_F16 or
+ * OZ_F32), any address and leading dimension; everything is computed in FP32 from the unrounded h and each output rounded once.
+ *  - residual may be NULL (h = x).  H (k x rows, the sum, rounded) and Y (k x rows, y rounded) are written where not NULL;
+ *    their leading dimensions are >= k in any case.  H may be X or residual.
+ *  - Q, S as OZ_BLOCK_ROW's of ozaki_quantize_f8.  rstd: rows floats.
+ *  - eps >= 0.  A token with Inf or NaN (or whose squares pass the range of FP32) gives NaN or zeros of its own; no
+ *    other token sees it.  k <= OZ_MAX_NORM_WIDTH.  k or rows equal to 0: nothing is done. */
+#define OZ_MAX_NORM_WIDTH 32768
+int ozaki_rms_norm_f8(int k, int rows, int dtype, const void* X, int ldx, const void* residual, int ldr, const void* W, float eps,
+                      void* Q, int ldq, float* S, int lds, void* H, int ldh, float* rstd, void* Y, int ldy, cudaStream_t stream);
+
+/* The gradients for dY = dL/dy (k x rows), the forward's h and rstd, and dH = dL/dh by other paths (NULL: none), with
+ * g = dy W:  dX = dH + rstd (g - h rstd^2 mean(g h)), which is dL/dx and dL/dresidual alike, and dW = sum over the
+ * tokens of dy h rstd (k values; rows equal to 0: zeros).  All of dtype; sums are FP32.  dX may be dY, H or dH.  Results
+ * do not depend on timing.  The workspace is 256-byte aligned (OZ_ENOMEM if too small). */
+size_t ozaki_rms_norm_backward_workspace_bytes(int k, int rows);
+int ozaki_rms_norm_backward_ws(int k, int rows, int dtype, const void* dY, int lddy, const void* H, int ldh, const void* W,
+                               const float* rstd, const void* dH, int lddh, void* dX, int lddx, void* dW, void* workspace,
+                               size_t ws_bytes, cudaStream_t stream);
+int ozaki_rms_norm_backward(int k, int rows, int dtype, const void* dY, int lddy, const void* H, int ldh, const void* W,
+                            const float* rstd, const void* dH, int lddh, void* dX, int lddx, void* dW, cudaStream_t stream);
+
+/* ---------------------------------------------------------------- clipping by the global norm */
+
+/* norm = the 2-norm over all elements of `count` tensors, and outs[i] = grads[i] * min(1, max_norm / (norm + eps)) for each.
+ * dtypes (OZ_BF16, OZ_F16 or OZ_F32 of tensor i and its output), grads, outs and counts (elements) are HOST arrays of `count` entries,
+ * read before the call returns; the tensors are contiguous DEVICE memory and norm is one DEVICE float.
+ *  - outs[i] may be grads[i] (in place: nothing is written where the factor is 1); otherwise they must not overlap.
+ *  - Squares are summed in FP32 32 at a time and in FP64 from there on, without overflow or underflow.
+ *  - A norm of Inf makes the factor 0, one of NaN makes it NaN.  No tensor or element: norm 0.
+ *  - count <= 40960, max_norm >= 0, eps >= 0.  The result does not depend on timing. */
+size_t ozaki_clip_grad_norm_workspace_bytes(void);
+int ozaki_clip_grad_norm_ws(int count, const int* dtypes, const void* const* grads, void* const* outs, const long long* counts,
+                            float max_norm, float eps, float* norm, void* workspace, size_t ws_bytes, cudaStream_t stream);
+int ozaki_clip_grad_norm(int count, const int* dtypes, const void* const* grads, void* const* outs, const long long* counts,
+                         float max_norm, float eps, float* norm, cudaStream_t stream);
+
 /* ---------------------------------------------------------------- status */
 
 /* Waits for the work queued on `stream` (0 = legacy default stream), then returns the

@@ -1,17 +1,26 @@
 // oz_block8.cu -- products of 8-bit floating-point matrices with a 32-bit scale for each block of 128,
 // grouped by expert as oz_grouped.cu's, and their gradients.
 //
-//   forward  Y_e = W_e^T X_e     D[n, row] = sum_b sw[e, n/128, b] sx[row, b] sum_{k in b} W_e[k, n] X[k, row]
-//   dgrad    dX_e = W_e dY_e     D[k, row] = sum_b sw[e, b, k/128] sy[row, b] sum_{n in b} W_e[k, n] dY[n, row]
+//   forward  Y_e = W_e^T X_e     D[row, n] = sum_b sx[row, b] sw[e, n/128, b] sum_{k in b} X[k, row] W_e[k, n]
+//   dgrad    dX_e = W_e dY_e     D[row, k] = sum_b sy[row, b] sw[e, b, k/128] sum_{n in b} dY[n, row] W_e[k, n]
 //   wgrad    dW_e = X_e dY_e^T   D[k, n]   = sum_b sx[b, k] sy[b, n] sum_{row in b} X[k, row] dY[n, row]
 // (column-major; b runs over the blocks of 128 of the sum's index).  A block's products are summed by the
 // tensor cores (kind::f8f6f4, FP32 sums of 128 products) and its sum is scaled and added to FP32 sums in
 // registers, rounding to nearest: any FP32 scales are taken, and no sum is longer than 128 on the tensor cores.
 //
-// Kernel shape: clusters of two CTAs (cta_group::2), persistent over tiles of 256 m x up to 256 n, m along
-// the output's contiguous dimension, so that a CTA's 128 m share one row of the weights' scales.
-//   warp 0: TMA producer   warp 1: TMEM owner + MMA issuer (leader)   warp 2: scales   warps 4-11: epilogue
-// 6 stages of 32 KB: 128 (or 64 ...) rows of 128 bytes of A and of B, K-major or MN-major as they lie in memory.
+// Kernel shape: clusters of two CTAs (cta_group::2), persistent over tiles of 256 m (the first index of D above) x
+// 256 n, 128 m in each CTA.
+//   warp 0: TMA producer   warp 1: TMEM owner + MMA issuer (leader)   warp 2: scales (wgrad)   warps 4-11: epilogue
+// 6 stages of 32 KB: 128 x 128 bytes of A and two tiles of 64 n of B, K-major or MN-major as they lie in memory.
+// What bounds it: every 128 k each of a CTA's 128 x 256 sums is read from tensor memory, scaled and added, while the
+// MMAs take 512 cycles.  So:
+//  - rows of tokens are m, one a lane (tcgen05.ld.32x32b): a lane needs one factor for its 128 columns, its row's
+//    scale times the one of the 128 features.  With features as m a lane needs every column's scale in
+//    a register: 128 KB a k-block through the 128 bytes a cycle of shared memory's way back, 1024 cycles.
+//  - wgrad has a scale for each row and column of a block.  It reads fragments (16x256b), where a lane's 32 sums are
+//    of 4 m x 8 n, although their way out of tensor memory is slower (560 cycles for 128 x 256, 32x32b: below 300).
+//  - the tile's halves of 128 columns are accumulators of their own, two each, and belong to 4 warps each: the way
+//    from the MMAs to the epilogue and back (about 1000 cycles with both CTAs' barriers) overlaps more.
 #include "oz_products.cuh"
 #include "oz_ragged.cuh"
 
@@ -24,8 +33,10 @@ constexpr int BK8 = kScaleBlock;
 constexpr int STEP8 = 32;                       // k of one MMA
 constexpr int STAGES8 = 6;
 constexpr uint32_t TILE8 = 128 * BK8;           // bytes of a stage's A (and of its B) in one CTA
+constexpr uint32_t HALF8 = 64 * BK8;            // of the 64 n that a CTA holds of one accumulator
+constexpr int ACC8 = 128;                       // columns of an accumulator; two for each half of the tile
 constexpr int EPI8_FIRST = 4, EPI8_WARPS = 8, THREADS8 = (EPI8_FIRST + EPI8_WARPS) * 32;
-constexpr int BLOCKS8 = 4;                      // blocks of 32 columns whose sums a warp holds
+constexpr int BLOCKS8 = ACC8 / 32;              // blocks of 32 columns whose sums a warp holds
 constexpr uint32_t STASH8 = 32 * 64;
 // Registers: the four warps of the first warpgroup give theirs to the epilogue, whose threads hold 128 sums.
 // 128 x 72 + 256 x 216 = 384 x 168, what the launch has.
@@ -33,36 +44,41 @@ constexpr int REGS_FEW = 72, REGS_MANY = 216;
 
 enum Op8 { kForward8, kDgrad8, kWgrad8 };
 
+// wgrad: scales of a k-block in shared memory, 256 of n and 128 of the CTA's m.
+constexpr int SLOTS8 = 4, BATCH8 = 2, SLOT_FLOATS8 = 256 + 128;  // BATCH8: k-blocks whose scales are fetched at once
 template <Op8 OP>
-struct Scales8 {
-  static constexpr int SLOTS = OP == kWgrad8 ? 4 : 8;
-  static constexpr int BATCH = SLOTS / 2;       // k-blocks whose scales are fetched at once
-  static constexpr int FLOATS = OP == kWgrad8 ? 256 + 128 : 256;
-  static constexpr uint32_t BYTES = SLOTS * FLOATS * 4;
-};
+constexpr uint32_t kScaleBytes8 = OP == kWgrad8 ? SLOTS8 * SLOT_FLOATS8 * 4 : 0;
 
 struct Params8 {
-  CUtensorMap tmA, tmB, tmB128;
-  int M, N, K;    // contiguous extent of the output; wgrad: its rows; otherwise the sum's length
+  CUtensorMap tmA, tmA128, tmB;
+  int N, K;       // forward, dgrad: the output's contiguous extent, the sum's length
+  int M;          // wgrad: the output's contiguous extent (N: its rows)
   int groups, rows, bn;
   int vec, out_type;
   uint32_t idesc;
   const int32_t* offsets;
   void* out;
   long long ld, stride;
-  const float *sa, *sb;     // scales of A and B
-  long long sa_group, sb_ld;
-  int sa_m, sa_k;           // forward, dgrad: strides of a block along m and along the sum
+  const float *sa, *sb;       // scales of A and of B
+  long long sa_ld, sb_ld;     // distance of a row scale's (column scale's) blocks
+  long long sb_group;         // forward, dgrad: of the matrices' scales,
+  int sb_n, sb_k;             // and strides of a block along n and along the sum
   int* status;
   unsigned long long epi_wait_ns;
 };
 
-// Deals out the tiles, as GroupedWalk does: a group's rows in equal tiles (a multiple of 32 rows, at most bn) by
-// the output's m, the group's tiles by row tile; wgrad: the output's tiles of every group.
+struct Unit8 {
+  int m0, n0;       // the tile's first token (wgrad: first k) and first n
+  int mcount, ncount;  // how many of its 256 x bn exist
+  int group, kb0, kbs;  // kb0: the sum's first block of 128 (wgrad: of the laid-out rows)
+};
+
+// Deals out the tiles: a group's tokens in tiles of 256, each with all tiles of n in turn; wgrad: the output's
+// tiles of every group.
 template <Op8 OP>
 struct Walk8 {
-  static constexpr bool A_MN = OP != kForward8, B_MN = OP == kWgrad8, RAGGED_SUM = OP == kWgrad8;
-  static constexpr int BOX = 32;  // ragged rows: the small box of B (the large one has 128 rows)
+  static constexpr bool A_MN = OP == kWgrad8, B_MN = OP != kForward8, RAGGED_SUM = OP == kWgrad8;
+  static constexpr int BOX = 32;  // few tokens: the small box of A (the large one has 128 rows)
   static constexpr size_t kTableBytes = (2 * (OZ_MAX_GROUPS + 1) + 1) * 4;
 
   const Params8& a;
@@ -76,7 +92,7 @@ struct Walk8 {
     if (threadIdx.x == 0) {
       tma_prefetch_desc(&a.tmA);
       tma_prefetch_desc(&a.tmB);
-      if (!B_MN) tma_prefetch_desc(&a.tmB128);
+      if (!A_MN) tma_prefetch_desc(&a.tmA128);
     }
     let_next_start();
     wait_for_previous();
@@ -84,11 +100,11 @@ struct Walk8 {
     if (clamp_offsets(a.offsets, a.groups, a.rows, off) && lane == 0 && blockIdx.x == 0) atomicExch(a.status, OZ_EINVAL);
     __syncwarp();
     if (RAGGED_SUM) return;
-    const int tiles_m = ceil_div(a.M, BM);
+    const int tiles_n = ceil_div(a.N, a.bn);
     int sum = 0;
     for (int b = 0; b <= a.groups; b += 32) {
       const int i = b + lane;
-      int t = i >= 1 && i <= a.groups ? ceil_div(off[i] - off[i - 1], a.bn) * tiles_m : 0;
+      int t = i >= 1 && i <= a.groups ? ceil_div(off[i] - off[i - 1], BM) * tiles_n : 0;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xFFFFFFFFu, t, d);
@@ -100,57 +116,34 @@ struct Walk8 {
   }
 
   __device__ Walk8(const Params8& p, const int* table) : a(p), off(table), prefix(table + OZ_MAX_GROUPS + 1) {
-    tiles_m = ceil_div(a.M, BM);
-    tiles_n = RAGGED_SUM ? ceil_div(a.N, a.bn) : 0;
+    tiles_m = RAGGED_SUM ? ceil_div(a.M, BM) : 0;
+    tiles_n = ceil_div(a.N, a.bn);
     total = RAGGED_SUM ? a.groups * tiles_m * tiles_n : prefix[a.groups];
     idx = static_cast<int>(blockIdx.x >> 1) - static_cast<int>(gridDim.x >> 1);
   }
 
-  __device__ bool next(Unit& u) {
+  __device__ bool next(Unit8& u) {
     idx += static_cast<int>(gridDim.x >> 1);
     if (idx >= total) return false;
-    int group;
     if (RAGGED_SUM) {
       const int per = tiles_m * tiles_n;
-      group = idx / per;
-      const int r = idx - group * per, tn = r / tiles_m;
+      u.group = idx / per;
+      const int r = idx - u.group * per, tn = r / tiles_m;
       u.m0 = (r - tn * tiles_m) * BM;
-      u.n0 = u.orow = tn * a.bn;
-      u.nn = min(a.bn, a.N - u.n0);
-      u.kb1 = ceil_div(off[group + 1] - off[group], BK8);
-      u.k0 = a.offsets ? first_column_block(off[group], group) : 0;  // in blocks
-      u.zA = u.zB = 0;
-      u.nmma = BN;
+      u.mcount = min(BM, a.M - u.m0);
+      u.n0 = tn * a.bn;
+      u.kbs = ceil_div(off[u.group + 1] - off[u.group], BK8);
+      u.kb0 = a.offsets ? first_column_block(off[u.group], u.group) : 0;
     } else {
-      group = group_of(prefix, a.groups, idx);
-      const int r = idx - prefix[group], tn = r / tiles_m;
-      const int len = off[group + 1] - off[group];
-      const int w = ceil_div(ceil_div(len, ceil_div(len, a.bn)), 32) * 32;
-      u.m0 = (r - tn * tiles_m) * BM;
-      u.n0 = u.orow = off[group] + tn * w;
-      u.nn = min(w, len - tn * w);
-      u.kb1 = ceil_div(a.K, BK8);
-      u.k0 = 0;
-      u.zA = group;
-      u.zB = 0;
-      u.nmma = ceil_div(u.nn, 32) * 32;
+      u.group = group_of(prefix, a.groups, idx);
+      const int r = idx - prefix[u.group], tm = r / tiles_n;
+      u.m0 = off[u.group] + tm * BM;
+      u.mcount = min(BM, off[u.group + 1] - u.m0);
+      u.n0 = (r - tm * tiles_n) * a.bn;
+      u.kbs = ceil_div(a.K, BK8);
+      u.kb0 = 0;
     }
-    u.kb0 = 0;
-    u.a_mn = A_MN;
-    u.b_mn = B_MN;
-    const bool wide = u.nmma > 128;
-    u.mapA = &a.tmA;
-    u.mapB = !B_MN && wide ? &a.tmB128 : &a.tmB;
-    u.box_b = B_MN || wide ? 128 : BOX;
-    u.boxes = B_MN || wide ? 1 : ceil_div(u.nmma / 2, BOX);
-    u.box_bytes = u.box_b * BK8;
-    u.idesc = a.idesc | (static_cast<uint32_t>(u.nmma >> 3) << 17);
-    u.m_extent = a.M;
-    u.out = static_cast<uint16_t*>(a.out) + (RAGGED_SUM ? group * a.stride : 0);
-    u.ld = a.ld;
-    u.out_type = a.out_type;
-    u.vec = a.vec;
-    u.sym = false;
+    u.ncount = min(a.bn, a.N - u.n0);
     return true;
   }
 
@@ -160,18 +153,23 @@ struct Walk8 {
     const int lo = off[0], hi = off[a.groups], loose = lo + a.rows - hi;
     for (int i = static_cast<int>(blockIdx.x) * EPI8_WARPS + warp; i < loose; i += gridDim.x * EPI8_WARPS) {
       uint16_t* row = static_cast<uint16_t*>(a.out) + static_cast<long long>(i < lo ? i : hi + i - lo) * a.ld;
-      for (int c = threadIdx.x & 31; c < a.M; c += 32) row[c] = 0;
+      for (int c = threadIdx.x & 31; c < a.N; c += 32) row[c] = 0;
     }
   }
 };
 
+// High words of the shared-memory descriptors.  MN-major B lies in rows of 64 bytes, so that an accumulator's 64
+// columns of a CTA are a tile of their own: 64-byte swizzle, 8 k rows are 512 bytes.
+constexpr uint32_t DESC_HIGH_64 = (512u >> 4) | (1u << 14) | (4u << 29);
+
+template <uint32_t B_HIGH>
 __device__ __forceinline__ void umma8_pair(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
-      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(DESC_HIGH)
+      "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(DESC_HIGH), "r"(B_HIGH)
       : "memory");
 }
 
@@ -181,56 +179,56 @@ constexpr uint32_t idesc8_base(int fa, int fb, bool a_mn, bool b_mn) {
          (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(BM >> 4) << 24);
 }
 
-// Two neighbouring sums in one instruction: a += b s.
-__device__ __forceinline__ void fma_two(float& a0, float& a1, float b0, float b1, float2 s) {
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tmov.b64 z, {%4, %5};\n\t"
-      "fma.rn.f32x2 x, y, z, x;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "+f"(a0), "+f"(a1)
-      : "f"(b0), "f"(b1), "f"(s.x), "f"(s.y));
-}
-__device__ __forceinline__ float2 mul_two(float2 a, float b) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\t"
-      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b));
-  return r;
+// c += a b for an a from tensor memory.  volatile: stays behind the wait for the tensor-memory load.
+__device__ __forceinline__ void fma_loaded(float a, float b, float& c) { asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(c) : "f"(a), "f"(b)); }
+// Two neighbouring sums: c += v (b s).
+__device__ __forceinline__ void fma_loaded(float v0, float v1, float2 b, float s, float& c0, float& c1) {
+  asm volatile(
+      "{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%4, %5};\n\tmov.b64 y, {%6, %6};\n\tmul.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 y, {%2, %3};\n\tmov.b64 z, {%0, %1};\n\tfma.rn.f32x2 z, y, x, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "+f"(c0), "+f"(c1)
+      : "f"(v0), "f"(v1), "f"(b.x), "f"(b.y), "f"(s));
 }
 
-// A block's sums v, scaled, added to the running ones.  s: this block's 32 column scales in shared memory.
-// sm: wgrad's scales of this lane's four m (the others have theirs in s).
-template <Op8 OP>
-__device__ __forceinline__ void add_scaled(float (&run)[32], const float (&v)[32], const float* s, const float (&sm)[4]) {
+// 32 finished columns of this lane's row to the output: through the warp's stash, 16 bytes a lane, or, where not all of
+// them exist or stores cannot be wide, an element a lane.  row0, col: the block's first; rows, cols: how many exist.
+__device__ __forceinline__ void emit_rows(const Params8& a, const float (&v)[32], uint8_t* stash, long long row0, int rows, int col, int cols) {
   const int lane = threadIdx.x & 31;
+  uint32_t w[16];
+  pack_block(v, w, a.out_type == kOutBf16);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const float2 sn = *reinterpret_cast<const float2*>(s + 8 * q + 2 * (lane & 3));
+  for (int p = 0; p < 4; ++p) *reinterpret_cast<uint4*>(stash + stash_at(lane, p)) = make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
+  __syncwarp();
+  uint16_t* out = static_cast<uint16_t*>(a.out) + row0 * a.ld + col;
+  if (a.vec && cols >= 32) {
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {  // m = lane / 4 + 8 h
-      const int i = 16 * (h >> 1) + 4 * q + 2 * (h & 1);
-      fma_two(run[i], run[i + 1], v[i], v[i + 1], OP == kWgrad8 ? mul_two(sn, sm[h]) : sn);
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      if (r < rows) *reinterpret_cast<uint4*>(out + r * a.ld + 8 * (lane & 3)) = *reinterpret_cast<const uint4*>(stash + stash_at(r, lane & 3));
     }
+  } else if (lane < cols) {
+    for (int r = 0; r < min(rows, 32); ++r) out[r * a.ld + lane] = *reinterpret_cast<const uint16_t*>(stash + stash_at(r, lane >> 3) + (lane & 7) * 2);
   }
+  __syncwarp();
 }
 
 template <Op8 OP>
 __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_constant__ Params8 a) {
   typedef Walk8<OP> Walk;
-  typedef Scales8<OP> Sc;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + STAGES8 * TILE8;
   float* scales = reinterpret_cast<float*>(smem + 2 * STAGES8 * TILE8);
-  uint8_t* stash = smem + 2 * STAGES8 * TILE8 + Sc::BYTES;
+  uint8_t* stash = smem + 2 * STAGES8 * TILE8 + kScaleBytes8<OP>;
   uint64_t* bars = reinterpret_cast<uint64_t*>(stash + EPI8_WARPS * STASH8);
   uint64_t* full = bars;                     // [STAGES8] TMA (both CTAs) -> MMA  (used in the leader)
   uint64_t* empty = full + STAGES8;          // [STAGES8] MMA -> TMA              (both CTAs)
-  uint64_t* accfull = empty + STAGES8;       // [4]       MMA -> epilogue         (both CTAs)
-  uint64_t* accempty = accfull + 4;          // [4]       epilogues (both) -> MMA (used in the leader)
-  uint64_t* sfull = accempty + 4;            // [SLOTS]   scales -> epilogue      (per CTA)
-  uint64_t* sempty = sfull + Sc::SLOTS;      // [SLOTS]   epilogue -> scales      (per CTA)
-  uint64_t* drain = sempty + Sc::SLOTS;      // [1]       all MMAs of the pair done (both CTAs)
+  uint64_t* accfull = empty + STAGES8;       // [2][2]    MMA -> epilogue, by buffer and half (both CTAs)
+  uint64_t* accempty = accfull + 4;          // [2][2]    the half's warps (both) -> MMA (used in the leader)
+  uint64_t* sfull = accempty + 4;            // [SLOTS8]  scales -> epilogue      (per CTA)
+  uint64_t* sempty = sfull + SLOTS8;         // [SLOTS8]  epilogue -> scales      (per CTA)
+  uint64_t* drain = sempty + SLOTS8;         // [1]       all MMAs of the pair done (both CTAs)
   uint64_t* exitbar = drain + 1;             // [1]       the peer has finished (per CTA)
   uint64_t* proddone = exitbar + 1;          // [1]       both producers have stopped (used in the leader)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(proddone + 1);
@@ -240,7 +238,6 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const uint32_t acc_cols = a.bn > 128 ? 256 : 128, nacc = TMEM_COLS / acc_cols;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES8; ++i) {
@@ -249,9 +246,9 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&accfull[i], 1);
-      mbar_init(&accempty[i], 2 * EPI8_WARPS);
+      mbar_init(&accempty[i], EPI8_WARPS);  // four warps of either CTA
     }
-    for (int i = 0; i < Sc::SLOTS; ++i) {
+    for (int i = 0; i < SLOTS8; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&sempty[i], EPI8_WARPS);
     }
@@ -280,15 +277,19 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
         int stage = 0;
         uint32_t phase = 0, issued = 0;
         const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+        const int halves = a.bn / ACC8;
         Walk walk(a, table);
-        Unit u{};
+        Unit8 u{};
         bool ok = true;
         while (ok && !*abort_flag && walk.next(u)) {
-          const int rowA = u.m0 + static_cast<int>(rank) * HALF_M;
-          const int rowB = u.n0 + static_cast<int>(rank) * (u.nmma >> 1);
-          const uint32_t bytes = TILE8 + u.boxes * u.box_bytes;
-          int k = u.k0 * BK8;
-          for (int kb = 0; kb < u.kb1; ++kb, k += BK8) {
+          const int m = u.m0 + static_cast<int>(rank) * HALF_M;
+          // Tokens: only what the tile has, in one box of 128 or in boxes of 32.  What the stage holds in the other rows
+          // are sums of rows that are not stored.
+          const int have = min(HALF_M, u.mcount - static_cast<int>(rank) * HALF_M);
+          const bool whole = Walk::A_MN || have > 64;
+          const int boxes = whole ? 1 : max(0, ceil_div(max(have, 0), Walk::BOX));
+          const uint32_t bytes = (whole ? TILE8 : boxes * Walk::BOX * BK8) + halves * HALF8;
+          for (int kb = u.kb0; kb < u.kb0 + u.kbs; ++kb) {
             if (!mbar_wait_or_abort(&empty[stage], phase ^ 1, kWaitLimitNs, abort_flag)) {
               ok = false;
               break;
@@ -297,15 +298,20 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
             mbar_arrive_expect_tx_cluster(bar, bytes);
             uint8_t* dA = sA + stage * TILE8;
             uint8_t* dB = sB + stage * TILE8;
-            if (Walk::A_MN)
-              tma_load_3d_pair(dA, u.mapA, bar, rowA, k, u.zA);
-            else
-              tma_load_3d_pair(dA, u.mapA, bar, k, rowA, u.zA);
-            if (Walk::B_MN) {
-              tma_load_3d_pair(dB, u.mapB, bar, rowB, k, u.zB);
-            } else {
-              for (int b = 0; b < u.boxes; ++b) tma_load_3d_pair(dB + b * u.box_bytes, u.mapB, bar, k, rowB + u.box_b * b, u.zB);
+            const int k = kb * BK8;
+            for (int h = 0; h < halves; ++h) {
+              const int n = u.n0 + ACC8 * h + 64 * static_cast<int>(rank), z = OP == kWgrad8 ? 0 : u.group;
+              if (Walk::B_MN)
+                tma_load_3d_pair(dB + h * HALF8, &a.tmB, bar, n, k, z);
+              else
+                tma_load_3d_pair(dB + h * HALF8, &a.tmB, bar, k, n, z);
             }
+            if (Walk::A_MN)
+              tma_load_3d_pair(dA, &a.tmA, bar, m, k, 0);
+            else if (whole)
+              tma_load_3d_pair(dA, &a.tmA128, bar, k, m, 0);
+            else
+              for (int b = 0; b < boxes; ++b) tma_load_3d_pair(dA + b * Walk::BOX * BK8, &a.tmA, bar, k, m + Walk::BOX * b, 0);
             ++issued;
             if (++stage == STAGES8) {
               stage = 0;
@@ -334,31 +340,46 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
       if (rank == 0 && elect_one()) {
         // ------------------------------------------------------------ MMA issuer (leader only)
         int stage = 0;
-        uint32_t phase = 0, acc = 0, acc_phase = 1, consumed = 0;
+        uint32_t phase = 0, buf = 0, acc_phase = 1, consumed = 0;
         bool ok = true;
         const uint32_t a_desc = desc_low(smem_u32(sA), Walk::A_MN), b_desc = desc_low(smem_u32(sB), Walk::B_MN);
-        constexpr uint32_t a_step = (Walk::A_MN ? STEP8 * 128 : STEP8) >> 4, b_step = (Walk::B_MN ? STEP8 * 128 : STEP8) >> 4;
+        constexpr uint32_t a_step = (Walk::A_MN ? STEP8 * 128 : STEP8) >> 4, b_step = (Walk::B_MN ? STEP8 * 64 : STEP8) >> 4;
+        constexpr uint32_t B_HIGH = Walk::B_MN ? DESC_HIGH_64 : DESC_HIGH;
+        const uint32_t idesc = a.idesc;
+        const bool two_halves = a.bn > ACC8;
         Walk walk(a, table);
-        Unit u{};
+        Unit8 u{};
         while (ok && !*abort_flag && walk.next(u)) {
-          for (int left = u.kb1; left > 0; --left) {
-            if (!mbar_wait_or_abort(&accempty[acc], acc_phase, kWaitLimitNs, abort_flag) ||
-                !mbar_wait_or_abort(&full[stage], phase, kWaitLimitNs, abort_flag)) {
+          for (int left = u.kbs; left > 0; --left) {
+            if (!mbar_wait_or_abort(&full[stage], phase, kWaitLimitNs, abort_flag)) {
               ok = false;
               break;
             }
             ++consumed;
-            tc_fence_after();
             const uint32_t ad = a_desc + stage * (TILE8 >> 4), bd = b_desc + stage * (TILE8 >> 4);
-            const uint32_t d_tmem = tmem_base + acc * acc_cols;
-#pragma unroll
-            for (int kk = 0; kk < BK8 / STEP8; ++kk) umma8_pair(d_tmem, ad + kk * a_step, bd + kk * b_step, u.idesc, kk > 0 ? 1u : 0u);
-            umma_commit_pair(&empty[stage], 0x3);
-            umma_commit_pair(&accfull[acc], 0x3);
-            if (++acc == nacc) {
-              acc = 0;
-              acc_phase ^= 1;
+            if (!mbar_wait_or_abort(&accempty[2 * buf], acc_phase, kWaitLimitNs, abort_flag)) {
+              ok = false;
+              break;
             }
+            tc_fence_after();
+            const uint32_t d_tmem = tmem_base + buf * (2 * ACC8);
+#pragma unroll
+            for (int kk = 0; kk < BK8 / STEP8; ++kk) umma8_pair<B_HIGH>(d_tmem, ad + kk * a_step, bd + kk * b_step, idesc, kk > 0 ? 1u : 0u);
+            umma_commit_pair(&accfull[2 * buf], 0x3);
+            if (two_halves) {
+              if (!mbar_wait_or_abort(&accempty[2 * buf + 1], acc_phase, kWaitLimitNs, abort_flag)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < BK8 / STEP8; ++kk)
+                umma8_pair<B_HIGH>(d_tmem + ACC8, ad + kk * a_step, bd + (HALF8 >> 4) + kk * b_step, idesc, kk > 0 ? 1u : 0u);
+              umma_commit_pair(&accfull[2 * buf + 1], 0x3);
+            }
+            umma_commit_pair(&empty[stage], 0x3);
+            acc_phase ^= buf;
+            buf ^= 1;
             if (++stage == STAGES8) {
               stage = 0;
               phase ^= 1;
@@ -384,53 +405,42 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
         }
         umma_commit_pair(drain, 0x3);
       }
-    } else if (warp == 2) {
+    } else if (warp == 2 && OP == kWgrad8) {
       // -------------------------------------------------------------- scales (both CTAs)
-      // A slot holds a k-block's scales: for each of the tile's n, times the one of the CTA's 128 m (forward,
-      // dgrad); those of n and of m (wgrad).  BATCH blocks are fetched at once, while the epilogue uses the
-      // ones before.
+      // A slot holds a k-block's scales of the tile's n and of the CTA's m.  BATCH8 blocks are fetched at once, while
+      // the epilogue uses the ones before.
       int slot = 0;
       uint32_t sphase = 1;
       bool ok = true;
       Walk walk(a, table);
-      Unit u{};
+      Unit8 u{};
       while (ok && !*abort_flag && walk.next(u)) {
-        const int mblock = u.m0 / 128 + static_cast<int>(rank);
-        const bool inside = mblock * 128 < a.M;
-        const float* sa = OP == kWgrad8 ? a.sa + static_cast<long long>(u.k0) * a.sa_group + mblock * 128
-                                        : a.sa + u.zA * a.sa_group + static_cast<long long>(mblock) * a.sa_m;
-        const float* sb = a.sb + u.k0 * a.sb_ld + u.orow;
-        for (int kb = 0; ok && kb < u.kb1; kb += Sc::BATCH) {
-          float n[Sc::BATCH][8], m[Sc::BATCH][4];
+        const int m0 = u.m0 + static_cast<int>(rank) * HALF_M, mine = u.mcount - static_cast<int>(rank) * HALF_M;
+        const float* sm = a.sa + u.kb0 * a.sa_ld + m0;
+        const float* sn = a.sb + u.kb0 * a.sb_ld + u.n0;
+        for (int kb = 0; ok && kb < u.kbs; kb += BATCH8) {
+          float n[BATCH8][8], m[BATCH8][4];
 #pragma unroll
-          for (int j = 0; j < Sc::BATCH; ++j) {
-            const bool have = kb + j < u.kb1;
-            const float* row = sb + (kb + j) * a.sb_ld;
+          for (int j = 0; j < BATCH8; ++j) {
+            const bool have = kb + j < u.kbs;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) n[j][i] = have && lane + 32 * i < u.nn ? row[lane + 32 * i] : 0.0f;
-            if (OP == kWgrad8) {
-              const float* col = sa + (kb + j) * a.sa_group;
+            for (int i = 0; i < 8; ++i) n[j][i] = have && lane + 32 * i < u.ncount ? sn[(kb + j) * a.sb_ld + lane + 32 * i] : 0.0f;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) m[j][i] = have && mblock * 128 + lane + 32 * i < a.M ? col[lane + 32 * i] : 0.0f;
-            } else {
-              m[j][0] = have && inside ? sa[static_cast<long long>(kb + j) * a.sa_k] : 0.0f;
-            }
+            for (int i = 0; i < 4; ++i) m[j][i] = have && lane + 32 * i < mine ? sm[(kb + j) * a.sa_ld + lane + 32 * i] : 0.0f;
           }
 #pragma unroll
-          for (int j = 0; j < Sc::BATCH; ++j) {
-            if (kb + j < u.kb1 && ok) {
+          for (int j = 0; j < BATCH8; ++j) {
+            if (kb + j < u.kbs && ok) {
               ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&sempty[slot], sphase, kWaitLimitNs, abort_flag));
               if (ok) {
-                float* to = scales + slot * Sc::FLOATS;
+                float* to = scales + slot * SLOT_FLOATS8;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) to[lane + 32 * i] = OP == kWgrad8 ? n[j][i] : n[j][i] * m[j][0];
-                if (OP == kWgrad8) {
+                for (int i = 0; i < 8; ++i) to[lane + 32 * i] = n[j][i];
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) to[256 + lane + 32 * i] = m[j][i];
-                }
+                for (int i = 0; i < 4; ++i) to[256 + lane + 32 * i] = m[j][i];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sfull[slot]);
-                if (++slot == Sc::SLOTS) {
+                if (++slot == SLOTS8) {
                   slot = 0;
                   sphase ^= 1;
                 }
@@ -444,66 +454,159 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
   } else {
     // -------------------------------------------------------------- epilogue (both CTAs)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_MANY));
-    // A warp scales and sums its 32 lanes of every second block of 32 columns.
-    const int quad = warp & 3, first = (warp - EPI8_FIRST) >> 2;
+    // A warp scales and sums 32 lanes of one half's 128 columns.
+    const int quad = warp & 3, half = (warp - EPI8_FIRST) >> 2;
     uint8_t* my_stash = stash + (warp - EPI8_FIRST) * STASH8;
-    const uint32_t accempty_leader = mapa_shared(smem_u32(accempty), 0);
-    uint32_t acc = 0, acc_phase = 0, slot = 0, sphase = 0;
+    const uint32_t accempty_leader = mapa_shared(smem_u32(accempty), 0) + half * 8;
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + half * ACC8;
+    const int mrow = static_cast<int>(rank) * HALF_M + quad * 32;
+    uint32_t buf = 0, acc_phase = 0;
     bool ok = true;
     Walk walk(a, table);
     walk.outside(warp - EPI8_FIRST);
-    Unit u{};
-    while (ok && walk.next(u)) {
-      const int nblocks = ceil_div(u.nn, 32);
-      float run[BLOCKS8][32];
+    auto wait = [&](uint64_t* bar, uint32_t phase, uint64_t limit) {
+      if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, phase))) return true;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar, phase, limit, abort_flag));
+      if (!ok && lane == 0 && !*abort_flag) stop_pair(abort_flag, a.status);
+      return ok;
+    };
+    auto sums_there = [&]() {
+      const bool there = wait(&accfull[2 * buf + half], acc_phase, a.epi_wait_ns);
+      tc_fence_after();
+      return there;
+    };
+    // All of this warp's sums of an accumulator are in registers: it goes back to the MMAs.
+    auto release = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(accempty_leader + buf * 16);
+      acc_phase ^= buf;
+      buf ^= 1;
+    };
+    Unit8 u{};
+    if constexpr (OP != kWgrad8) {
+      while (ok && half * ACC8 < a.bn && walk.next(u)) {
+        const int rows = u.mcount - mrow, col = u.n0 + half * ACC8;
+        const int blocks = rows > 0 ? min(BLOCKS8, ceil_div(max(0, u.n0 + u.ncount - col), 32)) : 0;  // of 32 columns
+        float run[BLOCKS8][32];
 #pragma unroll
-      for (int i = 0; i < BLOCKS8 * 32; ++i) run[i >> 5][i & 31] = 0.0f;
-      for (int kb = 0; kb < u.kb1; ++kb) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_abort(&sfull[slot], sphase, kWaitLimitNs, abort_flag) &&
-                                         mbar_wait_or_abort(&accfull[acc], acc_phase, a.epi_wait_ns, abort_flag))) {
-          ok = false;
-          if (lane == 0 && !*abort_flag) stop_pair(abort_flag, a.status);
-          break;
-        }
-        tc_fence_after();
-        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * acc_cols;
-        const float* s = scales + slot * Sc::FLOATS;
-        float sm[4] = {};
-        if (OP == kWgrad8) {
-#pragma unroll
-          for (int h = 0; h < 4; ++h) sm[h] = s[256 + quad * 32 + (lane >> 2) + 8 * h];
-        }
-#pragma unroll
-        for (int j = 0; j < BLOCKS8; ++j) {
-          const int cb = 2 * j + first;
-          if (cb < nblocks) {
-            float v[32];
-            tmem_ld_block(taddr + cb * 32, v);
-            tmem_wait_block(v);
-            add_scaled<OP>(run[j], v, s + 32 * cb, sm);
+        for (int i = 0; i < BLOCKS8 * 32; ++i) run[i >> 5][i & 31] = 0.0f;
+        // This lane's row's scales and those of the half's features, fetched two k-blocks ahead and multiplied only when
+        // they are used (a product formed at once would wait for both).  Lanes without a row take the last one's.
+        const float* sx = a.sa + u.m0 + mrow + min(lane, rows - 1);
+        const float* sw = a.sb + u.group * a.sb_group + static_cast<long long>(col / 128) * a.sb_n;
+        float x0 = 0.0f, w0 = 0.0f, x1 = 0.0f, w1 = 0.0f;
+        if (blocks && u.kbs) {
+          x0 = x1 = *sx;
+          w0 = w1 = *sw;
+          if (u.kbs > 1) {
+            x1 = *(sx += a.sa_ld);
+            w1 = *(sw += a.sb_k);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_cluster(accempty_leader + acc * 8);
-          mbar_arrive(&sempty[slot]);
-        }
-        if (++acc == nacc) {
-          acc = 0;
-          acc_phase ^= 1;
-        }
-        if (++slot == Sc::SLOTS) {
-          slot = 0;
-          sphase ^= 1;
-        }
-      }
-      if (!ok) break;
-      const Target target = target_of(u, static_cast<int>(rank) * HALF_M + quad * 32, my_stash);
+        for (int kb = 0; kb < u.kbs && sums_there(); ++kb) {
+          const uint32_t from = lanes + buf * (2 * ACC8);
+          if (blocks == BLOCKS8) {  // a block is read while the one before it is scaled and added
+            uint32_t v[2][32];
+            tmem_ld32(from, v[0]);
+            const float f = x0 * w0;
+            x0 = x1, w0 = w1;
+            if (kb + 2 < u.kbs) {
+              x1 = *(sx += a.sa_ld);
+              w1 = *(sw += a.sb_k);
+            }
 #pragma unroll
-      for (int j = 0; j < BLOCKS8; ++j) {
-        const int cb = 2 * j + first;
-        if (cb < nblocks) emit<false, true>(u, target, run[j], cb, my_stash);
+            for (int j = 0; j < BLOCKS8; ++j) {
+              tmem_ld_wait();
+              if (j + 1 < BLOCKS8) tmem_ld32(from + 32 * (j + 1), v[(j + 1) & 1]);
+              else release();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) fma_loaded(__uint_as_float(v[j & 1][i]), f, run[j][i]);
+            }
+          } else if (blocks) {
+            const float f = x0 * w0;
+            x0 = x1, w0 = w1;
+            if (kb + 2 < u.kbs) {
+              x1 = *(sx += a.sa_ld);
+              w1 = *(sw += a.sb_k);
+            }
+#pragma unroll
+            for (int j = 0; j < BLOCKS8 - 1; ++j) {
+              if (j < blocks) {
+                uint32_t v[32];
+                tmem_ld32(from + 32 * j, v);
+                tmem_ld_wait();
+                if (j + 1 == blocks) release();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) fma_loaded(__uint_as_float(v[i]), f, run[j][i]);
+              }
+            }
+          } else {
+            release();
+          }
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < BLOCKS8; ++j)
+          if (j < blocks) emit_rows(a, run[j], my_stash, u.m0 + mrow, rows, col + 32 * j, u.n0 + u.ncount - col - 32 * j);
+      }
+    } else {
+      uint32_t slot = 0, sphase = 0;
+      while (ok && walk.next(u)) {
+        const int columns = min(ACC8, u.ncount - half * ACC8);
+        const int blocks = u.mcount > mrow ? max(0, ceil_div(max(0, columns), 32)) : 0;
+        float run[BLOCKS8][32];
+#pragma unroll
+        for (int i = 0; i < BLOCKS8 * 32; ++i) run[i >> 5][i & 31] = 0.0f;
+        for (int kb = 0; kb < u.kbs; ++kb) {
+          if (!wait(&sfull[slot], sphase, kWaitLimitNs) || !sums_there()) break;
+          const float* sn = scales + slot * SLOT_FLOATS8 + half * ACC8 + 2 * (lane & 3);
+          float sm[4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) sm[h] = scales[slot * SLOT_FLOATS8 + 256 + quad * 32 + (lane >> 2) + 8 * h];
+          const uint32_t from = lanes + buf * (2 * ACC8);
+#pragma unroll
+          for (int j = 0; j < BLOCKS8; ++j) {
+            if (j < blocks) {
+              float v[32];
+              float2 s[4];
+              tmem_ld_block(from + 32 * j, v);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) s[q] = *reinterpret_cast<const float2*>(sn + 32 * j + 8 * q);
+              tmem_ld_wait();
+              if (j + 1 == blocks) release();
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {  // m = lane / 4 + 8 h, n = 8 q + 2 (lane % 4), + 1
+                  const int i = 16 * (h >> 1) + 4 * q + 2 * (h & 1);
+                  fma_loaded(v[i], v[i + 1], s[q], sm[h], run[j][i], run[j][i + 1]);
+                }
+              }
+            }
+          }
+          if (blocks == 0) release();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sempty[slot]);
+          if (++slot == SLOTS8) {
+            slot = 0;
+            sphase ^= 1;
+          }
+        }
+        if (!ok) break;
+        Unit t{};  // as the 16-bit products' epilogue takes it
+        t.m0 = u.m0;
+        t.m_extent = a.M;
+        t.nn = u.ncount - half * ACC8;
+        t.orow = u.n0 + half * ACC8;
+        t.out = static_cast<uint16_t*>(a.out) + u.group * a.stride;
+        t.ld = a.ld;
+        t.out_type = a.out_type;
+        t.vec = a.vec;
+        const Target target = target_of(t, mrow, my_stash);
+#pragma unroll
+        for (int j = 0; j < BLOCKS8; ++j)
+          if (j < blocks) emit<false, true>(t, target, run[j], j, my_stash);
       }
     }
   }
@@ -528,14 +631,15 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
 }
 
 // ------------------------------------------------------------------ host side
-// [mats][rows][cols] of bytes; box {128, box_rows, 1}.
-bool make_map8(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t mats, uint64_t ld, uint64_t stride, int box_rows) {
+// [mats][rows][cols] of bytes; box {box_cols, box_rows, 1}, swizzled over its rows of 128 or 64 bytes.
+bool make_map8(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t mats, uint64_t ld, uint64_t stride, int box_cols,
+               int box_rows) {
   const EncodeTiled fn = reinterpret_cast<EncodeTiled>(tensor_map_encoder());
   const cuuint64_t dims[3] = {cols, rows, mats}, strides[2] = {ld, stride};
-  const cuuint32_t box[3] = {BK8, static_cast<cuuint32_t>(box_rows), 1}, estr[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1}, estr[3] = {1, 1, 1};
   return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 struct Operand8 {
@@ -550,16 +654,16 @@ struct Operand8 {
            ((rows == 1 || ld % 16 == 0) && (mats == 1 || stride % 16 == 0) && (reinterpret_cast<uintptr_t>(p) & 15) == 0 &&
             (reinterpret_cast<uintptr_t>(scales) & 3) == 0);
   }
-  bool map(CUtensorMap* m, int box_rows) const {
+  bool map(CUtensorMap* m, int box_cols, int box_rows) const {
     const uint64_t pitch = rows > 1 ? ld : roundup(cols, 16);  // one row has no stride to speak of
-    return make_map8(m, p, cols, rows, mats, pitch, mats > 1 ? stride : pitch * rows, box_rows);
+    return make_map8(m, p, cols, rows, mats, pitch, mats > 1 ? stride : pitch * rows, box_cols, box_rows);
   }
 };
 
 struct Problem8 {
   Op8 op;
   int n, k, rows, groups;
-  Operand8 a, b;  // A: W, or X (wgrad); B: X, or dY
+  Operand8 a, b;  // A: X, or dY (dgrad); B: W, or dY (wgrad)
   long long lds_a, lds_b;  // row scales: distance of blocks; column scales: likewise
   const int32_t* offsets;
   int out_type;
@@ -577,7 +681,7 @@ int check8(const Problem8& p) {
   if (p.groups < 1 || p.groups > OZ_MAX_GROUPS || (!p.offsets && p.groups != 1)) return OZ_EINVAL;
   if (p.out_type != OZ_BF16 && p.out_type != OZ_F16) return OZ_EINVAL;
   if (!p.a.valid() || !p.b.valid()) return OZ_EINVAL;
-  if (p.op == kWgrad8 ? p.lds_a < (p.k > 1 ? p.k : 1) || p.lds_b < (p.n > 1 ? p.n : 1) : p.lds_b < (p.rows > 1 ? p.rows : 1)) return OZ_EINVAL;
+  if (p.op == kWgrad8 ? p.lds_a < (p.k > 1 ? p.k : 1) || p.lds_b < (p.n > 1 ? p.n : 1) : p.lds_a < (p.rows > 1 ? p.rows : 1)) return OZ_EINVAL;
   const int m = p.m_out();
   if (p.ldo < (m > 1 ? m : 1)) return OZ_EINVAL;
   if (p.op == kWgrad8 && p.groups > 1 && p.strideo < static_cast<long long>(p.ldo) * p.n) return OZ_EINVAL;
@@ -591,37 +695,34 @@ template <Op8 OP>
 int launch8(const Problem8& p, const Device& d, cudaStream_t stream) {
   typedef Walk8<OP> Walk;
   Params8 a{};
-  a.M = p.m_out();
-  a.N = p.n;
+  a.N = OP == kDgrad8 ? p.k : p.n;
   a.K = OP == kForward8 ? p.k : p.n;
+  a.M = p.k;
   a.groups = p.groups;
   a.rows = p.rows;
   a.bn = BN;
   a.vec = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.ldo % 8 == 0 && (OP != kWgrad8 || p.groups == 1 || p.strideo % 8 == 0);
   a.out_type = p.out_type == OZ_BF16 ? kOutBf16 : kOutF16;
-  a.idesc = idesc8_base(p.a.type == OZ_E5M2, p.b.type == OZ_E5M2, Walk::A_MN, Walk::B_MN);
+  a.idesc = idesc8_base(p.a.type == OZ_E5M2, p.b.type == OZ_E5M2, Walk::A_MN, Walk::B_MN) | (static_cast<uint32_t>(ACC8 >> 3) << 17);
   a.offsets = p.offsets;
   a.out = p.out;
   a.ld = p.ldo;
   a.stride = p.strideo;
   a.sa = p.a.scales;
   a.sb = p.b.scales;
+  a.sa_ld = p.lds_a;
   a.sb_ld = p.lds_b;
   const int kb = ceil_div(p.k, 128);
-  if (OP == kWgrad8) {
-    a.sa_group = p.lds_a;
-  } else {
-    a.sa_group = static_cast<long long>(ceil_div(p.n, 128)) * kb;
-    a.sa_m = OP == kForward8 ? kb : 1;
-    a.sa_k = OP == kForward8 ? 1 : kb;
-  }
-  bool ok = p.a.map(&a.tmA, 128) && p.b.map(&a.tmB, OP == kWgrad8 ? 128 : Walk::BOX);
-  if (OP != kWgrad8) ok = ok && p.b.map(&a.tmB128, 128);
+  a.sb_group = static_cast<long long>(ceil_div(p.n, 128)) * kb;
+  a.sb_n = OP == kForward8 ? kb : 1;
+  a.sb_k = OP == kForward8 ? 1 : kb;
+  bool ok = p.b.map(&a.tmB, Walk::B_MN ? 64 : 128, Walk::B_MN ? 128 : 64) && p.a.map(&a.tmA, 128, OP == kWgrad8 ? 128 : Walk::BOX);
+  if (OP != kWgrad8) ok = ok && p.a.map(&a.tmA128, 128, 128);
   if (!ok) return OZ_ECUDA;
   a.status = d.status;
   a.epi_wait_ns = epilogue_wait_ns();
   auto kernel = block8_kernel<OP>;
-  constexpr size_t smem = 1024 /*alignment*/ + 2 * STAGES8 * TILE8 + Scales8<OP>::BYTES + EPI8_WARPS * STASH8 + 512 /*barriers*/ + Walk::kTableBytes;
+  constexpr size_t smem = 1024 /*alignment*/ + 2 * STAGES8 * TILE8 + kScaleBytes8<OP> + EPI8_WARPS * STASH8 + 512 /*barriers*/ + Walk::kTableBytes;
   static_assert(smem <= 232448, "shared memory budget");
   static_assert(smem + 2 * 16384 > 232448, "alone on its SM, as the other holders of tensor memory");
   cudaLaunchConfig_t cfg = {};
@@ -686,14 +787,14 @@ extern "C" {
 int ozaki_grouped_gemm_f8(int n, int k, int rows, int groups, int type_w, const void* W, int ldw, long long strideW, const float* SW,
                           int type_x, const void* X, int ldx, const float* SX, int ldsx, const int32_t* offsets, int dtype, void* Y,
                           int ldy, cudaStream_t stream) {
-  return run8(Problem8{kForward8, n, k, rows, groups, {W, type_w, k, n, groups, ldw, strideW, SW}, {X, type_x, k, rows, 1, ldx, 0, SX},
-                       0, ldsx, offsets, dtype, Y, ldy, 0}, stream);
+  return run8(Problem8{kForward8, n, k, rows, groups, {X, type_x, k, rows, 1, ldx, 0, SX}, {W, type_w, k, n, groups, ldw, strideW, SW},
+                       ldsx, 0, offsets, dtype, Y, ldy, 0}, stream);
 }
 int ozaki_grouped_gemm_f8_dgrad(int n, int k, int rows, int groups, int type_w, const void* W, int ldw, long long strideW, const float* SW,
                                 int type_dy, const void* dY, int lddy, const float* SdY, int ldsdy, const int32_t* offsets, int dtype,
                                 void* dX, int lddx, cudaStream_t stream) {
-  return run8(Problem8{kDgrad8, n, k, rows, groups, {W, type_w, k, n, groups, ldw, strideW, SW}, {dY, type_dy, n, rows, 1, lddy, 0, SdY},
-                       0, ldsdy, offsets, dtype, dX, lddx, 0}, stream);
+  return run8(Problem8{kDgrad8, n, k, rows, groups, {dY, type_dy, n, rows, 1, lddy, 0, SdY}, {W, type_w, k, n, groups, ldw, strideW, SW},
+                       ldsdy, 0, offsets, dtype, dX, lddx, 0}, stream);
 }
 int ozaki_grouped_gemm_f8_wgrad(int n, int k, int rows, int groups, int type_dy, const void* dY, int lddy, const float* SdY, int ldsdy,
                                 int type_x, const void* X, int ldx, const float* SX, int ldsx, const int32_t* offsets, int dtype,

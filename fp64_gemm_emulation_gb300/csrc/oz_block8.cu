@@ -495,26 +495,25 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
         // they are used (a product formed at once would wait for both).  Lanes without a row take the last one's.
         const float* sx = a.sa + u.m0 + mrow + min(lane, rows - 1);
         const float* sw = a.sb + u.group * a.sb_group + static_cast<long long>(col / 128) * a.sb_n;
-        float x0 = 0.0f, w0 = 0.0f, x1 = 0.0f, w1 = 0.0f;
+        float x[2] = {}, w[2] = {};
         if (blocks && u.kbs) {
-          x0 = x1 = *sx;
-          w0 = w1 = *sw;
+          x[0] = x[1] = *sx;
+          w[0] = w[1] = *sw;
           if (u.kbs > 1) {
-            x1 = *(sx += a.sa_ld);
-            w1 = *(sw += a.sb_k);
+            x[1] = *(sx += a.sa_ld);
+            w[1] = *(sw += a.sb_k);
           }
         }
-        for (int kb = 0; kb < u.kbs && sums_there(); ++kb) {
+        auto step = [&](int kb, float& x, float& w) {
           const uint32_t from = lanes + buf * (2 * ACC8);
+          const float f = x * w;
+          if (blocks && kb + 2 < u.kbs) {
+            x = *(sx += a.sa_ld);
+            w = *(sw += a.sb_k);
+          }
           if (blocks == BLOCKS8) {  // a block is read while the one before it is scaled and added
             uint32_t v[2][32];
             tmem_ld32(from, v[0]);
-            const float f = x0 * w0;
-            x0 = x1, w0 = w1;
-            if (kb + 2 < u.kbs) {
-              x1 = *(sx += a.sa_ld);
-              w1 = *(sw += a.sb_k);
-            }
 #pragma unroll
             for (int j = 0; j < BLOCKS8; ++j) {
               tmem_ld_wait();
@@ -524,12 +523,6 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
               for (int i = 0; i < 32; ++i) fma_loaded(__uint_as_float(v[j & 1][i]), f, run[j][i]);
             }
           } else if (blocks) {
-            const float f = x0 * w0;
-            x0 = x1, w0 = w1;
-            if (kb + 2 < u.kbs) {
-              x1 = *(sx += a.sa_ld);
-              w1 = *(sw += a.sb_k);
-            }
 #pragma unroll
             for (int j = 0; j < BLOCKS8 - 1; ++j) {
               if (j < blocks) {
@@ -544,6 +537,12 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
           } else {
             release();
           }
+        };
+        // Two k-blocks a turn, so that no scale under way is moved from one register to another.
+        for (int kb = 0; kb < u.kbs && sums_there(); kb += 2) {
+          step(kb, x[0], w[0]);
+          if (kb + 1 == u.kbs || !sums_there()) break;
+          step(kb + 1, x[1], w[1]);
         }
         if (!ok) break;
 #pragma unroll

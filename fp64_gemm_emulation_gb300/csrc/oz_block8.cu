@@ -10,7 +10,8 @@
 //
 // Kernel shape: clusters of two CTAs (cta_group::2), persistent over tiles of 256 m (the first index of D above) x
 // 256 n, 128 m in each CTA.
-//   warp 0: TMA producer   warp 1: TMEM owner + MMA issuer (leader)   warp 2: scales (wgrad)   warps 4-11: epilogue
+//   warp 0: TMA producer   warps 1 and 3: MMA issuers of the two halves (leader; 1: TMEM owner)   warp 2: scales (wgrad)
+//   warps 4-11: epilogue
 // 6 stages of 32 KB: 128 x 128 bytes of A and two tiles of 64 n of B, K-major or MN-major as they lie in memory.
 // What bounds it: every 128 k each of a CTA's 128 x 256 sums is read from tensor memory, scaled and added, while the
 // MMAs take 512 cycles.  So:
@@ -21,6 +22,8 @@
 //    of 4 m x 8 n, although their way out of tensor memory is slower (560 cycles for 128 x 256, 32x32b: below 300).
 //  - the tile's halves of 128 columns are accumulators of their own, two each, and belong to 4 warps each: the way
 //    from the MMAs to the epilogue and back (about 1000 cycles with both CTAs' barriers) overlaps more.
+//  - a k-block costs one thread about 100 cycles for each wait and each copy, and 50 for a commit: the halves' MMAs are
+//    issued by a thread each, and an operand is one copy where its tile is whole blocks of 128.
 #include "oz_products.cuh"
 #include "oz_ragged.cuh"
 
@@ -40,7 +43,7 @@ constexpr int BLOCKS8 = ACC8 / 32;              // blocks of 32 columns whose su
 constexpr uint32_t STASH8 = 32 * 64;
 // Registers: the four warps of the first warpgroup give theirs to the epilogue, whose threads hold 128 sums.
 // 128 x 72 + 256 x 216 = 384 x 168, what the launch has.
-constexpr int REGS_FEW = 72, REGS_MANY = 216;
+constexpr int REGS_FEW = 56, REGS_MANY = 224;
 
 enum Op8 { kForward8, kDgrad8, kWgrad8 };
 
@@ -55,6 +58,7 @@ struct Params8 {
   int M;          // wgrad: the output's contiguous extent (N: its rows)
   int groups, rows, bn;
   int vec, out_type;
+  int b_whole;    // tmB's box is the CTA's whole tile of B
   uint32_t idesc;
   const int32_t* offsets;
   void* out;
@@ -115,12 +119,15 @@ struct Walk8 {
     }
   }
 
-  __device__ Walk8(const Params8& p, const int* table) : a(p), off(table), prefix(table + OZ_MAX_GROUPS + 1) {
+  // at: the tile before the pair's next one.
+  __device__ Walk8(const Params8& p, const int* table, int at) : a(p), off(table), prefix(table + OZ_MAX_GROUPS + 1) {
     tiles_m = RAGGED_SUM ? ceil_div(a.M, BM) : 0;
     tiles_n = ceil_div(a.N, a.bn);
     total = RAGGED_SUM ? a.groups * tiles_m * tiles_n : prefix[a.groups];
-    idx = static_cast<int>(blockIdx.x >> 1) - static_cast<int>(gridDim.x >> 1);
+    idx = at;
   }
+  __device__ Walk8(const Params8& p, const int* table)
+      : Walk8(p, table, static_cast<int>(blockIdx.x >> 1) - static_cast<int>(gridDim.x >> 1)) {}
 
   __device__ bool next(Unit8& u) {
     idx += static_cast<int>(gridDim.x >> 1);
@@ -223,12 +230,12 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
   uint8_t* stash = smem + 2 * STAGES8 * TILE8 + kScaleBytes8<OP>;
   uint64_t* bars = reinterpret_cast<uint64_t*>(stash + EPI8_WARPS * STASH8);
   uint64_t* full = bars;                     // [STAGES8] TMA (both CTAs) -> MMA  (used in the leader)
-  uint64_t* empty = full + STAGES8;          // [STAGES8] MMA -> TMA              (both CTAs)
+  uint64_t* empty = full + STAGES8;          // [STAGES8] MMA issuers -> TMA      (both CTAs)
   uint64_t* accfull = empty + STAGES8;       // [2][2]    MMA -> epilogue, by buffer and half (both CTAs)
   uint64_t* accempty = accfull + 4;          // [2][2]    the half's warps (both) -> MMA (used in the leader)
   uint64_t* sfull = accempty + 4;            // [SLOTS8]  scales -> epilogue      (per CTA)
   uint64_t* sempty = sfull + SLOTS8;         // [SLOTS8]  epilogue -> scales      (per CTA)
-  uint64_t* drain = sempty + SLOTS8;         // [1]       all MMAs of the pair done (both CTAs)
+  uint64_t* drain = sempty + SLOTS8;         // [1]       all MMAs of the pair done, by each issuer (both CTAs)
   uint64_t* exitbar = drain + 1;             // [1]       the peer has finished (per CTA)
   uint64_t* proddone = exitbar + 1;          // [1]       both producers have stopped (used in the leader)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(proddone + 1);
@@ -238,11 +245,12 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
+  const int halves = a.bn / ACC8;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES8; ++i) {
       mbar_init(&full[i], 2);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], halves);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&accfull[i], 1);
@@ -252,7 +260,7 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
       mbar_init(&sfull[i], 1);
       mbar_init(&sempty[i], EPI8_WARPS);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, halves);
     mbar_init(exitbar, 1);
     mbar_init(proddone, 2);
     *abort_flag = 0;
@@ -277,7 +285,6 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
         int stage = 0;
         uint32_t phase = 0, issued = 0;
         const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
-        const int halves = a.bn / ACC8;
         Walk walk(a, table);
         Unit8 u{};
         bool ok = true;
@@ -299,12 +306,20 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
             uint8_t* dA = sA + stage * TILE8;
             uint8_t* dB = sB + stage * TILE8;
             const int k = kb * BK8;
-            for (int h = 0; h < halves; ++h) {
-              const int n = u.n0 + ACC8 * h + 64 * static_cast<int>(rank), z = OP == kWgrad8 ? 0 : u.group;
+            const int z = OP == kWgrad8 ? 0 : u.group;
+            if (a.b_whole) {
               if (Walk::B_MN)
-                tma_load_3d_pair(dB + h * HALF8, &a.tmB, bar, n, k, z);
+                tma_load_5d_pair(dB, &a.tmB, bar, 0, k, static_cast<int>(rank), u.n0 / ACC8, z);
               else
-                tma_load_3d_pair(dB + h * HALF8, &a.tmB, bar, k, n, z);
+                tma_load_4d_pair(dB, &a.tmB, bar, k, 64 * static_cast<int>(rank), u.n0 / ACC8, z);
+            } else {
+              for (int h = 0; h < halves; ++h) {
+                const int n = u.n0 + ACC8 * h + 64 * static_cast<int>(rank);
+                if (Walk::B_MN)
+                  tma_load_3d_pair(dB + h * HALF8, &a.tmB, bar, n, k, z);
+                else
+                  tma_load_3d_pair(dB + h * HALF8, &a.tmB, bar, k, n, z);
+              }
             }
             if (Walk::A_MN)
               tma_load_3d_pair(dA, &a.tmA, bar, m, k, 0);
@@ -336,17 +351,18 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
           }
         }
       }
-    } else if (warp == 1) {
-      if (rank == 0 && elect_one()) {
-        // ------------------------------------------------------------ MMA issuer (leader only)
+    } else if (warp & 1) {
+      const int half = warp >> 1;
+      if (rank == 0 && half < halves && elect_one()) {
+        // ------------------------------------------------------------ MMA issuers (leader only), one for each half
         int stage = 0;
         uint32_t phase = 0, buf = 0, acc_phase = 1, consumed = 0;
         bool ok = true;
-        const uint32_t a_desc = desc_low(smem_u32(sA), Walk::A_MN), b_desc = desc_low(smem_u32(sB), Walk::B_MN);
+        const uint32_t a_desc = desc_low(smem_u32(sA), Walk::A_MN), b_desc = desc_low(smem_u32(sB) + half * HALF8, Walk::B_MN);
         constexpr uint32_t a_step = (Walk::A_MN ? STEP8 * 128 : STEP8) >> 4, b_step = (Walk::B_MN ? STEP8 * 64 : STEP8) >> 4;
         constexpr uint32_t B_HIGH = Walk::B_MN ? DESC_HIGH_64 : DESC_HIGH;
         const uint32_t idesc = a.idesc;
-        const bool two_halves = a.bn > ACC8;
+        const uint32_t d_half = tmem_base + half * ACC8;
         Walk walk(a, table);
         Unit8 u{};
         while (ok && !*abort_flag && walk.next(u)) {
@@ -356,27 +372,15 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
               break;
             }
             ++consumed;
-            const uint32_t ad = a_desc + stage * (TILE8 >> 4), bd = b_desc + stage * (TILE8 >> 4);
-            if (!mbar_wait_or_abort(&accempty[2 * buf], acc_phase, kWaitLimitNs, abort_flag)) {
+            if (!mbar_wait_or_abort(&accempty[2 * buf + half], acc_phase, kWaitLimitNs, abort_flag)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t d_tmem = tmem_base + buf * (2 * ACC8);
+            const uint32_t ad = a_desc + stage * (TILE8 >> 4), bd = b_desc + stage * (TILE8 >> 4), d = d_half + buf * (2 * ACC8);
 #pragma unroll
-            for (int kk = 0; kk < BK8 / STEP8; ++kk) umma8_pair<B_HIGH>(d_tmem, ad + kk * a_step, bd + kk * b_step, idesc, kk > 0 ? 1u : 0u);
-            umma_commit_pair(&accfull[2 * buf], 0x3);
-            if (two_halves) {
-              if (!mbar_wait_or_abort(&accempty[2 * buf + 1], acc_phase, kWaitLimitNs, abort_flag)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-#pragma unroll
-              for (int kk = 0; kk < BK8 / STEP8; ++kk)
-                umma8_pair<B_HIGH>(d_tmem + ACC8, ad + kk * a_step, bd + (HALF8 >> 4) + kk * b_step, idesc, kk > 0 ? 1u : 0u);
-              umma_commit_pair(&accfull[2 * buf + 1], 0x3);
-            }
+            for (int kk = 0; kk < BK8 / STEP8; ++kk) umma8_pair<B_HIGH>(d, ad + kk * a_step, bd + kk * b_step, idesc, kk > 0 ? 1u : 0u);
+            umma_commit_pair(&accfull[2 * buf + half], 0x3);
             umma_commit_pair(&empty[stage], 0x3);
             acc_phase ^= buf;
             buf ^= 1;
@@ -388,20 +392,22 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
         }
         if (!ok && !*abort_flag) stop_pair(abort_flag, a.status);
         // Account for every copy before the pair may exit (see the residue GEMM).
-        if (mbar_wait_acquire_cluster(proddone, 0)) {
-          const uint32_t n0 = issued_by[0], n1 = issued_by[1];
-          const uint32_t top = n0 > n1 ? n0 : n1;
-          for (uint32_t q = consumed; q < top && q < consumed + STAGES8; ++q) {
-            const int st = static_cast<int>(q % STAGES8);
-            if (q >= n0) mbar_arrive(&full[st]);
-            if (q >= n1) mbar_arrive(&full[st]);
-            if (!mbar_wait(&full[st], (q / STAGES8) & 1)) {
-              stop_pair(abort_flag, a.status);
-              break;
+        if (half == 0) {
+          if (mbar_wait_acquire_cluster(proddone, 0)) {
+            const uint32_t n0 = issued_by[0], n1 = issued_by[1];
+            const uint32_t top = n0 > n1 ? n0 : n1;
+            for (uint32_t q = consumed; q < top && q < consumed + STAGES8; ++q) {
+              const int st = static_cast<int>(q % STAGES8);
+              if (q >= n0) mbar_arrive(&full[st]);
+              if (q >= n1) mbar_arrive(&full[st]);
+              if (!mbar_wait(&full[st], (q / STAGES8) & 1)) {
+                stop_pair(abort_flag, a.status);
+                break;
+              }
             }
+          } else {
+            stop_pair(abort_flag, a.status);
           }
-        } else {
-          stop_pair(abort_flag, a.status);
         }
         umma_commit_pair(drain, 0x3);
       }
@@ -463,7 +469,7 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
     uint32_t buf = 0, acc_phase = 0;
     bool ok = true;
     Walk walk(a, table);
-    walk.outside(warp - EPI8_FIRST);
+    walk.outside(warp - EPI8_FIRST);  // (wgrad walks on with it)
     auto wait = [&](uint64_t* bar, uint32_t phase, uint64_t limit) {
       if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, phase))) return true;
       ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar, phase, limit, abort_flag));
@@ -483,46 +489,83 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
       acc_phase ^= buf;
       buf ^= 1;
     };
-    Unit8 u{};
     if constexpr (OP != kWgrad8) {
-      while (ok && half * ACC8 < a.bn && walk.next(u)) {
-        const int rows = u.mcount - mrow, col = u.n0 + half * ACC8;
-        const int blocks = rows > 0 ? min(BLOCKS8, ceil_div(max(0, u.n0 + u.ncount - col), 32)) : 0;  // of 32 columns
+      // The sums take nearly all registers: the walker is made anew for each tile, and where the tile goes waits in the
+      // warp's stash.
+      int4* const kept = reinterpret_cast<int4*>(my_stash);  // first row, rows, first column, columns
+      for (int at = static_cast<int>(blockIdx.x >> 1) - static_cast<int>(gridDim.x >> 1); ok && half * ACC8 < a.bn;
+           at += static_cast<int>(gridDim.x >> 1)) {
+        int left, blocks;  // k-blocks to come, blocks of 32 columns
+        const float *sx, *sw;
+        {
+          Walk walk(a, table, at);
+          Unit8 u;
+          if (!walk.next(u)) break;
+          const int rows = u.mcount - mrow, col = u.n0 + half * ACC8, cols = u.ncount - half * ACC8;
+          blocks = rows > 0 ? min(BLOCKS8, ceil_div(max(0, cols), 32)) : 0;
+          left = u.kbs;
+          // This lane's row's scales and those of the half's features.  Lanes without a row take the last one's.
+          sx = a.sa + u.m0 + mrow + min(lane, rows - 1);
+          sw = a.sb + u.group * a.sb_group + static_cast<long long>(col / 128) * a.sb_n;
+          __syncwarp();
+          if (lane == 0) *kept = make_int4(u.m0 + mrow, rows, col, cols);
+        }
         float run[BLOCKS8][32];
 #pragma unroll
         for (int i = 0; i < BLOCKS8 * 32; ++i) run[i >> 5][i & 31] = 0.0f;
-        // This lane's row's scales and those of the half's features, fetched two k-blocks ahead and multiplied only when
-        // they are used (a product formed at once would wait for both).  Lanes without a row take the last one's.
-        const float* sx = a.sa + u.m0 + mrow + min(lane, rows - 1);
-        const float* sw = a.sb + u.group * a.sb_group + static_cast<long long>(col / 128) * a.sb_n;
+        // Scales are fetched two k-blocks ahead and multiplied only when they are used (a product formed at once would
+        // wait for both).
         float x[2] = {}, w[2] = {};
-        if (blocks && u.kbs) {
+        if (blocks && left) {
           x[0] = x[1] = *sx;
           w[0] = w[1] = *sw;
-          if (u.kbs > 1) {
+          if (left > 1) {
             x[1] = *(sx += a.sa_ld);
             w[1] = *(sw += a.sb_k);
           }
         }
-        auto step = [&](int kb, float& x, float& w) {
-          const uint32_t from = lanes + buf * (2 * ACC8);
+        auto factor = [&](float& x, float& w) {
           const float f = x * w;
-          if (blocks && kb + 2 < u.kbs) {
+          if (left > 2) {
             x = *(sx += a.sa_ld);
             w = *(sw += a.sb_k);
           }
-          if (blocks == BLOCKS8) {  // a block is read while the one before it is scaled and added
-            uint32_t v[2][32];
-            tmem_ld32(from, v[0]);
+          return f;
+        };
+        if (blocks == BLOCKS8) {
+          // Half a block is read while the one before it is scaled and added, across k-blocks too; after the last one
+          // the read is of a free accumulator's columns, and dropped.
+          uint32_t v[2][16];
+          auto step = [&](float& x, float& w) {
+            const float f = factor(x, w);
 #pragma unroll
-            for (int j = 0; j < BLOCKS8; ++j) {
+            for (int j = 0; j < 2 * BLOCKS8; ++j) {
               tmem_ld_wait();
-              if (j + 1 < BLOCKS8) tmem_ld32(from + 32 * (j + 1), v[(j + 1) & 1]);
-              else release();
+              if (j + 1 == 2 * BLOCKS8) {
+                release();
+                if (--left > 0) sums_there();
+              }
+              tmem_ld16(lanes + buf * (2 * ACC8) + 16 * ((j + 1) % (2 * BLOCKS8)), v[(j + 1) & 1]);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) fma_loaded(__uint_as_float(v[j & 1][i]), f, run[j][i]);
+              for (int i = 0; i < 16; ++i) fma_loaded(__uint_as_float(v[j & 1][i]), f, run[j >> 1][16 * (j & 1) + i]);
             }
-          } else if (blocks) {
+          };
+          if (left > 0 && sums_there()) {
+            tmem_ld16(lanes + buf * (2 * ACC8), v[0]);
+            // Two k-blocks a turn, so that no scale under way is moved from one register to another.
+            while (ok && left > 0) {
+              step(x[0], w[0]);
+              if (!ok || left == 0) break;
+              step(x[1], w[1]);
+            }
+            tmem_ld_wait();
+          }
+        } else {
+          auto step = [&](float& x, float& w) {
+            const float f = blocks ? factor(x, w) : 0.0f;
+            const uint32_t from = lanes + buf * (2 * ACC8);
+            --left;
+            if (blocks == 0) release();
 #pragma unroll
             for (int j = 0; j < BLOCKS8 - 1; ++j) {
               if (j < blocks) {
@@ -534,23 +577,24 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
                 for (int i = 0; i < 32; ++i) fma_loaded(__uint_as_float(v[i]), f, run[j][i]);
               }
             }
-          } else {
-            release();
+          };
+          while (left > 0 && sums_there()) {
+            step(x[0], w[0]);
+            if (left == 0 || !sums_there()) break;
+            step(x[1], w[1]);
           }
-        };
-        // Two k-blocks a turn, so that no scale under way is moved from one register to another.
-        for (int kb = 0; kb < u.kbs && sums_there(); kb += 2) {
-          step(kb, x[0], w[0]);
-          if (kb + 1 == u.kbs || !sums_there()) break;
-          step(kb + 1, x[1], w[1]);
         }
         if (!ok) break;
+        __syncwarp();
+        const int4 to = *kept;
+        __syncwarp();
 #pragma unroll
         for (int j = 0; j < BLOCKS8; ++j)
-          if (j < blocks) emit_rows(a, run[j], my_stash, u.m0 + mrow, rows, col + 32 * j, u.n0 + u.ncount - col - 32 * j);
+          if (j < blocks) emit_rows(a, run[j], my_stash, to.x, to.y, to.z + 32 * j, to.w - 32 * j);
       }
     } else {
       uint32_t slot = 0, sphase = 0;
+      Unit8 u{};
       while (ok && walk.next(u)) {
         const int columns = min(ACC8, u.ncount - half * ACC8);
         const int blocks = u.mcount > mrow ? max(0, ceil_div(max(0, columns), 32)) : 0;
@@ -630,14 +674,12 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
 }
 
 // ------------------------------------------------------------------ host side
-// [mats][rows][cols] of bytes; box {box_cols, box_rows, 1}, swizzled over its rows of 128 or 64 bytes.
-bool make_map8(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t mats, uint64_t ld, uint64_t stride, int box_cols,
-               int box_rows) {
+// A tensor map of bytes, swizzled over its rows of 128 or 64 bytes (box[0]).
+bool encode8(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
   const EncodeTiled fn = reinterpret_cast<EncodeTiled>(tensor_map_encoder());
-  const cuuint64_t dims[3] = {cols, rows, mats}, strides[2] = {ld, stride};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1}, estr[3] = {1, 1, 1};
-  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, box[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -653,9 +695,30 @@ struct Operand8 {
            ((rows == 1 || ld % 16 == 0) && (mats == 1 || stride % 16 == 0) && (reinterpret_cast<uintptr_t>(p) & 15) == 0 &&
             (reinterpret_cast<uintptr_t>(scales) & 3) == 0);
   }
+  uint64_t pitch() const { return rows > 1 ? ld : roundup(cols, 16); }  // one row has no stride to speak of
+  uint64_t mat_pitch() const { return mats > 1 ? stride : pitch() * rows; }
+  // [mats][rows][cols], box {box_cols, box_rows, 1}.
   bool map(CUtensorMap* m, int box_cols, int box_rows) const {
-    const uint64_t pitch = rows > 1 ? ld : roundup(cols, 16);  // one row has no stride to speak of
-    return make_map8(m, p, cols, rows, mats, pitch, mats > 1 ? stride : pitch * rows, box_cols, box_rows);
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(mats)};
+    const cuuint64_t strides[2] = {pitch(), mat_pitch()};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
+    return encode8(m, p, 3, dims, strides, box);
+  }
+  // B, where its n are whole blocks of 128: a box holds 64 n of each of `halves` neighbouring blocks.
+  //   K-major:  [mats][n / 128][128][k], box {128, 64, halves, 1}
+  //   MN-major: [mats][n / 128][2][k][64], box {64, 128, 1, halves, 1}
+  bool map_halves(CUtensorMap* m, bool mn, int halves) const {
+    const cuuint32_t h = static_cast<cuuint32_t>(halves);
+    if (mn) {
+      const cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(rows), 2, static_cast<cuuint64_t>(cols / 128), static_cast<cuuint64_t>(mats)};
+      const cuuint64_t strides[4] = {pitch(), 64, 128, mat_pitch()};
+      const cuuint32_t box[5] = {64, 128, 1, h, 1};
+      return encode8(m, p, 5, dims, strides, box);
+    }
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(cols), 128, static_cast<cuuint64_t>(rows / 128), static_cast<cuuint64_t>(mats)};
+    const cuuint64_t strides[3] = {pitch(), 128 * pitch(), mat_pitch()};
+    const cuuint32_t box[4] = {128, 64, h, 1};
+    return encode8(m, p, 4, dims, strides, box);
   }
 };
 
@@ -715,7 +778,9 @@ int launch8(const Problem8& p, const Device& d, cudaStream_t stream) {
   a.sb_group = static_cast<long long>(ceil_div(p.n, 128)) * kb;
   a.sb_n = OP == kForward8 ? kb : 1;
   a.sb_k = OP == kForward8 ? 1 : kb;
-  bool ok = p.b.map(&a.tmB, Walk::B_MN ? 64 : 128, Walk::B_MN ? 128 : 64) && p.a.map(&a.tmA, 128, OP == kWgrad8 ? 128 : Walk::BOX);
+  a.b_whole = a.N % 128 == 0;
+  bool ok = (a.b_whole ? p.b.map_halves(&a.tmB, Walk::B_MN, a.bn / ACC8) : p.b.map(&a.tmB, Walk::B_MN ? 64 : 128, Walk::B_MN ? 128 : 64)) &&
+            p.a.map(&a.tmA, 128, OP == kWgrad8 ? 128 : Walk::BOX);
   if (OP != kWgrad8) ok = ok && p.a.map(&a.tmA128, 128, 128);
   if (!ok) return OZ_ECUDA;
   a.status = d.status;

@@ -219,6 +219,17 @@ __device__ __forceinline__ void emit_rows(const Params8& a, const float (&v)[32]
   __syncwarp();
 }
 
+// 32 lanes x 16 columns in the fragments of tcgen05.ld.16x256b.x2: element i is
+//   m = 16 (i / 8) + lane / 4 + 8 ((i / 2) % 2),   n = 8 ((i / 4) % 2) + 2 (lane % 4) + i % 2
+__device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, float (&v)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[8 * h]), "=f"(v[8 * h + 1]), "=f"(v[8 * h + 2]), "=f"(v[8 * h + 3]), "=f"(v[8 * h + 4]), "=f"(v[8 * h + 5]),
+                   "=f"(v[8 * h + 6]), "=f"(v[8 * h + 7])
+                 : "r"(taddr + (h ? 16u << 16 : 0u)));
+}
+
 template <Op8 OP>
 __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_constant__ Params8 a) {
   typedef Walk8<OP> Walk;
@@ -468,8 +479,7 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
     const int mrow = static_cast<int>(rank) * HALF_M + quad * 32;
     uint32_t buf = 0, acc_phase = 0;
     bool ok = true;
-    Walk walk(a, table);
-    walk.outside(warp - EPI8_FIRST);  // (wgrad walks on with it)
+    Walk(a, table).outside(warp - EPI8_FIRST);
     auto wait = [&](uint64_t* bar, uint32_t phase, uint64_t limit) {
       if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, phase))) return true;
       ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar, phase, limit, abort_flag));
@@ -594,49 +604,78 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
       }
     } else {
       uint32_t slot = 0, sphase = 0;
-      Unit8 u{};
-      while (ok && walk.next(u)) {
-        const int columns = min(ACC8, u.ncount - half * ACC8);
-        const int blocks = u.mcount > mrow ? max(0, ceil_div(max(0, columns), 32)) : 0;
+      auto scales_there = [&]() { return wait(&sfull[slot], sphase, kWaitLimitNs); };
+      auto scales_done = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty[slot]);
+        if (++slot == SLOTS8) {
+          slot = 0;
+          sphase ^= 1;
+        }
+      };
+      Unit8* const kept = reinterpret_cast<Unit8*>(my_stash);
+      for (int at = static_cast<int>(blockIdx.x >> 1) - static_cast<int>(gridDim.x >> 1); ok; at += static_cast<int>(gridDim.x >> 1)) {
+        int left, blocks;
+        {
+          Walk walk(a, table, at);
+          Unit8 u;
+          if (!walk.next(u)) break;
+          blocks = u.mcount > mrow ? min(BLOCKS8, ceil_div(max(0, u.ncount - half * ACC8), 32)) : 0;
+          left = u.kbs;
+          __syncwarp();
+          if (lane == 0) *kept = u;
+        }
         float run[BLOCKS8][32];
 #pragma unroll
         for (int i = 0; i < BLOCKS8 * 32; ++i) run[i >> 5][i & 31] = 0.0f;
-        for (int kb = 0; kb < u.kbs; ++kb) {
-          if (!wait(&sfull[slot], sphase, kWaitLimitNs) || !sums_there()) break;
-          const float* sn = scales + slot * SLOT_FLOATS8 + half * ACC8 + 2 * (lane & 3);
-          float sm[4];
+        if (blocks) {
+          // 16 columns are read while the ones before them are scaled and added, across k-blocks too: all 128, whether the
+          // tile has them or not, and 16 of a free accumulator after the last k-block.
+          float v[2][16], sm[4];
+          auto scales_of_m = [&]() {
 #pragma unroll
-          for (int h = 0; h < 4; ++h) sm[h] = scales[slot * SLOT_FLOATS8 + 256 + quad * 32 + (lane >> 2) + 8 * h];
-          const uint32_t from = lanes + buf * (2 * ACC8);
+            for (int h = 0; h < 4; ++h) sm[h] = scales[slot * SLOT_FLOATS8 + 256 + quad * 32 + (lane >> 2) + 8 * h];
+          };
+          if (left > 0 && scales_there() && sums_there()) {
+            scales_of_m();
+            tmem_ld_frag16(lanes + buf * (2 * ACC8), v[0]);
+          }
+          while (ok && left > 0) {
 #pragma unroll
-          for (int j = 0; j < BLOCKS8; ++j) {
-            if (j < blocks) {
-              float v[32];
-              float2 s[4];
-              tmem_ld_block(from + 32 * j, v);
+            for (int j = 0; j < 2 * BLOCKS8; ++j) {
+              float2 s[2];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) s[q] = *reinterpret_cast<const float2*>(sn + 32 * j + 8 * q);
+              for (int q = 0; q < 2; ++q)
+                s[q] = *reinterpret_cast<const float2*>(scales + slot * SLOT_FLOATS8 + half * ACC8 + 2 * (lane & 3) + 16 * j + 8 * q);
               tmem_ld_wait();
-              if (j + 1 == blocks) release();
+              if (j + 1 == 2 * BLOCKS8) {
+                release();
+                scales_done();
+                if (--left > 0 && scales_there()) sums_there();
+              }
+              tmem_ld_frag16(lanes + buf * (2 * ACC8) + 16 * ((j + 1) % (2 * BLOCKS8)), v[(j + 1) & 1]);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
+              for (int q = 0; q < 2; ++q) {
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {  // m = lane / 4 + 8 h, n = 8 q + 2 (lane % 4), + 1
-                  const int i = 16 * (h >> 1) + 4 * q + 2 * (h & 1);
-                  fma_loaded(v[i], v[i + 1], s[q], sm[h], run[j][i], run[j][i + 1]);
+                for (int h = 0; h < 4; ++h) {  // m = lane / 4 + 8 h, n = 16 j + 8 q + 2 (lane % 4), + 1
+                  const int i = 8 * (h >> 1) + 4 * q + 2 * (h & 1), r = 16 * (h >> 1) + 8 * (j & 1) + 4 * q + 2 * (h & 1);
+                  fma_loaded(v[j & 1][i], v[j & 1][i + 1], s[q], sm[h], run[j >> 1][r], run[j >> 1][r + 1]);
                 }
               }
             }
+            if (ok && left > 0) scales_of_m();
           }
-          if (blocks == 0) release();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sempty[slot]);
-          if (++slot == SLOTS8) {
-            slot = 0;
-            sphase ^= 1;
+          tmem_ld_wait();
+        } else {
+          for (; left > 0 && scales_there() && sums_there(); --left) {
+            release();
+            scales_done();
           }
         }
         if (!ok) break;
+        __syncwarp();
+        const Unit8 u = *kept;
+        __syncwarp();
         Unit t{};  // as the 16-bit products' epilogue takes it
         t.m0 = u.m0;
         t.m_extent = a.M;

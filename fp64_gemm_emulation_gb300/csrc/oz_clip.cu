@@ -15,7 +15,10 @@
 namespace oz {
 namespace {
 
-constexpr int kThreads = 256, kChunk = 16384;  // elements of a chunk
+constexpr int kThreads = 256;
+// Elements of a chunk: enough for a CTA's 16-byte loads to follow each other, few enough for all CTAs to get some.
+constexpr int kChunk = 16384, kLongChunk = 65536;
+constexpr long long kLongTotal = 1ll << 27;    // elements of a launch from which on chunks are long
 constexpr int kMaxSums = 4096;                 // CTAs whose sums the workspace holds
 
 struct Tensor {
@@ -31,6 +34,7 @@ struct ClipParams {
   Tensor t[N];
   int tensors;
   int first_sum, all_sums;  // where this launch's sums start; how many there are
+  int chunk;                // elements
   long long chunks;
   double* sums;
   float limit, eps;
@@ -55,7 +59,7 @@ __device__ __forceinline__ double squares(const Eight<T> (&v)[N]) {
   for (int i = 0; i < N; ++i) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float x = to_float(v[i].e[e]);
+      const float x = v[i].get(e);
       most = fmaxf(most, fabsf(x));
       sum = fmaf(x, x, sum);
     }
@@ -67,34 +71,32 @@ __device__ __forceinline__ double squares(const Eight<T> (&v)[N]) {
   for (int i = 0; i < N; ++i) {
 #pragma unroll 1
     for (int e = 0; e < 8; ++e) {
-      const double x = to_float(v[i].e[e]);
+      const double x = v[i].get(e);
       d = fma(x, x, d);
     }
   }
   return d;
 }
 
+// Four eights of a chunk of `count` elements, from c + i STEP on; zeros behind its end.
+constexpr int kEights = 4, STEP = kThreads * 8;
 template <class T>
-__device__ __forceinline__ double chunk_squares(const Tensor& t, long long from) {
+__device__ __forceinline__ void load_eights(Eight<T> (&v)[kEights], const T* p, int c, int count, bool aligned) {
+#pragma unroll
+  for (int i = 0; i < kEights; ++i) {
+    const int at = c + i * STEP;
+    v[i] = aligned && at + 8 <= count ? load_eight(p + at) : gather_eight(p + at, 1, [&](int e) { return at + e < count; });
+  }
+}
+
+template <class T>
+__device__ __forceinline__ double chunk_squares(const Tensor& t, long long from, int chunk) {
   const T* p = static_cast<const T*>(t.in) + from;
-  const int count = static_cast<int>(min(static_cast<long long>(kChunk), t.count - from));
+  const int count = static_cast<int>(min(static_cast<long long>(chunk), t.count - from));
   double d = 0.0;
-  constexpr int N = 4, STEP = kThreads * 8;
-  for (int c = 8 * threadIdx.x; c < count; c += N * STEP) {
-    Eight<T> v[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int at = c + i * STEP;
-      if (t.aligned && at + 8 <= count) {
-        v[i] = load_eight(p + at);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (at + e < count) v[i].e[e] = p[at + e];
-          else from_float(0.0f, v[i].e[e]);
-        }
-      }
-    }
+  for (int c = 8 * threadIdx.x; c < count; c += kEights * STEP) {
+    Eight<T> v[kEights];
+    load_eights(v, p, c, count, t.aligned);
     d += squares(v);
   }
   return d;
@@ -120,33 +122,36 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ C
   double d = 0.0;
   for (long long chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
     const Tensor& t = a.t[tensor_of(a, chunk)];
-    const long long from = (chunk - t.first) * kChunk;
-    d += t.dtype == OZ_F32 ? chunk_squares<float>(t, from)
-         : t.dtype == OZ_BF16 ? chunk_squares<__nv_bfloat16>(t, from)
-                              : chunk_squares<__half>(t, from);
+    const long long from = (chunk - t.first) * a.chunk;
+    d += t.dtype == OZ_F32 ? chunk_squares<float>(t, from, a.chunk)
+         : t.dtype == OZ_BF16 ? chunk_squares<__nv_bfloat16>(t, from, a.chunk)
+                              : chunk_squares<__half>(t, from, a.chunk);
   }
   d = block_sum(d, meet);
   if (threadIdx.x == 0) a.sums[a.first_sum + blockIdx.x] = d;
 }
 
 template <class T>
-__device__ __forceinline__ void scale_chunk(const Tensor& t, long long from, float f) {
+__device__ __forceinline__ void scale_chunk(const Tensor& t, long long from, int chunk, float f) {
   const T* p = static_cast<const T*>(t.in) + from;
   T* q = static_cast<T*>(t.out) + from;
-  const int count = static_cast<int>(min(static_cast<long long>(kChunk), t.count - from));
-  constexpr int STEP = kThreads * 8;
-#pragma unroll 4
-  for (int c = 8 * threadIdx.x; c < count; c += STEP) {
-    if (t.aligned && c + 8 <= count) {
-      const Eight<T> v = load_eight(p + c);
+  const int count = static_cast<int>(min(static_cast<long long>(chunk), t.count - from));
+  for (int c = 8 * threadIdx.x; c < count; c += kEights * STEP) {
+    Eight<T> v[kEights];  // all loads before the first store, which could be to the same memory
+    load_eights(v, p, c, count, t.aligned);
+#pragma unroll
+    for (int i = 0; i < kEights; ++i) {
+      const int at = c + i * STEP;
       float x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = to_float(v.e[e]) * f;
-      store_eight(q + c, x);
-    } else {
+      for (int e = 0; e < 8; ++e) x[e] = v[i].get(e) * f;
+      if (t.aligned && at + 8 <= count) {
+        store_eight(q + at, x);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < count) from_float(to_float(p[c + e]) * f, q[c + e]);
+        for (int e = 0; e < 8; ++e)
+          if (at + e < count) from_float(x[e], q[at + e]);
+      }
     }
   }
 }
@@ -166,10 +171,10 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
     const long long chunk = a.chunks - 1 - i;
     const Tensor& t = a.t[tensor_of(a, chunk)];
     if (f == 1.0f && t.in == t.out) continue;
-    const long long from = (chunk - t.first) * kChunk;
-    if (t.dtype == OZ_F32) scale_chunk<float>(t, from, f);
-    else if (t.dtype == OZ_BF16) scale_chunk<__nv_bfloat16>(t, from, f);
-    else scale_chunk<__half>(t, from, f);
+    const long long from = (chunk - t.first) * a.chunk;
+    if (t.dtype == OZ_F32) scale_chunk<float>(t, from, a.chunk, f);
+    else if (t.dtype == OZ_BF16) scale_chunk<__nv_bfloat16>(t, from, a.chunk, f);
+    else scale_chunk<__half>(t, from, a.chunk, f);
   }
 }
 
@@ -197,6 +202,9 @@ int clip_launches(const Work& w, float limit, float eps, float* norm, uint8_t* w
   auto fill = [&](int l) {
     a.tensors = 0;
     a.chunks = 0;
+    long long total = 0;
+    for (int i = l * N; i < w.count && i < (l + 1) * N; ++i) total += w.counts[i];
+    a.chunk = total >= kLongTotal ? kLongChunk : kChunk;
     for (int i = l * N; i < w.count && i < (l + 1) * N; ++i) {
       if (w.counts[i] == 0) continue;
       Tensor& t = a.t[a.tensors++];
@@ -206,7 +214,7 @@ int clip_launches(const Work& w, float limit, float eps, float* norm, uint8_t* w
       t.first = a.chunks;
       t.dtype = w.dtypes[i];
       t.aligned = ((reinterpret_cast<uintptr_t>(t.in) | reinterpret_cast<uintptr_t>(t.out)) & 15) == 0;
-      a.chunks += (t.count + kChunk - 1) / kChunk;
+      a.chunks += (t.count + a.chunk - 1) / a.chunk;
     }
     const long long grid = a.chunks < most ? a.chunks : most;
     return static_cast<unsigned>(grid < 1 ? 1 : grid);

@@ -9,37 +9,87 @@
 
 namespace oz {
 
-__device__ __forceinline__ float to_float(float v) { return v; }
-__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void from_float(float v, float& r) { r = v; }
 __device__ __forceinline__ void from_float(float v, __half& r) { r = __float2half_rn(v); }
 __device__ __forceinline__ void from_float(float v, __nv_bfloat16& r) { r = __float2bfloat16_rn(v); }
 
-// Eight neighbours, 16-byte aligned.
+// An element's bits, and its value.
+template <class T>
+struct Bits {
+  typedef uint16_t Raw;
+};
+template <>
+struct Bits<float> {
+  typedef uint32_t Raw;
+};
+__device__ __forceinline__ float value_of(uint32_t raw, float) { return __uint_as_float(raw); }
+__device__ __forceinline__ float value_of(uint32_t raw, __half) { return __half2float(__ushort_as_half(static_cast<unsigned short>(raw))); }
+__device__ __forceinline__ float value_of(uint32_t raw, __nv_bfloat16) { return __uint_as_float(raw << 16); }
+template <class T>
+__device__ __forceinline__ float to_float(const T& v) {
+  return value_of(*reinterpret_cast<const typename Bits<T>::Raw*>(&v), T());
+}
+
+// Eight elements in as many registers as they fill (16-bit ones in pairs, the first in the low half).
 template <class T>
 struct alignas(16) Eight {
-  T e[8];
+  static constexpr int WORDS = 2 * sizeof(T);
+  uint32_t w[WORDS];
+  __device__ __forceinline__ float get(int e) const {
+    if (sizeof(T) == 4) return __uint_as_float(w[e]);
+    return value_of(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu, T());
+  }
 };
+template <>
+__device__ __forceinline__ float Eight<__nv_bfloat16>::get(int e) const {
+  return __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+}
 
+// Element e is at row[e * step] where valid(e), zero otherwise.
+template <class T, class V>
+__device__ __forceinline__ Eight<T> gather_eight(const T* row, int step, V valid) {
+  const typename Bits<T>::Raw* raw = reinterpret_cast<const typename Bits<T>::Raw*>(row);
+  Eight<T> r;
+  if (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < Eight<T>::WORDS; ++e) r.w[e] = valid(e) ? raw[e * step] : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = valid(2 * i) ? raw[2 * i * step] : 0u, hi = valid(2 * i + 1) ? raw[(2 * i + 1) * step] : 0u;
+      r.w[i] = lo | hi << 16;
+    }
+  }
+  return r;
+}
+// Eight neighbours, 16-byte aligned.
 template <class T>
 __device__ __forceinline__ Eight<T> load_eight(const T* p) {
   Eight<T> r;
-  const uint4* from = reinterpret_cast<const uint4*>(p);
-  uint4* to = reinterpret_cast<uint4*>(&r);
 #pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) to[i] = from[i];
+  for (int i = 0; i < Eight<T>::WORDS / 4; ++i) {
+    const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+    r.w[4 * i] = x.x, r.w[4 * i + 1] = x.y, r.w[4 * i + 2] = x.z, r.w[4 * i + 3] = x.w;
+  }
   return r;
+}
+__device__ __forceinline__ uint32_t pack_two(float a, float b, __half) {
+  const __half2 x = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+__device__ __forceinline__ uint32_t pack_two(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&x);
 }
 template <class T>
 __device__ __forceinline__ void store_eight(T* p, const float (&v)[8]) {
-  Eight<T> r;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) from_float(v[i], r.e[i]);
-  const uint4* from = reinterpret_cast<const uint4*>(&r);
   uint4* to = reinterpret_cast<uint4*>(p);
-#pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) to[i] = from[i];
+  if constexpr (sizeof(T) == 4) {
+    to[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    to[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+  } else {
+    to[0] = make_uint4(pack_two(v[0], v[1], T()), pack_two(v[2], v[3], T()), pack_two(v[4], v[5], T()), pack_two(v[6], v[7], T()));
+  }
 }
 
 // Magnitudes as ordered bits: a NaN is above Inf and Inf above all numbers, so a maximum keeps them.

@@ -7,7 +7,8 @@
 // output is rounded once.
 //
 // Bound by memory: every row is read once, held in registers between its sum and its results, and written
-// once.  Several threads share a row, eight elements each: neighbours where rows start at multiples of 16
+// once.  With many rows the CTAs stay, keep w in registers, and fetch their next row while they work on one: the
+// waits of a row (for its values, its sum's barrier) would otherwise follow each other.  Several threads share a row, eight elements each: neighbours where rows start at multiples of 16
 // bytes (16-byte accesses; a block of 128 is 16 threads), otherwise 32 apart (a warp's accesses of two
 // bytes are then neighbours; a block is half of a warp's 256 elements).
 #include "oz_elements.cuh"
@@ -16,8 +17,6 @@
 
 namespace oz {
 namespace {
-
-constexpr int kRowsBack = 2;  // CTAs of the backward pass on an SM
 
 struct NormParams {
   int k, rows;
@@ -63,15 +62,8 @@ __device__ __forceinline__ int first_column(int j) {
 
 template <class T, bool VEC>
 __device__ __forceinline__ Eight<T> fetch(const T* row, int c, int k) {
-  Eight<T> r;
   if (VEC && c + 8 <= k) return load_eight(row + c);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int at = c + e * (VEC ? 1 : 32);
-    if (at < k) r.e[e] = row[at];
-    else from_float(0.0f, r.e[e]);
-  }
-  return r;
+  return gather_eight(row + c, VEC ? 1 : 32, [&](int e) { return c + e * (VEC ? 1 : 32) < k; });
 }
 template <class T, bool VEC>
 __device__ __forceinline__ void put(T* row, int c, int k, const float (&v)[8]) {
@@ -86,139 +78,158 @@ __device__ __forceinline__ void put(T* row, int c, int k, const float (&v)[8]) {
   }
 }
 
-// RUNS: runs of eight elements a thread holds.  blockDim (threads of a row, rows).
-template <class T, bool VEC, int RUNS>
-__global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormParams a) {
-  __shared__ float meet[32];
+// RUNS: runs of eight elements a thread holds.  blockDim (threads of a row, rows).  STAY: a CTA takes every
+// gridDim.x-th group of rows, at most 256 threads; otherwise one.
+template <class T, bool VEC, int RUNS, bool STAY>
+__global__ void __launch_bounds__(STAY ? 256 : 1024, STAY ? (RUNS == 1 ? 4 : RUNS == 2 ? 3 : 2) : 1) norm_kernel(const __grid_constant__ NormParams a) {
+  __shared__ float meet[2][32];
   let_next_start();
   wait_for_previous();
-  const int row = blockIdx.x * blockDim.y + threadIdx.y;
-  const bool have = row < a.rows;  // (a whole warp's; rows of several warps are alone in their CTA)
-  const int lane = threadIdx.x & 31;
-  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-  const T* res = static_cast<const T*>(a.residual) + row * a.ldr;
-  float h[RUNS][8];
-  float sum = 0.0f;
+  const int lane = threadIdx.x & 31, step = STAY ? gridDim.x * blockDim.y : a.rows;
+  int row = blockIdx.x * blockDim.y + threadIdx.y, turn = 0;
+  Eight<T> nx[RUNS], nr[RUNS], w[RUNS];
+  auto ask = [&](int row) {
 #pragma unroll
-  for (int j = 0; j < RUNS; ++j) {
-    const int c = first_column<VEC>(j);
+    for (int j = 0; j < RUNS; ++j) {
+      const int c = first_column<VEC>(j), k = row < a.rows ? a.k : 0;
+      nx[j] = fetch<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx, c, k);
+      if (a.residual) nr[j] = fetch<T, VEC>(static_cast<const T*>(a.residual) + row * a.ldr, c, k);
+    }
+  };
+  ask(row);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[j][e] = 0.0f;
-    if (have && c < a.k) {
-      const Eight<T> vx = fetch<T, VEC>(x, c, a.k);
-      if (a.residual) {
-        const Eight<T> vr = fetch<T, VEC>(res, c, a.k);
+  for (int j = 0; j < RUNS; ++j) w[j] = fetch<T, VEC>(static_cast<const T*>(a.w), first_column<VEC>(j), a.k);
+  for (; row < a.rows; row += step, turn ^= 1) {
+    float h[RUNS][8];
+    float sum = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[j][e] = to_float(vx.e[e]) + to_float(vr.e[e]);
-      } else {
+    for (int j = 0; j < RUNS; ++j) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[j][e] = to_float(vx.e[e]);
+      for (int e = 0; e < 8; ++e) {
+        h[j][e] = nx[j].get(e);
+        if (a.residual) h[j][e] += nr[j].get(e);
+        sum = fmaf(h[j][e], h[j][e], sum);
       }
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fmaf(h[j][e], h[j][e], sum);
-  }
-  sum = row_sum(sum, meet);
-  const float r = 1.0f / sqrtf(sum / static_cast<float>(a.k) + a.eps);
-  if (!have) return;
-  if (threadIdx.x == 0) a.rstd[row] = r;
-#pragma unroll
-  for (int j = 0; j < RUNS; ++j) {
-    const int c = first_column<VEC>(j);
-    float y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = 0.0f;
-    if (c < a.k) {
-      if (a.h) put<T, VEC>(static_cast<T*>(a.h) + row * a.ldh, c, a.k, h[j]);
-      const Eight<T> w = fetch<T, VEC>(static_cast<const T*>(a.w), c, a.k);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = h[j][e] * r * to_float(w.e[e]);
-      if (a.y) put<T, VEC>(static_cast<T*>(a.y) + row * a.ldy, c, a.k, y);
-    }
+    if (STAY) ask(row + step);
+    sum = row_sum(sum, meet[turn]);
+    const float r = 1.0f / sqrtf(sum / static_cast<float>(a.k) + a.eps);
+    if (threadIdx.x == 0) a.rstd[row] = r;
     uint8_t* q = a.q + row * a.ldq;
-    if (VEC) {  // 16 lanes hold a block
-      uint32_t most = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) most = max(most, magnitude(y[e]));
+    for (int j = 0; j < RUNS; ++j) {
+      const int c = first_column<VEC>(j);
+      if (c < a.k && a.h) put<T, VEC>(static_cast<T*>(a.h) + row * a.ldh, c, a.k, h[j]);
 #pragma unroll
-      for (int d = 1; d < 16; d <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
-      const float scale = scale_of<false>(most);
-      const uint2 v = eight_bits<false>(y, 1.0f / scale);
-      if (c + 8 <= a.k) {
-        *reinterpret_cast<uint2*>(q + c) = v;
-      } else {
+      for (int e = 0; e < 8; ++e) h[j][e] = h[j][e] * r * w[j].get(e);
+      float (&y)[8] = h[j];
+      if (c < a.k && a.y) put<T, VEC>(static_cast<T*>(a.y) + row * a.ldy, c, a.k, y);
+      if (VEC) {  // 16 lanes hold a block
+        uint32_t most = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most = max(most, c + e < a.k ? magnitude(y[e]) : 0u);
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+        const float scale = scale_of<false>(most);
+        const uint2 v = eight_bits<false>(y, 1.0f / scale);
+        if (c + 8 <= a.k) {
+          *reinterpret_cast<uint2*>(q + c) = v;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c + e < a.k) q[c + e] = static_cast<uint8_t>(e < 4 ? v.x >> (8 * e) : v.y >> (8 * (e - 4)));
+        }
+        if ((lane & 15) == 0 && c < a.k) a.s[c / kScaleBlock * a.lds + row] = scale;
+      } else {  // the warp holds two blocks, elements 0 - 3 and 4 - 7
+        uint32_t first = 0, second = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          first = max(first, c + 32 * e < a.k ? magnitude(y[e]) : 0u);
+          second = max(second, c + 32 * (e + 4) < a.k ? magnitude(y[e + 4]) : 0u);
+        }
+        const float scale[2] = {scale_of<false>(__reduce_max_sync(0xFFFFFFFFu, first)), scale_of<false>(__reduce_max_sync(0xFFFFFFFFu, second))};
+        const float inverse[2] = {1.0f / scale[0], 1.0f / scale[1]};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] *= inverse[e >> 2];
+        const uint2 v = eight_bits<false>(y, 1.0f);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (c + e < a.k) q[c + e] = static_cast<uint8_t>(e < 4 ? v.x >> (8 * e) : v.y >> (8 * (e - 4)));
+          if (c + 32 * e < a.k) q[c + 32 * e] = static_cast<uint8_t>(e < 4 ? v.x >> (8 * e) : v.y >> (8 * (e - 4)));
+        if (lane == 0 && c < a.k) a.s[c / kScaleBlock * a.lds + row] = scale[0];
+        if (lane == 0 && c + 128 < a.k) a.s[(c / kScaleBlock + 1) * a.lds + row] = scale[1];
       }
-      if ((lane & 15) == 0 && c < a.k) a.s[c / kScaleBlock * a.lds + row] = scale;
-    } else {  // the warp holds two blocks, elements 0 - 3 and 4 - 7
-      uint32_t first = 0, second = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        first = max(first, magnitude(y[e]));
-        second = max(second, magnitude(y[e + 4]));
-      }
-      const float scale[2] = {scale_of<false>(__reduce_max_sync(0xFFFFFFFFu, first)), scale_of<false>(__reduce_max_sync(0xFFFFFFFFu, second))};
-      const float inverse[2] = {1.0f / scale[0], 1.0f / scale[1]};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] *= inverse[e >> 2];
-      const uint2 v = eight_bits<false>(y, 1.0f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + 32 * e < a.k) q[c + 32 * e] = static_cast<uint8_t>(e < 4 ? v.x >> (8 * e) : v.y >> (8 * (e - 4)));
-      if (lane == 0 && c < a.k) a.s[c / kScaleBlock * a.lds + row] = scale[0];
-      if (lane == 0 && c + 128 < a.k) a.s[(c / kScaleBlock + 1) * a.lds + row] = scale[1];
     }
   }
 }
 
 // Gradients: a CTA takes every gridDim.x-th row and keeps dw's sums of its columns in registers; the CTAs' sums
 // go to the workspace and are added in their order by a second launch, so results do not depend on timing.
+// With one run a thread the next row is fetched meanwhile (two and more leave no registers for it).
 template <class T, bool VEC, int RUNS>
 __global__ void __launch_bounds__(1024) norm_back_kernel(const __grid_constant__ NormBackParams a) {
+  constexpr bool EARLY = RUNS == 1;
   __shared__ float meet[2][32];
   let_next_start();
   wait_for_previous();
   float dw[RUNS][8];
 #pragma unroll
   for (int i = 0; i < RUNS * 8; ++i) dw[i >> 3][i & 7] = 0.0f;
-  Eight<T> dy[RUNS], h[RUNS], w[RUNS];
+  Eight<T> dy[RUNS], h[RUNS], dh[RUNS], w[RUNS];
+  float r = 0.0f;
+  auto ask = [&](int row) {
+    const int k = row < a.rows ? a.k : 0;
+#pragma unroll
+    for (int j = 0; j < RUNS; ++j) {
+      const int c = first_column<VEC>(j);
+      dy[j] = fetch<T, VEC>(static_cast<const T*>(a.dy) + row * a.lddy, c, k);
+      h[j] = fetch<T, VEC>(static_cast<const T*>(a.h) + row * a.ldh, c, k);
+      if (EARLY && a.dh) dh[j] = fetch<T, VEC>(static_cast<const T*>(a.dh) + row * a.lddh, c, k);
+    }
+    if (k) r = a.rstd[row];
+  };
+  if (EARLY) ask(blockIdx.x);
 #pragma unroll
   for (int j = 0; j < RUNS; ++j) w[j] = fetch<T, VEC>(static_cast<const T*>(a.w), first_column<VEC>(j), a.k);
   int turn = 0;
   for (int row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-    const float r = a.rstd[row];
+    if (!EARLY) ask(row);
     float dot = 0.0f;
-#pragma unroll
-    for (int j = 0; j < RUNS; ++j) {
-      const int c = first_column<VEC>(j);
-      dy[j] = fetch<T, VEC>(static_cast<const T*>(a.dy) + row * a.lddy, c, a.k);
-      h[j] = fetch<T, VEC>(static_cast<const T*>(a.h) + row * a.ldh, c, a.k);
-    }
+    const float rs = r;
+    float g[EARLY ? 8 : 1], x[EARLY ? 8 : 1];  // one run: dy w and h in FP32, so that the next row's may come
 #pragma unroll
     for (int j = 0; j < RUNS; ++j) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float d = to_float(dy[j].e[e]), x = to_float(h[j].e[e]);
-        dot = fmaf(d * to_float(w[j].e[e]), x, dot);
-        dw[j][e] = fmaf(d * r, x, dw[j][e]);
+        const float d = dy[j].get(e), v = h[j].get(e), gw = d * w[j].get(e);
+        dot = fmaf(gw, v, dot);
+        dw[j][e] = fmaf(d * rs, v, dw[j][e]);
+        if (EARLY) g[e] = gw, x[e] = v;
       }
+    }
+    float dx[8];
+    if (EARLY) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dx[e] = a.dh ? dh[0].get(e) : 0.0f;
+      ask(row + gridDim.x);
     }
     // Two rooms in turn: a warp writes one again only after the other's barrier.
     dot = row_sum(dot, meet[turn]) / static_cast<float>(a.k);
-    const float f = r * r * dot;
+    const float f = rs * rs * dot;
 #pragma unroll
     for (int j = 0; j < RUNS; ++j) {
       const int c = first_column<VEC>(j);
       if (c >= a.k) continue;
-      float dx[8];
+      if (EARLY) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dx[e] = r * (to_float(dy[j].e[e]) * to_float(w[j].e[e]) - to_float(h[j].e[e]) * f);
-      if (a.dh) {
-        const Eight<T> dh = fetch<T, VEC>(static_cast<const T*>(a.dh) + row * a.lddh, c, a.k);
+        for (int e = 0; e < 8; ++e) dx[e] += rs * (g[e] - x[e] * f);
+      } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dx[e] += to_float(dh.e[e]);
+        for (int e = 0; e < 8; ++e) dx[e] = rs * (dy[j].get(e) * w[j].get(e) - h[j].get(e) * f);
+        if (a.dh) {
+          dh[j] = fetch<T, VEC>(static_cast<const T*>(a.dh) + row * a.lddh, c, a.k);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dx[e] += dh[j].get(e);
+        }
       }
       put<T, VEC>(static_cast<T*>(a.dx) + row * a.lddx, c, a.k, dx);
     }
@@ -266,22 +277,26 @@ struct Shape {
   int threads, rows, runs;  // threads of a row, rows of a CTA, runs a thread
 };
 
-// Threads of a row: one run each where that is few rows' latency or few threads, otherwise about 256 threads.
+// Threads of a row: one run each for few rows (latency), otherwise about 256 threads.
 Shape shape_of(int k, bool spread) {
   const int runs_all = (k + 255) / 256 * 32;  // whole warps of runs
   int runs = 1;
   while (runs < 4 && (runs_all / runs > 1024 || (!spread && runs_all / runs > 256))) runs *= 2;
   const int threads = ((runs_all + runs - 1) / runs + 31) / 32 * 32;
-  return {threads, threads > 32 ? 1 : 4, runs};
+  return {threads, threads >= 128 ? 1 : 128 / threads, runs};
 }
 
 template <class T, bool VEC>
 cudaError_t launch_norm(const NormParams& a, int sms, cudaStream_t stream) {
-  const Shape s = shape_of(a.k, a.rows < 4 * sms);
+  Shape s = shape_of(a.k, a.rows < 4 * sms);
+  if (s.threads > 32) s.rows = 1;  // (several rows of one warp each need no barrier)
+  const int groups = (a.rows + s.rows - 1) / s.rows, threads = s.threads * s.rows;
+  const int resident = sms * (threads <= 256 ? 256 / threads : 1) * (s.runs == 1 ? 4 : s.runs == 2 ? 3 : 2);
+  const bool stay = threads <= 256 && groups > resident;
   cudaError_t e = cudaErrorInvalidValue;
   auto go = [&](void (*kernel)(NormParams)) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.rows + s.rows - 1) / s.rows);
+    cfg.gridDim = dim3(stay ? resident : groups);
     cfg.blockDim = dim3(s.threads, s.rows);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -293,9 +308,9 @@ cudaError_t launch_norm(const NormParams& a, int sms, cudaStream_t stream) {
     if (e != cudaSuccess) cudaGetLastError();
   };
   switch (s.runs) {
-    case 1: go(norm_kernel<T, VEC, 1>); break;
-    case 2: go(norm_kernel<T, VEC, 2>); break;
-    default: go(norm_kernel<T, VEC, 4>); break;
+    case 1: go(stay ? norm_kernel<T, VEC, 1, true> : norm_kernel<T, VEC, 1, false>); break;
+    case 2: go(stay ? norm_kernel<T, VEC, 2, true> : norm_kernel<T, VEC, 2, false>); break;
+    default: go(stay ? norm_kernel<T, VEC, 4, true> : norm_kernel<T, VEC, 4, false>); break;
   }
   return e;
 }
@@ -310,7 +325,7 @@ cudaError_t norm_of_type(const NormParams& a, int sms, cudaStream_t stream) {
 
 template <class T, bool VEC>
 cudaError_t launch_norm_back(const NormBackParams& a, cudaStream_t stream) {
-  const Shape s = shape_of(a.k, true);
+  const Shape s = shape_of(a.k, true);  // (one row a CTA)
   auto kernel = s.runs == 1 ? norm_back_kernel<T, VEC, 1> : s.runs == 2 ? norm_back_kernel<T, VEC, 2> : norm_back_kernel<T, VEC, 4>;
   return launch_overlapping(kernel, dim3(a.parts), s.threads, 0, stream, a);
 }
@@ -324,8 +339,9 @@ cudaError_t norm_back_of_type(const NormBackParams& a, cudaStream_t stream) {
   return launch_overlapping(norm_weight_kernel<T>, dim3((a.k + 31) / 32), 256, 0, stream, a.part, a.parts, a.k, static_cast<T*>(a.dw));
 }
 
+// CTAs of the backward pass: as many as run at once on 152 SMs (at most 64 registers a thread).
 int parts_of(int rows, int k) {
-  const int most = 152 * kRowsBack * (k <= 2048 ? 4 : k <= 4096 ? 2 : 1);
+  const int threads = shape_of(k, true).threads, most = 152 * (threads >= 128 ? 1024 / threads : 8);
   return rows < most ? rows : most;
 }
 

@@ -7,6 +7,11 @@
 // Bound by memory: an element is read once and its one or two bytes are written once.  A CTA holds a 128 x 128
 // tile in registers (a thread eight neighbours of eight rows, 16 rows apart), so that all three kinds of
 // block are inside a tile: rows by shuffles among 16 lanes, columns by one exchange in shared memory.
+// Two CTAs of such threads fit an SM, and their 64 KB of 16-bit tiles on the way do not keep the memory busy:
+// 16-bit elements (FP32 tiles are twice as large) are copied into shared memory three tiles ahead, where each
+// thread finds its own eight 16-byte pieces again, so that no barrier is needed.
+#include <atomic>
+
 #include "oz_elements.cuh"
 #include "oz_device.cuh"
 #include "oz_ragged.cuh"
@@ -42,11 +47,42 @@ __device__ __forceinline__ void put_bytes(uint8_t* row, int c, int k, uint2 w) {
   }
 }
 
-// BLOCK: an OZ_BLOCK_*.
-template <class T, int BLOCK, bool E5M2>
+// Where a tile lies: its matrix, block of rows, first row, how many rows it has, and this thread's first column.
+struct Place {
+  int mat, block, row, count, c;
+};
+
+template <bool MATRIX, bool RAGGED_POSSIBLE>
+__device__ __forceinline__ Place place_of(const QuantParams& a, const int* off, long long tile) {
+  Place p;
+  const long long rt = tile / a.col_tiles;
+  p.c = static_cast<int>(tile - rt * a.col_tiles) * TILE + 8 * (threadIdx.x & 15);
+  p.mat = MATRIX ? static_cast<int>(rt / a.row_tiles) : 0;
+  p.block = static_cast<int>(rt - static_cast<long long>(p.mat) * a.row_tiles);
+  p.row = p.block * TILE;
+  p.count = min(TILE, a.rows - p.row);
+  if (RAGGED_POSSIBLE && a.offsets) {
+    int lo = 0, hi = a.groups;  // the last group whose first block is not past this one
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first_column_block(off[mid], mid) <= p.block) lo = mid; else hi = mid;
+    }
+    const int b = p.block - first_column_block(off[lo], lo);
+    p.row = off[lo] + b * TILE;
+    p.count = b < 0 ? 0 : max(0, min(TILE, off[lo + 1] - p.row));
+  }
+  return p;
+}
+
+constexpr int kAhead = 3;  // tiles on their way into shared memory
+constexpr int kTileBytes16 = TILE * TILE * 2;
+
+// BLOCK: an OZ_BLOCK_*.  AHEAD: 16-bit rows at multiples of 16 bytes.
+template <class T, int BLOCK, bool E5M2, bool AHEAD>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constant__ QuantParams a) {
   constexpr bool ROW = BLOCK == OZ_BLOCK_ROW || BLOCK == OZ_BLOCK_BOTH, COLUMN = BLOCK == OZ_BLOCK_COLUMN || BLOCK == OZ_BLOCK_BOTH;
   constexpr bool MATRIX = BLOCK == OZ_BLOCK_MATRIX;
+  extern __shared__ uint4 ahead[];  // [kAhead][8][kThreads]
   __shared__ int off[COLUMN ? OZ_MAX_GROUPS + 1 : 1];
   __shared__ uint32_t most[kThreads / 32][TILE];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -58,36 +94,43 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
     if (warp == 0 && clamp_offsets(a.offsets, a.groups, a.rows, off) && lane == 0 && blockIdx.x == 0) atomicExch(a.status, OZ_EINVAL);
     __syncthreads();
   }
-  for (long long tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
-    const long long rt = tile / a.col_tiles;
-    const int c = static_cast<int>(tile - rt * a.col_tiles) * TILE + c8;
-    const int mat = MATRIX ? static_cast<int>(rt / a.row_tiles) : 0;
-    const int block = static_cast<int>(rt - static_cast<long long>(mat) * a.row_tiles);
-    int row = block * TILE, count = min(TILE, a.rows - row);  // the tile's first row, how many it has
-    if (ragged) {
-      int lo = 0, hi = a.groups;  // the last group whose first block is not past this one
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first_column_block(off[mid], mid) <= block) lo = mid; else hi = mid;
+  // A tile's pieces of this thread into its places of slot s; those that do not exist as zeros.
+  auto send = [&](long long tile, int slot) {
+    if (tile < a.tiles) {
+      const Place p = place_of<MATRIX, COLUMN>(a, off, tile);
+      const T* x = static_cast<const T*>(a.x) + p.mat * a.stride_x + p.c;
+      const int bytes = max(0, min(8, a.k - p.c)) * 2;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + 16 * i;
+        const bool have = r < p.count && bytes;
+        const uint32_t to = smem_u32(ahead + (slot * 8 + i) * kThreads + threadIdx.x);
+        const T* from = have ? x + static_cast<long long>(p.row + r) * a.ldx : static_cast<const T*>(a.x);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(have ? bytes : 0) : "memory");
       }
-      const int b = block - first_column_block(off[lo], lo);
-      row = off[lo] + b * TILE;
-      count = b < 0 ? 0 : max(0, min(TILE, off[lo + 1] - row));
     }
-    const T* x = static_cast<const T*>(a.x) + mat * a.stride_x;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int slot = 0;
+  if (AHEAD) {
+    for (int s = 0; s < kAhead; ++s) send(blockIdx.x + static_cast<long long>(s) * gridDim.x, s);
+  }
+  for (long long tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+    const Place place = place_of<MATRIX, COLUMN>(a, off, tile);
+    const int c = place.c, mat = place.mat, block = place.block, row = place.row, count = place.count;
     Eight<T> v[8];
+    if constexpr (AHEAD) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = r0 + 16 * i;
-      const T* from = x + static_cast<long long>(row + r) * a.ldx + c;
-      if (r < count && a.aligned && c + 8 <= a.k) {
-        v[i] = load_eight(from);
-      } else {
+      for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const Eight<T>*>(ahead + (slot * 8 + i) * kThreads + threadIdx.x);
+    } else {
+      const T* x = static_cast<const T*>(a.x) + mat * a.stride_x;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (r < count && c + e < a.k) v[i].e[e] = from[e];
-          else from_float(0.0f, v[i].e[e]);
-        }
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + 16 * i;
+        const T* from = x + static_cast<long long>(row + r) * a.ldx + c;
+        v[i] = r < count && a.aligned && c + 8 <= a.k ? load_eight(from)
+                                                      : gather_eight(from, 1, [&](int e) { return r < count && c + e < a.k; });
       }
     }
     uint32_t by_row[8], by_col[8] = {};
@@ -96,10 +139,14 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
       by_row[i] = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t m = magnitude(to_float(v[i].e[e]));
+        const uint32_t m = magnitude(v[i].get(e));
         by_row[i] = max(by_row[i], m);
         if (COLUMN) by_col[e] = max(by_col[e], m);
       }
+    }
+    if constexpr (AHEAD) {  // the slot has been read (every value of it is in a maximum)
+      send(tile + static_cast<long long>(kAhead) * gridDim.x, slot);
+      slot = slot + 1 == kAhead ? 0 : slot + 1;
     }
     if (ROW) {
 #pragma unroll
@@ -111,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
           const float scale = scale_of<E5M2>(by_row[i]);
           float f[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = to_float(v[i].e[e]);
+          for (int e = 0; e < 8; ++e) f[e] = v[i].get(e);
           put_bytes(a.q + static_cast<long long>(row + r) * a.ldq, c, a.k, eight_bits<E5M2>(f, 1.0f / scale));
           if (c8 == 0) a.s[c / TILE * a.lds + row + r] = scale;
         }
@@ -144,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
         if (r < written) {
           float f[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = to_float(v[i].e[e]) * inverse[e];
+          for (int e = 0; e < 8; ++e) f[e] = v[i].get(e) * inverse[e];
           put_bytes(a.qc + (to + r) * a.ldqc, c, a.k, r < count ? eight_bits<E5M2>(f, 1.0f) : make_uint2(0, 0));
         }
       }
@@ -169,7 +216,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
         if (r < count) {
           float f[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = to_float(v[i].e[e]);
+          for (int e = 0; e < 8; ++e) f[e] = v[i].get(e);
           put_bytes(q + static_cast<long long>(row + r) * a.ldq, c, a.k, eight_bits<E5M2>(f, inverse));
         }
       }
@@ -203,11 +250,39 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
   }
 }
 
+template <class T, int BLOCK, bool E5M2, bool AHEAD>
+cudaError_t start(const QuantParams& a, cudaStream_t stream) {
+  auto kernel = quantize_kernel<T, BLOCK, E5M2, AHEAD>;
+  constexpr int smem = AHEAD ? kAhead * kTileBytes16 : 0;
+  long long grid = 1 << 20;
+  if (AHEAD) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    // The shared-memory limit is the function's, in this context: set on the first launch (and again below, should a
+    // launch be refused, in a new context after a device reset).
+    static std::atomic<bool> ready[64] = {};
+    const bool known = dev < 64 && ready[dev].load(std::memory_order_acquire);
+    if (e == cudaSuccess && !known) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev].store(true, std::memory_order_release);
+    grid = 2 * sms;  // as many as run at once
+    const dim3 ctas(static_cast<unsigned>(a.tiles < grid ? a.tiles : grid));
+    e = launch_overlapping(kernel, ctas, kThreads, smem, stream, a);
+    if (e != cudaErrorInvalidValue || !known) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_overlapping(kernel, dim3(static_cast<unsigned>(a.tiles < grid ? a.tiles : grid)), kThreads, smem, stream, a);
+}
+
 template <class T, int BLOCK>
 cudaError_t launch_quantize(QuantParams a, bool e5m2, cudaStream_t stream) {
   a.aligned = rows_aligned<T>(a.x, a.ldx, a.rows) && (a.mats == 1 || a.stride_x * sizeof(T) % 16 == 0);
-  const unsigned grid = static_cast<unsigned>(a.tiles < 1 << 20 ? a.tiles : 1 << 20);
-  return launch_overlapping(e5m2 ? quantize_kernel<T, BLOCK, true> : quantize_kernel<T, BLOCK, false>, dim3(grid), kThreads, 0, stream, a);
+  if constexpr (sizeof(T) == 2) {
+    if (a.aligned) return e5m2 ? start<T, BLOCK, true, true>(a, stream) : start<T, BLOCK, false, true>(a, stream);
+  }
+  return e5m2 ? start<T, BLOCK, true, false>(a, stream) : start<T, BLOCK, false, false>(a, stream);
 }
 
 template <class T>

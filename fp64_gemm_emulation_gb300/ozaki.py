@@ -14,6 +14,7 @@ exception.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import os
@@ -819,23 +820,30 @@ def _f8(dtype) -> int:
     return code
 
 
-def _new_f8(shape, dtype, device):
-    """A new 8-bit tensor whose rows start at multiples of 16 bytes."""
-    k = shape[-1]
-    if k % 16 == 0:
-        return _torch().empty(shape, dtype=dtype, device=device)
-    return _torch().empty((*shape[:-1], (k + 15) // 16 * 16), dtype=dtype, device=device)[..., :k]
+def _new(shape, dtype, device, ld: int | None = None):
+    """A new row-major tensor whose rows start ld elements apart (by default, without gaps)."""
+    n = len(shape) - 1
+    stride = [1] * (n + 1)
+    if n:
+        stride[n - 1] = step = shape[n] if ld is None else ld
+        for i in range(n - 2, -1, -1):
+            stride[i] = step = step * shape[i + 1]
+    return _torch().empty_strided(shape, stride, dtype=dtype, device=device)
+
+
+def _ld16(k: int) -> int:
+    """The row stride of a new 8-bit tensor: rows start at multiples of 16 bytes."""
+    return (k + 15) // 16 * 16 or 16
 
 
 def _row_scales(S, what: str, rows: int, k: int, device) -> int:
     """Leading dimension of the scales of row blocks: (rows, blocks) with the rows of a block next to each other."""
-    shape, blocks = S.shape, (k + 127) // 128
+    shape, stride, blocks = S.shape, S.stride(), (k + 127) // 128
     if S.dtype != _torch().float32 or S.device != device:
         raise ValueError(f"{what} must be float32 on the operands' device")
-    if len(shape) != 2 or shape[0] != rows or shape[1] != blocks:
+    if shape != (rows, blocks):
         raise ValueError(f"{what} must have shape ({rows}, {blocks}): {tuple(shape)}")
-    stride = S.stride()
-    if (rows > 1 and stride[0] != 1) or (blocks > 1 and stride[1] < rows):
+    if (rows > 1 and stride[0] != 1) or (blocks > 1 and not rows <= stride[1] <= _INT_MAX):
         raise ValueError(f"{what} must be column-major (stride(0) == 1): colmajor makes it so")
     return max(1, rows, stride[1] if blocks > 1 else 0)
 
@@ -843,45 +851,48 @@ def _row_scales(S, what: str, rows: int, k: int, device) -> int:
 def _column_scales(S, what: str, blocks: int, k: int, device) -> int:
     if S.dtype != _torch().float32 or S.device != device:
         raise ValueError(f"{what} must be float32 on the operands' device")
-    if tuple(S.shape) != (blocks, k):
+    if S.shape != (blocks, k):
         raise ValueError(f"{what} must have shape ({blocks}, {k}): {tuple(S.shape)}")
     return _tokens(S, what, k)
 
 
-def _matrix_scales(S, what: str, shape, device):
-    want = (*shape[:-2], (shape[-2] + 127) // 128, (shape[-1] + 127) // 128)
-    if S.dtype != _torch().float32 or S.device != device or not S.is_contiguous():
-        raise ValueError(f"{what} must be contiguous float32 on the operands' device")
-    if S.shape != want:
-        raise ValueError(f"{what} must have shape {want}: {tuple(S.shape)}")
-
-
-def _f8_rows(Q, what: str, features: int | None = None) -> int:
-    """Leading dimension of an 8-bit operand, whose rows start at multiples of 16 bytes."""
-    ld = _tokens(Q, what, features)
-    if Q.numel() and (Q.data_ptr() % 16 or (Q.shape[0] > 1 and ld % 16)):
+def _f8_rows(Q, what: str, features: int | None = None):
+    """(rows, features, leading dimension) of an 8-bit operand, whose rows start at multiples of 16 bytes."""
+    shape, stride = Q.shape, Q.stride()
+    if len(shape) == 2 and 1 < shape[0] <= _INT_MAX and 0 < shape[1] <= stride[0] <= _INT_MAX and stride[1] == 1 and \
+            features in (None, shape[1]) and not (stride[0] | Q.data_ptr()) & 15:
+        return shape[0], shape[1], stride[0]
+    ld = _tokens(Q, what, features)  # (says what is wrong)
+    if Q.numel() and (Q.data_ptr() & 15 or (shape[0] > 1 and ld & 15)):
         raise ValueError(f"{what} must have rows that start at multiples of 16 bytes")
-    return ld
+    return shape[0], shape[1], ld
 
 
 def _f8_experts(W, SW, device):
     """(groups, n, k, row stride, matrix stride) of 8-bit weights (groups, n, k), or (n, k) for one group."""
-    if W.dim() == 2:
+    if len(W.shape) == 2:
         W, SW = W[None], (SW[None] if SW.dim() == 2 else SW)
-    ld, stride = _experts(W, "W")
-    groups, n, k = W.shape
-    if n and k and (W.data_ptr() % 16 or (n > 1 and ld % 16) or (groups > 1 and stride % 16)):
+    groups, n, k = shape = W.shape
+    stride = W.stride()
+    if n > 1 and groups > 1 and 0 < k <= stride[1] <= _INT_MAX and stride[2] == 1 and stride[0] >= stride[1] * n and n <= _INT_MAX:
+        ld, step = stride[1], stride[0]
+    else:
+        ld, step = _experts(W, "W")  # (says what is wrong)
+    if n and k and (W.data_ptr() & 15 or (n > 1 and ld & 15) or (groups > 1 and step & 15)):
         raise ValueError("W must have rows and matrices that start at multiples of 16 bytes")
-    if W.device != device:
+    if W.device != device or SW.device != device:
         raise ValueError("operands must share one device")
-    _matrix_scales(SW, "the scales of W", W.shape, device)
-    return groups, n, k, ld, stride
+    want = (groups, (n + 127) // 128, (k + 127) // 128)
+    if SW.dtype != _torch().float32 or SW.shape != want or not SW.is_contiguous():
+        raise ValueError(f"the scales of W must be contiguous float32 of shape {want}: {tuple(SW.shape)}")
+    return groups, n, k, ld, step
 
 
 def _cuda(t, what: str):
-    if t.device.type != "cuda":
+    device = t.device
+    if device.type != "cuda":
         raise ValueError(f"{what} must be a CUDA tensor")
-    return t.device
+    return device
 
 
 def _product_offsets(offsets, groups: int | None, device):
@@ -893,20 +904,26 @@ def _product_offsets(offsets, groups: int | None, device):
     return offsets.data_ptr()
 
 
-def _output(out, what: str, shape, dtype, device):
-    """A new 16-bit output, or the given one, checked."""
+def _output(out, what: str, rows: int, features: int, dtype, device):
+    """(output, its type's code, its leading dimension): new, 16-bit, or the given one, checked."""
     if out is None:
         if dtype is None:
             dtype = _torch().bfloat16
-        out = _torch().empty(shape, dtype=dtype, device=device)
-    elif out.device != device or (dtype is not None and out.dtype != dtype):
-        raise ValueError(f"{what} must be on the operands' device, with the dtype asked for")
-    if out.shape != shape:
-        raise ValueError(f"{what} must have shape {tuple(shape)}: {tuple(out.shape)}")
-    code = _dtype(out)
+        out, ld = _new((rows, features), dtype, device), max(1, features)
+    else:
+        if out.device != device or (dtype is not None and out.dtype != dtype):
+            raise ValueError(f"{what} must be on the operands' device, with the dtype asked for")
+        ld = _tokens(out, what, features)
+        if out.shape[0] != rows:
+            raise ValueError(f"{what} must have {rows} rows")
+    return out, _16bit(out, what), ld
+
+
+def _16bit(t, what: str) -> int:
+    code = _dtype(t)
     if code == OZ_F32:
         raise TypeError(f"{what} must be bfloat16 or float16")
-    return out, code
+    return code
 
 
 def ozaki_f8_column_blocks(rows: int, groups: int | None = None) -> int:
@@ -948,17 +965,16 @@ def ozaki_quantize_f8(X, block: str = "row", offsets=None, dtype=None, stream=No
         n, k = X.shape[-2:]
         X3 = X if X.dim() == 3 else X[None] if X.dim() == 2 else X.view(-1, n, k)
         ldx, sx = _experts(X3, "X")
-        mats = X3.shape[0]
-        Q = _new_f8(X.shape, dtype, device)
-        S = torch.empty((*X.shape[:-2], (n + 127) // 128, (k + 127) // 128), dtype=torch.float32, device=device)
-        ldq = (k + 15) // 16 * 16 or 16
+        mats, ldq = X3.shape[0], _ld16(k)
+        Q = _new(X.shape, dtype, device, ldq)
+        S = _new((*X.shape[:-2], (n + 127) // 128, (k + 127) // 128), torch.float32, device)
         if mats:
             _run_on("ozaki_quantize_f8", (kind, k, n, mats, code, X.data_ptr(), ldx, sx, None, eight, Q.data_ptr(), ldq, ldq * n,
                                           S.data_ptr(), 0, None, 0, None, 0), None, None, device)
         return Q, S
     ldx = _tokens(X, "X")
     rows, k = X.shape
-    ldq = (k + 15) // 16 * 16 or 16
+    ldq = _ld16(k)
     groups, off, results, args = 1, None, [], []
     if offsets is not None:
         _offsets(offsets, None, device)
@@ -967,16 +983,16 @@ def ozaki_quantize_f8(X, block: str = "row", offsets=None, dtype=None, stream=No
             if groups > OZ_MAX_GROUPS:
                 raise ValueError(f"at most {OZ_MAX_GROUPS} groups: {groups}")
     if kind != OZ_BLOCK_COLUMN:
-        Q = _new_f8((rows, k), dtype, device)
-        S = torch.empty(((k + 127) // 128, rows), dtype=torch.float32, device=device)
-        results += [Q, S.t()]
+        Q = _new((rows, k), dtype, device, ldq)
+        S = torch.empty_strided((rows, (k + 127) // 128), (1, max(1, rows)), dtype=torch.float32, device=device)
+        results += [Q, S]
         args += [Q.data_ptr(), ldq, 0, S.data_ptr(), max(1, rows)]
     else:
         args += [None, 0, 0, None, 0]
     if kind != OZ_BLOCK_ROW:
         blocks = rows // 128 + groups if off else (rows + 127) // 128
-        Q = _new_f8((128 * blocks if off else rows, k), dtype, device)
-        S = torch.empty((blocks, k), dtype=torch.float32, device=device)
+        Q = _new((128 * blocks if off else rows, k), dtype, device, ldq)
+        S = _new((blocks, k), torch.float32, device)
         results += [Q, S]
         args += [Q.data_ptr(), ldq, S.data_ptr(), max(1, k)]
     else:
@@ -995,11 +1011,10 @@ def ozaki_grouped_gemm_f8(X, SX, W, SW, offsets=None, Y=None, dtype=None, stream
         return _call_on(other, ozaki_grouped_gemm_f8, X, SX, W, SW, offsets, Y, dtype)
     device = _cuda(X, "X")
     groups, n, k, ldw, sw = _f8_experts(W, SW, device)
-    ldx, rows = _f8_rows(X, "X", k), X.shape[0]
+    rows, _, ldx = _f8_rows(X, "X", k)
     lds = _row_scales(SX, "the scales of X", rows, k, device)
     off = _product_offsets(offsets, groups, device)
-    Y, code = _output(Y, "Y", (rows, n), dtype, device)
-    ldy = _tokens(Y, "Y", n)
+    Y, code, ldy = _output(Y, "Y", rows, n, dtype, device)
     _run_on("ozaki_grouped_gemm_f8", (n, k, rows, groups, _f8(W.dtype), W.data_ptr(), ldw, sw, SW.data_ptr(), _f8(X.dtype), X.data_ptr(),
                                       ldx, SX.data_ptr(), lds, off, code, Y.data_ptr(), ldy), None, None, device)
     return Y
@@ -1011,11 +1026,10 @@ def ozaki_grouped_gemm_f8_dgrad(dY, SdY, W, SW, offsets=None, dX=None, dtype=Non
         return _call_on(other, ozaki_grouped_gemm_f8_dgrad, dY, SdY, W, SW, offsets, dX, dtype)
     device = _cuda(dY, "dY")
     groups, n, k, ldw, sw = _f8_experts(W, SW, device)
-    lddy, rows = _f8_rows(dY, "dY", n), dY.shape[0]
+    rows, _, lddy = _f8_rows(dY, "dY", n)
     lds = _row_scales(SdY, "the scales of dY", rows, n, device)
     off = _product_offsets(offsets, groups, device)
-    dX, code = _output(dX, "dX", (rows, k), dtype, device)
-    lddx = _tokens(dX, "dX", k)
+    dX, code, lddx = _output(dX, "dX", rows, k, dtype, device)
     _run_on("ozaki_grouped_gemm_f8_dgrad", (n, k, rows, groups, _f8(W.dtype), W.data_ptr(), ldw, sw, SW.data_ptr(), _f8(dY.dtype), dY.data_ptr(),
                                             lddy, SdY.data_ptr(), lds, off, code, dX.data_ptr(), lddx), None, None, device)
     return dX
@@ -1030,9 +1044,9 @@ def ozaki_grouped_gemm_f8_wgrad(dY, SdY, X, SX, offsets=None, dW=None, dtype=Non
     if stream is not None and (other := _other_stream(stream, dY.device)):
         return _call_on(other, ozaki_grouped_gemm_f8_wgrad, dY, SdY, X, SX, offsets, dW, dtype, rows)
     device = _cuda(dY, "dY")
-    lddy, ldx = _f8_rows(dY, "dY"), _f8_rows(X, "X")
-    laid, n, k = dY.shape[0], dY.shape[1], X.shape[1]
-    if X.shape[0] != laid or X.device != device:
+    laid, n, lddy = _f8_rows(dY, "dY")
+    laid_x, k, ldx = _f8_rows(X, "X")
+    if laid_x != laid or X.device != device:
         raise ValueError("X and dY must have the same rows, on one device")
     off = _product_offsets(offsets, None, device)
     if off is None:
@@ -1047,8 +1061,15 @@ def ozaki_grouped_gemm_f8_wgrad(dY, SdY, X, SX, offsets=None, dW=None, dtype=Non
         if laid != 128 * (rows // 128 + groups):
             raise ValueError(f"with offsets X and dY must have 128 * (rows // 128 + groups) rows: {laid}")
     ldsy, ldsx = _column_scales(SdY, "the scales of dY", blocks, n, device), _column_scales(SX, "the scales of X", blocks, k, device)
-    dW, code = _output(dW, "dW", (groups, n, k), dtype, device)
-    ldw, sw = _experts(dW, "dW")
+    if dW is None:
+        dW, ldw, sw = _new((groups, n, k), dtype or _torch().bfloat16, device), max(1, k), max(1, k) * n
+    else:
+        if dW.device != device or (dtype is not None and dW.dtype != dtype):
+            raise ValueError("dW must be on the operands' device, with the dtype asked for")
+        ldw, sw = _experts(dW, "dW")
+        if dW.shape != (groups, n, k):
+            raise ValueError(f"dW must have shape {(groups, n, k)}: {tuple(dW.shape)}")
+    code = _16bit(dW, "dW")
     _run_on("ozaki_grouped_gemm_f8_wgrad", (n, k, rows, groups, _f8(dY.dtype), dY.data_ptr(), lddy, SdY.data_ptr(), ldsy, _f8(X.dtype),
                                             X.data_ptr(), ldx, SX.data_ptr(), ldsx, off, code, dW.data_ptr(), ldw, sw), None, None, device)
     return dW
@@ -1058,9 +1079,13 @@ def ozaki_grouped_gemm_f8_wgrad(dY, SdY, X, SX, offsets=None, dW=None, dtype=Non
 def _norm_rows(t, what: str, rows: int, k: int, like) -> int:
     if t.dtype != like.dtype or t.device != like.device:
         raise ValueError(f"{what} must have X's dtype and device")
-    if t.shape[0] != rows:
+    shape, stride = t.shape, t.stride()
+    if shape == (rows, k) and rows > 1 and k > 0 and stride[1] == 1 and k <= stride[0] <= _INT_MAX:
+        return stride[0]
+    ld = _tokens(t, what, k)  # (says what is wrong)
+    if shape[0] != rows:
         raise ValueError(f"{what} must have {rows} rows")
-    return _tokens(t, what, k)
+    return ld
 
 
 def _norm_weight(W, k: int, like):
@@ -1088,18 +1113,20 @@ def ozaki_rms_norm_f8(X, W, residual=None, eps: float = 1e-6, H=None, Y=None, st
     if residual is not None:
         ldr = _norm_rows(residual, "residual", rows, k, X)
         if H is None:
-            H = torch.empty((rows, k), dtype=X.dtype, device=device)
-    if H is not None:
+            H = torch.empty_strided((rows, k), (k, 1), dtype=X.dtype, device=device)
+        else:
+            ldh = _norm_rows(H, "H", rows, k, X)
+    elif H is not None:
         ldh = _norm_rows(H, "H", rows, k, X)
     if Y is not None:
         ldy = _norm_rows(Y, "Y", rows, k, X)
-    Q = _new_f8((rows, k), torch.float8_e4m3fn, device)
-    S = torch.empty(((k + 127) // 128, rows), dtype=torch.float32, device=device)
-    rstd = torch.empty(rows, dtype=torch.float32, device=device)
+    ldq, lds = _ld16(k), max(1, rows)
+    Q = torch.empty_strided((rows, k), (ldq, 1), dtype=torch.float8_e4m3fn, device=device)
+    S = torch.empty_strided((rows, (k + 127) // 128), (1, lds), dtype=torch.float32, device=device)
+    rstd = torch.empty_strided((rows,), (1,), dtype=torch.float32, device=device)
     _run_on("ozaki_rms_norm_f8", (k, rows, code, X.data_ptr(), ldx, _ptr(residual), ldr, W.data_ptr(), float(eps), Q.data_ptr(),
-                                  (k + 15) // 16 * 16 or 16, S.data_ptr(), max(1, rows), _ptr(H), ldh, rstd.data_ptr(), _ptr(Y), ldy),
-            None, None, device)
-    return Q, S.t(), X if H is None else H, rstd
+                                  ldq, S.data_ptr(), lds, _ptr(H), ldh, rstd.data_ptr(), _ptr(Y), ldy), None, None, device)
+    return Q, S, X if H is None else H, rstd
 
 
 def ozaki_rms_norm_backward(dY, H, W, rstd, dH=None, dX=None, workspace=None, stream=None):
@@ -1121,9 +1148,10 @@ def ozaki_rms_norm_backward(dY, H, W, rstd, dH=None, dX=None, workspace=None, st
         raise ValueError(f"rstd must be a contiguous float32 vector of {rows} values on the operands' device")
     lddh = _norm_rows(dH, "dH", rows, k, dY) if dH is not None else max(1, k)
     if dX is None:
-        dX = torch.empty((rows, k), dtype=dY.dtype, device=device)
-    lddx = _norm_rows(dX, "dX", rows, k, dY)
-    dW = torch.empty(k, dtype=dY.dtype, device=device)
+        dX, lddx = torch.empty_strided((rows, k), (k, 1), dtype=dY.dtype, device=device), max(1, k)
+    else:
+        lddx = _norm_rows(dX, "dX", rows, k, dY)
+    dW = torch.empty_strided((k,), (1,), dtype=dY.dtype, device=device)
     _run_on("ozaki_rms_norm_backward", (k, rows, code, dY.data_ptr(), lddy, H.data_ptr(), ldh, W.data_ptr(), rstd.data_ptr(), _ptr(dH), lddh,
                                         dX.data_ptr(), lddx, dW.data_ptr()), workspace, None, device)
     return dX, dW
@@ -1144,8 +1172,8 @@ def ozaki_clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None, wo
     """The 2-norm over all tensors of grads (a float32 scalar on the device), each of which is multiplied by
     min(1, max_norm / (norm + eps)): in place, or into the tensors of out.
 
-    Tensors are contiguous, bfloat16, float16 or float32 (each its own), on one device; out has their shapes and dtypes, and each of
-    its tensors is its gradient itself or does not overlap any.  A norm of Inf makes the factor 0, one of NaN makes it NaN."""
+    Tensors are contiguous, bfloat16, float16 or float32 (each its own), on one device; out has their dtypes and numbers of
+    elements, and each of its tensors is its gradient itself or does not overlap any.  A norm of Inf makes the factor 0, one of NaN makes it NaN."""
     torch = _torch()
     grads = list(grads)
     outs = grads if out is None else list(out)
@@ -1165,15 +1193,16 @@ def ozaki_clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None, wo
     except KeyError as e:
         raise TypeError(f"dtype must be bfloat16, float16 or float32: {e}") from None
     n = len(grads)
-    tensors = grads if outs is grads else grads + outs
-    if any([t.device != device for t in tensors]) or not all([t.is_contiguous() for t in tensors]):
+    tensors, T = grads if outs is grads else grads + outs, torch.Tensor
+    if set(map(T.get_device, tensors)) != {device.index} or not all(map(T.is_contiguous, tensors)):
         raise ValueError("gradients and outputs must be contiguous CUDA tensors on one device")
-    if outs is not grads and any([a.dtype != b.dtype or a.shape != b.shape for a, b in zip(grads, outs)]):
-        raise ValueError("outputs must have their gradients' shapes and dtypes")
-    norm = torch.empty((), dtype=torch.float32, device=device)
-    pointers = (ctypes.c_void_p * n)(*[t.data_ptr() for t in grads])
-    to = pointers if outs is grads else (ctypes.c_void_p * n)(*[t.data_ptr() for t in outs])
-    _run_on("ozaki_clip_grad_norm", (n, (ctypes.c_int * n)(*codes), pointers, to, (ctypes.c_longlong * n)(*[t.numel() for t in grads]),
+    counts = array.array("q", map(T.numel, grads))
+    if outs is not grads and ([t.dtype for t in outs] != [t.dtype for t in grads] or array.array("q", map(T.numel, outs)) != counts):
+        raise ValueError("outputs must have their gradients' dtypes and numbers of elements")
+    norm = torch.empty_strided((), (), dtype=torch.float32, device=device)
+    codes, pointers = array.array("i", codes), array.array("Q", map(T.data_ptr, grads))
+    to = pointers if outs is grads else array.array("Q", map(T.data_ptr, outs))
+    _run_on("ozaki_clip_grad_norm", (n, codes.buffer_info()[0], pointers.buffer_info()[0], to.buffer_info()[0], counts.buffer_info()[0],
                                      float(max_norm), float(eps), norm.data_ptr()), workspace, None, device)
     return norm
 

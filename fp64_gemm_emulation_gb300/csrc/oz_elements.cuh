@@ -92,6 +92,135 @@ __device__ __forceinline__ void store_eight(T* p, const float (&v)[8]) {
   }
 }
 
+// Elements c .. c + 7 of a row of k, zeros from k on (c is a multiple of 8), in two steps, so that other work comes
+// between the loads and their first use.  ALIGNED: rows start at multiples of 16 bytes.  Otherwise the 16-byte pieces
+// that hold the elements are loaded, and shifted into place when they are taken.  A piece may reach into the
+// neighbouring rows or the gap between them, but not out of the matrix, whose elements lie in [first, end): at
+// its two ends elements are loaded one at a time.
+template <class T, bool ALIGNED>
+struct Asked {
+  uint32_t x[Eight<T>::WORDS + (ALIGNED ? 0 : 4)];
+  int o;  // bytes before element c in x
+};
+
+template <class T, bool ALIGNED>
+__device__ __forceinline__ void ask_eight(Asked<T, ALIGNED>& r, const T* row, int c, int k, const T* first, const T* end) {
+  constexpr int PIECE = 16 / sizeof(T), N = Eight<T>::WORDS / 4 + (ALIGNED ? 0 : 1);
+  r.o = ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+  const T* from = row + c - r.o / static_cast<int>(sizeof(T));
+  if (ALIGNED ? c + 8 <= k : c < k && from >= first && from + N * PIECE <= end) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(from)[i];
+      r.x[4 * i] = v.x, r.x[4 * i + 1] = v.y, r.x[4 * i + 2] = v.z, r.x[4 * i + 3] = v.w;
+    }
+  } else {
+    const Eight<T> v = gather_eight(row + c, 1, [&](int e) { return c + e < k; });
+#pragma unroll
+    for (int i = 0; i < Eight<T>::WORDS; ++i) r.x[i] = v.w[i];
+    r.o = 0;
+  }
+}
+
+template <class T, bool ALIGNED>
+__device__ __forceinline__ Eight<T> take_eight(const Asked<T, ALIGNED>& r, int c, int k) {
+  constexpr int W = Eight<T>::WORDS;
+  Eight<T> v;
+  if constexpr (ALIGNED) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v.w[i] = r.x[i];
+  } else {
+    uint32_t x[W + 4];
+#pragma unroll
+    for (int i = 0; i < W + 4; ++i) x[i] = r.x[i];
+    if (r.o & 8) {
+#pragma unroll
+      for (int i = 0; i < W + 2; ++i) x[i] = x[i + 2];
+    }
+    if (r.o & 4) {
+#pragma unroll
+      for (int i = 0; i < W + 1; ++i) x[i] = x[i + 1];
+    }
+    if (sizeof(T) == 2 && (r.o & 2)) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], 16);
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) v.w[i] = x[i];
+  }
+  if (!ALIGNED && c + 8 > k) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        if (c + i >= k) v.w[i] = 0;
+      } else {
+        if (c + 2 * i >= k) v.w[i] = 0;
+        else if (c + 2 * i + 1 >= k) v.w[i] &= 0xFFFFu;
+      }
+    }
+  }
+  return v;
+}
+
+// Both steps at once.
+template <class T, bool ALIGNED>
+__device__ __forceinline__ Eight<T> fetch_eight(const T* row, int c, int k, const T* first, const T* end) {
+  Asked<T, ALIGNED> r;
+  ask_eight(r, row, c, k, first, end);
+  return take_eight(r, c, k);
+}
+
+// v to elements c .. c + 7 of a row of k.  Called by a whole warp, whose lanes' c are 8 apart.  A row that does not start
+// at a multiple of 16 bytes is written in 16-byte pieces all the same: a lane's begins with the last elements of
+// the lane before it.  What no whole piece holds (at the row's and the warp's ends) goes an element at a time.
+template <class T, bool ALIGNED>
+__device__ __forceinline__ void store_eight_of_row(T* row, int c, int k, const float (&v)[8]) {
+  const int o = ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+  if (o == 0) {
+    if (c + 8 <= k) {
+      store_eight(row + c, v);
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < k) from_float(v[e], row[c + e]);
+    return;
+  }
+  constexpr int W = Eight<T>::WORDS, PIECE = 16 / sizeof(T);
+  const int s = o / static_cast<int>(sizeof(T)), lane = threadIdx.x & 31, q = 16 - o;
+  uint32_t x[W + 4];
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    if constexpr (sizeof(T) == 4) x[4 + i] = __float_as_uint(v[i]);
+    else x[4 + i] = pack_two(v[2 * i], v[2 * i + 1], T());
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = __shfl_up_sync(0xFFFFFFFFu, x[W + i], 1);
+  if (q & 8) {
+#pragma unroll
+    for (int i = 0; i < W + 2; ++i) x[i] = x[i + 2];
+  }
+  if (q & 4) {
+#pragma unroll
+    for (int i = 0; i < W + 1; ++i) x[i] = x[i + 1];
+  }
+  if (sizeof(T) == 2 && (q & 2)) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], 16);
+  }
+  // Piece i holds elements c - s + i PIECE and on.
+  auto whole = [&](int i) { return c - s + (i + 1) * PIECE <= k && (lane > 0 || i > 0); };
+#pragma unroll
+  for (int i = 0; i < W / 4; ++i)
+    if (whole(i)) *reinterpret_cast<uint4*>(row + c - s + i * PIECE) = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+  const bool next = lane < 31 && c + 8 - s + PIECE <= k;  // the next lane's first piece
+  if (lane == 0 || !next || !whole(W / 4 - 1)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < k && !(e >= 8 - s ? next : whole((e + s) / PIECE))) from_float(v[e], row[c + e]);
+  }
+}
+
 // Magnitudes as ordered bits: a NaN is above Inf and Inf above all numbers, so a maximum keeps them.
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 

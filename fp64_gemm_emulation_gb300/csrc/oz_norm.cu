@@ -8,9 +8,9 @@
 //
 // Bound by memory: every row is read once, held in registers between its sum and its results, and written
 // once.  With many rows the CTAs stay, keep w in registers, and fetch their next row while they work on one: the
-// waits of a row (for its values, its sum's barrier) would otherwise follow each other.  Several threads share a row, eight elements each: neighbours where rows start at multiples of 16
-// bytes (16-byte accesses; a block of 128 is 16 threads), otherwise 32 apart (a warp's accesses of two
-// bytes are then neighbours; a block is half of a warp's 256 elements).
+// waits of a row (for its values, its sum's barrier) would otherwise follow each other.  Several threads share a row, eight neighbours each (a block of 128 is 16 threads); rows that do not
+// start at multiples of 16 bytes are read and written in 16-byte pieces too, shifted (7777 rows of 2049 bfloat16
+// values backward: 68 us with an access an element).
 #include "oz_elements.cuh"
 #include "oz_device.cuh"
 #include "oz_ragged.cuh"
@@ -36,6 +36,7 @@ struct NormBackParams {
   long long lddy, ldh, lddh, lddx;
   float* part;  // [CTAs][k]
   int parts;
+  int period;   // rows after which one starts alike against 16 bytes
 };
 
 // The sum over a row's threads (blockDim.x of them, whole warps); meet: room for 32 floats of each row.
@@ -53,30 +54,20 @@ __device__ __forceinline__ float row_sum(float v, float* meet) {
   return v;
 }
 
-// Where a thread's eight elements of run j lie: column(j) + e * STEP.
-template <bool VEC>
-__device__ __forceinline__ int first_column(int j) {
-  const int t = threadIdx.x + j * blockDim.x;
-  return VEC ? 8 * t : (t >> 5) * 256 + (t & 31);
-}
+// The first of a thread's eight columns of run j.
+__device__ __forceinline__ int first_column(int j) { return 8 * static_cast<int>(threadIdx.x + j * blockDim.x); }
 
+// A matrix that is read by eights.
 template <class T, bool VEC>
-__device__ __forceinline__ Eight<T> fetch(const T* row, int c, int k) {
-  if (VEC && c + 8 <= k) return load_eight(row + c);
-  return gather_eight(row + c, VEC ? 1 : 32, [&](int e) { return c + e * (VEC ? 1 : 32) < k; });
-}
-template <class T, bool VEC>
-__device__ __forceinline__ void put(T* row, int c, int k, const float (&v)[8]) {
-  if (VEC && c + 8 <= k) {
-    store_eight(row + c, v);
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int at = c + e * (VEC ? 1 : 32);
-    if (at < k) from_float(v[e], row[at]);
-  }
-}
+struct Rows {
+  const T *first, *end;
+  long long ld;
+  int rows, k;
+  __device__ Rows(const void* p, long long ld, int rows, int k)
+      : first(static_cast<const T*>(p)), end(first + (rows - 1) * ld + k), ld(ld), rows(rows), k(k) {}
+  __device__ void ask(Asked<T, VEC>& r, int row, int c) const { ask_eight(r, first + row * ld, c, row < rows ? k : 0, first, end); }
+  __device__ Eight<T> fetch(int row, int c) const { return fetch_eight<T, VEC>(first + row * ld, c, row < rows ? k : 0, first, end); }
+};
 
 // RUNS: runs of eight elements a thread holds.  blockDim (threads of a row, rows).  STAY: a CTA takes every
 // gridDim.x-th group of rows, at most 256 threads; otherwise one.
@@ -87,27 +78,35 @@ __global__ void __launch_bounds__(STAY ? 256 : 1024, STAY ? (RUNS == 1 ? 4 : RUN
   wait_for_previous();
   const int lane = threadIdx.x & 31, step = STAY ? gridDim.x * blockDim.y : a.rows;
   int row = blockIdx.x * blockDim.y + threadIdx.y, turn = 0;
-  Eight<T> nx[RUNS], nr[RUNS], w[RUNS];
+  const Rows<T, VEC> x(a.x, a.ldx, a.rows, a.k), res(a.residual, a.ldr, a.rows, a.k);
+  Asked<T, VEC> nx[RUNS], nr[RUNS];
+  Eight<T> w[RUNS];
   auto ask = [&](int row) {
 #pragma unroll
     for (int j = 0; j < RUNS; ++j) {
-      const int c = first_column<VEC>(j), k = row < a.rows ? a.k : 0;
-      nx[j] = fetch<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx, c, k);
-      if (a.residual) nr[j] = fetch<T, VEC>(static_cast<const T*>(a.residual) + row * a.ldr, c, k);
+      x.ask(nx[j], row, first_column(j));
+      if (a.residual) res.ask(nr[j], row, first_column(j));
     }
   };
   ask(row);
 #pragma unroll
-  for (int j = 0; j < RUNS; ++j) w[j] = fetch<T, VEC>(static_cast<const T*>(a.w), first_column<VEC>(j), a.k);
+  for (int j = 0; j < RUNS; ++j) w[j] = Rows<T, VEC>(a.w, 0, 1, a.k).fetch(0, first_column(j));
   for (; row < a.rows; row += step, turn ^= 1) {
     float h[RUNS][8];
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < RUNS; ++j) {
+      const int c = first_column(j);
+      const Eight<T> vx = take_eight(nx[j], c, a.k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[j][e] = vx.get(e);
+      if (a.residual) {
+        const Eight<T> vr = take_eight(nr[j], c, a.k);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[j][e] += vr.get(e);
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        h[j][e] = nx[j].get(e);
-        if (a.residual) h[j][e] += nr[j].get(e);
         sum = fmaf(h[j][e], h[j][e], sum);
       }
     }
@@ -118,131 +117,140 @@ __global__ void __launch_bounds__(STAY ? 256 : 1024, STAY ? (RUNS == 1 ? 4 : RUN
     uint8_t* q = a.q + row * a.ldq;
 #pragma unroll
     for (int j = 0; j < RUNS; ++j) {
-      const int c = first_column<VEC>(j);
-      if (c < a.k && a.h) put<T, VEC>(static_cast<T*>(a.h) + row * a.ldh, c, a.k, h[j]);
+      const int c = first_column(j);
+      if (a.h) store_eight_of_row<T, VEC>(static_cast<T*>(a.h) + row * a.ldh, c, a.k, h[j]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[j][e] = h[j][e] * r * w[j].get(e);
       float (&y)[8] = h[j];
-      if (c < a.k && a.y) put<T, VEC>(static_cast<T*>(a.y) + row * a.ldy, c, a.k, y);
-      if (VEC) {  // 16 lanes hold a block
-        uint32_t most = 0;
+      if (a.y) store_eight_of_row<T, VEC>(static_cast<T*>(a.y) + row * a.ldy, c, a.k, y);
+      uint32_t most = 0;  // 16 lanes hold a block
 #pragma unroll
-        for (int e = 0; e < 8; ++e) most = max(most, c + e < a.k ? magnitude(y[e]) : 0u);
+      for (int e = 0; e < 8; ++e) most = max(most, c + e < a.k ? magnitude(y[e]) : 0u);
 #pragma unroll
-        for (int d = 1; d < 16; d <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
-        const float scale = scale_of<false>(most);
-        const uint2 v = eight_bits<false>(y, 1.0f / scale);
-        if (c + 8 <= a.k) {
-          *reinterpret_cast<uint2*>(q + c) = v;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (c + e < a.k) q[c + e] = static_cast<uint8_t>(e < 4 ? v.x >> (8 * e) : v.y >> (8 * (e - 4)));
-        }
-        if ((lane & 15) == 0 && c < a.k) a.s[c / kScaleBlock * a.lds + row] = scale;
-      } else {  // the warp holds two blocks, elements 0 - 3 and 4 - 7
-        uint32_t first = 0, second = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          first = max(first, c + 32 * e < a.k ? magnitude(y[e]) : 0u);
-          second = max(second, c + 32 * (e + 4) < a.k ? magnitude(y[e + 4]) : 0u);
-        }
-        const float scale[2] = {scale_of<false>(__reduce_max_sync(0xFFFFFFFFu, first)), scale_of<false>(__reduce_max_sync(0xFFFFFFFFu, second))};
-        const float inverse[2] = {1.0f / scale[0], 1.0f / scale[1]};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] *= inverse[e >> 2];
-        const uint2 v = eight_bits<false>(y, 1.0f);
+      for (int d = 1; d < 16; d <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+      const float scale = scale_of<false>(most);
+      const uint2 v = eight_bits<false>(y, 1.0f / scale);
+      if (c + 8 <= a.k) {
+        *reinterpret_cast<uint2*>(q + c) = v;
+      } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (c + 32 * e < a.k) q[c + 32 * e] = static_cast<uint8_t>(e < 4 ? v.x >> (8 * e) : v.y >> (8 * (e - 4)));
-        if (lane == 0 && c < a.k) a.s[c / kScaleBlock * a.lds + row] = scale[0];
-        if (lane == 0 && c + 128 < a.k) a.s[(c / kScaleBlock + 1) * a.lds + row] = scale[1];
+          if (c + e < a.k) q[c + e] = static_cast<uint8_t>(e < 4 ? v.x >> (8 * e) : v.y >> (8 * (e - 4)));
       }
+      if ((lane & 15) == 0 && c < a.k) a.s[c / kScaleBlock * a.lds + row] = scale;
     }
   }
 }
 
-// Gradients: a CTA takes every gridDim.x-th row and keeps dw's sums of its columns in registers; the CTAs' sums
-// go to the workspace and are added in their order by a second launch, so results do not depend on timing.
+// Gradients: a CTA takes every so many rows and keeps dw's sums of its columns in registers; the CTAs' sums go to
+// the workspace and are added in their order by a second launch, so results do not depend on timing.
 // With one run a thread the next row is fetched meanwhile (two and more leave no registers for it).
-template <class T, bool VEC, int RUNS>
+//
+// Rows that do not start at multiples of 16 bytes: the rows whose starts lie alike against 16 bytes are every
+// `period`-th, and a CTA takes only such.  Its threads' eight columns then start `shift` elements before a multiple of
+// 8, so that all their accesses are of whole 16-byte pieces, and w and dw still belong to fixed threads; only a row's
+// first and last piece hold elements that are not the row's (read where they are the matrix's own, never written).
+// PIECES: all matrices lie alike (and one thread's eight elements are whole pieces); otherwise element by element.
+template <class T, bool PIECES>
+struct Columns {
+  const T *first, *end;  // the matrix
+  long long ld;
+  int rows, k;
+  __device__ Columns(const void* p, long long ld, int rows, int k)
+      : first(static_cast<const T*>(p)), end(first + (rows - 1) * ld + k), ld(ld), rows(rows), k(k) {}
+  __device__ Eight<T> load(int row, int c) const {  // without a mask: columns outside [0, k) may be anything
+    const T* from = first + row * ld + c;
+    if (PIECES && row < rows && c < k && from >= first && from + 8 <= end) return load_eight(from);
+    return gather_eight(from, 1, [&](int e) { return row < rows && c + e >= 0 && c + e < k; });
+  }
+};
+
+template <class T, bool PIECES, int RUNS>
 __global__ void __launch_bounds__(1024) norm_back_kernel(const __grid_constant__ NormBackParams a) {
   constexpr bool EARLY = RUNS == 1;
   __shared__ float meet[2][32];
   let_next_start();
   wait_for_previous();
+  const int kind = static_cast<int>(blockIdx.x) % a.period;  // rows kind, kind + period, ...
+  const int shift = PIECES ? static_cast<int>((reinterpret_cast<uintptr_t>(a.dy) + kind * a.lddy * sizeof(T)) & 15) / static_cast<int>(sizeof(T)) : 0;
+  const int step = a.period * ((static_cast<int>(gridDim.x) - kind + a.period - 1) / a.period);  // (CTAs of this kind)
+  auto column = [&](int j) { return first_column(j) - shift; };
+  auto mask = [&](int c, float (&v)[8]) {
+    if (c < 0 || c + 8 > a.k) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < 0 || c + e >= a.k) v[e] = 0.0f;
+    }
+  };
   float dw[RUNS][8];
 #pragma unroll
   for (int i = 0; i < RUNS * 8; ++i) dw[i >> 3][i & 7] = 0.0f;
-  Eight<T> dy[RUNS], h[RUNS], dh[RUNS], w[RUNS];
+  const Columns<T, PIECES> rdy(a.dy, a.lddy, a.rows, a.k), rh(a.h, a.ldh, a.rows, a.k), rdh(a.dh, a.lddh, a.rows, a.k);
+  Eight<T> dy[RUNS], h[RUNS], dh[RUNS] = {}, w[RUNS];
   float r = 0.0f;
   auto ask = [&](int row) {
-    const int k = row < a.rows ? a.k : 0;
 #pragma unroll
     for (int j = 0; j < RUNS; ++j) {
-      const int c = first_column<VEC>(j);
-      dy[j] = fetch<T, VEC>(static_cast<const T*>(a.dy) + row * a.lddy, c, k);
-      h[j] = fetch<T, VEC>(static_cast<const T*>(a.h) + row * a.ldh, c, k);
-      if (EARLY && a.dh) dh[j] = fetch<T, VEC>(static_cast<const T*>(a.dh) + row * a.lddh, c, k);
+      dy[j] = rdy.load(row, column(j));
+      h[j] = rh.load(row, column(j));
+      if (EARLY && a.dh) dh[j] = rdh.load(row, column(j));
     }
-    if (k) r = a.rstd[row];
+    if (row < a.rows) r = a.rstd[row];
   };
-  if (EARLY) ask(blockIdx.x);
+  int row = kind + a.period * (static_cast<int>(blockIdx.x) / a.period), turn = 0;
+  if (EARLY) ask(row);
 #pragma unroll
-  for (int j = 0; j < RUNS; ++j) w[j] = fetch<T, VEC>(static_cast<const T*>(a.w), first_column<VEC>(j), a.k);
-  int turn = 0;
-  for (int row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+  for (int j = 0; j < RUNS; ++j) w[j] = Columns<T, false>(a.w, 0, 1, a.k).load(0, column(j));
+  for (; row < a.rows; row += step, turn ^= 1) {
     if (!EARLY) ask(row);
     float dot = 0.0f;
     const float rs = r;
-    float g[EARLY ? 8 : 1], x[EARLY ? 8 : 1];  // one run: dy w and h in FP32, so that the next row's may come
+    Eight<T> dy1[EARLY ? 1 : RUNS], h1[EARLY ? 1 : RUNS], dh1[EARLY ? 1 : RUNS];  // this row's
 #pragma unroll
     for (int j = 0; j < RUNS; ++j) {
+      dy1[j] = dy[j], h1[j] = h[j], dh1[j] = dh[j];
+      float d[8], v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] = dy[j].get(e), v[e] = h[j].get(e);
+      mask(column(j), d);
+      mask(column(j), v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float d = dy[j].get(e), v = h[j].get(e), gw = d * w[j].get(e);
-        dot = fmaf(gw, v, dot);
-        dw[j][e] = fmaf(d * rs, v, dw[j][e]);
-        if (EARLY) g[e] = gw, x[e] = v;
+        dot = fmaf(d[e] * w[j].get(e), v[e], dot);
+        dw[j][e] = fmaf(d[e] * rs, v[e], dw[j][e]);
       }
     }
-    float dx[8];
-    if (EARLY) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) dx[e] = a.dh ? dh[0].get(e) : 0.0f;
-      ask(row + gridDim.x);
-    }
+    if (EARLY) ask(row + step);
     // Two rooms in turn: a warp writes one again only after the other's barrier.
     dot = row_sum(dot, meet[turn]) / static_cast<float>(a.k);
     const float f = rs * rs * dot;
 #pragma unroll
     for (int j = 0; j < RUNS; ++j) {
-      const int c = first_column<VEC>(j);
-      if (c >= a.k) continue;
-      if (EARLY) {
+      const int c = column(j);
+      if (!EARLY && a.dh) dh1[j] = rdh.load(row, c);
+      float dx[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dx[e] += rs * (g[e] - x[e] * f);
+      for (int e = 0; e < 8; ++e) {
+        dx[e] = rs * (dy1[j].get(e) * w[j].get(e) - h1[j].get(e) * f);
+        if (a.dh) dx[e] += dh1[j].get(e);
+      }
+      T* to = static_cast<T*>(a.dx) + row * a.lddx + c;
+      if (PIECES && c >= 0 && c + 8 <= a.k) {
+        store_eight(to, dx);
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dx[e] = rs * (dy[j].get(e) * w[j].get(e) - h[j].get(e) * f);
-        if (a.dh) {
-          dh[j] = fetch<T, VEC>(static_cast<const T*>(a.dh) + row * a.lddh, c, a.k);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dx[e] += dh[j].get(e);
-        }
+        for (int e = 0; e < 8; ++e)
+          if (c + e >= 0 && c + e < a.k) from_float(dx[e], to[e]);
       }
-      put<T, VEC>(static_cast<T*>(a.dx) + row * a.lddx, c, a.k, dx);
     }
   }
 #pragma unroll
   for (int j = 0; j < RUNS; ++j) {
-    const int c = first_column<VEC>(j);
+    const int c = column(j);
     float* part = a.part + static_cast<long long>(blockIdx.x) * a.k;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int at = c + e * (VEC ? 1 : 32);
-      if (at < a.k) part[at] = dw[j][e];
-    }
+    for (int e = 0; e < 8; ++e)
+      if (c + e >= 0 && c + e < a.k) part[c + e] = dw[j][e];
   }
 }
 
@@ -323,18 +331,29 @@ cudaError_t norm_of_type(const NormParams& a, int sms, cudaStream_t stream) {
   return vec ? launch_norm<T, true>(a, sms, stream) : launch_norm<T, false>(a, sms, stream);
 }
 
-template <class T, bool VEC>
+template <class T, bool PIECES>
 cudaError_t launch_norm_back(const NormBackParams& a, cudaStream_t stream) {
-  const Shape s = shape_of(a.k, true);  // (one row a CTA)
-  auto kernel = s.runs == 1 ? norm_back_kernel<T, VEC, 1> : s.runs == 2 ? norm_back_kernel<T, VEC, 2> : norm_back_kernel<T, VEC, 4>;
+  // (one row a CTA; a shift takes up to seven columns more)
+  const bool shifted = PIECES && (a.period > 1 || (reinterpret_cast<uintptr_t>(a.dy) & 15));
+  const Shape s = shape_of(shifted ? a.k + 7 : a.k, true);
+  auto kernel = s.runs == 1 ? norm_back_kernel<T, PIECES, 1> : s.runs == 2 ? norm_back_kernel<T, PIECES, 2> : norm_back_kernel<T, PIECES, 4>;
   return launch_overlapping(kernel, dim3(a.parts), s.threads, 0, stream, a);
 }
 
 template <class T>
-cudaError_t norm_back_of_type(const NormBackParams& a, cudaStream_t stream) {
-  const bool vec = rows_aligned<T>(a.dy, a.lddy, a.rows) && rows_aligned<T>(a.h, a.ldh, a.rows) && rows_aligned<T>(a.w, 0, 1) &&
-                   rows_aligned<T>(a.dx, a.lddx, a.rows) && (!a.dh || rows_aligned<T>(a.dh, a.lddh, a.rows));
-  const cudaError_t e = vec ? launch_norm_back<T, true>(a, stream) : launch_norm_back<T, false>(a, stream);
+cudaError_t norm_back_of_type(NormBackParams a, cudaStream_t stream) {
+  // Whether all matrices' rows lie alike against 16 bytes, and after how many rows they do so again.
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.dy) & 15;
+  auto alike = [&](const void* p, long long ld) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == at && (a.rows == 1 || (ld - a.lddy) * static_cast<long long>(sizeof(T)) % 16 == 0);
+  };
+  // (The widest rows leave no room for a shift.)
+  const bool pieces = alike(a.h, a.ldh) && alike(a.dx, a.lddx) && (!a.dh || alike(a.dh, a.lddh)) && a.k + 7 <= OZ_MAX_NORM_WIDTH;
+  a.period = 1;
+  if (pieces && a.rows > 1) {
+    while (a.period < 16 && a.period * a.lddy * static_cast<long long>(sizeof(T)) % 16) a.period *= 2;
+  }
+  const cudaError_t e = pieces ? launch_norm_back<T, true>(a, stream) : launch_norm_back<T, false>(a, stream);
   if (e != cudaSuccess) return e;
   return launch_overlapping(norm_weight_kernel<T>, dim3((a.k + 31) / 32), 256, 0, stream, a.part, a.parts, a.k, static_cast<T*>(a.dw));
 }
@@ -359,7 +378,7 @@ int norm_back(int k, int rows, int dtype, const void* dY, int lddy, const void* 
   for (const void* p : {dY, H, W, static_cast<const void*>(dX)})
     if (!p || !element_aligned(p, dtype)) return OZ_EINVAL;
   if (!rstd || (reinterpret_cast<uintptr_t>(rstd) & 3) || !element_aligned(dH, dtype)) return OZ_EINVAL;
-  const NormBackParams a{k, rows, dY, H, W, dH, rstd, dX, dW, lddy, ldh, lddh, lddx, static_cast<float*>(workspace), parts_of(rows, k)};
+  const NormBackParams a{k, rows, dY, H, W, dH, rstd, dX, dW, lddy, ldh, lddh, lddx, static_cast<float*>(workspace), parts_of(rows, k), 1};
   if (!workspace || ws_bytes < sizeof(float) * static_cast<size_t>(k) * a.parts || (reinterpret_cast<uintptr_t>(workspace) & 255)) return OZ_ENOMEM;
   const cudaError_t e = dtype == OZ_BF16 ? norm_back_of_type<__nv_bfloat16>(a, stream)
                         : dtype == OZ_F16 ? norm_back_of_type<__half>(a, stream)

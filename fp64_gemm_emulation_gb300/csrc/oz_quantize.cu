@@ -32,7 +32,6 @@ struct QuantParams {
   long long lds, ldsc;
   int col_tiles, row_tiles;
   long long tiles;
-  int aligned;
   int* status;
 };
 
@@ -77,14 +76,15 @@ __device__ __forceinline__ Place place_of(const QuantParams& a, const int* off, 
 constexpr int kAhead = 3;  // tiles on their way into shared memory
 constexpr int kTileBytes16 = TILE * TILE * 2;
 
-// BLOCK: an OZ_BLOCK_*.  AHEAD: 16-bit rows at multiples of 16 bytes.
-template <class T, int BLOCK, bool E5M2, bool AHEAD>
+// BLOCK: an OZ_BLOCK_*.  ALIGNED: rows at multiples of 16 bytes.
+template <class T, int BLOCK, bool E5M2, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constant__ QuantParams a) {
   constexpr bool ROW = BLOCK == OZ_BLOCK_ROW || BLOCK == OZ_BLOCK_BOTH, COLUMN = BLOCK == OZ_BLOCK_COLUMN || BLOCK == OZ_BLOCK_BOTH;
-  constexpr bool MATRIX = BLOCK == OZ_BLOCK_MATRIX;
+  constexpr bool MATRIX = BLOCK == OZ_BLOCK_MATRIX, AHEAD = ALIGNED && sizeof(T) == 2;
   extern __shared__ uint4 ahead[];  // [kAhead][8][kThreads]
   __shared__ int off[COLUMN ? OZ_MAX_GROUPS + 1 : 1];
   __shared__ uint32_t most[kThreads / 32][TILE];
+  __shared__ __align__(16) float inverses[COLUMN ? TILE : 4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c8 = 8 * (threadIdx.x & 15), r0 = threadIdx.x >> 4;
   let_next_start();
@@ -124,14 +124,15 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const Eight<T>*>(ahead + (slot * 8 + i) * kThreads + threadIdx.x);
     } else {
-      const T* x = static_cast<const T*>(a.x) + mat * a.stride_x;
+      const T *x = static_cast<const T*>(a.x) + mat * a.stride_x, *end = x + static_cast<long long>(a.rows - 1) * a.ldx + a.k;
+      Asked<T, ALIGNED> asked[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = r0 + 16 * i;
-        const T* from = x + static_cast<long long>(row + r) * a.ldx + c;
-        v[i] = r < count && a.aligned && c + 8 <= a.k ? load_eight(from)
-                                                      : gather_eight(from, 1, [&](int e) { return r < count && c + e < a.k; });
+        ask_eight(asked[i], x + static_cast<long long>(row + r) * a.ldx, c, r < count ? a.k : 0, x, end);
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = take_eight(asked[i], c, r0 + 16 * i < count ? a.k : 0);
     }
     uint32_t by_row[8], by_col[8] = {};
 #pragma unroll
@@ -149,18 +150,29 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
       slot = slot + 1 == kAhead ? 0 : slot + 1;
     }
     if (ROW) {
+      // The maxima of eight rows over 16 lanes: exchanged so that after three steps a lane holds one row's over eight
+      // lanes, which costs 8 shuffles instead of 32, and a lane works out one row's scale instead of eight.
+#pragma unroll
+      for (int half = 4; half > 0; half >>= 1) {
+        const bool upper = lane & half;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+          const uint32_t give = upper ? by_row[i] : by_row[i + half], keep = upper ? by_row[i + half] : by_row[i];
+          by_row[i] = max(keep, __shfl_xor_sync(0xFFFFFFFFu, give, half));
+        }
+      }
+      const float scale = scale_of<E5M2>(max(by_row[0], __shfl_xor_sync(0xFFFFFFFFu, by_row[0], 8))), inverse = 1.0f / scale;
+      const int mine = r0 + 16 * (lane & 7);  // this lane's row
+      if ((lane & 8) == 0 && mine < count) a.s[c / TILE * a.lds + row + mine] = scale;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int d = 1; d < 16; d <<= 1) by_row[i] = max(by_row[i], __shfl_xor_sync(0xFFFFFFFFu, by_row[i], d));
+        const float by = __shfl_sync(0xFFFFFFFFu, inverse, (lane & 16) | i);
         const int r = r0 + 16 * i;
         if (r < count) {
-          const float scale = scale_of<E5M2>(by_row[i]);
           float f[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) f[e] = v[i].get(e);
-          put_bytes(a.q + static_cast<long long>(row + r) * a.ldq, c, a.k, eight_bits<E5M2>(f, 1.0f / scale));
-          if (c8 == 0) a.s[c / TILE * a.lds + row + r] = scale;
+          put_bytes(a.q + static_cast<long long>(row + r) * a.ldq, c, a.k, eight_bits<E5M2>(f, by));
         }
       }
     }
@@ -172,15 +184,21 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
         for (int e = 0; e < 8; ++e) most[warp][c8 + e] = by_col[e];
       }
       __syncthreads();
-      float inverse[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      if (threadIdx.x < TILE) {  // a column's scale is one thread's
         uint32_t m = 0;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) m = max(m, most[w][c8 + e]);
+        for (int w = 0; w < kThreads / 32; ++w) m = max(m, most[w][threadIdx.x]);
         const float scale = scale_of<E5M2>(m);
-        inverse[e] = 1.0f / scale;
-        if (r0 == 0 && c + e < a.k) a.sc[block * a.ldsc + c + e] = scale;
+        inverses[threadIdx.x] = 1.0f / scale;
+        const int column = c - c8 + static_cast<int>(threadIdx.x);
+        if (column < a.k) a.sc[block * a.ldsc + column] = scale;
+      }
+      __syncthreads();
+      float inverse[8];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 x = reinterpret_cast<const float4*>(inverses + c8)[i];
+        inverse[4 * i] = x.x, inverse[4 * i + 1] = x.y, inverse[4 * i + 2] = x.z, inverse[4 * i + 3] = x.w;
       }
       // The rows as they are, or the block's own 128 with zeros behind the group's last.
       const long long to = ragged ? static_cast<long long>(block) * TILE : row;
@@ -195,7 +213,6 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
           put_bytes(a.qc + (to + r) * a.ldqc, c, a.k, r < count ? eight_bits<E5M2>(f, 1.0f) : make_uint2(0, 0));
         }
       }
-      __syncthreads();  // most is free again
     }
     if (MATRIX) {
       uint32_t m = 0;
@@ -250,9 +267,10 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
   }
 }
 
-template <class T, int BLOCK, bool E5M2, bool AHEAD>
+template <class T, int BLOCK, bool E5M2, bool ALIGNED>
 cudaError_t start(const QuantParams& a, cudaStream_t stream) {
-  auto kernel = quantize_kernel<T, BLOCK, E5M2, AHEAD>;
+  auto kernel = quantize_kernel<T, BLOCK, E5M2, ALIGNED>;
+  constexpr bool AHEAD = ALIGNED && sizeof(T) == 2;
   constexpr int smem = AHEAD ? kAhead * kTileBytes16 : 0;
   long long grid = 1 << 20;
   if (AHEAD) {
@@ -277,11 +295,9 @@ cudaError_t start(const QuantParams& a, cudaStream_t stream) {
 }
 
 template <class T, int BLOCK>
-cudaError_t launch_quantize(QuantParams a, bool e5m2, cudaStream_t stream) {
-  a.aligned = rows_aligned<T>(a.x, a.ldx, a.rows) && (a.mats == 1 || a.stride_x * sizeof(T) % 16 == 0);
-  if constexpr (sizeof(T) == 2) {
-    if (a.aligned) return e5m2 ? start<T, BLOCK, true, true>(a, stream) : start<T, BLOCK, false, true>(a, stream);
-  }
+cudaError_t launch_quantize(const QuantParams& a, bool e5m2, cudaStream_t stream) {
+  const bool aligned = rows_aligned<T>(a.x, a.ldx, a.rows) && (a.mats == 1 || a.stride_x * sizeof(T) % 16 == 0);
+  if (aligned) return e5m2 ? start<T, BLOCK, true, true>(a, stream) : start<T, BLOCK, false, true>(a, stream);
   return e5m2 ? start<T, BLOCK, true, false>(a, stream) : start<T, BLOCK, false, false>(a, stream);
 }
 

@@ -15,9 +15,9 @@
 namespace oz {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kResident = 5;  // CTAs of an SM: no more are launched, so that all get equally many chunks
 // Elements of a chunk: enough for a CTA's 16-byte loads to follow each other, few enough for all CTAs to get some.
-constexpr int kChunk = 16384, kLongChunk = 65536;
+constexpr int kChunk = 16384, kLongChunk = 32768;
 constexpr long long kLongTotal = 1ll << 27;    // elements of a launch from which on chunks are long
 constexpr int kMaxSums = 4096;                 // CTAs whose sums the workspace holds
 
@@ -67,10 +67,10 @@ __device__ __forceinline__ double squares(const Eight<T> (&v)[N]) {
   // (a NaN is not in most, but in sum)
   if (most == 0.0f || (most >= 8.8817842e-16f && most <= 3.6028797e16f)) return static_cast<double>(sum);
   double d = 0.0;
-#pragma unroll 1
+#pragma unroll
   for (int i = 0; i < N; ++i) {
-#pragma unroll 1
-    for (int e = 0; e < 8; ++e) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {  // (unrolled: an index known only at run time would put v into memory)
       const double x = v[i].get(e);
       d = fma(x, x, d);
     }
@@ -115,7 +115,7 @@ __device__ __forceinline__ double block_sum(double d, double* meet) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ ClipParams<N> a) {
+__global__ void __launch_bounds__(kThreads, kResident) sum_kernel(const __grid_constant__ ClipParams<N> a) {
   __shared__ double meet[kThreads / 32];
   let_next_start();
   wait_for_previous();
@@ -157,7 +157,7 @@ __device__ __forceinline__ void scale_chunk(const Tensor& t, long long from, int
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ ClipParams<N> a) {
+__global__ void __launch_bounds__(kThreads, kResident) scale_kernel(const __grid_constant__ ClipParams<N> a) {
   __shared__ double meet[kThreads / 32];
   let_next_start();
   wait_for_previous();
@@ -197,7 +197,7 @@ int clip_launches(const Work& w, float limit, float eps, float* norm, uint8_t* w
   a.limit = limit;
   a.eps = eps;
   const int launches = w.count ? (w.count + N - 1) / N : 1;
-  const int most = kMaxSums / launches < 8 * sms ? kMaxSums / launches : 8 * sms;
+  const int most = kMaxSums / launches < kResident * sms ? kMaxSums / launches : kResident * sms;
   int sums = 0;
   auto fill = [&](int l) {
     a.tensors = 0;

@@ -242,8 +242,8 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
   uint64_t* bars = reinterpret_cast<uint64_t*>(stash + EPI8_WARPS * STASH8);
   uint64_t* full = bars;                     // [STAGES8] TMA (both CTAs) -> MMA  (used in the leader)
   uint64_t* empty = full + STAGES8;          // [STAGES8] MMA issuers -> TMA      (both CTAs)
-  uint64_t* accfull = empty + STAGES8;       // [2][2]    MMA -> epilogue, by buffer and half (both CTAs)
-  uint64_t* accempty = accfull + 4;          // [2][2]    the half's warps (both) -> MMA (used in the leader)
+  uint64_t* accfull = empty + STAGES8;       // [4]       MMA -> epilogue, by buffer and half (both CTAs)
+  uint64_t* accempty = accfull + 4;          // [4]       the half's warps (both) -> MMA (used in the leader)
   uint64_t* sfull = accempty + 4;            // [SLOTS8]  scales -> epilogue      (per CTA)
   uint64_t* sempty = sfull + SLOTS8;         // [SLOTS8]  epilogue -> scales      (per CTA)
   uint64_t* drain = sempty + SLOTS8;         // [1]       all MMAs of the pair done, by each issuer (both CTAs)
@@ -256,7 +256,8 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const int halves = a.bn / ACC8;
+  // Accumulator buf * halves + half: two buffers of two halves, or four of one.
+  const uint32_t halves = a.bn / ACC8, buffers = 4 / halves;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES8; ++i) {
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
               else
                 tma_load_4d_pair(dB, &a.tmB, bar, k, 64 * static_cast<int>(rank), u.n0 / ACC8, z);
             } else {
-              for (int h = 0; h < halves; ++h) {
+              for (int h = 0; h < static_cast<int>(halves); ++h) {
                 const int n = u.n0 + ACC8 * h + 64 * static_cast<int>(rank);
                 if (Walk::B_MN)
                   tma_load_3d_pair(dB + h * HALF8, &a.tmB, bar, n, k, z);
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
         }
       }
     } else if (warp & 1) {
-      const int half = warp >> 1;
+      const uint32_t half = warp >> 1;
       if (rank == 0 && half < halves && elect_one()) {
         // ------------------------------------------------------------ MMA issuers (leader only), one for each half
         int stage = 0;
@@ -373,7 +374,6 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
         constexpr uint32_t a_step = (Walk::A_MN ? STEP8 * 128 : STEP8) >> 4, b_step = (Walk::B_MN ? STEP8 * 64 : STEP8) >> 4;
         constexpr uint32_t B_HIGH = Walk::B_MN ? DESC_HIGH_64 : DESC_HIGH;
         const uint32_t idesc = a.idesc;
-        const uint32_t d_half = tmem_base + half * ACC8;
         Walk walk(a, table);
         Unit8 u{};
         while (ok && !*abort_flag && walk.next(u)) {
@@ -383,18 +383,21 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
               break;
             }
             ++consumed;
-            if (!mbar_wait_or_abort(&accempty[2 * buf + half], acc_phase, kWaitLimitNs, abort_flag)) {
+            const uint32_t acc = buf * halves + half;
+            if (!mbar_wait_or_abort(&accempty[acc], acc_phase, kWaitLimitNs, abort_flag)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t ad = a_desc + stage * (TILE8 >> 4), bd = b_desc + stage * (TILE8 >> 4), d = d_half + buf * (2 * ACC8);
+            const uint32_t ad = a_desc + stage * (TILE8 >> 4), bd = b_desc + stage * (TILE8 >> 4), d = tmem_base + acc * ACC8;
 #pragma unroll
             for (int kk = 0; kk < BK8 / STEP8; ++kk) umma8_pair<B_HIGH>(d, ad + kk * a_step, bd + kk * b_step, idesc, kk > 0 ? 1u : 0u);
-            umma_commit_pair(&accfull[2 * buf + half], 0x3);
+            umma_commit_pair(&accfull[acc], 0x3);
             umma_commit_pair(&empty[stage], 0x3);
-            acc_phase ^= buf;
-            buf ^= 1;
+            if (++buf == buffers) {
+              buf = 0;
+              acc_phase ^= 1;
+            }
             if (++stage == STAGES8) {
               stage = 0;
               phase ^= 1;
@@ -472,12 +475,13 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
     // -------------------------------------------------------------- epilogue (both CTAs)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_MANY));
     // A warp scales and sums 32 lanes of one half's 128 columns.
-    const int quad = warp & 3, half = (warp - EPI8_FIRST) >> 2;
+    const uint32_t half = (warp - EPI8_FIRST) >> 2;
+    const int quad = warp & 3;
     uint8_t* my_stash = stash + (warp - EPI8_FIRST) * STASH8;
-    const uint32_t accempty_leader = mapa_shared(smem_u32(accempty), 0) + half * 8;
-    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + half * ACC8;
+    const uint32_t accempty_leader = mapa_shared(smem_u32(accempty), 0);
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
     const int mrow = static_cast<int>(rank) * HALF_M + quad * 32;
-    uint32_t buf = 0, acc_phase = 0;
+    uint32_t acc = half, acc_phase = 0;  // its accumulators: half, half + halves, ...
     bool ok = true;
     Walk(a, table).outside(warp - EPI8_FIRST);
     auto wait = [&](uint64_t* bar, uint32_t phase, uint64_t limit) {
@@ -487,7 +491,7 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
       return ok;
     };
     auto sums_there = [&]() {
-      const bool there = wait(&accfull[2 * buf + half], acc_phase, a.epi_wait_ns);
+      const bool there = wait(&accfull[acc], acc_phase, a.epi_wait_ns);
       tc_fence_after();
       return there;
     };
@@ -495,15 +499,17 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
     auto release = [&]() {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(accempty_leader + buf * 16);
-      acc_phase ^= buf;
-      buf ^= 1;
+      if (lane == 0) mbar_arrive_cluster(accempty_leader + acc * 8);
+      if ((acc += halves) >= 4) {
+        acc = half;
+        acc_phase ^= 1;
+      }
     };
     if constexpr (OP != kWgrad8) {
       // The sums take nearly all registers: the walker is made anew for each tile, and where the tile goes waits in the
       // warp's stash.
       int4* const kept = reinterpret_cast<int4*>(my_stash);  // first row, rows, first column, columns
-      for (int at = static_cast<int>(blockIdx.x >> 1) - static_cast<int>(gridDim.x >> 1); ok && half * ACC8 < a.bn;
+      for (int at = static_cast<int>(blockIdx.x >> 1) - static_cast<int>(gridDim.x >> 1); ok && half < halves;
            at += static_cast<int>(gridDim.x >> 1)) {
         int left, blocks;  // k-blocks to come, blocks of 32 columns
         const float *sx, *sw;
@@ -511,7 +517,7 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
           Walk walk(a, table, at);
           Unit8 u;
           if (!walk.next(u)) break;
-          const int rows = u.mcount - mrow, col = u.n0 + half * ACC8, cols = u.ncount - half * ACC8;
+          const int rows = u.mcount - mrow, col = u.n0 + static_cast<int>(half) * ACC8, cols = u.ncount - static_cast<int>(half) * ACC8;
           blocks = rows > 0 ? min(BLOCKS8, ceil_div(max(0, cols), 32)) : 0;
           left = u.kbs;
           // This lane's row's scales and those of the half's features.  Lanes without a row take the last one's.
@@ -555,13 +561,13 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
                 release();
                 if (--left > 0) sums_there();
               }
-              tmem_ld16(lanes + buf * (2 * ACC8) + 16 * ((j + 1) % (2 * BLOCKS8)), v[(j + 1) & 1]);
+              tmem_ld16(lanes + acc * ACC8 + 16 * ((j + 1) % (2 * BLOCKS8)), v[(j + 1) & 1]);
 #pragma unroll
               for (int i = 0; i < 16; ++i) fma_loaded(__uint_as_float(v[j & 1][i]), f, run[j >> 1][16 * (j & 1) + i]);
             }
           };
           if (left > 0 && sums_there()) {
-            tmem_ld16(lanes + buf * (2 * ACC8), v[0]);
+            tmem_ld16(lanes + acc * ACC8, v[0]);
             // Two k-blocks a turn, so that no scale under way is moved from one register to another.
             while (ok && left > 0) {
               step(x[0], w[0]);
@@ -573,7 +579,7 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
         } else {
           auto step = [&](float& x, float& w) {
             const float f = blocks ? factor(x, w) : 0.0f;
-            const uint32_t from = lanes + buf * (2 * ACC8);
+            const uint32_t from = lanes + acc * ACC8;
             --left;
             if (blocks == 0) release();
 #pragma unroll
@@ -620,7 +626,7 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
           Walk walk(a, table, at);
           Unit8 u;
           if (!walk.next(u)) break;
-          blocks = u.mcount > mrow ? min(BLOCKS8, ceil_div(max(0, u.ncount - half * ACC8), 32)) : 0;
+          blocks = u.mcount > mrow ? min(BLOCKS8, ceil_div(max(0, u.ncount - static_cast<int>(half) * ACC8), 32)) : 0;
           left = u.kbs;
           __syncwarp();
           if (lane == 0) *kept = u;
@@ -638,7 +644,7 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
           };
           if (left > 0 && scales_there() && sums_there()) {
             scales_of_m();
-            tmem_ld_frag16(lanes + buf * (2 * ACC8), v[0]);
+            tmem_ld_frag16(lanes + acc * ACC8, v[0]);
           }
           while (ok && left > 0) {
 #pragma unroll
@@ -653,7 +659,7 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
                 scales_done();
                 if (--left > 0 && scales_there()) sums_there();
               }
-              tmem_ld_frag16(lanes + buf * (2 * ACC8) + 16 * ((j + 1) % (2 * BLOCKS8)), v[(j + 1) & 1]);
+              tmem_ld_frag16(lanes + acc * ACC8 + 16 * ((j + 1) % (2 * BLOCKS8)), v[(j + 1) & 1]);
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
 #pragma unroll
@@ -679,8 +685,8 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
         Unit t{};  // as the 16-bit products' epilogue takes it
         t.m0 = u.m0;
         t.m_extent = a.M;
-        t.nn = u.ncount - half * ACC8;
-        t.orow = u.n0 + half * ACC8;
+        t.nn = u.ncount - static_cast<int>(half) * ACC8;
+        t.orow = u.n0 + static_cast<int>(half) * ACC8;
         t.out = static_cast<uint16_t*>(a.out) + u.group * a.stride;
         t.ld = a.ld;
         t.out_type = a.out_type;
@@ -802,6 +808,14 @@ int launch8(const Problem8& p, const Device& d, cudaStream_t stream) {
   a.groups = p.groups;
   a.rows = p.rows;
   a.bn = BN;
+  // Tiles of 128 n where that takes fewer turns of all pairs: they take 0.72 of the time of tiles of 256 (8192 x 4096 x
+  // 8192: 325 us, and 227; 64 rows x 4096 x 8192, one turn of either: 16.3 us, and 18.9).  (The rows of each
+  // group are not known here: at most so many tiles.)
+  if (OP != kWgrad8) {
+    const int tiles_m = p.groups == 1 ? ceil_div(p.rows, BM) : (p.groups < p.rows ? p.groups : p.rows) + p.rows / BM;
+    const long long wide = static_cast<long long>(tiles_m) * ceil_div(a.N, BN), narrow = static_cast<long long>(tiles_m) * ceil_div(a.N, ACC8);
+    if ((narrow + d.pairs - 1) / d.pairs * 18 < (wide + d.pairs - 1) / d.pairs * 25) a.bn = ACC8;
+  }
   a.vec = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.ldo % 8 == 0 && (OP != kWgrad8 || p.groups == 1 || p.strideo % 8 == 0);
   a.out_type = p.out_type == OZ_BF16 ? kOutBf16 : kOutF16;
   a.idesc = idesc8_base(p.a.type == OZ_E5M2, p.b.type == OZ_E5M2, Walk::A_MN, Walk::B_MN) | (static_cast<uint32_t>(ACC8 >> 3) << 17);

@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   // Accumulator buf * halves + half: two buffers of two halves, or four of one.
-  const uint32_t halves = a.bn / ACC8, buffers = 4 / halves;
+  const uint32_t halves = OP == kWgrad8 ? 2 : a.bn / ACC8, buffers = 4 / halves;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES8; ++i) {

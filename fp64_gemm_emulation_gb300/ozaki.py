@@ -857,15 +857,15 @@ def _column_scales(S, what: str, blocks: int, k: int, device) -> int:
 
 
 def _f8_rows(Q, what: str, features: int | None = None):
-    """(rows, features, leading dimension) of an 8-bit operand, whose rows start at multiples of 16 bytes."""
-    shape, stride = Q.shape, Q.stride()
+    """(rows, features, leading dimension, type) of an 8-bit operand, whose rows start at multiples of 16 bytes."""
+    shape, stride, code = Q.shape, Q.stride(), _f8(Q.dtype)
     if len(shape) == 2 and 1 < shape[0] <= _INT_MAX and 0 < shape[1] <= stride[0] <= _INT_MAX and stride[1] == 1 and \
             features in (None, shape[1]) and not (stride[0] | Q.data_ptr()) & 15:
-        return shape[0], shape[1], stride[0]
+        return shape[0], shape[1], stride[0], code
     ld = _tokens(Q, what, features)  # (says what is wrong)
     if Q.numel() and (Q.data_ptr() & 15 or (shape[0] > 1 and ld & 15)):
         raise ValueError(f"{what} must have rows that start at multiples of 16 bytes")
-    return shape[0], shape[1], ld
+    return shape[0], shape[1], ld, code
 
 
 def _f8_experts(W, SW, device):
@@ -1011,11 +1011,11 @@ def ozaki_grouped_gemm_f8(X, SX, W, SW, offsets=None, Y=None, dtype=None, stream
         return _call_on(other, ozaki_grouped_gemm_f8, X, SX, W, SW, offsets, Y, dtype)
     device = _cuda(X, "X")
     groups, n, k, ldw, sw = _f8_experts(W, SW, device)
-    rows, _, ldx = _f8_rows(X, "X", k)
+    rows, _, ldx, tx = _f8_rows(X, "X", k)
     lds = _row_scales(SX, "the scales of X", rows, k, device)
     off = _product_offsets(offsets, groups, device)
     Y, code, ldy = _output(Y, "Y", rows, n, dtype, device)
-    _run_on("ozaki_grouped_gemm_f8", (n, k, rows, groups, _f8(W.dtype), W.data_ptr(), ldw, sw, SW.data_ptr(), _f8(X.dtype), X.data_ptr(),
+    _run_on("ozaki_grouped_gemm_f8", (n, k, rows, groups, _f8(W.dtype), W.data_ptr(), ldw, sw, SW.data_ptr(), tx, X.data_ptr(),
                                       ldx, SX.data_ptr(), lds, off, code, Y.data_ptr(), ldy), None, None, device)
     return Y
 
@@ -1026,11 +1026,11 @@ def ozaki_grouped_gemm_f8_dgrad(dY, SdY, W, SW, offsets=None, dX=None, dtype=Non
         return _call_on(other, ozaki_grouped_gemm_f8_dgrad, dY, SdY, W, SW, offsets, dX, dtype)
     device = _cuda(dY, "dY")
     groups, n, k, ldw, sw = _f8_experts(W, SW, device)
-    rows, _, lddy = _f8_rows(dY, "dY", n)
+    rows, _, lddy, tdy = _f8_rows(dY, "dY", n)
     lds = _row_scales(SdY, "the scales of dY", rows, n, device)
     off = _product_offsets(offsets, groups, device)
     dX, code, lddx = _output(dX, "dX", rows, k, dtype, device)
-    _run_on("ozaki_grouped_gemm_f8_dgrad", (n, k, rows, groups, _f8(W.dtype), W.data_ptr(), ldw, sw, SW.data_ptr(), _f8(dY.dtype), dY.data_ptr(),
+    _run_on("ozaki_grouped_gemm_f8_dgrad", (n, k, rows, groups, _f8(W.dtype), W.data_ptr(), ldw, sw, SW.data_ptr(), tdy, dY.data_ptr(),
                                             lddy, SdY.data_ptr(), lds, off, code, dX.data_ptr(), lddx), None, None, device)
     return dX
 
@@ -1044,8 +1044,8 @@ def ozaki_grouped_gemm_f8_wgrad(dY, SdY, X, SX, offsets=None, dW=None, dtype=Non
     if stream is not None and (other := _other_stream(stream, dY.device)):
         return _call_on(other, ozaki_grouped_gemm_f8_wgrad, dY, SdY, X, SX, offsets, dW, dtype, rows)
     device = _cuda(dY, "dY")
-    laid, n, lddy = _f8_rows(dY, "dY")
-    laid_x, k, ldx = _f8_rows(X, "X")
+    laid, n, lddy, tdy = _f8_rows(dY, "dY")
+    laid_x, k, ldx, tx = _f8_rows(X, "X")
     if laid_x != laid or X.device != device:
         raise ValueError("X and dY must have the same rows, on one device")
     off = _product_offsets(offsets, None, device)
@@ -1070,7 +1070,7 @@ def ozaki_grouped_gemm_f8_wgrad(dY, SdY, X, SX, offsets=None, dW=None, dtype=Non
         if dW.shape != (groups, n, k):
             raise ValueError(f"dW must have shape {(groups, n, k)}: {tuple(dW.shape)}")
     code = _16bit(dW, "dW")
-    _run_on("ozaki_grouped_gemm_f8_wgrad", (n, k, rows, groups, _f8(dY.dtype), dY.data_ptr(), lddy, SdY.data_ptr(), ldsy, _f8(X.dtype),
+    _run_on("ozaki_grouped_gemm_f8_wgrad", (n, k, rows, groups, tdy, dY.data_ptr(), lddy, SdY.data_ptr(), ldsy, tx,
                                             X.data_ptr(), ldx, SX.data_ptr(), ldsx, off, code, dW.data_ptr(), ldw, sw), None, None, device)
     return dW
 

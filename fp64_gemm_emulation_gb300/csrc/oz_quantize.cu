@@ -11,6 +11,7 @@
 // 16-bit elements (FP32 tiles are twice as large) are copied into shared memory three tiles ahead, where each
 // thread finds its own eight 16-byte pieces again, so that no barrier is needed.
 #include <atomic>
+#include <type_traits>
 
 #include "oz_elements.cuh"
 #include "oz_device.cuh"
@@ -30,8 +31,7 @@ struct QuantParams {
   long long ldq, stride_q, ldqc;
   float *s, *sc;
   long long lds, ldsc;
-  int col_tiles, row_tiles;
-  long long tiles;
+  int col_tiles, row_tiles, tiles;
   int* status;
 };
 
@@ -46,18 +46,36 @@ __device__ __forceinline__ void put_bytes(uint8_t* row, int c, int k, uint2 w) {
   }
 }
 
+// The larger of two magnitudes, of two pairs of 16-bit ones; NaN is the largest.
+template <class T>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  if constexpr (sizeof(T) == 4) {
+    return max(a, b);
+  } else {
+    uint32_t r;
+    if constexpr (std::is_same<T, __half>::value) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+}
+// The bits of a magnitude in FP32.
+template <class T>
+__device__ __forceinline__ uint32_t raw_magnitude(uint32_t raw) {
+  return magnitude(value_of(raw, T()));
+}
+
 // Where a tile lies: its matrix, block of rows, first row, how many rows it has, and this thread's first column.
 struct Place {
   int mat, block, row, count, c;
 };
 
 template <bool MATRIX, bool RAGGED_POSSIBLE>
-__device__ __forceinline__ Place place_of(const QuantParams& a, const int* off, long long tile) {
+__device__ __forceinline__ Place place_of(const QuantParams& a, const int* off, int tile) {
   Place p;
-  const long long rt = tile / a.col_tiles;
-  p.c = static_cast<int>(tile - rt * a.col_tiles) * TILE + 8 * (threadIdx.x & 15);
-  p.mat = MATRIX ? static_cast<int>(rt / a.row_tiles) : 0;
-  p.block = static_cast<int>(rt - static_cast<long long>(p.mat) * a.row_tiles);
+  const int rt = tile / a.col_tiles;
+  p.c = (tile - rt * a.col_tiles) * TILE + 8 * (threadIdx.x & 15);
+  p.mat = MATRIX ? rt / a.row_tiles : 0;
+  p.block = rt - p.mat * a.row_tiles;
   p.row = p.block * TILE;
   p.count = min(TILE, a.rows - p.row);
   if (RAGGED_POSSIBLE && a.offsets) {
@@ -95,27 +113,28 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
     __syncthreads();
   }
   // A tile's pieces of this thread into its places of slot s; those that do not exist as zeros.
-  auto send = [&](long long tile, int slot) {
+  auto send = [&](int tile, int slot) {
     if (tile < a.tiles) {
       const Place p = place_of<MATRIX, COLUMN>(a, off, tile);
-      const T* x = static_cast<const T*>(a.x) + p.mat * a.stride_x + p.c;
+      const T* from = static_cast<const T*>(a.x) + p.mat * a.stride_x + static_cast<long long>(p.row + r0) * a.ldx + p.c;
       const int bytes = max(0, min(8, a.k - p.c)) * 2;
+      uint32_t to = smem_u32(ahead + slot * 8 * kThreads + threadIdx.x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int r = r0 + 16 * i;
-        const bool have = r < p.count && bytes;
-        const uint32_t to = smem_u32(ahead + (slot * 8 + i) * kThreads + threadIdx.x);
-        const T* from = have ? x + static_cast<long long>(p.row + r) * a.ldx : static_cast<const T*>(a.x);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(have ? bytes : 0) : "memory");
+        const bool have = r0 + 16 * i < p.count && bytes;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(have ? from : static_cast<const T*>(a.x)), "r"(have ? bytes : 0)
+                     : "memory");
+        from += 16 * a.ldx;
+        to += kThreads * 16;
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   int slot = 0;
   if (AHEAD) {
-    for (int s = 0; s < kAhead; ++s) send(blockIdx.x + static_cast<long long>(s) * gridDim.x, s);
+    for (int s = 0; s < kAhead; ++s) send(blockIdx.x + s * gridDim.x, s);
   }
-  for (long long tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+  for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
     const Place place = place_of<MATRIX, COLUMN>(a, off, tile);
     const int c = place.c, mat = place.mat, block = place.block, row = place.row, count = place.count;
     Eight<T> v[8];
@@ -134,21 +153,39 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = take_eight(asked[i], c, r0 + 16 * i < count ? a.k : 0);
     }
-    uint32_t by_row[8], by_col[8] = {};
+    // Largest magnitudes: of FP32 values as bits, of 16-bit ones two at a time (in by_col both columns' in a word).
+    constexpr int PAIRS = sizeof(T) == 2 ? 2 : 1;
+    uint32_t by_row[8], by_col[8 / PAIRS] = {};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       by_row[i] = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t m = magnitude(v[i].get(e));
-        by_row[i] = max(by_row[i], m);
-        if (COLUMN) by_col[e] = max(by_col[e], m);
+      for (int e = 0; e < 8 / PAIRS; ++e) {
+        by_row[i] = larger<T>(by_row[i], v[i].w[e] & (PAIRS == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu));
+        if (COLUMN) by_col[e] = larger<T>(by_col[e], v[i].w[e] & (PAIRS == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu));
       }
+      if (PAIRS == 2) by_row[i] = max(by_row[i] & 0xFFFFu, by_row[i] >> 16);
     }
     if constexpr (AHEAD) {  // the slot has been read (every value of it is in a maximum)
-      send(tile + static_cast<long long>(kAhead) * gridDim.x, slot);
+      send(tile + kAhead * gridDim.x, slot);
       slot = slot + 1 == kAhead ? 0 : slot + 1;
     }
+    // What make hands to its second argument for each i, to this thread's columns of row `first` + r0 + 16 i, of which
+    // `rows` exist.  Called by whole warps.
+    const bool whole_columns = c - c8 + TILE <= a.k;
+    auto put_rows = [&](uint8_t* q, long long ld, long long first, int rows, auto make) {
+      uint8_t* to = q + (first + r0) * ld;
+      if (whole_columns && rows == TILE) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i, to += 16 * ld) make(i, [&](uint2 w) { *reinterpret_cast<uint2*>(to + c) = w; });
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i, to += 16 * ld)
+          make(i, [&](uint2 w) {
+            if (r0 + 16 * i < rows) put_bytes(to, c, a.k, w);
+          });
+      }
+    };
     if (ROW) {
       // The maxima of eight rows over 16 lanes: exchanged so that after three steps a lane holds one row's over eight
       // lanes, which costs 8 shuffles instead of 32, and a lane works out one row's scale instead of eight.
@@ -161,34 +198,30 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
           by_row[i] = max(keep, __shfl_xor_sync(0xFFFFFFFFu, give, half));
         }
       }
-      const float scale = scale_of<E5M2>(max(by_row[0], __shfl_xor_sync(0xFFFFFFFFu, by_row[0], 8))), inverse = 1.0f / scale;
+      const float scale = scale_of<E5M2>(raw_magnitude<T>(max(by_row[0], __shfl_xor_sync(0xFFFFFFFFu, by_row[0], 8)))), inverse = 1.0f / scale;
       const int mine = r0 + 16 * (lane & 7);  // this lane's row
       if ((lane & 8) == 0 && mine < count) a.s[c / TILE * a.lds + row + mine] = scale;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      put_rows(a.q, a.ldq, row, count, [&](int i, auto store) {
         const float by = __shfl_sync(0xFFFFFFFFu, inverse, (lane & 16) | i);
-        const int r = r0 + 16 * i;
-        if (r < count) {
-          float f[8];
+        float f[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = v[i].get(e);
-          put_bytes(a.q + static_cast<long long>(row + r) * a.ldq, c, a.k, eight_bits<E5M2>(f, by));
-        }
-      }
+        for (int e = 0; e < 8; ++e) f[e] = v[i].get(e);
+        store(eight_bits<E5M2>(f, by));
+      });
     }
     if (COLUMN) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) by_col[e] = max(by_col[e], __shfl_xor_sync(0xFFFFFFFFu, by_col[e], 16));
+      for (int e = 0; e < 8 / PAIRS; ++e) by_col[e] = larger<T>(by_col[e], __shfl_xor_sync(0xFFFFFFFFu, by_col[e], 16));
       if (lane < 16) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) most[warp][c8 + e] = by_col[e];
+        for (int e = 0; e < 8 / PAIRS; ++e) most[warp][c8 / PAIRS + e] = by_col[e];
       }
       __syncthreads();
       if (threadIdx.x < TILE) {  // a column's scale is one thread's
         uint32_t m = 0;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) m = max(m, most[w][threadIdx.x]);
-        const float scale = scale_of<E5M2>(m);
+        for (int w = 0; w < kThreads / 32; ++w) m = max(m, static_cast<uint32_t>(reinterpret_cast<const typename Bits<T>::Raw*>(most[w])[threadIdx.x]));
+        const float scale = scale_of<E5M2>(raw_magnitude<T>(m));
         inverses[threadIdx.x] = 1.0f / scale;
         const int column = c - c8 + static_cast<int>(threadIdx.x);
         if (column < a.k) a.sc[block * a.ldsc + column] = scale;
@@ -200,19 +233,13 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
         const float4 x = reinterpret_cast<const float4*>(inverses + c8)[i];
         inverse[4 * i] = x.x, inverse[4 * i + 1] = x.y, inverse[4 * i + 2] = x.z, inverse[4 * i + 3] = x.w;
       }
-      // The rows as they are, or the block's own 128 with zeros behind the group's last.
-      const long long to = ragged ? static_cast<long long>(block) * TILE : row;
-      const int written = ragged ? TILE : count;
+      // The rows as they are, or the block's own 128 with zeros behind the group's last (which were read as zeros).
+      put_rows(a.qc, a.ldqc, ragged ? static_cast<long long>(block) * TILE : row, ragged ? TILE : count, [&](int i, auto store) {
+        float f[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = r0 + 16 * i;
-        if (r < written) {
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = v[i].get(e) * inverse[e];
-          put_bytes(a.qc + (to + r) * a.ldqc, c, a.k, r < count ? eight_bits<E5M2>(f, 1.0f) : make_uint2(0, 0));
-        }
-      }
+        for (int e = 0; e < 8; ++e) f[e] = v[i].get(e) * inverse[e];
+        store(r0 + 16 * i < count ? eight_bits<E5M2>(f, 1.0f) : make_uint2(0, 0));
+      });
     }
     if (MATRIX) {
       uint32_t m = 0;
@@ -224,19 +251,14 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
 #pragma unroll
       for (int w = 0; w < kThreads / 32; ++w) m = max(m, most[0][w]);
       __syncthreads();
-      const float scale = scale_of<E5M2>(m), inverse = 1.0f / scale;
+      const float scale = scale_of<E5M2>(raw_magnitude<T>(m)), inverse = 1.0f / scale;
       if (threadIdx.x == 0) a.s[(static_cast<long long>(mat) * a.row_tiles + block) * a.col_tiles + c / TILE] = scale;
-      uint8_t* q = a.q + mat * a.stride_q;
+      put_rows(a.q + mat * a.stride_q, a.ldq, row, count, [&](int i, auto store) {
+        float f[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = r0 + 16 * i;
-        if (r < count) {
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = v[i].get(e);
-          put_bytes(q + static_cast<long long>(row + r) * a.ldq, c, a.k, eight_bits<E5M2>(f, inverse));
-        }
-      }
+        for (int e = 0; e < 8; ++e) f[e] = v[i].get(e);
+        store(eight_bits<E5M2>(f, inverse));
+      });
     }
   }
   // Rows that belong to no group are in no tile: a warp a block of 128.
@@ -272,7 +294,7 @@ cudaError_t start(const QuantParams& a, cudaStream_t stream) {
   auto kernel = quantize_kernel<T, BLOCK, E5M2, ALIGNED>;
   constexpr bool AHEAD = ALIGNED && sizeof(T) == 2;
   constexpr int smem = AHEAD ? kAhead * kTileBytes16 : 0;
-  long long grid = 1 << 20;
+  int grid = 1 << 20;
   if (AHEAD) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -366,7 +388,9 @@ int ozaki_quantize_f8(int block, int k, int rows, int groups, int dtype, const v
   a.lds = lds;
   a.ldsc = ldsc;
   a.col_tiles = column_blocks(k, 1, false);
-  a.tiles = static_cast<long long>(a.col_tiles) * a.row_tiles * a.mats;
+  const long long tiles = static_cast<long long>(a.col_tiles) * a.row_tiles * a.mats;
+  if (tiles > INT32_MAX / 2) return OZ_EINVAL;  // (2^44 elements)
+  a.tiles = static_cast<int>(tiles);
   a.status = device_status_ptr();
   if (!a.status) return OZ_ECUDA;
   const bool e5m2 = type == OZ_E5M2;

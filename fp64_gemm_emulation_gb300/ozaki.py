@@ -909,7 +909,7 @@ def _output(out, what: str, rows: int, features: int, dtype, device):
     if out is None:
         if dtype is None:
             dtype = _torch().bfloat16
-        out, ld = _new((rows, features), dtype, device), max(1, features)
+        out, ld = _torch().empty_strided((rows, features), (features, 1), dtype=dtype, device=device), features or 1
     else:
         if out.device != device or (dtype is not None and out.dtype != dtype):
             raise ValueError(f"{what} must be on the operands' device, with the dtype asked for")
@@ -1080,7 +1080,7 @@ def _norm_rows(t, what: str, rows: int, k: int, like) -> int:
     if t.dtype != like.dtype or t.device != like.device:
         raise ValueError(f"{what} must have X's dtype and device")
     shape, stride = t.shape, t.stride()
-    if shape == (rows, k) and rows > 1 and k > 0 and stride[1] == 1 and k <= stride[0] <= _INT_MAX:
+    if shape == (rows, k) and k > 0 and stride[1] == 1 and k <= stride[0] <= _INT_MAX:
         return stride[0]
     ld = _tokens(t, what, k)  # (says what is wrong)
     if shape[0] != rows:
@@ -1103,8 +1103,8 @@ def ozaki_rms_norm_f8(X, W, residual=None, eps: float = 1e-6, H=None, Y=None, st
         return _call_on(other, ozaki_rms_norm_f8, X, W, residual, eps, H, Y)
     torch = _torch()
     device, code = _cuda(X, "X"), _dtype(X)
-    ldx = _tokens(X, "X")
-    rows, k = X.shape
+    rows, k = X.shape if X.dim() == 2 else (0, 0)
+    ldx = _norm_rows(X, "X", rows, k, X)
     if k > OZ_MAX_NORM_WIDTH:
         raise ValueError(f"at most {OZ_MAX_NORM_WIDTH} features: {k}")
     _norm_weight(W, k, X)

@@ -12,7 +12,7 @@
 // 256 n, 128 m in each CTA.
 //   warp 0: TMA producer   warps 1 and 3: MMA issuers of the two halves (leader; 1: TMEM owner)   warp 2: scales (wgrad)
 //   warps 4-11: epilogue
-// 6 stages of 32 KB: 128 x 128 bytes of A and two tiles of 64 n of B, K-major or MN-major as they lie in memory.
+// 4 stages (wgrad: 6) of 32 KB: 128 x 128 bytes of A and two tiles of 64 n of B, K-major or MN-major as they lie in memory.
 // What bounds it: every 128 k each of a CTA's 128 x 256 sums is read from tensor memory, scaled and added, while the
 // MMAs take 512 cycles.  So:
 //  - rows of tokens are m, one a lane (tcgen05.ld.32x32b): a lane needs one factor for its 128 columns, its row's
@@ -34,23 +34,27 @@ using namespace prod;
 
 constexpr int BK8 = kScaleBlock;
 constexpr int STEP8 = 32;                       // k of one MMA
-constexpr int STAGES8 = 6;
 constexpr uint32_t TILE8 = 128 * BK8;           // bytes of a stage's A (and of its B) in one CTA
 constexpr uint32_t HALF8 = 64 * BK8;            // of the 64 n that a CTA holds of one accumulator
 constexpr int ACC8 = 128;                       // columns of an accumulator; two for each half of the tile
 constexpr int EPI8_FIRST = 4, EPI8_WARPS = 8, THREADS8 = (EPI8_FIRST + EPI8_WARPS) * 32;
 constexpr int BLOCKS8 = ACC8 / 32;              // blocks of 32 columns whose sums a warp holds
-constexpr uint32_t STASH8 = 32 * 64;
 // Registers: the four warps of the first warpgroup give theirs to the epilogue, whose threads hold 128 sums.
 // 128 x 72 + 256 x 216 = 384 x 168, what the launch has.
-constexpr int REGS_FEW = 56, REGS_MANY = 224;
+constexpr int REGS_FEW = 72, REGS_MANY = 216;
 
 enum Op8 { kForward8, kDgrad8, kWgrad8 };
 
 // wgrad: scales of a k-block in shared memory, 256 of n and 128 of the CTA's m.
 constexpr int SLOTS8 = 4, BATCH8 = 2, SLOT_FLOATS8 = 256 + 128;  // BATCH8: k-blocks whose scales are fetched at once
+// The ring of stages, the scales, and the epilogue warps' stashes: wgrad's a block of 32 x 32, otherwise 32 rows of 128
+// finished columns, which leave while the next tile is summed (16 bytes more a row: no bank conflicts, and room for a note).
 template <Op8 OP>
-constexpr uint32_t kScaleBytes8 = OP == kWgrad8 ? SLOTS8 * SLOT_FLOATS8 * 4 : 0;
+struct Smem8 {
+  static constexpr int STAGES = OP == kWgrad8 ? 6 : 4;
+  static constexpr uint32_t SCALES = OP == kWgrad8 ? SLOTS8 * SLOT_FLOATS8 * 4 : 0;
+  static constexpr uint32_t ROW = ACC8 * 2 + 16, STASH = OP == kWgrad8 ? 32 * 64 : 32 * ROW;
+};
 
 struct Params8 {
   CUtensorMap tmA, tmA128, tmB;
@@ -197,26 +201,39 @@ __device__ __forceinline__ void fma_loaded(float v0, float v1, float2 b, float s
       : "f"(v0), "f"(v1), "f"(b.x), "f"(b.y), "f"(s));
 }
 
-// 32 finished columns of this lane's row to the output: through the warp's stash, 16 bytes a lane, or, where not all of
-// them exist or stores cannot be wide, an element a lane.  row0, col: the block's first; rows, cols: how many exist.
-__device__ __forceinline__ void emit_rows(const Params8& a, const float (&v)[32], uint8_t* stash, long long row0, int rows, int col, int cols) {
-  const int lane = threadIdx.x & 31;
+// 32 finished columns of this lane's row into its row of the stash.
+__device__ __forceinline__ void stash_row(uint8_t* row, const float (&v)[32], bool bf16) {
   uint32_t w[16];
-  pack_block(v, w, a.out_type == kOutBf16);
+  pack_block(v, w, bf16);
 #pragma unroll
-  for (int p = 0; p < 4; ++p) *reinterpret_cast<uint4*>(stash + stash_at(lane, p)) = make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
-  __syncwarp();
+  for (int p = 0; p < 4; ++p) *reinterpret_cast<uint4*>(row + 16 * p) = make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
+}
+
+// The warp's finished rows from its stash (`pitch` bytes a row) to the output.  Each lane sends its own row off as a bulk
+// copy, which the next tile's sums do not wait for (8192 x 4096 x 8192: 224 us; 226 with 16-byte stores by the lanes, 202
+// with no stores at all).  Elements behind the last whole 16 bytes are stored one by one, and so is everything where
+// rows do not start at multiples of 16 bytes.  row0, col: the first; rows, cols: how many exist.
+__device__ __forceinline__ void send_rows(const Params8& a, uint8_t* stash, uint32_t pitch, long long row0, int rows, int col, int cols) {
+  const int lane = threadIdx.x & 31;
+  cols = min(cols, ACC8);
   uint16_t* out = static_cast<uint16_t*>(a.out) + row0 * a.ld + col;
-  if (a.vec && cols >= 32) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2);
-      if (r < rows) *reinterpret_cast<uint4*>(out + r * a.ld + 8 * (lane & 3)) = *reinterpret_cast<const uint4*>(stash + stash_at(r, lane & 3));
+  if (a.vec) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (lane < rows) {
+      const uint8_t* from = stash + lane * pitch;
+      uint16_t* to = out + lane * a.ld;
+      const int whole = cols & ~7;
+      if (whole)
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(smem_u32(from)), "r"(2 * whole) : "memory");
+      for (int c = whole; c < cols; ++c) to[c] = reinterpret_cast<const uint16_t*>(from)[c];
     }
-  } else if (lane < cols) {
-    for (int r = 0; r < min(rows, 32); ++r) out[r * a.ld + lane] = *reinterpret_cast<const uint16_t*>(stash + stash_at(r, lane >> 3) + (lane & 7) * 2);
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  } else {
+    __syncwarp();
+    for (int r = 0; r < min(rows, 32); ++r)
+      for (int c = lane; c < cols; c += 32) out[r * a.ld + c] = reinterpret_cast<const uint16_t*>(stash + r * pitch)[c];
+    __syncwarp();
   }
-  __syncwarp();
 }
 
 // 32 lanes x 16 columns in the fragments of tcgen05.ld.16x256b.x2: element i is
@@ -233,12 +250,14 @@ __device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, float (&v)[16]) {
 template <Op8 OP>
 __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_constant__ Params8 a) {
   typedef Walk8<OP> Walk;
+  constexpr int STAGES8 = Smem8<OP>::STAGES;
+  constexpr uint32_t STASH8 = Smem8<OP>::STASH;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + STAGES8 * TILE8;
   float* scales = reinterpret_cast<float*>(smem + 2 * STAGES8 * TILE8);
-  uint8_t* stash = smem + 2 * STAGES8 * TILE8 + kScaleBytes8<OP>;
+  uint8_t* stash = smem + 2 * STAGES8 * TILE8 + Smem8<OP>::SCALES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(stash + EPI8_WARPS * STASH8);
   uint64_t* full = bars;                     // [STAGES8] TMA (both CTAs) -> MMA  (used in the leader)
   uint64_t* empty = full + STAGES8;          // [STAGES8] MMA issuers -> TMA      (both CTAs)
@@ -508,30 +527,25 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
     if constexpr (OP != kWgrad8) {
       // The sums take nearly all registers: the walker is made anew for each tile, and where the tile goes waits in the
       // warp's stash.
-      int4* const kept = reinterpret_cast<int4*>(my_stash);  // first row, rows, first column, columns
-      for (int at = static_cast<int>(blockIdx.x >> 1) - static_cast<int>(gridDim.x >> 1); ok && half < halves;
-           at += static_cast<int>(gridDim.x >> 1)) {
-        int left, blocks;  // k-blocks to come, blocks of 32 columns
-        const float *sx, *sw;
-        {
-          Walk walk(a, table, at);
-          Unit8 u;
-          if (!walk.next(u)) break;
-          const int rows = u.mcount - mrow, col = u.n0 + static_cast<int>(half) * ACC8, cols = u.ncount - static_cast<int>(half) * ACC8;
-          blocks = rows > 0 ? min(BLOCKS8, ceil_div(max(0, cols), 32)) : 0;
-          left = u.kbs;
-          // This lane's row's scales and those of the half's features.  Lanes without a row take the last one's.
-          sx = a.sa + u.m0 + mrow + min(lane, rows - 1);
-          sw = a.sb + u.group * a.sb_group + static_cast<long long>(col / 128) * a.sb_n;
-          __syncwarp();
-          if (lane == 0) *kept = make_int4(u.m0 + mrow, rows, col, cols);
-        }
-        float run[BLOCKS8][32];
-#pragma unroll
-        for (int i = 0; i < BLOCKS8 * 32; ++i) run[i >> 5][i & 31] = 0.0f;
-        // Scales are fetched two k-blocks ahead and multiplied only when they are used (a product formed at once would
-        // wait for both).
-        float x[2] = {}, w[2] = {};
+      int4* const kept = reinterpret_cast<int4*>(my_stash + ACC8 * 2);  // first row, rows, first column, columns
+      int at = static_cast<int>(blockIdx.x >> 1) - static_cast<int>(gridDim.x >> 1);
+      int left = 0, blocks = 0;  // k-blocks to come, blocks of 32 columns
+      const float *sx, *sw;      // this lane's row's scales (lanes without a row take the last one's), the half's features'
+      // Scales are fetched two k-blocks ahead and multiplied only when they are used (a product formed at once would
+      // wait for both); a tile's first ones before the tile before it is stored.
+      float x[2] = {}, w[2] = {};
+      auto begin = [&]() {
+        Walk walk(a, table, at);
+        at += static_cast<int>(gridDim.x >> 1);
+        Unit8 u;
+        if (!walk.next(u)) return false;
+        const int rows = u.mcount - mrow, col = u.n0 + static_cast<int>(half) * ACC8, cols = u.ncount - static_cast<int>(half) * ACC8;
+        blocks = rows > 0 ? min(BLOCKS8, ceil_div(max(0, cols), 32)) : 0;
+        left = u.kbs;
+        sx = a.sa + u.m0 + mrow + min(lane, rows - 1);
+        sw = a.sb + u.group * a.sb_group + static_cast<long long>(col / 128) * a.sb_n;
+        __syncwarp();
+        if (lane == 0) *kept = make_int4(u.m0 + mrow, rows, col, cols);
         if (blocks && left) {
           x[0] = x[1] = *sx;
           w[0] = w[1] = *sw;
@@ -540,6 +554,13 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
             w[1] = *(sw += a.sb_k);
           }
         }
+        return true;
+      };
+      for (bool more = half < halves && begin(); ok && more;) {
+        float run[BLOCKS8][32];
+#pragma unroll
+        for (int i = 0; i < BLOCKS8 * 32; ++i) run[i >> 5][i & 31] = 0.0f;
+        const int tile_blocks = blocks;
         auto factor = [&](float& x, float& w) {
           const float f = x * w;
           if (left > 2) {
@@ -604,10 +625,16 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
         __syncwarp();
         const int4 to = *kept;
         __syncwarp();
+        more = begin();
+        if (tile_blocks) {
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the stash's last rows have left it
 #pragma unroll
-        for (int j = 0; j < BLOCKS8; ++j)
-          if (j < blocks) emit_rows(a, run[j], my_stash, to.x, to.y, to.z + 32 * j, to.w - 32 * j);
+          for (int j = 0; j < BLOCKS8; ++j)
+            if (j < tile_blocks) stash_row(my_stash + lane * Smem8<OP>::ROW + 64 * j, run[j], a.out_type == kOutBf16);
+          send_rows(a, my_stash, Smem8<OP>::ROW, to.x, to.y, to.z, to.w);
+        }
       }
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else {
       uint32_t slot = 0, sphase = 0;
       auto scales_there = [&]() { return wait(&sfull[slot], sphase, kWaitLimitNs); };
@@ -839,7 +866,7 @@ int launch8(const Problem8& p, const Device& d, cudaStream_t stream) {
   a.status = d.status;
   a.epi_wait_ns = epilogue_wait_ns();
   auto kernel = block8_kernel<OP>;
-  constexpr size_t smem = 1024 /*alignment*/ + 2 * STAGES8 * TILE8 + kScaleBytes8<OP> + EPI8_WARPS * STASH8 + 512 /*barriers*/ + Walk::kTableBytes;
+  constexpr size_t smem = 1024 /*alignment*/ + 2 * Smem8<OP>::STAGES * TILE8 + Smem8<OP>::SCALES + EPI8_WARPS * Smem8<OP>::STASH + 512 /*barriers*/ + Walk::kTableBytes;
   static_assert(smem <= 232448, "shared memory budget");
   static_assert(smem + 2 * 16384 > 232448, "alone on its SM, as the other holders of tensor memory");
   cudaLaunchConfig_t cfg = {};

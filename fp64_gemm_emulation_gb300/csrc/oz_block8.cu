@@ -504,8 +504,8 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
     bool ok = true;
     Walk(a, table).outside(warp - EPI8_FIRST);
     auto wait = [&](uint64_t* bar, uint32_t phase, uint64_t limit) {
-      if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, phase))) return true;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar, phase, limit, abort_flag));
+      if (__all_sync(0xFFFFFFFFu, limit ? mbar_try_wait(bar, phase) : mbar_test_wait(bar, phase))) return true;
+      ok = limit && __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar, phase, limit, abort_flag));
       if (!ok && lane == 0 && !*abort_flag) stop_pair(abort_flag, a.status);
       return ok;
     };
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
 #pragma unroll
             for (int h = 0; h < 4; ++h) sm[h] = scales[slot * SLOT_FLOATS8 + 256 + quad * 32 + (lane >> 2) + 8 * h];
           };
-          if (left > 0 && scales_there() && sums_there()) {
+          if (left > 0 && sums_there() && scales_there()) {
             scales_of_m();
             tmem_ld_frag16(lanes + acc * ACC8, v[0]);
           }
@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
           }
           tmem_ld_wait();
         } else {
-          for (; left > 0 && scales_there() && sums_there(); --left) {
+          for (; left > 0 && sums_there() && scales_there(); --left) {
             release();
             scales_done();
           }

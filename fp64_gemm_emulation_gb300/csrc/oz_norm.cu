@@ -153,15 +153,16 @@ __global__ void __launch_bounds__(STAY ? 256 : 1024, STAY ? (RUNS == 1 ? 4 : RUN
 // PIECES: all matrices lie alike (and one thread's eight elements are whole pieces); otherwise element by element.
 template <class T, bool PIECES>
 struct Columns {
-  const T *first, *end;  // the matrix
-  long long ld;
-  int rows, k;
-  __device__ Columns(const void* p, long long ld, int rows, int k)
-      : first(static_cast<const T*>(p)), end(first + (rows - 1) * ld + k), ld(ld), rows(rows), k(k) {}
-  __device__ Eight<T> load(int row, int c) const {  // without a mask: columns outside [0, k) may be anything
-    const T* from = first + row * ld + c;
-    if (PIECES && row < rows && c < k && from >= first && from + 8 <= end) return load_eight(from);
-    return gather_eight(from, 1, [&](int e) { return row < rows && c + e >= 0 && c + e < k; });
+  const T *at, *end;  // the next row's first element, the matrix's end
+  long long step;     // elements from one of the CTA's rows to the next
+  __device__ Columns(const void* p, long long ld, int rows, int k, int row, int step)
+      : at(static_cast<const T*>(p) + row * ld), end(static_cast<const T*>(p) + (rows - 1) * ld + k), step(step * ld) {}
+  // Eight columns of that row from c on, without a mask: what is in columns outside [0, k) may be anything.  first: the
+  // matrix's first row, before which nothing is read.
+  __device__ Eight<T> load(int c, int k, bool first) const {
+    const T* from = at + c;
+    if (PIECES && ((c >= 0 && c + 8 <= k) || (c < k && !(first && c < 0) && from + 8 <= end))) return load_eight(from);
+    return gather_eight(from, 1, [&](int e) { return c + e >= 0 && c + e < k; });
   }
 };
 
@@ -185,22 +186,28 @@ __global__ void __launch_bounds__(1024) norm_back_kernel(const __grid_constant__
   float dw[RUNS][8];
 #pragma unroll
   for (int i = 0; i < RUNS * 8; ++i) dw[i >> 3][i & 7] = 0.0f;
-  const Columns<T, PIECES> rdy(a.dy, a.lddy, a.rows, a.k), rh(a.h, a.ldh, a.rows, a.k), rdh(a.dh, a.lddh, a.rows, a.k);
-  Eight<T> dy[RUNS], h[RUNS], dh[RUNS] = {}, w[RUNS];
+  int row = kind + a.period * (static_cast<int>(blockIdx.x) / a.period), turn = 0;
+  Columns<T, PIECES> rdy(a.dy, a.lddy, a.rows, a.k, row, step), rh(a.h, a.ldh, a.rows, a.k, row, step), rdh(a.dh, a.lddh, a.rows, a.k, row, step);
+  T* to_row = static_cast<T*>(a.dx) + row * a.lddx;
+  const float each = 1.0f / static_cast<float>(a.k);
+  Eight<T> dy[RUNS] = {}, h[RUNS] = {}, dh[RUNS] = {}, w[RUNS];
   float r = 0.0f;
   auto ask = [&](int row) {
+    if (row >= a.rows) return;
 #pragma unroll
     for (int j = 0; j < RUNS; ++j) {
-      dy[j] = rdy.load(row, column(j));
-      h[j] = rh.load(row, column(j));
-      if (EARLY && a.dh) dh[j] = rdh.load(row, column(j));
+      dy[j] = rdy.load(column(j), a.k, row == 0);
+      h[j] = rh.load(column(j), a.k, row == 0);
+      if (EARLY && a.dh) dh[j] = rdh.load(column(j), a.k, row == 0);
     }
-    if (row < a.rows) r = a.rstd[row];
+    r = a.rstd[row];
+    rdy.at += rdy.step;
+    rh.at += rh.step;
+    if (EARLY) rdh.at += rdh.step;
   };
-  int row = kind + a.period * (static_cast<int>(blockIdx.x) / a.period), turn = 0;
   if (EARLY) ask(row);
 #pragma unroll
-  for (int j = 0; j < RUNS; ++j) w[j] = Columns<T, false>(a.w, 0, 1, a.k).load(0, column(j));
+  for (int j = 0; j < RUNS; ++j) w[j] = Columns<T, false>(a.w, 0, 1, a.k, 0, 0).load(column(j), a.k, false);
   for (; row < a.rows; row += step, turn ^= 1) {
     if (!EARLY) ask(row);
     float dot = 0.0f;
@@ -222,19 +229,19 @@ __global__ void __launch_bounds__(1024) norm_back_kernel(const __grid_constant__
     }
     if (EARLY) ask(row + step);
     // Two rooms in turn: a warp writes one again only after the other's barrier.
-    dot = row_sum(dot, meet[turn]) / static_cast<float>(a.k);
+    dot = row_sum(dot, meet[turn]) * each;
     const float f = rs * rs * dot;
 #pragma unroll
     for (int j = 0; j < RUNS; ++j) {
       const int c = column(j);
-      if (!EARLY && a.dh) dh1[j] = rdh.load(row, c);
+      if (!EARLY && a.dh) dh1[j] = rdh.load(c, a.k, row == 0);
       float dx[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         dx[e] = rs * (dy1[j].get(e) * w[j].get(e) - h1[j].get(e) * f);
         if (a.dh) dx[e] += dh1[j].get(e);
       }
-      T* to = static_cast<T*>(a.dx) + row * a.lddx + c;
+      T* to = to_row + c;
       if (PIECES && c >= 0 && c + 8 <= a.k) {
         store_eight(to, dx);
       } else {
@@ -243,6 +250,8 @@ __global__ void __launch_bounds__(1024) norm_back_kernel(const __grid_constant__
           if (c + e >= 0 && c + e < a.k) from_float(dx[e], to[e]);
       }
     }
+    to_row += step * a.lddx;
+    if (!EARLY) rdh.at += rdh.step;
   }
 #pragma unroll
   for (int j = 0; j < RUNS; ++j) {
@@ -274,6 +283,8 @@ __global__ void __launch_bounds__(256) norm_weight_kernel(const float* part, int
     from_float(v, dw[c]);
   }
 }
+
+constexpr int kMaxRows = INT32_MAX - (1 << 20);  // a row's number and a step of all CTAs stay an int
 
 int sm_count() {
   int dev = 0, sms = 0;
@@ -365,7 +376,7 @@ int parts_of(int rows, int k) {
 }
 
 int check_back(int k, int rows, int dtype, long long lddy, long long ldh, long long lddh, long long lddx) {
-  if (k < 0 || rows < 0 || k > OZ_MAX_NORM_WIDTH || !element_bytes(dtype)) return OZ_EINVAL;
+  if (k < 0 || rows < 0 || rows > kMaxRows || k > OZ_MAX_NORM_WIDTH || !element_bytes(dtype)) return OZ_EINVAL;
   const long long least = k > 1 ? k : 1;
   return lddy < least || ldh < least || lddh < least || lddx < least ? OZ_EINVAL : OZ_OK;
 }
@@ -395,7 +406,7 @@ extern "C" {
 
 int ozaki_rms_norm_f8(int k, int rows, int dtype, const void* X, int ldx, const void* residual, int ldr, const void* W, float eps,
                       void* Q, int ldq, float* S, int lds, void* H, int ldh, float* rstd, void* Y, int ldy, cudaStream_t stream) {
-  if (k < 0 || rows < 0 || k > OZ_MAX_NORM_WIDTH || !element_bytes(dtype) || !(eps >= 0.0f)) return OZ_EINVAL;
+  if (k < 0 || rows < 0 || rows > kMaxRows || k > OZ_MAX_NORM_WIDTH || !element_bytes(dtype) || !(eps >= 0.0f)) return OZ_EINVAL;
   const int least = k > 1 ? k : 1;
   if (ldx < least || ldr < least || ldh < least || ldy < least || ldq < least || lds < (rows > 1 ? rows : 1)) return OZ_EINVAL;
   if (k == 0 || rows == 0) return OZ_OK;

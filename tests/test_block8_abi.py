@@ -106,7 +106,7 @@ def norm(k=16, rows=8, dtype=oz.OZ_BF16, X=P, ldx=16, R=P, ldr=16, W=P, eps=1e-6
     return lib.ozaki_rms_norm_f8(k, rows, dtype, X, ldx, R, ldr, W, eps, Q, ldq, S, lds, H, ldh, rstd, Y, ldy, None)
 
 
-@pytest.mark.parametrize("bad", [dict(k=-1), dict(k=oz.OZ_MAX_NORM_WIDTH + 1), dict(rows=-1), dict(dtype=0), dict(dtype=oz.OZ_E4M3), dict(eps=-1.0),
+@pytest.mark.parametrize("bad", [dict(k=-1), dict(k=oz.OZ_MAX_NORM_WIDTH + 1), dict(rows=-1), dict(rows=2**31 - 1, lds=2**31 - 1), dict(dtype=0), dict(dtype=oz.OZ_E4M3), dict(eps=-1.0),
                                  dict(eps=float("nan")), dict(ldx=15), dict(ldr=15), dict(ldh=15), dict(ldy=15), dict(ldq=15), dict(ldq=24), dict(lds=7),
                                  dict(X=None), dict(W=None), dict(Q=None), dict(S=None), dict(rstd=None), dict(X=P + 1), dict(R=P + 1), dict(W=P + 1),
                                  dict(H=P + 1), dict(Y=P + 1), dict(Q=P + 8), dict(S=P + 2), dict(rstd=P + 2)])
@@ -120,7 +120,7 @@ def back(k=16, rows=8, dtype=oz.OZ_BF16, dY=P, lddy=16, H=P, ldh=16, W=P, rstd=P
     return a if ws is None or nbytes < 1 << 20 else (a, lib.ozaki_rms_norm_backward(*args, None))
 
 
-@pytest.mark.parametrize("bad", [dict(k=-1), dict(k=oz.OZ_MAX_NORM_WIDTH + 1), dict(rows=-1), dict(dtype=0), dict(lddy=15), dict(ldh=15), dict(lddh=15),
+@pytest.mark.parametrize("bad", [dict(k=-1), dict(k=oz.OZ_MAX_NORM_WIDTH + 1), dict(rows=-1), dict(rows=2**31 - 1), dict(dtype=0), dict(lddy=15), dict(ldh=15), dict(lddh=15),
                                  dict(lddx=15), dict(dY=None), dict(H=None), dict(W=None), dict(rstd=None), dict(dX=None), dict(dW=None), dict(dY=P + 1)])
 def test_norm_backward_refuses_bad_arguments(bad):
     if "dY" in bad and bad["dY"]:

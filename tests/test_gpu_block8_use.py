@@ -244,6 +244,26 @@ def test_offsets_past_32_bits():
         assert torch.equal(a[tail].float(), b.float())
 
 
+# ------------------------------------------------------------------ a wait that runs out
+def test_an_expired_wait_is_reported_and_the_next_call_is_right():
+    x, _, w, _, dy, o = layer()
+    q, s = oz.ozaki_quantize_f8(x, "row")
+    wq, ws = oz.ozaki_quantize_f8(w, "matrix")
+    dq, ds, dqc, dsc = oz.ozaki_quantize_f8(dy, "both", o)
+    xqc, xsc = oz.ozaki_quantize_f8(x, "column", o)
+    calls = [lambda: oz.ozaki_grouped_gemm_f8(q, s, wq, ws, o), lambda: oz.ozaki_grouped_gemm_f8_dgrad(dq, ds, wq, ws, o),
+             lambda: oz.ozaki_grouped_gemm_f8_wgrad(dqc, dsc, xqc, xsc, o)]
+    for call in calls:
+        want = call()
+        oz.ozaki_set_epilogue_wait_ns(0)
+        try:
+            call()
+            assert oz.ozaki_get_device_status() == oz.OZ_ETIMEOUT
+        finally:
+            oz.ozaki_set_epilogue_wait_ns(-1)
+        assert torch.equal(call(), want)
+
+
 # ------------------------------------------------------------------ a training step
 def test_eight_bit_layer_gradients():
     rows, experts, k, n = 500, 3, 200, 160

@@ -1,4 +1,5 @@
-"""Build libozaki.so (sm_103a) in-tree with nvcc: one object per .cu, compiled in parallel.
+"""Build libozaki.so (sm_103a) in-tree with nvcc: one object per .cu, compiled in parallel; and, beside it, the binding's
+helper _tensor_lists.so (host code against torch's headers) with g++.
 
 Usage: ``python -m fp64_gemm_emulation_gb300.build_lib`` (also called by
 ``__graft_entry__.build()``).  Objects go to ``fp64_gemm_emulation_gb300/_build/``,
@@ -19,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libozaki.so")
+LISTS = os.path.join(PKG, "_tensor_lists.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
@@ -37,6 +39,29 @@ def _stale(obj: str, src: str, headers: list[str]) -> bool:
         return True
     t = os.path.getmtime(obj)
     return any(os.path.getmtime(p) > t for p in [src] + headers)
+
+
+def build_lists(verbose: bool = False, force: bool = False) -> str:
+    """_tensor_lists.so, a Python module (csrc/tensor_lists.cpp)."""
+    src = os.path.join(CSRC, "tensor_lists.cpp")
+    if not force and not _stale(LISTS, src, []):
+        return ""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"], "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           src, "-o", LISTS + ".tmp", "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + lib]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(LISTS + ".tmp", LISTS)
+    return r.stderr
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
@@ -58,10 +83,12 @@ def build(verbose: bool = False, force: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return r.stderr
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(todo), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(todo) + 1, os.cpu_count() or 1))) as ex:
+        lists = ex.submit(build_lists, verbose, force)
         for msg in ex.map(compile_one, todo):
             if verbose and msg:
                 print(msg, file=sys.stderr)
+        lists.result()
     if todo or force or not os.path.exists(LIB):
         cmd = [exe] + ARCH + ["-shared", "-o", LIB + ".tmp"] + objs
         if verbose:

@@ -9,6 +9,10 @@
 //
 // Squares: 32 elements at a time in FP32 where the largest of them is between 2^-50 and 2^55 (what the others
 // then lose below 2^-126 is under 2^-26 of the sum), otherwise in FP64; the running sum is FP64 throughout.
+#include <algorithm>
+#include <utility>
+#include <vector>
+
 #include "oz_elements.cuh"
 #include "oz_device.cuh"
 
@@ -245,14 +249,33 @@ extern "C" {
 
 size_t ozaki_clip_grad_norm_workspace_bytes(void) { return kClipBytes; }
 
-static int clip_check(const Work& w, float limit, float eps, const float* norm) {
+static int clip_check(const Work& w, float limit, float eps, const float* norm) try {
   if (w.count < 0 || w.count > kMaxTensors || !(limit >= 0.0f) || !(eps >= 0.0f) || !norm || (reinterpret_cast<uintptr_t>(norm) & 3)) return OZ_EINVAL;
   if (w.count && (!w.dtypes || !w.in || !w.out || !w.counts)) return OZ_EINVAL;
   for (int i = 0; i < w.count; ++i) {
     if (!element_bytes(w.dtypes[i]) || w.counts[i] < 0) return OZ_EINVAL;
     if (w.counts[i] && (!w.in[i] || !w.out[i] || !element_aligned(w.in[i], w.dtypes[i]) || !element_aligned(w.out[i], w.dtypes[i]))) return OZ_EINVAL;
   }
+  // No two outputs may meet: a tensor that is listed twice would be scaled once or twice, as it happens.
+  std::vector<std::pair<uintptr_t, uintptr_t>> spans;
+  spans.reserve(w.count);
+  for (int i = 0; i < w.count; ++i) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(w.out[i]);
+    if (w.counts[i]) spans.emplace_back(at, at + element_bytes(w.dtypes[i]) * static_cast<uintptr_t>(w.counts[i]));
+  }
+  if (!std::is_sorted(spans.begin(), spans.end())) std::sort(spans.begin(), spans.end());
+  for (size_t i = 1; i < spans.size(); ++i)
+    if (spans[i].first < spans[i - 1].second) return OZ_EINVAL;
   return OZ_OK;
+} catch (...) {  // no host memory
+  return OZ_ENOMEM;
+}
+
+static int clip_run(const Work& w, float limit, float eps, float* norm, void* workspace, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return OZ_ECUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  return w.count <= kFew ? clip_launches<kFew>(w, limit, eps, norm, ws, sms, stream) : clip_launches<kMany>(w, limit, eps, norm, ws, sms, stream);
 }
 
 int ozaki_clip_grad_norm_ws(int count, const int* dtypes, const void* const* grads, void* const* outs, const long long* counts,
@@ -261,15 +284,13 @@ int ozaki_clip_grad_norm_ws(int count, const int* dtypes, const void* const* gra
   const int rc = clip_check(w, max_norm, eps, norm);
   if (rc) return rc;
   if (!workspace || ws_bytes < kClipBytes || (reinterpret_cast<uintptr_t>(workspace) & 255)) return OZ_ENOMEM;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return OZ_ECUDA;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  return count <= kFew ? clip_launches<kFew>(w, max_norm, eps, norm, ws, sms, stream) : clip_launches<kMany>(w, max_norm, eps, norm, ws, sms, stream);
+  return clip_run(w, max_norm, eps, norm, workspace, stream);
 }
 
 int ozaki_clip_grad_norm(int count, const int* dtypes, const void* const* grads, void* const* outs, const long long* counts,
                          float max_norm, float eps, float* norm, cudaStream_t stream) {
-  int rc = clip_check(Work{count, dtypes, grads, outs, counts}, max_norm, eps, norm);
+  const Work w{count, dtypes, grads, outs, counts};
+  int rc = clip_check(w, max_norm, eps, norm);
   if (rc) return rc;
   void* ws = nullptr;
   keep_default_pool_cached();
@@ -277,7 +298,7 @@ int ozaki_clip_grad_norm(int count, const int* dtypes, const void* const* grads,
     cudaGetLastError();
     return OZ_ENOMEM;
   }
-  rc = ozaki_clip_grad_norm_ws(count, dtypes, grads, outs, counts, max_norm, eps, norm, ws, kClipBytes, stream);
+  rc = clip_run(w, max_norm, eps, norm, ws, stream);
   if (cudaFreeAsync(ws, stream) != cudaSuccess && rc == OZ_OK) rc = OZ_ECUDA;
   return rc;
 }

@@ -14,7 +14,6 @@ exception.
 """
 from __future__ import annotations
 
-import array
 import ctypes
 import functools
 import os
@@ -1168,6 +1167,13 @@ def ozaki_rms_norm_backward_workspace_bytes(k: int, rows: int) -> int:
 
 
 # ------------------------------------------------------------------ clipping by the global norm
+def _tensor_lists():
+    """The module that gathers what the library wants to know of many tensors (built beside it; it needs torch)."""
+    from . import _tensor_lists
+
+    return _tensor_lists
+
+
 def ozaki_clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None, workspace=None, stream=None):
     """The 2-norm over all tensors of grads (a float32 scalar on the device), each of which is multiplied by
     min(1, max_norm / (norm + eps)): in place, or into the tensors of out.
@@ -1185,25 +1191,12 @@ def ozaki_clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None, wo
         for t in (*grads, *outs):
             t.record_stream(other)
         return result
-    if len(outs) != len(grads):
-        raise ValueError(f"out must hold {len(grads)} tensors: {len(outs)}")
-    _dtype(grads[0])
-    try:
-        codes = [_DTYPE_CODES[t.dtype] for t in grads]
-    except KeyError as e:
-        raise TypeError(f"dtype must be bfloat16, float16 or float32: {e}") from None
     n = len(grads)
-    tensors, T = grads if outs is grads else grads + outs, torch.Tensor
-    if set(map(T.get_device, tensors)) != {device.index} or not all(map(T.is_contiguous, tensors)):
-        raise ValueError("gradients and outputs must be contiguous CUDA tensors on one device")
-    counts = array.array("q", map(T.numel, grads))
-    if outs is not grads and ([t.dtype for t in outs] != [t.dtype for t in grads] or array.array("q", map(T.numel, outs)) != counts):
-        raise ValueError("outputs must have their gradients' dtypes and numbers of elements")
+    if len(outs) != n:
+        raise ValueError(f"out must hold {n} tensors: {len(outs)}")
+    _, codes, pointers, to, counts = _tensor_lists().pairs(grads, outs)
     norm = torch.empty_strided((), (), dtype=torch.float32, device=device)
-    codes, pointers = array.array("i", codes), array.array("Q", map(T.data_ptr, grads))
-    to = pointers if outs is grads else array.array("Q", map(T.data_ptr, outs))
-    _run_on("ozaki_clip_grad_norm", (n, codes.buffer_info()[0], pointers.buffer_info()[0], to.buffer_info()[0], counts.buffer_info()[0],
-                                     float(max_norm), float(eps), norm.data_ptr()), workspace, None, device)
+    _run_on("ozaki_clip_grad_norm", (n, codes, pointers, to, counts, float(max_norm), float(eps), norm.data_ptr()), workspace, None, device)
     return norm
 
 

@@ -490,7 +490,7 @@ int ozaki_grouped_gemm_f8_wgrad(int n, int k, int rows, int groups, int type_dy,
  * feature), and y in OZ_E4M3 with OZ_BLOCK_ROW scales.  Elements of X, residual, W, H and Y are of dtype (OZ_BF16, OZ_F16 or
  * OZ_F32), any address and leading dimension; everything is computed in FP32 from the unrounded h and each output rounded once.
  *  - residual may be NULL (h = x).  H (k x rows, the sum, rounded) and Y (k x rows, y rounded) are written where not NULL;
- *    their leading dimensions are >= k in any case.  H may be X or residual.
+ *    their leading dimensions are >= k in any case.  H may be X or residual; nothing else may overlap.
  *  - Q, S as OZ_BLOCK_ROW's of ozaki_quantize_f8.  rstd: rows floats.
  *  - eps >= 0.  A token with Inf or NaN (or whose squares pass the range of FP32) gives NaN or zeros of its own; no
  *    other token sees it.  k <= OZ_MAX_NORM_WIDTH.  k or rows equal to 0: nothing is done. */
@@ -514,7 +514,8 @@ int ozaki_rms_norm_backward(int k, int rows, int dtype, const void* dY, int lddy
 /* norm = the 2-norm over all elements of `count` tensors, and outs[i] = grads[i] * min(1, max_norm / (norm + eps)) for each.
  * dtypes (OZ_BF16, OZ_F16 or OZ_F32 of tensor i and its output), grads, outs and counts (elements) are HOST arrays of `count` entries,
  * read before the call returns; the tensors are contiguous DEVICE memory and norm is one DEVICE float.
- *  - outs[i] may be grads[i] (in place: nothing is written where the factor is 1); otherwise they must not overlap.
+ *  - outs[i] may be grads[i] (in place: nothing is written where the factor is 1); otherwise they must not overlap.  No two
+ *    outputs may overlap (OZ_EINVAL): a tensor is listed once.
  *  - Squares are summed in FP32 32 at a time and in FP64 from there on, without overflow or underflow.
  *  - A norm of Inf makes the factor 0, one of NaN makes it NaN.  No tensor or element: norm 0.
  *  - count <= 40960, max_norm >= 0, eps >= 0.  The result does not depend on timing. */

@@ -151,6 +151,15 @@ def test_clip_refuses_bad_arguments(bad):
     assert clip(**bad) == oz.OZ_EINVAL
 
 
+def test_clip_refuses_outputs_that_meet():
+    f32, bf16 = oz.OZ_F32, oz.OZ_BF16
+    assert clip(counts=(5, 5), grads=[P, P]) == oz.OZ_EINVAL                                    # one tensor twice
+    assert clip(counts=(5, 5), grads=[P + 16, P]) == oz.OZ_EINVAL                               # its end in another's
+    assert clip(counts=(5, 5), dtypes=[bf16, f32], grads=[P + 64, P + 128], outs=[P, P + 8]) == oz.OZ_EINVAL
+    for fine in (dict(counts=(4, 5), grads=[P, P + 16]), dict(counts=(5, 4), grads=[P + 16, P]), dict(counts=(5, 0), grads=[P, P])):
+        assert clip(**fine, ws=None) == oz.OZ_ENOMEM  # past the checks of the tensors
+
+
 def test_clip_workspace():
     need = oz.ozaki_clip_grad_norm_workspace_bytes()
     assert clip(ws=None) == oz.OZ_ENOMEM and clip(nbytes=need - 1) == oz.OZ_ENOMEM and clip(ws=P + 8) == oz.OZ_ENOMEM
@@ -168,3 +177,19 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         oz.ozaki_quantize_f8(x, "tile")
     with pytest.raises(ValueError, match="no gradients"):
         oz.ozaki_clip_grad_norm([], 1.0)
+
+
+@pytest.mark.parametrize("lists, error", [
+    (([torch.zeros(3)], [torch.zeros(3)]), ValueError),  # not on a GPU
+    (([3], [3]), TypeError),
+    (([torch.zeros(3, dtype=torch.float64)], [None]), ValueError),
+    (((), ()), TypeError),                               # lists
+    (([],), TypeError),
+])
+def test_facts_of_tensors_refuse(lists, error):
+    with pytest.raises(error):
+        oz._tensor_lists().pairs(*lists)
+
+
+def test_facts_of_no_tensors():
+    assert oz._tensor_lists().pairs([], []) == (-1, b"", b"", b"", b"")

@@ -8,9 +8,10 @@
 //
 // Bound by memory: every row is read once, held in registers between its sum and its results, and written
 // once.  With many rows the CTAs stay, keep w in registers, and fetch their next row while they work on one: the
-// waits of a row (for its values, its sum's barrier) would otherwise follow each other.  Several threads share a row, eight neighbours each (a block of 128 is 16 threads); rows that do not
-// start at multiples of 16 bytes are read and written in 16-byte pieces too, shifted (7777 rows of 2049 bfloat16
-// values backward: 68 us with an access an element).
+// waits of a row (for its values, its sum's barrier) would otherwise follow each other (16384 rows of 4096 bfloat16 values
+// with a residual: 77 us, 6.1 TB/s; 127 with a CTA a row).  Several threads share a row, eight neighbours each (a block of
+// 128 is 16 threads); rows that do not start at multiples of 16 bytes are read and written in 16-byte pieces too, shifted
+// (7777 rows of 2049 bfloat16 values backward: 47 us, 2.7 TB/s; 68 with an access an element).
 #include "oz_elements.cuh"
 #include "oz_device.cuh"
 #include "oz_ragged.cuh"
@@ -157,11 +158,11 @@ struct Columns {
   long long step;     // elements from one of the CTA's rows to the next
   __device__ Columns(const void* p, long long ld, int rows, int k, int row, int step)
       : at(static_cast<const T*>(p) + row * ld), end(static_cast<const T*>(p) + (rows - 1) * ld + k), step(step * ld) {}
-  // Eight columns of that row from c on, without a mask: what is in columns outside [0, k) may be anything.  first: the
-  // matrix's first row, before which nothing is read.
-  __device__ Eight<T> load(int c, int k, bool first) const {
+  // Eight columns of that row from c on, without a mask: what is in columns outside [0, k) may be anything.  Nothing is read
+  // before the matrix's first element, which the columns before row 0 .. 6 may be (rows have a distance of at least 1).
+  __device__ Eight<T> load(int c, int k, int row) const {
     const T* from = at + c;
-    if (PIECES && ((c >= 0 && c + 8 <= k) || (c < k && !(first && c < 0) && from + 8 <= end))) return load_eight(from);
+    if (PIECES && ((c >= 0 && c + 8 <= k) || (c < k && (c >= 0 || row > 6) && from + 8 <= end))) return load_eight(from);
     return gather_eight(from, 1, [&](int e) { return c + e >= 0 && c + e < k; });
   }
 };
@@ -196,9 +197,9 @@ __global__ void __launch_bounds__(1024) norm_back_kernel(const __grid_constant__
     if (row >= a.rows) return;
 #pragma unroll
     for (int j = 0; j < RUNS; ++j) {
-      dy[j] = rdy.load(column(j), a.k, row == 0);
-      h[j] = rh.load(column(j), a.k, row == 0);
-      if (EARLY && a.dh) dh[j] = rdh.load(column(j), a.k, row == 0);
+      dy[j] = rdy.load(column(j), a.k, row);
+      h[j] = rh.load(column(j), a.k, row);
+      if (EARLY && a.dh) dh[j] = rdh.load(column(j), a.k, row);
     }
     r = a.rstd[row];
     rdy.at += rdy.step;
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(1024) norm_back_kernel(const __grid_constant__
   };
   if (EARLY) ask(row);
 #pragma unroll
-  for (int j = 0; j < RUNS; ++j) w[j] = Columns<T, false>(a.w, 0, 1, a.k, 0, 0).load(column(j), a.k, false);
+  for (int j = 0; j < RUNS; ++j) w[j] = Columns<T, false>(a.w, 0, 1, a.k, 0, 0).load(column(j), a.k, 0);
   for (; row < a.rows; row += step, turn ^= 1) {
     if (!EARLY) ask(row);
     float dot = 0.0f;
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(1024) norm_back_kernel(const __grid_constant__
 #pragma unroll
     for (int j = 0; j < RUNS; ++j) {
       const int c = column(j);
-      if (!EARLY && a.dh) dh1[j] = rdh.load(c, a.k, row == 0);
+      if (!EARLY && a.dh) dh1[j] = rdh.load(c, a.k, row);
       float dx[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {

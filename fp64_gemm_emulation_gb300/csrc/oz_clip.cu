@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(kThreads, kResident) scale_kernel(const __grid
   for (int i = threadIdx.x; i < a.all_sums; i += kThreads) all += __ldcg(a.sums + i);
   const float norm = static_cast<float>(sqrt(block_sum(all, meet)));
   float f = a.limit / (norm + a.eps);
-  if (f > 1.0f) f = 1.0f;  // NaN stays
+  // A NaN stays, but for 0 / 0 and Inf / Inf.
+  if (f > 1.0f || norm == 0.0f || (norm == a.limit && isinf(norm))) f = 1.0f;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
   for (long long i = blockIdx.x; i < a.chunks; i += gridDim.x) {
     const long long chunk = a.chunks - 1 - i;

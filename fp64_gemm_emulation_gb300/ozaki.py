@@ -1179,7 +1179,8 @@ def ozaki_clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None, wo
     min(1, max_norm / (norm + eps)): in place, or into the tensors of out.
 
     Tensors are contiguous, bfloat16, float16 or float32 (each its own), on one device; out has their dtypes and numbers of
-    elements, and each of its tensors is its gradient itself or does not overlap any.  A norm of Inf makes the factor 0, one of NaN makes it NaN."""
+    elements, and each of its tensors is its gradient itself or does not overlap any; no tensor is listed twice.  A norm of Inf
+    makes the factor 0, one of NaN makes it NaN; max_norm = inf only takes the norm."""
     torch = _torch()
     grads = list(grads)
     outs = grads if out is None else list(out)

@@ -492,8 +492,9 @@ int ozaki_grouped_gemm_f8_wgrad(int n, int k, int rows, int groups, int type_dy,
  *  - residual may be NULL (h = x).  H (k x rows, the sum, rounded) and Y (k x rows, y rounded) are written where not NULL;
  *    their leading dimensions are >= k in any case.  H may be X or residual; nothing else may overlap.
  *  - Q, S as OZ_BLOCK_ROW's of ozaki_quantize_f8.  rstd: rows floats.
- *  - eps >= 0.  A token with Inf or NaN (or whose squares pass the range of FP32) gives NaN or zeros of its own; no
- *    other token sees it.  k <= OZ_MAX_NORM_WIDTH.  k or rows equal to 0: nothing is done. */
+ *  - eps >= 0 (a token of zeros with eps = 0 gives NaN).  A token with Inf or NaN (or whose squares pass the range of FP32)
+ *    gives NaN or zeros of its own; no other token sees it.
+ *  - k <= OZ_MAX_NORM_WIDTH, rows <= 2^31 - 1 - 2^20.  k or rows equal to 0: nothing is done. */
 #define OZ_MAX_NORM_WIDTH 32768
 int ozaki_rms_norm_f8(int k, int rows, int dtype, const void* X, int ldx, const void* residual, int ldr, const void* W, float eps,
                       void* Q, int ldq, float* S, int lds, void* H, int ldh, float* rstd, void* Y, int ldy, cudaStream_t stream);
@@ -517,7 +518,8 @@ int ozaki_rms_norm_backward(int k, int rows, int dtype, const void* dY, int lddy
  *  - outs[i] may be grads[i] (in place: nothing is written where the factor is 1); otherwise they must not overlap.  No two
  *    outputs may overlap (OZ_EINVAL): a tensor is listed once.
  *  - Squares are summed in FP32 32 at a time and in FP64 from there on, without overflow or underflow.
- *  - A norm of Inf makes the factor 0, one of NaN makes it NaN.  No tensor or element: norm 0.
+ *  - A norm of Inf makes the factor 0, one of NaN makes it NaN.  A norm of 0 makes it 1, and so does max_norm = Inf (unless
+ *    the norm is NaN).  No tensor or element: norm 0.
  *  - count <= 40960, max_norm >= 0, eps >= 0.  The result does not depend on timing. */
 size_t ozaki_clip_grad_norm_workspace_bytes(void);
 int ozaki_clip_grad_norm_ws(int count, const int* dtypes, const void* const* grads, void* const* outs, const long long* counts,

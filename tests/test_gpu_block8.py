@@ -469,6 +469,19 @@ def test_clip_inf_and_nan():
     assert torch.isnan(oz.ozaki_clip_grad_norm([g, h], 1.0)) and torch.isnan(h).all()
 
 
+def test_clip_zeros_and_no_limit():
+    inf = float("inf")
+    for limit, eps in ((0.0, 0.0), (1.0, 0.0), (inf, 0.0), (inf, 1e-6)):  # 0 / 0 among them
+        g, out = [torch.zeros(1000, device="cuda")], [torch.full((1000,), 7.0, device="cuda")]
+        assert oz.ozaki_clip_grad_norm(g, limit, eps, out=out).item() == 0 and (out[0] == 0).all()
+    g = randn(1000)
+    g[3] = inf
+    keep = g.clone()
+    assert oz.ozaki_clip_grad_norm([g], inf).item() == inf and torch.equal(g, keep)  # Inf / Inf
+    g[4] = float("nan")
+    assert torch.isnan(oz.ozaki_clip_grad_norm([g], inf)) and torch.isnan(g).all()
+
+
 @pytest.mark.parametrize("workspace", [True, False])
 def test_clip_repeated_calls_agree(workspace):
     # back to back on one stream, their launches overlapping, each with its own tensors

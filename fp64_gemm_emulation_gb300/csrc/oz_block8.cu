@@ -39,6 +39,7 @@ constexpr uint32_t HALF8 = 64 * BK8;            // of the 64 n that a CTA holds 
 constexpr int ACC8 = 128;                       // columns of an accumulator; two for each half of the tile
 constexpr int EPI8_FIRST = 4, EPI8_WARPS = 8, THREADS8 = (EPI8_FIRST + EPI8_WARPS) * 32;
 constexpr int BLOCKS8 = ACC8 / 32;              // blocks of 32 columns whose sums a warp holds
+constexpr int EARLY8 = 3;                       // reads of 16 columns before the next accumulator's first
 // Registers: the four warps of the first warpgroup give theirs to the epilogue, whose threads hold 128 sums.
 // 128 x 72 + 256 x 216 = 384 x 168, what the launch has.
 constexpr int REGS_FEW = 72, REGS_MANY = 216;
@@ -524,6 +525,13 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
         acc_phase ^= 1;
       }
     };
+    // Whether the accumulator after this one is full by now: asked EARLY8 reads before the answer is needed, as a wait that
+    // is over at once takes 80 cycles of a k-block's 820 (8192 x 4096 x 8192: 224 us instead of 228; wgrad of 32768 rows
+    // and 16 groups, which waits for scales too: 386 instead of 405).
+    auto next_there = [&]() {
+      const bool turn = acc + halves >= 4;
+      return mbar_test_wait(&accfull[turn ? half : acc + halves], acc_phase ^ (turn ? 1u : 0u));
+    };
     if constexpr (OP != kWgrad8) {
       // The sums take nearly all registers: the walker is made anew for each tile, and where the tile goes waits in the
       // warp's stash.
@@ -575,12 +583,17 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
           uint32_t v[2][16];
           auto step = [&](float& x, float& w) {
             const float f = factor(x, w);
+            bool early = false;
 #pragma unroll
             for (int j = 0; j < 2 * BLOCKS8; ++j) {
               tmem_ld_wait();
+              if (j + EARLY8 == 2 * BLOCKS8) early = next_there();
               if (j + 1 == 2 * BLOCKS8) {
                 release();
-                if (--left > 0) sums_there();
+                if (--left > 0) {
+                  if (__all_sync(0xFFFFFFFFu, early)) tc_fence_after();
+                  else sums_there();
+                }
               }
               tmem_ld16(lanes + acc * ACC8 + 16 * ((j + 1) % (2 * BLOCKS8)), v[(j + 1) & 1]);
 #pragma unroll
@@ -674,8 +687,12 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
             tmem_ld_frag16(lanes + acc * ACC8, v[0]);
           }
           while (ok && left > 0) {
+            bool early = false;
 #pragma unroll
             for (int j = 0; j < 2 * BLOCKS8; ++j) {
+              if (j + EARLY8 == 2 * BLOCKS8) {
+                early = next_there() & mbar_test_wait(&sfull[slot + 1 == SLOTS8 ? 0 : slot + 1], sphase ^ (slot + 1 == SLOTS8 ? 1u : 0u));
+              }
               float2 s[2];
 #pragma unroll
               for (int q = 0; q < 2; ++q)
@@ -684,7 +701,10 @@ __global__ void __launch_bounds__(THREADS8, 1) block8_kernel(const __grid_consta
               if (j + 1 == 2 * BLOCKS8) {
                 release();
                 scales_done();
-                if (--left > 0 && scales_there()) sums_there();
+                if (--left > 0) {
+                  if (__all_sync(0xFFFFFFFFu, early)) tc_fence_after();
+                  else if (scales_there()) sums_there();
+                }
               }
               tmem_ld_frag16(lanes + acc * ACC8 + 16 * ((j + 1) % (2 * BLOCKS8)), v[(j + 1) & 1]);
 #pragma unroll

@@ -11,7 +11,7 @@
 // waits of a row (for its values, its sum's barrier) would otherwise follow each other (16384 rows of 4096 bfloat16 values
 // with a residual: 77 us, 6.1 TB/s; 127 with a CTA a row).  Several threads share a row, eight neighbours each (a block of
 // 128 is 16 threads); rows that do not start at multiples of 16 bytes are read and written in 16-byte pieces too, shifted
-// (7777 rows of 2049 bfloat16 values backward: 47 us, 2.7 TB/s; 68 with an access an element).
+// (7777 rows of 2049 bfloat16 values backward: 41 us, 3.1 TB/s; 68 with an access an element).
 #include "oz_elements.cuh"
 #include "oz_device.cuh"
 #include "oz_ragged.cuh"
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(STAY ? 256 : 1024, STAY ? (RUNS == 1 ? 4 : RUN
 
 // Gradients: a CTA takes every so many rows and keeps dw's sums of its columns in registers; the CTAs' sums go to
 // the workspace and are added in their order by a second launch, so results do not depend on timing.
-// With one run a thread the next row is fetched meanwhile (two and more leave no registers for it).
+// With one run a thread the next row is fetched into registers meanwhile (two and more leave none for it).
 //
 // Rows that do not start at multiples of 16 bytes: the rows whose starts lie alike against 16 bytes are every
 // `period`-th, and a CTA takes only such.  Its threads' eight columns then start `shift` elements before a multiple of
@@ -168,7 +168,7 @@ struct Columns {
 };
 
 template <class T, bool PIECES, int RUNS>
-__global__ void __launch_bounds__(1024) norm_back_kernel(const __grid_constant__ NormBackParams a) {
+__global__ void __launch_bounds__(1024, 1) norm_back_kernel(const __grid_constant__ NormBackParams a) {
   constexpr bool EARLY = RUNS == 1;
   __shared__ float meet[2][32];
   let_next_start();
@@ -264,6 +264,142 @@ __global__ void __launch_bounds__(1024) norm_back_kernel(const __grid_constant__
   }
 }
 
+// The same for 16-bit elements where all accesses are whole pieces, rows of at most two runs: a CTA's next two rows are on
+// their way into shared memory, where each thread finds its own pieces again (so no barrier is needed), twice: for the
+// sum, and behind the barrier for dx, so that a row takes no registers meanwhile.  (FP32: a thread's two pieces are
+// neighbours, and copied apart they use half of each sector: 8192 x 4096 141 us instead of 108.)
+// Against a row ahead in registers: 16384 x 4096 with dh 116 -> 90 us (6.0 TB/s), 4096 x 16384 288 -> 90, 7777 x 2049 46 -> 41.
+// EDGES: pieces that are not whole columns of the row exist (compiled in, their code costs rows without them a fifth:
+// 16384 x 4096 117 us).
+constexpr int kRowsAhead = 2;
+template <class T, int RUNS, bool EDGES>
+__global__ void __maxnreg__(RUNS == 1 && EDGES ? 56 : 64) norm_back_staged_kernel(const __grid_constant__ NormBackParams a) {
+  static_assert(sizeof(T) == 2, "a run is one piece");
+  extern __shared__ uint4 staged[];  // [kRowsAhead][dy, h, dh][RUNS][threads]
+  __shared__ float meet[2][32];
+  let_next_start();
+  wait_for_previous();
+  const int threads = blockDim.x, matrix = RUNS * threads, slot_size = (a.dh ? 3 : 2) * matrix;
+  const int kind = EDGES ? static_cast<int>(blockIdx.x) % a.period : 0;  // rows kind, kind + period, ...
+  const int shift = !EDGES ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(a.dy) + kind * a.lddy * sizeof(T)) & 15) / static_cast<int>(sizeof(T));
+  const int step = a.period * ((static_cast<int>(gridDim.x) - kind + a.period - 1) / a.period);  // (CTAs of this kind)
+  auto column = [&](int j) { return first_column(j) - shift; };
+  float dw[RUNS][8];
+#pragma unroll
+  for (int i = 0; i < RUNS * 8; ++i) dw[i >> 3][i & 7] = 0.0f;
+  Eight<T> w[RUNS];
+#pragma unroll
+  for (int j = 0; j < RUNS; ++j)
+    w[j] = gather_eight(static_cast<const T*>(a.w) + column(j), 1, [&](int e) { return column(j) + e >= 0 && column(j) + e < a.k; });
+
+  // This thread's piece of run j of a row into its place.  A row's first and last piece may reach into its neighbours (their
+  // elements are made zeros when the piece has arrived), but not out of the matrix: before row 0 .. 6 or behind the last
+  // one (rows have a distance of at least 1) it is gathered.
+  auto fill = [&](const void* p, long long ld, int row, int j, uint4* to) {
+    const int c = column(j);
+    const T* from = static_cast<const T*>(p) + row * ld + c;
+    if (EDGES ? (c >= 0 && c + 8 <= a.k) || (c < a.k && (c >= 0 || row > 6) && (a.rows - 1 - row) * ld + a.k >= c + 8) : c < a.k) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+    } else if (EDGES && c < a.k) {
+      const Eight<T> v = gather_eight(from, 1, [&](int e) { return c + e >= 0 && c + e < a.k; });
+      *to = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    }
+  };
+  auto send = [&](int row, uint4* to) {
+    if (row < a.rows) {
+#pragma unroll
+      for (int j = 0; j < RUNS; ++j) {
+        fill(a.dy, a.lddy, row, j, to + j * threads);
+        fill(a.h, a.ldh, row, j, to + matrix + j * threads);
+        if (a.dh) fill(a.dh, a.lddh, row, j, to + 2 * matrix + j * threads);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto take = [&](const uint4* from) {
+    const uint4 x = *from;
+    Eight<T> v;
+    v.w[0] = x.x, v.w[1] = x.y, v.w[2] = x.z, v.w[3] = x.w;
+    return v;
+  };
+  int row = kind + a.period * (static_cast<int>(blockIdx.x) / a.period), turn = 0;
+  uint4* slot = staged + threadIdx.x;
+#pragma unroll
+  for (int j = 0; j < RUNS; ++j) {
+    if (column(j) < a.k) continue;  // behind the rows: never filled
+    for (int i = j * threads; i < kRowsAhead * slot_size; i += matrix) slot[i] = make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < kRowsAhead; ++i) send(row + i * step, slot + i * slot_size);
+  float r = row < a.rows ? a.rstd[row] : 0.0f;
+  for (; row < a.rows; row += step, turn ^= 1) {
+    const float rs = r;
+    if (row + step < a.rows) r = a.rstd[row + step];
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRowsAhead - 1) : "memory");
+#pragma unroll
+    for (int j = 0; j < RUNS; ++j) {
+      const int c = column(j);
+      if (EDGES && c < a.k && (c < 0 || c + 8 > a.k)) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          uint4* at = slot + m * matrix + j * threads;
+          Eight<T> v = take(at);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (c + 2 * i < 0 || c + 2 * i >= a.k) v.w[i] &= 0xFFFF0000u;
+            if (c + 2 * i + 1 < 0 || c + 2 * i + 1 >= a.k) v.w[i] &= 0xFFFFu;
+          }
+          *at = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+        }
+      }
+    }
+    float dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < RUNS; ++j) {
+      const Eight<T> dy = take(slot + j * threads), h = take(slot + matrix + j * threads);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dot = fmaf(dy.get(e) * w[j].get(e), h.get(e), dot);
+        dw[j][e] = fmaf(dy.get(e) * rs, h.get(e), dw[j][e]);
+      }
+    }
+    // Two rooms in turn: a warp writes one again only after the other's barrier.
+    dot = row_sum(dot, meet[turn]) / static_cast<float>(a.k);
+    const float f = rs * rs * dot;
+#pragma unroll
+    for (int j = 0; j < RUNS; ++j) {
+      const int c = column(j);
+      const Eight<T> dy = take(slot + j * threads), h = take(slot + matrix + j * threads);
+      float dx[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dx[e] = rs * (dy.get(e) * w[j].get(e) - h.get(e) * f);
+      if (a.dh) {
+        const Eight<T> dh = take(slot + 2 * matrix + j * threads);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dx[e] += dh.get(e);
+      }
+      T* to = static_cast<T*>(a.dx) + row * a.lddx + c;
+      if (EDGES ? c >= 0 && c + 8 <= a.k : c < a.k) {
+        store_eight(to, dx);
+      } else if (EDGES) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e >= 0 && c + e < a.k) from_float(dx[e], to[e]);
+      }
+    }
+    send(row + kRowsAhead * step, slot);
+    slot = slot == staged + threadIdx.x ? slot + slot_size : slot - slot_size;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  float* part = a.part + static_cast<long long>(blockIdx.x) * a.k;
+#pragma unroll
+  for (int j = 0; j < RUNS; ++j) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (column(j) + e >= 0 && column(j) + e < a.k) part[column(j) + e] = dw[j][e];
+  }
+}
+
 // dw: 32 columns a CTA, 8 warps each a run of parts, added in order.
 template <class T>
 __global__ void __launch_bounds__(256) norm_weight_kernel(const float* part, int parts, int k, T* dw) {
@@ -343,12 +479,30 @@ cudaError_t norm_of_type(const NormParams& a, int sms, cudaStream_t stream) {
   return vec ? launch_norm<T, true>(a, sms, stream) : launch_norm<T, false>(a, sms, stream);
 }
 
+// CTAs of the backward pass: as many as run at once on 152 SMs (at most 64 registers a thread, staged 56: 7777 rows of 2049
+// take four CTAs of 288 threads instead of three).
+int parts_of(int rows, int k, bool staged = true) {
+  const int threads = shape_of(k, true).threads, most = 152 * (threads >= 128 ? (staged ? 1152 : 1024) / threads : 8);
+  return rows < most ? rows : most;
+}
+
 template <class T, bool PIECES>
-cudaError_t launch_norm_back(const NormBackParams& a, cudaStream_t stream) {
+cudaError_t launch_norm_back(NormBackParams& a, cudaStream_t stream) {
   // (one row a CTA; a shift takes up to seven columns more)
   const bool shifted = PIECES && (a.period > 1 || (reinterpret_cast<uintptr_t>(a.dy) & 15));
   const Shape s = shape_of(shifted ? a.k + 7 : a.k, true);
-  auto kernel = s.runs == 1 ? norm_back_kernel<T, PIECES, 1> : s.runs == 2 ? norm_back_kernel<T, PIECES, 2> : norm_back_kernel<T, PIECES, 4>;
+  if constexpr (PIECES && sizeof(T) == 2) {
+    if (s.runs <= 2) {
+      auto kernel = shifted || a.k % 8 ? (s.runs == 1 ? norm_back_staged_kernel<T, 1, true> : norm_back_staged_kernel<T, 2, true>)
+                                       : (s.runs == 1 ? norm_back_staged_kernel<T, 1, false> : norm_back_staged_kernel<T, 2, false>);
+      const int smem = kRowsAhead * (a.dh ? 3 : 2) * s.runs * 16 * s.threads;
+      const cudaError_t e = smem > 48000 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
+      return e != cudaSuccess ? e : launch_overlapping(kernel, dim3(a.parts), s.threads, smem, stream, a);
+    }
+  }
+  a.parts = parts_of(a.rows, a.k, false);
+  auto kernel = norm_back_kernel<T, PIECES, 4>;
+  if constexpr (!(PIECES && sizeof(T) == 2)) kernel = s.runs == 1 ? norm_back_kernel<T, PIECES, 1> : s.runs == 2 ? norm_back_kernel<T, PIECES, 2> : kernel;
   return launch_overlapping(kernel, dim3(a.parts), s.threads, 0, stream, a);
 }
 
@@ -368,12 +522,6 @@ cudaError_t norm_back_of_type(NormBackParams a, cudaStream_t stream) {
   const cudaError_t e = pieces ? launch_norm_back<T, true>(a, stream) : launch_norm_back<T, false>(a, stream);
   if (e != cudaSuccess) return e;
   return launch_overlapping(norm_weight_kernel<T>, dim3((a.k + 31) / 32), 256, 0, stream, a.part, a.parts, a.k, static_cast<T*>(a.dw));
-}
-
-// CTAs of the backward pass: as many as run at once on 152 SMs (at most 64 registers a thread).
-int parts_of(int rows, int k) {
-  const int threads = shape_of(k, true).threads, most = 152 * (threads >= 128 ? 1024 / threads : 8);
-  return rows < most ? rows : most;
 }
 
 int check_back(int k, int rows, int dtype, long long lddy, long long ldh, long long lddh, long long lddx) {

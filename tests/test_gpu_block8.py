@@ -355,6 +355,34 @@ def test_norm_backward(rows, k, dtype, with_dh):
     assert ((dw.double() - z.sum(0)).abs() <= HALF[dtype] * z.sum(0).abs() + (rows + 4) * 2.0 ** -24 * (1 + HALF[dtype]) * z.abs().sum(0) + TINY[dtype]).all()
 
 
+# many rows a CTA (they are fetched ahead): whole pieces, rows that start anywhere, one and two runs a thread, several rows in 16 bytes
+@pytest.mark.parametrize("rows, k, pad", [(2600, 520, 0), (2600, 513, 0), (5000, 3, 0), (5000, 1, 0), (1500, 4096, 8), (1500, 4095, 3), (500, 8200, 0), (500, 8193, 1), (400, 16384, 0)])
+def test_norm_backward_of_many_rows(rows, k, pad):
+    dtype = torch.bfloat16
+    dy, h, dh = (torch.full((rows * (k + pad) + 9,), float("nan"), dtype=dtype, device="cuda")[1:1 + rows * (k + pad)].view(rows, k + pad)[:, :k] if k % 8 else
+                 torch.full((rows, k + pad), float("nan"), dtype=dtype, device="cuda")[:, :k] for _ in range(3))
+    for i, t in enumerate((dy, h, dh)):
+        t.copy_(randn(rows, k, dtype=dtype, seed=i))
+        t[5::7] = float("nan")  # each row's neighbours
+    w = (1 + randn(k, seed=4, scale=0.2)).to(dtype)
+    rstd = 1 + torch.rand(rows, generator=torch.Generator().manual_seed(1)).cuda()
+    keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+    keep[5::7] = False
+    H, W, D, r = h[keep].double(), w.double(), dy[keep].double(), rstd[keep].double()[:, None]
+    g = D * W
+    want = r * (g - H * r.square() * (g * H).mean(1, keepdim=True)) + dh[keep].double()
+    mag = r * (g.abs() + H.abs() * r.square() * (g * H).abs().mean(1, keepdim=True)) + dh[keep].double().abs()
+    for to in (None, dh):  # into dH itself at last
+        dx, _ = oz.ozaki_rms_norm_backward(dy, h, w, rstd, dh, dX=to)
+        assert ((dx[keep].double() - want).abs() <= HALF[dtype] * want.abs() + 2.0 ** -17 * mag + TINY[dtype]).all()
+        assert torch.isnan(dx[~keep]).all()
+    for t in (dy, h):
+        t[5::7] = 0
+    _, dw = oz.ozaki_rms_norm_backward(dy, h, w, rstd)
+    z = dy.double() * h.double() * rstd.double()[:, None]
+    assert ((dw.double() - z.sum(0)).abs() <= HALF[dtype] * z.sum(0).abs() + (rows + 4) * 2.0 ** -24 * (1 + HALF[dtype]) * z.abs().sum(0) + TINY[dtype]).all()
+
+
 def test_norm_backward_is_the_derivative():
     # differences of the loss sum(c y) + sum(d h) in 64 bits
     rows, k = 6, 200

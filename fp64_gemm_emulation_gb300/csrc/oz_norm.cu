@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(1024, 1) norm_back_kernel(const __grid_constan
 // 16384 x 4096 117 us).
 constexpr int kRowsAhead = 2;
 template <class T, int RUNS, bool EDGES>
-__global__ void __maxnreg__(RUNS == 1 && EDGES ? 56 : 64) norm_back_staged_kernel(const __grid_constant__ NormBackParams a) {
+__global__ void __launch_bounds__(1024, 1) norm_back_staged_kernel(const __grid_constant__ NormBackParams a) {
   static_assert(sizeof(T) == 2, "a run is one piece");
   extern __shared__ uint4 staged[];  // [kRowsAhead][dy, h, dh][RUNS][threads]
   __shared__ float meet[2][32];
@@ -479,15 +479,15 @@ cudaError_t norm_of_type(const NormParams& a, int sms, cudaStream_t stream) {
   return vec ? launch_norm<T, true>(a, sms, stream) : launch_norm<T, false>(a, sms, stream);
 }
 
-// CTAs of the backward pass: as many as run at once on 152 SMs (at most 64 registers a thread, staged 56: 7777 rows of 2049
-// take four CTAs of 288 threads instead of three).
-int parts_of(int rows, int k, bool staged = true) {
-  const int threads = shape_of(k, true).threads, most = 152 * (threads >= 128 ? (staged ? 1152 : 1024) / threads : 8);
+// CTAs of the backward pass: as many as run at once on 152 SMs (at most 64 registers a thread; with 56 four CTAs of 7777 rows of
+// 2049 fit instead of three, which leaves the next launch's no room: 54 us a call instead of 41).
+int parts_of(int rows, int k) {
+  const int threads = shape_of(k, true).threads, most = 152 * (threads >= 128 ? 1024 / threads : 8);
   return rows < most ? rows : most;
 }
 
 template <class T, bool PIECES>
-cudaError_t launch_norm_back(NormBackParams& a, cudaStream_t stream) {
+cudaError_t launch_norm_back(const NormBackParams& a, cudaStream_t stream) {
   // (one row a CTA; a shift takes up to seven columns more)
   const bool shifted = PIECES && (a.period > 1 || (reinterpret_cast<uintptr_t>(a.dy) & 15));
   const Shape s = shape_of(shifted ? a.k + 7 : a.k, true);
@@ -500,7 +500,6 @@ cudaError_t launch_norm_back(NormBackParams& a, cudaStream_t stream) {
       return e != cudaSuccess ? e : launch_overlapping(kernel, dim3(a.parts), s.threads, smem, stream, a);
     }
   }
-  a.parts = parts_of(a.rows, a.k, false);
   auto kernel = norm_back_kernel<T, PIECES, 4>;
   if constexpr (!(PIECES && sizeof(T) == 2)) kernel = s.runs == 1 ? norm_back_kernel<T, PIECES, 1> : s.runs == 2 ? norm_back_kernel<T, PIECES, 2> : kernel;
   return launch_overlapping(kernel, dim3(a.parts), s.threads, 0, stream, a);

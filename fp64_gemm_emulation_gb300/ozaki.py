@@ -1169,8 +1169,10 @@ def ozaki_rms_norm_backward_workspace_bytes(k: int, rows: int) -> int:
 # ------------------------------------------------------------------ clipping by the global norm
 def _tensor_lists():
     """The module that gathers what the library wants to know of many tensors (built beside it; it needs torch)."""
-    from . import _tensor_lists
-
+    try:
+        from . import _tensor_lists
+    except ImportError as e:
+        raise ImportError("_tensor_lists.so is missing: build it with `python -m fp64_gemm_emulation_gb300.build_lib`") from e
     return _tensor_lists
 
 

@@ -233,16 +233,42 @@ __device__ __forceinline__ float scale_of(uint32_t amax) {
   return s < 1.17549435e-38f ? 1.17549435e-38f : s;
 }
 
-// Eight values times 1 / scale, to the nearest 8-bit ones (largest values stay finite; NaN stays NaN).  The
-// product with the reciprocal is within 2^-23 of the quotient, so a value that near to the middle
-// between two 8-bit ones may go to either.
+// The quotient a / b, a > 0, as y + rest: y below it by at most 6 steps, rest >= 0 what it lacks, so that v y + v rest, rounded
+// once, is v a / b within 2^-40 before that.  (rest >= 0: a v of -0 stays one.)  Where y is below 2^-100, rest is below the
+// normal range: then within 2^-29.  A b of Inf gives zeros, a NaN NaN.
+struct Quotient {
+  float y, rest;
+};
+// near: within 2^-23 of b / a.  (With the division's rounding 3 / 2 of that, 3 steps at most.)
+__device__ __forceinline__ Quotient quotient_of(float a, float b, float near) {
+  const float y = __uint_as_float(max(__float_as_uint(1.0f / near), 3u) - 3u);
+  return {y, y == 0.0f ? 0.0f : fmaf(-y, b, a) * (y * (1.0f / a))};
+}
+// What a block's values are multiplied by: one over its scale before that was rounded, so that a 16-bit value in the middle
+// between two 8-bit ones is found there.
 template <bool E5M2>
-__device__ __forceinline__ uint2 eight_bits(const float (&v)[8], float inverse) {
+__device__ __forceinline__ Quotient inverse_of(uint32_t amax, float scale) {
+  constexpr float LARGEST = E5M2 ? 57344.0f : 448.0f;
+  const float v = __uint_as_float(amax);
+  const bool exact = v >= LARGEST * 1.17549435e-38f && v <= 3.40282347e38f;
+  return quotient_of(exact ? LARGEST : 1.0f, exact ? v : scale, scale);
+}
+
+// v times the quotient r, rounded to FP32 once.
+__device__ __forceinline__ float times(float v, Quotient r) { return fmaf(v, r.y, v * r.rest); }
+
+// Eight values times quotients (r(e): of value e), to the nearest 8-bit ones (largest values stay finite; NaN stays NaN).
+template <bool E5M2, class R>
+__device__ __forceinline__ uint2 eight_bits(const float (&v)[8], R r) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * inverse, v[2 * i + 1] * inverse), __NV_SATFINITE, E5M2 ? __NV_E5M2 : __NV_E4M3);
+    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(times(v[2 * i], r(2 * i)), times(v[2 * i + 1], r(2 * i + 1))), __NV_SATFINITE, E5M2 ? __NV_E5M2 : __NV_E4M3);
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+template <bool E5M2>
+__device__ __forceinline__ uint2 eight_bits(const float (&v)[8], Quotient r) {
+  return eight_bits<E5M2>(v, [&](int) { return r; });
 }
 
 // Whether rows of T from p on, ld apart, all start at multiples of 16 bytes.

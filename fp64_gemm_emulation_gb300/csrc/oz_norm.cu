@@ -3,13 +3,12 @@
 //
 //   forward   h = x + residual,  r = 1 / sqrt(mean(h^2) + eps),  y = h r w   -> q, scales (of y), h, r; y if wanted
 //   backward  g = dy w,  dx = dh + r (g - h r^2 mean(g h)),  dw = sum over rows of dy h r
-// All in FP32: y is quantised (and rounded, where wanted) from the FP32 sum h, not from the stored one, so each
-// output is rounded once.
+// All in FP32, from the FP32 sum h, not from the stored one; q is rounded from the ratio of h w to its block's largest.
 //
 // Bound by memory: every row is read once, held in registers between its sum and its results, and written
 // once.  With many rows the CTAs stay, keep w in registers, and fetch their next row while they work on one: the
 // waits of a row (for its values, its sum's barrier) would otherwise follow each other (16384 rows of 4096 bfloat16 values
-// with a residual: 77 us, 6.1 TB/s; 127 with a CTA a row).  Several threads share a row, eight neighbours each (a block of
+// with a residual: 79 us, 5.9 TB/s; 127 with a CTA a row).  Several threads share a row, eight neighbours each (a block of
 // 128 is 16 threads); rows that do not start at multiples of 16 bytes are read and written in 16-byte pieces too, shifted
 // (7777 rows of 2049 bfloat16 values backward: 41 us, 3.1 TB/s; 68 with an access an element).
 #include "oz_elements.cuh"
@@ -70,6 +69,9 @@ struct Rows {
   __device__ Eight<T> fetch(int row, int c) const { return fetch_eight<T, VEC>(first + row * ld, c, row < rows ? k : 0, first, end); }
 };
 
+// q is y / scale, in which r cancels: 448 h w / (the block's largest |h w|), so that the roundings of r, of the scale and of h r
+// do not come before the one to 8 bits (with two 16-bit summands h w often is exact).  h is multiplied by r's power of two
+// all the same, which rounds nothing, so that h w leaves the range of FP32 only where y does.
 // RUNS: runs of eight elements a thread holds.  blockDim (threads of a row, rows).  STAY: a CTA takes every
 // gridDim.x-th group of rows, at most 256 threads; otherwise one.
 template <class T, bool VEC, int RUNS, bool STAY>
@@ -115,22 +117,47 @@ __global__ void __launch_bounds__(STAY ? 256 : 1024, STAY ? (RUNS == 1 ? 4 : RUN
     sum = row_sum(sum, meet[turn]);
     const float r = 1.0f / sqrtf(sum / static_cast<float>(a.k) + a.eps);
     if (threadIdx.x == 0) a.rstd[row] = r;
-    uint8_t* q = a.q + row * a.ldq;
+    const uint32_t bits = __float_as_uint(r);
+    const float power = r < __int_as_float(0x7F800000) ? __uint_as_float(bits & 0x7F800000u) : r, mantissa = __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u);
+    // The largest |h w| of each run's block, which 16 lanes hold.
+    uint32_t most[RUNS];
 #pragma unroll
     for (int j = 0; j < RUNS; ++j) {
       const int c = first_column(j);
       if (a.h) store_eight_of_row<T, VEC>(static_cast<T*>(a.h) + row * a.ldh, c, a.k, h[j]);
+      most[j] = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[j][e] = h[j][e] * r * w[j].get(e);
-      float (&y)[8] = h[j];
-      if (a.y) store_eight_of_row<T, VEC>(static_cast<T*>(a.y) + row * a.ldy, c, a.k, y);
-      uint32_t most = 0;  // 16 lanes hold a block
+      for (int e = 0; e < 8; ++e) {
+        h[j][e] = h[j][e] * power * w[j].get(e);
+        most[j] = max(most[j], c + e < a.k ? magnitude(h[j][e]) : 0u);
+      }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) most = max(most, c + e < a.k ? magnitude(y[e]) : 0u);
+      for (int d = 1; d < 16; d <<= 1) most[j] = max(most[j], __shfl_xor_sync(0xFFFFFFFFu, most[j], d));
+    }
+    // A lane works out the scale of one run's block.
+    const int mine = lane & (RUNS - 1);
+    uint32_t amax = most[0];
 #pragma unroll
-      for (int d = 1; d < 16; d <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
-      const float scale = scale_of<false>(most);
-      const uint2 v = eight_bits<false>(y, 1.0f / scale);
+    for (int j = 1; j < RUNS; ++j) amax = mine == j ? most[j] : amax;
+    const float top = __uint_as_float(amax), scale = scale_of<false>(magnitude(top * mantissa));
+    const bool least = !(top >= 448.0f * 1.17549435e-38f), exact = !least && top <= 3.40282347e38f;  // least: the smallest scales, and 1; NaN too
+    const Quotient inverse = quotient_of(exact ? 448.0f : 1.0f, exact ? top : scale, exact ? top * (1.0f / 448.0f) : scale);
+    const bool any_least = __any_sync(0xFFFFFFFFu, least);
+    const int block = 8 * ((static_cast<int>(threadIdx.x) & ~15) + mine * static_cast<int>(blockDim.x));
+    if ((lane & 15) < RUNS && block < a.k) a.s[block / kScaleBlock * a.lds + row] = scale;
+    uint8_t* q = a.q + row * a.ldq;
+#pragma unroll
+    for (int j = 0; j < RUNS; ++j) {
+      const int c = first_column(j), from = (lane & 16) | j;
+      const Quotient by = {__shfl_sync(0xFFFFFFFFu, inverse.y, from), __shfl_sync(0xFFFFFFFFu, inverse.rest, from)};
+      float to_y = mantissa;
+      if (any_least) {
+        const float f = __shfl_sync(0xFFFFFFFFu, least ? mantissa : 1.0f, from);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[j][e] *= f;
+        if (f != 1.0f) to_y = 1.0f;
+      }
+      const uint2 v = eight_bits<false>(h[j], by);
       if (c + 8 <= a.k) {
         *reinterpret_cast<uint2*>(q + c) = v;
       } else {
@@ -138,7 +165,11 @@ __global__ void __launch_bounds__(STAY ? 256 : 1024, STAY ? (RUNS == 1 ? 4 : RUN
         for (int e = 0; e < 8; ++e)
           if (c + e < a.k) q[c + e] = static_cast<uint8_t>(e < 4 ? v.x >> (8 * e) : v.y >> (8 * (e - 4)));
       }
-      if ((lane & 15) == 0 && c < a.k) a.s[c / kScaleBlock * a.lds + row] = scale;
+      if (a.y) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[j][e] *= to_y;
+        store_eight_of_row<T, VEC>(static_cast<T*>(a.y) + row * a.ldy, c, a.k, h[j]);
+      }
     }
   }
 }

@@ -10,8 +10,9 @@
 // Three CTAs of such threads fit an SM, and what they have asked for of 16-bit tiles while they work on one does not
 // keep the memory busy: 16-bit elements (FP32 tiles are twice as large) are copied into shared memory two tiles ahead,
 // where each thread finds its own eight 16-byte pieces again, so that no barrier is needed.
-// Measured: 8 x 2048 x 4096 FP32 in matrix blocks 52 us (6.4 TB/s); 16384 x 4096 bfloat16 in both 56 us (4.9 TB/s: the
-// instructions of two conversions an element bound it, 63,000 a scheduler).
+// Measured: 8 x 2048 x 4096 FP32 in matrix blocks 53 us (6.3 TB/s); 16384 x 4096 bfloat16 in both 62 us (4.4 TB/s: the
+// instructions of two conversions an element bound it; 56 us with one product a conversion instead of a product and a sum,
+// which sent values in the middle between two 8-bit ones to either).
 #include <atomic>
 #include <type_traits>
 
@@ -97,14 +98,19 @@ constexpr int kAhead = 2;  // tiles on their way into shared memory
 constexpr int kTileBytes16 = TILE * TILE * 2;
 
 // BLOCK: an OZ_BLOCK_*.  ALIGNED: rows at multiples of 16 bytes.
+// CTAs of an SM: three of 16-bit tiles in shared memory; two hold their tile in 128 registers a thread, but for both blocks at once and
+// for shifted pieces.
+constexpr int resident_ctas(int block, bool aligned, bool ahead) {
+  return ahead ? 3 : block == OZ_BLOCK_BOTH || (!aligned && block != OZ_BLOCK_COLUMN) ? 1 : 2;
+}
 template <class T, int BLOCK, bool E5M2, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads, ALIGNED && sizeof(T) == 2 ? 3 : 1) quantize_kernel(const __grid_constant__ QuantParams a) {
+__global__ void __launch_bounds__(kThreads, resident_ctas(BLOCK, ALIGNED, ALIGNED && sizeof(T) == 2)) quantize_kernel(const __grid_constant__ QuantParams a) {
   constexpr bool ROW = BLOCK == OZ_BLOCK_ROW || BLOCK == OZ_BLOCK_BOTH, COLUMN = BLOCK == OZ_BLOCK_COLUMN || BLOCK == OZ_BLOCK_BOTH;
   constexpr bool MATRIX = BLOCK == OZ_BLOCK_MATRIX, AHEAD = ALIGNED && sizeof(T) == 2;
   extern __shared__ uint4 ahead[];  // [kAhead][8][kThreads]
   __shared__ int off[COLUMN ? OZ_MAX_GROUPS + 1 : 1];
   __shared__ uint32_t most[kThreads / 32][TILE];
-  __shared__ __align__(16) float inverses[COLUMN ? TILE : 4];
+  __shared__ __align__(16) float inverses[2][COLUMN ? TILE : 4];  // y, rest
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c8 = 8 * (threadIdx.x & 15), r0 = threadIdx.x >> 4;
   let_next_start();
@@ -172,21 +178,24 @@ __global__ void __launch_bounds__(kThreads, ALIGNED && sizeof(T) == 2 ? 3 : 1) q
       send(tile + kAhead * gridDim.x, slot);
       slot = slot + 1 == kAhead ? 0 : slot + 1;
     }
-    // What make hands to its second argument for each i, to this thread's columns of row `first` + r0 + 16 i, of which
-    // `rows` exist.  Called by whole warps.
-    const bool whole_columns = c - c8 + TILE <= a.k;
+    // What make returns for each i, to this thread's columns of row `first` + r0 + 16 i, of which `rows` exist.  Called by whole
+    // warps.
     auto put_rows = [&](uint8_t* q, long long ld, long long first, int rows, auto make) {
-      uint8_t* to = q + (first + r0) * ld;
-      if (whole_columns && rows == TILE) {
+      uint8_t* to = q + (first + r0) * ld + c;
+      if (c - c8 + TILE <= a.k && rows == TILE) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i, to += 16 * ld) make(i, [&](uint2 w) { *reinterpret_cast<uint2*>(to + c) = w; });
+        for (int i = 0; i < 8; ++i, to += 16 * ld) *reinterpret_cast<uint2*>(to) = make(i);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i, to += 16 * ld)
-          make(i, [&](uint2 w) {
-            if (r0 + 16 * i < rows) put_bytes(to, c, a.k, w);
-          });
+        for (int i = 0; i < 8; ++i, to += 16 * ld) {
+          const uint2 w = make(i);
+          if (r0 + 16 * i < rows) put_bytes(to - c, c, a.k, w);
+        }
       }
+    };
+    auto unpack = [&](int i, float (&f)[8]) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = v[i].get(e);
     };
     if (ROW) {
       // The maxima of eight rows over 16 lanes: exchanged so that after three steps a lane holds one row's over eight
@@ -200,18 +209,19 @@ __global__ void __launch_bounds__(kThreads, ALIGNED && sizeof(T) == 2 ? 3 : 1) q
           by_row[i] = max(keep, __shfl_xor_sync(0xFFFFFFFFu, give, half));
         }
       }
-      const float scale = scale_of<E5M2>(raw_magnitude<T>(max(by_row[0], __shfl_xor_sync(0xFFFFFFFFu, by_row[0], 8)))), inverse = 1.0f / scale;
+      const uint32_t amax = raw_magnitude<T>(max(by_row[0], __shfl_xor_sync(0xFFFFFFFFu, by_row[0], 8)));
+      const float scale = scale_of<E5M2>(amax);
+      const Quotient inverse = inverse_of<E5M2>(amax, scale);
       const int mine = r0 + 16 * (lane & 7);  // this lane's row
       if ((lane & 8) == 0 && mine < count) a.s[c / TILE * a.lds + row + mine] = scale;
-      put_rows(a.q, a.ldq, row, count, [&](int i, auto store) {
-        const float by = __shfl_sync(0xFFFFFFFFu, inverse, (lane & 16) | i);
+      put_rows(a.q, a.ldq, row, count, [&](int i) {
+        const Quotient by = {__shfl_sync(0xFFFFFFFFu, inverse.y, (lane & 16) | i), __shfl_sync(0xFFFFFFFFu, inverse.rest, (lane & 16) | i)};
         float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = v[i].get(e);
-        store(eight_bits<E5M2>(f, by));
+        unpack(i, f);
+        return eight_bits<E5M2>(f, by);
       });
     }
-    if (COLUMN) {
+    if constexpr (COLUMN) {
 #pragma unroll
       for (int e = 0; e < 8 / PAIRS; ++e) by_col[e] = larger<T>(by_col[e], __shfl_xor_sync(0xFFFFFFFFu, by_col[e], 16));
       if (lane < 16) {
@@ -223,24 +233,27 @@ __global__ void __launch_bounds__(kThreads, ALIGNED && sizeof(T) == 2 ? 3 : 1) q
         uint32_t m = 0;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) m = max(m, static_cast<uint32_t>(reinterpret_cast<const typename Bits<T>::Raw*>(most[w])[threadIdx.x]));
-        const float scale = scale_of<E5M2>(raw_magnitude<T>(m));
-        inverses[threadIdx.x] = 1.0f / scale;
+        m = raw_magnitude<T>(m);
+        const float scale = scale_of<E5M2>(m);
+        const Quotient inverse = inverse_of<E5M2>(m, scale);
+        inverses[0][threadIdx.x] = inverse.y;
+        inverses[1][threadIdx.x] = inverse.rest;
         const int column = c - c8 + static_cast<int>(threadIdx.x);
         if (column < a.k) a.sc[block * a.ldsc + column] = scale;
       }
       __syncthreads();
-      float inverse[8];
+      Quotient inverse[8];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float4 x = reinterpret_cast<const float4*>(inverses + c8)[i];
-        inverse[4 * i] = x.x, inverse[4 * i + 1] = x.y, inverse[4 * i + 2] = x.z, inverse[4 * i + 3] = x.w;
+        const float4 y = reinterpret_cast<const float4*>(inverses[0] + c8)[i], x = reinterpret_cast<const float4*>(inverses[1] + c8)[i];
+        inverse[4 * i] = {y.x, x.x}, inverse[4 * i + 1] = {y.y, x.y}, inverse[4 * i + 2] = {y.z, x.z}, inverse[4 * i + 3] = {y.w, x.w};
       }
       // The rows as they are, or the block's own 128 with zeros behind the group's last (which were read as zeros).
-      put_rows(a.qc, a.ldqc, ragged ? static_cast<long long>(block) * TILE : row, ragged ? TILE : count, [&](int i, auto store) {
+      put_rows(a.qc, a.ldqc, ragged ? static_cast<long long>(block) * TILE : row, ragged ? TILE : count, [&](int i) {
         float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = v[i].get(e) * inverse[e];
-        store(r0 + 16 * i < count ? eight_bits<E5M2>(f, 1.0f) : make_uint2(0, 0));
+        unpack(i, f);
+        const uint2 w = eight_bits<E5M2>(f, [&](int e) { return inverse[e]; });
+        return r0 + 16 * i < count ? w : make_uint2(0, 0);
       });
     }
     if (MATRIX) {
@@ -253,13 +266,14 @@ __global__ void __launch_bounds__(kThreads, ALIGNED && sizeof(T) == 2 ? 3 : 1) q
 #pragma unroll
       for (int w = 0; w < kThreads / 32; ++w) m = max(m, most[0][w]);
       __syncthreads();
-      const float scale = scale_of<E5M2>(raw_magnitude<T>(m)), inverse = 1.0f / scale;
+      m = raw_magnitude<T>(m);
+      const float scale = scale_of<E5M2>(m);
+      const Quotient inverse = inverse_of<E5M2>(m, scale);
       if (threadIdx.x == 0) a.s[(static_cast<long long>(mat) * a.row_tiles + block) * a.col_tiles + c / TILE] = scale;
-      put_rows(a.q + mat * a.stride_q, a.ldq, row, count, [&](int i, auto store) {
+      put_rows(a.q + mat * a.stride_q, a.ldq, row, count, [&](int i) {
         float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = v[i].get(e);
-        store(eight_bits<E5M2>(f, inverse));
+        unpack(i, f);
+        return eight_bits<E5M2>(f, inverse);
       });
     }
   }
@@ -279,8 +293,9 @@ __global__ void __launch_bounds__(kThreads, ALIGNED && sizeof(T) == 2 ? 3 : 1) q
         if (c < a.k) f[e] = to_float(x[c]);
         m = max(m, magnitude(f[e]));
       }
-      const float scale = scale_of<E5M2>(__reduce_max_sync(0xFFFFFFFFu, m));
-      const uint2 v = eight_bits<E5M2>(f, 1.0f / scale);
+      m = __reduce_max_sync(0xFFFFFFFFu, m);
+      const float scale = scale_of<E5M2>(m);
+      const uint2 v = eight_bits<E5M2>(f, inverse_of<E5M2>(m, scale));
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int c = b * TILE + lane + 32 * e;

@@ -444,9 +444,9 @@ int ozaki_newton_schulz(int m, int n, int batch, int dtype, const void* G, int l
 int ozaki_f8_column_blocks(int rows, int groups, int ragged);
 
 /* X (OZ_BF16, OZ_F16 or OZ_F32; ldx >= k) in 8 bits (type: OZ_E4M3 or OZ_E5M2): a block's scale is its largest magnitude
- * over the type's largest value (448, 57344), not below 2^-126, and 1 for a block of zeros; q is x / scale to
- * the nearest (through the scale's reciprocal: a quotient within 2^-22 of the middle between two values may go
- * to either).  A block that holds Inf or NaN gets an Inf or NaN scale, and everything computed from it is NaN or Inf.
+ * over the type's largest value (448, 57344), not below 2^-126, and 1 for a block of zeros; q is x over that scale
+ * before its rounding, to the nearest, ties to even (an OZ_F32 quotient within 2^-24 of the middle between two values is rounded
+ * to FP32 first).  A block that holds Inf or NaN gets an Inf or NaN scale, and everything computed from it is NaN or Inf.
  *  - Q and S: OZ_BLOCK_ROW, _BOTH, _MATRIX.  QC and SC: OZ_BLOCK_COLUMN, _BOTH.  The others are not used.
  *  - groups: the matrices of OZ_BLOCK_MATRIX (strideX, strideQ between them), or the groups of `offsets` (device
  *    memory, groups + 1 ints, as in the grouped products, clamped and reported likewise), 1 without them.

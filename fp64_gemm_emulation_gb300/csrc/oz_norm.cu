@@ -11,6 +11,8 @@
 // with a residual: 79 us, 5.9 TB/s; 127 with a CTA a row).  Several threads share a row, eight neighbours each (a block of
 // 128 is 16 threads); rows that do not start at multiples of 16 bytes are read and written in 16-byte pieces too, shifted
 // (7777 rows of 2049 bfloat16 values backward: 41 us, 3.1 TB/s; 68 with an access an element).
+#include <atomic>
+
 #include "oz_elements.cuh"
 #include "oz_device.cuh"
 #include "oz_ragged.cuh"
@@ -517,6 +519,29 @@ int parts_of(int rows, int k) {
   return rows < most ? rows : most;
 }
 
+// The shared-memory limit is the function's, in this context, for all host threads: the most that any launch takes, set once
+// (and again should a launch be refused, in a new context after a device reset).
+template <class T, int RUNS, bool EDGES>
+cudaError_t launch_staged(const NormBackParams& a, int threads, cudaStream_t stream) {
+  auto kernel = norm_back_staged_kernel<T, RUNS, EDGES>;
+  constexpr int piece = kRowsAhead * RUNS * 16, most = 3 * piece * 1024;
+  static std::atomic<bool> ready[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  for (int attempt = 0; attempt < 2 && e == cudaSuccess; ++attempt) {
+    if (attempt || dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+      if (e != cudaSuccess) break;
+      if (dev < 64) ready[dev].store(true, std::memory_order_release);
+    }
+    e = launch_overlapping(kernel, dim3(a.parts), threads, (a.dh ? 3 : 2) * piece * threads, stream, a);
+    if (e != cudaErrorInvalidValue) return e;
+    if (!attempt) e = cudaSuccess;
+  }
+  cudaGetLastError();
+  return e;
+}
+
 template <class T, bool PIECES>
 cudaError_t launch_norm_back(const NormBackParams& a, cudaStream_t stream) {
   // (one row a CTA; a shift takes up to seven columns more)
@@ -524,11 +549,9 @@ cudaError_t launch_norm_back(const NormBackParams& a, cudaStream_t stream) {
   const Shape s = shape_of(shifted ? a.k + 7 : a.k, true);
   if constexpr (PIECES && sizeof(T) == 2) {
     if (s.runs <= 2) {
-      auto kernel = shifted || a.k % 8 ? (s.runs == 1 ? norm_back_staged_kernel<T, 1, true> : norm_back_staged_kernel<T, 2, true>)
-                                       : (s.runs == 1 ? norm_back_staged_kernel<T, 1, false> : norm_back_staged_kernel<T, 2, false>);
-      const int smem = kRowsAhead * (a.dh ? 3 : 2) * s.runs * 16 * s.threads;
-      const cudaError_t e = smem > 48000 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
-      return e != cudaSuccess ? e : launch_overlapping(kernel, dim3(a.parts), s.threads, smem, stream, a);
+      const bool edges = shifted || a.k % 8;
+      if (s.runs == 1) return edges ? launch_staged<T, 1, true>(a, s.threads, stream) : launch_staged<T, 1, false>(a, s.threads, stream);
+      return edges ? launch_staged<T, 2, true>(a, s.threads, stream) : launch_staged<T, 2, false>(a, s.threads, stream);
     }
   }
   auto kernel = norm_back_kernel<T, PIECES, 4>;

@@ -1,0 +1,41 @@
+"""What build_lib builds, and when (a stand-in for nvcc that writes its output file; no compiler is run)."""
+import stat
+
+import pytest
+
+from fp64_gemm_emulation_gb300 import build_lib
+
+
+@pytest.fixture
+def tree(tmp_path, monkeypatch):
+    """A source tree with one kernel file; calls: the stand-in's command lines."""
+    src, log = tmp_path / "csrc", tmp_path / "calls"
+    src.mkdir()
+    (src / "a.cu").write_text("// a kernel\n")
+    (src / "tensor_lists.cpp").write_text("// a module\n")
+    fake = tmp_path / "nvcc"
+    fake.write_text(f'#!/bin/sh\necho "$@" >> {log}\nwhile [ "$1" != -o ]; do shift; done\necho made > "$2"\n')
+    fake.chmod(fake.stat().st_mode | stat.S_IXUSR)
+    monkeypatch.setenv("NVCC", str(fake))
+    for name, path in (("CSRC", src), ("INCLUDE", tmp_path), ("BUILD", tmp_path / "_build"), ("LIB", tmp_path / "libozaki.so"), ("LISTS", tmp_path / "_tensor_lists.so")):
+        monkeypatch.setattr(build_lib, name, str(path))
+
+    def calls():
+        lines = log.read_text().splitlines() if log.exists() else []
+        log.unlink(missing_ok=True)
+        return ["link" if "-shared" in line.split() else "compile" for line in lines]
+
+    return tmp_path, calls
+
+
+def test_the_library_needs_no_helper(tree, monkeypatch, capsys):
+    def fails(*_):
+        raise RuntimeError("no torch here")
+
+    monkeypatch.setattr(build_lib, "build_lists", fails)
+    tmp, calls = tree
+    assert build_lib.build() == str(tmp / "libozaki.so") and (tmp / "libozaki.so").exists()
+    assert calls() == ["compile", "link"]
+    assert "no torch here" in capsys.readouterr().err
+    build_lib.build()
+    assert calls() == []

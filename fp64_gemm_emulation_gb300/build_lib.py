@@ -88,7 +88,7 @@ def build(verbose: bool = False, force: bool = False) -> str:
         for msg in ex.map(compile_one, todo):
             if verbose and msg:
                 print(msg, file=sys.stderr)
-        if todo or force or not os.path.exists(LIB):
+        if force or _stale(LIB, objs[0], objs):
             cmd = [exe] + ARCH + ["-shared", "-o", LIB + ".tmp"] + objs
             if verbose:
                 print(" ".join(cmd), flush=True)

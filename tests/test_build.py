@@ -1,4 +1,5 @@
 """What build_lib builds, and when (a stand-in for nvcc that writes its output file; no compiler is run)."""
+import os
 import stat
 
 import pytest
@@ -39,3 +40,14 @@ def test_the_library_needs_no_helper(tree, monkeypatch, capsys):
     assert "no torch here" in capsys.readouterr().err
     build_lib.build()
     assert calls() == []
+
+
+def test_objects_newer_than_the_library_are_linked(tree, monkeypatch):
+    monkeypatch.setattr(build_lib, "build_lists", lambda *_: "")
+    tmp, calls = tree
+    build_lib.build()
+    calls()
+    then = os.path.getmtime(tmp / "_build" / "a.o")
+    os.utime(tmp / "libozaki.so", (then - 100, then - 100))  # as a build leaves it that ended before its link
+    build_lib.build()
+    assert calls() == ["link"]

@@ -42,14 +42,18 @@ def _stale(obj: str, src: str, headers: list[str]) -> bool:
 
 
 def build_lists(verbose: bool = False, force: bool = False) -> str:
-    """_tensor_lists.so, a Python module (csrc/tensor_lists.cpp)."""
-    src = os.path.join(CSRC, "tensor_lists.cpp")
-    if not force and not _stale(LISTS, src, []):
-        return ""
+    """_tensor_lists.so, a Python module (csrc/tensor_lists.cpp).  It is bound to torch's and Python's binary interfaces: what it
+    was built for stands beside the objects, and another torch or Python builds it anew."""
     import sysconfig
 
     import torch
 
+    src, stamp = os.path.join(CSRC, "tensor_lists.cpp"), os.path.join(BUILD, "tensor_lists.for")
+    built_for = f"torch {torch.__version__} at {os.path.dirname(torch.__file__)}, {sysconfig.get_config_var('SOABI')}"
+    if not force and not _stale(LISTS, src, []) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == built_for:
+                return ""
     root = os.path.dirname(torch.__file__)
     inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"], "-isystem", inc,
@@ -61,6 +65,9 @@ def build_lists(verbose: bool = False, force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
     os.replace(LISTS + ".tmp", LISTS)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(built_for)
     return r.stderr
 
 

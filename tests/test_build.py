@@ -51,3 +51,27 @@ def test_objects_newer_than_the_library_are_linked(tree, monkeypatch):
     os.utime(tmp / "libozaki.so", (then - 100, then - 100))  # as a build leaves it that ended before its link
     build_lib.build()
     assert calls() == ["link"]
+
+
+def test_the_helper_is_built_anew_for_another_torch(tree, monkeypatch):
+    import torch
+
+    tmp, _ = tree
+    (tmp / "bin").mkdir()
+    fake = tmp / "bin" / "g++"
+    fake.write_text((tmp / "nvcc").read_text().replace("calls", "gxx"))
+    fake.chmod(fake.stat().st_mode | stat.S_IXUSR)
+    monkeypatch.setenv("PATH", str(tmp / "bin"), prepend=os.pathsep)
+
+    def built():
+        build_lib.build_lists()
+        log = tmp / "gxx"
+        n = len(log.read_text().splitlines()) if log.exists() else 0
+        log.unlink(missing_ok=True)
+        return n
+
+    assert [built(), built()] == [1, 0]
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert [built(), built()] == [1, 0]
+    (tmp / "_build" / "tensor_lists.for").unlink()  # one that was built before this was kept
+    assert [built(), built()] == [1, 0]

@@ -1172,7 +1172,9 @@ def _tensor_lists():
     try:
         from . import _tensor_lists
     except ImportError as e:
-        raise ImportError("_tensor_lists.so is missing: build it with `python -m fp64_gemm_emulation_gb300.build_lib`") from e
+        there = os.path.exists(os.path.join(_PKG, "_tensor_lists.so"))
+        what = f"does not load ({e}): build it for this torch and Python" if there else "is missing: build it"
+        raise ImportError(f"_tensor_lists.so {what} with `python -m fp64_gemm_emulation_gb300.build_lib`") from e
     return _tensor_lists
 
 

@@ -75,3 +75,25 @@ def test_the_helper_is_built_anew_for_another_torch(tree, monkeypatch):
     assert [built(), built()] == [1, 0]
     (tmp / "_build" / "tensor_lists.for").unlink()  # one that was built before this was kept
     assert [built(), built()] == [1, 0]
+
+
+@pytest.mark.parametrize("there, says", [(True, "undefined symbol"), (False, "is missing")])
+def test_a_helper_that_does_not_load_says_why(there, says, monkeypatch, tmp_path):
+    import sys
+
+    import fp64_gemm_emulation_gb300 as package
+    from fp64_gemm_emulation_gb300 import ozaki as oz
+
+    class Fails:
+        def find_spec(self, name, *_):
+            if name.endswith("_tensor_lists"):
+                raise ImportError("undefined symbol: f")
+
+    monkeypatch.setattr(oz, "_PKG", str(tmp_path))
+    if there:
+        (tmp_path / "_tensor_lists.so").write_text("")
+    monkeypatch.delitem(sys.modules, "fp64_gemm_emulation_gb300._tensor_lists", raising=False)
+    monkeypatch.delattr(package, "_tensor_lists", raising=False)
+    monkeypatch.setattr(sys, "meta_path", [Fails(), *sys.meta_path])
+    with pytest.raises(ImportError, match=says):
+        oz._tensor_lists()

@@ -6,7 +6,9 @@
 //   wgrad    dW_e = X_e dY_e^T   D[k, n]   = sum_b sx[b, k] sy[b, n] sum_{row in b} X[k, row] dY[n, row]
 // (column-major; b runs over the blocks of 128 of the sum's index).  A block's products are summed by the
 // tensor cores (kind::f8f6f4, FP32 sums of 128 products) and its sum is scaled and added to FP32 sums in
-// registers, rounding to nearest: any FP32 scales are taken, and no sum is longer than 128 on the tensor cores.
+// registers, rounding to nearest: no sum is longer than 128 on the tensor cores.  The two scales of a sum are multiplied first: a
+// product below 2^-126 is off by up to 2^-150, one of 2^128 and more is Inf.  (To add such blocks in FP64 instead cost the
+// others: 8192 x 4096 x 8192 234 us instead of 227, 64 rows 17.9 instead of 15.9, weight gradient 410 instead of 385.)
 //
 // Kernel shape: clusters of two CTAs (cta_group::2), persistent over tiles of 256 m (the first index of D above) x
 // 256 n, 128 m in each CTA.

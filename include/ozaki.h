@@ -466,7 +466,9 @@ int ozaki_quantize_f8(int block, int k, int rows, int groups, int dtype, const v
  * Shapes, groups and offsets as in ozaki_grouped_gemm; offsets == NULL (with groups == 1): one group of all rows, a
  * dense layer.  Each operand is OZ_E4M3 or OZ_E5M2 (type_*), the output OZ_BF16 or OZ_F16 (dtype).
  *  - A block's 128 products are summed by the tensor cores, scaled in FP32 and added to FP32 sums; the result is rounded once.
- *  - Scales: any FP32 numbers (SW, SX, SdY, laid out as above).
+ *  - Scales (SW, SX, SdY, laid out as above): FP32 numbers of either sign, and 0.  The two that meet at a block are multiplied
+ *    first, in FP32.  A product below 2^-126 is off by up to 2^-150, which is at most 2^-125 (OZ_E4M3) or 2^-111 (OZ_E5M2, both
+ *    operands) of absolute error a block in the result; one of 2^128 or more is Inf, and makes sums of 0 NaN.
  *  - Operands start at multiples of 16 bytes, and so do their columns and matrices; OZ_EINVAL otherwise (quantised
  *    operands are made that way).
  *  - wgrad with offsets: rows is the number of tokens that the offsets speak of; X and dY hold the

@@ -391,7 +391,7 @@ int ozaki_quantize_f8(int block, int k, int rows, int groups, int dtype, const v
   a.rows = rows;
   a.groups = groups;
   a.mats = matrix ? groups : 1;
-  a.x = X;
+  a.x = X ? X : QC;  // no rows: pieces are still asked for, of no bytes, from an address that has to be one
   a.ldx = ldx;
   a.stride_x = strideX;
   a.offsets = offsets;

@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import sys
 
@@ -962,7 +963,7 @@ def ozaki_quantize_f8(X, block: str = "row", offsets=None, dtype=None, stream=No
         if X.dim() < 2:
             raise ValueError("X must have shape (..., n, k)")
         n, k = X.shape[-2:]
-        X3 = X if X.dim() == 3 else X[None] if X.dim() == 2 else X.view(-1, n, k)
+        X3 = X if X.dim() == 3 else X[None] if X.dim() == 2 else X.view(math.prod(X.shape[:-2]), n, k)
         ldx, sx = _experts(X3, "X")
         mats, ldq = X3.shape[0], _ld16(k)
         Q = _new(X.shape, dtype, device, ldq)

@@ -19,3 +19,16 @@ def test_no_rows_with_offsets(block, dtype):
     if block == "both":
         assert got[0].shape == (0, 136) and got[1].shape == (0, 2)
     assert oz.ozaki_get_device_status() == oz.OZ_OK
+
+
+@pytest.mark.parametrize("shape", [(0, 3, 40, 136), (2, 3, 0, 136), (2, 3, 40, 0), (0, 40, 136), (0, 136), (3, 2, 1, 1)])
+def test_batches_without_elements(shape):
+    q, s = oz.ozaki_quantize_f8(torch.ones(shape, dtype=torch.bfloat16, device="cuda"), "matrix")
+    assert q.shape == shape and s.shape == (*shape[:-2], -(-shape[-2] // 128), -(-shape[-1] // 128))
+    assert torch.equal(q.float(), torch.full(shape, 448.0, device="cuda"))
+
+
+def test_batches_that_lie_unevenly_are_refused():
+    x = torch.ones(3, 4, 40, 136, dtype=torch.bfloat16, device="cuda")[:, :2]
+    with pytest.raises((ValueError, RuntimeError)):
+        oz.ozaki_quantize_f8(x, "matrix")

@@ -71,13 +71,18 @@ struct Rows {
   __device__ Eight<T> fetch(int row, int c) const { return fetch_eight<T, VEC>(first + row * ld, c, row < rows ? k : 0, first, end); }
 };
 
+// CTAs of 256 threads on an SM: what the registers hold; shifted pieces of two runs spill with a third (16384 x 4095 bfloat16 with a
+// residual 230 us instead of 203).
+__host__ __device__ constexpr int resident_ctas(bool vec, int runs) { return runs == 1 ? 4 : runs == 2 && vec ? 3 : 2; }
+
 // q is y / scale, in which r cancels: 448 h w / (the block's largest |h w|), so that the roundings of r, of the scale and of h r
 // do not come before the one to 8 bits (with two 16-bit summands h w often is exact).  h is multiplied by r's power of two
 // all the same, which rounds nothing, so that h w leaves the range of FP32 only where y does.
+//
 // RUNS: runs of eight elements a thread holds.  blockDim (threads of a row, rows).  STAY: a CTA takes every
 // gridDim.x-th group of rows, at most 256 threads; otherwise one.
 template <class T, bool VEC, int RUNS, bool STAY>
-__global__ void __launch_bounds__(STAY ? 256 : 1024, STAY ? (RUNS == 1 ? 4 : RUNS == 2 ? 3 : 2) : 1) norm_kernel(const __grid_constant__ NormParams a) {
+__global__ void __launch_bounds__(STAY ? 256 : 1024, STAY ? resident_ctas(VEC, RUNS) : 1) norm_kernel(const __grid_constant__ NormParams a) {
   __shared__ float meet[2][32];
   let_next_start();
   wait_for_previous();
@@ -480,7 +485,7 @@ cudaError_t launch_norm(const NormParams& a, int sms, cudaStream_t stream) {
   Shape s = shape_of(a.k, a.rows < 4 * sms);
   if (s.threads > 32) s.rows = 1;  // (several rows of one warp each need no barrier)
   const int groups = (a.rows + s.rows - 1) / s.rows, threads = s.threads * s.rows;
-  const int resident = sms * (threads <= 256 ? 256 / threads : 1) * (s.runs == 1 ? 4 : s.runs == 2 ? 3 : 2);
+  const int resident = sms * (threads <= 256 ? 256 / threads : 1) * resident_ctas(VEC, s.runs);
   const bool stay = threads <= 256 && groups > resident;
   cudaError_t e = cudaErrorInvalidValue;
   auto go = [&](void (*kernel)(NormParams)) {
@@ -512,8 +517,9 @@ cudaError_t norm_of_type(const NormParams& a, int sms, cudaStream_t stream) {
   return vec ? launch_norm<T, true>(a, sms, stream) : launch_norm<T, false>(a, sms, stream);
 }
 
-// CTAs of the backward pass: as many as run at once on 152 SMs (at most 64 registers a thread; with 56 four CTAs of 7777 rows of
-// 2049 fit instead of three, which leaves the next launch's no room: 54 us a call instead of 41).
+// CTAs of the backward pass: 1024 threads of them an SM, of 152 (64 registers a thread), counted for k columns: rows that are shifted
+// have up to 7 more, which can make a warp more (7777 rows of 2049: 288 threads, so three of the four CTAs counted run at once;
+// with 56 registers all four do, which leaves the next launch's no room: 54 us a call instead of 41).
 int parts_of(int rows, int k) {
   const int threads = shape_of(k, true).threads, most = 152 * (threads >= 128 ? 1024 / threads : 8);
   return rows < most ? rows : most;

@@ -490,7 +490,8 @@ int ozaki_grouped_gemm_f8_wgrad(int n, int k, int rows, int groups, int type_dy,
 
 /* For each token (column of X, k features): h = x + residual, rstd = 1 / sqrt(mean(h^2) + eps), y = h rstd W (feature by
  * feature), and y in OZ_E4M3 with OZ_BLOCK_ROW scales.  Elements of X, residual, W, H and Y are of dtype (OZ_BF16, OZ_F16 or
- * OZ_F32), any address and leading dimension; everything is computed in FP32 from the unrounded h and each output rounded once.
+ * OZ_F32), any address and leading dimension; everything is computed in FP32 from the unrounded h and rounded at the end.
+ *  - q is rounded from 448 h W / (the block's largest |h W|), ties to even, so that the roundings of rstd and of the scale do not enter it.
  *  - residual may be NULL (h = x).  H (k x rows, the sum, rounded) and Y (k x rows, y rounded) are written where not NULL;
  *    their leading dimensions are >= k in any case.  H may be X or residual; nothing else may overlap.
  *  - Q, S as OZ_BLOCK_ROW's of ozaki_quantize_f8.  rstd: rows floats.

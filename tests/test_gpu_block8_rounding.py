@@ -35,12 +35,9 @@ def quotients(x, block, eight):
 
 
 # multiples of a power of two meet the middle of two 8-bit values often; the others cover the range (1e-44 is below the normal one)
-@pytest.mark.parametrize("size", [1.0, 1e-44, 1e-36, 1e-20, 1e30, 1.5e38])
+@pytest.mark.parametrize("dtype,size", [(torch.float16, 1.0)] + [(d, s) for d in (torch.bfloat16, torch.float32) for s in (1.0, 1e-44, 1e-36, 1e-20, 1e30, 1.5e38)])
 @pytest.mark.parametrize("eight", [E4M3, E5M2])
-@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
-def test_quantised_values_are_the_rounded_quotients(dtype, eight, size):
-    if dtype == torch.float16 and size != 1.0:
-        pytest.skip("outside the type")
+def test_quantised_values_are_the_rounded_quotients(dtype, size, eight):
     gen = torch.Generator(device="cuda").manual_seed(3)
     rows, k = 300, 520
     for x in (torch.randint(-127, 128, (rows, k), generator=gen, device="cuda").float() / 128, torch.randn(rows, k, generator=gen, device="cuda").clamp(-2, 2)):
